@@ -23,11 +23,16 @@ OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_STATUS, ERR_TIMEOUT, ERR_NOT_ORTHOGONAL = -1, -2, -3, -4, -5, -6
 ERR_TOO_LARGE = -7
 STATUS_BAD_PAGE, STATUS_BAD_SEQLEN, STATUS_TIMEOUT, STATUS_NONFINITE, STATUS_SATURATED = 1, 2, 4, 8, 16
+STATUS_NO_PAGES, STATUS_BAD_TREE = 32, 64
 V_ABSORBED, V_EXPLICIT = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 KIND_K, KIND_V = 0, 1
 DECODE_SIMT, DECODE_MMA, DECODE_TC = 0, 1, 2
 META_F16, META_U8, META_CB = 0, 1, 2
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+ROPE_HALF, ROPE_PAIRS = 0, 1
+DTYPE_BF16, DTYPE_FP32, DTYPE_FP16 = 0, 1, 2
+MAX_DRAFT = 256
 
 # every symbol include/oscar.h declares
 EXPORTS = (
@@ -38,6 +43,8 @@ EXPORTS = (
     "oscar_decode_attention_noalloc", "oscar_trace_ctas", "oscar_decode_step",
     "oscar_decode_attention_shared", "oscar_decode_step_shared",
     "oscar_trace_timeline", "oscar_check_wait_timeout", "oscar_set_codebook", "oscar_calibrate_codebook",
+    "oscar_build_tables", "oscar_tree_layout", "oscar_rope_frequencies", "oscar_rope_turns", "oscar_rope",
+    "oscar_tree_workspace_bytes", "oscar_tree_attention", "oscar_commit_draft",
 )
 
 
@@ -53,12 +60,17 @@ class Layout(ctypes.Structure):
         "num_int2_pages", "num_bf16_pages", "v_mode", "max_batch", "max_splits", "meta_format")]
 
 
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("in_token", "in_head", "out_token", "out_head")] + [("heads", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"OSCAR CUDA library not built ({LIB_PATH} missing); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32p, sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
-    c_int, c_float = ctypes.c_int, ctypes.c_float
+    c_int, c_float, c_double = ctypes.c_int, ctypes.c_float, ctypes.c_double
     sig = {
         "oscar_cache_bytes": [ctypes.POINTER(Layout), sz, sz],
         "oscar_cache_create": [ctypes.POINTER(Layout), vp, vp, ctypes.POINTER(vp)],
@@ -89,6 +101,17 @@ def _load() -> ctypes.CDLL:
                                           vp, vp],
         "oscar_decode_step_shared": [vp, c_int, c_int, vp, vp, vp, i32p, i32p, c_int, c_int, i32p, c_float, vp,
                                      c_int, vp, vp],
+        "oscar_build_tables": [vp, c_int, i32p, i32p, i32p, c_int, i32p, i32p, i32p, i32p, i32p, i32p, i32p, c_int, vp],
+        "oscar_tree_layout": [vp, c_int, c_int, i32p, i32p, i32p, vp, i32p, vp],
+        "oscar_rope_frequencies": [c_int, c_double, c_int, c_double, c_double, c_double, c_double, vp,
+                                   ctypes.POINTER(c_float)],
+        "oscar_rope_turns": [vp, c_int, vp],
+        "oscar_rope": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p, vp, c_int,
+                       c_int, c_float, c_int, vp],
+        "oscar_tree_workspace_bytes": [vp, c_int, c_int, c_int, sz],
+        "oscar_tree_attention": [vp, c_int, c_int, c_int, vp, vp, vp, vp, i32p, i32p, i32p, c_int, i32p, c_float, vp,
+                                 c_int, vp, vp, ctypes.c_size_t, vp],
+        "oscar_commit_draft": [vp, c_int, c_int, c_int, vp, vp, i32p, i32p, c_int, i32p, i32p, c_int, i32p, vp],
         "oscar_decode_attention_noalloc": [ctypes.POINTER(Layout), vp, c_int, c_int, vp, i32p, i32p, c_int, i32p,
                                            c_float, vp, c_int, vp, vp, vp],
     }
@@ -133,6 +156,28 @@ def _dev_i32(x, device):
         assert x.dtype == torch.int32 and x.is_cuda and x.is_contiguous()
         return x
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=device)
+
+
+def _own_i32(t, numel: int):
+    """An int32 device tensor the library writes (never copied): contiguous, of at least numel elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or \
+            t.numel() < numel:
+        raise OscarError(ERR_INVALID_ARG, f"int32 device tensor of at least {numel} elements")
+    return t
+
+
+def _check_words(t, B: int, T: int, what: str):
+    import torch
+    if t.dtype not in (torch.int64, torch.uint64) or not t.is_cuda or not t.is_contiguous() or \
+            tuple(t.shape) != (B, T, (T + 63) // 64):
+        raise OscarError(ERR_INVALID_ARG, what)
+
+
+def _check_bf16(t, shape, what: str):
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise OscarError(ERR_INVALID_ARG, what)
 
 
 @dataclass
@@ -309,6 +354,118 @@ class OscarCache:
                                           _stream(stream)), "oscar_decode_step")
         return out
 
+    # ---- verifying drafted tokens -----------------------------------------------------
+    def build_tables(self, old_lens, new_lens, hist_pt, bf16_pt, free_int2, free_bf16, rings, max_tokens: int = 0,
+                     rings_out=None, cu_tokens=None, slots=None, stream=None):
+        """Page tables and token slots of requests growing (or released) from old_lens to new_lens; the tables and
+        the free rings are int32 device tensors updated in place, the ring positions too unless rings_out is given.
+        With max_tokens, or a slots tensor [max_tokens, 4], each new token's (position, region, page, row) is
+        written. Returns (rings_out, cu_tokens, slots)."""
+        import torch
+        old, new = _dev_i32(old_lens, self.device), _dev_i32(new_lens, self.device)
+        B = old.numel()
+        for t, n in ((hist_pt, 0), (bf16_pt, B * (self.cfg.sink + self.cfg.recent) // self.cfg.page_size),
+                     (free_int2, self.cfg.num_int2_pages), (free_bf16, self.cfg.num_bf16_pages), (rings, 4)):
+            _own_i32(t, n)
+        rings_out = rings if rings_out is None else _own_i32(rings_out, 4)
+        cu_tokens = torch.empty(B + 1, dtype=torch.int32, device=self.device) if cu_tokens is None else \
+            _own_i32(cu_tokens, B + 1)
+        if slots is None and max_tokens:
+            slots = torch.empty(max_tokens, 4, dtype=torch.int32, device=self.device)
+        if slots is not None:
+            max_tokens = _own_i32(slots, 0).numel() // 4
+        if new.numel() != B or hist_pt.dim() != 2 or hist_pt.shape[0] != B:
+            raise OscarError(ERR_INVALID_ARG, "oscar_build_tables")
+        _check(_lib.oscar_build_tables(self._h, B, _ptr(old), _ptr(new), _ptr(hist_pt), hist_pt.shape[1],
+                                       _ptr(bf16_pt), _ptr(free_int2), _ptr(free_bf16), _ptr(rings), _ptr(rings_out),
+                                       _ptr(cu_tokens), _ptr(slots), max_tokens, _stream(stream)),
+               "oscar_build_tables")
+        return rings_out, cu_tokens, slots
+
+    def tree_layout(self, parents, seq_lens, n_draft=None, mask=None, positions=None, stream=None):
+        """Ancestor masks (int64 [B, T, ceil(T / 64)], 64 nodes a word) and positions (int32 [B, T]) of the trees
+        given by parents [B, T]."""
+        import torch
+        pa, sl = _dev_i32(parents, self.device), _dev_i32(seq_lens, self.device)
+        nd = None if n_draft is None else _dev_i32(n_draft, self.device)
+        B, T = pa.shape
+        if sl.numel() != B or (nd is not None and nd.numel() != B):
+            raise OscarError(ERR_INVALID_ARG, "oscar_tree_layout")
+        if mask is None:
+            mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=self.device)
+        if positions is None:
+            positions = torch.empty(B, T, dtype=torch.int32, device=self.device)
+        _check_words(mask, B, T, "oscar_tree_layout")
+        _own_i32(positions, B * T)
+        _check(_lib.oscar_tree_layout(self._h, B, T, _ptr(pa), _ptr(nd), _ptr(sl), _ptr(mask), _ptr(positions),
+                                      _stream(stream)), "oscar_tree_layout")
+        return mask, positions
+
+    def tree_workspace_bytes(self, batch: int, T: int, max_hist_pages: int) -> int:
+        n = ctypes.c_size_t()
+        _check(_lib.oscar_tree_workspace_bytes(self._h, batch, T, max_hist_pages, ctypes.byref(n)),
+               "oscar_tree_workspace_bytes")
+        return n.value
+
+    def tree_attention(self, layer: int, q, k_draft, v_draft, mask, seq_lens, hist_pt, bf16_pt, sm_scale: float,
+                       n_draft=None, out=None, out_dtype: int = OUT_BF16, lse=None, workspace=None, stream=None):
+        """Attention of drafted nodes q [B, T, Hq, 128] over the cache's seq_lens tokens and, by mask, the drafted
+        k_draft, v_draft [B, T, Hkv, 128]. workspace: a uint8 tensor of tree_workspace_bytes, allocated per call
+        when not given; calls that may overlap need one each."""
+        import torch
+        sl = _dev_i32(seq_lens, self.device)
+        hp = _dev_i32(hist_pt, self.device)
+        bp = _dev_i32(bf16_pt, self.device)
+        nd = None if n_draft is None else _dev_i32(n_draft, self.device)
+        B, T = int(q.shape[0]), int(q.shape[1])
+        _check_bf16(q, (B, T, self.cfg.num_q_heads, self.cfg.head_dim), "oscar_tree_attention")
+        for t in (k_draft, v_draft):
+            _check_bf16(t, (B, T, self.cfg.num_kv_heads, self.cfg.head_dim), "oscar_tree_attention")
+        _check_words(mask, B, T, "oscar_tree_attention")
+        mhp = hp.shape[1] if hp.dim() == 2 else 0
+        if sl.numel() != B or (nd is not None and nd.numel() != B) or hp.numel() != B * mhp or bp.shape[0] != B:
+            raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16,
+                              device=self.device)
+        elif out.dtype != (torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16) or not out.is_contiguous() or \
+                out.shape != q.shape:
+            raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
+        if workspace is None:
+            s = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(self.tree_workspace_bytes(B, T, mhp), dtype=torch.uint8, device=self.device)
+        _check(_lib.oscar_tree_attention(self._h, layer, B, T, _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
+                                         _ptr(nd), _ptr(sl), _ptr(hp), mhp, _ptr(bp), float(sm_scale), _ptr(out),
+                                         out_dtype, _ptr(lse), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)),
+               "oscar_tree_attention")
+        return out
+
+    def commit_draft(self, layer: int, k_draft, v_draft, seq_lens_before, n_accept, hist_pt, bf16_pt, path=None,
+                     max_accept: int | None = None, stream=None):
+        """Append nodes path[r, :n_accept[r]] of k_draft, v_draft [B, T, Hkv, 128] at seq_lens_before[r]; without a
+        path nodes 0 .. n_accept[r] - 1 (max_accept of them at most, T by default)."""
+        sl = _dev_i32(seq_lens_before, self.device)
+        na = _dev_i32(n_accept, self.device)
+        hp = _dev_i32(hist_pt, self.device)
+        bp = _dev_i32(bf16_pt, self.device)
+        pa = None if path is None else _dev_i32(path, self.device)
+        B, T = int(k_draft.shape[0]), int(k_draft.shape[1])
+        for t in (k_draft, v_draft):
+            _check_bf16(t, (B, T, self.cfg.num_kv_heads, self.cfg.head_dim), "oscar_commit_draft")
+        if pa is not None:
+            max_accept = pa.shape[1]
+        elif max_accept is None:
+            max_accept = T
+        mhp = hp.shape[1] if hp.dim() == 2 else 0
+        if sl.numel() != B or na.numel() != B or hp.numel() != B * mhp or bp.shape[0] != B or \
+                (pa is not None and pa.shape[0] != B):
+            raise OscarError(ERR_INVALID_ARG, "oscar_commit_draft")
+        _check(_lib.oscar_commit_draft(self._h, layer, B, T, _ptr(k_draft), _ptr(v_draft), _ptr(sl), _ptr(na),
+                                       max_accept, _ptr(pa), _ptr(hp), mhp, _ptr(bp), _stream(stream)),
+               "oscar_commit_draft")
+
     def set_decode_algo(self, algo: int):
         _check(_lib.oscar_set_decode_algo(self._h, algo), "oscar_set_decode_algo")
 
@@ -379,6 +536,59 @@ def bf16_decode(kv_pages, q, seq_lens, page_table, sm_scale: float, num_kv_heads
                                   _ptr(workspace), workspace.numel() * workspace.element_size(), max_splits,
                                   _stream(stream)), "oscar_bf16_decode")
     return out
+
+
+class RopePlan:
+    """Rotary frequencies of a head's first rotary_dim channels (ROPE_* scaling) in the form rope() reads, on a
+    device; inv_freq (float64, radians per position and pair) may be given instead of the base and its scaling."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE, factor: float = 1.0,
+                 original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None,
+                 scale: float | None = None, device="cuda"):
+        import torch
+        self.rotary_dim = int(rotary_dim)
+        f = np.zeros(max(1, self.rotary_dim // 2), np.float64)
+        s = ctypes.c_float(1.0)
+        if inv_freq is None:
+            _check(_lib.oscar_rope_frequencies(self.rotary_dim, base, scaling, factor, original_length, beta_fast,
+                                               beta_slow, _ptr(f), ctypes.byref(s)), "oscar_rope_frequencies")
+        else:
+            f = np.ascontiguousarray(inv_freq, np.float64)
+            if f.shape != (self.rotary_dim // 2,):
+                raise OscarError(ERR_INVALID_ARG, "RopePlan: one frequency per pair")
+        turns = np.zeros(f.shape, np.uint64)
+        _check(_lib.oscar_rope_turns(_ptr(f), f.size, _ptr(turns)), "oscar_rope_turns")
+        self.inv_freq, self.scale = f, float(s.value) if scale is None else float(scale)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+
+
+def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool = False, q_out=None, k_out=None,
+         stream=None):
+    """Rotate q [N, Hq, D] and k [N, Hkv, D] (k may be None) by positions [N]; inverse gives the gradient. Token and
+    head strides are free, a head's channels contiguous. Written to q_out, k_out (new tensors when not given; the
+    inputs themselves for in place). Rows with a negative position are left as they are: new tensors hold them
+    unset. Returns (q_out, k_out)."""
+    import torch
+    dtypes = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32, torch.float16: DTYPE_FP16}
+    pos = _dev_i32(positions, q.device)
+    args, outs = [], []
+    for x, out in ((q, q_out), (k, k_out)):
+        t = RopeTensor()
+        if x is not None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+            if x.dtype not in dtypes or x.dtype != q.dtype or out.dtype != x.dtype or x.dim() != 3 or \
+                    out.shape != x.shape or x.shape[0] != pos.numel() or x.shape[2] != q.shape[2] or \
+                    (x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1)) or not x.is_cuda or \
+                    out.device != x.device or plan.turns.device != x.device:
+                raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+            t = RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                           x.shape[1])
+        args.append(t)
+        outs.append(out)
+    _check(_lib.oscar_rope(ctypes.byref(args[0]), ctypes.byref(args[1]), pos.numel(), q.shape[2], dtypes[q.dtype],
+                           _ptr(pos), _ptr(plan.turns), plan.rotary_dim, layout, plan.scale, int(inverse),
+                           _stream(stream)), "oscar_rope")
+    return outs[0], outs[1]
 
 
 def calibrate_codebook(x_rot, tau) -> np.ndarray:

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "kernels.cuh"
+#include "tree.cuh"
 
 using namespace oscar;
 
@@ -187,6 +188,8 @@ int configure_once() {
   if (g_configured[dev]) return OSCAR_OK;
   int rc = configure_write_path_kernels();
   if (rc == OSCAR_OK) rc = configure_decode_kernels();
+  if (rc == OSCAR_OK) rc = configure_tables_kernel();
+  if (rc == OSCAR_OK) rc = configure_commit_kernel();
   if (rc == OSCAR_OK) g_configured[dev] = true;
   return rc;
 }
@@ -349,7 +352,8 @@ int oscar_cache_create(const oscar_layout* layout, void* pool, void* workspace, 
   c->timeline_cap = 0;
   c->prof_on = false;
   c->prof_cap = c->prof_n = 0;
-  if (cudaMemset(c->status, 0, sizeof(int)) != cudaSuccess) {
+  // the status word and, 128 bytes behind it, the ticket of oscar_build_tables
+  if (cudaMemset(c->status, 0, kAlign) != cudaSuccess) {
     delete c;
     return OSCAR_ERR_CUDA;
   }
@@ -643,6 +647,166 @@ int oscar_decode_step_shared(oscar_cache* c, int layer, int B, const void* q, co
                              float* lse, void* stream) {
   return step_impl(c, layer, B, q, k, v, seq_lens_before, hist_pt, max_hist_pages, shared_hist_pages, bf16_pt,
                    sm_scale, out, out_dtype, lse, stream);
+}
+
+int oscar_build_tables(oscar_cache* c, int B, const int32_t* old_lens, const int32_t* new_lens, int32_t* hist_pt,
+                       int max_hist_pages, int32_t* bf16_pt, int32_t* free_int2, int32_t* free_bf16,
+                       const int32_t* rings_in, int32_t* rings_out, int32_t* cu_tokens, int32_t* slots, int max_tokens,
+                       void* stream) {
+  if (!c || B < 0 || max_hist_pages < 0 || max_tokens < 0) return OSCAR_ERR_INVALID_ARG;
+  if (B > kMaxTableBatch) return OSCAR_ERR_UNSUPPORTED;
+  if (!rings_in || !rings_out || (B > 0 && (!old_lens || !new_lens || !bf16_pt || !free_bf16))) return OSCAR_ERR_INVALID_ARG;
+  if (B > 0 && ((max_hist_pages > 0 && !hist_pt) || (c->lay.num_int2_pages > 0 && !free_int2))) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16(slots)) return OSCAR_ERR_INVALID_ARG;
+  return launch_build_tables(c->lay, B, old_lens, new_lens, hist_pt, max_hist_pages, bf16_pt, free_int2, free_bf16,
+                             rings_in, rings_out, cu_tokens, slots, max_tokens, c->status,
+                             reinterpret_cast<unsigned*>(c->ws + 128), c->sms, static_cast<cudaStream_t>(stream));
+}
+
+int oscar_tree_layout(oscar_cache* c, int B, int T, const int32_t* parents, const int32_t* n_draft,
+                      const int32_t* seq_lens, uint64_t* mask, int32_t* positions, void* stream) {
+  if (!c || B < 0 || T < 1) return OSCAR_ERR_INVALID_ARG;
+  if (T > kMaxDraft) return OSCAR_ERR_UNSUPPORTED;
+  if (B == 0) return OSCAR_OK;
+  if (!parents || !seq_lens || !mask || !positions) return OSCAR_ERR_INVALID_ARG;
+  return launch_tree_layout(B, T, parents, n_draft, seq_lens, mask, positions, c->status,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int oscar_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                           double beta_fast, double beta_slow, double* inv_freq, float* scale) {
+  if (rotary_dim < 2 || rotary_dim % 2 || !(base > 1.0) || !std::isfinite(base) || !inv_freq || !scale)
+    return OSCAR_ERR_INVALID_ARG;
+  if (scaling < OSCAR_ROPE_NONE || scaling > OSCAR_ROPE_YARN) return OSCAR_ERR_INVALID_ARG;
+  if (scaling != OSCAR_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return OSCAR_ERR_INVALID_ARG;
+  if (scaling == OSCAR_ROPE_NTK && rotary_dim == 2) return OSCAR_ERR_INVALID_ARG;
+  if (scaling == OSCAR_ROPE_YARN &&
+      (!(original_length >= 1.0) || !std::isfinite(original_length) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+       !std::isfinite(beta_fast)))
+    return OSCAR_ERR_INVALID_ARG;
+  const int half = rotary_dim / 2;
+  if (scaling == OSCAR_ROPE_NTK) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+  // pair index at which a frequency turns beta times in the original length
+  auto pair_of = [&](double beta) {
+    return half * std::log(original_length / (2.0 * M_PI * beta)) / std::log(base);
+  };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == OSCAR_ROPE_YARN) {
+    lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
+    hi = std::min(std::ceil(pair_of(beta_slow)), (double)(rotary_dim - 1));
+  }
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(base, -(double)i / half);
+    double r = 0.0;                                // share of the interpolated frequency
+    if (scaling == OSCAR_ROPE_LINEAR) r = 1.0;
+    if (scaling == OSCAR_ROPE_YARN) r = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+    inv_freq[i] = f / factor * r + f * (1.0 - r);
+    if (r == 0.0) inv_freq[i] = f;
+  }
+  *scale = scaling == OSCAR_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return OSCAR_OK;
+}
+
+int oscar_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
+  if (!inv_freq || !turns || n < 1) return OSCAR_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    // f / (2 pi) as the sum of two doubles (2 pi = two_pi + two_pi_lo), so that all 64 bits are meant
+    constexpr double two_pi = 2.0 * M_PI, two_pi_lo = 2.4492935982947064e-16, two64 = 18446744073709551616.0;
+    const double f = inv_freq[i], t = f / two_pi;
+    if (!(t >= 0.0) || !(t < 1.0)) return OSCAR_ERR_INVALID_ARG;
+    const double rest = (std::fma(-t, two_pi, f) - t * two_pi_lo) / two_pi;
+    const double whole = std::floor(t * two64);            // t < 1 has 53 bits: below 2^64
+    turns[i] = (uint64_t)whole + (uint64_t)std::llround(t * two64 - whole + rest * two64);
+  }
+  return OSCAR_OK;
+}
+
+int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+               const int32_t* positions, const uint64_t* turns, int rotary_dim, int layout, float scale, int inverse,
+               void* stream) {
+  if (N < 0 || head_dim < 2 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return OSCAR_ERR_INVALID_ARG;
+  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_FP32 && dtype != OSCAR_DTYPE_FP16) return OSCAR_ERR_INVALID_ARG;
+  if (layout != OSCAR_ROPE_HALF && layout != OSCAR_ROPE_PAIRS) return OSCAR_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || (inverse != 0 && inverse != 1)) return OSCAR_ERR_INVALID_ARG;
+  if (head_dim % 2 || head_dim > 512) return OSCAR_ERR_UNSUPPORTED;
+  oscar_rope_tensor t[2] = {};
+  const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
+  for (int i = 0; i < 2; ++i) {
+    const oscar_rope_tensor* x = i ? k : q;
+    if (!x || x->heads == 0) continue;
+    if (x->heads < 0 || x->in_token < 0 || x->in_head < 0 || x->out_token < 0 || x->out_head < 0) return OSCAR_ERR_INVALID_ARG;
+    if (N > 0 && (!x->in || !x->out)) return OSCAR_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(x->in) | reinterpret_cast<uintptr_t>(x->out)) % size) return OSCAR_ERR_INVALID_ARG;
+    if (x->in == x->out && (x->in_token != x->out_token || x->in_head != x->out_head)) return OSCAR_ERR_INVALID_ARG;
+    t[i] = *x;
+  }
+  if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
+  if (!positions || !turns) return OSCAR_ERR_INVALID_ARG;
+  return launch_rope(t[0], t[1], N, head_dim, rotary_dim, dtype, positions, turns, layout, scale, inverse,
+                     static_cast<cudaStream_t>(stream));
+}
+
+int oscar_tree_workspace_bytes(const oscar_cache* c, int B, int T, int max_hist_pages, size_t* bytes) {
+  if (!c || !bytes || B < 0 || B > c->lay.max_batch || T < 1 || max_hist_pages < 0) return OSCAR_ERR_INVALID_ARG;
+  if (T > kMaxDraft) return OSCAR_ERR_UNSUPPORTED;
+  int ns = 1, nb = 1;
+  tree_splits(B, T, c->lay.num_kv_heads, c->lay.num_q_heads / c->lay.num_kv_heads, (c->lay.sink + c->lay.recent) / kP,
+              max_hist_pages, c->sms, 1 << 20, &ns, &nb);
+  *bytes = std::max(kAlign, align_up((size_t)B * T * c->lay.num_q_heads * (ns + nb) * kPartFloats * sizeof(float)));
+  return OSCAR_OK;
+}
+
+int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q, const void* k_draft,
+                         const void* v_draft, const uint64_t* mask, const int32_t* n_draft, const int32_t* seq_lens,
+                         const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, float sm_scale, void* out,
+                         int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!c || layer < 0 || layer >= c->lay.num_layers || B < 0 || B > c->lay.max_batch || T < 1 || max_hist_pages < 0)
+    return OSCAR_ERR_INVALID_ARG;
+  if (out_dtype != OSCAR_OUT_BF16 && out_dtype != OSCAR_OUT_FP32) return OSCAR_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return OSCAR_ERR_INVALID_ARG;
+  if (T > kMaxDraft || B > 65535) return OSCAR_ERR_UNSUPPORTED;
+  if (B == 0) return OSCAR_OK;
+  if (!q || !k_draft || !v_draft || !mask || !seq_lens || !bf16_pt || !out || !workspace ||
+      (max_hist_pages > 0 && !hist_pt))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out)) return OSCAR_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return OSCAR_ERR_INVALID_ARG;
+  const int hq = c->lay.num_q_heads, hkv = c->lay.num_kv_heads;
+  const size_t slots = workspace_bytes / ((size_t)B * T * hq * kPartFloats * sizeof(float));
+  if (slots < 2) return OSCAR_ERR_INVALID_ARG;
+  TreeArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kd = static_cast<const __nv_bfloat16*>(k_draft);
+  a.vd = static_cast<const __nv_bfloat16*>(v_draft);
+  a.mask = reinterpret_cast<const unsigned long long*>(mask);
+  a.n_draft = n_draft;
+  a.seq_lens = seq_lens;
+  a.hist_pt = hist_pt;
+  a.max_hist_pages = max_hist_pages;
+  a.bf16_pt = bf16_pt;
+  a.T = T;
+  a.W = (T + 63) / 64;
+  tree_splits(B, T, hkv, hq / hkv, (c->lay.sink + c->lay.recent) / kP, max_hist_pages, c->sms,
+              (int)std::min(slots, (size_t)1 << 20), &a.nsplit, &a.nb);
+  a.scale_log2 = sm_scale * kLog2e;
+  a.partials = static_cast<float*>(workspace);
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.lse = lse;
+  return launch_tree_attention(view(c, layer), a, B, static_cast<cudaStream_t>(stream));
+}
+
+int oscar_commit_draft(oscar_cache* c, int layer, int B, int T, const void* k_draft, const void* v_draft,
+                       const int32_t* seq_lens_before, const int32_t* n_accept, int max_accept, const int32_t* path,
+                       const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream) {
+  if (!c || layer < 0 || layer >= c->lay.num_layers || B < 0 || T < 1 || max_hist_pages < 0) return OSCAR_ERR_INVALID_ARG;
+  if (max_accept < 1 || max_accept > c->lay.recent || (!path && max_accept > T)) return OSCAR_ERR_INVALID_ARG;
+  if (B == 0) return OSCAR_OK;
+  if (!k_draft || !v_draft || !seq_lens_before || !n_accept || !bf16_pt || (max_hist_pages > 0 && !hist_pt))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16(k_draft) || !aligned16(v_draft)) return OSCAR_ERR_INVALID_ARG;
+  return launch_commit_draft(view(c, layer), B, T, k_draft, v_draft, seq_lens_before, n_accept, max_accept, path,
+                             hist_pt, max_hist_pages, bf16_pt, static_cast<cudaStream_t>(stream));
 }
 
 int oscar_get_status(oscar_cache* c, int* code) {

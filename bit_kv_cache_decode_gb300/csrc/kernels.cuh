@@ -107,6 +107,26 @@ int launch_merge(const LayerView& lv, const DecodeWorkspace& ws, int B, int nspl
                  int out_dtype, float* lse, cudaStream_t st);
 constexpr int kMergeChunk = 96;            // partial slots staged in shared memory at a time by the merge
 int configure_merge_kernel();
+
+// verifying drafted tokens: rope.cu, tables.cu, tree_attention.cu, tree_merge.cu, commit.cu
+constexpr int kMaxDraft = OSCAR_MAX_DRAFT, kMaxTableBatch = OSCAR_MAX_TABLE_BATCH;
+int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, int dim, int rot, int dtype,
+                const int* positions, const uint64_t* turns, int layout, float scale, int inverse, cudaStream_t st);
+int launch_build_tables(const oscar_layout& lay, int B, const int* old_lens, const int* new_lens, int* hist_pt,
+                        int max_hist_pages, int* bf16_pt, int* free_int2, int* free_bf16, const int* rings_in,
+                        int* rings_out, int* cu_tokens, int* slots, int max_tokens, int* status, unsigned* ticket,
+                        int sms, cudaStream_t st);
+int configure_tables_kernel();
+int launch_tree_layout(int B, int T, const int* parents, const int* n_draft, const int* seq_lens, uint64_t* mask,
+                       int* positions, int* status, cudaStream_t st);
+struct TreeArgs;
+void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
+                 int* nb);
+int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
+int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const void* v, const int* seq_lens,
+                        const int* n_accept, int max_accept, const int* path, const int* hist_pt, int max_hist_pages,
+                        const int* bf16_pt, cudaStream_t st);
+int configure_commit_kernel();
 constexpr int kSharedRows = 128;   // query rows (request x head) per CTA of the shared-prefix decode
 int launch_decode_shared(const LayerView& lv, const DecodeWorkspace& ws, const DecodeArgs& a, cudaStream_t st);
 int configure_shared_kernel();

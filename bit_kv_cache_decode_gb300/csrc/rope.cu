@@ -1,0 +1,179 @@
+// Rotary positions (sm_103a): pairs of a head's channels turned by position * frequency, forward and
+// inverse (the inverse is the gradient: the rotation is orthogonal up to its scale).
+//
+//   (a, b) -> s (a cos t - b sin t, b cos t + a sin t),   t = pos * f,
+//
+// pairs are (i, i + rot/2) (half layout) or (2i, 2i + 1) (pairs layout), i < rot/2; the channels from rot on
+// are passed through.
+//
+// Angles. A float32 product pos * f loses the angle of far positions (at pos 1e5 its half unit is 4e-3
+// radians). The plan therefore holds each frequency as a 64-bit fraction of a turn, F = round(f / (2 pi) 2^64),
+// and the angle is the integer product pos * F modulo 2^64: the full turns fall off by themselves, and the
+// error stays below pos 2^-65 turns. Its upper 32 bits, as a signed number of half turns, go to sincospif.
+//
+// Each (token, pair) angle is computed once per CTA into shared memory and serves all heads. A thread keeps
+// one 16-byte unit of the head and walks the heads, so the kernel moves 16 bytes per access and is bound by
+// memory: every element is read and written once.
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTable = 1024;                   // (cos, sin) entries of a CTA's tokens
+
+struct RopeSide {                                  // q or k
+  const void* in;
+  void* out;
+  long long in_tok, in_head, out_tok, out_head;    // strides in elements
+  int heads;
+};
+struct RopeArgs {
+  RopeSide q, k;
+  const int* positions;
+  const unsigned long long* turns;                 // [rot / 2]
+  int n, dim, rot;
+  int tokens;                                      // tokens per CTA
+  float scale;
+  int inverse;
+};
+
+template <typename T> __device__ __forceinline__ float to_f(T x);
+template <> __device__ __forceinline__ float to_f(float x) { return x; }
+template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+
+// V elements, loaded and stored as one 16-byte access (WIDE) or one by one (rows on any element boundary)
+template <typename T, int V, bool WIDE> struct alignas(WIDE ? sizeof(T) * V : sizeof(T)) Vec { T v[V]; };
+
+// One head's unit u: half layout: V channels from V u of the first half and their partners; pairs layout: V
+// channels (V / 2 pairs) from V u; units past the rotary part copy V channels.
+template <typename T, int V, bool HALF, bool WIDE>
+__device__ __forceinline__ void rope_unit(const T* __restrict__ in, T* __restrict__ out, int u, int rot, int rot_units,
+                                          const float2* cs) {
+  using W = Vec<T, V, WIDE>;
+  if (u >= rot_units) {                            // passed through
+    if (in == out) return;
+    const int at = rot + (u - rot_units) * V;
+    *reinterpret_cast<W*>(out + at) = *reinterpret_cast<const W*>(in + at);
+  } else if (HALF) {
+    const int at = u * V, half = rot / 2;
+    W a = *reinterpret_cast<const W*>(in + at), b = *reinterpret_cast<const W*>(in + at + half);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float x = to_f(a.v[e]), y = to_f(b.v[e]);
+      a.v[e] = from_f<T>(x * cs[e].x - y * cs[e].y);
+      b.v[e] = from_f<T>(y * cs[e].x + x * cs[e].y);
+    }
+    *reinterpret_cast<W*>(out + at) = a;
+    *reinterpret_cast<W*>(out + at + half) = b;
+  } else {
+    const int at = u * V;
+    W a = *reinterpret_cast<const W*>(in + at);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      const float x = to_f(a.v[2 * e]), y = to_f(a.v[2 * e + 1]);
+      a.v[2 * e] = from_f<T>(x * cs[e].x - y * cs[e].y);
+      a.v[2 * e + 1] = from_f<T>(y * cs[e].x + x * cs[e].y);
+    }
+    *reinterpret_cast<W*>(out + at) = a;
+  }
+}
+
+template <typename T, int V, bool HALF, bool WIDE>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a) {
+  __shared__ float2 table[kRopeTable];             // [token][pair]: (cos, sin) times the scale
+  const int half = a.rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
+  for (int i = tid; i < nt * half; i += nthr) {
+    const int t = i / half, j = i - t * half;
+    const int pos = a.positions[t0 + t];
+    const unsigned long long turn = (unsigned long long)(unsigned)pos * a.turns[j];
+    float s, c;
+    sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+    table[i] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
+  }
+  __syncthreads();
+  constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
+  const int rot_units = HALF ? half / V : a.rot / V;
+  const int units = rot_units + (a.dim - a.rot) / V;
+  const int heads = a.q.heads + a.k.heads;
+  for (int u = threadIdx.x; u < units; u += blockDim.x)
+    for (int t = 0; t < nt; ++t) {
+      if (a.positions[t0 + t] < 0) continue;       // a padded row: left as it is
+      float2 cs[kPer];
+      if (u < rot_units) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) cs[e] = table[t * half + u * kPer + e];
+      }
+#pragma unroll 4
+      for (int h = threadIdx.y; h < heads; h += blockDim.y) {
+        const bool isq = h < a.q.heads;
+        const RopeSide& s = isq ? a.q : a.k;
+        const int hh = isq ? h : h - a.q.heads;
+        rope_unit<T, V, HALF, WIDE>(static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + hh * s.in_head,
+                              static_cast<T*>(s.out) + (t0 + t) * s.out_tok + hh * s.out_head, u, a.rot, rot_units, cs);
+      }
+    }
+}
+
+template <typename T, int V, bool HALF, bool WIDE>
+int launch_as(RopeArgs a, cudaStream_t st) {
+  const int half = a.rot / 2;
+  const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / V;
+  // as many tokens as fill the CTA's table, but two CTAs per SM and more while there are tokens for them
+  a.tokens = std::max(1, std::min(kRopeTable / half, a.n / 304));
+  const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
+  k_rope<T, V, HALF, WIDE><<<(a.n + a.tokens - 1) / a.tokens, dim3(bx, by), 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+template <typename T>
+int launch_typed(const RopeArgs& a, bool half_layout, bool wide, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (half_layout) return wide ? launch_as<T, V, true, true>(a, st) : launch_as<T, 1, true, false>(a, st);
+  return wide ? launch_as<T, V, false, true>(a, st) : launch_as<T, 2, false, false>(a, st);
+}
+
+bool vector_ok(const oscar_rope_tensor& t, int size, int v) {
+  if (t.heads == 0) return true;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out);
+  return p % 16 == 0 && t.in_token % v == 0 && t.in_head % v == 0 && t.out_token % v == 0 && t.out_head % v == 0 &&
+         size * v == 16;
+}
+
+RopeSide side(const oscar_rope_tensor& t) {
+  return {t.in, t.out, t.in_token, t.in_head, t.out_token, t.out_head, t.heads};
+}
+
+}  // namespace
+
+int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, int dim, int rot, int dtype,
+                const int* positions, const uint64_t* turns, int layout, float scale, int inverse, cudaStream_t st) {
+  RopeArgs a;
+  a.q = side(q);
+  a.k = side(k);
+  a.positions = positions;
+  a.turns = reinterpret_cast<const unsigned long long*>(turns);
+  a.n = n;
+  a.dim = dim;
+  a.rot = rot;
+  a.scale = scale;
+  a.inverse = inverse;
+  const bool half_layout = layout == OSCAR_ROPE_HALF;
+  // 16-byte units where every row, half and remainder starts on one, else element by element
+  const int size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2, v = 16 / size;
+  const bool wide = vector_ok(q, size, v) && vector_ok(k, size, v) && (half_layout ? rot / 2 : rot) % v == 0 &&
+                    (dim - rot) % v == 0;
+  if (dtype == OSCAR_DTYPE_FP32) return launch_typed<float>(a, half_layout, wide, st);
+  if (dtype == OSCAR_DTYPE_FP16) return launch_typed<__half>(a, half_layout, wide, st);
+  return launch_typed<__nv_bfloat16>(a, half_layout, wide, st);
+}
+
+}  // namespace oscar

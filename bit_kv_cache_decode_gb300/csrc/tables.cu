@@ -1,0 +1,307 @@
+// Page tables, token slots and tree masks built on the GPU (sm_103a), so that a serving loop that keeps its
+// lengths on the device needs no host round trip between steps.
+//
+// k_build_tables. Request r goes from old_lens[r] to new_lens[r] tokens. With H(L) = ceil(max(0, L - sink -
+// recent) / 64) history pages and F(L) = ceil(min(L, sink) / 64) + ceil(clamp(L - sink, 0, recent) / 64) BF16
+// pages, the call pops H(new) - H(old) and F(new) - F(old) page ids from the free rings in (request, page)
+// order, or, for new = 0, pushes the request's pages back. Ids are popped at `head` and pushed at head + count,
+// so entries that are read and entries that are written never overlap and no thread waits for another.
+//
+// Every CTA scans the lengths itself (a few KB, in L2 after the first), then takes its share of the tables and
+// of the new tokens' slots; a slot's page is looked up from the request's table or, for a page popped by this
+// call, from the ring, never from an entry another CTA writes. The last CTA to finish reading writes the new
+// ring positions, which may alias the old ones. The kernel is bound by its launch for small batches and by the
+// 16-byte slot stores for long prompts.
+//
+// k_tree_layout. Ancestor sets by pointer doubling: after step k a node's bit set holds its ancestors within
+// 2^k steps, so T nodes take log2 T steps of one OR per word.
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kTabThreads = 256;
+
+struct TablesArgs {
+  int B, sink, recent;
+  const int *old_lens, *new_lens;
+  int* hist_pt;
+  int max_hist_pages;
+  int* bf16_pt;
+  int nbf;
+  int *free_int2, *free_bf16;
+  int cap_int2, cap_bf16;
+  const int* rings_in;
+  int* rings_out;
+  int* cu_tokens;
+  int4* slots;
+  int max_tokens;
+  int* status;
+  unsigned* ticket;
+};
+
+__device__ __forceinline__ int hist_pages(int L, int sink, int recent) {
+  return (int)(((long long)max(0, L - sink - recent) + kP - 1) / kP);
+}
+__device__ __forceinline__ int bf16_pages(int L, int sink, int recent) {
+  return (min(L, sink) + kP - 1) / kP + (min(max(L - sink, 0), recent) + kP - 1) / kP;
+}
+
+// inclusive block scan of three counts
+__device__ __forceinline__ void block_scan3(long long (&v)[3], long long (*red)[3]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      const long long x = __shfl_up_sync(0xffffffffu, v[e], o);
+      if (lane >= o) v[e] += x;
+    }
+  __syncthreads();
+  if (lane == 31)
+    for (int e = 0; e < 3; ++e) red[w][e] = v[e];
+  __syncthreads();
+  for (int i = 0; i < w; ++i)
+    for (int e = 0; e < 3; ++e) v[e] += red[i][e];
+}
+
+__global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
+  extern __shared__ int smem[];
+  int* tok0 = smem;                                // [B + 1] first new token of a request
+  int* pop_h = tok0 + a.B + 1;                     // [B + 1] history pages popped (pushed: ~) before it
+  int* pop_b = pop_h + a.B + 1;
+  __shared__ long long red[kTabThreads / 32][3];
+  __shared__ int s_ring[4], s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (tid < 4) s_ring[tid] = a.rings_in[tid];
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+
+  // ---- the scan: tokens, pages popped, pages pushed. Released requests count pushes in the upper half. ----
+  long long carry[3] = {0, 0, 0};                  // tokens, history pops | pushes << 32, BF16 pops | pushes << 32
+  int bad = 0;
+  for (int r0 = 0; r0 < a.B; r0 += kTabThreads) {
+    const int r = r0 + tid;
+    long long v[3] = {0, 0, 0};
+    if (r < a.B) {
+      const int o = a.old_lens[r], n = a.new_lens[r];
+      if (o < 0 || n < 0 || (n < o && n != 0) || hist_pages(n, a.sink, a.recent) > a.max_hist_pages ||
+          hist_pages(o, a.sink, a.recent) > a.max_hist_pages) {
+        bad |= OSCAR_STATUS_BAD_SEQLEN;
+      } else {
+        const int ho = hist_pages(o, a.sink, a.recent), hn = hist_pages(n, a.sink, a.recent);
+        const int bo = bf16_pages(o, a.sink, a.recent), bn = bf16_pages(n, a.sink, a.recent);
+        v[0] = max(0, n - o);
+        v[1] = n >= o ? hn - ho : (long long)ho << 32;
+        v[2] = n >= o ? bn - bo : (long long)bo << 32;
+      }
+    }
+    const long long mine[3] = {v[0], v[1], v[2]};
+    block_scan3(v, red);
+    if (r < a.B) {
+      const long long t = carry[0] + v[0] - mine[0], h = carry[1] + v[1] - mine[1], b = carry[2] + v[2] - mine[2];
+      const bool release = mine[1] >> 32 || mine[2] >> 32;
+      tok0[r] = (int)min(t, (long long)0x7fffffff);
+      pop_h[r] = release ? (int)(h >> 32) : (int)h;
+      pop_b[r] = release ? (int)(b >> 32) : (int)b;
+    }
+    for (int e = 0; e < 3; ++e) {
+      long long total = 0;
+      for (int i = 0; i < kTabThreads / 32; ++i) total += red[i][e];
+      carry[e] += total;
+    }
+    __syncthreads();
+  }
+  const int take_h = (int)carry[1], take_b = (int)carry[2], push_h = (int)(carry[1] >> 32), push_b = (int)(carry[2] >> 32);
+  if (tid == 0) tok0[a.B] = (int)min(carry[0], (long long)0x7fffffff);
+  if (carry[0] > (a.slots != nullptr ? a.max_tokens : 0x7fffffff)) bad |= OSCAR_STATUS_BAD_SEQLEN;
+  for (int e = 0; e < 2; ++e) {
+    const int head = s_ring[2 * e], count = s_ring[2 * e + 1], cap = e ? a.cap_bf16 : a.cap_int2;
+    if (head < 0 || count < 0 || count > cap || (cap > 0 && head >= cap) || (e ? push_b : push_h) > cap - count)
+      bad |= OSCAR_STATUS_BAD_PAGE;
+    else if ((e ? take_b : take_h) > count)
+      bad |= OSCAR_STATUS_NO_PAGES;
+  }
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  bad = s_bad;
+  const int total = tok0[a.B];
+
+  if (bad == 0) {
+    auto ring = [](int head, int i, int cap) { return (int)(((long long)head + i) % cap); };
+    // page j of request r, whether it is in the table already or popped by this call
+    auto hist_id = [&](int r, int j, int held) {
+      return j < held ? a.hist_pt[(size_t)r * a.max_hist_pages + j]
+                      : a.free_int2[ring(s_ring[0], pop_h[r] + j - held, a.cap_int2)];
+    };
+    auto bf16_id = [&](int r, int j, int held) {
+      return j < held ? a.bf16_pt[(size_t)r * a.nbf + j] : a.free_bf16[ring(s_ring[2], pop_b[r] + j - held, a.cap_bf16)];
+    };
+    // ---- table entries: one warp per request ----
+    const int warps = gridDim.x * (kTabThreads / 32);
+    for (int r = blockIdx.x * (kTabThreads / 32) + w; r < a.B; r += warps) {
+      const int o = a.old_lens[r], n = a.new_lens[r];
+      const int ho = hist_pages(o, a.sink, a.recent), hn = hist_pages(n, a.sink, a.recent);
+      const int bo = bf16_pages(o, a.sink, a.recent), bn = bf16_pages(n, a.sink, a.recent);
+      if (n >= o) {
+        for (int j = ho + lane; j < hn; j += 32) a.hist_pt[(size_t)r * a.max_hist_pages + j] = hist_id(r, j, ho);
+        for (int j = bo + lane; j < bn; j += 32) a.bf16_pt[(size_t)r * a.nbf + j] = bf16_id(r, j, bo);
+      } else {                                     // released: its pages to the rings' ends
+        for (int j = lane; j < ho; j += 32) {
+          int* e = a.hist_pt + (size_t)r * a.max_hist_pages + j;
+          a.free_int2[ring(s_ring[0], s_ring[1] + pop_h[r] + j, a.cap_int2)] = *e;
+          *e = -1;
+        }
+        for (int j = lane; j < bo; j += 32) {
+          int* e = a.bf16_pt + (size_t)r * a.nbf + j;
+          a.free_bf16[ring(s_ring[2], s_ring[3] + pop_b[r] + j, a.cap_bf16)] = *e;
+          *e = -1;
+        }
+      }
+    }
+    // ---- slots: one new token per thread ----
+    const int stride = gridDim.x * kTabThreads;
+    for (long long t = (long long)blockIdx.x * kTabThreads + tid; t < total && a.slots != nullptr; t += stride) {
+      int lo = 0, hi = a.B - 1;                    // the last request that starts at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tok0[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int r = lo, o = a.old_lens[r], L = a.new_lens[r], pos = o + (int)(t - tok0[r]);
+      const int bo = bf16_pages(o, a.sink, a.recent);
+      int4 s;
+      s.x = pos;
+      if (pos < a.sink) {
+        s.y = 0;
+        s.z = bf16_id(r, pos / kP, bo);
+        s.w = pos % kP;
+      } else if (pos >= L - a.recent) {
+        const int at = (pos - a.sink) % a.recent;
+        s.y = 2;
+        s.z = bf16_id(r, a.sink / kP + at / kP, bo);
+        s.w = at % kP;
+      } else {
+        s.y = 1;
+        s.z = hist_id(r, (pos - a.sink) / kP, hist_pages(o, a.sink, a.recent));
+        s.w = (pos - a.sink) % kP;
+      }
+      a.slots[t] = s;
+    }
+    if (blockIdx.x == 0 && a.cu_tokens != nullptr)
+      for (int r = tid; r <= a.B; r += kTabThreads) a.cu_tokens[r] = tok0[r];
+  } else if (blockIdx.x == 0 && tid == 0) {
+    flag(a.status, bad);
+  }
+  // ---- the new ring positions, by the last CTA that has read the old ones ----
+  __syncthreads();
+  if (tid == 0) {
+    bool last = true;
+    if (gridDim.x > 1) {
+      __threadfence();
+      last = atomicInc(a.ticket, gridDim.x - 1) == gridDim.x - 1;   // wraps to 0: ready for the next call
+    }
+    if (last) {
+      const bool ok = bad == 0;
+      a.rings_out[0] = ok && a.cap_int2 > 0 ? (int)(((long long)s_ring[0] + take_h) % a.cap_int2) : s_ring[0];
+      a.rings_out[1] = s_ring[1] + (ok ? push_h - take_h : 0);
+      a.rings_out[2] = ok && a.cap_bf16 > 0 ? (int)(((long long)s_ring[2] + take_b) % a.cap_bf16) : s_ring[2];
+      a.rings_out[3] = s_ring[3] + (ok ? push_b - take_b : 0);
+    }
+  }
+}
+
+// One CTA per request, one thread per node.
+__global__ void __launch_bounds__(kMaxDraft) k_tree_layout(const int* __restrict__ parents, const int* __restrict__ n_draft,
+                                                           const int* __restrict__ seq_lens, int T, int W,
+                                                           unsigned long long* __restrict__ mask,
+                                                           int* __restrict__ positions, int* status) {
+  __shared__ unsigned long long anc[2][kMaxDraft][kMaxDraft / 64];
+  __shared__ short up[2][kMaxDraft];               // the node 2^k steps above, -1 past the root, -2 past a bad parent
+  const int b = blockIdx.x, i = threadIdx.x;
+  int n = n_draft != nullptr ? n_draft[b] : T;
+  if ((n < 0 || n > T) && i == 0) flag(status, OSCAR_STATUS_BAD_TREE);
+  n = min(max(n, 0), T);
+  const int L = seq_lens[b];
+  if (i < T) {
+    int p = i < n ? parents[(size_t)b * T + i] : -1;
+    if (p < -1 || p >= i) {
+      flag(status, OSCAR_STATUS_BAD_TREE);
+      p = -2;
+    }
+    up[0][i] = (short)p;
+    for (int wd = 0; wd < W; ++wd) anc[0][i][wd] = wd == (i >> 6) ? 1ull << (i & 63) : 0ull;
+  }
+  __syncthreads();
+  int cur = 0;
+  for (int step = 1; step < T; step <<= 1) {
+    if (i < T) {
+      const int p = up[cur][i];
+      for (int wd = 0; wd < W; ++wd) anc[cur ^ 1][i][wd] = anc[cur][i][wd] | (p >= 0 ? anc[cur][p][wd] : 0ull);
+      up[cur ^ 1][i] = p >= 0 ? up[cur][p] : (short)p;
+    }
+    cur ^= 1;
+    __syncthreads();
+  }
+  if (i >= T) return;
+  const bool live = i < n && up[cur][i] != -2;     // T steps up lead past the root, or to a bad parent
+  int depth = 0;
+  for (int wd = 0; wd < W; ++wd) {
+    const unsigned long long m = live ? anc[cur][i][wd] : 0ull;
+    depth += __popcll(m);
+    mask[((size_t)b * T + i) * W + wd] = m;
+  }
+  positions[(size_t)b * T + i] = live ? L + depth - 1 : -1;
+}
+
+}  // namespace
+
+int launch_build_tables(const oscar_layout& lay, int B, const int* old_lens, const int* new_lens, int* hist_pt,
+                        int max_hist_pages, int* bf16_pt, int* free_int2, int* free_bf16, const int* rings_in,
+                        int* rings_out, int* cu_tokens, int* slots, int max_tokens, int* status, unsigned* ticket,
+                        int sms, cudaStream_t st) {
+  TablesArgs a;
+  a.B = B;
+  a.sink = lay.sink;
+  a.recent = lay.recent;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.hist_pt = hist_pt;
+  a.max_hist_pages = max_hist_pages;
+  a.bf16_pt = bf16_pt;
+  a.nbf = (lay.sink + lay.recent) / kP;
+  a.free_int2 = free_int2;
+  a.free_bf16 = free_bf16;
+  a.cap_int2 = lay.num_int2_pages;
+  a.cap_bf16 = lay.num_bf16_pages;
+  a.rings_in = rings_in;
+  a.rings_out = rings_out;
+  a.cu_tokens = cu_tokens;
+  a.slots = reinterpret_cast<int4*>(slots);
+  a.max_tokens = max_tokens;
+  a.status = status;
+  a.ticket = ticket;
+  // a CTA per 1,024 tokens there may be (or per 8 requests), at most one per SM: each scans all lengths
+  const int want = std::max(slots != nullptr ? (max_tokens + 1023) / 1024 : 1, (B + 7) / 8);
+  const int grid = std::max(1, std::min(sms, want));
+  k_build_tables<<<grid, kTabThreads, 3 * (B + 1) * sizeof(int), st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+int configure_tables_kernel() {
+  return cudaFuncSetAttribute(k_build_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              3 * (kMaxTableBatch + 1) * (int)sizeof(int)) == cudaSuccess
+             ? OSCAR_OK
+             : OSCAR_ERR_CUDA;
+}
+
+int launch_tree_layout(int B, int T, const int* parents, const int* n_draft, const int* seq_lens, uint64_t* mask,
+                       int* positions, int* status, cudaStream_t st) {
+  k_tree_layout<<<B, (T + 31) / 32 * 32, 0, st>>>(parents, n_draft, seq_lens, T, (T + 63) / 64,
+                                                  reinterpret_cast<unsigned long long*>(mask), positions, status);
+  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+}  // namespace oscar

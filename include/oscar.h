@@ -52,10 +52,9 @@
  *    OSCAR_META_F16 format (the compact OSCAR_META_U8 format is described with
  *    its define below):
  *      [0, 2048)    K codes, row t at 32 t: channel j in byte j/4, bits 2(j%4)
- *      [2048, 4096) V codes, rows (2p, 2p+1) at 2048 + 64 p; channel octet o
- *                   (channels 8o..8o+7) is the 32-bit word at +4 o whose low
- *                   half is row 2p's two packed bytes (2o, 2o+1) and high half
- *                   row 2p+1's
+ *      [2048, 4096) V codes, channel-major: channel c's 64 codes in the 16 bytes
+ *                   at 2048 + 16 (c ^ ((c >> 4) & 7)); row t in their 32-bit word
+ *                   (t >> 1) & 3 at bit 16 (t & 1) + 4 (t >> 4) + 2 ((t >> 3) & 1)
  *      [4096, 4608) K metadata, row t at 4096 + 8 t: fp16 scale0, zero0,
  *                   scale1, zero1 (group g = channels 64g..64g+63)
  *      [4608, 5120) V metadata, same layout
@@ -97,6 +96,10 @@ extern "C" {
                                          outside +-65504 and was stored saturated (fp16 and
                                          codebook metadata formats; clip thresholds that keep
                                          every group inside +-65504 rule it out) */
+
+#define OSCAR_STATUS_NO_PAGES   32    /* a free ring holds fewer pages than oscar_build_tables
+                                         needs: nothing was changed                          */
+#define OSCAR_STATUS_BAD_TREE   64    /* a draft's parent, node index or node count out of range */
 
 /* V handling (MarkTechPost article, "服务系统：混合精度缓存布局": R_V may be
  * absorbed offline into the value/output projections). */
@@ -326,6 +329,133 @@ int oscar_decode_step_shared(oscar_cache* cache, int layer, int B, const void* q
                              const int32_t* seq_lens_before, const int32_t* hist_pt, int max_hist_pages,
                              int shared_hist_pages, const int32_t* bf16_pt, float sm_scale, void* out, int out_dtype,
                              float* lse, void* stream);
+
+/* ---- verifying drafted tokens --------------------------------------------- */
+
+/* The steps of a speculative decoder's verify call, all on the device and capturable into a CUDA graph:
+ * oscar_build_tables gives the requests their pages, oscar_tree_layout turns the draft's tree into masks and
+ * positions, oscar_rope rotates q and k by them, oscar_tree_attention attends from every drafted node over the
+ * cache and the node's drafted ancestors, and oscar_commit_draft moves the accepted path into the cache. */
+
+#define OSCAR_MAX_DRAFT  256   /* largest T, drafted nodes of a request            */
+#define OSCAR_MAX_TABLE_BATCH 4096   /* largest B of oscar_build_tables            */
+
+/* Page tables and token slots of requests that go from old_lens[r] to new_lens[r] tokens.
+ *  old_lens, new_lens : device int32 [B]. new >= old >= 0 grows the request, new = 0 < old releases it.
+ *  hist_pt, bf16_pt   : the page tables, as everywhere. Entries of pages that the new length adds are written,
+ *                       those of a released request become -1, all others stay.
+ *  free_int2, free_bf16 : device int32 [num_int2_pages], [num_bf16_pages]: rings of free page ids
+ *  rings_in, rings_out  : device int32 [4]: head and count of the INT2 ring, head and count of the BF16 ring
+ *                       (entries head .. head + count - 1 modulo the ring's size are free). Pages are taken at
+ *                       the head in (request, page) order and released to the end. rings_out may be rings_in.
+ *  cu_tokens          : device int32 [B+1] or NULL: first new token of each request, in request order
+ *  slots              : device int32 [max_tokens][4], 16-byte aligned, or NULL: per new token its position, its
+ *                       region (0 sink, 1 history, 2 recent), page id and row, once all new tokens are in.
+ *                       Rows behind the last new token stay as they are.
+ * Pages shared by several requests (prefix caching) have no reference count: do not release them here.
+ * Nothing is changed, and a status bit says why, if a length is negative, shrinks to other than 0 or needs more
+ * than max_hist_pages pages, or the new tokens exceed max_tokens (BAD_SEQLEN), a ring's head or count is out of
+ * range (BAD_PAGE) or a ring is too short (NO_PAGES). One word of the cache's workspace orders the call's CTAs:
+ * as for decode, calls on one cache must not overlap. Errors: INVALID_ARG (B < 0, null pointers, slots not
+ * 16-byte aligned, max_tokens < 0), UNSUPPORTED (B > OSCAR_MAX_TABLE_BATCH), CUDA. */
+int oscar_build_tables(oscar_cache* cache, int B, const int32_t* old_lens, const int32_t* new_lens,
+                       int32_t* hist_pt, int max_hist_pages, int32_t* bf16_pt, int32_t* free_int2,
+                       int32_t* free_bf16, const int32_t* rings_in, int32_t* rings_out, int32_t* cu_tokens,
+                       int32_t* slots, int max_tokens, void* stream);
+
+/* Masks and positions of drafted trees.
+ *  parents   : device int32 [B][T]: the parent of node i, below i, or -1 where it follows the last cached token
+ *  n_draft   : device int32 [B], nodes of each request (0 .. T), or NULL: T
+ *  seq_lens  : device int32 [B], cached tokens
+ *  mask      : device uint64 [B][T][(T + 63) / 64]: bit j of node i's words is set when j is i or above it
+ *  positions : device int32 [B][T]: seq_lens[r] + the number of drafted nodes above i
+ * Nodes from n_draft[r] on, and nodes at or below a parent out of range (BAD_TREE), get an empty mask and
+ * position -1. Errors: INVALID_ARG (B < 0, T < 1, null pointers), UNSUPPORTED (T > OSCAR_MAX_DRAFT), CUDA. */
+int oscar_tree_layout(oscar_cache* cache, int B, int T, const int32_t* parents, const int32_t* n_draft,
+                      const int32_t* seq_lens, uint64_t* mask, int32_t* positions, void* stream);
+
+/* Rotary positions. Plan: the frequency of every pair of channels (host).
+ *  rotary_dim : rotated channels of a head, even; pair i turns by inv_freq[i] radians per position
+ *  base       : inv_freq[i] = base^(-2 i / rotary_dim) before scaling, base > 1
+ *  scaling    : OSCAR_ROPE_NONE; OSCAR_ROPE_LINEAR: all frequencies divided by factor; OSCAR_ROPE_NTK: the base
+ *               times factor^(rotary_dim / (rotary_dim - 2)) (rotary_dim > 2); OSCAR_ROPE_YARN: pairs that turn
+ *               less than beta_slow times in original_length positions are divided by factor, pairs that turn
+ *               more than beta_fast times stay, a linear ramp over the pair index between them; *scale becomes
+ *               0.1 ln(factor) + 1 (1 for the other kinds)
+ *  inv_freq   : host float64 [rotary_dim / 2];  scale : factor of the rotated values
+ * oscar_rope_turns turns frequencies (n of them, 0 <= f < 2 pi) into the table oscar_rope reads, 64-bit fractions
+ * of a turn per position: integer products keep the angle of any position exact to 2^-33 turns. Copy it to the
+ * device once. Errors: INVALID_ARG. */
+#define OSCAR_ROPE_NONE   0
+#define OSCAR_ROPE_LINEAR 1
+#define OSCAR_ROPE_NTK    2
+#define OSCAR_ROPE_YARN   3
+int oscar_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                           double beta_fast, double beta_slow, double* inv_freq, float* scale);
+int oscar_rope_turns(const double* inv_freq, int n, uint64_t* turns);
+
+#define OSCAR_ROPE_HALF  0    /* pair i: channels i and i + rotary_dim / 2 */
+#define OSCAR_ROPE_PAIRS 1    /* pair i: channels 2i and 2i + 1            */
+#define OSCAR_DTYPE_BF16 0
+#define OSCAR_DTYPE_FP32 1
+#define OSCAR_DTYPE_FP16 2
+
+/* [N][heads][head_dim] rows, strides in elements, the channels of a head contiguous. out = in with equal strides
+ * works in place; any other overlap is undefined. */
+typedef struct oscar_rope_tensor {
+  const void* in;
+  void* out;
+  int64_t in_token, in_head, out_token, out_head;
+  int heads;                       /* 0: no such tensor */
+} oscar_rope_tensor;
+
+/* Rotate token n's heads of q and k by positions[n] (device int32 [N]):
+ *   (a, b) -> scale (a cos t - b sin t, b cos t + a sin t), t = position * inv_freq of the pair,
+ * or with -t where inverse is 1: the gradient of the forward rotation. Channels from rotary_dim on are copied.
+ * Rows with a negative position are left as they are. q and k have one dtype (OSCAR_DTYPE_*); products in
+ * float32, one rounding at the end.
+ *  turns : device uint64 [rotary_dim / 2] from oscar_rope_turns
+ * Errors: INVALID_ARG (null pointers, N < 0, negative heads or strides, odd or too large rotary_dim, a bad dtype,
+ * layout or scale), UNSUPPORTED (head_dim odd or above 512), CUDA. Works without a cache. */
+int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+               const int32_t* positions, const uint64_t* turns, int rotary_dim, int layout, float scale, int inverse,
+               void* stream);
+
+/* Attention of drafted nodes over the cache and their drafted ancestors.
+ *  q                : device bf16 [B][T][Hq][128]; k_draft, v_draft : device bf16 [B][T][Hkv][128] (not in the cache)
+ *  mask             : device uint64 [B][T][(T + 63) / 64]: bit j of row i lets node i attend to drafted node j;
+ *                     bits from n_draft[r] on are ignored. Any pattern is allowed (oscar_tree_layout's, a chain, a
+ *                     block), also an empty row, which then attends to the cache alone.
+ *  n_draft          : device int32 [B] (0 .. T), or NULL: T
+ *  seq_lens         : device int32 [B]: cached tokens (>= 0), all visible to every node
+ *  out              : device [B][T][Hq][128], bf16 or fp32 (out_dtype), in the value basis of
+ *                     oscar_decode_attention; lse : device float32 [B][T][Hq] or NULL
+ *  workspace        : device, 256-byte aligned, of oscar_tree_workspace_bytes(cache, B, T, max_hist_pages) bytes; less
+ *                     is accepted down to two slots per query row, B T Hq 1056 bytes, and splits the history less.
+ *                     Calls that may overlap need a workspace each.
+ * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
+ * infinity in a drafted row reaches the rows that attend to it and no others.
+ * The cache is only read. q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
+ * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT), CUDA. */
+int oscar_tree_workspace_bytes(const oscar_cache* cache, int B, int T, int max_hist_pages, size_t* bytes);
+int oscar_tree_attention(oscar_cache* cache, int layer, int B, int T, const void* q, const void* k_draft,
+                         const void* v_draft, const uint64_t* mask, const int32_t* n_draft, const int32_t* seq_lens,
+                         const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, float sm_scale, void* out,
+                         int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Append the accepted drafted tokens: for j < n_accept[r], node path[r][j] at position seq_lens_before[r] + j, with
+ * the bytes that n_accept[r] calls of oscar_append_kv would leave (each demotes the token that leaves the recent
+ * window).
+ *  k_draft, v_draft : device bf16 [B][T][Hkv][128], 16-byte aligned
+ *  n_accept         : device int32 [B], 0 .. max_accept
+ *  path             : device int32 [B][max_accept], or NULL: nodes 0, 1, 2, ... (a ragged append of T tokens)
+ *  max_accept       : 1 .. recent; with a path it may exceed T (a node may be named twice)
+ * A request with a length or count out of range is left as it is (BAD_SEQLEN); a token whose node (BAD_TREE), page
+ * (BAD_PAGE) or history page (BAD_SEQLEN, BAD_PAGE) is out of range is left out. Errors: INVALID_ARG (as
+ * oscar_append_kv, T < 1, max_accept outside 1 .. recent, path NULL with max_accept > T), CUDA. */
+int oscar_commit_draft(oscar_cache* cache, int layer, int B, int T, const void* k_draft, const void* v_draft,
+                       const int32_t* seq_lens_before, const int32_t* n_accept, int max_accept, const int32_t* path,
+                       const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream);
 
 /* Choose the INT2 decode kernel (OSCAR_DECODE_MMA by default). */
 int oscar_set_decode_algo(oscar_cache* cache, int algo);
