@@ -190,6 +190,7 @@ int configure_once() {
   if (rc == OSCAR_OK) rc = configure_decode_kernels();
   if (rc == OSCAR_OK) rc = configure_tables_kernel();
   if (rc == OSCAR_OK) rc = configure_commit_kernel();
+  if (rc == OSCAR_OK) rc = configure_tree_kernels();
   if (rc == OSCAR_OK) g_configured[dev] = true;
   return rc;
 }
@@ -764,7 +765,7 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
     return OSCAR_ERR_INVALID_ARG;
   if (out_dtype != OSCAR_OUT_BF16 && out_dtype != OSCAR_OUT_FP32) return OSCAR_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return OSCAR_ERR_INVALID_ARG;
-  if (T > kMaxDraft || B > 65535) return OSCAR_ERR_UNSUPPORTED;
+  if (T > kMaxDraft || B > 65535 || (c->lay.sink + c->lay.recent) / kP > kMaxTreeBf16Pages) return OSCAR_ERR_UNSUPPORTED;
   if (B == 0) return OSCAR_OK;
   if (!q || !k_draft || !v_draft || !mask || !seq_lens || !bf16_pt || !out || !workspace ||
       (max_hist_pages > 0 && !hist_pt))

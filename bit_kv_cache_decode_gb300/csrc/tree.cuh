@@ -5,6 +5,8 @@
 
 namespace oscar {
 
+constexpr int kMaxTreeBf16Pages = 2040;   // sink and recent pages of a request
+
 struct TreeArgs {
   const __nv_bfloat16 *q, *kd, *vd;       // [B][T][hq][128], [B][T][hkv][128]
   const unsigned long long* mask;         // [B][T][W]: the drafted nodes a node attends to

@@ -436,7 +436,8 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
  * infinity in a drafted row reaches the rows that attend to it and no others.
  * The cache is only read. q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
- * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT), CUDA. */
+ * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT, B > 65535, sink + recent above
+ * 130,560 tokens), CUDA. */
 int oscar_tree_workspace_bytes(const oscar_cache* cache, int B, int T, int max_hist_pages, size_t* bytes);
 int oscar_tree_attention(oscar_cache* cache, int layer, int B, int T, const void* q, const void* k_draft,
                          const void* v_draft, const uint64_t* mask, const int32_t* n_draft, const int32_t* seq_lens,

@@ -9,7 +9,7 @@ if torch.cuda.is_available():
     import bit_kv_cache_decode_gb300 as osc
     from gpu_cases import DEV, build_decode_case, pool_from_device, queries, to_dev_bf16, tokens
 import synth
-from tree_cases import attend, mask_words, random_mask
+from tree_cases import attend, attend_rounded, mask_words, random_mask
 
 
 def draft(seed, B, T, hkv, gq, scale=1.0):
@@ -23,27 +23,22 @@ def dev(x):
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=DEV)
 
 
-def compare(out, lse, case, lens, q, kd, vd, mask, n, v_mode, sm, requests=None):
+def compare(out, lse, case, lens, q, kd, vd, mask, n, v_mode, sm):
     cache, prm, hp, bp = case
     pm = pool_from_device(cache, 0)
     got, lg = out.double().cpu().numpy(), None if lse is None else lse.double().cpu().numpy()
     eps = torch.finfo(out.dtype).eps / 2
-    worst = 0.0
-    for b in range(len(lens)) if requests is None else requests:
+    for b in range(len(lens)):
         k = int(n[b])
         o, l, bound, lb = attend(pm, prm, int(lens[b]), hp[b], bp[b], v_mode == 0, *(x[b, :k].astype(np.float64)
                                  for x in (q, kd, vd)), mask[b, :k, :k], sm)
         off = np.abs(got[b, :k] - o)
         tol = bound + eps * np.abs(o) * (1 + 2 ** -6)
         assert (off <= tol).all(), (b, (off / tol).max())
-        if k and np.abs(o).max() > 0:
-            worst = max(worst, (off.max(-1) / np.maximum(np.abs(o).max(-1), 1e-30)).max())
         if lg is not None:
             fin = np.isfinite(l)
             assert np.array_equal(np.isfinite(lg[b, :k]), fin) and (lg[b, :k][~fin] == -np.inf).all()
             assert (np.abs(lg[b, :k][fin] - l[fin]) <= lb[fin]).all()
-    print(f"worst row error {worst:.2e}")
-    return worst
 
 
 @pytest.mark.parametrize("meta", ["f16", "u8", "cb"])
@@ -120,21 +115,32 @@ def test_peaked_and_diffuse_logits(scale, aligned):
 
 
 def test_long_context_and_error_size():
-    # 20K tokens over many splits; the rows' error stays near the cache's one-token decode
+    # 20K tokens over many splits: the outputs are small means of large values, and the error is what the stated
+    # roundings make, nothing more
     lens, hkv, gq, T = [20011], 1, 4, 24
     case = build_decode_case(lens, hkv, gq, 0, seed=64)
     q, kd, vd = draft(64, 1, T, hkv, gq)
     mask = random_mask(np.random.default_rng(2), 1, T, "tree")
-    cache, _, hp, bp = case
+    cache, prm, hp, bp = case
     args = [to_dev_bf16(x) for x in (q, kd, vd)] + [torch.from_numpy(mask_words(mask)).to(DEV), dev(lens), dev(hp), dev(bp)]
+    ref, sd = attend_rounded(pool_from_device(cache, 0), prm, lens[0], hp[0], bp[0], *(x[0].astype(np.float64) for x in (q, kd, vd)),
+                             mask[0], synth.sm_scale())
+
+    def check(out):
+        compare(out, None, case, lens, q, kd, vd, mask, [T], 0, synth.sm_scale())
+        off = np.abs(out[0].double().cpu().numpy() - ref)
+        # a rotated query channel within float32's error of an fp16 tie may round the other way: 2^-10 of one of 128
+        # products of the logits, a tenth of a deviation of the weights' rounding
+        assert (off <= 8.2 * sd + 2.0 ** -18 * np.abs(ref) + 2.0 ** -21).all(), (off / sd).max()
+
     out = cache.tree_attention(0, *args, synth.sm_scale(), out_dtype=osc.OUT_FP32)
-    assert compare(out, None, case, lens, q, kd, vd, mask, [T], 0, synth.sm_scale()) <= 2e-3
+    check(out)
     again = cache.tree_attention(0, *args, synth.sm_scale(), out_dtype=osc.OUT_FP32)
     assert torch.equal(out, again)                         # no order of summation is left to chance
     need = 1 * T * gq * 2 * 528                            # two slots per row: the history in one piece
     ws = torch.empty(-(-need // 256) * 256, dtype=torch.uint8, device=DEV)
     small = cache.tree_attention(0, *args, synth.sm_scale(), out_dtype=osc.OUT_FP32, workspace=ws)
-    assert compare(small, None, case, lens, q, kd, vd, mask, [T], 0, synth.sm_scale()) <= 2e-3
+    check(small)
     with pytest.raises(osc.OscarError) as e:
         cache.tree_attention(0, *args, synth.sm_scale(), workspace=ws[:need - 1])
     assert e.value.code == osc.ERR_INVALID_ARG
