@@ -774,7 +774,6 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return OSCAR_ERR_INVALID_ARG;
   const int hq = c->lay.num_q_heads, hkv = c->lay.num_kv_heads;
   const size_t slots = workspace_bytes / ((size_t)B * T * hq * kPartFloats * sizeof(float));
-  if (slots < 2) return OSCAR_ERR_INVALID_ARG;
   TreeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.kd = static_cast<const __nv_bfloat16*>(k_draft);
@@ -789,6 +788,7 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   a.W = (T + 63) / 64;
   tree_splits(B, T, hkv, hq / hkv, (c->lay.sink + c->lay.recent) / kP, max_hist_pages, c->sms,
               (int)std::min(slots, (size_t)1 << 20), &a.nsplit, &a.nb);
+  if (a.nsplit == 0) return OSCAR_ERR_INVALID_ARG;   // too little workspace for the history's length
   a.scale_log2 = sm_scale * kLog2e;
   a.partials = static_cast<float*>(workspace);
   a.out = out;

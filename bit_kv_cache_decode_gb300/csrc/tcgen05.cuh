@@ -35,6 +35,42 @@ __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
+// umma, umma_ta and umma_commit for a converged warp that holds the same operands in all its lanes: one elected
+// lane issues (elect.sync picks the same lane every time, so a commit follows its own MMAs). The operands can then
+// stay in uniform registers; a descriptor is given as its low word (address and leading offset) and its constant
+// high word, so that stepping through an operand is one 32-bit add. With operands that the compiler cannot keep
+// uniform an MMA takes 90 to 150 cycles to issue; these take 32, 64 and 128 for N = 64, 128 and 256, the tensor
+// pipe's own pace (measured, M = 128, K = 16, A in tensor memory).
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, bool sw128 = false) {
+  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (sw128 ? 2u << 29 : 0u);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ void umma_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 a, b;\nelect.sync _|q, 0xffffffff;\nsetp.ne.u32 p, %6, 0;\n"
+      "mov.b64 a, {%1, %2};\nmov.b64 b, {%3, %4};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 b;\nelect.sync _|q, 0xffffffff;\nsetp.ne.u32 p, %5, 0;\n"
+      "mov.b64 b, {%2, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }

@@ -6,23 +6,28 @@
 // The T gq query rows of a kv head are the M = 128 rows of a tensor-core tile, so a page is read and unpacked
 // once for all of them.
 //
-// Grid (slot, kv head x row tile, request), one CTA per SM. A slot is a range of the request's history pages in
-// tiles of two pages (128 tokens), or of its BF16 and draft pages in tiles of one (64 tokens). Per tile:
+// Grid (slot, kv head x row tile, request), one CTA per SM. A slot is a range of the request's history pages, or of
+// its BF16 and draft pages. A page (64 tokens) is a tile:
 //  * S = Q K^T, A = the rows in TMEM (history: q R_K as fp16, rotated by this CTA at its start; else q as bf16),
 //    B = the keys in shared memory: history keys dequantised to fp16 (zero + scale code, one rounding).
-//  * row threads (thread = row = TMEM lane): running maximum, weights p = 2^(x - m), their sum in float32. The
-//    maximum moves only when it grows by more than 2^8, so O is seldom rescaled; history weights are fp16 and
-//    carry 2^7 more, so that weights down to 2^-31 of the row's largest still count.
-//  * O += P V, A = P in TMEM, B = the values in shared memory, dequantised like the keys; BF16 tiles take P as two
+//  * row threads (thread = row = TMEM lane): weights p = 2^(x - m) and their sum in float32. m is a reference near
+//    the running maximum, not the maximum: a page whose weights sum to at most 2^15 keeps it (fp16 holds them), any
+//    other sets it to the row's maximum, rescales O and redoes its weights. So no page but the first looks for a
+//    maximum. History weights carry 2^7, so that weights down to 2^-31 of the largest still count.
+//  * O += P V, A = P in TMEM, B = the values in shared memory, dequantised like the keys; BF16 pages take P as two
 //    bf16 parts, since their tokens often carry most of the weight.
 // Values are rounded with their zero point in place: with scale * code alone, the rounding of the products and of
 // the zero point's sum would no longer cancel where many tokens average out.
 //
-// The M128 N128 K16 MMA takes 89 cycles with A in TMEM whatever N up to 128 is (138 for N = 256, 108 with A in
-// shared memory), so a 128-token tile is 16 MMAs, 1,424 cycles; everything else is arranged to fit beside them.
-// TMEM is full: S of two tiles (2 x 128 columns), O (128), P (64), Q (64). Roles: warps 0-3 rows, 4-7 unpack
-// keys, 8-11 unpack values (all double-buffered), 12 issues the MMAs in the order S(i+1), O(i), so that S of the
-// next tile runs while the rows work on this one, 13 streams the pages through a ring of bulk copies.
+// Even and odd pages are two streams with an S, P and O, a reference and a sum each, joined when the slot ends: the
+// row threads of one stream work while the tensor pipe runs the other's products, and neither waits for the
+// other's reference. TMEM is full: O of two streams (2 x 128 columns), S (2 x 64), P (2 x 32), Q (64).
+// Warpgroups: 0-1 rows of the even and odd pages, 2-3 unpack keys, 4-5 unpack values (even and odd pages), 6: warp 24
+// issues S(i + 2), warp 25 streams the pages through a ring of bulk copies, warp 26 turns the
+// values' scales and zeros into the pairs the value warps multiply by, warp 27 issues O(i).
+// A history page is 8 MMAs of M128 N64 K16 (32 cycles each) and 4 of M128 N128 K16 (64): 512 cycles of the tensor
+// pipe. The CUDA cores issue about 570 warp instructions per scheduler and page beside them (rows 210, keys 150,
+// values 165, control 40), which bounds the kernel.
 // Every wait is bounded; a CTA whose wait expires flags OSCAR_STATUS_TIMEOUT and writes empty partials.
 #include <algorithm>
 
@@ -33,40 +38,47 @@
 namespace oscar {
 namespace {
 
-constexpr int kRowWarps = 4, kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kLoadWarp = 13;
-constexpr int kTreeThreads = 14 * 32;
+constexpr int kRowWarps = 8, kKWarp0 = 8, kVWarp0 = 16, kMmaWarp = 24, kLoadWarp = 25, kMetaWarp = 26,
+              kMmaOWarp = 27;
+constexpr int kTreeThreads = 28 * 32;
+// registers per thread: at launch, then of the rows, the unpacking and the control warpgroups; the shares stay within
+// what the CTA was launched with
+constexpr int kRegsLaunch = 72, kRegsRows = 96, kRegsUnpack = 64, kRegsCtl = 56;
+static_assert(2 * kRegsRows + 4 * kRegsUnpack + kRegsCtl <= 7 * kRegsLaunch, "register shares");
 constexpr int kRows = 128;                         // query rows of a CTA
-constexpr int kTok = 2 * kP;                       // tokens of a history tile
-constexpr int kStages = 4;                         // ring stages of one tile (two page blocks)
-constexpr int kStageBytes = 2 * kBlockBytes;
-constexpr int kOpBytes = kTok * kD * 2;            // a tile's unpacked keys or values: 32 KB
-constexpr int kSbo = (kD / 8) * 128;               // K-major, no swizzle: 2,048 B between 8-row blocks
-static_assert(kTok == kD, "keys (rows = tokens) and values (rows = channels) have one geometry");
-constexpr int kSboV64 = (kP / 8) * 128 + 16;       // values of a BF16 tile: 64 tokens, padded against bank conflicts
-constexpr int kOffK = 0, kOffV = kOffK + 2 * kOpBytes, kOffRing = kOffV + 2 * kOpBytes;
+constexpr int kStages = 8;                         // ring stages of one page block
+constexpr int kBufs = 4;                           // unpacked pages: keys, and values
+constexpr int kSboK = (kD / 8) * 128;              // keys: rows = tokens, 128 channels: 2,048 B between 8-row blocks
+constexpr int kSboV = (kP / 8) * 128;              // values: rows = channels, 64 tokens
+constexpr int kSboVNear = kSboV + 16;              // values of a BF16 page, padded against bank conflicts
+constexpr int kKBytes = kP * kD * 2, kVBytes = kD / 8 * kSboVNear + 256;
+static_assert(kVBytes % 256 == 0, "operand alignment");
+constexpr int kImgBytes = kD * kD * 2;             // one part of the rotation
+constexpr int kOffK = 0, kOffV = kOffK + kBufs * kKBytes, kOffRing = kOffV + kBufs * kVBytes;
+static_assert(kBufs * kKBytes >= 2 * kImgBytes && kBufs * kVBytes >= kRows * kD * 2, "the rotation's operands fit");
 constexpr int kPids = 4096;                        // page ids of a slot kept in shared memory
-constexpr int kOffPid = kOffRing + kStages * kStageBytes;
-constexpr int kOffBar = kOffPid + kPids * 4;
-// BF16 slots keep no page ids; the same bytes hold a bit set per tile of the value rows that are not finite
+constexpr int kOffPid = kOffRing + kStages * kBlockBytes;
+// BF16 slots keep no page ids; the same bytes hold a bit set per page of the value rows that are not finite
 constexpr int kPoisonTiles = kPids / 2;
-static_assert(kMaxTreeBf16Pages + kMaxDraft / kP <= kPoisonTiles, "a set for every BF16 and draft tile");
-constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBKFull = kBEmpty + kStages, kBVFull = kBKFull + 2,
-              kBSDone = kBVFull + 2, kBSFree = kBSDone + 2, kBODone = kBSFree + 2, kBPReady = kBODone + 2,
-              kBImg = kBPReady + 1, kBQ = kBImg + 1, kBFinal = kBQ + 1, kNumBars = kBFinal + 1;
+static_assert(kMaxTreeBf16Pages + kMaxDraft / kP <= kPoisonTiles, "a set for every BF16 and draft page");
+// [stage][group][scale, zero][32 token pairs in the order of the values' k positions], fp16 pairs
+constexpr int kMetaStage = 2 * 2 * 32 * 4;
+constexpr int kOffMeta = kOffPid + kPids * 4;
+constexpr int kOffJoin = kOffMeta + kStages * kMetaStage;   // [2 streams][128 rows] (M, l)
+constexpr int kOffBar = kOffJoin + 2 * kRows * 8;
+constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages, kBKFull = kBMeta + kStages,
+              kBVFull = kBKFull + kBufs, kBKFree = kBVFull + kBufs, kBVFree = kBKFree + kBufs, kBSDone = kBVFree + kBufs,
+              kBSFree = kBSDone + 2, kBPReady = kBSFree + 2, kBODone = kBPReady + 2, kBImg = kBODone + 2, kBQ = kBImg + 1,
+              kBFinal = kBQ + 1, kNumBars = kBFinal + 1;
 constexpr int kTreeSmem = kOffBar + kNumBars * 8 + 16 + 1024;   // + TMEM address, flag, alignment slack
-constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kColQ = 448, kTmemCols = 512;
-constexpr uint32_t kIdescF16 = idesc_f16(128, 128);
+constexpr uint32_t kColO = 0, kColS = 256, kColP = 384, kColQ = 448, kTmemCols = 512;   // stream e: + 128 e, 64 e, 32 e
+constexpr uint32_t kIdescS = idesc_f16(128, 64), kIdescO = idesc_f16(128, 128);
 constexpr uint32_t kBf16Bits = (1u << 7) | (1u << 10);              // A and B bf16
-constexpr uint32_t kIdescBf16 = idesc_f16(128, 128) | kBf16Bits, kIdescBf16N64 = idesc_f16(128, 64) | kBf16Bits;
-constexpr float kLazy = 8.f;                       // log2 growth of a maximum that forces a rescale
-constexpr float kBias = 7.f;                       // log2 of the factor of history weights: 2^(8 + 7) fits fp16
+constexpr float kLazy = 8.f;                       // BF16 pages: log2 growth of a maximum that forces a rescale
+constexpr float kBias = 7.f;                       // log2 of the factor of history weights
+constexpr float kMostSum = 32768.f;                // a page's weights may sum to this: each fits fp16
 constexpr uint32_t kMagic = 0x64006400u;           // fp16 1024.0 in both halves
 
-// K-major operand with the 128-byte swizzle (the rotation images)
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
 // the code at position p (0 .. 3) of both 16-bit halves as exact fp16 values: (1024 + c 4^p) 4^-p - 1024 4^-p
 __device__ __forceinline__ uint32_t codes_at(uint32_t x, int p) {
   return hfma2_u(and_or(x, 0x00030003u << (2 * p), kMagic), 0x3C003C00u - (uint32_t)(p * 0x08000800u),
@@ -116,193 +128,223 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // What the roles share.
 struct Ctx {
   uint8_t* smem;
-  uint32_t bar0, tmem;
+  uint32_t bar0;
   volatile int* failed;
-  __device__ uint32_t bar(int k) const { return bar0 + 8u * (uint32_t)k; }
-  // one wait of a whole warp; false ends its work
-  __device__ bool wait(int k, int phase) const {
-    const bool ok = *failed == 0 && mbar_wait(bar(k), (uint32_t)phase & 1u);
+  // the slot's pages: ids in shared memory (-1: out of range), tokens left from its first page on
+  const int* pids;
+  int rest;
+  // all 512 columns are allocated: they start at column 0 (checked). A constant address keeps the MMAs' operands uniform.
+  static constexpr uint32_t tmem = 0;
+  __device__ __forceinline__ uint32_t bar(int k) const { return bar0 + 8u * (uint32_t)k; }
+  // one wait of a whole warp; false (the CTA has failed, or the wait expired) ends its work
+  __device__ __forceinline__ bool wait(int k, int phase) const {
+    const uint32_t parity = (uint32_t)phase & 1u;
+    bool ok = mbar_try(bar(k), parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const unsigned long long t0 = global_ns();     // a small loop: the roles' code shares the instruction caches
+#pragma unroll 1
+    while (!ok && *failed == 0 && global_ns() - t0 <= kWaitNs) ok = mbar_try(bar(k), parity);
     return __all_sync(0xffffffffu, ok);
   }
-  __device__ void arrive(int k) const {
+  __device__ __forceinline__ void arrive(int k) const {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar(k));
   }
+  // valid tokens of history page i of the slot
+  __device__ __forceinline__ int tokens(int i) const { return pids[i] >= 0 ? min(kP, rest - i * kP) : 0; }
 };
 
-// O of this warp's rows times al
-__device__ __forceinline__ void rescale_o(uint32_t trow, float al) {
+// O of this warp's rows, of one stream, times al
+__device__ __forceinline__ void rescale_o(uint32_t to, float al) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float o[32];
-    tmem_ld32(trow + kColO + 32 * c, o);
+    tmem_ld32(to + 32 * c, o);
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] *= al;
-    tmem_st32(trow + kColO + 32 * c, o);
+    tmem_st32(to + 32 * c, o);
   }
 }
 
-// ---- row threads, history tiles ------------------------------------------------------------------------
-// tokens(k): valid tokens of page k of the slot
-template <typename Tokens>
-__device__ __forceinline__ bool rows_history(const Ctx& c, int n, float F, Tokens tokens, float& m, float& lsum) {
-  const uint32_t trow = c.tmem + ((uint32_t)(32 * (threadIdx.x >> 5)) << 16);
-  float2 l2 = make_float2(0.f, 0.f);
-  const float2 F2 = make_float2(F, F);
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1;
-    if (!c.wait(kBSDone + b, i >> 1)) return false;
-    tc_fence_after();
-    const int nv[2] = {tokens(2 * i), tokens(2 * i + 1)};
-    const bool whole = nv[0] == kP && nv[1] == kP;
-    float mx = -INFINITY;
+// ---- row threads, history pages ------------------------------------------------------------------------
+// Weights of 32 tokens from their S columns as fp16 pairs in the k order of the values: pair 4w + p holds tokens
+// 16 (p >> 1) + 2w + 8 (p & 1) and the next. Their sum is added to t2.
+__device__ __forceinline__ void weights32(const float (&s)[32], float2 F2, float2 nm2, uint32_t (&r)[16], float2& t2) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float s[32];
-      tmem_ld32(trow + kColS + 128 * b + 32 * q, s);
-      if (whole) {
+  for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, s[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * (q & 1) + e < nv[q >> 1] ? s[e] : -INFINITY);
-      }
+    for (int p = 0; p < 4; ++p) {
+      const int t = 16 * (p >> 1) + 2 * w + 8 * (p & 1);
+      const float2 x = __ffma2_rn(make_float2(s[t], s[t + 1]), F2, nm2);
+      const float2 v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      t2 = __fadd2_rn(t2, v);
+      r[4 * w + p] = pack_f16x2(v.x, v.y);
     }
-    float al = 1.f;
-    const bool grow = (mx - m) * F > kLazy;
-    if (grow) {
-      al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
-      m = mx;
-    }
-    bool free_o = i == 0;                          // O(i - 1) is complete
-    if (__any_sync(0xffffffffu, grow)) {
-      l2 = __fmul2_rn(l2, make_float2(al, al));
-      if (i > 0) {
-        if (!c.wait(kBODone + ((i - 1) & 1), (i - 1) >> 1)) return false;
-        tc_fence_after();
-        rescale_o(trow, al);
-        free_o = true;
-      }
-    }
-    const float mF = m == -INFINITY ? 0.f : fmaf(m, F, -kBias);
-    const float2 nm2 = make_float2(-mF, -mF);
-#pragma unroll
-    for (int pi = 0; pi < 2; ++pi) {
-      float s[2][32];
-      tmem_ld32x2(trow + kColS + 128 * b + 64 * pi, trow + kColS + 128 * b + 64 * pi + 32, s[0], s[1]);
-      if (pi == 1) {
-        tc_fence_before();
-        c.arrive(kBSFree + b);
-      }
-      if (!whole) {
-#pragma unroll
-        for (int e = 0; e < kP; ++e)
-          if (e >= nv[pi]) s[e >> 5][e & 31] = -INFINITY;
-      }
-      uint32_t r[32];                              // column 8w + p: the weights of tokens t, t + 1
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int t = 16 * (p >> 1) + 2 * w + 8 * (p & 1);
-          const float2 x = __ffma2_rn(make_float2(s[t >> 5][t & 31], s[t >> 5][(t & 31) + 1]), F2, nm2);
-          const float2 v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          l2 = __fadd2_rn(l2, v);
-          r[8 * w + p] = pack_f16x2(v.x, v.y);
-        }
-      if (!free_o) {
-        if (!c.wait(kBODone + ((i - 1) & 1), (i - 1) >> 1)) return false;
-        tc_fence_after();
-        free_o = true;
-      }
-      tmem_st32u(trow + kColP + 32 * pi, r);
-    }
-    tmem_wait_st();
-    tc_fence_before();
-    c.arrive(kBPReady);
-  }
-  lsum = l2.x + l2.y;
-  return true;
 }
 
-// ---- row threads, BF16 and draft tiles -----------------------------------------------------------------
-// bits(i): the tokens of tile i that this row sees
-template <typename Bits>
-__device__ __forceinline__ bool rows_bf16(const Ctx& c, int n, float F, Bits bits, float& m, float& lsum) {
-  const uint32_t trow = c.tmem + ((uint32_t)(32 * (threadIdx.x >> 5)) << 16);
-  const volatile unsigned long long* poison = reinterpret_cast<const unsigned long long*>(c.smem + kOffPid);
+// The pages e, e + 2, ... of the slot.
+__device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F, float& m, float& lsum) {
+  const uint32_t lane0 = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
+  const uint32_t to = c.tmem + lane0 + kColO + 128 * e, ts = c.tmem + lane0 + kColS + 64 * e, tp = c.tmem + lane0 + kColP + 32 * e;
   float l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1;
-    const unsigned long long see = bits(i);
-    if (!c.wait(kBSDone + b, i >> 1) || !c.wait(kBVFull + b, i >> 1)) return false;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int ph = i >> 1, live = c.tokens(i);
+    if (!c.wait(kBSDone + e, ph)) return false;
     tc_fence_after();
-    if (see & poison[i]) l = NAN;                  // a NaN or infinity among the values the row sees
-    float s[2][32];
-    tmem_ld32x2(trow + kColS + 128 * b, trow + kColS + 128 * b + 32, s[0], s[1]);
+    if (live < kP) {                               // the end of the history: its S columns, whatever they are, become -inf
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        float s[32];
+        tmem_ld32(ts + 32 * q, s);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) s[x] = 32 * q + x < live ? s[x] : -INFINITY;
+        tmem_st32(ts + 32 * q, s);
+      }
+    }
+    uint32_t r0[16], r1[16];
+    float sum;
+    bool redone = false, free_o = i < 2;           // O of the stream's last page is complete
+#pragma unroll 1
+    for (;;) {
+      // the page's weights against the reference m
+      const float mF = m == -INFINITY ? 0.f : fmaf(m, F, -kBias);
+      const float2 F2 = make_float2(F, F), nm2 = make_float2(-mF, -mF);
+      float2 t2 = make_float2(0.f, 0.f);
+      {
+        float s0[32], s1[32];
+        tmem_ld32x2(ts, ts + 32, s0, s1);
+        weights32(s0, F2, nm2, r0, t2);
+        weights32(s1, F2, nm2, r1, t2);
+      }
+      sum = t2.x + t2.y;
+      const bool over = !redone && (sum > kMostSum || m == -INFINITY);
+      if (!__any_sync(0xffffffffu, over)) break;
+      redone = true;                               // against the rows' maxima, once
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        float s[32];
+        tmem_ld32(ts + 32 * q, s);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) mx = fmaxf(mx, s[x]);
+      }
+      float al = 1.f;
+      if (over && mx > m) {
+        al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
+        m = mx;
+      }
+      l *= al;
+      if (!free_o) {
+        if (!c.wait(kBODone + e, ph - 1)) return false;
+        tc_fence_after();
+        rescale_o(to, al);
+        free_o = true;
+      }
+    }
     tc_fence_before();
-    c.arrive(kBSFree + b);
-    float mx = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kP; ++e) {
-      if (!(see >> e & 1)) s[e >> 5][e & 31] = -INFINITY;
-      mx = fmaxf(mx, s[e >> 5][e & 31]);
-    }
-    float al = 1.f;
-    const bool grow = (mx - m) * F > kLazy;
-    if (grow) {
-      al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
-      m = mx;
-    }
-    if (i > 0) {
-      if (!c.wait(kBODone + ((i - 1) & 1), (i - 1) >> 1)) return false;
+    c.arrive(kBSFree + e);
+    l += sum;
+    if (!free_o) {                                 // the stream's last O has read the weights before these
+      if (!c.wait(kBODone + e, ph - 1)) return false;
       tc_fence_after();
-      if (__any_sync(0xffffffffu, grow)) rescale_o(trow, al);
     }
-    l *= al;
-    const float mF = m == -INFINITY ? 0.f : m * F;
-    uint32_t hi[32], lo[32];                       // p = hi + lo, pairs of tokens 2j, 2j + 1
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float x = fast_exp2(fmaf(s[j >> 4][2 * (j & 15)], F, -mF)), y = fast_exp2(fmaf(s[j >> 4][2 * (j & 15) + 1], F, -mF));
-      l += x + y;
-      hi[j] = pack_bf16x2(x, y);
-      lo[j] = pack_bf16x2(x - __uint_as_float(hi[j] << 16), y - __uint_as_float(hi[j] & 0xffff0000u));
-    }
-    tmem_st32u(trow + kColP, hi);
-    tmem_st32u(trow + kColP + 32, lo);
+    tmem_st16(tp, r0);
+    tmem_st16(tp + 16, r1);
     tmem_wait_st();
     tc_fence_before();
-    c.arrive(kBPReady);
+    c.arrive(kBPReady + e);
   }
   lsum = l;
   return true;
 }
 
-// ---- key warps, history tiles --------------------------------------------------------------------------
-// Key row t of the tile: the 16-channel block u is one word of codes; k positions 2q, 2q + 1 of the block are
-// channels 16u + q, 16u + 8 + q (the rows' fragments use the same order).
+// ---- row threads, BF16 and draft pages -----------------------------------------------------------------
+// bits(i): the tokens of page i that this row sees. The low parts of the weights go where S was: S(i + 2) waits for O(i).
+template <typename Bits>
+__device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bits bits, float& m, float& lsum) {
+  const uint32_t lane0 = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
+  const uint32_t to = c.tmem + lane0 + kColO + 128 * e, ts = c.tmem + lane0 + kColS + 64 * e, tp = c.tmem + lane0 + kColP + 32 * e;
+  const volatile unsigned long long* poison = reinterpret_cast<const unsigned long long*>(c.smem + kOffPid);
+  float l = 0.f;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int ph = i >> 1;
+    const unsigned long long see = bits(i);
+    if (!c.wait(kBSDone + e, ph) || !c.wait(kBVFull + i % kBufs, i / kBufs)) return false;
+    tc_fence_after();
+    if (see & poison[i]) l = NAN;                  // a NaN or infinity among the values the row sees
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+      float s[32];
+      tmem_ld32(ts + 32 * q, s);
+      const uint32_t mine = (uint32_t)(see >> (32 * q));
+#pragma unroll
+      for (int x = 0; x < 32; ++x) mx = fmaxf(mx, mine >> x & 1u ? s[x] : -INFINITY);
+    }
+    float al = 1.f;
+    const bool grow = (mx - m) * F > kLazy;
+    if (grow) {
+      al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
+      m = mx;
+    }
+    if (__any_sync(0xffffffffu, grow) && i >= 2) { // O of the stream's last page is complete: S(i) waited for it
+      rescale_o(to, al);
+    }
+    l *= al;
+    const float mF = m == -INFINITY ? 0.f : m * F;
+    uint32_t lo[32];                               // p = hi + lo, pairs of tokens 2j, 2j + 1
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float s[32];
+      uint32_t hi[16];
+      tmem_ld32(ts + 32 * q, s);
+      const uint32_t mine = (uint32_t)(see >> (32 * q));
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = mine >> (2 * j) & 1u ? fast_exp2(fmaf(s[2 * j], F, -mF)) : 0.f;
+        const float y = mine >> (2 * j + 1) & 1u ? fast_exp2(fmaf(s[2 * j + 1], F, -mF)) : 0.f;
+        l += x + y;
+        hi[j] = pack_bf16x2(x, y);
+        lo[16 * q + j] = pack_bf16x2(x - __uint_as_float(hi[j] << 16), y - __uint_as_float(hi[j] & 0xffff0000u));
+      }
+      tmem_st16(tp + 16 * q, hi);
+    }
+    tmem_st32u(ts, lo);
+    tmem_wait_st();
+    tc_fence_before();
+    c.arrive(kBPReady + e);
+  }
+  lsum = l;
+  return true;
+}
+
+// ---- key warps, history pages --------------------------------------------------------------------------
+// Key row t: the 16-channel block u is one word of codes; k positions 2q, 2q + 1 of the block are channels 16u + q,
+// 16u + 8 + q (the rows' fragments use the same order).
 template <int FMT>
-__device__ __forceinline__ bool keys_history(const Ctx& c, const LayerView& lv, int h, int n) {
-  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) - kKWarp0;
+__device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, int h, int e, int n) {
+  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3;
   const float* mc = meta_consts(lv, h, 0);
   const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_K) : 0u;
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1, st = i % kStages;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int b = i % kBufs, st = i % kStages;
     if (!c.wait(kBFull + st, i / kStages)) return false;
-    if (i >= 2 && !c.wait(kBSDone + b, (i - 2) >> 1)) return false;
-    uint8_t* dst = c.smem + kOffK + b * kOpBytes;
+    if (i >= kBufs && !c.wait(kBKFree + b, i / kBufs - 1)) return false;
+    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
+    uint8_t* dst = c.smem + kOffK + b * kKBytes;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = (lane & 7) + 8 * (kw + 4 * k), row = t & 63;
-      const uint8_t* blk = c.smem + kOffRing + st * kStageBytes + (t >> 6) * kBlockBytes;
-      const uint2 sz = scale_zero<FMT>(blk, 0, row, mc);
+    for (int k = 0; k < 2; ++k) {
+      const int t = (lane & 7) + 8 * (kw + 4 * k);
+      const uint2 sz = scale_zero<FMT>(blk, 0, t, mc);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int u = (lane >> 3) + 4 * g;
         const uint32_t m = g ? sz.y : sz.x, s2 = __byte_perm(m, m, 0x1010), z2 = __byte_perm(m, m, 0x3232);
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + kKCodesOff + 32 * row + 4 * u), y = x >> 8;
-        uint8_t* d = dst + (t >> 3) * kSbo + (2 * u) * 128 + (t & 7) * 16;
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + kKCodesOff + 32 * t + 4 * u), y = x >> 8;
+        uint8_t* d = dst + (t >> 3) * kSboK + (2 * u) * 128 + (t & 7) * 16;
         *reinterpret_cast<uint4*>(d) = make_uint4(value_at<FMT>(x, 0, lut, s2, z2), value_at<FMT>(x, 1, lut, s2, z2),
                                                   value_at<FMT>(x, 2, lut, s2, z2), value_at<FMT>(x, 3, lut, s2, z2));
         *reinterpret_cast<uint4*>(d + 128) = make_uint4(value_at<FMT>(y, 0, lut, s2, z2), value_at<FMT>(y, 1, lut, s2, z2),
@@ -316,58 +358,65 @@ __device__ __forceinline__ bool keys_history(const Ctx& c, const LayerView& lv, 
   return true;
 }
 
-// ---- value warps, history tiles ------------------------------------------------------------------------
-// Value channel c: word w of its codes holds tokens 16 (p >> 1) + 2w + 8 (p & 1) + e at k positions 16w + 2p + e of
-// the page (the order of the weights' columns). Tokens past the end get scale and zero 0: the block's bytes there
-// may be anything, and 0 times a NaN would reach O.
-template <int FMT, typename Tokens>
-__device__ __forceinline__ bool values_history(const Ctx& c, const LayerView& lv, int h, int n, Tokens tokens) {
-  const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) - kVWarp0, w = lane >> 3, cl = lane & 7;
+// ---- value warps, history pages ------------------------------------------------------------------------
+// Value channel c: word w of its codes holds tokens 16 (p >> 1) + 2w + 8 (p & 1) + e at code positions p. Positions
+// p < 4 are tokens 0 .. 31 of the page, the others tokens 32 .. 63, so token half hf takes the k positions
+// 32 hf + 8w + 2 (p & 3) + e: 16 bytes a word, and the rows store the weights of 32 tokens as 16 columns.
+
+// Warp 26: the scales and zeros of a page as fp16 pairs in that order. Tokens past the end get 0 and 0: the block's
+// bytes there may be anything, and 0 times a NaN would reach O.
+template <int FMT>
+__device__ __forceinline__ bool value_pairs(const Ctx c, const LayerView& lv, int h, int n) {
+  const int lane = threadIdx.x & 31;
+  const int w = (lane >> 2) & 3, p = (lane & 3) + 4 * (lane >> 4), t = 16 * (p >> 1) + 2 * w + 8 * (p & 1);
   const float* mc = meta_consts(lv, h, 0);
-  const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_V) : 0u;
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int b = i & 1, st = i % kStages;
+    const int st = i % kStages, nv = c.tokens(i);
     if (!c.wait(kBFull + st, i / kStages)) return false;
-    if (i >= 2 && !c.wait(kBODone + b, (i - 2) >> 1)) return false;
-    uint8_t* dst = c.smem + kOffV + b * kOpBytes;
+    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
+    uint2 a = scale_zero<FMT>(blk, 1, t, mc), d = scale_zero<FMT>(blk, 1, t + 1, mc);
+    if (t >= nv) a = make_uint2(0u, 0u);
+    if (t + 1 >= nv) d = make_uint2(0u, 0u);
+    uint32_t* m = reinterpret_cast<uint32_t*>(c.smem + kOffMeta + st * kMetaStage) + lane;
+    m[0] = __byte_perm(a.x, d.x, 0x5410);
+    m[32] = __byte_perm(a.x, d.x, 0x7632);
+    m[64] = __byte_perm(a.y, d.y, 0x5410);
+    m[96] = __byte_perm(a.y, d.y, 0x7632);
+    c.arrive(kBMeta + st);
+    if (lane == 0) mbar_arrive(c.bar(kBEmpty + st));
+  }
+  return true;
+}
+
+template <int FMT>
+__device__ __forceinline__ bool values_history(const Ctx c, const LayerView& lv, int h, int e, int n) {
+  // a thread has one word position w and four channels
+  const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) & 3, w = lane >> 3, cl = lane & 7;
+  const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_V) : 0u;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int b = i % kBufs, st = i % kStages;
+    if (!c.wait(kBFull + st, i / kStages) || !c.wait(kBMeta + st, i / kStages)) return false;
+    if (i >= kBufs && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
+    uint8_t* dst = c.smem + kOffV + b * kVBytes;
+    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
+    const uint4* mp = reinterpret_cast<const uint4*>(c.smem + kOffMeta + st * kMetaStage) + w;
 #pragma unroll
-    for (int pi = 0; pi < 2; ++pi) {
-      const uint8_t* blk = c.smem + kOffRing + st * kStageBytes + pi * kBlockBytes;
-      const int nv = tokens(2 * i + pi);
-      uint32_t s2[2][8], z2[2][8];
+    for (int g = 0; g < 2; ++g) {
+      // pairs of positions 0-3 (tokens 0-31) and 4-7 of word w
+      const uint4 s0 = mp[16 * g], s1 = mp[16 * g + 4], z0 = mp[16 * g + 8], z1 = mp[16 * g + 12];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int t = 16 * (p >> 1) + 2 * w + 8 * (p & 1);
-        uint2 a, d;
-        if (FMT == kFmtU8) {
-          a = scale_zero<FMT>(blk, 1, t, mc);
-          d = scale_zero<FMT>(blk, 1, t + 1, mc);
-        } else if (FMT == kFmtCB) {
-          a = scale_zero<FMT>(blk, 1, t, mc);
-          d = scale_zero<FMT>(blk, 1, t + 1, mc);
-        } else {
-          const uint4 m = *reinterpret_cast<const uint4*>(blk + kVMetaOff + 8 * t);
-          a = make_uint2(m.x, m.y);
-          d = make_uint2(m.z, m.w);
-        }
-        if (t >= nv) a = make_uint2(0u, 0u);
-        if (t + 1 >= nv) d = make_uint2(0u, 0u);
-        s2[0][p] = __byte_perm(a.x, d.x, 0x5410);
-        z2[0][p] = __byte_perm(a.x, d.x, 0x7632);
-        s2[1][p] = __byte_perm(a.y, d.y, 0x5410);
-        z2[1][p] = __byte_perm(a.y, d.y, 0x7632);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int ch = cl + 8 * (vw + 4 * j), g = j >> 1;
+      for (int j = 0; j < 2; ++j) {
+        const int ch = cl + 8 * (vw + 4 * j + 8 * g);
         const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + v_chan_off(ch) + 4 * w), y = x >> 8;
-        uint8_t* d = dst + (ch >> 3) * kSbo + (8 * pi + 2 * w) * 128 + (ch & 7) * 16;
+        uint8_t* d = dst + (ch >> 3) * kSboV + w * 128 + (ch & 7) * 16;
         *reinterpret_cast<uint4*>(d) =
-            make_uint4(value_at<FMT>(x, 0, lut, s2[g][0], z2[g][0]), value_at<FMT>(x, 1, lut, s2[g][1], z2[g][1]),
-                       value_at<FMT>(x, 2, lut, s2[g][2], z2[g][2]), value_at<FMT>(x, 3, lut, s2[g][3], z2[g][3]));
-        *reinterpret_cast<uint4*>(d + 128) =
-            make_uint4(value_at<FMT>(y, 0, lut, s2[g][4], z2[g][4]), value_at<FMT>(y, 1, lut, s2[g][5], z2[g][5]),
-                       value_at<FMT>(y, 2, lut, s2[g][6], z2[g][6]), value_at<FMT>(y, 3, lut, s2[g][7], z2[g][7]));
+            make_uint4(value_at<FMT>(x, 0, lut, s0.x, z0.x), value_at<FMT>(x, 1, lut, s0.y, z0.y),
+                       value_at<FMT>(x, 2, lut, s0.z, z0.z), value_at<FMT>(x, 3, lut, s0.w, z0.w));
+        *reinterpret_cast<uint4*>(d + 4 * 128) =
+            make_uint4(value_at<FMT>(y, 0, lut, s1.x, z1.x), value_at<FMT>(y, 1, lut, s1.y, z1.y),
+                       value_at<FMT>(y, 2, lut, s1.z, z1.z), value_at<FMT>(y, 3, lut, s1.w, z1.w));
       }
     }
     fence_async();
@@ -377,20 +426,23 @@ __device__ __forceinline__ bool values_history(const Ctx& c, const LayerView& lv
   return true;
 }
 
-// A BF16 or draft tile: rows 0 .. rows - 1 of K and V at k0, v0, `step` elements apart.
+// A BF16 or draft page: rows 0 .. rows - 1 of K and V at k0, v0, `step` elements apart.
 struct Near {
   const __nv_bfloat16 *k, *v;
   size_t step;
   int rows;
   bool draft;
 };
+// one of the bf16 values of a word is a NaN or an infinity
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return __vcmpeq2(x & 0x7F807F80u, 0x7F807F80u); }
 
-// ---- key warps, BF16 tiles (natural channel order) -----------------------------------------------------
+// ---- key warps, BF16 pages (natural channel order) -----------------------------------------------------
 template <typename Page>
-__device__ __forceinline__ bool keys_bf16(const Ctx& c, int* status, int n, Page page) {
-  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) - kKWarp0;
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1;
+__device__ __forceinline__ bool keys_bf16(const Ctx c, int* status, int e, int n, Page page) {
+  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int b = i % kBufs;
     const Near p = page(i);
     uint4 x[2][4];
 #pragma unroll
@@ -399,57 +451,67 @@ __device__ __forceinline__ bool keys_bf16(const Ctx& c, int* status, int n, Page
       for (int j = 0; j < 4; ++j) {
         const int t = (lane & 7) + 8 * (kw + 4 * k), ck = (lane >> 3) + 4 * j;
         x[k][j] = t < p.rows ? *reinterpret_cast<const uint4*>(p.k + t * p.step + 8 * ck) : make_uint4(0u, 0u, 0u, 0u);
-        if (p.draft && (bf16x2_nonfinite(x[k][j].x) || bf16x2_nonfinite(x[k][j].y) || bf16x2_nonfinite(x[k][j].z) ||
-                        bf16x2_nonfinite(x[k][j].w)))
-          flag(status, OSCAR_STATUS_NONFINITE);
       }
-    if (i >= 2 && !c.wait(kBSDone + b, (i - 2) >> 1)) return false;
+    if (i >= kBufs && !c.wait(kBKFree + b, i / kBufs - 1)) return false;
+    uint32_t bad = 0u;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int t = (lane & 7) + 8 * (kw + 4 * k), ck = (lane >> 3) + 4 * j;
-        *reinterpret_cast<uint4*>(c.smem + kOffK + b * kOpBytes + (t >> 3) * kSbo + ck * 128 + (t & 7) * 16) = x[k][j];
+        bad |= nonfinite2(x[k][j].x) | nonfinite2(x[k][j].y) | nonfinite2(x[k][j].z) | nonfinite2(x[k][j].w);
+        *reinterpret_cast<uint4*>(c.smem + kOffK + b * kKBytes + (t >> 3) * kSboK + ck * 128 + (t & 7) * 16) = x[k][j];
       }
+    if (bad != 0u && p.draft) flag(status, OSCAR_STATUS_NONFINITE);
     fence_async();
     c.arrive(kBKFull + b);
   }
   return true;
 }
 
-// ---- value warps, BF16 tiles: transposed, non-finite values replaced by 0 and their rows noted ----------
+// ---- value warps, BF16 pages: transposed, non-finite values replaced by 0 and their rows noted ----------
 template <typename Page>
-__device__ __forceinline__ bool values_bf16(const Ctx& c, int* status, int n, Page page) {
-  const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) - kVWarp0;
+__device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int n, Page page) {
+  const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) & 3;
   unsigned long long* poison = reinterpret_cast<unsigned long long*>(c.smem + kOffPid);
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1;
+#pragma unroll 1
+  for (int i = e; i < n; i += 2) {
+    const int b = i % kBufs;
     const Near p = page(i);
-    uint32_t x[4][8];                              // [octet, channel half][token]: channels 2 cp, 2 cp + 1
+    uint32_t x[4][8];                              // [token octet, channel half][token]: channels 2 cp, 2 cp + 1
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = 8 * (vw + 4 * (k >> 1)) + e, cp = lane + 32 * (k & 1);
-        x[k][e] = t < p.rows ? *reinterpret_cast<const uint32_t*>(p.v + t * p.step + 2 * cp) : 0u;
+      for (int t = 0; t < 8; ++t) {
+        const int row = 8 * (vw + 4 * (k >> 1)) + t, cp = lane + 32 * (k & 1);
+        x[k][t] = row < p.rows ? *reinterpret_cast<const uint32_t*>(p.v + row * p.step + 2 * cp) : 0u;
       }
-    if (i >= 2 && !c.wait(kBODone + b, (i - 2) >> 1)) return false;
+    if (i >= kBufs && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
+    uint32_t bad = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) bad |= nonfinite2(x[k][t]);
+    if (bad != 0u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (nonfinite2(x[k][t])) {
+            atomicOr(poison + i, 1ull << (8 * (vw + 4 * (k >> 1)) + t));
+            x[k][t] = 0u;
+          }
+      if (p.draft) flag(status, OSCAR_STATUS_NONFINITE);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (bf16x2_nonfinite(x[k][e])) {
-          if (p.draft) flag(status, OSCAR_STATUS_NONFINITE);
-          atomicOr(poison + i, 1ull << (8 * (vw + 4 * (k >> 1)) + e));
-          x[k][e] = 0u;
-        }
       const int o = vw + 4 * (k >> 1), ch = 2 * (lane + 32 * (k & 1));
-      uint8_t* d = c.smem + kOffV + b * kOpBytes + (ch >> 3) * kSboV64 + o * 128 + (ch & 7) * 16;
+      uint8_t* d = c.smem + kOffV + b * kVBytes + (ch >> 3) * kSboVNear + o * 128 + (ch & 7) * 16;
       uint32_t lo[4], hi[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo[e] = __byte_perm(x[k][2 * e], x[k][2 * e + 1], 0x5410);
-        hi[e] = __byte_perm(x[k][2 * e], x[k][2 * e + 1], 0x7632);
+      for (int t = 0; t < 4; ++t) {
+        lo[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x5410);
+        hi[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x7632);
       }
       *reinterpret_cast<uint4*>(d) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       *reinterpret_cast<uint4*>(d + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -465,7 +527,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int slot = blockIdx.x, h = blockIdx.y % lv.hkv, qt = blockIdx.y / lv.hkv, b = blockIdx.z;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int gq = lv.hq / lv.hkv;
   const bool hist = slot < a.nsplit;
   pdl_wait();
@@ -495,38 +557,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     Lh = np * kP;
   }
   const int nbf = (lv.sink + lv.recent) / kP, near_pages = nbf + (nodes + kP - 1) / kP;
-  int p0, cnt;                                     // first page and number of pages of the slot
+  int p0, n;                                       // first page and number of pages of the slot
   if (hist) {
     p0 = (int)((long long)slot * np / a.nsplit);
-    cnt = (int)((long long)(slot + 1) * np / a.nsplit) - p0;
+    n = (int)((long long)(slot + 1) * np / a.nsplit) - p0;
   } else {
     p0 = (slot - a.nsplit) * near_pages / a.nb;
-    cnt = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
+    n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
   }
-  const int n = hist ? (cnt + 1) / 2 : cnt;        // tiles
-  const int* pt = a.hist_pt + (size_t)b * a.max_hist_pages + p0;
-  auto checked = [&](int id) { return id >= 0 && id < lv.n_int2 ? id : -1; };
-  auto page_id = [&](int k) { return k < kPids ? pids[k] : checked(__ldg(pt + k)); };
-  auto tokens = [&](int k) { return k < cnt && page_id(k) >= 0 ? min(kP, Lh - (p0 + k) * kP) : 0; };
+  c.pids = pids;
+  c.rest = Lh - p0 * kP;
 
   const int active = (live + 31) / 32;             // row warps with rows
-  if (w == kMmaWarp) {
+  if (w == kLoadWarp) {
     if (lane == 0) {
+      mbar_init_n(c.bar(kBImg), 1);
       for (int s = 0; s < kStages; ++s) {
         mbar_init_n(c.bar(kBFull + s), 1);
-        mbar_init_n(c.bar(kBEmpty + s), 8);
+        mbar_init_n(c.bar(kBEmpty + s), 4 + 4 + 1);  // a key and a value warpgroup, warp 26
+        mbar_init_n(c.bar(kBMeta + s), 1);
       }
-      for (int j = 0; j < 2; ++j) {
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      if (hist && n > 0) {                         // the rotation, requested before anything else is known
+        const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
+        mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
+        for (int p = 0; p < 2; ++p)                // R = b1 + b2 to about 17 bits
+          bulk_copy_hint(smem_addr(smem + kOffK + p * kImgBytes), img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
+      }
+    }
+    __syncwarp();
+  } else if (w == kMmaWarp) {
+    if (lane == 0) {
+      for (int j = 0; j < kBufs; ++j) {
         mbar_init_n(c.bar(kBKFull + j), 4);
         mbar_init_n(c.bar(kBVFull + j), 4);
+        mbar_init_n(c.bar(kBKFree + j), 1);
+        mbar_init_n(c.bar(kBVFree + j), 1);
+      }
+      for (int j = 0; j < 2; ++j) {
         mbar_init_n(c.bar(kBSDone + j), 1);
         mbar_init_n(c.bar(kBSFree + j), active);
+        mbar_init_n(c.bar(kBPReady + j), active);
         mbar_init_n(c.bar(kBODone + j), 1);
       }
-      mbar_init_n(c.bar(kBPReady), active);
-      mbar_init_n(c.bar(kBImg), 1);
       mbar_init_n(c.bar(kBQ), 1);
-      mbar_init_n(c.bar(kBFinal), 1);
+      mbar_init_n(c.bar(kBFinal), 2);                // both issuing warps
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       *c.failed = 0;
     }
@@ -535,92 +610,81 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (hist && w >= kKWarp0) {
-    // page ids, those out of range as -1
-    const int step = kTreeThreads - 32 * (kKWarp0 + 1);          // the threads of warps 4 .. 11 and 13
-    const int at = w == kLoadWarp ? 8 * 32 + lane : tid - 32 * kKWarp0;
-    for (int k = at; k < cnt && k < kPids; k += step) {
-      const int id = checked(__ldg(pt + k));
-      if (id < 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
-      pids[k] = id;
-    }
   } else if (w >= kKWarp0 && w < kMmaWarp) {
-    for (int k = tid - 32 * kKWarp0; k < 2 * n; k += 32 * 8) pids[k] = 0;   // the tiles' sets of non-finite rows
+    const int at = tid - 32 * kKWarp0, step = 32 * (kMmaWarp - kKWarp0);
+    if (hist) {                                    // page ids, those out of range as -1
+      const int* pt = a.hist_pt + (size_t)b * a.max_hist_pages + p0;
+      for (int k = at; k < n; k += step) {         // at most kPids, see tree_splits
+        int id = __ldg(pt + k);
+        if (id < 0 || id >= lv.n_int2) {
+          flag(lv.status, OSCAR_STATUS_BAD_PAGE);
+          id = -1;
+        }
+        pids[k] = id;
+      }
+    } else {                                       // the tiles' sets of non-finite rows
+      for (int k = at; k < 2 * n; k += step) pids[k] = 0;
+    }
   }
-  // ---- the rows: history tiles stage q for the rotation, BF16 tiles keep it -------------------------------
-  const int row = tid, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;   // row threads
-  uint4 q4[16];
+  // ---- the rows' q, staged where the values go: the rotation's A operand ----------------------------------
+  // thread = row; the odd pages' warpgroup takes the upper half of the channels
+  const int row = tid & (kRows - 1), half = (tid >> 7) & 1, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;
+  uint8_t* const qs = smem + kOffV + (row >> 3) * kSboK + (row & 7) * 16;
   if (w < kRowWarps && n > 0) {
     const uint4* src = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + node) * lv.hq + hq) * kD);
+    uint32_t bad = 0u;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      q4[j] = row < live ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-      if (bf16x2_nonfinite(q4[j].x) || bf16x2_nonfinite(q4[j].y) || bf16x2_nonfinite(q4[j].z) || bf16x2_nonfinite(q4[j].w))
-        flag(lv.status, OSCAR_STATUS_NONFINITE);
+    for (int j = 0; j < 8; ++j) {
+      const uint4 x = row < live ? src[8 * half + j] : make_uint4(0u, 0u, 0u, 0u);
+      bad |= nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w);
+      *reinterpret_cast<uint4*>(qs + (8 * half + j) * 128) = x;
     }
-    if (hist) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        *reinterpret_cast<uint4*>(smem + kOffV + (row >> 3) * kSbo + j * 128 + (row & 7) * 16) = q4[j];
-      fence_async();
-    }
+    if (bad != 0u) flag(lv.status, OSCAR_STATUS_NONFINITE);
+    fence_async();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  c.tmem = *tmem_slot;
+  bool ok = *tmem_slot == c.tmem;
 
-  auto issue_tile = [&](int i) {                   // tile i into ring stage i % kStages (one thread)
-    const int st = i % kStages;
-    int id[2];
-    uint32_t bytes = 0;
-    for (int j = 0; j < 2; ++j) {
-      id[j] = 2 * i + j < cnt ? page_id(2 * i + j) : -1;
-      if (id[j] >= 0) bytes += (uint32_t)lv.blk_bytes;
-    }
-    mbar_expect_tx(c.bar(kBFull + st), bytes);     // also with no page: the phase completes
-    const uint64_t pol = l2_evict_first();
-    for (int j = 0; j < 2; ++j)
-      if (id[j] >= 0)
-        bulk_copy_hint(smem_addr(smem + kOffRing + st * kStageBytes + j * kBlockBytes), int2_block(lv, id[j], h),
-                       (uint32_t)lv.blk_bytes, c.bar(kBFull + st), pol);
+  auto issue_page = [&](int i) {                   // page i into ring stage i % kStages (one thread)
+    const int st = i % kStages, id = pids[i];
+    mbar_expect_tx(c.bar(kBFull + st), id >= 0 ? (uint32_t)lv.blk_bytes : 0u);   // also for no page: the phase completes
+    if (id >= 0)
+      bulk_copy_hint(smem_addr(smem + kOffRing + st * kBlockBytes), int2_block(lv, id, h), (uint32_t)lv.blk_bytes,
+                     c.bar(kBFull + st), l2_evict_first());
   };
 
   // ---- the rows' A operand in TMEM -------------------------------------------------------------------------
   float F = a.scale_log2;
-  bool ok = true;
-  if (n > 0 && hist) {
+  if (ok && n > 0 && hist) {
     if (w == kLoadWarp) {
-      if (lane == 0) {
-        const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
-        mbar_expect_tx(c.bar(kBImg), 2 * kOpBytes);
-        for (int p = 0; p < 2; ++p)                // R = b1 + b2 to about 17 bits
-          bulk_copy_hint(smem_addr(smem + kOffK + p * kOpBytes), img + p * kOpBytes, kOpBytes, c.bar(kBImg), l2_evict_last());
-        for (int i = 0; i < min(n, kStages); ++i) issue_tile(i);
-      }
+      if (lane == 0)
+        for (int i = 0; i < min(n, kStages); ++i) issue_page(i);
       __syncwarp();
     } else if (w == kMmaWarp) {
       ok = c.wait(kBImg, 0);
-      if (ok && lane == 0) {
+      if (ok) {
         tc_fence_after();
         const uint32_t a0 = smem_addr(smem + kOffV), b0 = smem_addr(smem + kOffK);
+#pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma(c.tmem + kColS, umma_desc(a0 + kk * 256, 128, kSbo),
-                 desc_sw128(b0 + p * kOpBytes + (kk >> 2) * (kOpBytes / 2) + (kk & 3) * 32), kIdescBf16, (p | kk) != 0);
-        umma_commit(c.bar(kBQ));
+            umma_warp(c.tmem + kColO, desc_lo(a0, 128) + 16 * kk, desc_hi(kSboK),
+                      desc_lo(b0, 16) + (p * kImgBytes + (kk >> 2) * (kImgBytes / 2) + (kk & 3) * 32) / 16, desc_hi(1024, true),
+                      kIdescO | kBf16Bits, (p | kk) != 0);
+        umma_commit_warp(c.bar(kBQ));
       }
-      __syncwarp();
     } else if (w < kRowWarps) {
       ok = c.wait(kBQ, 0);
       if (ok) {
         tc_fence_after();
-        const uint32_t trow = c.tmem + ((uint32_t)(32 * w) << 16);
+        const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16);
         float y[32], mx = 0.f;
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          tmem_ld32(trow + kColS + 32 * k, y);
+          tmem_ld32(trow + kColO + 32 * k, y);
 #pragma unroll
           for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(y[e]));
         }
@@ -630,8 +694,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
         const float sc = exp2f((float)sigma);
         F *= exp2f((float)-sigma);
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          tmem_ld32(trow + kColS + 32 * k, y);
+        for (int k = 2 * half; k < 2 * half + 2; ++k) {
+          tmem_ld32(trow + kColO + 32 * k, y);
           uint32_t r[16];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -642,13 +706,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
         tmem_wait_st();
       }
     }
-  } else if (n > 0 && w < kRowWarps) {
-    const uint32_t trow = c.tmem + ((uint32_t)(32 * w) << 16);
+  } else if (ok && n > 0 && w < kRowWarps) {
+    const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16);
+#pragma unroll 1
+    for (int k = 2 * half; k < 2 * half + 2; ++k) {
+      uint32_t r[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t r[16] = {q4[4 * k].x, q4[4 * k].y, q4[4 * k].z, q4[4 * k].w, q4[4 * k + 1].x, q4[4 * k + 1].y,
-                              q4[4 * k + 1].z, q4[4 * k + 1].w, q4[4 * k + 2].x, q4[4 * k + 2].y, q4[4 * k + 2].z,
-                              q4[4 * k + 2].w, q4[4 * k + 3].x, q4[4 * k + 3].y, q4[4 * k + 3].z, q4[4 * k + 3].w};
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(qs + (4 * k + j) * 128);
+        r[4 * j] = x.x;
+        r[4 * j + 1] = x.y;
+        r[4 * j + 2] = x.z;
+        r[4 * j + 3] = x.w;
+      }
       tmem_st16(trow + kColQ + 16 * k, r);
     }
     tmem_wait_st();
@@ -682,86 +752,141 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     return r;
   };
 
-  float m = -INFINITY, lsum = 0.f;
-  ok = *c.failed == 0;
-  if (ok) {
-    if (w < kRowWarps) {
-      if (w < active) {
-        if (hist) {
-          ok = rows_history(c, n, F, tokens, m, lsum);
-        } else {
-          auto bits = [&](int i) -> unsigned long long {
-            const Near p = near(i);
-            unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
-            if (p.draft) see &= row < live ? a.mask[((size_t)b * a.T + node) * a.W + (p0 + i - nbf)] : 0ull;
-            return see;
-          };
-          ok = rows_bf16(c, n, F, bits, m, lsum);
-        }
-        if (ok && n > 0) ok = c.wait(kBODone + ((n - 1) & 1), (n - 1) >> 1);
-      }
-    } else if (w < kVWarp0) {
-      ok = hist ? keys_history<FMT>(c, lv, h, n) : keys_bf16(c, lv.status, n, near);
-    } else if (w < kMmaWarp) {
-      ok = hist ? values_history<FMT>(c, lv, h, n, tokens) : values_bf16(c, lv.status, n, near);
-    } else if (w == kLoadWarp) {
+  // ---- the control warps: page stream, scale pairs, MMAs ----
+  auto control = [&](int w) -> bool {
+    if (w == kLoadWarp) {
+      bool fine = true;
       if (hist)
-        for (int i = kStages; i < n && ok; ++i) {
-          ok = c.wait(kBEmpty + i % kStages, i / kStages - 1);
-          if (ok && lane == 0) issue_tile(i);
+        for (int i = kStages; i < n && fine; ++i) {
+          fine = c.wait(kBEmpty + i % kStages, i / kStages - 1);
+          if (fine && lane == 0) issue_page(i);
           __syncwarp();
         }
-    } else {
-      // ---- the MMAs: S(0), then S(i + 1) and O(i) ----
-      const uint32_t k0 = smem_addr(smem + kOffK), v0 = smem_addr(smem + kOffV);
-      auto issue_s = [&](int i) {
-        const uint32_t kb = k0 + (i & 1) * kOpBytes, d = c.tmem + kColS + 128 * (i & 1);
+      return fine;
+    }
+    if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, lv, h, n);
+    // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4 and stream i & 1
+    static_assert(kBufs == 4, "two pages of each stream");
+    const uint32_t more = hist ? 0u : kBf16Bits;
+    if (w == kMmaWarp) {
+      const uint32_t kd = desc_lo(smem_addr(smem + kOffK), 128);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int b = i % kBufs, e = i & 1;
+        if (!c.wait(kBKFull + b, i / kBufs)) return false;
+        // S(i - 2) is out of the way: read, or (BF16 pages, whose weights' low parts follow it there) used by O(i - 2)
+        if (i >= 2 && !c.wait((hist ? kBSFree : kBODone) + e, (i - 2) >> 1)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_ta(d, c.tmem + kColQ + 8 * kk, umma_desc(kb + kk * 256, 128, kSbo), hist ? kIdescF16 : kIdescBf16N64, kk > 0);
-        umma_commit(c.bar(kBSDone + (i & 1)));
-      };
-      auto issue_o = [&](int i) {
-        const uint32_t vb = v0 + (i & 1) * kOpBytes;
-        if (hist) {
+          umma_ta_warp(c.tmem + kColS + 64 * e, c.tmem + kColQ + 8 * kk, kd + b * (kKBytes >> 4) + 16 * kk, desc_hi(kSboK),
+                       kIdescS | more, kk > 0);
+        umma_commit_warp(c.bar(kBSDone + e));
+        umma_commit_warp(c.bar(kBKFree + b));
+      }
+    } else {
+      const uint32_t vd = desc_lo(smem_addr(smem + kOffV), 128), vh = hist ? desc_hi(kSboV) : desc_hi(kSboVNear);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int b = i % kBufs, e = i & 1;
+        if (!c.wait(kBVFull + b, i / kBufs) || !c.wait(kBPReady + e, i >> 1)) return false;
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ta(c.tmem + kColO, c.tmem + kColP + 8 * kk, umma_desc(vb + kk * 256, 128, kSbo), kIdescF16, (i | kk) != 0);
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColP + 32 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                       kIdescO | more, i > 1 || kk > 0);
+        if (!hist) {                               // the weights' low parts
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColS + 64 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                         kIdescO | more, true);
+        }
+        umma_commit_warp(c.bar(kBODone + e));
+        umma_commit_warp(c.bar(kBVFree + b));
+      }
+    }
+    return true;
+  };
+
+  ok = *c.failed == 0;
+  const int e = (w >> 2) & 1;                      // the stream of this warpgroup (rows, keys, values)
+  if (w < kRowWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+    if ((w & 3) < active) {
+      float m = -INFINITY, lsum = 0.f;
+      if (ok && hist) {
+        ok = rows_history(c, e, n, F, m, lsum);
+      } else if (ok) {
+        auto bits = [&](int i) -> unsigned long long {
+          const Near p = near(i);
+          unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
+          if (p.draft) see &= row < live ? a.mask[((size_t)b * a.T + node) * a.W + (p0 + i - nbf)] : 0ull;
+          return see;
+        };
+        ok = rows_bf16(c, e, n, F, bits, m, lsum);
+      }
+      const int last = n - 1 - ((n - 1 - e) & 1);            // the stream's last page
+      if (ok && e < n) ok = c.wait(kBODone + e, last >> 1);
+      // the sums of both streams, for the join
+      const float ref = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
+      reinterpret_cast<float2*>(smem + kOffJoin)[e * kRows + row] = make_float2(ref, lsum);
+      // ---- partials: thread = row, a warpgroup per half of the channels; the streams' O joined. Both streams' row
+      // warps meet first (each has waited for its stream's last product); a CTA that failed writes empty ones ----
+      if (!ok) *c.failed = 1;
+      tc_fence_before();
+      asm volatile("bar.sync 1, %0;" ::"r"(64 * active) : "memory");
+      tc_fence_after();
+      const bool good = *c.failed == 0 && n > 0;
+      const float2* join = reinterpret_cast<const float2*>(smem + kOffJoin) + row;
+      const float2 j0 = join[0], j1 = n > 1 ? join[kRows] : make_float2(-INFINITY, 0.f);
+      const float M = fmaxf(j0.x, j1.x);
+      const float w0 = j0.x == -INFINITY ? 0.f : exp2f(j0.x - M), w1 = j1.x == -INFINITY ? 0.f : exp2f(j1.x - M);
+      float* part = tree_part(a, lv.hq, b, min(node, a.T - 1), hq, slot);
+      const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO;
+      if (row < live && half == 0)
+        *reinterpret_cast<float2*>(part) = good ? make_float2(M, w0 * j0.y + w1 * j1.y) : make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+      for (int k = 2 * half; k < 2 * half + 2; ++k) {
+        float x[32], y[32];
+        if (__all_sync(0xffffffffu, good)) {
+          if (n > 1) {
+            tmem_ld32x2(to + 32 * k, to + 128 + 32 * k, x, y);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) x[t] = w0 * x[t] + w1 * y[t];
+          } else {
+            tmem_ld32(to + 32 * k, x);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) x[t] *= w0;
+          }
         } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)           // high parts, then low parts
-            umma_ta(c.tmem + kColO, c.tmem + kColP + 8 * kk, umma_desc(vb + (kk & 3) * 256, 128, kSboV64), kIdescBf16,
-                    (i | kk) != 0);
+          for (int t = 0; t < 32; ++t) x[t] = 0.f;
         }
-        umma_commit(c.bar(kBODone + (i & 1)));
-      };
-      for (int i = -1; i < n && ok; ++i) {
-        if (i + 1 < n) {
-          const int j = i + 1;
-          ok = c.wait(kBKFull + (j & 1), j >> 1);
-          if (ok && j >= 2) ok = c.wait(kBSFree + (j & 1), (j - 2) >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) issue_s(j);
-          __syncwarp();
-        }
-        if (i >= 0) {
-          ok = c.wait(kBVFull + (i & 1), i >> 1) && c.wait(kBPReady, i);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) issue_o(i);
-          __syncwarp();
+        if (row < live) {
+#pragma unroll
+          for (int t = 0; t < 32; t += 4)
+            *reinterpret_cast<float4*>(part + 4 + 32 * k + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
         }
       }
     }
+  } else if (w < kVWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    if (ok) ok = hist ? keys_history<FMT>(c, lv, h, e, n) : keys_bf16(c, lv.status, e, n, near);
+  } else if (w < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    if (ok) ok = hist ? values_history<FMT>(c, lv, h, e, n) : values_bf16(c, lv.status, e, n, near);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (ok) ok = control(w);
   }
   if (!ok) {
-    if (*c.failed == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
+    if (lane == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
     *c.failed = 1;
   }
-  if (w == kMmaWarp && lane == 0) {                // every MMA completes before TMEM is read or released
-    umma_commit(c.bar(kBFinal));
+  if (w == kMmaWarp || w == kMmaOWarp) {           // every MMA completes before TMEM is read or released
+    umma_commit_warp(c.bar(kBFinal));
     mbar_wait(c.bar(kBFinal), 0);
+    __syncwarp();
   }
   if (w == kLoadWarp && lane == 0 && hist && n > 0 && *c.failed != 0) {
     // copies still in flight land before the CTA leaves: each stage's newest (bounded waits)
@@ -771,31 +896,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   }
   tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  // ---- partials: thread = row ------------------------------------------------------------------------------
-  if (w < active) {
-    const bool good = *c.failed == 0 && n > 0;     // block-uniform after the barrier
-    float* part = tree_part(a, lv.hq, b, min(node, a.T - 1), hq, slot);
-    const uint32_t trow = c.tmem + ((uint32_t)(32 * w) << 16);
-    const float M = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
-    if (row < live) *reinterpret_cast<float2*>(part) = good ? make_float2(M, lsum) : make_float2(-INFINITY, 0.f);
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      float o[32];
-      if (good) tmem_ld32(trow + kColO + 32 * k, o);
-      if (row < live) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(part + 4 + 32 * k + e) =
-              good ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
   if (w == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -812,6 +915,8 @@ int launch_fmt(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
 
 template <int FMT>
 int configure_fmt() {
+  cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
+  if (cudaFuncGetAttributes(&at, k_tree_attention<FMT>) != cudaSuccess || at.numRegs < kRegsLaunch) return OSCAR_ERR_CUDA;
   if (cudaFuncSetAttribute(k_tree_attention<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem) != cudaSuccess)
     return OSCAR_ERR_CUDA;
   return set_max_shared_carveout(reinterpret_cast<const void*>(k_tree_attention<FMT>));
@@ -820,21 +925,22 @@ int configure_fmt() {
 }  // namespace
 
 // Slots of a query row: the history over nsplit of them, the BF16 and draft pages over nb. One CTA runs on an SM at a
-// time; its start (rotation of the rows, first pages) and its end cost about as much as kFixed history tiles, a BF16
-// tile, which is not pipelined as deeply, about as much as two. The counts that need the fewest waves times tiles
+// time; its start (rotation of the rows, first pages) and its end cost about as much as kFixed history pages, a BF16
+// page, which is not pipelined as deeply, about as much as kNear. The counts that need the fewest waves times pages
 // win, and of equal ones those with the fewest slots, which the merge reads.
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
                  int* nb) {
-  constexpr double kFixed = 6.0;
+  constexpr double kFixed = 20.0, kNear = 5.0;
   const long units = (long)B * hkv * ((T * gq + kRows - 1) / kRows);
-  const int near = nbf + (T + kP - 1) / kP, tiles = std::max(1, (max_hist_pages + 1) / 2);
+  const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
   double best = 0.0;
-  *nsplit = *nb = 1;
+  *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
+  const int least = (pages + kPids - 1) / kPids;   // a slot's page ids fit shared memory
   for (int m = 1; m <= near && m < max_slots; ++m)
-    for (int s = 1; s <= std::min(tiles, 2 * sms) && s + m <= max_slots; ++s) {
+    for (int s = least; s <= std::max(least, std::min(pages, 2 * sms)) && s + m <= max_slots; ++s) {
       const long waves = (units * (s + m) + sms - 1) / sms;
-      const int work = std::max((tiles + s - 1) / s, 2 * ((near + m - 1) / m));
-      const double cost = (double)waves * (work + kFixed) + 0.05 * (s + m);
+      const double work = std::max((double)((pages + s - 1) / s), kNear * ((near + m - 1) / m));
+      const double cost = (double)waves * (work + kFixed) + 0.1 * (s + m);
       if (best == 0.0 || cost < best) {
         best = cost;
         *nsplit = s;
