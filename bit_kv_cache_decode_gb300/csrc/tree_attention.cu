@@ -65,12 +65,16 @@ static_assert(kMaxTreeBf16Pages + kMaxDraft / kP <= kPoisonTiles, "a set for eve
 constexpr int kMetaStage = 2 * 2 * 32 * 4;
 constexpr int kOffMeta = kOffPid + kPids * 4;
 constexpr int kOffJoin = kOffMeta + kStages * kMetaStage;   // [2 streams][128 rows] (M, l)
-constexpr int kOffBar = kOffJoin + 2 * kRows * 8;
+constexpr int kOffF = kOffJoin + 2 * kRows * 8;    // [128 rows] factor of a row's logits
+constexpr int kOffInfo = kOffF + kRows * 4;        // what the roles read about the slot: kI*
+constexpr int kIPages = 0, kIRest = 4, kIFirst = 8, kILen = 12, kINodes = 16, kILive = 20;
+constexpr int kOffBar = kOffInfo + 32;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages, kBKFull = kBMeta + kStages,
               kBVFull = kBKFull + kBufs, kBKFree = kBVFull + kBufs, kBVFree = kBKFree + kBufs, kBSDone = kBVFree + kBufs,
               kBSFree = kBSDone + 2, kBPReady = kBSFree + 2, kBODone = kBPReady + 2, kBImg = kBODone + 2, kBQ = kBImg + 1,
               kBFinal = kBQ + 1, kNumBars = kBFinal + 1;
-constexpr int kTreeSmem = kOffBar + kNumBars * 8 + 16 + 1024;   // + TMEM address, flag, alignment slack
+constexpr int kOffTmem = kOffBar + kNumBars * 8, kOffFailed = kOffTmem + 4;   // TMEM address, failure flag
+constexpr int kTreeSmem = kOffTmem + 16 + 1024;    // + alignment slack
 constexpr uint32_t kColO = 0, kColS = 256, kColP = 384, kColQ = 448, kTmemCols = 512;   // stream e: + 128 e, 64 e, 32 e
 constexpr uint32_t kIdescS = idesc_f16(128, 64), kIdescO = idesc_f16(128, 128);
 constexpr uint32_t kBf16Bits = (1u << 7) | (1u << 10);              // A and B bf16
@@ -94,17 +98,39 @@ template <int FMT>
 __device__ __forceinline__ uint32_t value_at(uint32_t x, int p, uint32_t lut, uint32_t s2, uint32_t z2) {
   return hfma2_u(FMT == kFmtCB ? levels_at(x, p, lut) : codes_at(x, p), s2, z2);
 }
-// (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}
+// shared memory by 32-bit address: the roles' pointers stay one register each
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 x;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+// (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}; blk: shared address of the page block
 template <int FMT>
-__device__ __forceinline__ uint2 scale_zero(const uint8_t* blk, int kind, int row, const float* mc) {
+__device__ __forceinline__ uint2 scale_zero(uint32_t blk, int kind, int row, const float* mc) {
   if (FMT == kFmtU8) {
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(blk + (kind ? kVMetaOffU8 : kKMetaOff) + 4 * row);
+    const uint32_t m = lds32(blk + (kind ? kVMetaOffU8 : kKMetaOff) + 4 * row);
     const float* c = mc + 8 * kind;
     const float2 a = u8_scale_zero(m & 0xffu, (m >> 8) & 0xffu, c[0], c[1], c[2]);
     const float2 b = u8_scale_zero((m >> 16) & 0xffu, m >> 24, c[4], c[5], c[6]);
     return make_uint2(pack_f16x2(a.x, a.y), pack_f16x2(b.x, b.y));
   }
-  uint2 m = *reinterpret_cast<const uint2*>(blk + (kind ? kVMetaOff : kKMetaOff) + 8 * row);
+  uint2 m = lds64(blk + (kind ? kVMetaOff : kKMetaOff) + 8 * row);
   if (FMT == kFmtCB) {                             // range 256 / 255: the levels are k_c / 256
     const float f = 256.f / 255.f;
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&m.x));
@@ -127,15 +153,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // What the roles share.
 struct Ctx {
-  uint8_t* smem;
-  uint32_t bar0;
-  volatile int* failed;
-  // the slot's pages: ids in shared memory (-1: out of range), tokens left from its first page on
-  const int* pids;
-  int rest;
+  uint32_t base;                                   // shared memory, 1,024-byte aligned
+  int rest;                                        // history: tokens from the slot's first page on
   // all 512 columns are allocated: they start at column 0 (checked). A constant address keeps the MMAs' operands uniform.
   static constexpr uint32_t tmem = 0;
-  __device__ __forceinline__ uint32_t bar(int k) const { return bar0 + 8u * (uint32_t)k; }
+  __device__ __forceinline__ uint32_t bar(int k) const { return base + kOffBar + 8u * (uint32_t)k; }
+  __device__ __forceinline__ bool failed() const { return lds32(base + kOffFailed) != 0u; }
+  __device__ __forceinline__ void fail() const { sts32(base + kOffFailed, 1u); }
   // one wait of a whole warp; false (the CTA has failed, or the wait expired) ends its work
   __device__ __forceinline__ bool wait(int k, int phase) const {
     const uint32_t parity = (uint32_t)phase & 1u;
@@ -143,15 +167,24 @@ struct Ctx {
     if (__all_sync(0xffffffffu, ok)) return true;
     const unsigned long long t0 = global_ns();     // a small loop: the roles' code shares the instruction caches
 #pragma unroll 1
-    while (!ok && *failed == 0 && global_ns() - t0 <= kWaitNs) ok = mbar_try(bar(k), parity);
+    while (!ok && !failed() && global_ns() - t0 <= kWaitNs) ok = mbar_try(bar(k), parity);
     return __all_sync(0xffffffffu, ok);
   }
   __device__ __forceinline__ void arrive(int k) const {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar(k));
   }
+  __device__ __forceinline__ void arrive(int j, int k) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive(bar(j));
+      mbar_arrive(bar(k));
+    }
+  }
   // valid tokens of history page i of the slot
-  __device__ __forceinline__ int tokens(int i) const { return pids[i] >= 0 ? min(kP, rest - i * kP) : 0; }
+  __device__ __forceinline__ int tokens(int i) const {
+    return (int)lds32(base + kOffPid + 4 * i) >= 0 ? min(kP, rest - i * kP) : 0;
+  }
 };
 
 // O of this warp's rows, of one stream, times al
@@ -212,10 +245,11 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
       const float2 F2 = make_float2(F, F), nm2 = make_float2(-mF, -mF);
       float2 t2 = make_float2(0.f, 0.f);
       {
-        float s0[32], s1[32];
-        tmem_ld32x2(ts, ts + 32, s0, s1);
-        weights32(s0, F2, nm2, r0, t2);
-        weights32(s1, F2, nm2, r1, t2);
+        float s[32];
+        tmem_ld32(ts, s);
+        weights32(s, F2, nm2, r0, t2);
+        tmem_ld32(ts + 32, s);
+        weights32(s, F2, nm2, r1, t2);
       }
       sum = t2.x + t2.y;
       const bool over = !redone && (sum > kMostSum || m == -INFINITY);
@@ -265,7 +299,6 @@ template <typename Bits>
 __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bits bits, float& m, float& lsum) {
   const uint32_t lane0 = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
   const uint32_t to = c.tmem + lane0 + kColO + 128 * e, ts = c.tmem + lane0 + kColS + 64 * e, tp = c.tmem + lane0 + kColP + 32 * e;
-  const volatile unsigned long long* poison = reinterpret_cast<const unsigned long long*>(c.smem + kOffPid);
   float l = 0.f;
 #pragma unroll 1
   for (int i = e; i < n; i += 2) {
@@ -273,7 +306,8 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
     const unsigned long long see = bits(i);
     if (!c.wait(kBSDone + e, ph) || !c.wait(kBVFull + i % kBufs, i / kBufs)) return false;
     tc_fence_after();
-    if (see & poison[i]) l = NAN;                  // a NaN or infinity among the values the row sees
+    const uint2 bad = lds64(c.base + kOffPid + 8 * i);
+    if ((uint32_t)see & bad.x || (uint32_t)(see >> 32) & bad.y) l = NAN;   // a NaN or infinity among the values the row sees
     float mx = -INFINITY;
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {
@@ -325,35 +359,33 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
 // 16u + 8 + q (the rows' fragments use the same order).
 template <int FMT>
 __device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, int h, int e, int n) {
-  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3, t0 = (lane & 7) + 8 * kw, u0 = lane >> 3;
   const float* mc = meta_consts(lv, h, 0);
   const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_K) : 0u;
+  const uint32_t dst0 = c.base + kOffK + kw * kSboK + 2 * u0 * 128 + (t0 & 7) * 16;
 #pragma unroll 1
   for (int i = e; i < n; i += 2) {
     const int b = i % kBufs, st = i % kStages;
     if (!c.wait(kBFull + st, i / kStages)) return false;
     if (i >= kBufs && !c.wait(kBKFree + b, i / kBufs - 1)) return false;
-    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
-    uint8_t* dst = c.smem + kOffK + b * kKBytes;
+    const uint32_t blk = c.base + kOffRing + st * kBlockBytes, codes = blk + kKCodesOff + 32 * t0 + 4 * u0;
+    const uint32_t dst = dst0 + b * kKBytes;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int t = (lane & 7) + 8 * (kw + 4 * k);
-      const uint2 sz = scale_zero<FMT>(blk, 0, t, mc);
+    for (int k = 0; k < 2; ++k) {                  // tokens t0, t0 + 32
+      const uint2 sz = scale_zero<FMT>(blk, 0, t0 + 32 * k, mc);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int u = (lane >> 3) + 4 * g;
+      for (int g = 0; g < 2; ++g) {                // 16-channel blocks u0, u0 + 4: one of each group
         const uint32_t m = g ? sz.y : sz.x, s2 = __byte_perm(m, m, 0x1010), z2 = __byte_perm(m, m, 0x3232);
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + kKCodesOff + 32 * t + 4 * u), y = x >> 8;
-        uint8_t* d = dst + (t >> 3) * kSboK + (2 * u) * 128 + (t & 7) * 16;
-        *reinterpret_cast<uint4*>(d) = make_uint4(value_at<FMT>(x, 0, lut, s2, z2), value_at<FMT>(x, 1, lut, s2, z2),
-                                                  value_at<FMT>(x, 2, lut, s2, z2), value_at<FMT>(x, 3, lut, s2, z2));
-        *reinterpret_cast<uint4*>(d + 128) = make_uint4(value_at<FMT>(y, 0, lut, s2, z2), value_at<FMT>(y, 1, lut, s2, z2),
-                                                        value_at<FMT>(y, 2, lut, s2, z2), value_at<FMT>(y, 3, lut, s2, z2));
+        const uint32_t x = lds32(codes + 1024 * k + 16 * g), y = x >> 8;
+        const uint32_t d = dst + 4 * k * kSboK + 8 * g * 128;
+        sts128(d, make_uint4(value_at<FMT>(x, 0, lut, s2, z2), value_at<FMT>(x, 1, lut, s2, z2),
+                             value_at<FMT>(x, 2, lut, s2, z2), value_at<FMT>(x, 3, lut, s2, z2)));
+        sts128(d + 128, make_uint4(value_at<FMT>(y, 0, lut, s2, z2), value_at<FMT>(y, 1, lut, s2, z2),
+                                   value_at<FMT>(y, 2, lut, s2, z2), value_at<FMT>(y, 3, lut, s2, z2)));
       }
     }
     fence_async();
-    c.arrive(kBKFull + b);
-    if (lane == 0) mbar_arrive(c.bar(kBEmpty + st));
+    c.arrive(kBKFull + b, kBEmpty + st);
   }
   return true;
 }
@@ -374,54 +406,51 @@ __device__ __forceinline__ bool value_pairs(const Ctx c, const LayerView& lv, in
   for (int i = 0; i < n; ++i) {
     const int st = i % kStages, nv = c.tokens(i);
     if (!c.wait(kBFull + st, i / kStages)) return false;
-    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
+    const uint32_t blk = c.base + kOffRing + st * kBlockBytes, to = c.base + kOffMeta + st * kMetaStage + 4 * lane;
     uint2 a = scale_zero<FMT>(blk, 1, t, mc), d = scale_zero<FMT>(blk, 1, t + 1, mc);
     if (t >= nv) a = make_uint2(0u, 0u);
     if (t + 1 >= nv) d = make_uint2(0u, 0u);
-    uint32_t* m = reinterpret_cast<uint32_t*>(c.smem + kOffMeta + st * kMetaStage) + lane;
-    m[0] = __byte_perm(a.x, d.x, 0x5410);
-    m[32] = __byte_perm(a.x, d.x, 0x7632);
-    m[64] = __byte_perm(a.y, d.y, 0x5410);
-    m[96] = __byte_perm(a.y, d.y, 0x7632);
-    c.arrive(kBMeta + st);
-    if (lane == 0) mbar_arrive(c.bar(kBEmpty + st));
+    sts32(to, __byte_perm(a.x, d.x, 0x5410));
+    sts32(to + 128, __byte_perm(a.x, d.x, 0x7632));
+    sts32(to + 256, __byte_perm(a.y, d.y, 0x5410));
+    sts32(to + 384, __byte_perm(a.y, d.y, 0x7632));
+    c.arrive(kBMeta + st, kBEmpty + st);
   }
   return true;
 }
 
 template <int FMT>
 __device__ __forceinline__ bool values_history(const Ctx c, const LayerView& lv, int h, int e, int n) {
-  // a thread has one word position w and four channels
+  // a thread has one word position w and the channels cl + 8 (vw + 4 j + 8 g); their 16-byte slots (v_chan_off) swap
+  // the low three bits of the channel with (channel >> 4) & 7 = (vw >> 1) + 2 j + 4 g
   const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) & 3, w = lane >> 3, cl = lane & 7;
   const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_V) : 0u;
+  const uint32_t slot0 = kVCodesOff + vw * 128 + (cl ^ (vw >> 1)) * 16 + 4 * w;
+  const uint32_t dst0 = c.base + kOffV + vw * kSboV + w * 128 + cl * 16, meta0 = c.base + kOffMeta + 16 * w;
 #pragma unroll 1
   for (int i = e; i < n; i += 2) {
     const int b = i % kBufs, st = i % kStages;
-    if (!c.wait(kBFull + st, i / kStages) || !c.wait(kBMeta + st, i / kStages)) return false;
+    if (!c.wait(kBMeta + st, i / kStages)) return false;   // after the page itself
     if (i >= kBufs && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
-    uint8_t* dst = c.smem + kOffV + b * kVBytes;
-    const uint8_t* blk = c.smem + kOffRing + st * kBlockBytes;
-    const uint4* mp = reinterpret_cast<const uint4*>(c.smem + kOffMeta + st * kMetaStage) + w;
+    const uint32_t codes = c.base + kOffRing + st * kBlockBytes + slot0, meta = meta0 + st * kMetaStage;
+    const uint32_t dst = dst0 + b * kVBytes;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       // pairs of positions 0-3 (tokens 0-31) and 4-7 of word w
-      const uint4 s0 = mp[16 * g], s1 = mp[16 * g + 4], z0 = mp[16 * g + 8], z1 = mp[16 * g + 12];
+      const uint4 s0 = lds128(meta + 256 * g), s1 = lds128(meta + 256 * g + 64);
+      const uint4 z0 = lds128(meta + 256 * g + 128), z1 = lds128(meta + 256 * g + 192);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int ch = cl + 8 * (vw + 4 * j + 8 * g);
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + v_chan_off(ch) + 4 * w), y = x >> 8;
-        uint8_t* d = dst + (ch >> 3) * kSboV + w * 128 + (ch & 7) * 16;
-        *reinterpret_cast<uint4*>(d) =
-            make_uint4(value_at<FMT>(x, 0, lut, s0.x, z0.x), value_at<FMT>(x, 1, lut, s0.y, z0.y),
-                       value_at<FMT>(x, 2, lut, s0.z, z0.z), value_at<FMT>(x, 3, lut, s0.w, z0.w));
-        *reinterpret_cast<uint4*>(d + 4 * 128) =
-            make_uint4(value_at<FMT>(y, 0, lut, s1.x, z1.x), value_at<FMT>(y, 1, lut, s1.y, z1.y),
-                       value_at<FMT>(y, 2, lut, s1.z, z1.z), value_at<FMT>(y, 3, lut, s1.w, z1.w));
+        const uint32_t x = lds32((codes ^ (32 * j + 64 * g)) + 512 * j + 1024 * g), y = x >> 8;
+        const uint32_t d = dst + (4 * j + 8 * g) * kSboV;
+        sts128(d, make_uint4(value_at<FMT>(x, 0, lut, s0.x, z0.x), value_at<FMT>(x, 1, lut, s0.y, z0.y),
+                             value_at<FMT>(x, 2, lut, s0.z, z0.z), value_at<FMT>(x, 3, lut, s0.w, z0.w)));
+        sts128(d + 4 * 128, make_uint4(value_at<FMT>(y, 0, lut, s1.x, z1.x), value_at<FMT>(y, 1, lut, s1.y, z1.y),
+                                       value_at<FMT>(y, 2, lut, s1.z, z1.z), value_at<FMT>(y, 3, lut, s1.w, z1.w)));
       }
     }
     fence_async();
-    c.arrive(kBVFull + b);
-    if (lane == 0) mbar_arrive(c.bar(kBEmpty + st));
+    c.arrive(kBVFull + b, kBEmpty + st);
   }
   return true;
 }
@@ -460,7 +489,7 @@ __device__ __forceinline__ bool keys_bf16(const Ctx c, int* status, int e, int n
       for (int j = 0; j < 4; ++j) {
         const int t = (lane & 7) + 8 * (kw + 4 * k), ck = (lane >> 3) + 4 * j;
         bad |= nonfinite2(x[k][j].x) | nonfinite2(x[k][j].y) | nonfinite2(x[k][j].z) | nonfinite2(x[k][j].w);
-        *reinterpret_cast<uint4*>(c.smem + kOffK + b * kKBytes + (t >> 3) * kSboK + ck * 128 + (t & 7) * 16) = x[k][j];
+        sts128(c.base + kOffK + b * kKBytes + (t >> 3) * kSboK + ck * 128 + (t & 7) * 16, x[k][j]);
       }
     if (bad != 0u && p.draft) flag(status, OSCAR_STATUS_NONFINITE);
     fence_async();
@@ -473,7 +502,6 @@ __device__ __forceinline__ bool keys_bf16(const Ctx c, int* status, int e, int n
 template <typename Page>
 __device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int n, Page page) {
   const int lane = threadIdx.x & 31, vw = (threadIdx.x >> 5) & 3;
-  unsigned long long* poison = reinterpret_cast<unsigned long long*>(c.smem + kOffPid);
 #pragma unroll 1
   for (int i = e; i < n; i += 2) {
     const int b = i % kBufs;
@@ -498,7 +526,8 @@ __device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int
 #pragma unroll
         for (int t = 0; t < 8; ++t)
           if (nonfinite2(x[k][t])) {
-            atomicOr(poison + i, 1ull << (8 * (vw + 4 * (k >> 1)) + t));
+            const int row = 8 * (vw + 4 * (k >> 1)) + t;
+            asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(c.base + kOffPid + 8 * i + 4 * (row >> 5)), "r"(1u << (row & 31)) : "memory");
             x[k][t] = 0u;
           }
       if (p.draft) flag(status, OSCAR_STATUS_NONFINITE);
@@ -506,20 +535,226 @@ __device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int o = vw + 4 * (k >> 1), ch = 2 * (lane + 32 * (k & 1));
-      uint8_t* d = c.smem + kOffV + b * kVBytes + (ch >> 3) * kSboVNear + o * 128 + (ch & 7) * 16;
+      const uint32_t d = c.base + kOffV + b * kVBytes + (ch >> 3) * kSboVNear + o * 128 + (ch & 7) * 16;
       uint32_t lo[4], hi[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         lo[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x5410);
         hi[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x7632);
       }
-      *reinterpret_cast<uint4*>(d) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(d + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      sts128(d, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      sts128(d + 16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
     }
     fence_async();
     c.arrive(kBVFull + b);
   }
   return true;
+}
+
+// Page i of the slot into ring stage i % kStages (one thread).
+__device__ __forceinline__ void issue_page(const Ctx c, const LayerView& lv, int h, int i) {
+  const int st = i % kStages, id = (int)lds32(c.base + kOffPid + 4 * i);
+  mbar_expect_tx(c.bar(kBFull + st), id >= 0 ? (uint32_t)lv.blk_bytes : 0u);   // also for no page: the phase completes
+  if (id >= 0)
+    bulk_copy_hint(c.base + kOffRing + st * kBlockBytes, int2_block(lv, id, h), (uint32_t)lv.blk_bytes, c.bar(kBFull + st),
+                   l2_evict_first());
+}
+
+// The control warps: page stream, scale pairs, MMAs.
+template <int FMT>
+__device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w, int h, bool hist, int n) {
+  const int lane = threadIdx.x & 31;
+  if (w == kLoadWarp) {
+    if (!hist) return true;
+#pragma unroll 1
+    for (int i = kStages; i < n; ++i) {
+      if (!c.wait(kBEmpty + i % kStages, i / kStages - 1)) return false;
+      if (lane == 0) issue_page(c, lv, h, i);
+      __syncwarp();
+    }
+    return true;
+  }
+  if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, lv, h, n);
+  // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4 and stream i & 1
+  static_assert(kBufs == 4, "two pages of each stream");
+  const uint32_t more = hist ? 0u : kBf16Bits;
+  if (w == kMmaWarp) {
+    const uint32_t kd = desc_lo(c.base + kOffK, 128);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int b = i % kBufs, e = i & 1;
+      if (!c.wait(kBKFull + b, i / kBufs)) return false;
+      // S(i - 2) is out of the way: read, or (BF16 pages, whose weights' low parts follow it there) used by O(i - 2)
+      if (i >= 2 && !c.wait((hist ? kBSFree : kBODone) + e, (i - 2) >> 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_ta_warp(c.tmem + kColS + 64 * e, c.tmem + kColQ + 8 * kk, kd + b * (kKBytes >> 4) + 16 * kk, desc_hi(kSboK),
+                     kIdescS | more, kk > 0);
+      umma_commit_warp(c.bar(kBSDone + e));
+      umma_commit_warp(c.bar(kBKFree + b));
+    }
+  } else {
+    const uint32_t vd = desc_lo(c.base + kOffV, 128), vh = hist ? desc_hi(kSboV) : desc_hi(kSboVNear);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int b = i % kBufs, e = i & 1;
+      if (!c.wait(kBVFull + b, i / kBufs) || !c.wait(kBPReady + e, i >> 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColP + 32 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                     kIdescO | more, i > 1 || kk > 0);
+      if (!hist) {                               // the weights' low parts
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColS + 64 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                       kIdescO | more, true);
+      }
+      umma_commit_warp(c.bar(kBODone + e));
+      umma_commit_warp(c.bar(kBVFree + b));
+    }
+  }
+  return true;
+}
+
+// The BF16 and draft pages of a slot.
+struct NearPages {
+  const LayerView& lv;
+  const TreeArgs& a;
+  int b, h, p0, L, nodes;
+  __device__ __forceinline__ Near operator()(int i) const {
+    const int u = p0 + i, nbf = (lv.sink + lv.recent) / kP;
+    Near r = {nullptr, nullptr, (size_t)kD, 0, u >= nbf};
+    if (u >= nbf) {
+      const size_t at = (((size_t)b * a.T + (u - nbf) * kP) * lv.hkv + h) * kD;
+      r.k = a.kd + at;
+      r.v = a.vd + at;
+      r.step = (size_t)lv.hkv * kD;
+      r.rows = min(kP, nodes - (u - nbf) * kP);
+      return r;
+    }
+    const int rows = u < lv.sink / kP ? min(L, lv.sink) - u * kP : min(max(L - lv.sink, 0), lv.recent) - (u - lv.sink / kP) * kP;
+    if (rows <= 0) return r;
+    const int id = a.bf16_pt[(size_t)b * nbf + u];
+    if (id < 0 || id >= lv.n_bf16) {
+      if ((threadIdx.x & 31) == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
+      return r;
+    }
+    r.k = bf16_row(lv, id, h, 0, 0);
+    r.v = bf16_row(lv, id, h, 1, 0);
+    r.rows = min(kP, rows);
+    return r;
+  }
+};
+
+// Partials of a slot, thread = row, a warpgroup per half of the channels: the streams' O joined. Both streams' row warps
+// meet first (each has waited for its stream's last product); a CTA that failed writes empty ones.
+__device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv, const TreeArgs& a, int h, int qt, int n, int live) {
+  const int tid = threadIdx.x, w = tid >> 5, row = tid & (kRows - 1), half = (tid >> 7) & 1;
+  const int gq = lv.hq / lv.hkv, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;
+  tc_fence_before();
+  asm volatile("bar.sync 1, %0;" ::"r"(64 * ((live + 31) / 32)) : "memory");
+  tc_fence_after();
+  const bool good = __all_sync(0xffffffffu, !c.failed() && n > 0);
+  const uint2 u0 = lds64(c.base + kOffJoin + 8 * row), u1 = lds64(c.base + kOffJoin + 8 * (kRows + row));
+  const float m0 = __uint_as_float(u0.x), m1 = n > 1 ? __uint_as_float(u1.x) : -INFINITY;
+  const float M = fmaxf(m0, m1);
+  const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+  float* part = tree_part(a, lv.hq, blockIdx.z, min(node, a.T - 1), hq, blockIdx.x);
+  const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO;
+  if (row < live && half == 0) {
+    const float l = w0 * __uint_as_float(u0.y) + (n > 1 ? w1 * __uint_as_float(u1.y) : 0.f);
+    *reinterpret_cast<float2*>(part) = good ? make_float2(M, l) : make_float2(-INFINITY, 0.f);
+  }
+#pragma unroll 1
+  for (int k = 2 * half; k < 2 * half + 2; ++k) {
+    float x[32], y[32];
+    if (!good) {
+#pragma unroll
+      for (int t = 0; t < 32; ++t) x[t] = 0.f;
+    } else if (n > 1) {
+      tmem_ld32x2(to + 32 * k, to + 128 + 32 * k, x, y);
+#pragma unroll
+      for (int t = 0; t < 32; ++t) x[t] = w0 * x[t] + w1 * y[t];
+    } else {
+      tmem_ld32(to + 32 * k, x);
+#pragma unroll
+      for (int t = 0; t < 32; ++t) x[t] *= w0;
+    }
+    if (row < live) {
+#pragma unroll
+      for (int t = 0; t < 32; t += 4)
+        *reinterpret_cast<float4*>(part + 4 + 32 * k + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Ctx c;
+  c.base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t info = c.base + kOffInfo;
+  const int w = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int h = blockIdx.y % lv.hkv, qt = blockIdx.y / lv.hkv, e = (w >> 2) & 1;   // e: the warpgroup's stream
+  const bool hist = (int)blockIdx.x < a.nsplit;
+  const int n = (int)lds32(info + kIPages);
+  c.rest = (int)lds32(info + kIRest);
+  const NearPages near = {lv, a, (int)blockIdx.z, h, (int)lds32(info + kIFirst), (int)lds32(info + kILen), (int)lds32(info + kINodes)};
+  bool ok = !c.failed();
+  if (w < kRowWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+    const int live = (int)lds32(info + kILive), row = threadIdx.x & (kRows - 1);
+    if (32 * (w & 3) < live) {
+      const float F = __uint_as_float(lds32(c.base + kOffF + 4 * row));
+      float m = -INFINITY, lsum = 0.f;
+      if (ok && hist) {
+        ok = rows_history(c, e, n, F, m, lsum);
+      } else if (ok) {
+        const int node = (qt * kRows + row) / (lv.hq / lv.hkv), nbf = (lv.sink + lv.recent) / kP;
+        auto bits = [&](int i) -> unsigned long long {
+          const Near p = near(i);
+          unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
+          if (p.draft) see &= row < live ? a.mask[((size_t)blockIdx.z * a.T + node) * a.W + (near.p0 + i - nbf)] : 0ull;
+          return see;
+        };
+        ok = rows_bf16(c, e, n, F, bits, m, lsum);
+      }
+      const int last = n - 1 - ((n - 1 - e) & 1);            // the stream's last page
+      if (ok && e < n) ok = c.wait(kBODone + e, last >> 1);
+      if (!ok) c.fail();
+      // the sums of both streams, for the join
+      const float ref = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
+      sts32(c.base + kOffJoin + 8 * (e * kRows + row), __float_as_uint(ref));
+      sts32(c.base + kOffJoin + 8 * (e * kRows + row) + 4, __float_as_uint(lsum));
+      write_partials(c, lv, a, h, qt, n, live);
+    }
+  } else if (w < kVWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    if (ok) ok = hist ? keys_history<FMT>(c, lv, h, e, n) : keys_bf16(c, lv.status, e, n, near);
+  } else if (w < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    if (ok) ok = hist ? values_history<FMT>(c, lv, h, e, n) : values_bf16(c, lv.status, e, n, near);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (ok) ok = control<FMT>(c, lv, w, h, hist, n);
+  }
+  if (!ok) {
+    if (lane == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
+    c.fail();
+  }
+  if (w == kMmaWarp || w == kMmaOWarp) {           // every MMA completes before TMEM is released
+    umma_commit_warp(c.bar(kBFinal));
+    mbar_wait(c.bar(kBFinal), 0);
+    __syncwarp();
+  }
+  if (w == kLoadWarp && lane == 0 && hist && n > 0 && c.failed()) {
+    // copies still in flight land before the CTA leaves: each stage's newest (bounded waits)
+    mbar_wait(c.bar(kBImg), 0);
+    for (int s = 0; s < kStages; ++s)
+      for (int ph = 0; ph < 2; ++ph) mbar_wait(c.bar(kBFull + s), ph);
+  }
 }
 
 template <int FMT>
@@ -538,11 +773,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   if (live <= 0) return;
 
   Ctx c;
-  c.smem = smem;
-  c.bar0 = smem_addr(smem + kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
-  c.failed = reinterpret_cast<volatile int*>(smem + kOffBar + kNumBars * 8 + 4);
-  int* pids = reinterpret_cast<int*>(smem + kOffPid);   // BF16 slots: see kPoisonTiles
+  c.base = smem_addr(smem);
 
   // ---- the slot's tokens -----------------------------------------------------------------------------------
   int L = a.seq_lens[b];
@@ -565,8 +796,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     p0 = (slot - a.nsplit) * near_pages / a.nb;
     n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
   }
-  c.pids = pids;
-  c.rest = Lh - p0 * kP;
 
   const int active = (live + 31) / 32;             // row warps with rows
   if (w == kLoadWarp) {
@@ -582,7 +811,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
         const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
         mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
         for (int p = 0; p < 2; ++p)                // R = b1 + b2 to about 17 bits
-          bulk_copy_hint(smem_addr(smem + kOffK + p * kImgBytes), img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
+          bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
       }
     }
     __syncwarp();
@@ -603,10 +832,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       mbar_init_n(c.bar(kBQ), 1);
       mbar_init_n(c.bar(kBFinal), 2);                // both issuing warps
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      *c.failed = 0;
+      sts32(c.base + kOffFailed, 0u);
+      const uint32_t info = c.base + kOffInfo;
+      sts32(info + kIPages, (uint32_t)n);
+      sts32(info + kIRest, (uint32_t)(Lh - p0 * kP));
+      sts32(info + kIFirst, (uint32_t)p0);
+      sts32(info + kILen, (uint32_t)L);
+      sts32(info + kINodes, (uint32_t)nodes);
+      sts32(info + kILive, (uint32_t)live);
     }
     __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.base + kOffTmem),
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -620,16 +856,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
           flag(lv.status, OSCAR_STATUS_BAD_PAGE);
           id = -1;
         }
-        pids[k] = id;
+        sts32(c.base + kOffPid + 4 * k, (uint32_t)id);
       }
     } else {                                       // the tiles' sets of non-finite rows
-      for (int k = at; k < 2 * n; k += step) pids[k] = 0;
+      for (int k = at; k < 2 * n; k += step) sts32(c.base + kOffPid + 4 * k, 0u);
     }
   }
   // ---- the rows' q, staged where the values go: the rotation's A operand ----------------------------------
   // thread = row; the odd pages' warpgroup takes the upper half of the channels
   const int row = tid & (kRows - 1), half = (tid >> 7) & 1, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;
-  uint8_t* const qs = smem + kOffV + (row >> 3) * kSboK + (row & 7) * 16;
+  const uint32_t qs = c.base + kOffV + (row >> 3) * kSboK + (row & 7) * 16;
   if (w < kRowWarps && n > 0) {
     const uint4* src = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + node) * lv.hq + hq) * kD);
     uint32_t bad = 0u;
@@ -637,7 +873,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     for (int j = 0; j < 8; ++j) {
       const uint4 x = row < live ? src[8 * half + j] : make_uint4(0u, 0u, 0u, 0u);
       bad |= nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w);
-      *reinterpret_cast<uint4*>(qs + (8 * half + j) * 128) = x;
+      sts128(qs + (8 * half + j) * 128, x);
     }
     if (bad != 0u) flag(lv.status, OSCAR_STATUS_NONFINITE);
     fence_async();
@@ -645,28 +881,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  bool ok = *tmem_slot == c.tmem;
-
-  auto issue_page = [&](int i) {                   // page i into ring stage i % kStages (one thread)
-    const int st = i % kStages, id = pids[i];
-    mbar_expect_tx(c.bar(kBFull + st), id >= 0 ? (uint32_t)lv.blk_bytes : 0u);   // also for no page: the phase completes
-    if (id >= 0)
-      bulk_copy_hint(smem_addr(smem + kOffRing + st * kBlockBytes), int2_block(lv, id, h), (uint32_t)lv.blk_bytes,
-                     c.bar(kBFull + st), l2_evict_first());
-  };
+  bool ok = lds32(c.base + kOffTmem) == c.tmem;
 
   // ---- the rows' A operand in TMEM -------------------------------------------------------------------------
   float F = a.scale_log2;
   if (ok && n > 0 && hist) {
     if (w == kLoadWarp) {
       if (lane == 0)
-        for (int i = 0; i < min(n, kStages); ++i) issue_page(i);
+        for (int i = 0; i < min(n, kStages); ++i) issue_page(c, lv, h, i);
       __syncwarp();
     } else if (w == kMmaWarp) {
       ok = c.wait(kBImg, 0);
       if (ok) {
         tc_fence_after();
-        const uint32_t a0 = smem_addr(smem + kOffV), b0 = smem_addr(smem + kOffK);
+        const uint32_t a0 = c.base + kOffV, b0 = c.base + kOffK;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -713,7 +941,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       uint32_t r[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(qs + (4 * k + j) * 128);
+        const uint4 x = lds128(qs + (4 * k + j) * 128);
         r[4 * j] = x.x;
         r[4 * j + 1] = x.y;
         r[4 * j + 2] = x.z;
@@ -723,182 +951,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     }
     tmem_wait_st();
   }
-  if (!ok) *c.failed = 1;
+  if (w < kRowWarps && half == 0) sts32(c.base + kOffF + 4 * row, __float_as_uint(F));
+  if (!ok) c.fail();
   tc_fence_before();
   __syncthreads();                                 // Q is in; the rotation's operands may be overwritten
   tc_fence_after();
 
-  auto near = [&](int i) {
-    const int u = p0 + i;
-    Near r = {nullptr, nullptr, (size_t)kD, 0, u >= nbf};
-    if (u >= nbf) {
-      const size_t at = (((size_t)b * a.T + (u - nbf) * kP) * lv.hkv + h) * kD;
-      r.k = a.kd + at;
-      r.v = a.vd + at;
-      r.step = (size_t)lv.hkv * kD;
-      r.rows = min(kP, nodes - (u - nbf) * kP);
-      return r;
-    }
-    const int rows = u < lv.sink / kP ? min(L, lv.sink) - u * kP : min(max(L - lv.sink, 0), lv.recent) - (u - lv.sink / kP) * kP;
-    if (rows <= 0) return r;
-    const int id = a.bf16_pt[(size_t)b * nbf + u];
-    if (id < 0 || id >= lv.n_bf16) {
-      if (lane == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
-      return r;
-    }
-    r.k = bf16_row(lv, id, h, 0, 0);
-    r.v = bf16_row(lv, id, h, 1, 0);
-    r.rows = min(kP, rows);
-    return r;
-  };
-
-  // ---- the control warps: page stream, scale pairs, MMAs ----
-  auto control = [&](int w) -> bool {
-    if (w == kLoadWarp) {
-      bool fine = true;
-      if (hist)
-        for (int i = kStages; i < n && fine; ++i) {
-          fine = c.wait(kBEmpty + i % kStages, i / kStages - 1);
-          if (fine && lane == 0) issue_page(i);
-          __syncwarp();
-        }
-      return fine;
-    }
-    if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, lv, h, n);
-    // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4 and stream i & 1
-    static_assert(kBufs == 4, "two pages of each stream");
-    const uint32_t more = hist ? 0u : kBf16Bits;
-    if (w == kMmaWarp) {
-      const uint32_t kd = desc_lo(smem_addr(smem + kOffK), 128);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int b = i % kBufs, e = i & 1;
-        if (!c.wait(kBKFull + b, i / kBufs)) return false;
-        // S(i - 2) is out of the way: read, or (BF16 pages, whose weights' low parts follow it there) used by O(i - 2)
-        if (i >= 2 && !c.wait((hist ? kBSFree : kBODone) + e, (i - 2) >> 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ta_warp(c.tmem + kColS + 64 * e, c.tmem + kColQ + 8 * kk, kd + b * (kKBytes >> 4) + 16 * kk, desc_hi(kSboK),
-                       kIdescS | more, kk > 0);
-        umma_commit_warp(c.bar(kBSDone + e));
-        umma_commit_warp(c.bar(kBKFree + b));
-      }
-    } else {
-      const uint32_t vd = desc_lo(smem_addr(smem + kOffV), 128), vh = hist ? desc_hi(kSboV) : desc_hi(kSboVNear);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int b = i % kBufs, e = i & 1;
-        if (!c.wait(kBVFull + b, i / kBufs) || !c.wait(kBPReady + e, i >> 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColP + 32 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
-                       kIdescO | more, i > 1 || kk > 0);
-        if (!hist) {                               // the weights' low parts
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColS + 64 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
-                         kIdescO | more, true);
-        }
-        umma_commit_warp(c.bar(kBODone + e));
-        umma_commit_warp(c.bar(kBVFree + b));
-      }
-    }
-    return true;
-  };
-
-  ok = *c.failed == 0;
-  const int e = (w >> 2) & 1;                      // the stream of this warpgroup (rows, keys, values)
-  if (w < kRowWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-    if ((w & 3) < active) {
-      float m = -INFINITY, lsum = 0.f;
-      if (ok && hist) {
-        ok = rows_history(c, e, n, F, m, lsum);
-      } else if (ok) {
-        auto bits = [&](int i) -> unsigned long long {
-          const Near p = near(i);
-          unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
-          if (p.draft) see &= row < live ? a.mask[((size_t)b * a.T + node) * a.W + (p0 + i - nbf)] : 0ull;
-          return see;
-        };
-        ok = rows_bf16(c, e, n, F, bits, m, lsum);
-      }
-      const int last = n - 1 - ((n - 1 - e) & 1);            // the stream's last page
-      if (ok && e < n) ok = c.wait(kBODone + e, last >> 1);
-      // the sums of both streams, for the join
-      const float ref = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
-      reinterpret_cast<float2*>(smem + kOffJoin)[e * kRows + row] = make_float2(ref, lsum);
-      // ---- partials: thread = row, a warpgroup per half of the channels; the streams' O joined. Both streams' row
-      // warps meet first (each has waited for its stream's last product); a CTA that failed writes empty ones ----
-      if (!ok) *c.failed = 1;
-      tc_fence_before();
-      asm volatile("bar.sync 1, %0;" ::"r"(64 * active) : "memory");
-      tc_fence_after();
-      const bool good = *c.failed == 0 && n > 0;
-      const float2* join = reinterpret_cast<const float2*>(smem + kOffJoin) + row;
-      const float2 j0 = join[0], j1 = n > 1 ? join[kRows] : make_float2(-INFINITY, 0.f);
-      const float M = fmaxf(j0.x, j1.x);
-      const float w0 = j0.x == -INFINITY ? 0.f : exp2f(j0.x - M), w1 = j1.x == -INFINITY ? 0.f : exp2f(j1.x - M);
-      float* part = tree_part(a, lv.hq, b, min(node, a.T - 1), hq, slot);
-      const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO;
-      if (row < live && half == 0)
-        *reinterpret_cast<float2*>(part) = good ? make_float2(M, w0 * j0.y + w1 * j1.y) : make_float2(-INFINITY, 0.f);
-#pragma unroll 1
-      for (int k = 2 * half; k < 2 * half + 2; ++k) {
-        float x[32], y[32];
-        if (__all_sync(0xffffffffu, good)) {
-          if (n > 1) {
-            tmem_ld32x2(to + 32 * k, to + 128 + 32 * k, x, y);
-#pragma unroll
-            for (int t = 0; t < 32; ++t) x[t] = w0 * x[t] + w1 * y[t];
-          } else {
-            tmem_ld32(to + 32 * k, x);
-#pragma unroll
-            for (int t = 0; t < 32; ++t) x[t] *= w0;
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = 0.f;
-        }
-        if (row < live) {
-#pragma unroll
-          for (int t = 0; t < 32; t += 4)
-            *reinterpret_cast<float4*>(part + 4 + 32 * k + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
-        }
-      }
-    }
-  } else if (w < kVWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
-    if (ok) ok = hist ? keys_history<FMT>(c, lv, h, e, n) : keys_bf16(c, lv.status, e, n, near);
-  } else if (w < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
-    if (ok) ok = hist ? values_history<FMT>(c, lv, h, e, n) : values_bf16(c, lv.status, e, n, near);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-    if (ok) ok = control(w);
-  }
-  if (!ok) {
-    if (lane == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
-    *c.failed = 1;
-  }
-  if (w == kMmaWarp || w == kMmaOWarp) {           // every MMA completes before TMEM is read or released
-    umma_commit_warp(c.bar(kBFinal));
-    mbar_wait(c.bar(kBFinal), 0);
-    __syncwarp();
-  }
-  if (w == kLoadWarp && lane == 0 && hist && n > 0 && *c.failed != 0) {
-    // copies still in flight land before the CTA leaves: each stage's newest (bounded waits)
-    mbar_wait(c.bar(kBImg), 0);
-    for (int s = 0; s < kStages; ++s)
-      for (int ph = 0; ph < 2; ++ph) mbar_wait(c.bar(kBFull + s), ph);
-  }
+  // ---- the roles. What they need is read back from shared memory: nothing of the start is kept in registers ----
+  run_roles<FMT>(lv, a);
   tc_fence_before();
   __syncthreads();
   if (w == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(lds32(c.base + kOffTmem)), "r"(kTmemCols)
+                 : "memory");
   }
 }
 
