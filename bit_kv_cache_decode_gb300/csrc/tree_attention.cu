@@ -245,11 +245,10 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
       const float2 F2 = make_float2(F, F), nm2 = make_float2(-mF, -mF);
       float2 t2 = make_float2(0.f, 0.f);
       {
-        float s[32];
-        tmem_ld32(ts, s);
-        weights32(s, F2, nm2, r0, t2);
-        tmem_ld32(ts + 32, s);
-        weights32(s, F2, nm2, r1, t2);
+        float s0[32], s1[32];
+        tmem_ld32x2(ts, ts + 32, s0, s1);
+        weights32(s0, F2, nm2, r0, t2);
+        weights32(s1, F2, nm2, r1, t2);
       }
       sum = t2.x + t2.y;
       const bool over = !redone && (sum > kMostSum || m == -INFINITY);
@@ -370,20 +369,27 @@ __device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, i
     if (i >= kBufs && !c.wait(kBKFree + b, i / kBufs - 1)) return false;
     const uint32_t blk = c.base + kOffRing + st * kBlockBytes, codes = blk + kKCodesOff + 32 * t0 + 4 * u0;
     const uint32_t dst = dst0 + b * kKBytes;
+    // tokens t0, t0 + 32 (k) and the 16-channel blocks u0, u0 + 4 (g), one of each group; all loads first
+    uint2 sz[2];
+    uint32_t x[2][2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {                  // tokens t0, t0 + 32
-      const uint2 sz = scale_zero<FMT>(blk, 0, t0 + 32 * k, mc);
+    for (int k = 0; k < 2; ++k) {
+      sz[k] = scale_zero<FMT>(blk, 0, t0 + 32 * k, mc);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {                // 16-channel blocks u0, u0 + 4: one of each group
-        const uint32_t m = g ? sz.y : sz.x, s2 = __byte_perm(m, m, 0x1010), z2 = __byte_perm(m, m, 0x3232);
-        const uint32_t x = lds32(codes + 1024 * k + 16 * g), y = x >> 8;
-        const uint32_t d = dst + 4 * k * kSboK + 8 * g * 128;
-        sts128(d, make_uint4(value_at<FMT>(x, 0, lut, s2, z2), value_at<FMT>(x, 1, lut, s2, z2),
-                             value_at<FMT>(x, 2, lut, s2, z2), value_at<FMT>(x, 3, lut, s2, z2)));
-        sts128(d + 128, make_uint4(value_at<FMT>(y, 0, lut, s2, z2), value_at<FMT>(y, 1, lut, s2, z2),
-                                   value_at<FMT>(y, 2, lut, s2, z2), value_at<FMT>(y, 3, lut, s2, z2)));
-      }
+      for (int g = 0; g < 2; ++g) x[k][g] = lds32(codes + 1024 * k + 16 * g);
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t m = g ? sz[k].y : sz[k].x, s2 = __byte_perm(m, m, 0x1010), z2 = __byte_perm(m, m, 0x3232);
+        const uint32_t lo = x[k][g], hi = lo >> 8;
+        const uint32_t d = dst + 4 * k * kSboK + 8 * g * 128;
+        sts128(d, make_uint4(value_at<FMT>(lo, 0, lut, s2, z2), value_at<FMT>(lo, 1, lut, s2, z2),
+                             value_at<FMT>(lo, 2, lut, s2, z2), value_at<FMT>(lo, 3, lut, s2, z2)));
+        sts128(d + 128, make_uint4(value_at<FMT>(hi, 0, lut, s2, z2), value_at<FMT>(hi, 1, lut, s2, z2),
+                                   value_at<FMT>(hi, 2, lut, s2, z2), value_at<FMT>(hi, 3, lut, s2, z2)));
+      }
     fence_async();
     c.arrive(kBKFull + b, kBEmpty + st);
   }
@@ -434,21 +440,28 @@ __device__ __forceinline__ bool values_history(const Ctx c, const LayerView& lv,
     if (i >= kBufs && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
     const uint32_t codes = c.base + kOffRing + st * kBlockBytes + slot0, meta = meta0 + st * kMetaStage;
     const uint32_t dst = dst0 + b * kVBytes;
+    uint32_t x[2][2];
+    uint4 s2[2][2], z2[2][2];                      // [group][positions 0-3 (tokens 0-31), 4-7] of word w
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      // pairs of positions 0-3 (tokens 0-31) and 4-7 of word w
-      const uint4 s0 = lds128(meta + 256 * g), s1 = lds128(meta + 256 * g + 64);
-      const uint4 z0 = lds128(meta + 256 * g + 128), z1 = lds128(meta + 256 * g + 192);
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t x = lds32((codes ^ (32 * j + 64 * g)) + 512 * j + 1024 * g), y = x >> 8;
-        const uint32_t d = dst + (4 * j + 8 * g) * kSboV;
-        sts128(d, make_uint4(value_at<FMT>(x, 0, lut, s0.x, z0.x), value_at<FMT>(x, 1, lut, s0.y, z0.y),
-                             value_at<FMT>(x, 2, lut, s0.z, z0.z), value_at<FMT>(x, 3, lut, s0.w, z0.w)));
-        sts128(d + 4 * 128, make_uint4(value_at<FMT>(y, 0, lut, s1.x, z1.x), value_at<FMT>(y, 1, lut, s1.y, z1.y),
-                                       value_at<FMT>(y, 2, lut, s1.z, z1.z), value_at<FMT>(y, 3, lut, s1.w, z1.w)));
+        x[g][j] = lds32((codes ^ (32 * j + 64 * g)) + 512 * j + 1024 * g);
+        s2[g][j] = lds128(meta + 256 * g + 64 * j);
+        z2[g][j] = lds128(meta + 256 * g + 128 + 64 * j);
       }
-    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = x[g][j], hi = lo >> 8;
+        const uint32_t d = dst + (4 * j + 8 * g) * kSboV;
+        sts128(d, make_uint4(value_at<FMT>(lo, 0, lut, s2[g][0].x, z2[g][0].x), value_at<FMT>(lo, 1, lut, s2[g][0].y, z2[g][0].y),
+                             value_at<FMT>(lo, 2, lut, s2[g][0].z, z2[g][0].z), value_at<FMT>(lo, 3, lut, s2[g][0].w, z2[g][0].w)));
+        sts128(d + 4 * 128,
+               make_uint4(value_at<FMT>(hi, 0, lut, s2[g][1].x, z2[g][1].x), value_at<FMT>(hi, 1, lut, s2[g][1].y, z2[g][1].y),
+                          value_at<FMT>(hi, 2, lut, s2[g][1].z, z2[g][1].z), value_at<FMT>(hi, 3, lut, s2[g][1].w, z2[g][1].w)));
+      }
     fence_async();
     c.arrive(kBVFull + b, kBEmpty + st);
   }
