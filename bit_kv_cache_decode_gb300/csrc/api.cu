@@ -284,6 +284,12 @@ void codebook_consts(const uint8_t* k, float* out) {
   out[7] = 0.f;
 }
 
+// one slot of the tree attention's partials for B requests
+size_t tree_slot_bytes(const oscar_cache* c, int B, int T) {
+  const int gq = c->lay.num_q_heads / c->lay.num_kv_heads;
+  return (size_t)B * c->lay.num_kv_heads * tree_tiles(T, gq) * tree_tile_rows(T, gq) * kPartFloats * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -750,10 +756,10 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
 int oscar_tree_workspace_bytes(const oscar_cache* c, int B, int T, int max_hist_pages, size_t* bytes) {
   if (!c || !bytes || B < 0 || B > c->lay.max_batch || T < 1 || max_hist_pages < 0) return OSCAR_ERR_INVALID_ARG;
   if (T > kMaxDraft) return OSCAR_ERR_UNSUPPORTED;
-  int ns = 1, nb = 1;
+  int ns = 1, nb = 1, pps = 1;
   tree_splits(B, T, c->lay.num_kv_heads, c->lay.num_q_heads / c->lay.num_kv_heads, (c->lay.sink + c->lay.recent) / kP,
-              max_hist_pages, c->sms, 1 << 20, &ns, &nb);
-  *bytes = std::max(kAlign, align_up((size_t)B * T * c->lay.num_q_heads * (ns + nb) * kPartFloats * sizeof(float)));
+              max_hist_pages, c->sms, 1 << 20, &ns, &nb, &pps);
+  *bytes = std::max(kAlign, align_up(tree_slot_bytes(c, B, T) * (ns + nb)));
   return OSCAR_OK;
 }
 
@@ -773,7 +779,7 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out)) return OSCAR_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return OSCAR_ERR_INVALID_ARG;
   const int hq = c->lay.num_q_heads, hkv = c->lay.num_kv_heads;
-  const size_t slots = workspace_bytes / ((size_t)B * T * hq * kPartFloats * sizeof(float));
+  const size_t slots = workspace_bytes / tree_slot_bytes(c, B, T);
   TreeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.kd = static_cast<const __nv_bfloat16*>(k_draft);
@@ -787,7 +793,8 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   a.T = T;
   a.W = (T + 63) / 64;
   tree_splits(B, T, hkv, hq / hkv, (c->lay.sink + c->lay.recent) / kP, max_hist_pages, c->sms,
-              (int)std::min(slots, (size_t)1 << 20), &a.nsplit, &a.nb);
+              (int)std::min(slots, (size_t)1 << 20), &a.nsplit, &a.nb, &a.pps);
+  a.rows = tree_tile_rows(T, hq / hkv);
   if (a.nsplit == 0) return OSCAR_ERR_INVALID_ARG;   // too little workspace for the history's length
   a.scale_log2 = sm_scale * kLog2e;
   a.partials = static_cast<float*>(workspace);

@@ -121,7 +121,7 @@ int launch_tree_layout(int B, int T, const int* parents, const int* n_draft, con
                        int* positions, int* status, cudaStream_t st);
 struct TreeArgs;
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
-                 int* nb);
+                 int* nb, int* pps);
 int configure_tree_kernels();
 int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
 int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const void* v, const int* seq_lens,

@@ -12,8 +12,8 @@
 // error stays below pos 2^-65 turns. Its upper 32 bits, as a signed number of half turns, go to sincospif.
 //
 // Each (token, pair) angle is computed once per CTA into shared memory and serves all heads. A thread keeps
-// one 16-byte unit of the head and walks the heads, so the kernel moves 16 bytes per access and is bound by
-// memory: every element is read and written once.
+// one 16-byte unit of the head and walks tokens and heads, four units in flight, so the kernel moves 16 bytes per
+// access and is bound by memory: every element is read and written once.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -36,6 +36,7 @@ struct RopeArgs {
   const unsigned long long* turns;                 // [rot / 2]
   int n, dim, rot;
   int tokens;                                      // tokens per CTA
+  unsigned per_head;                               // ceil(2^32 / heads), i / heads for i heads < 2^32; 0 for one head
   float scale;
   int inverse;
 };
@@ -53,74 +54,94 @@ template <> __device__ __forceinline__ __half from_f(float x) { return __float2h
 template <typename T, int V, bool WIDE> struct alignas(WIDE ? sizeof(T) * V : sizeof(T)) Vec { T v[V]; };
 
 // One head's unit u: half layout: V channels from V u of the first half and their partners; pairs layout: V
-// channels (V / 2 pairs) from V u; units past the rotary part copy V channels.
+// channels (V / 2 pairs) from V u; units past the rotary part copy V channels. Loading and turning are apart, so that
+// a thread has several units' loads in flight before it stores any (in place, the compiler may not reorder them).
 template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ void rope_unit(const T* __restrict__ in, T* __restrict__ out, int u, int rot, int rot_units,
-                                          const float2* cs) {
+struct Unit {
   using W = Vec<T, V, WIDE>;
-  if (u >= rot_units) {                            // passed through
-    if (in == out) return;
-    const int at = rot + (u - rot_units) * V;
-    *reinterpret_cast<W*>(out + at) = *reinterpret_cast<const W*>(in + at);
-  } else if (HALF) {
-    const int at = u * V, half = rot / 2;
-    W a = *reinterpret_cast<const W*>(in + at), b = *reinterpret_cast<const W*>(in + at + half);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = to_f(a.v[e]), y = to_f(b.v[e]);
-      a.v[e] = from_f<T>(x * cs[e].x - y * cs[e].y);
-      b.v[e] = from_f<T>(y * cs[e].x + x * cs[e].y);
-    }
-    *reinterpret_cast<W*>(out + at) = a;
-    *reinterpret_cast<W*>(out + at + half) = b;
-  } else {
-    const int at = u * V;
-    W a = *reinterpret_cast<const W*>(in + at);
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      const float x = to_f(a.v[2 * e]), y = to_f(a.v[2 * e + 1]);
-      a.v[2 * e] = from_f<T>(x * cs[e].x - y * cs[e].y);
-      a.v[2 * e + 1] = from_f<T>(y * cs[e].x + x * cs[e].y);
-    }
-    *reinterpret_cast<W*>(out + at) = a;
+  W a, b;
+  __device__ __forceinline__ void load(const T* in, int at, int half, bool rotary) {
+    a = *reinterpret_cast<const W*>(in + at);
+    if (HALF && rotary) b = *reinterpret_cast<const W*>(in + at + half);
   }
-}
+  __device__ __forceinline__ void turn(const float2* cs) {
+    if (HALF) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = to_f(a.v[e]), y = to_f(b.v[e]);
+        a.v[e] = from_f<T>(x * cs[e].x - y * cs[e].y);
+        b.v[e] = from_f<T>(y * cs[e].x + x * cs[e].y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        const float x = to_f(a.v[2 * e]), y = to_f(a.v[2 * e + 1]);
+        a.v[2 * e] = from_f<T>(x * cs[e].x - y * cs[e].y);
+        a.v[2 * e + 1] = from_f<T>(y * cs[e].x + x * cs[e].y);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* out, int at, int half, bool rotary) const {
+    *reinterpret_cast<W*>(out + at) = a;
+    if (HALF && rotary) *reinterpret_cast<W*>(out + at + half) = b;
+  }
+};
 
 template <typename T, int V, bool HALF, bool WIDE>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a) {
   __shared__ float2 table[kRopeTable];             // [token][pair]: (cos, sin) times the scale
+  __shared__ int pos_s[kRopeTable];
   const int half = a.rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
+  for (int i = tid; i < nt; i += nthr) pos_s[i] = a.positions[t0 + i];
+  __syncthreads();
   for (int i = tid; i < nt * half; i += nthr) {
     const int t = i / half, j = i - t * half;
-    const int pos = a.positions[t0 + t];
-    const unsigned long long turn = (unsigned long long)(unsigned)pos * a.turns[j];
+    const unsigned long long turn = (unsigned long long)(unsigned)pos_s[t] * a.turns[j];
     float s, c;
     sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
     table[i] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
   }
   __syncthreads();
   constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
+  constexpr int kBatch = 4;                        // units a thread has in flight
   const int rot_units = HALF ? half / V : a.rot / V;
   const int units = rot_units + (a.dim - a.rot) / V;
-  const int heads = a.q.heads + a.k.heads;
-  for (int u = threadIdx.x; u < units; u += blockDim.x)
-    for (int t = 0; t < nt; ++t) {
-      if (a.positions[t0 + t] < 0) continue;       // a padded row: left as it is
-      float2 cs[kPer];
-      if (u < rot_units) {
+  const int heads = a.q.heads + a.k.heads, items = nt * heads;
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    const bool rotary = u < rot_units;
+    const int at = rotary ? u * V : a.rot + (u - rot_units) * V;
+    for (int i0 = threadIdx.y; i0 < items; i0 += kBatch * blockDim.y) {
+      Unit<T, V, HALF, WIDE> x[kBatch];
+      T* out[kBatch];
+      int tok[kBatch];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) cs[e] = table[t * half + u * kPer + e];
-      }
-#pragma unroll 4
-      for (int h = threadIdx.y; h < heads; h += blockDim.y) {
+      for (int k = 0; k < kBatch; ++k) {
+        const unsigned i = i0 + k * blockDim.y;    // (token, head): i = t heads + h
+        const int t = a.per_head != 0u ? __umulhi(i, a.per_head) : i, h = (int)i - t * heads;
         const bool isq = h < a.q.heads;
         const RopeSide& s = isq ? a.q : a.k;
         const int hh = isq ? h : h - a.q.heads;
-        rope_unit<T, V, HALF, WIDE>(static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + hh * s.in_head,
-                              static_cast<T*>(s.out) + (t0 + t) * s.out_tok + hh * s.out_head, u, a.rot, rot_units, cs);
+        const T* in = static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + hh * s.in_head;
+        out[k] = static_cast<T*>(s.out) + (t0 + t) * s.out_tok + hh * s.out_head;
+        tok[k] = t;
+        // a padded row is left as it is, and so is what is passed through in place
+        if ((int)i >= items || pos_s[t] < 0 || (!rotary && in == out[k])) out[k] = nullptr;
+        if (out[k] != nullptr) x[k].load(in, at, half, rotary);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (out[k] == nullptr) continue;
+        if (rotary) {
+          float2 cs[kPer];
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) cs[e] = table[tok[k] * half + u * kPer + e];
+          x[k].turn(cs);
+        }
+        x[k].store(out[k], at, half, rotary);
       }
     }
+  }
 }
 
 template <typename T, int V, bool HALF, bool WIDE>
@@ -129,6 +150,8 @@ int launch_as(RopeArgs a, cudaStream_t st) {
   const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / V;
   // as many tokens as fill the CTA's table, but two CTAs per SM and more while there are tokens for them
   a.tokens = std::max(1, std::min(kRopeTable / half, a.n / 304));
+  const unsigned heads = a.q.heads + a.k.heads;
+  a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
   k_rope<T, V, HALF, WIDE><<<(a.n + a.tokens - 1) / a.tokens, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;

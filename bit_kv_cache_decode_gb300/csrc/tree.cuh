@@ -7,6 +7,8 @@ namespace oscar {
 
 constexpr int kMaxTreeBf16Pages = 2040;   // sink and recent pages of a request
 
+constexpr int kTreeRows = 128;            // query rows (node, head) of a tile, the tensor cores' M
+
 struct TreeArgs {
   const __nv_bfloat16 *q, *kd, *vd;       // [B][T][hq][128], [B][T][hkv][128]
   const unsigned long long* mask;         // [B][T][W]: the drafted nodes a node attends to
@@ -15,24 +17,37 @@ struct TreeArgs {
   int max_hist_pages;
   const int* bf16_pt;
   int T, W;
-  int nsplit;                             // history slots of a row, then nb slots of BF16 and draft pages
-  int nb;
+  int nsplit, pps;                        // history slots at most, pages a slot takes at most
+  int nb;                                 // slots of BF16 and draft pages, after the nsplit history slots
+  int rows;                               // rows of a tile that have partials: min(128, T gq rounded up to 8)
   float scale_log2;                       // sm_scale * log2(e)
-  float* partials;                        // [B * T * hq][nsplit + nb][kPartFloats]
+  float* partials;                        // per (request, row tile, kv head) and slot: see tree_part
   void* out;
   int out_dtype;
   float* lse;
 };
 
+// query rows of a kv head that have partials in a tile, and tiles
+inline int tree_tiles(int T, int gq) { return (T * gq + kTreeRows - 1) / kTreeRows; }
+inline int tree_tile_rows(int T, int gq) { return T * gq >= kTreeRows ? kTreeRows : (T * gq + 7) / 8 * 8; }
+
 // nodes of request b that take part
 __device__ __forceinline__ int live_nodes(const TreeArgs& a, int b) {
   return a.n_draft != nullptr ? min(max(a.n_draft[b], 0), a.T) : a.T;
 }
-// the slot row of query row (b, node, head)
-__device__ __forceinline__ float* tree_part(const TreeArgs& a, int hq_total, int b, int node, int hq, int slot) {
-  return a.partials + ((((size_t)b * a.T + node) * hq_total + hq) * (a.nsplit + a.nb) + slot) * kPartFloats;
+// history pages of a request (length L), and the slots they are spread over
+__device__ __forceinline__ int tree_pages(const LayerView& lv, const TreeArgs& a, int L) {
+  return min((max(0, L - lv.sink - lv.recent) + kP - 1) / kP, a.max_hist_pages);
+}
+__device__ __forceinline__ int tree_hist_slots(const TreeArgs& a, int pages) { return (pages + a.pps - 1) / a.pps; }
+// Partials of slot `slot` of tile qt: acc as [32 channel quads][rows] float4, then (m, l) as [rows] float2, so that
+// the threads of a warp, one row each, write whole lines.
+__device__ __forceinline__ float* tree_part(const LayerView& lv, const TreeArgs& a, int b, int qt, int h, int slot) {
+  const int tiles = (a.T * (lv.hq / lv.hkv) + kTreeRows - 1) / kTreeRows;
+  return a.partials + ((((size_t)b * tiles + qt) * lv.hkv + h) * (a.nsplit + a.nb) + slot) * a.rows * kPartFloats;
 }
 
 int launch_tree_merge(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
+int configure_tree_merge();
 
 }  // namespace oscar

@@ -45,7 +45,7 @@ constexpr int kTreeThreads = 28 * 32;
 // what the CTA was launched with
 constexpr int kRegsLaunch = 72, kRegsRows = 96, kRegsUnpack = 64, kRegsCtl = 56;
 static_assert(2 * kRegsRows + 4 * kRegsUnpack + kRegsCtl <= 7 * kRegsLaunch, "register shares");
-constexpr int kRows = 128;                         // query rows of a CTA
+constexpr int kRows = kTreeRows;                   // query rows of a CTA
 constexpr int kStages = 8;                         // ring stages of one page block
 constexpr int kBufs = 4;                           // unpacked pages: keys, and values
 constexpr int kSboK = (kD / 8) * 128;              // keys: rows = tokens, 128 channels: 2,048 B between 8-row blocks
@@ -665,7 +665,6 @@ struct NearPages {
 // meet first (each has waited for its stream's last product); a CTA that failed writes empty ones.
 __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv, const TreeArgs& a, int h, int qt, int n, int live) {
   const int tid = threadIdx.x, w = tid >> 5, row = tid & (kRows - 1), half = (tid >> 7) & 1;
-  const int gq = lv.hq / lv.hkv, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;
   tc_fence_before();
   asm volatile("bar.sync 1, %0;" ::"r"(64 * ((live + 31) / 32)) : "memory");
   tc_fence_after();
@@ -674,11 +673,11 @@ __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv,
   const float m0 = __uint_as_float(u0.x), m1 = n > 1 ? __uint_as_float(u1.x) : -INFINITY;
   const float M = fmaxf(m0, m1);
   const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-  float* part = tree_part(a, lv.hq, blockIdx.z, min(node, a.T - 1), hq, blockIdx.x);
+  float* part = tree_part(lv, a, blockIdx.z, qt, h, blockIdx.x);
   const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO;
   if (row < live && half == 0) {
     const float l = w0 * __uint_as_float(u0.y) + (n > 1 ? w1 * __uint_as_float(u1.y) : 0.f);
-    *reinterpret_cast<float2*>(part) = good ? make_float2(M, l) : make_float2(-INFINITY, 0.f);
+    *reinterpret_cast<float2*>(part + a.rows * kD + 2 * row) = good ? make_float2(M, l) : make_float2(-INFINITY, 0.f);
   }
 #pragma unroll 1
   for (int k = 2 * half; k < 2 * half + 2; ++k) {
@@ -696,9 +695,9 @@ __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv,
       for (int t = 0; t < 32; ++t) x[t] *= w0;
     }
     if (row < live) {
+      float4* dst = reinterpret_cast<float4*>(part) + 8 * k * a.rows + row;
 #pragma unroll
-      for (int t = 0; t < 32; t += 4)
-        *reinterpret_cast<float4*>(part + 4 + 32 * k + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
+      for (int t = 0; t < 8; ++t) dst[t * a.rows] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
     }
   }
 }
@@ -794,21 +793,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     if (tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
     L = 0;
   }
-  int Lh = max(0, L - lv.sink - lv.recent), np = (Lh + kP - 1) / kP;
-  if (np > a.max_hist_pages) {
+  int Lh = max(0, L - lv.sink - lv.recent);
+  const int np = tree_pages(lv, a, L);
+  if (Lh > np * kP) {
     if (tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
-    np = a.max_hist_pages;
     Lh = np * kP;
   }
-  const int nbf = (lv.sink + lv.recent) / kP, near_pages = nbf + (nodes + kP - 1) / kP;
+  const int near_pages = (lv.sink + lv.recent) / kP + (nodes + kP - 1) / kP;
   int p0, n;                                       // first page and number of pages of the slot
   if (hist) {
-    p0 = (int)((long long)slot * np / a.nsplit);
-    n = (int)((long long)(slot + 1) * np / a.nsplit) - p0;
+    const int slots = tree_hist_slots(a, np);
+    if (slot >= slots) return;                     // a shorter request: the merge knows
+    p0 = (int)((long long)slot * np / slots);
+    n = (int)((long long)(slot + 1) * np / slots) - p0;
   } else {
     p0 = (slot - a.nsplit) * near_pages / a.nb;
     n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
   }
+  c.rest = 0;
 
   const int active = (live + 31) / 32;             // row warps with rows
   if (w == kLoadWarp) {
@@ -983,9 +985,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
 
 template <int FMT>
 int launch_fmt(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
-  const int tiles = (a.T * (lv.hq / lv.hkv) + kRows - 1) / kRows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.nsplit + a.nb, lv.hkv * tiles, B);
+  cfg.gridDim = dim3(a.nsplit + a.nb, lv.hkv * tree_tiles(a.T, lv.hq / lv.hkv), B);
   cfg.blockDim = dim3(kTreeThreads);
   cfg.dynamicSmemBytes = kTreeSmem;
   cfg.stream = st;
@@ -1006,14 +1007,16 @@ int configure_fmt() {
 // Slots of a query row: the history over nsplit of them, the BF16 and draft pages over nb. One CTA runs on an SM at a
 // time; its start (rotation of the rows, first pages) and its end cost about as much as kFixed history pages, a BF16
 // page, which is not pipelined as deeply, about as much as kNear. The counts that need the fewest waves times pages
-// win, and of equal ones those with the fewest slots, which the merge reads.
+// win, and of equal ones those with the fewest slots, which the merge reads. The host knows the page tables' width
+// only: a request shorter than that is spread over as many slots as its own pages fill, *pps each.
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
-                 int* nb) {
+                 int* nb, int* pps) {
   constexpr double kFixed = 20.0, kNear = 5.0;
   const long units = (long)B * hkv * ((T * gq + kRows - 1) / kRows);
   const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
   double best = 0.0;
   *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
+  *pps = 1;
   const int least = (pages + kPids - 1) / kPids;   // a slot's page ids fit shared memory
   for (int m = 1; m <= near && m < max_slots; ++m)
     for (int s = least; s <= std::max(least, std::min(pages, 2 * sms)) && s + m <= max_slots; ++s) {
@@ -1024,6 +1027,7 @@ void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int
         best = cost;
         *nsplit = s;
         *nb = m;
+        *pps = (pages + s - 1) / s;
       }
     }
 }
@@ -1035,7 +1039,7 @@ int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStr
 }
 
 int configure_tree_kernels() {
-  if (configure_fmt<kFmtF16>() != OSCAR_OK || configure_fmt<kFmtU8>() != OSCAR_OK) return OSCAR_ERR_CUDA;
+  if (configure_tree_merge() != OSCAR_OK || configure_fmt<kFmtF16>() != OSCAR_OK || configure_fmt<kFmtU8>() != OSCAR_OK) return OSCAR_ERR_CUDA;
   return configure_fmt<kFmtCB>();
 }
 

@@ -431,8 +431,9 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  *  out              : device [B][T][Hq][128], bf16 or fp32 (out_dtype), in the value basis of
  *                     oscar_decode_attention; lse : device float32 [B][T][Hq] or NULL
  *  workspace        : device, 256-byte aligned, of oscar_tree_workspace_bytes(cache, B, T, max_hist_pages) bytes; less
- *                     is accepted down to two slots per query row, B T Hq 1056 bytes (one more for every 4,096
- *                     history pages beyond the first 4,096), and splits the history less.
+ *                     is accepted and splits the history less, down to two slots of 528 bytes (one more for every
+ *                     4,096 history pages beyond the first 4,096) for each query row, where the T Hq / Hkv rows of
+ *                     a request and kv head count as a multiple of 8 up to 128 and of 128 above.
  *                     Calls that may overlap need a workspace each.
  * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
  * infinity in a drafted row reaches the rows that attend to it and no others.
