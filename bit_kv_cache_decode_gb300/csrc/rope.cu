@@ -12,8 +12,13 @@
 // error stays below pos 2^-65 turns. Its upper 32 bits, as a signed number of half turns, go to sincospif.
 //
 // Each (token, pair) angle is computed once per CTA into shared memory and serves all heads. A thread keeps
-// one 16-byte unit of the head and walks tokens and heads, four units in flight, so the kernel moves 16 bytes per
-// access and is bound by memory: every element is read and written once.
+// one unit of the head (16 bytes, or the 8 or 4 that the strides and the halves allow) and walks tokens and heads,
+// two units in flight; every element is read and written once, so the kernel is bound by memory. For 49,153 tokens
+// x 40 heads x 128 bf16 (1.007 GB): pairs layout 157 us (half of the head rotated; 6.42 TB/s, 95 % of the copy rate),
+// half layout 161 us (whole head). What carried it: streaming loads and stores (206 us with the default policy);
+// short CTAs of 8 tokens (32 tokens: 239 us); two units per thread (one: 166 us; four: 230 us, fewer threads fit);
+// 8 CTAs per SM for the pairs layout (6: 167 us) and 6 for the half layout, whose unit has two parts (8: 171 us);
+// narrower units rather than single elements (head 64, 24 channels rotated in halves: 138 us, elements 364 us).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -23,6 +28,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 1024;                   // (cos, sin) entries of a CTA's tokens
+constexpr int kRopeTokens = 8;                     // tokens of a CTA, at most
 
 struct RopeSide {                                  // q or k
   const void* in;
@@ -50,7 +56,11 @@ template <> __device__ __forceinline__ float from_f(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 
-// V elements, loaded and stored as one 16-byte access (WIDE) or one by one (rows on any element boundary)
+// V elements, loaded and stored as one access (WIDE: 16, 8 or 4 bytes) or one by one (rows on any element boundary)
+template <int BYTES> struct AccessOf;
+template <> struct AccessOf<16> { using type = uint4; };
+template <> struct AccessOf<8> { using type = uint2; };
+template <> struct AccessOf<4> { using type = unsigned; };
 template <typename T, int V, bool WIDE> struct alignas(WIDE ? sizeof(T) * V : sizeof(T)) Vec { T v[V]; };
 
 // One head's unit u: half layout: V channels from V u of the first half and their partners; pairs layout: V
@@ -59,10 +69,24 @@ template <typename T, int V, bool WIDE> struct alignas(WIDE ? sizeof(T) * V : si
 template <typename T, int V, bool HALF, bool WIDE>
 struct Unit {
   using W = Vec<T, V, WIDE>;
+  using Bits = typename AccessOf<WIDE ? sizeof(T) * V : 16>::type;
   W a, b;
+  // each element is touched once: streaming accesses where they are wide
+  static __device__ __forceinline__ W get(const T* at) {
+    if constexpr (WIDE) {
+      const Bits x = __ldcs(reinterpret_cast<const Bits*>(at));
+      return *reinterpret_cast<const W*>(&x);
+    } else {
+      return *reinterpret_cast<const W*>(at);
+    }
+  }
+  static __device__ __forceinline__ void put(T* at, const W& x) {
+    if constexpr (WIDE) __stcs(reinterpret_cast<Bits*>(at), *reinterpret_cast<const Bits*>(&x));
+    else *reinterpret_cast<W*>(at) = x;
+  }
   __device__ __forceinline__ void load(const T* in, int at, int half, bool rotary) {
-    a = *reinterpret_cast<const W*>(in + at);
-    if (HALF && rotary) b = *reinterpret_cast<const W*>(in + at + half);
+    a = get(in + at);
+    if (HALF && rotary) b = get(in + at + half);
   }
   __device__ __forceinline__ void turn(const float2* cs) {
     if (HALF) {
@@ -82,15 +106,15 @@ struct Unit {
     }
   }
   __device__ __forceinline__ void store(T* out, int at, int half, bool rotary) const {
-    *reinterpret_cast<W*>(out + at) = a;
-    if (HALF && rotary) *reinterpret_cast<W*>(out + at + half) = b;
+    put(out + at, a);
+    if (HALF && rotary) put(out + at + half, b);
   }
 };
 
 template <typename T, int V, bool HALF, bool WIDE>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a) {
   __shared__ float2 table[kRopeTable];             // [token][pair]: (cos, sin) times the scale
-  __shared__ int pos_s[kRopeTable];
+  __shared__ int pos_s[kRopeTokens];
   const int half = a.rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
   for (int i = tid; i < nt; i += nthr) pos_s[i] = a.positions[t0 + i];
@@ -104,7 +128,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a) {
   }
   __syncthreads();
   constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
-  constexpr int kBatch = 4;                        // units a thread has in flight
+  constexpr int kBatch = 2;                        // units a thread has in flight
   const int rot_units = HALF ? half / V : a.rot / V;
   const int units = rot_units + (a.dim - a.rot) / V;
   const int heads = a.q.heads + a.k.heads, items = nt * heads;
@@ -148,8 +172,8 @@ template <typename T, int V, bool HALF, bool WIDE>
 int launch_as(RopeArgs a, cudaStream_t st) {
   const int half = a.rot / 2;
   const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / V;
-  // as many tokens as fill the CTA's table, but two CTAs per SM and more while there are tokens for them
-  a.tokens = std::max(1, std::min(kRopeTable / half, a.n / 304));
+  // two CTAs per SM and more while there are tokens for them
+  a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.n / 304));
   const unsigned heads = a.q.heads + a.k.heads;
   a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
@@ -157,18 +181,31 @@ int launch_as(RopeArgs a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
+// the widest access, of 16 bytes at most, that every row, half and remainder starts on a multiple of; else elements
 template <typename T>
-int launch_typed(const RopeArgs& a, bool half_layout, bool wide, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (half_layout) return wide ? launch_as<T, V, true, true>(a, st) : launch_as<T, 1, true, false>(a, st);
-  return wide ? launch_as<T, V, false, true>(a, st) : launch_as<T, 2, false, false>(a, st);
+int launch_typed(const RopeArgs& a, bool half_layout, int bytes, cudaStream_t st) {
+  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), V4 = 4 / sizeof(T);
+  if (half_layout) {
+    if (bytes == 16) return launch_as<T, V16, true, true>(a, st);
+    if (bytes == 8) return launch_as<T, V8, true, true>(a, st);
+    if constexpr (V4 > 1) {
+      if (bytes == 4) return launch_as<T, V4, true, true>(a, st);
+    }
+    return launch_as<T, 1, true, false>(a, st);
+  }
+  if (bytes == 16) return launch_as<T, V16, false, true>(a, st);
+  if (bytes == 8) return launch_as<T, V8, false, true>(a, st);
+  if constexpr (V4 > 1) {
+    if (bytes == 4) return launch_as<T, V4, false, true>(a, st);
+  }
+  return launch_as<T, 2, false, false>(a, st);
 }
 
-bool vector_ok(const oscar_rope_tensor& t, int size, int v) {
+// whether accesses of v elements of `size` bytes fit a tensor's rows
+bool fits(const oscar_rope_tensor& t, int size, int v) {
   if (t.heads == 0) return true;
   const uintptr_t p = reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out);
-  return p % 16 == 0 && t.in_token % v == 0 && t.in_head % v == 0 && t.out_token % v == 0 && t.out_head % v == 0 &&
-         size * v == 16;
+  return p % (size * v) == 0 && t.in_token % v == 0 && t.in_head % v == 0 && t.out_token % v == 0 && t.out_head % v == 0;
 }
 
 RopeSide side(const oscar_rope_tensor& t) {
@@ -190,13 +227,15 @@ int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, i
   a.scale = scale;
   a.inverse = inverse;
   const bool half_layout = layout == OSCAR_ROPE_HALF;
-  // 16-byte units where every row, half and remainder starts on one, else element by element
-  const int size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2, v = 16 / size;
-  const bool wide = vector_ok(q, size, v) && vector_ok(k, size, v) && (half_layout ? rot / 2 : rot) % v == 0 &&
-                    (dim - rot) % v == 0;
-  if (dtype == OSCAR_DTYPE_FP32) return launch_typed<float>(a, half_layout, wide, st);
-  if (dtype == OSCAR_DTYPE_FP16) return launch_typed<__half>(a, half_layout, wide, st);
-  return launch_typed<__nv_bfloat16>(a, half_layout, wide, st);
+  const int size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
+  int bytes = 16;
+  for (; bytes > size; bytes /= 2) {
+    const int v = bytes / size;
+    if (fits(q, size, v) && fits(k, size, v) && (half_layout ? rot / 2 : rot) % v == 0 && (dim - rot) % v == 0) break;
+  }
+  if (dtype == OSCAR_DTYPE_FP32) return launch_typed<float>(a, half_layout, bytes, st);
+  if (dtype == OSCAR_DTYPE_FP16) return launch_typed<__half>(a, half_layout, bytes, st);
+  return launch_typed<__nv_bfloat16>(a, half_layout, bytes, st);
 }
 
 }  // namespace oscar
