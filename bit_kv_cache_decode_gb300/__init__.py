@@ -158,25 +158,44 @@ def _dev_i32(x, device):
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=device)
 
 
-def _own_i32(t, numel: int):
+def _here(t) -> tuple[int, int]:
+    """The current device, which t has to be on, and its current stream. (The handle is asked for directly: building
+    torch's stream object costs 3 us of a call.)"""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        raise OscarError(ERR_INVALID_ARG, "tensors on the current device")
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _in_i32(x, dev: int):
+    """int32 values for the library to read: a contiguous tensor on device dev, or host values that are copied."""
+    import torch
+    if isinstance(x, torch.Tensor):
+        if x.dtype != torch.int32 or x.get_device() != dev or not x.is_contiguous():
+            raise OscarError(ERR_INVALID_ARG, "contiguous int32 tensor on the current device")
+        return x
+    return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=dev)
+
+
+def _own_i32(t, numel: int, dev: int):
     """An int32 device tensor the library writes (never copied): contiguous, of at least numel elements."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or \
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous() or \
             t.numel() < numel:
-        raise OscarError(ERR_INVALID_ARG, f"int32 device tensor of at least {numel} elements")
+        raise OscarError(ERR_INVALID_ARG, f"contiguous int32 tensor of at least {numel} elements on the current device")
     return t
 
 
-def _check_words(t, B: int, T: int, what: str):
+def _check_words(t, B: int, T: int, dev: int, what: str):
     import torch
-    if t.dtype not in (torch.int64, torch.uint64) or not t.is_cuda or not t.is_contiguous() or \
-            tuple(t.shape) != (B, T, (T + 63) // 64):
+    if t.dtype not in (torch.int64, torch.uint64) or t.get_device() != dev or not t.is_contiguous() or \
+            t.shape != (B, T, (T + 63) // 64):
         raise OscarError(ERR_INVALID_ARG, what)
 
 
-def _check_bf16(t, shape, what: str):
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+def _check_like(t, dtype, shape, dev: int, what: str):
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
         raise OscarError(ERR_INVALID_ARG, what)
 
 
@@ -362,43 +381,56 @@ class OscarCache:
         With max_tokens, or a slots tensor [max_tokens, 4], each new token's (position, region, page, row) is
         written. Returns (rings_out, cu_tokens, slots)."""
         import torch
-        old, new = _dev_i32(old_lens, self.device), _dev_i32(new_lens, self.device)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.build_tables(old_lens, new_lens, hist_pt, bf16_pt, free_int2, free_bf16, rings, max_tokens,
+                                         rings_out, cu_tokens, slots)
+        dev, st = _here(self.pool)
+        old, new = _in_i32(old_lens, dev), _in_i32(new_lens, dev)
         B = old.numel()
-        for t, n in ((hist_pt, 0), (bf16_pt, B * (self.cfg.sink + self.cfg.recent) // self.cfg.page_size),
-                     (free_int2, self.cfg.num_int2_pages), (free_bf16, self.cfg.num_bf16_pages), (rings, 4)):
-            _own_i32(t, n)
-        rings_out = rings if rings_out is None else _own_i32(rings_out, 4)
-        cu_tokens = torch.empty(B + 1, dtype=torch.int32, device=self.device) if cu_tokens is None else \
-            _own_i32(cu_tokens, B + 1)
+        _own_i32(hist_pt, 0, dev)
+        _own_i32(bf16_pt, B * (self.cfg.sink + self.cfg.recent) // self.cfg.page_size, dev)
+        _own_i32(free_int2, self.cfg.num_int2_pages, dev)
+        _own_i32(free_bf16, self.cfg.num_bf16_pages, dev)
+        _own_i32(rings, 4, dev)
+        rings_out = rings if rings_out is None else _own_i32(rings_out, 4, dev)
+        cu_tokens = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_tokens is None else \
+            _own_i32(cu_tokens, B + 1, dev)
         if slots is None and max_tokens:
-            slots = torch.empty(max_tokens, 4, dtype=torch.int32, device=self.device)
+            slots = torch.empty(max_tokens, 4, dtype=torch.int32, device=dev)
         if slots is not None:
-            max_tokens = _own_i32(slots, 0).numel() // 4
+            max_tokens = _own_i32(slots, 0, dev).numel() // 4
         if new.numel() != B or hist_pt.dim() != 2 or hist_pt.shape[0] != B:
             raise OscarError(ERR_INVALID_ARG, "oscar_build_tables")
-        _check(_lib.oscar_build_tables(self._h, B, _ptr(old), _ptr(new), _ptr(hist_pt), hist_pt.shape[1],
-                                       _ptr(bf16_pt), _ptr(free_int2), _ptr(free_bf16), _ptr(rings), _ptr(rings_out),
-                                       _ptr(cu_tokens), _ptr(slots), max_tokens, _stream(stream)),
-               "oscar_build_tables")
+        _check(_lib.oscar_build_tables(self._h, B, old.data_ptr(), new.data_ptr(), hist_pt.data_ptr(), hist_pt.shape[1],
+                                       bf16_pt.data_ptr(), free_int2.data_ptr(), free_bf16.data_ptr(),
+                                       rings.data_ptr(), rings_out.data_ptr(), cu_tokens.data_ptr(), _ptr(slots),
+                                       max_tokens, st), "oscar_build_tables")
         return rings_out, cu_tokens, slots
 
     def tree_layout(self, parents, seq_lens, n_draft=None, mask=None, positions=None, stream=None):
         """Ancestor masks (int64 [B, T, ceil(T / 64)], 64 nodes a word) and positions (int32 [B, T]) of the trees
         given by parents [B, T]."""
         import torch
-        pa, sl = _dev_i32(parents, self.device), _dev_i32(seq_lens, self.device)
-        nd = None if n_draft is None else _dev_i32(n_draft, self.device)
-        B, T = pa.shape
-        if sl.numel() != B or (nd is not None and nd.numel() != B):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.tree_layout(parents, seq_lens, n_draft, mask, positions)
+        dev, st = _here(self.pool)
+        pa, sl = _in_i32(parents, dev), _in_i32(seq_lens, dev)
+        nd = None if n_draft is None else _in_i32(n_draft, dev)
+        if pa.dim() != 2 or sl.numel() != pa.shape[0] or (nd is not None and nd.numel() != pa.shape[0]):
             raise OscarError(ERR_INVALID_ARG, "oscar_tree_layout")
+        B, T = pa.shape
         if mask is None:
-            mask = torch.empty(B, T, (T + 63) // 64, dtype=torch.int64, device=self.device)
+            mask = torch.empty((B, T, (T + 63) // 64), dtype=torch.int64, device=dev)
+        else:
+            _check_words(mask, B, T, dev, "oscar_tree_layout")
         if positions is None:
-            positions = torch.empty(B, T, dtype=torch.int32, device=self.device)
-        _check_words(mask, B, T, "oscar_tree_layout")
-        _own_i32(positions, B * T)
-        _check(_lib.oscar_tree_layout(self._h, B, T, _ptr(pa), _ptr(nd), _ptr(sl), _ptr(mask), _ptr(positions),
-                                      _stream(stream)), "oscar_tree_layout")
+            positions = torch.empty((B, T), dtype=torch.int32, device=dev)
+        else:
+            _own_i32(positions, B * T, dev)
+        _check(_lib.oscar_tree_layout(self._h, B, T, pa.data_ptr(), _ptr(nd), sl.data_ptr(), mask.data_ptr(),
+                                      positions.data_ptr(), st), "oscar_tree_layout")
         return mask, positions
 
     def tree_workspace_bytes(self, batch: int, T: int, max_hist_pages: int) -> int:
@@ -413,57 +445,69 @@ class OscarCache:
         k_draft, v_draft [B, T, Hkv, 128]. workspace: a uint8 tensor of tree_workspace_bytes, allocated per call
         when not given; calls that may overlap need one each."""
         import torch
-        sl = _dev_i32(seq_lens, self.device)
-        hp = _dev_i32(hist_pt, self.device)
-        bp = _dev_i32(bf16_pt, self.device)
-        nd = None if n_draft is None else _dev_i32(n_draft, self.device)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.tree_attention(layer, q, k_draft, v_draft, mask, seq_lens, hist_pt, bf16_pt, sm_scale,
+                                           n_draft, out, out_dtype, lse, workspace)
+        dev, st = _here(self.pool)
+        sl, hp, bp = _in_i32(seq_lens, dev), _in_i32(hist_pt, dev), _in_i32(bf16_pt, dev)
+        nd = None if n_draft is None else _in_i32(n_draft, dev)
         B, T = int(q.shape[0]), int(q.shape[1])
-        _check_bf16(q, (B, T, self.cfg.num_q_heads, self.cfg.head_dim), "oscar_tree_attention")
-        for t in (k_draft, v_draft):
-            _check_bf16(t, (B, T, self.cfg.num_kv_heads, self.cfg.head_dim), "oscar_tree_attention")
-        _check_words(mask, B, T, "oscar_tree_attention")
+        rows = (B, T, self.cfg.num_q_heads, self.cfg.head_dim)
+        drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
+        _check_like(q, torch.bfloat16, rows, dev, "oscar_tree_attention")
+        _check_like(k_draft, torch.bfloat16, drafted, dev, "oscar_tree_attention")
+        _check_like(v_draft, torch.bfloat16, drafted, dev, "oscar_tree_attention")
+        _check_words(mask, B, T, dev, "oscar_tree_attention")
         mhp = hp.shape[1] if hp.dim() == 2 else 0
-        if sl.numel() != B or (nd is not None and nd.numel() != B) or hp.numel() != B * mhp or bp.shape[0] != B:
+        if sl.numel() != B or (nd is not None and nd.numel() != B) or hp.numel() != B * mhp or \
+                bp.numel() != B * ((self.cfg.sink + self.cfg.recent) // self.cfg.page_size):
             raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
+        out_type = torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16,
-                              device=self.device)
-        elif out.dtype != (torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16) or not out.is_contiguous() or \
-                out.shape != q.shape:
-            raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
+            out = torch.empty(rows, dtype=out_type, device=dev)
+        else:
+            _check_like(out, out_type, rows, dev, "oscar_tree_attention")
+        if lse is not None:
+            _check_like(lse, torch.float32, rows[:3], dev, "oscar_tree_attention")
         if workspace is None:
-            s = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(s):
-                workspace = torch.empty(self.tree_workspace_bytes(B, T, mhp), dtype=torch.uint8, device=self.device)
-        _check(_lib.oscar_tree_attention(self._h, layer, B, T, _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
-                                         _ptr(nd), _ptr(sl), _ptr(hp), mhp, _ptr(bp), float(sm_scale), _ptr(out),
-                                         out_dtype, _ptr(lse), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)),
-               "oscar_tree_attention")
+            workspace = torch.empty(self.tree_workspace_bytes(B, T, mhp), dtype=torch.uint8, device=dev)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
+        _check(_lib.oscar_tree_attention(self._h, layer, B, T, q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(),
+                                         mask.data_ptr(), _ptr(nd), sl.data_ptr(), hp.data_ptr(), mhp, bp.data_ptr(),
+                                         float(sm_scale), out.data_ptr(), out_dtype, _ptr(lse), workspace.data_ptr(),
+                                         workspace.nbytes, st), "oscar_tree_attention")
         return out
 
     def commit_draft(self, layer: int, k_draft, v_draft, seq_lens_before, n_accept, hist_pt, bf16_pt, path=None,
                      max_accept: int | None = None, stream=None):
         """Append nodes path[r, :n_accept[r]] of k_draft, v_draft [B, T, Hkv, 128] at seq_lens_before[r]; without a
         path nodes 0 .. n_accept[r] - 1 (max_accept of them at most, T by default)."""
-        sl = _dev_i32(seq_lens_before, self.device)
-        na = _dev_i32(n_accept, self.device)
-        hp = _dev_i32(hist_pt, self.device)
-        bp = _dev_i32(bf16_pt, self.device)
-        pa = None if path is None else _dev_i32(path, self.device)
+        import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.commit_draft(layer, k_draft, v_draft, seq_lens_before, n_accept, hist_pt, bf16_pt, path,
+                                         max_accept)
+        dev, st = _here(self.pool)
+        sl, na = _in_i32(seq_lens_before, dev), _in_i32(n_accept, dev)
+        hp, bp = _in_i32(hist_pt, dev), _in_i32(bf16_pt, dev)
+        pa = None if path is None else _in_i32(path, dev)
         B, T = int(k_draft.shape[0]), int(k_draft.shape[1])
-        for t in (k_draft, v_draft):
-            _check_bf16(t, (B, T, self.cfg.num_kv_heads, self.cfg.head_dim), "oscar_commit_draft")
+        drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
+        _check_like(k_draft, torch.bfloat16, drafted, dev, "oscar_commit_draft")
+        _check_like(v_draft, torch.bfloat16, drafted, dev, "oscar_commit_draft")
+        mhp = hp.shape[1] if hp.dim() == 2 else 0
+        if sl.numel() != B or na.numel() != B or hp.numel() != B * mhp or \
+                bp.numel() != B * ((self.cfg.sink + self.cfg.recent) // self.cfg.page_size) or \
+                (pa is not None and (pa.dim() != 2 or pa.shape[0] != B)):
+            raise OscarError(ERR_INVALID_ARG, "oscar_commit_draft")
         if pa is not None:
             max_accept = pa.shape[1]
         elif max_accept is None:
             max_accept = T
-        mhp = hp.shape[1] if hp.dim() == 2 else 0
-        if sl.numel() != B or na.numel() != B or hp.numel() != B * mhp or bp.shape[0] != B or \
-                (pa is not None and pa.shape[0] != B):
-            raise OscarError(ERR_INVALID_ARG, "oscar_commit_draft")
-        _check(_lib.oscar_commit_draft(self._h, layer, B, T, _ptr(k_draft), _ptr(v_draft), _ptr(sl), _ptr(na),
-                                       max_accept, _ptr(pa), _ptr(hp), mhp, _ptr(bp), _stream(stream)),
+        _check(_lib.oscar_commit_draft(self._h, layer, B, T, k_draft.data_ptr(), v_draft.data_ptr(), sl.data_ptr(),
+                                       na.data_ptr(), max_accept, _ptr(pa), hp.data_ptr(), mhp, bp.data_ptr(), st),
                "oscar_commit_draft")
 
     def set_decode_algo(self, algo: int):
@@ -569,25 +613,34 @@ def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool
     inputs themselves for in place). Rows with a negative position are left as they are: new tensors hold them
     unset. Returns (q_out, k_out)."""
     import torch
-    dtypes = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32, torch.float16: DTYPE_FP16}
-    pos = _dev_i32(positions, q.device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope(plan, q, k, positions, layout, inverse, q_out, k_out)
+    dev, st = _here(q)
+    pos = _in_i32(positions, dev)
+    dtype, shape, n = q.dtype, q.shape, pos.numel()
+    code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32 if dtype == torch.float32 else DTYPE_FP16
+    if (code == DTYPE_FP16 and dtype != torch.float16) or plan.turns.get_device() != dev or len(shape) != 3:
+        raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+    dim = shape[2]
     args, outs = [], []
     for x, out in ((q, q_out), (k, k_out)):
-        t = RopeTensor()
-        if x is not None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-            if x.dtype not in dtypes or x.dtype != q.dtype or out.dtype != x.dtype or x.dim() != 3 or \
-                    out.shape != x.shape or x.shape[0] != pos.numel() or x.shape[2] != q.shape[2] or \
-                    (x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1)) or not x.is_cuda or \
-                    out.device != x.device or plan.turns.device != x.device:
-                raise OscarError(ERR_INVALID_ARG, "oscar_rope")
-            t = RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-                           x.shape[1])
-        args.append(t)
+        if x is None:
+            args.append(RopeTensor())
+            outs.append(None)
+            continue
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype, device=dev)
+        if x.dtype != dtype or out.dtype != dtype or x.get_device() != dev or out.get_device() != dev or \
+                x.dim() != 3 or x.shape != out.shape or x.shape[0] != n or x.shape[2] != dim:
+            raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+        (it, ih, ic), (ot, oh, oc) = x.stride(), out.stride()
+        if dim > 1 and (ic != 1 or oc != 1):
+            raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+        args.append(RopeTensor(x.data_ptr(), out.data_ptr(), it, ih, ot, oh, x.shape[1]))
         outs.append(out)
-    _check(_lib.oscar_rope(ctypes.byref(args[0]), ctypes.byref(args[1]), pos.numel(), q.shape[2], dtypes[q.dtype],
-                           _ptr(pos), _ptr(plan.turns), plan.rotary_dim, layout, plan.scale, int(inverse),
-                           _stream(stream)), "oscar_rope")
+    _check(_lib.oscar_rope(args[0], args[1], n, dim, code, pos.data_ptr(), plan.turns.data_ptr(), plan.rotary_dim,
+                           layout, plan.scale, inverse, st), "oscar_rope")
     return outs[0], outs[1]
 
 
