@@ -814,7 +814,7 @@ int oscar_commit_draft(oscar_cache* c, int layer, int B, int T, const void* k_dr
     return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(k_draft) || !aligned16(v_draft)) return OSCAR_ERR_INVALID_ARG;
   return launch_commit_draft(view(c, layer), B, T, k_draft, v_draft, seq_lens_before, n_accept, max_accept, path,
-                             hist_pt, max_hist_pages, bf16_pt, static_cast<cudaStream_t>(stream));
+                             hist_pt, max_hist_pages, bf16_pt, c->sms, static_cast<cudaStream_t>(stream));
 }
 
 int oscar_get_status(oscar_cache* c, int* code) {

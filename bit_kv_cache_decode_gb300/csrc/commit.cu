@@ -4,12 +4,21 @@
 // Token j of request r (0 <= j < n_accept[r]) takes position p = L + j. If p >= sink + recent, the oldest
 // recent token, at position p - recent, is demoted first: rotated, clipped, quantised and packed into the
 // history. Its ring slot is the slot of p itself, and with n_accept <= recent no two tokens share a slot, so
-// the tokens are independent of one another: a CTA takes 16 of them (one tensor-core tile of demoted rows) of
-// one (request, kv head, K / V), stages the old rows, then rotates, quantises and overwrites.
+// the tokens are independent of one another. A unit of work is 16 of them (one tensor-core tile of demoted rows)
+// of one (request, kv head, K / V).
+//
+// A CTA serves one (kv head, K / V) and walks units: the places of 8 units at a time are looked up together, the
+// 64 KB of rotation fragments are fetched once, and a unit's old and new rows are loaded while the unit before it
+// is rotated. Half of the threads carry the old rows to the tile, the others the new rows to the slots, after a
+// barrier that follows the old rows' arrival.
 //
 // Rotation and quantiser are the append's own (rotate_tile16, quantize_pack_row), so the bytes are those of a
-// chain of oscar_append_kv calls. The call moves a few KB per request: its time is the latency of the launch,
-// the 64 KB of rotation fragments (from L2) and one tile.
+// chain of oscar_append_kv calls. The call moves a few KB per request; its time is latency: the launch, the
+// places, the fragments from L2 and a tile per unit (a tile's rows and fragments from shared memory, its 16 rows'
+// quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 22.4 us (a unit per CTA: 28.8 us; V fields set row
+// by row: 24.4 us); one request, 3 tokens: 5.7 us.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "qprep.cuh"
 #include "rotate.cuh"
@@ -29,119 +38,184 @@ struct CommitArgs {
   int T, max_accept, max_hist_pages;
 };
 
-__global__ void __launch_bounds__(kPrologueWarps * 32, 1) k_commit_draft(LayerView lv, CommitArgs a) {
+constexpr int kWarps = 16;                         // a warp rotates 8 channels of the tile and quantises a row of it
+constexpr int kUnits = 8;                          // units whose places are looked up together
+
+// The 2-bit V fields of a unit's demoted rows, channel-major in their pages. A channel's 64 rows are 16 bytes: thread
+// (channel, half) gathers the fields of the rows in its 8 bytes and sets them with one atomic pair per page (the
+// unit's rows are consecutive: one page or two). Atomics, as other rows of the same 8 bytes may be another unit's.
+// row0: the page row of the unit's row 0 (a row t's field is in half (t >> 2) & 1, so 8 of the 16 rows are a thread's).
+__device__ __forceinline__ void set_v_codes(const LayerView& lv, int h, int row0, const int* hpage,
+                                            const uint8_t (*codes)[kD / 4]) {
+  const int c = threadIdx.x & (kD - 1), half = threadIdx.x >> 7;
+  unsigned long long mask[2] = {0, 0}, value[2] = {0, 0};
+  int page[2] = {-1, -1};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = ((4 * half + (k & 3) - row0) & 7) + 8 * (k >> 2), t = row0 + i, e = t >= kP;
+    if (hpage[i] < 0) continue;
+    const int sh = 32 * (v_word(t) & 1) + v_bit(t % kP);
+    const unsigned long long m = 3ull << sh, v = (unsigned long long)((codes[i][c >> 2] >> (2 * (c & 3))) & 3) << sh;
+    mask[0] |= e ? 0ull : m;
+    value[0] |= e ? 0ull : v;
+    mask[1] |= e ? m : 0ull;
+    value[1] |= e ? v : 0ull;
+    if (e) page[1] = hpage[i];
+    else page[0] = hpage[i];
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (page[e] < 0) continue;
+    auto* at = reinterpret_cast<unsigned long long*>(int2_block_w(lv, page[e], h) + v_chan_off(c) + 8 * half);
+    atomicAnd(at, ~mask[e]);
+    if (value[e] != 0) atomicOr(at, value[e]);
+  }
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, CommitArgs a, int B) {
   extern __shared__ __align__(128) float smem[];
   uint32_t* frag_s = reinterpret_cast<uint32_t*>(smem);
   float* rows = smem + kRFragWords;                // [16][kTileStride]
   float* tau_s = rows + kTileFloats;               // [128]
   const uint32_t bars = smem_addr(tau_s + kD);
-  __shared__ int s_hpage[kTileRows], s_spage[kTileRows];   // demoted row's pages, -1: no demotion
-  __shared__ int s_page[kTileRows], s_row[kTileRows], s_node[kTileRows];   // new token's place, -1: none
-  const int b = blockIdx.x, h = blockIdx.y, kind = blockIdx.z & 1, j0 = (blockIdx.z >> 1) * kTileRows;
+  __shared__ int s_hpage[kUnits * kTileRows], s_hrow[kUnits * kTileRows];   // demoted row's place, -1: no demotion
+  __shared__ int s_page[kUnits * kTileRows], s_row[kUnits * kTileRows];     // new token's place, -1: none
+  __shared__ int s_node[kUnits * kTileRows];
+  __shared__ uint8_t codes[kTileRows][kD / 4];     // V rows' packed bytes
+  const int h = blockIdx.y, kind = blockIdx.z;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const int L = a.seq_lens[b];
-  int n = a.n_accept[b];
-  if (L < 0 || n < 0 || n > a.max_accept || L > 0x7fffffff - n) {   // the whole request is left as it is
-    if (tid == 0 && blockIdx.z == 0 && h == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
-    return;
-  }
-  if (j0 >= n) return;
-  const int nj = min(kTileRows, n - j0);
   const int per_req = (lv.sink + lv.recent) / kP;
+  const int tiles = (a.max_accept + kTileRows - 1) / kTileRows;
+  const long long units = (long long)B * tiles, step = gridDim.x;
+  const bool turns = kind == OSCAR_KIND_K || lv.v_explicit;   // this kind's rows are rotated
+  const float* prm = lv.params + (size_t)h * kParamFloats;
   auto in = [](int p, int count) { return p >= 0 && p < count; };
-  if (tid < kTileRows) {
-    int hpage = -1, spage = -1, page = -1, row = 0, node = -1;
-    if (tid < nj) {
-      const int p = L + j0 + tid;
-      node = a.path != nullptr ? a.path[(size_t)b * a.max_accept + j0 + tid] : j0 + tid;
-      if (!in(node, a.T)) {
-        flag(lv.status, OSCAR_STATUS_BAD_TREE);
-        node = -1;
+  if (tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
+  bool fetched = false, rotated = false;
+
+  for (long long u0 = blockIdx.x; u0 < units; u0 += kUnits * step) {
+    // ---- the places of 8 units' tokens, one per thread ----
+    const long long u = u0 + (tid >> 4) * step;
+    int b = 0, j = 0, L = 0, n = 0;
+    bool live = false;
+    if (tid < kUnits * kTileRows && u < units) {
+      b = (int)(u / tiles);
+      j = (int)(u - (long long)b * tiles) * kTileRows + (tid & 15);
+      L = a.seq_lens[b];
+      n = a.n_accept[b];
+      live = L >= 0 && n >= 0 && n <= a.max_accept && L <= 0x7fffffff - n;   // else the whole request is left as it is
+      if (!live && j == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
+      live = live && j < n;
+    }
+    const int p = L + j;
+    const bool full = live && p >= lv.sink + lv.recent;
+    const bool may = __syncthreads_or(full);       // some row may be demoted: the fragments start now
+    if (turns && may && !fetched) {
+      fetched = true;
+      if (lane == 0 && w < 8) {
+        const float* f = prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff);
+        constexpr int chunk = kRFragWords / 8;
+        mbar_init(bars + 8 * w);
+        bulk_load_hint(smem_addr(frag_s + w * chunk), f + w * chunk, chunk * 4, bars + 8 * w, l2_evict_last());
       }
-      const int slot = p < lv.sink ? p : lv.sink + (p - lv.sink) % lv.recent;
-      row = slot % kP;
-      page = a.bf16_pt[(size_t)b * per_req + slot / kP];
-      if (!in(page, lv.n_bf16)) {
-        flag(lv.status, OSCAR_STATUS_BAD_PAGE);
-        page = -1;
+    }
+    if (tid < kUnits * kTileRows) {
+      const int slot = !live ? 0 : p < lv.sink ? p : lv.sink + (p - lv.sink) % lv.recent;
+      const int hh = p - lv.recent - lv.sink;
+      const bool fits = full && hh / kP < a.max_hist_pages;
+      // three independent loads, checked afterwards
+      int node = !live ? -1 : a.path != nullptr ? a.path[(size_t)b * a.max_accept + j] : j;
+      int page = live ? a.bf16_pt[(size_t)b * per_req + slot / kP] : -1;
+      int hpage = fits ? a.hist_pt[(size_t)b * a.max_hist_pages + hh / kP] : -1;
+      if (live) {
+        const bool ok_node = in(node, a.T), ok_page = in(page, lv.n_bf16), ok_hist = !full || in(hpage, lv.n_int2);
+        if (!ok_node) flag(lv.status, OSCAR_STATUS_BAD_TREE);
+        if (!ok_page) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
+        // the old token has nowhere to go: the new one stays out
+        if (ok_node && ok_page && !ok_hist) flag(lv.status, fits ? OSCAR_STATUS_BAD_PAGE : OSCAR_STATUS_BAD_SEQLEN);
+        if (!ok_node || !ok_page || !ok_hist) page = hpage = -1;
       }
-      if (p >= lv.sink + lv.recent && page >= 0 && node >= 0) {
-        const int hh = p - lv.recent - lv.sink;
-        const bool fits = hh / kP < a.max_hist_pages;
-        hpage = fits ? a.hist_pt[(size_t)b * a.max_hist_pages + hh / kP] : -1;
-        if (!fits || !in(hpage, lv.n_int2)) {
-          flag(lv.status, fits ? OSCAR_STATUS_BAD_PAGE : OSCAR_STATUS_BAD_SEQLEN);
-          hpage = -1;
-          node = -1;                               // the old token has nowhere to go: the new one stays out
-        } else {
-          spage = page;
+      s_hpage[tid] = hpage;
+      s_hrow[tid] = hh & (kP - 1);                 // (hh < 0: row 0 of a unit whose later rows are demoted)
+      s_page[tid] = page;
+      s_row[tid] = slot % kP;
+      s_node[tid] = node;
+    }
+    __syncthreads();
+    // ---- unit by unit: 16 bytes of row r for each thread, an old row's or a new one's ----
+    const bool is_new = tid >= 256;
+    const int r = (tid >> 4) & 15, c8 = tid & 15;
+    auto load = [&](int q) {
+      const int m = q * kTileRows + r;
+      const uint4* src = nullptr;
+      if (q < kUnits && s_page[m] >= 0) {
+        if (is_new) {
+          const long long rb = (u0 + q * step) / tiles;
+          src = reinterpret_cast<const uint4*>((kind == OSCAR_KIND_K ? a.k : a.v) +
+                                               ((rb * a.T + s_node[m]) * lv.hkv + h) * kD + 8 * c8);
+        } else if (s_hpage[m] >= 0) {
+          src = reinterpret_cast<const uint4*>(bf16_row(lv, s_page[m], h, kind, s_row[m]) + 8 * c8);
         }
       }
-      if (node < 0) page = -1;
-    }
-    s_hpage[tid] = hpage;
-    s_spage[tid] = spage;
-    s_page[tid] = page;
-    s_row[tid] = row;
-    s_node[tid] = node;
-  }
-  const bool demotes = (long long)L + j0 + nj > lv.sink + lv.recent;   // some row of the tile is demoted
-  const bool rotate = demotes && (kind == OSCAR_KIND_K || lv.v_explicit);
-  const float* prm = lv.params + (size_t)h * kParamFloats;
-  if (rotate && tid == 0) {
-    const float* f = prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff);
-    constexpr int chunk = kRFragWords / 8;
-    for (int c = 0; c < 8; ++c) {
-      mbar_init(bars + 8 * c);
-      bulk_load_hint(smem_addr(frag_s + c * chunk), f + c * chunk, chunk * 4, bars + 8 * c, l2_evict_last());
-    }
-  }
-  if (tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
-  __syncthreads();
-  {
-    // the demoted rows, one 16-byte chunk per thread
-    const int r = tid >> 4, c8 = tid & 15;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (s_spage[r] >= 0) u = *reinterpret_cast<const uint4*>(bf16_row(lv, s_spage[r], h, kind, s_row[r]) + 8 * c8);
-    const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
-    float4* dst = reinterpret_cast<float4*>(rows + r * kTileStride + 8 * c8);
-    dst[0] = make_float4(__uint_as_float(wds[0] << 16), __uint_as_float(wds[0] & 0xffff0000u),
-                         __uint_as_float(wds[1] << 16), __uint_as_float(wds[1] & 0xffff0000u));
-    dst[1] = make_float4(__uint_as_float(wds[2] << 16), __uint_as_float(wds[2] & 0xffff0000u),
-                         __uint_as_float(wds[3] << 16), __uint_as_float(wds[3] & 0xffff0000u));
-  }
-  __syncthreads();                                 // the old rows are staged: their slots may be overwritten
-  if (rotate && !rotate_tile16(frag_s, rows, bars)) {
-    if (tid == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
-    mbar_wait(bars + 8 * w, 0);                    // one more bounded wait for the copies in flight
-    return;                                        // these tokens are left out
-  }
-  for (int r = w; r < nj; r += kPrologueWarps) {
-    if (s_hpage[r] >= 0) {
-      const int hh = L + j0 + r - lv.recent - lv.sink;
-      float y[4];
+      return src != nullptr ? *src : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 next = load(0);
+    for (int q = 0; q < kUnits && u0 + q * step < units; ++q) {
+      const int m = q * kTileRows + r;
+      const uint4 x = next;
+      if (!is_new) {
+        const uint32_t wds[4] = {x.x, x.y, x.z, x.w};
+        float4* dst = reinterpret_cast<float4*>(rows + r * kTileStride + 8 * c8);
+        dst[0] = make_float4(__uint_as_float(wds[0] << 16), __uint_as_float(wds[0] & 0xffff0000u),
+                             __uint_as_float(wds[1] << 16), __uint_as_float(wds[1] & 0xffff0000u));
+        dst[1] = make_float4(__uint_as_float(wds[2] << 16), __uint_as_float(wds[2] & 0xffff0000u),
+                             __uint_as_float(wds[3] << 16), __uint_as_float(wds[3] & 0xffff0000u));
+      }
+      const bool demotes = __syncthreads_or(s_hpage[m] >= 0);   // the tile is staged, the old rows are read
+      next = load(q + 1);
+      if (demotes) {
+        if (turns) {
+          rotated = true;
+          if (!rotate_tile16<kD / 8 / kWarps>(frag_s, rows, bars)) {
+            if (tid == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
+            if (w < 8) mbar_wait(bars + 8 * w, 0); // one more bounded wait for the copies in flight
+            return;                                // these tokens are left out
+          }
+        }
+        const int at = q * kTileRows + w;          // a warp's row
+        if (s_hpage[at] >= 0) {
+          float y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = rows[r * kTileStride + rot_channel(lane, e)];
-      quantize_pack_row(y, tau_s, int2_block_w(lv, s_hpage[r], h), hh % kP, kind,
-                        lv.meta_u8 ? meta_consts(lv, h, kind) : nullptr, lv.meta_cb ? cb_consts(lv, h, kind) : nullptr,
-                        lv.status);
+          for (int e = 0; e < 4; ++e) y[e] = rows[w * kTileStride + rot_channel(lane, e)];
+          uint8_t* blk = int2_block_w(lv, s_hpage[at], h);
+          const unsigned byte = quantize_row(y, tau_s, blk, s_hrow[at], kind,
+                                             lv.meta_u8 ? meta_consts(lv, h, kind) : nullptr,
+                                             lv.meta_cb ? cb_consts(lv, h, kind) : nullptr, lv.status);
+          if (kind == OSCAR_KIND_K) blk[kKCodesOff + s_hrow[at] * (kD / 4) + rev5(lane)] = (uint8_t)byte;
+          else codes[w][rev5(lane)] = (uint8_t)byte;
+        }
+      }
+      if (is_new && s_page[m] >= 0) {
+        if (bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y) || bf16x2_nonfinite(x.z) || bf16x2_nonfinite(x.w))
+          flag(lv.status, OSCAR_STATUS_NONFINITE);
+        *reinterpret_cast<uint4*>(bf16_row(lv, s_page[m], h, kind, s_row[m]) + 8 * c8) = x;
+      }
+      __syncthreads();                             // the tile is free, the codes are complete
+      if (demotes && kind == OSCAR_KIND_V) {
+        if (tid < 2 * kD) set_v_codes(lv, h, s_hrow[q * kTileRows], s_hpage + q * kTileRows, codes);
+        // the next unit's codes are written after a barrier of its own
+      }
     }
-    if (s_page[r] >= 0) {
-      const __nv_bfloat16* src =
-          (kind == OSCAR_KIND_K ? a.k : a.v) + (((size_t)b * a.T + s_node[r]) * lv.hkv + h) * kD;
-      const uint2 x = reinterpret_cast<const uint2*>(src)[lane];
-      if (__any_sync(0xffffffffu, bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y)) && lane == 0)
-        flag(lv.status, OSCAR_STATUS_NONFINITE);
-      reinterpret_cast<uint2*>(bf16_row(lv, s_page[r], h, kind, s_row[r]))[lane] = x;
-    }
+    __syncthreads();                               // the places are free
   }
+  if (fetched && !rotated && w < 8) mbar_wait(bars + 8 * w, 0);   // copies requested but unused: let them land
 }
 
 }  // namespace
 
 int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const void* v, const int* seq_lens,
                         const int* n_accept, int max_accept, const int* path, const int* hist_pt, int max_hist_pages,
-                        const int* bf16_pt, cudaStream_t st) {
+                        const int* bf16_pt, int sms, cudaStream_t st) {
   CommitArgs a;
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);
@@ -153,12 +227,17 @@ int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const 
   a.T = T;
   a.max_accept = max_accept;
   a.max_hist_pages = max_hist_pages;
-  const dim3 grid(B, lv.hkv, 2 * ((max_accept + kTileRows - 1) / kTileRows));
-  k_commit_draft<<<grid, kPrologueWarps * 32, kCommitSmem, st>>>(lv, a);
+  // two CTAs fit an SM; a (kv head, kind) gets its share of them, as many as it has units
+  const long long units = (long long)B * ((max_accept + kTileRows - 1) / kTileRows);
+  const int share = std::max(1, sms / lv.hkv);
+  const dim3 grid((unsigned)std::min<long long>(units, share), lv.hkv, 2);
+  k_commit_draft<<<grid, kWarps * 32, kCommitSmem, st>>>(lv, a, B);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 int configure_commit_kernel() {
+  if (cudaFuncSetAttribute(k_commit_draft, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+    return OSCAR_ERR_CUDA;
   return cudaFuncSetAttribute(k_commit_draft, cudaFuncAttributeMaxDynamicSharedMemorySize, kCommitSmem) == cudaSuccess
              ? OSCAR_OK
              : OSCAR_ERR_CUDA;

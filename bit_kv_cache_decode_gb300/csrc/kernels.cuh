@@ -126,7 +126,7 @@ int configure_tree_kernels();
 int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
 int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const void* v, const int* seq_lens,
                         const int* n_accept, int max_accept, const int* path, const int* hist_pt, int max_hist_pages,
-                        const int* bf16_pt, cudaStream_t st);
+                        const int* bf16_pt, int sms, cudaStream_t st);
 int configure_commit_kernel();
 constexpr int kSharedRows = 128;   // query rows (request x head) per CTA of the shared-prefix decode
 int launch_decode_shared(const LayerView& lv, const DecodeWorkspace& ws, const DecodeArgs& a, cudaStream_t st);

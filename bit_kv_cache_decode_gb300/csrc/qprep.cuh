@@ -78,6 +78,7 @@ __device__ __forceinline__ uint32_t f16x2_of(const float* x) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+template <int NB = 2>
 __device__ __forceinline__ bool rotate_tile16(const uint32_t* frag_s, float* rows, uint32_t bars) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t a[8][4];
@@ -90,15 +91,15 @@ __device__ __forceinline__ bool rotate_tile16(const uint32_t* frag_s, float* row
     a[kb][2] = f16x2_of(r0 + 8);       // row g, channels 16 kb + 2t + 8, +9
     a[kb][3] = f16x2_of(r8 + 8);
   }
-  float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  float acc[NB][4] = {};
   bool landed = true;
 #pragma unroll
   for (int kb = 0; kb < 8; ++kb) {
     landed = landed && mbar_wait(bars + 8 * kb, 0);
     if (!landed) break;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 f = *reinterpret_cast<const uint4*>(frag_s + ((kb * 16 + 2 * w + j) * 32 + lane) * 4);
+    for (int j = 0; j < NB; ++j) {
+      const uint4 f = *reinterpret_cast<const uint4*>(frag_s + ((kb * 16 + NB * w + j) * 32 + lane) * 4);
       float d[4];
       qp_mma(d, a[kb][0], a[kb][1], a[kb][2], a[kb][3], f.x, f.y, true);    // x R_hi
       qp_mma(d, a[kb][0], a[kb][1], a[kb][2], a[kb][3], f.z, f.w, false);   // + x R_lo
@@ -108,8 +109,8 @@ __device__ __forceinline__ bool rotate_tile16(const uint32_t* frag_s, float* row
   }
   if (!__syncthreads_and(landed)) return false;        // also: every warp has read its A rows
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int col = 8 * (2 * w + j) + 2 * t;            // rotated channel
+  for (int j = 0; j < NB; ++j) {
+    const int col = 8 * (NB * w + j) + 2 * t;            // rotated channel
     *reinterpret_cast<float2*>(rows + g * kTileStride + col) = make_float2(acc[j][0], acc[j][1]);
     *reinterpret_cast<float2*>(rows + (g + 8) * kTileStride + col) = make_float2(acc[j][2], acc[j][3]);
   }

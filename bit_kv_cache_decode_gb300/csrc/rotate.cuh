@@ -77,17 +77,17 @@ __device__ __forceinline__ void warp_rotate(const float* __restrict__ U, const f
 
 __device__ __forceinline__ float sat_fp16(float x) { return fminf(fmaxf(x, -65504.f), 65504.f); }
 
-// Quantise one rotated row held as y[r] (channel rot_channel(lane, r)) and
-// write its packed byte and group metadata into the page block `blk`, row
-// `row`, half `kind` (OSCAR_KIND_K / OSCAR_KIND_V). tau: float [128] clip
+// Quantise one rotated row held as y[r] (channel rot_channel(lane, r)), write its group metadata into the
+// page block `blk`, row `row`, half `kind` (OSCAR_KIND_K / OSCAR_KIND_V), and return the lane's packed byte
+// (byte rev5(lane) of the row: the codes of channels 4 rev5(lane) .. + 3). tau: float [128] clip
 // thresholds indexed by rotated channel. mc: null for the fp16 (scale, zero) metadata, else the
 // kind's compact-format constants {T, D, E, 0} for groups 0 and 1 (8 floats). cb: null, or the kind's
 // codebook constants {k_0..k_3, theta_0..theta_2, 0} (codebook format: fp16 range and zero).
 // status: when not null, OSCAR_STATUS_NONFINITE is flagged for a non-finite input value and
 // OSCAR_STATUS_SATURATED for fp16 metadata stored saturated.
-__device__ __forceinline__ void quantize_pack_row(const float (&y_in)[4], const float* __restrict__ tau,
-                                                  uint8_t* blk, int row, int kind, const float* __restrict__ mc,
-                                                  const float* __restrict__ cb = nullptr, int* status = nullptr) {
+__device__ __forceinline__ unsigned quantize_row(const float (&y_in)[4], const float* __restrict__ tau, uint8_t* blk,
+                                                 int row, int kind, const float* __restrict__ mc,
+                                                 const float* __restrict__ cb = nullptr, int* status = nullptr) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
 #pragma unroll
@@ -132,13 +132,6 @@ __device__ __forceinline__ void quantize_pack_row(const float (&y_in)[4], const 
     byte |= ((unsigned)c) << (2 * rev2(r));
   }
   if (status != nullptr && __any_sync(0xffffffffu, bad) && lane == 0) flag(status, OSCAR_STATUS_NONFINITE);
-  const int b = rev5(lane);
-  if (kind == OSCAR_KIND_K) {
-    blk[kKCodesOff + row * (kD / 4) + b] = (uint8_t)byte;
-  } else {                                       // channel-major: one 2-bit field per channel
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v_set_code(blk, rot_channel(lane, r), row, (byte >> (2 * rev2(r))) & 3u);
-  }
   if (lane < 2) {                                // lane 0: group 0, lane 1: group 1
     if (mc == nullptr) {
       __half2 sz = __halves2half2(s16, z16);
@@ -148,6 +141,21 @@ __device__ __forceinline__ void quantize_pack_row(const float (&y_in)[4], const 
       const int off = (kind == OSCAR_KIND_K ? kKMetaOff : kVMetaOffU8) + row * (kNG * 2) + lane * 2;
       *reinterpret_cast<uint16_t*>(blk + off) = (uint16_t)(mn8 | (mx8 << 8));
     }
+  }
+  return byte;
+}
+
+// The same, with the codes packed into the page block too.
+__device__ __forceinline__ void quantize_pack_row(const float (&y)[4], const float* __restrict__ tau, uint8_t* blk,
+                                                  int row, int kind, const float* __restrict__ mc,
+                                                  const float* __restrict__ cb = nullptr, int* status = nullptr) {
+  const int lane = threadIdx.x & 31;
+  const unsigned byte = quantize_row(y, tau, blk, row, kind, mc, cb, status);
+  if (kind == OSCAR_KIND_K) {
+    blk[kKCodesOff + row * (kD / 4) + rev5(lane)] = (uint8_t)byte;
+  } else {                                       // channel-major: one 2-bit field per channel
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v_set_code(blk, rot_channel(lane, r), row, (byte >> (2 * rev2(r))) & 3u);
   }
 }
 

@@ -10,8 +10,9 @@
 // Every CTA scans the lengths itself (a few KB, in L2 after the first), then takes its share of the tables and
 // of the new tokens' slots; a slot's page is looked up from the request's table or, for a page popped by this
 // call, from the ring, never from an entry another CTA writes. The last CTA to finish reading writes the new
-// ring positions, which may alias the old ones. The kernel is bound by its launch for small batches and by the
-// 16-byte slot stores for long prompts.
+// ring positions, which may alias the old ones. The kernel is bound by latency: its launch, the lengths, the scan, a
+// page id. 64 prompts of up to 16K tokens (slots 9 MB): 11.9 us; one prompt of 777: 5.1 us. Up to eight CTAs per SM
+// hide the slots' lookups (one: 18 us).
 //
 // k_tree_layout. Ancestor sets by pointer doubling: after step k a node's bit set holds its ancestors within
 // 2^k steps, so T nodes take log2 T steps of one OR per word.
@@ -49,79 +50,81 @@ __device__ __forceinline__ int bf16_pages(int L, int sink, int recent) {
   return (min(L, sink) + kP - 1) / kP + (min(max(L - sink, 0), recent) + kP - 1) / kP;
 }
 
-// inclusive block scan of three counts
-__device__ __forceinline__ void block_scan3(long long (&v)[3], long long (*red)[3]) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// tokens; page ids popped and pushed, of history and BF16 pages. 64 bits: the lengths are checked after they are summed
+struct Counts {
+  long long v[5];
+  __device__ void operator+=(const Counts& x) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      const long long x = __shfl_up_sync(0xffffffffu, v[e], o);
-      if (lane >= o) v[e] += x;
-    }
-  __syncthreads();
-  if (lane == 31)
-    for (int e = 0; e < 3; ++e) red[w][e] = v[e];
-  __syncthreads();
-  for (int i = 0; i < w; ++i)
-    for (int e = 0; e < 3; ++e) v[e] += red[i][e];
-}
+    for (int e = 0; e < 5; ++e) v[e] += x.v[e];
+  }
+};
+enum { kTokens, kPopH, kPushH, kPopB, kPushB };
 
 __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
   extern __shared__ int smem[];
   int* tok0 = smem;                                // [B + 1] first new token of a request
-  int* pop_h = tok0 + a.B + 1;                     // [B + 1] history pages popped (pushed: ~) before it
+  int* pop_h = tok0 + a.B + 1;                     // [B + 1] history pages popped before it (pushed, if it is released)
   int* pop_b = pop_h + a.B + 1;
-  __shared__ long long red[kTabThreads / 32][3];
+  __shared__ Counts red[kTabThreads / 32];
   __shared__ int s_ring[4], s_bad;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid < 4) s_ring[tid] = a.rings_in[tid];
   if (tid == 0) s_bad = 0;
-  __syncthreads();
 
-  // ---- the scan: tokens, pages popped, pages pushed. Released requests count pushes in the upper half. ----
-  long long carry[3] = {0, 0, 0};                  // tokens, history pops | pushes << 32, BF16 pops | pushes << 32
+  // ---- the scan: each thread counts a run of requests, the CTA scans the threads' sums ----
   int bad = 0;
-  for (int r0 = 0; r0 < a.B; r0 += kTabThreads) {
-    const int r = r0 + tid;
-    long long v[3] = {0, 0, 0};
-    if (r < a.B) {
-      const int o = a.old_lens[r], n = a.new_lens[r];
-      if (o < 0 || n < 0 || (n < o && n != 0) || hist_pages(n, a.sink, a.recent) > a.max_hist_pages ||
-          hist_pages(o, a.sink, a.recent) > a.max_hist_pages) {
-        bad |= OSCAR_STATUS_BAD_SEQLEN;
-      } else {
-        const int ho = hist_pages(o, a.sink, a.recent), hn = hist_pages(n, a.sink, a.recent);
-        const int bo = bf16_pages(o, a.sink, a.recent), bn = bf16_pages(n, a.sink, a.recent);
-        v[0] = max(0, n - o);
-        v[1] = n >= o ? hn - ho : (long long)ho << 32;
-        v[2] = n >= o ? bn - bo : (long long)bo << 32;
-      }
+  auto counts = [&](int r) {
+    Counts c = {};
+    const int o = a.old_lens[r], n = a.new_lens[r];
+    const int ho = hist_pages(o, a.sink, a.recent), hn = hist_pages(n, a.sink, a.recent);
+    if (o < 0 || n < 0 || (n < o && n != 0) || hn > a.max_hist_pages || ho > a.max_hist_pages) {
+      bad |= OSCAR_STATUS_BAD_SEQLEN;
+    } else {
+      const int bo = bf16_pages(o, a.sink, a.recent), bn = bf16_pages(n, a.sink, a.recent);
+      c.v[kTokens] = max(0, n - o);
+      c.v[kPopH] = n >= o ? hn - ho : 0;
+      c.v[kPushH] = n >= o ? 0 : ho;
+      c.v[kPopB] = n >= o ? bn - bo : 0;
+      c.v[kPushB] = n >= o ? 0 : bo;
     }
-    const long long mine[3] = {v[0], v[1], v[2]};
-    block_scan3(v, red);
-    if (r < a.B) {
-      const long long t = carry[0] + v[0] - mine[0], h = carry[1] + v[1] - mine[1], b = carry[2] + v[2] - mine[2];
-      const bool release = mine[1] >> 32 || mine[2] >> 32;
-      tok0[r] = (int)min(t, (long long)0x7fffffff);
-      pop_h[r] = release ? (int)(h >> 32) : (int)h;
-      pop_b[r] = release ? (int)(b >> 32) : (int)b;
-    }
-    for (int e = 0; e < 3; ++e) {
-      long long total = 0;
-      for (int i = 0; i < kTabThreads / 32; ++i) total += red[i][e];
-      carry[e] += total;
-    }
-    __syncthreads();
+    return c;
+  };
+  const int run = (a.B + kTabThreads - 1) / kTabThreads, r_lo = min(tid * run, a.B), r_hi = min(r_lo + run, a.B);
+  Counts mine = {};
+#pragma unroll 4
+  for (int r = r_lo; r < r_hi; ++r) mine += counts(r);
+  Counts upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    Counts x;
+#pragma unroll
+    for (int e = 0; e < 5; ++e) x.v[e] = __shfl_up_sync(0xffffffffu, upto.v[e], o);
+    if (lane >= o) upto += x;
   }
-  const int take_h = (int)carry[1], take_b = (int)carry[2], push_h = (int)(carry[1] >> 32), push_b = (int)(carry[2] >> 32);
-  if (tid == 0) tok0[a.B] = (int)min(carry[0], (long long)0x7fffffff);
-  if (carry[0] > (a.slots != nullptr ? a.max_tokens : 0x7fffffff)) bad |= OSCAR_STATUS_BAD_SEQLEN;
+  if (lane == 31) red[w] = upto;
+  __syncthreads();
+  Counts all = {}, at = {};
+#pragma unroll
+  for (int i = 0; i < kTabThreads / 32; ++i) {
+    if (i == w) at = all;
+    all += red[i];
+  }
+#pragma unroll
+  for (int e = 0; e < 5; ++e) at.v[e] += upto.v[e] - mine.v[e];
+  for (int r = r_lo; r < r_hi; ++r) {              // a request pops or pushes
+    const Counts c = counts(r);
+    tok0[r] = (int)min(at.v[kTokens], (long long)0x7fffffff);
+    pop_h[r] = (int)(c.v[kPushH] ? at.v[kPushH] : at.v[kPopH]);
+    pop_b[r] = (int)(c.v[kPushB] ? at.v[kPushB] : at.v[kPopB]);
+    at += c;
+  }
+  if (tid == 0) tok0[a.B] = (int)min(all.v[kTokens], (long long)0x7fffffff);
+  if (all.v[kTokens] > (a.slots != nullptr ? a.max_tokens : 0x7fffffff)) bad |= OSCAR_STATUS_BAD_SEQLEN;
   for (int e = 0; e < 2; ++e) {
     const int head = s_ring[2 * e], count = s_ring[2 * e + 1], cap = e ? a.cap_bf16 : a.cap_int2;
-    if (head < 0 || count < 0 || count > cap || (cap > 0 && head >= cap) || (e ? push_b : push_h) > cap - count)
+    if (head < 0 || count < 0 || count > cap || (cap > 0 && head >= cap) || all.v[e ? kPushB : kPushH] > cap - count)
       bad |= OSCAR_STATUS_BAD_PAGE;
-    else if ((e ? take_b : take_h) > count)
+    else if (all.v[e ? kPopB : kPopH] > count)
       bad |= OSCAR_STATUS_NO_PAGES;
   }
   if (bad) atomicOr(&s_bad, bad);
@@ -130,7 +133,10 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
   const int total = tok0[a.B];
 
   if (bad == 0) {
-    auto ring = [](int head, int i, int cap) { return (int)(((long long)head + i) % cap); };
+    auto ring = [](int head, int i, int cap) {        // head, i < cap (i: of the entries the call takes or adds)
+      const unsigned x = (unsigned)head + (unsigned)i;
+      return x - (x >= (unsigned)cap ? (unsigned)cap : 0u);
+    };
     // page j of request r, whether it is in the table already or popped by this call
     auto hist_id = [&](int r, int j, int held) {
       return j < held ? a.hist_pt[(size_t)r * a.max_hist_pages + j]
@@ -205,10 +211,10 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
     }
     if (last) {
       const bool ok = bad == 0;
-      a.rings_out[0] = ok && a.cap_int2 > 0 ? (int)(((long long)s_ring[0] + take_h) % a.cap_int2) : s_ring[0];
-      a.rings_out[1] = s_ring[1] + (ok ? push_h - take_h : 0);
-      a.rings_out[2] = ok && a.cap_bf16 > 0 ? (int)(((long long)s_ring[2] + take_b) % a.cap_bf16) : s_ring[2];
-      a.rings_out[3] = s_ring[3] + (ok ? push_b - take_b : 0);
+      a.rings_out[0] = ok && a.cap_int2 > 0 ? (int)((s_ring[0] + all.v[kPopH]) % a.cap_int2) : s_ring[0];
+      a.rings_out[1] = s_ring[1] + (ok ? (int)(all.v[kPushH] - all.v[kPopH]) : 0);
+      a.rings_out[2] = ok && a.cap_bf16 > 0 ? (int)((s_ring[2] + all.v[kPopB]) % a.cap_bf16) : s_ring[2];
+      a.rings_out[3] = s_ring[3] + (ok ? (int)(all.v[kPushB] - all.v[kPopB]) : 0);
     }
   }
 }
@@ -283,9 +289,9 @@ int launch_build_tables(const oscar_layout& lay, int B, const int* old_lens, con
   a.max_tokens = max_tokens;
   a.status = status;
   a.ticket = ticket;
-  // a CTA per 1,024 tokens there may be (or per 8 requests), at most one per SM: each scans all lengths
-  const int want = std::max(slots != nullptr ? (max_tokens + 1023) / 1024 : 1, (B + 7) / 8);
-  const int grid = std::max(1, std::min(sms, want));
+  // a CTA per 512 tokens there may be (or per 8 requests), at most eight per SM: each scans all lengths
+  const int want = std::max(slots != nullptr ? max_tokens / 512 + 1 : 1, (B + 7) / 8);
+  const int grid = std::max(1, std::min(8 * sms, want));
   k_build_tables<<<grid, kTabThreads, 3 * (B + 1) * sizeof(int), st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
