@@ -31,6 +31,9 @@ struct TreeArgs {
 inline int tree_tiles(int T, int gq) { return (T * gq + kTreeRows - 1) / kTreeRows; }
 inline int tree_tile_rows(int T, int gq) { return T * gq >= kTreeRows ? kTreeRows : (T * gq + 7) / 8 * 8; }
 
+// More than one tile: a CTA takes two, so that a page is unpacked once for 256 rows.
+inline bool tree_wide(int T, int gq) { return T * gq > kTreeRows; }
+
 // nodes of request b that take part
 __device__ __forceinline__ int live_nodes(const TreeArgs& a, int b) {
   return a.n_draft != nullptr ? min(max(a.n_draft[b], 0), a.T) : a.T;

@@ -45,7 +45,7 @@ constexpr int kTreeThreads = 28 * 32;
 // what the CTA was launched with
 constexpr int kRegsLaunch = 72, kRegsRows = 96, kRegsUnpack = 64, kRegsCtl = 56;
 static_assert(2 * kRegsRows + 4 * kRegsUnpack + kRegsCtl <= 7 * kRegsLaunch, "register shares");
-constexpr int kRows = kTreeRows;                   // query rows of a CTA
+constexpr int kRows = kTreeRows;                   // query rows of a tile
 constexpr int kStages = 8;                         // ring stages of one page block
 constexpr int kBufs = 4;                           // unpacked pages: keys, and values
 constexpr int kSboK = (kD / 8) * 128;              // keys: rows = tokens, 128 channels: 2,048 B between 8-row blocks
@@ -65,8 +65,8 @@ static_assert(kMaxTreeBf16Pages + kMaxDraft / kP <= kPoisonTiles, "a set for eve
 constexpr int kMetaStage = 2 * 2 * 32 * 4;
 constexpr int kOffMeta = kOffPid + kPids * 4;
 constexpr int kOffJoin = kOffMeta + kStages * kMetaStage;   // [2 streams][128 rows] (M, l)
-constexpr int kOffF = kOffJoin + 2 * kRows * 8;    // [128 rows] factor of a row's logits
-constexpr int kOffInfo = kOffF + kRows * 4;        // what the roles read about the slot: kI*
+constexpr int kOffF = kOffJoin + 2 * kRows * 8;    // [256 rows] factor of a row's logits
+constexpr int kOffInfo = kOffF + 2 * kRows * 4;    // what the roles read about the slot: kI*
 constexpr int kIPages = 0, kIRest = 4, kIFirst = 8, kILen = 12, kINodes = 16, kILive = 20;
 constexpr int kOffBar = kOffInfo + 32;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages, kBKFull = kBMeta + kStages,
@@ -74,7 +74,9 @@ constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages
               kBSFree = kBSDone + 2, kBPReady = kBSFree + 2, kBODone = kBPReady + 2, kBImg = kBODone + 2, kBQ = kBImg + 1,
               kBFinal = kBQ + 1, kNumBars = kBFinal + 1;
 constexpr int kOffTmem = kOffBar + kNumBars * 8, kOffFailed = kOffTmem + 4;   // TMEM address, failure flag
-constexpr int kTreeSmem = kOffTmem + 16 + 1024;    // + alignment slack
+constexpr int kOffQ = (kOffTmem + 16 + 127) / 128 * 128;   // two tiles: the second one's rows, an A operand
+// with alignment slack
+template <bool WIDE> constexpr int kTreeSmem = (WIDE ? kOffQ + kRows * kD * 2 : kOffTmem + 16) + 1024;
 constexpr uint32_t kColO = 0, kColS = 256, kColP = 384, kColQ = 448, kTmemCols = 512;   // stream e: + 128 e, 64 e, 32 e
 constexpr uint32_t kIdescS = idesc_f16(128, 64), kIdescO = idesc_f16(128, 128);
 constexpr uint32_t kBf16Bits = (1u << 7) | (1u << 10);              // A and B bf16
@@ -215,14 +217,15 @@ __device__ __forceinline__ void weights32(const float (&s)[32], float2 F2, float
     }
 }
 
-// The pages e, e + 2, ... of the slot.
+// The stream's pages: e, e + 2, ... of the slot, or with two tiles all of them.
+template <bool WIDE>
 __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F, float& m, float& lsum) {
   const uint32_t lane0 = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
   const uint32_t to = c.tmem + lane0 + kColO + 128 * e, ts = c.tmem + lane0 + kColS + 64 * e, tp = c.tmem + lane0 + kColP + 32 * e;
   float l = 0.f;
 #pragma unroll 1
-  for (int i = e; i < n; i += 2) {
-    const int ph = i >> 1, live = c.tokens(i);
+  for (int i = WIDE ? 0 : e; i < n; i += WIDE ? 1 : 2) {
+    const int ph = WIDE ? i : i >> 1, live = c.tokens(i);
     if (!c.wait(kBSDone + e, ph)) return false;
     tc_fence_after();
     if (live < kP) {                               // the end of the history: its S columns, whatever they are, become -inf
@@ -237,7 +240,7 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
     }
     uint32_t r0[16], r1[16];
     float sum;
-    bool redone = false, free_o = i < 2;           // O of the stream's last page is complete
+    bool redone = false, free_o = ph == 0;          // O of the stream's last page is complete
 #pragma unroll 1
     for (;;) {
       // the page's weights against the reference m
@@ -293,15 +296,16 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
 }
 
 // ---- row threads, BF16 and draft pages -----------------------------------------------------------------
-// bits(i): the tokens of page i that this row sees. The low parts of the weights go where S was: S(i + 2) waits for O(i).
-template <typename Bits>
+// bits(i): the tokens of page i that this row sees. The low parts of the weights go where S was: the stream's next S waits for
+// this O.
+template <bool WIDE, typename Bits>
 __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bits bits, float& m, float& lsum) {
   const uint32_t lane0 = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
   const uint32_t to = c.tmem + lane0 + kColO + 128 * e, ts = c.tmem + lane0 + kColS + 64 * e, tp = c.tmem + lane0 + kColP + 32 * e;
   float l = 0.f;
 #pragma unroll 1
-  for (int i = e; i < n; i += 2) {
-    const int ph = i >> 1;
+  for (int i = WIDE ? 0 : e; i < n; i += WIDE ? 1 : 2) {
+    const int ph = WIDE ? i : i >> 1;
     const unsigned long long see = bits(i);
     if (!c.wait(kBSDone + e, ph) || !c.wait(kBVFull + i % kBufs, i / kBufs)) return false;
     tc_fence_after();
@@ -322,7 +326,7 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
       al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
       m = mx;
     }
-    if (__any_sync(0xffffffffu, grow) && i >= 2) { // O of the stream's last page is complete: S(i) waited for it
+    if (__any_sync(0xffffffffu, grow) && ph > 0) { // O of the stream's last page is complete: S(i) waited for it
       rescale_o(to, al);
     }
     l *= al;
@@ -574,8 +578,8 @@ __device__ __forceinline__ void issue_page(const Ctx c, const LayerView& lv, int
 }
 
 // The control warps: page stream, scale pairs, MMAs.
-template <int FMT>
-__device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w, int h, bool hist, int n) {
+template <int FMT, bool WIDE>
+__device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w, int h, bool hist, int n, bool second) {
   const int lane = threadIdx.x & 31;
   if (w == kLoadWarp) {
     if (!hist) return true;
@@ -588,43 +592,58 @@ __device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w,
     return true;
   }
   if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, lv, h, n);
-  // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4 and stream i & 1
+  // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4. One tile: page i belongs to stream i & 1.
+  // Two tiles: to both streams, the second one's rows are an operand in shared memory.
   static_assert(kBufs == 4, "two pages of each stream");
   const uint32_t more = hist ? 0u : kBf16Bits;
   if (w == kMmaWarp) {
-    const uint32_t kd = desc_lo(c.base + kOffK, 128);
+    const uint32_t kd = desc_lo(c.base + kOffK, 128), qd = desc_lo(c.base + kOffQ, 128);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int b = i % kBufs, e = i & 1;
+      const int b = i % kBufs;
       if (!c.wait(kBKFull + b, i / kBufs)) return false;
-      // S(i - 2) is out of the way: read, or (BF16 pages, whose weights' low parts follow it there) used by O(i - 2)
-      if (i >= 2 && !c.wait((hist ? kBSFree : kBODone) + e, (i - 2) >> 1)) return false;
-      tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        umma_ta_warp(c.tmem + kColS + 64 * e, c.tmem + kColQ + 8 * kk, kd + b * (kKBytes >> 4) + 16 * kk, desc_hi(kSboK),
-                     kIdescS | more, kk > 0);
-      umma_commit_warp(c.bar(kBSDone + e));
+      for (int k = 0; k < (WIDE ? 2 : 1); ++k) {
+        if (k == 1 && !second) break;
+        const int e = WIDE ? k : i & 1, ph = WIDE ? i : i >> 1;
+        // the stream's last S is out of the way: read, or (BF16 pages, whose weights' low parts follow it there) used by O
+        if (ph > 0 && !c.wait((hist ? kBSFree : kBODone) + e, ph - 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t keys = kd + b * (kKBytes >> 4) + 16 * kk;
+          if (k == 1)
+            umma_warp(c.tmem + kColS + 64, qd + 16 * kk, desc_hi(kSboK), keys, desc_hi(kSboK), kIdescS | more, kk > 0);
+          else
+            umma_ta_warp(c.tmem + kColS + 64 * e, c.tmem + kColQ + 8 * kk, keys, desc_hi(kSboK), kIdescS | more, kk > 0);
+        }
+        umma_commit_warp(c.bar(kBSDone + e));
+      }
       umma_commit_warp(c.bar(kBKFree + b));
     }
   } else {
     const uint32_t vd = desc_lo(c.base + kOffV, 128), vh = hist ? desc_hi(kSboV) : desc_hi(kSboVNear);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int b = i % kBufs, e = i & 1;
-      if (!c.wait(kBVFull + b, i / kBufs) || !c.wait(kBPReady + e, i >> 1)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColP + 32 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
-                     kIdescO | more, i > 1 || kk > 0);
-      if (!hist) {                               // the weights' low parts
+      const int b = i % kBufs;
+      if (!c.wait(kBVFull + b, i / kBufs)) return false;
+#pragma unroll 1
+      for (int k = 0; k < (WIDE && second ? 2 : 1); ++k) {
+        const int e = WIDE ? k : i & 1, ph = WIDE ? i : i >> 1;
+        if (!c.wait(kBPReady + e, ph)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColS + 64 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
-                       kIdescO | more, true);
+          umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColP + 32 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                       kIdescO | more, ph > 0 || kk > 0);
+        if (!hist) {                               // the weights' low parts
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ta_warp(c.tmem + kColO + 128 * e, c.tmem + kColS + 64 * e + 8 * kk, vd + b * (kVBytes >> 4) + 16 * kk, vh,
+                         kIdescO | more, true);
+        }
+        umma_commit_warp(c.bar(kBODone + e));
       }
-      umma_commit_warp(c.bar(kBODone + e));
       umma_commit_warp(c.bar(kBVFree + b));
     }
   }
@@ -661,31 +680,41 @@ struct NearPages {
   }
 };
 
-// Partials of a slot, thread = row, a warpgroup per half of the channels: the streams' O joined. Both streams' row warps
-// meet first (each has waited for its stream's last product); a CTA that failed writes empty ones.
-__device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv, const TreeArgs& a, int h, int qt, int n, int live) {
+// Partials of a slot, thread = row. One tile: the streams' O joined, a warpgroup per half of the channels; both streams'
+// row warps meet first (each has waited for its stream's last product). Two tiles: a warpgroup each. A CTA that failed
+// writes empty ones. ref, l: the row's reference and sum of its stream.
+template <bool WIDE>
+__device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv, const TreeArgs& a, int h, int qt, int n, int live,
+                                               float ref, float l) {
   const int tid = threadIdx.x, w = tid >> 5, row = tid & (kRows - 1), half = (tid >> 7) & 1;
-  tc_fence_before();
-  asm volatile("bar.sync 1, %0;" ::"r"(64 * ((live + 31) / 32)) : "memory");
-  tc_fence_after();
-  const bool good = __all_sync(0xffffffffu, !c.failed() && n > 0);
-  const uint2 u0 = lds64(c.base + kOffJoin + 8 * row), u1 = lds64(c.base + kOffJoin + 8 * (kRows + row));
-  const float m0 = __uint_as_float(u0.x), m1 = n > 1 ? __uint_as_float(u1.x) : -INFINITY;
-  const float M = fmaxf(m0, m1);
-  const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-  float* part = tree_part(lv, a, blockIdx.z, qt, h, blockIdx.x);
-  const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO;
-  if (row < live && half == 0) {
-    const float l = w0 * __uint_as_float(u0.y) + (n > 1 ? w1 * __uint_as_float(u1.y) : 0.f);
-    *reinterpret_cast<float2*>(part + a.rows * kD + 2 * row) = good ? make_float2(M, l) : make_float2(-INFINITY, 0.f);
+  float M = ref, w0 = 1.f, w1 = 0.f;
+  if (!WIDE) {
+    sts32(c.base + kOffJoin + 8 * (half * kRows + row), __float_as_uint(ref));
+    sts32(c.base + kOffJoin + 8 * (half * kRows + row) + 4, __float_as_uint(l));
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"r"(64 * ((live + 31) / 32)) : "memory");
+    tc_fence_after();
+    const uint2 u0 = lds64(c.base + kOffJoin + 8 * row), u1 = lds64(c.base + kOffJoin + 8 * (kRows + row));
+    const float m0 = __uint_as_float(u0.x), m1 = n > 1 ? __uint_as_float(u1.x) : -INFINITY;
+    M = fmaxf(m0, m1);
+    w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M);
+    w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+    l = w0 * __uint_as_float(u0.y) + (n > 1 ? w1 * __uint_as_float(u1.y) : 0.f);
+  } else if (M == -INFINITY) {
+    w0 = 0.f;
   }
+  const bool good = __all_sync(0xffffffffu, !c.failed() && n > 0);
+  float* part = tree_part(lv, a, blockIdx.z, qt, h, blockIdx.x);
+  const uint32_t to = c.tmem + ((uint32_t)(32 * (w & 3)) << 16) + kColO + (WIDE ? 128 * half : 0);
+  if (row < live && (WIDE || half == 0))
+    *reinterpret_cast<float2*>(part + a.rows * kD + 2 * row) = good ? make_float2(M, l) : make_float2(-INFINITY, 0.f);
 #pragma unroll 1
-  for (int k = 2 * half; k < 2 * half + 2; ++k) {
+  for (int k = WIDE ? 0 : 2 * half; k < (WIDE ? 4 : 2 * half + 2); ++k) {
     float x[32], y[32];
     if (!good) {
 #pragma unroll
       for (int t = 0; t < 32; ++t) x[t] = 0.f;
-    } else if (n > 1) {
+    } else if (!WIDE && n > 1) {
       tmem_ld32x2(to + 32 * k, to + 128 + 32 * k, x, y);
 #pragma unroll
       for (int t = 0; t < 32; ++t) x[t] = w0 * x[t] + w1 * y[t];
@@ -702,27 +731,28 @@ __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv,
   }
 }
 
-template <int FMT>
+template <int FMT, bool WIDE>
 __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Ctx c;
   c.base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t info = c.base + kOffInfo;
   const int w = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int h = blockIdx.y % lv.hkv, qt = blockIdx.y / lv.hkv, e = (w >> 2) & 1;   // e: the warpgroup's stream
+  const int h = blockIdx.y % lv.hkv, e = (w >> 2) & 1;   // e: the warpgroup's stream
+  const int qt = WIDE ? 2 * (blockIdx.y / lv.hkv) + e : blockIdx.y / lv.hkv;
   const bool hist = (int)blockIdx.x < a.nsplit;
-  const int n = (int)lds32(info + kIPages);
+  const int n = (int)lds32(info + kIPages), all = (int)lds32(info + kILive);
   c.rest = (int)lds32(info + kIRest);
   const NearPages near = {lv, a, (int)blockIdx.z, h, (int)lds32(info + kIFirst), (int)lds32(info + kILen), (int)lds32(info + kINodes)};
   bool ok = !c.failed();
   if (w < kRowWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-    const int live = (int)lds32(info + kILive), row = threadIdx.x & (kRows - 1);
+    const int live = WIDE ? min(kRows, all - e * kRows) : all, row = threadIdx.x & (kRows - 1);
     if (32 * (w & 3) < live) {
-      const float F = __uint_as_float(lds32(c.base + kOffF + 4 * row));
+      const float F = __uint_as_float(lds32(c.base + kOffF + 4 * (WIDE ? e * kRows + row : row)));
       float m = -INFINITY, lsum = 0.f;
       if (ok && hist) {
-        ok = rows_history(c, e, n, F, m, lsum);
+        ok = rows_history<WIDE>(c, e, n, F, m, lsum);
       } else if (ok) {
         const int node = (qt * kRows + row) / (lv.hq / lv.hkv), nbf = (lv.sink + lv.recent) / kP;
         auto bits = [&](int i) -> unsigned long long {
@@ -731,16 +761,17 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
           if (p.draft) see &= row < live ? a.mask[((size_t)blockIdx.z * a.T + node) * a.W + (near.p0 + i - nbf)] : 0ull;
           return see;
         };
-        ok = rows_bf16(c, e, n, F, bits, m, lsum);
+        ok = rows_bf16<WIDE>(c, e, n, F, bits, m, lsum);
       }
-      const int last = n - 1 - ((n - 1 - e) & 1);            // the stream's last page
-      if (ok && e < n) ok = c.wait(kBODone + e, last >> 1);
+      // the stream's last product
+      if (WIDE) {
+        if (ok && n > 0) ok = c.wait(kBODone + e, n - 1);
+      } else {
+        if (ok && e < n) ok = c.wait(kBODone + e, (n - 1 - e) >> 1);
+      }
       if (!ok) c.fail();
-      // the sums of both streams, for the join
       const float ref = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
-      sts32(c.base + kOffJoin + 8 * (e * kRows + row), __float_as_uint(ref));
-      sts32(c.base + kOffJoin + 8 * (e * kRows + row) + 4, __float_as_uint(lsum));
-      write_partials(c, lv, a, h, qt, n, live);
+      write_partials<WIDE>(c, lv, a, h, qt, n, live, ref, lsum);
     }
   } else if (w < kVWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
@@ -750,7 +781,7 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
     if (ok) ok = hist ? values_history<FMT>(c, lv, h, e, n) : values_bf16(c, lv.status, e, n, near);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-    if (ok) ok = control<FMT>(c, lv, w, h, hist, n);
+    if (ok) ok = control<FMT, WIDE>(c, lv, w, h, hist, n, all > kRows);
   }
   if (!ok) {
     if (lane == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
@@ -769,26 +800,49 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
   }
 }
 
-template <int FMT>
+template <int FMT, bool WIDE>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv, TreeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  const int slot = blockIdx.x, h = blockIdx.y % lv.hkv, qt = blockIdx.y / lv.hkv, b = blockIdx.z;
+  constexpr int kCtaRows = WIDE ? 2 * kRows : kRows;
+  const int slot = blockIdx.x, h = blockIdx.y % lv.hkv, Q0 = (blockIdx.y / lv.hkv) * kCtaRows, b = blockIdx.z;
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int gq = lv.hq / lv.hkv;
   const bool hist = slot < a.nsplit;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int nodes = live_nodes(a, b);
-  if (a.n_draft != nullptr && a.n_draft[b] != nodes && tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_TREE);
-  const int live = min(kRows, nodes * gq - qt * kRows);   // this tile's query rows
-  if (live <= 0) return;
-
   Ctx c;
   c.base = smem_addr(smem);
+  c.rest = 0;
+  // the barriers but those whose count depends on the request, before the kernel before this one is waited for
+  if (w == kLoadWarp) {
+    for (int k = lane; k < kNumBars; k += 32) {
+      if (k >= kBSFree && k < kBODone) continue;
+      // kBEmpty: a key and a value warpgroup, warp 26; unpacked pages: a warpgroup; kBFinal: both issuing warps
+      mbar_init_n(c.bar(k), k >= kBEmpty && k < kBMeta ? 9 : k >= kBKFull && k < kBKFree ? 4 : k == kBFinal ? 2 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the rows' q: a warp takes 8 rows (lane & 7), loaded before anything is known about the request -------------
+  constexpr int kStagers = kMmaWarp;               // warps
+  auto load_q = [&](int blk, uint4 (&x)[4]) {
+    const int Q = Q0 + 8 * blk + (lane & 7), node = Q / gq, hq = h * gq + Q - node * gq;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + node) * lv.hq + hq) * kD);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = node < a.T ? src[(lane >> 3) + 4 * j] : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 x[4];
+  if (w < kStagers && w < kCtaRows / 8) load_q(w, x);
+  const int asked = a.n_draft != nullptr ? a.n_draft[b] : a.T;
+  int L = a.seq_lens[b];
+  const int nodes = min(max(asked, 0), a.T);
+  if (asked != nodes && tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_TREE);
+  const int live = min(kCtaRows, nodes * gq - Q0);  // this CTA's query rows
+  if (live <= 0) return;
 
   // ---- the slot's tokens -----------------------------------------------------------------------------------
-  int L = a.seq_lens[b];
   if (L < 0) {
     if (tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
     L = 0;
@@ -810,43 +864,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     p0 = (slot - a.nsplit) * near_pages / a.nb;
     n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
   }
-  c.rest = 0;
 
-  const int active = (live + 31) / 32;             // row warps with rows
   if (w == kLoadWarp) {
-    if (lane == 0) {
-      mbar_init_n(c.bar(kBImg), 1);
-      for (int s = 0; s < kStages; ++s) {
-        mbar_init_n(c.bar(kBFull + s), 1);
-        mbar_init_n(c.bar(kBEmpty + s), 4 + 4 + 1);  // a key and a value warpgroup, warp 26
-        mbar_init_n(c.bar(kBMeta + s), 1);
-      }
+    if (lane == 0 && hist && n > 0) {              // the rotation
+      const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
+      mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
+      for (int p = 0; p < 2; ++p)                  // R = b1 + b2 to about 17 bits
+        bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
+    }
+    if (lane < 2) {                                // row warps that have rows, of a stream
+      const int active = ((WIDE ? min(kRows, live - lane * kRows) : live) + 31) / 32;
+      mbar_init_n(c.bar(kBSFree + lane), max(active, 1));
+      mbar_init_n(c.bar(kBPReady + lane), max(active, 1));
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      if (hist && n > 0) {                         // the rotation, requested before anything else is known
-        const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
-        mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
-        for (int p = 0; p < 2; ++p)                // R = b1 + b2 to about 17 bits
-          bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
-      }
     }
     __syncwarp();
   } else if (w == kMmaWarp) {
+    // only now: the kernel before this one may still have been about to allocate its own
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.base + kOffTmem),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (w == kMetaWarp) {
     if (lane == 0) {
-      for (int j = 0; j < kBufs; ++j) {
-        mbar_init_n(c.bar(kBKFull + j), 4);
-        mbar_init_n(c.bar(kBVFull + j), 4);
-        mbar_init_n(c.bar(kBKFree + j), 1);
-        mbar_init_n(c.bar(kBVFree + j), 1);
-      }
-      for (int j = 0; j < 2; ++j) {
-        mbar_init_n(c.bar(kBSDone + j), 1);
-        mbar_init_n(c.bar(kBSFree + j), active);
-        mbar_init_n(c.bar(kBPReady + j), active);
-        mbar_init_n(c.bar(kBODone + j), 1);
-      }
-      mbar_init_n(c.bar(kBQ), 1);
-      mbar_init_n(c.bar(kBFinal), 2);                // both issuing warps
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       sts32(c.base + kOffFailed, 0u);
       const uint32_t info = c.base + kOffInfo;
       sts32(info + kIPages, (uint32_t)n);
@@ -857,10 +897,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       sts32(info + kILive, (uint32_t)live);
     }
     __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.base + kOffTmem),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (w >= kKWarp0 && w < kMmaWarp) {
     const int at = tid - 32 * kKWarp0, step = 32 * (kMmaWarp - kKWarp0);
     if (hist) {                                    // page ids, those out of range as -1
@@ -877,20 +913,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       for (int k = at; k < 2 * n; k += step) sts32(c.base + kOffPid + 4 * k, 0u);
     }
   }
-  // ---- the rows' q, staged where the values go: the rotation's A operand ----------------------------------
-  // thread = row; the odd pages' warpgroup takes the upper half of the channels
-  const int row = tid & (kRows - 1), half = (tid >> 7) & 1, Q = qt * kRows + row, node = Q / gq, hq = h * gq + Q % gq;
-  const uint32_t qs = c.base + kOffV + (row >> 3) * kSboK + (row & 7) * 16;
-  if (w < kRowWarps && n > 0) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + node) * lv.hq + hq) * kD);
-    uint32_t bad = 0u;
+  // q staged where the values go, the rotation's A operand (BF16 pages: the second tile where it is used); each row's
+  // largest magnitude, as bf16 bits, where the join will be
+  if (w < kStagers && n > 0) {
+#pragma unroll 1
+    for (int blk = w; blk < kCtaRows / 8; blk += kStagers) {
+      if (blk >= kStagers) load_q(blk, x);
+      const int r = 8 * blk + (lane & 7), rr = r & (kRows - 1);
+      const uint32_t dst = c.base + (!WIDE || r < kRows ? kOffV : hist ? kOffV + kRows * kD * 2 : kOffQ) +
+                           (rr >> 3) * kSboK + (rr & 7) * 16 + (lane >> 3) * 128;
+      uint32_t mx = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 x = row < live ? src[8 * half + j] : make_uint4(0u, 0u, 0u, 0u);
-      bad |= nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w);
-      sts128(qs + (8 * half + j) * 128, x);
+      for (int j = 0; j < 4; ++j) {
+        if (r >= live) x[j] = make_uint4(0u, 0u, 0u, 0u);
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                                   __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+        sts128(dst + 4 * j * 128, x[j]);
+      }
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      mx = max(mx & 0xffffu, mx >> 16);
+      if (lane < 8) {
+        sts32(c.base + kOffJoin + 4 * r, mx);
+        if (mx >= 0x7F80u) flag(lv.status, OSCAR_STATUS_NONFINITE);
+      }
     }
-    if (bad != 0u) flag(lv.status, OSCAR_STATUS_NONFINITE);
     fence_async();
   }
   tc_fence_before();
@@ -898,7 +945,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   tc_fence_after();
   bool ok = lds32(c.base + kOffTmem) == c.tmem;
 
-  // ---- the rows' A operand in TMEM -------------------------------------------------------------------------
+  // ---- the rows' A operand in TMEM (a second tile's in shared memory) -----------------------------------------
+  // thread = row; one tile: the second warpgroup takes the upper half of the channels
+  const int row = tid & (kRows - 1), half = (tid >> 7) & 1;
   float F = a.scale_log2;
   if (ok && n > 0 && hist) {
     if (w == kLoadWarp) {
@@ -910,70 +959,74 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       if (ok) {
         tc_fence_after();
         const uint32_t a0 = c.base + kOffV, b0 = c.base + kOffK;
+#pragma unroll 1
+        for (int t = 0; t < (WIDE && live > kRows ? 2 : 1); ++t)
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_warp(c.tmem + kColO, desc_lo(a0, 128) + 16 * kk, desc_hi(kSboK),
-                      desc_lo(b0, 16) + (p * kImgBytes + (kk >> 2) * (kImgBytes / 2) + (kk & 3) * 32) / 16, desc_hi(1024, true),
-                      kIdescO | kBf16Bits, (p | kk) != 0);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_warp(c.tmem + kColO + 128 * t, desc_lo(a0, 128) + t * (kRows * kD * 2 / 16) + 16 * kk, desc_hi(kSboK),
+                        desc_lo(b0, 16) + (p * kImgBytes + (kk >> 2) * (kImgBytes / 2) + (kk & 3) * 32) / 16,
+                        desc_hi(1024, true), kIdescO | kBf16Bits, (p | kk) != 0);
         umma_commit_warp(c.bar(kBQ));
       }
     } else if (w < kRowWarps) {
+      // q R_K has no channel above sqrt(128) max |q|, and one above max |q| / sqrt(128): 2^sigma brings that range to
+      // 2^7.5 .. 2^14.5, away from both ends of fp16
+      const int ex = (int)(lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >> 7), sigma = min(max(137 - ex, -120), 60);
+      const float sc = exp2f((float)sigma);
+      F *= exp2f((float)-sigma);
       ok = c.wait(kBQ, 0);
       if (ok) {
         tc_fence_after();
-        const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16);
-        float y[32], mx = 0.f;
+        const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16), from = trow + kColO + (WIDE ? 128 * half : 0);
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          tmem_ld32(trow + kColO + 32 * k, y);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(y[e]));
-        }
-        int e2 = 0;                                // 2^sigma brings the largest channel near 2^10
-        if (mx > 0.f && mx < INFINITY) frexpf(mx, &e2);
-        const int sigma = min(max(10 - e2, -60), 60);
-        const float sc = exp2f((float)sigma);
-        F *= exp2f((float)-sigma);
-#pragma unroll 1
-        for (int k = 2 * half; k < 2 * half + 2; ++k) {
-          tmem_ld32(trow + kColO + 32 * k, y);
+        for (int k = WIDE ? 0 : 2 * half; k < (WIDE ? 4 : 2 * half + 2); ++k) {
+          float y[32];
+          tmem_ld32(from + 32 * k, y);
           uint32_t r[16];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[8 * u + j] = pack_f16x2(y[16 * u + j] * sc, y[16 * u + 8 + j] * sc);
-          tmem_st16(trow + kColQ + 16 * k, r);
+          if (WIDE && half == 1) {
+            const uint32_t dst = c.base + kOffQ + (row >> 3) * kSboK + (row & 7) * 16 + 4 * k * 128;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sts128(dst + j * 128, make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]));
+          } else {
+            tmem_st16(trow + kColQ + 16 * k, r);
+          }
         }
         tmem_wait_st();
+        if (WIDE) fence_async();
       }
     }
-  } else if (ok && n > 0 && w < kRowWarps) {
+  } else if (ok && n > 0 && w < (WIDE ? kRowWarps / 2 : kRowWarps)) {
     const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16);
+    const uint32_t qs = c.base + kOffV + (row >> 3) * kSboK + (row & 7) * 16;
 #pragma unroll 1
-    for (int k = 2 * half; k < 2 * half + 2; ++k) {
+    for (int k = WIDE ? 0 : 2 * half; k < (WIDE ? 4 : 2 * half + 2); ++k) {
       uint32_t r[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 x = lds128(qs + (4 * k + j) * 128);
-        r[4 * j] = x.x;
-        r[4 * j + 1] = x.y;
-        r[4 * j + 2] = x.z;
-        r[4 * j + 3] = x.w;
+        const uint4 y = lds128(qs + (4 * k + j) * 128);
+        r[4 * j] = y.x;
+        r[4 * j + 1] = y.y;
+        r[4 * j + 2] = y.z;
+        r[4 * j + 3] = y.w;
       }
       tmem_st16(trow + kColQ + 16 * k, r);
     }
     tmem_wait_st();
   }
-  if (w < kRowWarps && half == 0) sts32(c.base + kOffF + 4 * row, __float_as_uint(F));
+  if (w < kRowWarps && (WIDE || half == 0)) sts32(c.base + kOffF + 4 * (WIDE ? tid : row), __float_as_uint(F));
   if (!ok) c.fail();
   tc_fence_before();
   __syncthreads();                                 // Q is in; the rotation's operands may be overwritten
   tc_fence_after();
 
   // ---- the roles. What they need is read back from shared memory: nothing of the start is kept in registers ----
-  run_roles<FMT>(lv, a);
+  run_roles<FMT, WIDE>(lv, a);
   tc_fence_before();
   __syncthreads();
   if (w == kMmaWarp) {
@@ -983,23 +1036,39 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   }
 }
 
+template <int FMT, bool WIDE>
+int launch_as(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const int tiles = tree_tiles(a.T, lv.hq / lv.hkv);
+  cfg.gridDim = dim3(a.nsplit + a.nb, lv.hkv * (WIDE ? (tiles + 1) / 2 : tiles), B);
+  cfg.blockDim = dim3(kTreeThreads);
+  cfg.dynamicSmemBytes = kTreeSmem<WIDE>;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_tree_attention<FMT, WIDE>, lv, a) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
 template <int FMT>
 int launch_fmt(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.nsplit + a.nb, lv.hkv * tree_tiles(a.T, lv.hq / lv.hkv), B);
-  cfg.blockDim = dim3(kTreeThreads);
-  cfg.dynamicSmemBytes = kTreeSmem;
-  cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, k_tree_attention<FMT>, lv, a) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+  return tree_wide(a.T, lv.hq / lv.hkv) ? launch_as<FMT, true>(lv, a, B, st) : launch_as<FMT, false>(lv, a, B, st);
 }
 
+template <int FMT, bool WIDE>
+int configure_as() {
+  cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
+  if (cudaFuncGetAttributes(&at, k_tree_attention<FMT, WIDE>) != cudaSuccess || at.numRegs < kRegsLaunch) return OSCAR_ERR_CUDA;
+  if (cudaFuncSetAttribute(k_tree_attention<FMT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem<WIDE>) !=
+      cudaSuccess)
+    return OSCAR_ERR_CUDA;
+  return set_max_shared_carveout(reinterpret_cast<const void*>(k_tree_attention<FMT, WIDE>));
+}
 template <int FMT>
 int configure_fmt() {
-  cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
-  if (cudaFuncGetAttributes(&at, k_tree_attention<FMT>) != cudaSuccess || at.numRegs < kRegsLaunch) return OSCAR_ERR_CUDA;
-  if (cudaFuncSetAttribute(k_tree_attention<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem) != cudaSuccess)
-    return OSCAR_ERR_CUDA;
-  return set_max_shared_carveout(reinterpret_cast<const void*>(k_tree_attention<FMT>));
+  const int rc = configure_as<FMT, false>();
+  return rc == OSCAR_OK ? configure_as<FMT, true>() : rc;
 }
 
 }  // namespace
@@ -1012,7 +1081,8 @@ int configure_fmt() {
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
                  int* nb, int* pps) {
   constexpr double kFixed = 20.0, kNear = 5.0;
-  const long units = (long)B * hkv * ((T * gq + kRows - 1) / kRows);
+  const int tiles = tree_tiles(T, gq);
+  const long units = (long)B * hkv * (tree_wide(T, gq) ? (tiles + 1) / 2 : tiles);
   const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
   double best = 0.0;
   *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
