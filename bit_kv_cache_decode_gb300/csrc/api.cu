@@ -792,6 +792,8 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   a.bf16_pt = bf16_pt;
   a.T = T;
   a.W = (T + 63) / 64;
+  a.gq_log2 = 0;
+  while (c->lay.num_kv_heads << a.gq_log2 < c->lay.num_q_heads) ++a.gq_log2;
   tree_splits(B, T, hkv, hq / hkv, (c->lay.sink + c->lay.recent) / kP, max_hist_pages, c->sms,
               (int)std::min(slots, (size_t)1 << 20), &a.nsplit, &a.nb, &a.pps);
   a.rows = tree_tile_rows(T, hq / hkv);

@@ -17,6 +17,7 @@ struct TreeArgs {
   int max_hist_pages;
   const int* bf16_pt;
   int T, W;
+  int gq_log2;                            // query heads of a kv head: 1, 2, 4 or 8
   int nsplit, pps;                        // history slots at most, pages a slot takes at most
   int nb;                                 // slots of BF16 and draft pages, after the nsplit history slots
   int rows;                               // rows of a tile that have partials: min(128, T gq rounded up to 8)
@@ -46,7 +47,7 @@ __device__ __forceinline__ int tree_hist_slots(const TreeArgs& a, int pages) { r
 // Partials of slot `slot` of tile qt: acc as [32 channel quads][rows] float4, then (m, l) as [rows] float2, so that
 // the threads of a warp, one row each, write whole lines.
 __device__ __forceinline__ float* tree_part(const LayerView& lv, const TreeArgs& a, int b, int qt, int h, int slot) {
-  const int tiles = (a.T * (lv.hq / lv.hkv) + kTreeRows - 1) / kTreeRows;
+  const int tiles = ((a.T << a.gq_log2) + kTreeRows - 1) / kTreeRows;
   return a.partials + ((((size_t)b * tiles + qt) * lv.hkv + h) * (a.nsplit + a.nb) + slot) * a.rows * kPartFloats;
 }
 

@@ -43,7 +43,7 @@ constexpr int kRowWarps = 8, kKWarp0 = 8, kVWarp0 = 16, kMmaWarp = 24, kLoadWarp
 constexpr int kTreeThreads = 28 * 32;
 // registers per thread: at launch, then of the rows, the unpacking and the control warpgroups; the shares stay within
 // what the CTA was launched with
-constexpr int kRegsLaunch = 72, kRegsRows = 96, kRegsUnpack = 64, kRegsCtl = 56;
+constexpr int kRegsLaunch = 72, kRegsRows = 112, kRegsUnpack = 56, kRegsCtl = 56;
 static_assert(2 * kRegsRows + 4 * kRegsUnpack + kRegsCtl <= 7 * kRegsLaunch, "register shares");
 constexpr int kRows = kTreeRows;                   // query rows of a tile
 constexpr int kStages = 8;                         // ring stages of one page block
@@ -228,43 +228,35 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
     const int ph = WIDE ? i : i >> 1, live = c.tokens(i);
     if (!c.wait(kBSDone + e, ph)) return false;
     tc_fence_after();
-    if (live < kP) {                               // the end of the history: its S columns, whatever they are, become -inf
-#pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        float s[32];
-        tmem_ld32(ts + 32 * q, s);
+    float s0[32], s1[32];                          // kept until the weights stand: S itself is free for the next page
+    tmem_ld32x2(ts, ts + 32, s0, s1);
+    tc_fence_before();
+    c.arrive(kBSFree + e);
+    if (live < kP) {                               // the end of the history
 #pragma unroll
-        for (int x = 0; x < 32; ++x) s[x] = 32 * q + x < live ? s[x] : -INFINITY;
-        tmem_st32(ts + 32 * q, s);
+      for (int x = 0; x < 32; ++x) {
+        s0[x] = x < live ? s0[x] : -INFINITY;
+        s1[x] = 32 + x < live ? s1[x] : -INFINITY;
       }
     }
     uint32_t r0[16], r1[16];
     float sum;
-    bool redone = false, free_o = ph == 0;          // O of the stream's last page is complete
+    bool redone = false, free_o = ph == 0;         // O of the stream's last page is complete
 #pragma unroll 1
     for (;;) {
       // the page's weights against the reference m
       const float mF = m == -INFINITY ? 0.f : fmaf(m, F, -kBias);
       const float2 F2 = make_float2(F, F), nm2 = make_float2(-mF, -mF);
       float2 t2 = make_float2(0.f, 0.f);
-      {
-        float s0[32], s1[32];
-        tmem_ld32x2(ts, ts + 32, s0, s1);
-        weights32(s0, F2, nm2, r0, t2);
-        weights32(s1, F2, nm2, r1, t2);
-      }
+      weights32(s0, F2, nm2, r0, t2);
+      weights32(s1, F2, nm2, r1, t2);
       sum = t2.x + t2.y;
       const bool over = !redone && (sum > kMostSum || m == -INFINITY);
       if (!__any_sync(0xffffffffu, over)) break;
       redone = true;                               // against the rows' maxima, once
       float mx = -INFINITY;
-#pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        float s[32];
-        tmem_ld32(ts + 32 * q, s);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) mx = fmaxf(mx, s[x]);
-      }
+      for (int x = 0; x < 32; ++x) mx = fmaxf(mx, fmaxf(s0[x], s1[x]));
       float al = 1.f;
       if (over && mx > m) {
         al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
@@ -278,8 +270,6 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
         free_o = true;
       }
     }
-    tc_fence_before();
-    c.arrive(kBSFree + e);
     l += sum;
     if (!free_o) {                                 // the stream's last O has read the weights before these
       if (!c.wait(kBODone + e, ph - 1)) return false;
@@ -754,7 +744,7 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
       if (ok && hist) {
         ok = rows_history<WIDE>(c, e, n, F, m, lsum);
       } else if (ok) {
-        const int node = (qt * kRows + row) / (lv.hq / lv.hkv), nbf = (lv.sink + lv.recent) / kP;
+        const int node = (qt * kRows + row) >> a.gq_log2, nbf = (lv.sink + lv.recent) / kP;
         auto bits = [&](int i) -> unsigned long long {
           const Near p = near(i);
           unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
@@ -807,7 +797,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   constexpr int kCtaRows = WIDE ? 2 * kRows : kRows;
   const int slot = blockIdx.x, h = blockIdx.y % lv.hkv, Q0 = (blockIdx.y / lv.hkv) * kCtaRows, b = blockIdx.z;
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int gq = lv.hq / lv.hkv;
+  const int gq_log2 = a.gq_log2, gq = 1 << gq_log2;
   const bool hist = slot < a.nsplit;
   Ctx c;
   c.base = smem_addr(smem);
@@ -828,7 +818,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   // ---- the rows' q: a warp takes 8 rows (lane & 7), loaded before anything is known about the request -------------
   constexpr int kStagers = kMmaWarp;               // warps
   auto load_q = [&](int blk, uint4 (&x)[4]) {
-    const int Q = Q0 + 8 * blk + (lane & 7), node = Q / gq, hq = h * gq + Q - node * gq;
+    const int Q = Q0 + 8 * blk + (lane & 7), node = Q >> gq_log2, hq = (h << gq_log2) + (Q & (gq - 1));
     const uint4* src = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + node) * lv.hq + hq) * kD);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = node < a.T ? src[(lane >> 3) + 4 * j] : make_uint4(0u, 0u, 0u, 0u);
@@ -858,8 +848,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   if (hist) {
     const int slots = tree_hist_slots(a, np);
     if (slot >= slots) return;                     // a shorter request: the merge knows
-    p0 = (int)((long long)slot * np / slots);
-    n = (int)((long long)(slot + 1) * np / slots) - p0;
+    n = np / slots;
+    p0 = slot * n + min(slot, np - slots * n);
+    n += slot < np - slots * n;
   } else {
     p0 = (slot - a.nsplit) * near_pages / a.nb;
     n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;

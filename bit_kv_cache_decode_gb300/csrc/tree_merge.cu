@@ -21,7 +21,7 @@ constexpr int kTmSmem = kD * kD * 4 + 16;          // explicit-V mode: U_V^T, a 
 __global__ void __launch_bounds__(kTmThreads) k_tree_merge(LayerView lv, TreeArgs a) {
   __shared__ __align__(16) float zs[kTmRows][kD + 4];
   const int r = threadIdx.x & (kTmRows - 1), quad = threadIdx.x / kTmRows, h = blockIdx.y, b = blockIdx.z;
-  const int gq = lv.hq / lv.hkv, Q = blockIdx.x * kTmRows + r, node = Q / gq, hq = h * gq + Q % gq;
+  const int gq = 1 << a.gq_log2, Q = blockIdx.x * kTmRows + r, node = Q >> a.gq_log2, hq = h * gq + (Q & (gq - 1));
   extern __shared__ __align__(128) float uvt[];
   const uint32_t bar = smem_addr(uvt + kD * kD);
   if (lv.v_explicit && threadIdx.x == 0) {         // the parameters come from no kernel
