@@ -240,10 +240,28 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
       }
     }
     uint32_t r0[16], r1[16];
-    float sum;
-    bool redone = false, free_o = ph == 0;         // O of the stream's last page is complete
+    float sum = 0.f;
+    bool free_o = ph == 0;                         // O of the stream's last page is complete
+    bool redo = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1
     for (;;) {
+      if (redo) {                                  // a reference at the rows' maxima: the first page, or weights too large
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) mx = fmaxf(mx, fmaxf(s0[x], s1[x]));
+        float al = 1.f;
+        if ((m == -INFINITY || sum > kMostSum) && mx > m) {
+          al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
+          m = mx;
+        }
+        l *= al;
+        if (!free_o) {
+          if (!c.wait(kBODone + e, ph - 1)) return false;
+          tc_fence_after();
+          rescale_o(to, al);
+          free_o = true;
+        }
+      }
       // the page's weights against the reference m
       const float mF = m == -INFINITY ? 0.f : fmaf(m, F, -kBias);
       const float2 F2 = make_float2(F, F), nm2 = make_float2(-mF, -mF);
@@ -251,24 +269,9 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
       weights32(s0, F2, nm2, r0, t2);
       weights32(s1, F2, nm2, r1, t2);
       sum = t2.x + t2.y;
-      const bool over = !redone && (sum > kMostSum || m == -INFINITY);
-      if (!__any_sync(0xffffffffu, over)) break;
-      redone = true;                               // against the rows' maxima, once
-      float mx = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < 32; ++x) mx = fmaxf(mx, fmaxf(s0[x], s1[x]));
-      float al = 1.f;
-      if (over && mx > m) {
-        al = m == -INFINITY ? 0.f : exp2f((m - mx) * F);
-        m = mx;
-      }
-      l *= al;
-      if (!free_o) {
-        if (!c.wait(kBODone + e, ph - 1)) return false;
-        tc_fence_after();
-        rescale_o(to, al);
-        free_o = true;
-      }
+      if (redo) break;
+      redo = __any_sync(0xffffffffu, sum > kMostSum);
+      if (!redo) break;
     }
     l += sum;
     if (!free_o) {                                 // the stream's last O has read the weights before these
@@ -811,6 +814,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
+    if (lane == 0 && hist) {                       // the rotation; the parameters come from no kernel
+      const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
+      mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
+      for (int p = 0; p < 2; ++p)                  // R = b1 + b2 to about 17 bits
+        bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
+    }
+    __syncwarp();
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -830,7 +840,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   const int nodes = min(max(asked, 0), a.T);
   if (asked != nodes && tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_TREE);
   const int live = min(kCtaRows, nodes * gq - Q0);  // this CTA's query rows
-  if (live <= 0) return;
+  auto leave = [&]() {                             // nothing to do here: the copies requested above land first
+    if (w == kLoadWarp && lane == 0 && hist) mbar_wait(c.bar(kBImg), 0);
+  };
+  if (live <= 0) return leave();
 
   // ---- the slot's tokens -----------------------------------------------------------------------------------
   if (L < 0) {
@@ -847,8 +860,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   int p0, n;                                       // first page and number of pages of the slot
   if (hist) {
     const int slots = tree_hist_slots(a, np);
-    if (slot >= slots) return;                     // a shorter request: the merge knows
-    n = np / slots;
+    if (slot >= slots) return leave();             // a shorter request: the merge knows
+    n = tree_div(np, slots);
     p0 = slot * n + min(slot, np - slots * n);
     n += slot < np - slots * n;
   } else {
@@ -857,12 +870,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
   }
 
   if (w == kLoadWarp) {
-    if (lane == 0 && hist && n > 0) {              // the rotation
-      const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
-      mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
-      for (int p = 0; p < 2; ++p)                  // R = b1 + b2 to about 17 bits
-        bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
-    }
     if (lane < 2) {                                // row warps that have rows, of a stream
       const int active = ((WIDE ? min(kRows, live - lane * kRows) : live) + 31) / 32;
       mbar_init_n(c.bar(kBSFree + lane), max(active, 1));
