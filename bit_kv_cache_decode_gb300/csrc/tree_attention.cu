@@ -6,7 +6,7 @@
 // The T gq query rows of a kv head are the M = 128 rows of a tensor-core tile, so a page is read and unpacked
 // once for all of them.
 //
-// Grid (slot, kv head x row tile, request), one CTA per SM. A slot is a range of the request's history pages, or of
+// Grid (slot, kv head x row tiles, request), one CTA per SM. A slot is a range of the request's history pages, or of
 // its BF16 and draft pages. A page (64 tokens) is a tile:
 //  * S = Q K^T, A = the rows in TMEM (history: q R_K as fp16, rotated by this CTA at its start; else q as bf16),
 //    B = the keys in shared memory: history keys dequantised to fp16 (zero + scale code, one rounding).
@@ -19,15 +19,21 @@
 // Values are rounded with their zero point in place: with scale * code alone, the rounding of the products and of
 // the zero point's sum would no longer cancel where many tokens average out.
 //
-// Even and odd pages are two streams with an S, P and O, a reference and a sum each, joined when the slot ends: the
-// row threads of one stream work while the tensor pipe runs the other's products, and neither waits for the
-// other's reference. TMEM is full: O of two streams (2 x 128 columns), S (2 x 64), P (2 x 32), Q (64).
-// Warpgroups: 0-1 rows of the even and odd pages, 2-3 unpack keys, 4-5 unpack values (even and odd pages), 6: warp 24
-// issues S(i + 2), warp 25 streams the pages through a ring of bulk copies, warp 26 turns the
-// values' scales and zeros into the pairs the value warps multiply by, warp 27 issues O(i).
-// A history page is 8 MMAs of M128 N64 K16 (32 cycles each) and 4 of M128 N128 K16 (64): 512 cycles of the tensor
-// pipe. The CUDA cores issue about 570 warp instructions per scheduler and page beside them (rows 210, keys 150,
-// values 165, control 40), which bounds the kernel.
+// Two streams with an S, P and O, a reference and a sum each keep the tensor pipe and the row threads busy beside each
+// other. With at most 128 query rows they are the even and the odd pages, joined when the slot ends. With more, a CTA
+// takes two tiles of rows (WIDE), a stream each, and every page is unpacked once for both: 136 rows over 2 x 33K tokens
+// 80 us (a CTA per tile: 105 us), 256 rows over 102,400 tokens 98 us (115 us). TMEM is full: O (2 x 128 columns), S
+// (2 x 64), P (2 x 32), the rows (64; a second tile's are an operand in shared memory).
+// Warpgroups: 0-1 rows of the two streams, 2-3 unpack keys, 4-5 unpack values (even and odd pages), 6: warp 24 issues
+// S, warp 25 streams the pages through a ring of bulk copies, warp 26 turns the values' scales and zeros into the pairs
+// the value warps multiply by, warp 27 issues O. A row thread reads a page's 64 logits at once and so frees S for the
+// stream's next product; it keeps them until its weights stand, in case it has to raise the reference.
+// A history page of one tile is 8 MMAs of M128 N64 K16 (32 cycles each) and 4 of M128 N128 K16 (64): 512 cycles of the
+// tensor pipe. The CUDA cores issue about 725 warp instructions per scheduler beside them (rows 250, keys 190, values
+// 190, control 95) and take 915 cycles a page, 1,770 for two tiles (1,000 instructions): the exponentials (4 cycles a
+// warp), the packed multiplies, adds and half-precision products (2 each) and the bit operations (2) share the issue
+// slots with the hand-overs between the roles. That bounds the kernel. Two threads to a row, half of a page's tokens
+// each, measured 15 % slower: the same instructions and more hand-overs.
 // Every wait is bounded; a CTA whose wait expires flags OSCAR_STATUS_TIMEOUT and writes empty partials.
 #include <algorithm>
 
@@ -971,9 +977,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     } else if (w < kRowWarps) {
       // q R_K has no channel above sqrt(128) max |q|, and one above max |q| / sqrt(128): 2^sigma brings that range to
       // 2^7.5 .. 2^14.5, away from both ends of fp16
-      const int ex = (int)(lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >> 7), sigma = min(max(137 - ex, -120), 60);
-      const float sc = exp2f((float)sigma);
-      F *= exp2f((float)-sigma);
+      const int ex = (int)(lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >> 7), sigma = min(max(137 - ex, -120), 100);
+      const float sc = __int_as_float((127 + sigma) << 23);
+      F *= __int_as_float((127 - sigma) << 23);
       ok = c.wait(kBQ, 0);
       if (ok) {
         tc_fence_after();

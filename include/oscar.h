@@ -356,8 +356,10 @@ int oscar_decode_step_shared(oscar_cache* cache, int layer, int B, const void* q
  * Nothing is changed, and a status bit says why, if a length is negative, shrinks to other than 0 or needs more
  * than max_hist_pages pages, or the new tokens exceed max_tokens (BAD_SEQLEN), a ring's head or count is out of
  * range (BAD_PAGE) or a ring is too short (NO_PAGES). One word of the cache's workspace orders the call's CTAs:
- * as for decode, calls on one cache must not overlap. Errors: INVALID_ARG (B < 0, null pointers, slots not
- * 16-byte aligned, max_tokens < 0), UNSUPPORTED (B > OSCAR_MAX_TABLE_BATCH), CUDA. */
+ * as for decode, calls on one cache must not overlap. oscar_append_kv and oscar_decode_step* read lengths and tables
+ * before they wait for the kernel just before them: there has to be another kernel between this call and theirs on
+ * the stream (the one that makes k and v is). Errors: INVALID_ARG (B < 0, null pointers, slots not 16-byte aligned,
+ * max_tokens < 0), UNSUPPORTED (B > OSCAR_MAX_TABLE_BATCH), CUDA. */
 int oscar_build_tables(oscar_cache* cache, int B, const int32_t* old_lens, const int32_t* new_lens,
                        int32_t* hist_pt, int max_hist_pages, int32_t* bf16_pt, int32_t* free_int2,
                        int32_t* free_bf16, const int32_t* rings_in, int32_t* rings_out, int32_t* cu_tokens,
@@ -437,7 +439,8 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  *                     Calls that may overlap need a workspace each.
  * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
  * infinity in a drafted row reaches the rows that attend to it and no others.
- * The cache is only read. q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
+ * The cache is only read; all inputs but the cache's rotations may come from the kernel just before.
+ * q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
  * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT, B > 65535, sink + recent above
  * 130,560 tokens), CUDA. */
 int oscar_tree_workspace_bytes(const oscar_cache* cache, int B, int T, int max_hist_pages, size_t* bytes);
@@ -454,7 +457,9 @@ int oscar_tree_attention(oscar_cache* cache, int layer, int B, int T, const void
  *  path             : device int32 [B][max_accept], or NULL: nodes 0, 1, 2, ... (a ragged append of T tokens)
  *  max_accept       : 1 .. recent; with a path it may exceed T (a node may be named twice)
  * A request with a length or count out of range is left as it is (BAD_SEQLEN); a token whose node (BAD_TREE), page
- * (BAD_PAGE) or history page (BAD_SEQLEN, BAD_PAGE) is out of range is left out. Errors: INVALID_ARG (as
+ * (BAD_PAGE) or history page (BAD_SEQLEN, BAD_PAGE) is out of range is left out. All inputs may come from the kernel
+ * just before. oscar_append_kv and oscar_decode_step* read the pool's rows before they wait: as after
+ * oscar_build_tables, there has to be another kernel between this call and theirs. Errors: INVALID_ARG (as
  * oscar_append_kv, T < 1, max_accept outside 1 .. recent, path NULL with max_accept > T), CUDA. */
 int oscar_commit_draft(oscar_cache* cache, int layer, int B, int T, const void* k_draft, const void* v_draft,
                        const int32_t* seq_lens_before, const int32_t* n_accept, int max_accept, const int32_t* path,

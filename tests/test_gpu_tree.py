@@ -64,8 +64,9 @@ def test_formats_heads_and_trees(meta, v_mode, gq, T):
 
 @pytest.mark.parametrize("lens", [[0, 1, 63], [64, 65, 128], [319, 320, 321], [383, 384, 385], [448, 449, 577], [2000, 40, 5000]])
 @pytest.mark.parametrize("kind", ["tree", "random", "none"])
-def test_lengths_and_empty_rows(lens, kind):
-    hkv, gq, T = 1, 4, 40
+@pytest.mark.parametrize("T", [9, 40])                     # rows of one tile and of two
+def test_lengths_and_empty_rows(lens, kind, T):
+    hkv, gq = 1, 4
     case = build_decode_case([max(x, 1) for x in lens], hkv, gq, 0, seed=61)
     rng = np.random.default_rng(5)
     q, kd, vd = draft(61, 3, T, hkv, gq)
@@ -96,8 +97,9 @@ def test_numbers_of_nodes(T):
 
 @pytest.mark.parametrize("scale", [8.0, 1 / 8.0])
 @pytest.mark.parametrize("aligned", [False, True])
-def test_peaked_and_diffuse_logits(scale, aligned):
-    lens, hkv, gq, T = [64 + 256 + 64 * 40 + 5], 2, 4, 33
+@pytest.mark.parametrize("T", [24, 33])
+def test_peaked_and_diffuse_logits(scale, aligned, T):
+    lens, hkv, gq = [64 + 256 + 64 * 40 + 5], 2, 4
     case = build_decode_case(lens, hkv, gq, 0, seed=63)
     q, kd, vd = draft(63, 1, T, hkv, gq)
     if aligned:                                            # queries along keys of several pages: late, growing maxima
@@ -112,6 +114,41 @@ def test_peaked_and_diffuse_logits(scale, aligned):
                                dev(lens), hp, bp, sm, out_dtype=osc.OUT_FP32)
     assert cache.get_status() == 0
     compare(out, None, case, lens, q, kd, vd, mask, [T], 0, sm)
+
+
+@pytest.mark.parametrize("T", [6, 40])
+@pytest.mark.parametrize("up", [-60, 1, 60, 100])
+def test_power_of_two_query_scales_change_nothing(T, up):
+    # q 2^up against sm_scale 2^-up: the same logits. The kernel's own scale of the rotated rows is a power of two too,
+    # so every rounding falls alike and the results are the same bits.
+    lens, hkv, gq = [64 + 256 + 64 * 5 + 9], 1, 4
+    cache, _, hp, bp = build_decode_case(lens, hkv, gq, 0, seed=65)
+    q, kd, vd = (to_dev_bf16(x) for x in draft(65, 1, T, hkv, gq))
+    mask = torch.from_numpy(mask_words(random_mask(np.random.default_rng(3), 1, T, "tree"))).to(DEV)
+    args = (kd, vd, mask, dev(lens), hp, bp)
+    plain = cache.tree_attention(0, q, *args, synth.sm_scale(), out_dtype=osc.OUT_FP32)
+    scaled = cache.tree_attention(0, (q.float() * 2.0 ** up).bfloat16(), *args, synth.sm_scale() * 2.0 ** -up,
+                                  out_dtype=osc.OUT_FP32)
+    assert cache.get_status() == 0 and torch.equal(plain, scaled)
+
+
+def test_three_tiles_and_short_drafts():
+    # 65 nodes x 4 heads are three row tiles; drafts that end in the first, at its end, in the second and the third
+    lens, hkv, gq, T = [700, 800, 900, 1000, 640], 1, 4, 65
+    case = build_decode_case(lens, hkv, gq, 0, seed=66)
+    rng = np.random.default_rng(6)
+    q, kd, vd = draft(66, 5, T, hkv, gq)
+    mask = random_mask(rng, 5, T, "tree")
+    n = np.array([5, 32, 33, 65, 0])
+    cache, _, hp, bp = case
+    out = torch.full((5, T, 4, 128), -77.0, device=DEV)
+    lse = torch.full((5, T, 4), -77.0, device=DEV)
+    cache.tree_attention(0, *(to_dev_bf16(x) for x in (q, kd, vd)), torch.from_numpy(mask_words(mask)).to(DEV),
+                         dev(lens), hp, bp, synth.sm_scale(), n_draft=dev(n), out=out, out_dtype=osc.OUT_FP32, lse=lse)
+    assert cache.get_status() == 0
+    compare(out, lse, case, lens, q, kd, vd, mask, n, 0, synth.sm_scale())
+    for b in range(5):
+        assert (out[b, n[b]:] == -77).all() and (lse[b, n[b]:] == -77).all()
 
 
 def test_long_context_and_error_size():
