@@ -158,44 +158,60 @@ def _dev_i32(x, device):
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=device)
 
 
+# torch's names that the calls below look up on every call, bound by the first of them: a call costs about 9 us on the
+# host, and looking them up afresh was 2 us of it
+_tensor = _i32 = _words = _bf16 = _f32 = _f16 = _empty = _get_device = _get_stream = None
+
+
+def _bind_torch():
+    global _tensor, _i32, _words, _bf16, _f32, _f16, _empty, _get_device, _get_stream
+    import torch
+    _i32, _words, _bf16, _f32, _f16 = torch.int32, (torch.int64, torch.uint64), torch.bfloat16, torch.float32, torch.float16
+    _empty, _get_device, _get_stream = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _tensor = torch.Tensor
+
+
+def _on(stream):
+    import torch
+    return torch.cuda.stream(stream)
+
+
 def _here(t) -> tuple[int, int]:
     """The current device, which t has to be on, and its current stream. (The handle is asked for directly: building
     torch's stream object costs 3 us of a call.)"""
-    import torch
-    dev = torch._C._cuda_getDevice()
+    if _tensor is None:
+        _bind_torch()
+    dev = _get_device()
     if t.get_device() != dev:
         raise OscarError(ERR_INVALID_ARG, "tensors on the current device")
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _get_stream(dev)
 
 
 def _in_i32(x, dev: int):
     """int32 values for the library to read: a contiguous tensor on device dev, or host values that are copied."""
-    import torch
-    if isinstance(x, torch.Tensor):
-        if x.dtype != torch.int32 or x.get_device() != dev or not x.is_contiguous():
+    if isinstance(x, _tensor):
+        if x.dtype is not _i32 or x.get_device() != dev or not x.is_contiguous():
             raise OscarError(ERR_INVALID_ARG, "contiguous int32 tensor on the current device")
         return x
+    import torch
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32), device=dev)
 
 
 def _own_i32(t, numel: int, dev: int):
     """An int32 device tensor the library writes (never copied): contiguous, of at least numel elements."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous() or \
+    if not isinstance(t, _tensor) or t.dtype is not _i32 or t.get_device() != dev or not t.is_contiguous() or \
             t.numel() < numel:
         raise OscarError(ERR_INVALID_ARG, f"contiguous int32 tensor of at least {numel} elements on the current device")
     return t
 
 
 def _check_words(t, B: int, T: int, dev: int, what: str):
-    import torch
-    if t.dtype not in (torch.int64, torch.uint64) or t.get_device() != dev or not t.is_contiguous() or \
-            t.shape != (B, T, (T + 63) // 64):
+    if t.dtype not in _words or t.get_device() != dev or not t.is_contiguous() or t.shape != (B, T, (T + 63) // 64):
         raise OscarError(ERR_INVALID_ARG, what)
 
 
 def _check_like(t, dtype, shape, dev: int, what: str):
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
         raise OscarError(ERR_INVALID_ARG, what)
 
 
@@ -380,9 +396,8 @@ class OscarCache:
         the free rings are int32 device tensors updated in place, the ring positions too unless rings_out is given.
         With max_tokens, or a slots tensor [max_tokens, 4], each new token's (position, region, page, row) is
         written. Returns (rings_out, cu_tokens, slots)."""
-        import torch
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on(stream):
                 return self.build_tables(old_lens, new_lens, hist_pt, bf16_pt, free_int2, free_bf16, rings, max_tokens,
                                          rings_out, cu_tokens, slots)
         dev, st = _here(self.pool)
@@ -394,10 +409,10 @@ class OscarCache:
         _own_i32(free_bf16, self.cfg.num_bf16_pages, dev)
         _own_i32(rings, 4, dev)
         rings_out = rings if rings_out is None else _own_i32(rings_out, 4, dev)
-        cu_tokens = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_tokens is None else \
+        cu_tokens = _empty(B + 1, dtype=_i32, device=dev) if cu_tokens is None else \
             _own_i32(cu_tokens, B + 1, dev)
         if slots is None and max_tokens:
-            slots = torch.empty(max_tokens, 4, dtype=torch.int32, device=dev)
+            slots = _empty(max_tokens, 4, dtype=_i32, device=dev)
         if slots is not None:
             max_tokens = _own_i32(slots, 0, dev).numel() // 4
         if new.numel() != B or hist_pt.dim() != 2 or hist_pt.shape[0] != B:
@@ -411,9 +426,8 @@ class OscarCache:
     def tree_layout(self, parents, seq_lens, n_draft=None, mask=None, positions=None, stream=None):
         """Ancestor masks (int64 [B, T, ceil(T / 64)], 64 nodes a word) and positions (int32 [B, T]) of the trees
         given by parents [B, T]."""
-        import torch
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on(stream):
                 return self.tree_layout(parents, seq_lens, n_draft, mask, positions)
         dev, st = _here(self.pool)
         pa, sl = _in_i32(parents, dev), _in_i32(seq_lens, dev)
@@ -422,11 +436,11 @@ class OscarCache:
             raise OscarError(ERR_INVALID_ARG, "oscar_tree_layout")
         B, T = pa.shape
         if mask is None:
-            mask = torch.empty((B, T, (T + 63) // 64), dtype=torch.int64, device=dev)
+            mask = _empty((B, T, (T + 63) // 64), dtype=_words[0], device=dev)
         else:
             _check_words(mask, B, T, dev, "oscar_tree_layout")
         if positions is None:
-            positions = torch.empty((B, T), dtype=torch.int32, device=dev)
+            positions = _empty((B, T), dtype=_i32, device=dev)
         else:
             _own_i32(positions, B * T, dev)
         _check(_lib.oscar_tree_layout(self._h, B, T, pa.data_ptr(), _ptr(nd), sl.data_ptr(), mask.data_ptr(),
@@ -444,9 +458,8 @@ class OscarCache:
         """Attention of drafted nodes q [B, T, Hq, 128] over the cache's seq_lens tokens and, by mask, the drafted
         k_draft, v_draft [B, T, Hkv, 128]. workspace: a uint8 tensor of tree_workspace_bytes, allocated per call
         when not given; calls that may overlap need one each."""
-        import torch
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on(stream):
                 return self.tree_attention(layer, q, k_draft, v_draft, mask, seq_lens, hist_pt, bf16_pt, sm_scale,
                                            n_draft, out, out_dtype, lse, workspace)
         dev, st = _here(self.pool)
@@ -455,23 +468,23 @@ class OscarCache:
         B, T = int(q.shape[0]), int(q.shape[1])
         rows = (B, T, self.cfg.num_q_heads, self.cfg.head_dim)
         drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
-        _check_like(q, torch.bfloat16, rows, dev, "oscar_tree_attention")
-        _check_like(k_draft, torch.bfloat16, drafted, dev, "oscar_tree_attention")
-        _check_like(v_draft, torch.bfloat16, drafted, dev, "oscar_tree_attention")
+        _check_like(q, _bf16, rows, dev, "oscar_tree_attention")
+        _check_like(k_draft, _bf16, drafted, dev, "oscar_tree_attention")
+        _check_like(v_draft, _bf16, drafted, dev, "oscar_tree_attention")
         _check_words(mask, B, T, dev, "oscar_tree_attention")
         mhp = hp.shape[1] if hp.dim() == 2 else 0
         if sl.numel() != B or (nd is not None and nd.numel() != B) or hp.numel() != B * mhp or \
                 bp.numel() != B * ((self.cfg.sink + self.cfg.recent) // self.cfg.page_size):
             raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
-        out_type = torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16
+        out_type = _f32 if out_dtype == OUT_FP32 else _bf16
         if out is None:
-            out = torch.empty(rows, dtype=out_type, device=dev)
+            out = _empty(rows, dtype=out_type, device=dev)
         else:
             _check_like(out, out_type, rows, dev, "oscar_tree_attention")
         if lse is not None:
-            _check_like(lse, torch.float32, rows[:3], dev, "oscar_tree_attention")
+            _check_like(lse, _f32, rows[:3], dev, "oscar_tree_attention")
         if workspace is None:
-            workspace = torch.empty(self.tree_workspace_bytes(B, T, mhp), dtype=torch.uint8, device=dev)
+            workspace = self.pool.new_empty(self.tree_workspace_bytes(B, T, mhp))
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
         _check(_lib.oscar_tree_attention(self._h, layer, B, T, q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(),
@@ -484,9 +497,8 @@ class OscarCache:
                      max_accept: int | None = None, stream=None):
         """Append nodes path[r, :n_accept[r]] of k_draft, v_draft [B, T, Hkv, 128] at seq_lens_before[r]; without a
         path nodes 0 .. n_accept[r] - 1 (max_accept of them at most, T by default)."""
-        import torch
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _on(stream):
                 return self.commit_draft(layer, k_draft, v_draft, seq_lens_before, n_accept, hist_pt, bf16_pt, path,
                                          max_accept)
         dev, st = _here(self.pool)
@@ -495,8 +507,8 @@ class OscarCache:
         pa = None if path is None else _in_i32(path, dev)
         B, T = int(k_draft.shape[0]), int(k_draft.shape[1])
         drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
-        _check_like(k_draft, torch.bfloat16, drafted, dev, "oscar_commit_draft")
-        _check_like(v_draft, torch.bfloat16, drafted, dev, "oscar_commit_draft")
+        _check_like(k_draft, _bf16, drafted, dev, "oscar_commit_draft")
+        _check_like(v_draft, _bf16, drafted, dev, "oscar_commit_draft")
         mhp = hp.shape[1] if hp.dim() == 2 else 0
         if sl.numel() != B or na.numel() != B or hp.numel() != B * mhp or \
                 bp.numel() != B * ((self.cfg.sink + self.cfg.recent) // self.cfg.page_size) or \
@@ -612,15 +624,14 @@ def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool
     head strides are free, a head's channels contiguous. Written to q_out, k_out (new tensors when not given; the
     inputs themselves for in place). Rows with a negative position are left as they are: new tensors hold them
     unset. Returns (q_out, k_out)."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             return rope(plan, q, k, positions, layout, inverse, q_out, k_out)
     dev, st = _here(q)
     pos = _in_i32(positions, dev)
     dtype, shape, n = q.dtype, q.shape, pos.numel()
-    code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32 if dtype == torch.float32 else DTYPE_FP16
-    if (code == DTYPE_FP16 and dtype != torch.float16) or plan.turns.get_device() != dev or len(shape) != 3:
+    code = DTYPE_BF16 if dtype is _bf16 else DTYPE_FP32 if dtype is _f32 else DTYPE_FP16
+    if (code == DTYPE_FP16 and dtype is not _f16) or plan.turns.get_device() != dev or len(shape) != 3:
         raise OscarError(ERR_INVALID_ARG, "oscar_rope")
     dim = shape[2]
     args, outs = [], []
@@ -630,8 +641,8 @@ def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool
             outs.append(None)
             continue
         if out is None:
-            out = torch.empty(x.shape, dtype=dtype, device=dev)
-        if x.dtype != dtype or out.dtype != dtype or x.get_device() != dev or out.get_device() != dev or \
+            out = _empty(x.shape, dtype=dtype, device=dev)
+        if x.dtype is not dtype or out.dtype is not dtype or x.get_device() != dev or out.get_device() != dev or \
                 x.dim() != 3 or x.shape != out.shape or x.shape[0] != n or x.shape[2] != dim:
             raise OscarError(ERR_INVALID_ARG, "oscar_rope")
         (it, ih, ic), (ot, oh, oc) = x.stride(), out.stride()

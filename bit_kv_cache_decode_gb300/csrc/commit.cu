@@ -4,18 +4,18 @@
 // Token j of request r (0 <= j < n_accept[r]) takes position p = L + j. If p >= sink + recent, the oldest
 // recent token, at position p - recent, is demoted first: rotated, clipped, quantised and packed into the
 // history. Its ring slot is the slot of p itself, and with n_accept <= recent no two tokens share a slot, so
-// the tokens are independent of one another. A unit of work is 16 of them (one tensor-core tile of demoted rows)
-// of one (request, kv head, K / V).
+// the tokens are independent of one another.
 //
-// A CTA serves one (kv head, K / V) and walks units: the places of 8 units at a time are looked up together, the
-// 64 KB of rotation fragments are fetched once, and a unit's old and new rows are loaded while the unit before it
-// is rotated. Half of the threads carry the old rows to the tile, the others the new rows to the slots, after a
-// barrier that follows the old rows' arrival.
+// A CTA serves one (kv head, K / V) and walks the requests in units of 16 tokens. The places of 8 units are looked up
+// together and listed, tokens that demote a row first; the list is worked off 16 tokens at a time, so that a tile of
+// the tensor cores is full though a request brings few. The 64 KB of rotation fragments are fetched once, and a
+// tile's old and new rows are loaded while the tile before it is rotated. Half of the threads carry the old rows to
+// the tile, the others the new rows to the slots, after a barrier that follows the old rows' arrival.
 //
 // Rotation and quantiser are the append's own (rotate_tile16, quantize_pack_row), so the bytes are those of a
 // chain of oscar_append_kv calls. The call moves a few KB per request; its time is latency: the launch, the
 // places, the fragments from L2 and a tile per unit (a tile's rows and fragments from shared memory, its 16 rows'
-// quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 22.4 us (a unit per CTA: 28.8 us; V fields set row
+// quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 20.5 us (a CTA per 16 tokens of a request: 28.8 us; V fields set row
 // by row: 24.4 us); one request, 3 tokens: 5.7 us.
 #include <algorithm>
 
@@ -41,34 +41,30 @@ struct CommitArgs {
 constexpr int kWarps = 16;                         // a warp rotates 8 channels of the tile and quantises a row of it
 constexpr int kUnits = 8;                          // units whose places are looked up together
 
-// The 2-bit V fields of a unit's demoted rows, channel-major in their pages. A channel's 64 rows are 16 bytes: thread
-// (channel, half) gathers the fields of the rows in its 8 bytes and sets them with one atomic pair per page (the
-// unit's rows are consecutive: one page or two). Atomics, as other rows of the same 8 bytes may be another unit's.
-// row0: the page row of the unit's row 0 (a row t's field is in half (t >> 2) & 1, so 8 of the 16 rows are a thread's).
-__device__ __forceinline__ void set_v_codes(const LayerView& lv, int h, int row0, const int* hpage,
+// The 2-bit V fields of a tile's demoted rows, channel-major in their pages. A channel's 64 rows are 16 bytes: thread
+// (channel, half) gathers the fields of the rows in its 8 bytes and sets them with one atomic pair per page (rows of a
+// page follow one another). Atomics, as other rows of the same 8 bytes may be another CTA's. hpage: -1 behind the
+// last demoted row.
+__device__ __forceinline__ void set_v_codes(const LayerView& lv, int h, const int* hpage, const int* hrow,
                                             const uint8_t (*codes)[kD / 4]) {
   const int c = threadIdx.x & (kD - 1), half = threadIdx.x >> 7;
-  unsigned long long mask[2] = {0, 0}, value[2] = {0, 0};
-  int page[2] = {-1, -1};
+  unsigned long long mask = 0, value = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = ((4 * half + (k & 3) - row0) & 7) + 8 * (k >> 2), t = row0 + i, e = t >= kP;
-    if (hpage[i] < 0) continue;
-    const int sh = 32 * (v_word(t) & 1) + v_bit(t % kP);
-    const unsigned long long m = 3ull << sh, v = (unsigned long long)((codes[i][c >> 2] >> (2 * (c & 3))) & 3) << sh;
-    mask[0] |= e ? 0ull : m;
-    value[0] |= e ? 0ull : v;
-    mask[1] |= e ? m : 0ull;
-    value[1] |= e ? v : 0ull;
-    if (e) page[1] = hpage[i];
-    else page[0] = hpage[i];
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (page[e] < 0) continue;
-    auto* at = reinterpret_cast<unsigned long long*>(int2_block_w(lv, page[e], h) + v_chan_off(c) + 8 * half);
-    atomicAnd(at, ~mask[e]);
-    if (value[e] != 0) atomicOr(at, value[e]);
+  for (int i = 0; i < kTileRows; ++i) {
+    const int page = hpage[i], t = hrow[i];
+    const bool mine = page >= 0 && v_word(t) >> 1 == half;
+    const int sh = 32 * (v_word(t) & 1) + v_bit(t);
+    const unsigned long long code = (codes[i][c >> 2] >> (2 * (c & 3))) & 3u;
+    mask |= mine ? 3ull << sh : 0ull;
+    value |= mine ? code << sh : 0ull;
+    if (i + 1 == kTileRows || hpage[i + 1] != page) {   // alike in all threads
+      if (mask != 0) {
+        auto* at = reinterpret_cast<unsigned long long*>(int2_block_w(lv, page, h) + v_chan_off(c) + 8 * half);
+        atomicAnd(at, ~mask);
+        if (value != 0) atomicOr(at, value);
+      }
+      mask = value = 0;
+    }
   }
 }
 
@@ -80,7 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
   const uint32_t bars = smem_addr(tau_s + kD);
   __shared__ int s_hpage[kUnits * kTileRows], s_hrow[kUnits * kTileRows];   // demoted row's place, -1: no demotion
   __shared__ int s_page[kUnits * kTileRows], s_row[kUnits * kTileRows];     // new token's place, -1: none
-  __shared__ int s_node[kUnits * kTileRows];
+  __shared__ int s_node[kUnits * kTileRows], s_req[kUnits * kTileRows], s_count[2][kUnits / 2];
   __shared__ uint8_t codes[kTileRows][kD / 4];     // V rows' packed bytes
   const int h = blockIdx.y, kind = blockIdx.z;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -90,7 +86,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
   const bool turns = kind == OSCAR_KIND_K || lv.v_explicit;   // this kind's rows are rotated
   const float* prm = lv.params + (size_t)h * kParamFloats;
   auto in = [](int p, int count) { return p >= 0 && p < count; };
-  if (tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
+  // every first load of a memory region takes thousands of cycles: what comes back is stored when the others are under way
+  const float tau = tid < kD ? prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid] : 0.f;
   bool fetched = false, rotated = false;
 
   for (long long u0 = blockIdx.x; u0 < units; u0 += kUnits * step) {
@@ -99,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
     int b = 0, j = 0, L = 0, n = 0;
     bool live = false;
     if (tid < kUnits * kTileRows && u < units) {
-      b = (int)(u / tiles);
+      b = tiles == 1 ? (int)u : (int)(u / tiles);
       j = (int)(u - (long long)b * tiles) * kTileRows + (tid & 15);
       L = a.seq_lens[b];
       n = a.n_accept[b];
@@ -135,33 +132,48 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
         if (ok_node && ok_page && !ok_hist) flag(lv.status, fits ? OSCAR_STATUS_BAD_PAGE : OSCAR_STATUS_BAD_SEQLEN);
         if (!ok_node || !ok_page || !ok_hist) page = hpage = -1;
       }
-      s_hpage[tid] = hpage;
-      s_hrow[tid] = hh & (kP - 1);                 // (hh < 0: row 0 of a unit whose later rows are demoted)
-      s_page[tid] = page;
-      s_row[tid] = slot % kP;
-      s_node[tid] = node;
+      // the list's order: demoting tokens by their place in the units, then the others
+      const unsigned demoting = __ballot_sync(0xffffffffu, hpage >= 0);
+      const unsigned other = __ballot_sync(0xffffffffu, hpage < 0 && page >= 0);
+      if (lane == 0) {
+        s_count[0][w] = __popc(demoting);
+        s_count[1][w] = __popc(other);
+      }
+      s_hpage[tid] = -1;
+      asm volatile("bar.sync 1, %0;" ::"n"(kUnits * kTileRows) : "memory");
+      int at = 0;
+      for (int i = 0; i < kUnits / 2; ++i) at += (i < w || hpage < 0 ? s_count[0][i] : 0) + (i < w && hpage < 0 ? s_count[1][i] : 0);
+      at += __popc((hpage >= 0 ? demoting : other) & ((1u << lane) - 1u));
+      if (page >= 0) {
+        s_hpage[at] = hpage;
+        s_hrow[at] = hh & (kP - 1);
+        s_page[at] = page;
+        s_row[at] = slot % kP;
+        s_node[at] = node;
+        s_req[at] = b;
+      }
     }
+    if (tid < kD) tau_s[tid] = tau;
     __syncthreads();
-    // ---- unit by unit: 16 bytes of row r for each thread, an old row's or a new one's ----
+    int listed = 0;
+    for (int i = 0; i < kUnits / 2; ++i) listed += s_count[0][i] + s_count[1][i];
+    // ---- 16 tokens of the list at a time: 16 bytes of row r for each thread, an old row's or a new one's ----
     const bool is_new = tid >= 256;
     const int r = (tid >> 4) & 15, c8 = tid & 15;
-    auto load = [&](int q) {
-      const int m = q * kTileRows + r;
+    auto load = [&](int m) {
       const uint4* src = nullptr;
-      if (q < kUnits && s_page[m] >= 0) {
-        if (is_new) {
-          const long long rb = (u0 + q * step) / tiles;
+      if (m < listed) {
+        if (is_new)
           src = reinterpret_cast<const uint4*>((kind == OSCAR_KIND_K ? a.k : a.v) +
-                                               ((rb * a.T + s_node[m]) * lv.hkv + h) * kD + 8 * c8);
-        } else if (s_hpage[m] >= 0) {
+                                               (((size_t)s_req[m] * a.T + s_node[m]) * lv.hkv + h) * kD + 8 * c8);
+        else if (s_hpage[m] >= 0)
           src = reinterpret_cast<const uint4*>(bf16_row(lv, s_page[m], h, kind, s_row[m]) + 8 * c8);
-        }
       }
       return src != nullptr ? *src : make_uint4(0u, 0u, 0u, 0u);
     };
-    uint4 next = load(0);
-    for (int q = 0; q < kUnits && u0 + q * step < units; ++q) {
-      const int m = q * kTileRows + r;
+    uint4 next = load(r);
+    for (int t0 = 0; t0 < listed; t0 += kTileRows) {
+      const int m = t0 + r;
       const uint4 x = next;
       if (!is_new) {
         const uint32_t wds[4] = {x.x, x.y, x.z, x.w};
@@ -171,8 +183,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
         dst[1] = make_float4(__uint_as_float(wds[2] << 16), __uint_as_float(wds[2] & 0xffff0000u),
                              __uint_as_float(wds[3] << 16), __uint_as_float(wds[3] & 0xffff0000u));
       }
-      const bool demotes = __syncthreads_or(s_hpage[m] >= 0);   // the tile is staged, the old rows are read
-      next = load(q + 1);
+      __syncthreads();                             // the tile is staged, the old rows are read
+      next = load(m + kTileRows);
+      const bool demotes = s_hpage[t0] >= 0;
       if (demotes) {
         if (turns) {
           rotated = true;
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
             return;                                // these tokens are left out
           }
         }
-        const int at = q * kTileRows + w;          // a warp's row
+        const int at = t0 + w;                     // a warp's row
         if (s_hpage[at] >= 0) {
           float y[4];
 #pragma unroll
@@ -195,16 +208,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
           else codes[w][rev5(lane)] = (uint8_t)byte;
         }
       }
-      if (is_new && s_page[m] >= 0) {
+      if (is_new && m < listed) {
         if (bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y) || bf16x2_nonfinite(x.z) || bf16x2_nonfinite(x.w))
           flag(lv.status, OSCAR_STATUS_NONFINITE);
         *reinterpret_cast<uint4*>(bf16_row(lv, s_page[m], h, kind, s_row[m]) + 8 * c8) = x;
       }
       __syncthreads();                             // the tile is free, the codes are complete
-      if (demotes && kind == OSCAR_KIND_V) {
-        if (tid < 2 * kD) set_v_codes(lv, h, s_hrow[q * kTileRows], s_hpage + q * kTileRows, codes);
-        // the next unit's codes are written after a barrier of its own
-      }
+      if (demotes && kind == OSCAR_KIND_V && tid < 2 * kD) set_v_codes(lv, h, s_hpage + t0, s_hrow + t0, codes);
+      // the next tile's codes are written after a barrier of its own
     }
     __syncthreads();                               // the places are free
   }

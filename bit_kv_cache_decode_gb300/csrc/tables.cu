@@ -11,7 +11,7 @@
 // of the new tokens' slots; a slot's page is looked up from the request's table or, for a page popped by this
 // call, from the ring, never from an entry another CTA writes. The last CTA to finish reading writes the new
 // ring positions, which may alias the old ones. The kernel is bound by latency: its launch, the lengths, the scan, a
-// page id. 64 prompts of up to 16K tokens (slots 9 MB): 11.9 us; one prompt of 777: 5.1 us. Up to eight CTAs per SM
+// page id. 64 prompts of up to 16K tokens (slots 9 MB): 11.1 us; one prompt of 777: 4.4 us. Up to eight CTAs per SM
 // hide the slots' lookups (one: 18 us).
 //
 // k_tree_layout. Ancestor sets by pointer doubling: after step k a node's bit set holds its ancestors within
@@ -68,8 +68,7 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
   __shared__ Counts red[kTabThreads / 32];
   __shared__ int s_ring[4], s_bad;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  if (tid < 4) s_ring[tid] = a.rings_in[tid];
-  if (tid == 0) s_bad = 0;
+  const int position = tid < 4 ? a.rings_in[tid] : 0;   // stored below, when the lengths are under way too
 
   // ---- the scan: each thread counts a run of requests, the CTA scans the threads' sums ----
   int bad = 0;
@@ -102,6 +101,8 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
     if (lane >= o) upto += x;
   }
   if (lane == 31) red[w] = upto;
+  if (tid < 4) s_ring[tid] = position;
+  if (tid == 0) s_bad = 0;
   __syncthreads();
   Counts all = {}, at = {};
 #pragma unroll
@@ -131,6 +132,14 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
   __syncthreads();
   bad = s_bad;
   const int total = tok0[a.B];
+  // ---- the new ring positions, by the last CTA that has read the old ones (each has them in shared memory) ----
+  if (tid == 0 && (gridDim.x == 1 || atomicInc(a.ticket, gridDim.x - 1) == gridDim.x - 1)) {   // wraps to 0: ready again
+    const bool ok = bad == 0;
+    a.rings_out[0] = ok && a.cap_int2 > 0 ? (int)((s_ring[0] + all.v[kPopH]) % a.cap_int2) : s_ring[0];
+    a.rings_out[1] = s_ring[1] + (ok ? (int)(all.v[kPushH] - all.v[kPopH]) : 0);
+    a.rings_out[2] = ok && a.cap_bf16 > 0 ? (int)((s_ring[2] + all.v[kPopB]) % a.cap_bf16) : s_ring[2];
+    a.rings_out[3] = s_ring[3] + (ok ? (int)(all.v[kPushB] - all.v[kPopB]) : 0);
+  }
 
   if (bad == 0) {
     auto ring = [](int head, int i, int cap) {        // head, i < cap (i: of the entries the call takes or adds)
@@ -201,22 +210,6 @@ __global__ void __launch_bounds__(kTabThreads) k_build_tables(TablesArgs a) {
   } else if (blockIdx.x == 0 && tid == 0) {
     flag(a.status, bad);
   }
-  // ---- the new ring positions, by the last CTA that has read the old ones ----
-  __syncthreads();
-  if (tid == 0) {
-    bool last = true;
-    if (gridDim.x > 1) {
-      __threadfence();
-      last = atomicInc(a.ticket, gridDim.x - 1) == gridDim.x - 1;   // wraps to 0: ready for the next call
-    }
-    if (last) {
-      const bool ok = bad == 0;
-      a.rings_out[0] = ok && a.cap_int2 > 0 ? (int)((s_ring[0] + all.v[kPopH]) % a.cap_int2) : s_ring[0];
-      a.rings_out[1] = s_ring[1] + (ok ? (int)(all.v[kPushH] - all.v[kPopH]) : 0);
-      a.rings_out[2] = ok && a.cap_bf16 > 0 ? (int)((s_ring[2] + all.v[kPopB]) % a.cap_bf16) : s_ring[2];
-      a.rings_out[3] = s_ring[3] + (ok ? (int)(all.v[kPushB] - all.v[kPopB]) : 0);
-    }
-  }
 }
 
 // One CTA per request, one thread per node.
@@ -227,12 +220,12 @@ __global__ void __launch_bounds__(kMaxDraft) k_tree_layout(const int* __restrict
   __shared__ unsigned long long anc[2][kMaxDraft][kMaxDraft / 64];
   __shared__ short up[2][kMaxDraft];               // the node 2^k steps above, -1 past the root, -2 past a bad parent
   const int b = blockIdx.x, i = threadIdx.x;
-  int n = n_draft != nullptr ? n_draft[b] : T;
-  if ((n < 0 || n > T) && i == 0) flag(status, OSCAR_STATUS_BAD_TREE);
-  n = min(max(n, 0), T);
-  const int L = seq_lens[b];
+  const int asked = n_draft != nullptr ? n_draft[b] : T, L = seq_lens[b];   // independent loads
+  const int parent = i < T ? parents[(size_t)b * T + i] : -1;
+  if ((asked < 0 || asked > T) && i == 0) flag(status, OSCAR_STATUS_BAD_TREE);
+  const int n = min(max(asked, 0), T);
   if (i < T) {
-    int p = i < n ? parents[(size_t)b * T + i] : -1;
+    int p = i < n ? parent : -1;
     if (p < -1 || p >= i) {
       flag(status, OSCAR_STATUS_BAD_TREE);
       p = -2;

@@ -33,12 +33,12 @@ __global__ void __launch_bounds__(kTmThreads) k_tree_merge(LayerView lv, TreeArg
   }
   pdl_wait();                                      // the partials are written by the preceding grid
   pdl_launch_dependents();
-  const int nodes = live_nodes(a, b);
+  const int nodes = live_nodes(a, b), len = a.seq_lens[b];   // independent loads
   if (blockIdx.x * kTmRows >= nodes * gq) {        // nothing here: let the copies land, then leave
     if (lv.v_explicit && threadIdx.x == 0) mbar_wait(bar, 0);
     return;
   }
-  const int hist_slots = tree_hist_slots(a, tree_pages(lv, a, a.seq_lens[b]));
+  const int hist_slots = tree_hist_slots(a, tree_pages(lv, a, len));
   const int qt = Q / kTreeRows, row = Q % kTreeRows;
   const size_t step = (size_t)a.rows * kPartFloats;
   const float* p0 = tree_part(lv, a, b, qt, h, 0);
