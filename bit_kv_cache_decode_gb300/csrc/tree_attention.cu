@@ -128,15 +128,18 @@ __device__ __forceinline__ void sts32(uint32_t at, uint32_t x) {
 __device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
-// (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}; blk: shared address of the page block
+// (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}; blk: shared address of the page block.
+// Compact format: a value is mn8 D - T + code (mx8 - mn8) E with D = 3 E and T = 127.5 D, that is E times
+// 3 mn8 - 382.5 + code (mx8 - mn8), which fp16 holds exactly. The group's E goes into the query rows and, for values,
+// into the partials. (Scale and zero rounded to fp16 tripled the outputs' error.)
 template <int FMT>
-__device__ __forceinline__ uint2 scale_zero(uint32_t blk, int kind, int row, const float* mc) {
+__device__ __forceinline__ uint2 scale_zero(uint32_t blk, int kind, int row) {
   if (FMT == kFmtU8) {
-    const uint32_t m = lds32(blk + (kind ? kVMetaOffU8 : kKMetaOff) + 4 * row);
-    const float* c = mc + 8 * kind;
-    const float2 a = u8_scale_zero(m & 0xffu, (m >> 8) & 0xffu, c[0], c[1], c[2]);
-    const float2 b = u8_scale_zero((m >> 16) & 0xffu, m >> 24, c[4], c[5], c[6]);
-    return make_uint2(pack_f16x2(a.x, a.y), pack_f16x2(b.x, b.y));
+    const uint32_t m = lds32(blk + (kind ? kVMetaOffU8 : kKMetaOff) + 4 * row);   // mn8, mx8 of group 0, of group 1
+    const uint32_t mn = hfma2_u(__byte_perm(m, kMagic, 0x5250), 0x3C003C00u, 0xE400E400u);   // (1024 + mn8) - 1024
+    const uint32_t mx = hfma2_u(__byte_perm(m, kMagic, 0x5351), 0x3C003C00u, 0xE400E400u);
+    const uint32_t s = hfma2_u(mn, 0xBC00BC00u, mx), z = hfma2_u(mn, 0x42004200u, 0xDDFADDFAu);   // 3 mn8 - 382.5
+    return make_uint2(__byte_perm(s, z, 0x5410), __byte_perm(s, z, 0x7632));
   }
   uint2 m = lds64(blk + (kind ? kVMetaOff : kKMetaOff) + 8 * row);
   if (FMT == kFmtCB) {                             // range 256 / 255: the levels are k_c / 256
@@ -362,7 +365,6 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
 template <int FMT>
 __device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, int h, int e, int n) {
   const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3, t0 = (lane & 7) + 8 * kw, u0 = lane >> 3;
-  const float* mc = meta_consts(lv, h, 0);
   const uint32_t lut = FMT == kFmtCB ? lut_of(lv, h, OSCAR_KIND_K) : 0u;
   const uint32_t dst0 = c.base + kOffK + kw * kSboK + 2 * u0 * 128 + (t0 & 7) * 16;
 #pragma unroll 1
@@ -377,7 +379,7 @@ __device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, i
     uint32_t x[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      sz[k] = scale_zero<FMT>(blk, 0, t0 + 32 * k, mc);
+      sz[k] = scale_zero<FMT>(blk, 0, t0 + 32 * k);
 #pragma unroll
       for (int g = 0; g < 2; ++g) x[k][g] = lds32(codes + 1024 * k + 16 * g);
     }
@@ -407,16 +409,15 @@ __device__ __forceinline__ bool keys_history(const Ctx c, const LayerView& lv, i
 // Warp 26: the scales and zeros of a page as fp16 pairs in that order. Tokens past the end get 0 and 0: the block's
 // bytes there may be anything, and 0 times a NaN would reach O.
 template <int FMT>
-__device__ __forceinline__ bool value_pairs(const Ctx c, const LayerView& lv, int h, int n) {
+__device__ __forceinline__ bool value_pairs(const Ctx c, int n) {
   const int lane = threadIdx.x & 31;
   const int w = (lane >> 2) & 3, p = (lane & 3) + 4 * (lane >> 4), t = 16 * (p >> 1) + 2 * w + 8 * (p & 1);
-  const float* mc = meta_consts(lv, h, 0);
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int st = i % kStages, nv = c.tokens(i);
     if (!c.wait(kBFull + st, i / kStages)) return false;
     const uint32_t blk = c.base + kOffRing + st * kBlockBytes, to = c.base + kOffMeta + st * kMetaStage + 4 * lane;
-    uint2 a = scale_zero<FMT>(blk, 1, t, mc), d = scale_zero<FMT>(blk, 1, t + 1, mc);
+    uint2 a = scale_zero<FMT>(blk, 1, t), d = scale_zero<FMT>(blk, 1, t + 1);
     if (t >= nv) a = make_uint2(0u, 0u);
     if (t + 1 >= nv) d = make_uint2(0u, 0u);
     sts32(to, __byte_perm(a.x, d.x, 0x5410));
@@ -590,7 +591,7 @@ __device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w,
     }
     return true;
   }
-  if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, lv, h, n);
+  if (w == kMetaWarp) return !hist || value_pairs<FMT>(c, n);
   // the MMAs, each kind issued by a warp of its own; page i is in buffer i % 4. One tile: page i belongs to stream i & 1.
   // Two tiles: to both streams, the second one's rows are an operand in shared memory.
   static_assert(kBufs == 4, "two pages of each stream");
@@ -681,10 +682,10 @@ struct NearPages {
 
 // Partials of a slot, thread = row. One tile: the streams' O joined, a warpgroup per half of the channels; both streams'
 // row warps meet first (each has waited for its stream's last product). Two tiles: a warpgroup each. A CTA that failed
-// writes empty ones. ref, l: the row's reference and sum of its stream.
+// writes empty ones. ref, l: the row's reference and sum of its stream. unit: what the values of a group were in units of.
 template <bool WIDE>
 __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv, const TreeArgs& a, int h, int qt, int n, int live,
-                                               float ref, float l) {
+                                               float ref, float l, float2 unit) {
   const int tid = threadIdx.x, w = tid >> 5, row = tid & (kRows - 1), half = (tid >> 7) & 1;
   float M = ref, w0 = 1.f, w1 = 0.f;
   if (!WIDE) {
@@ -710,17 +711,18 @@ __device__ __forceinline__ void write_partials(const Ctx c, const LayerView& lv,
 #pragma unroll 1
   for (int k = WIDE ? 0 : 2 * half; k < (WIDE ? 4 : 2 * half + 2); ++k) {
     float x[32], y[32];
+    const float u = k < 2 ? unit.x : unit.y, u0 = w0 * u, u1 = w1 * u;
     if (!good) {
 #pragma unroll
       for (int t = 0; t < 32; ++t) x[t] = 0.f;
     } else if (!WIDE && n > 1) {
       tmem_ld32x2(to + 32 * k, to + 128 + 32 * k, x, y);
 #pragma unroll
-      for (int t = 0; t < 32; ++t) x[t] = w0 * x[t] + w1 * y[t];
+      for (int t = 0; t < 32; ++t) x[t] = u0 * x[t] + u1 * y[t];
     } else {
       tmem_ld32(to + 32 * k, x);
 #pragma unroll
-      for (int t = 0; t < 32; ++t) x[t] *= w0;
+      for (int t = 0; t < 32; ++t) x[t] *= u0;
     }
     if (row < live) {
       float4* dst = reinterpret_cast<float4*>(part) + 8 * k * a.rows + row;
@@ -770,7 +772,12 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
       }
       if (!ok) c.fail();
       const float ref = m == -INFINITY ? -INFINITY : hist ? fmaf(m, F, -kBias) : m * F;
-      write_partials<WIDE>(c, lv, a, h, qt, n, live, ref, lsum);
+      float2 unit = make_float2(1.f, 1.f);
+      if (FMT == kFmtU8 && hist) {
+        const float* mc = meta_consts(lv, h, OSCAR_KIND_V);
+        unit = make_float2(mc[2], mc[6]);
+      }
+      write_partials<WIDE>(c, lv, a, h, qt, n, live, ref, lsum, unit);
     }
   } else if (w < kVWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
@@ -980,6 +987,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       const int ex = (int)(lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >> 7), sigma = min(max(137 - ex, -120), 100);
       const float sc = __int_as_float((127 + sigma) << 23);
       F *= __int_as_float((127 - sigma) << 23);
+      float unit[2] = {1.f, 1.f};                  // compact format: what the keys of a group are in units of
+      if (FMT == kFmtU8) {
+        const float* mc = meta_consts(lv, h, OSCAR_KIND_K);
+        const float most = fmaxf(mc[2], mc[6]), all = most > 0.f ? most : 1.f;
+        unit[0] = mc[2] / all;
+        unit[1] = mc[6] / all;
+        F *= all;
+      }
       ok = c.wait(kBQ, 0);
       if (ok) {
         tc_fence_after();
@@ -989,10 +1004,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
           float y[32];
           tmem_ld32(from + 32 * k, y);
           uint32_t r[16];
+          const float u_sc = FMT == kFmtU8 ? sc * (k < 2 ? unit[0] : unit[1]) : sc;
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[8 * u + j] = pack_f16x2(y[16 * u + j] * sc, y[16 * u + 8 + j] * sc);
+            for (int j = 0; j < 8; ++j) r[8 * u + j] = pack_f16x2(y[16 * u + j] * u_sc, y[16 * u + 8 + j] * u_sc);
           if (WIDE && half == 1) {
             const uint32_t dst = c.base + kOffQ + (row >> 3) * kSboK + (row & 7) * 16 + 4 * k * 128;
 #pragma unroll

@@ -184,6 +184,22 @@ def test_long_context_and_error_size():
     assert cache.get_status() == 0
 
 
+@pytest.mark.parametrize("T", [20, 40])
+def test_compact_metadata_rounds_neither_keys_nor_values(T):
+    lens, hkv, gq = [6011], 1, 4
+    case = build_decode_case(lens, hkv, gq, 0, seed=67, meta="u8")
+    q, kd, vd = draft(67, 1, T, hkv, gq)
+    mask = random_mask(np.random.default_rng(4), 1, T, "tree")
+    cache, prm, hp, bp = case
+    out = cache.tree_attention(0, *(to_dev_bf16(x) for x in (q, kd, vd)), torch.from_numpy(mask_words(mask)).to(DEV),
+                               dev(lens), hp, bp, synth.sm_scale(), out_dtype=osc.OUT_FP32)
+    assert cache.get_status() == 0
+    ref, sd = attend_rounded(pool_from_device(cache, 0), prm, lens[0], hp[0], bp[0], *(x[0].astype(np.float64) for x in (q, kd, vd)),
+                             mask[0], synth.sm_scale(), compact=True)
+    off = np.abs(out[0].double().cpu().numpy() - ref)      # the bound of the test above
+    assert (off <= 8.2 * sd + 2.0 ** -18 * np.abs(ref) + 2.0 ** -21).all(), (off / sd).max()
+
+
 def test_one_node_is_one_decode_step():
     # a single node over the cache and itself, before it is appended: with the recent window not yet full nothing is
     # demoted, so the tokens are those of oscar_decode_step

@@ -92,10 +92,11 @@ def attend(pm: P.PoolModel, prm, L, hist_pt, bf16_pt, v_absorbed, q, kd, vd, mas
     return o, lse, bound, lse_bound
 
 
-def attend_rounded(pm: P.PoolModel, prm, L, hist_pt, bf16_pt, q, kd, vd, mask, sm_scale):
+def attend_rounded(pm: P.PoolModel, prm, L, hist_pt, bf16_pt, q, kd, vd, mask, sm_scale, compact=False):
     """One request (fp16 metadata, V absorbed), with the history's operands rounded as the kernel rounds them: the
     rotated query row scaled by a power of two, and every dequantised key and value, to fp16. What is left of the
-    kernel's error is its weights' rounding to fp16 and float32 arithmetic.
+    kernel's error is its weights' rounding to fp16 and float32 arithmetic. Compact metadata: keys and values are whole
+    multiples of half a step of their group's grid and not rounded; the query row is rounded in units of the steps.
 
     Returns o and the standard deviation of o from the weights' rounding. Rounding a weight p to fp16 makes a relative
     error of at most 2^-11, spread over its interval: a variance of at most 2^-22 / 3, independent from token to token.
@@ -108,14 +109,19 @@ def attend_rounded(pm: P.PoolModel, prm, L, hist_pt, bf16_pt, q, kd, vd, mask, s
         seg, kk, vv = P.gather_request(pm, L, hist_pt, bf16_pt, heads=[h], params=prm)
         hist = np.array([s == "history" for s in seg] + [False] * n, bool)
         k, v = np.concatenate([kk[:, 0], kd[:, h]]), np.concatenate([vv[:, 0], vd[:, h]])
-        k[hist], v[hist] = k[hist].astype(np.float16), v[hist].astype(np.float16)
+        unit = np.ones(q.shape[2])
+        if compact:                                        # the grids' steps, of the larger one
+            unit = np.repeat(prm[h].tau_k.reshape(2, -1).max(1), 64).astype(np.float32)
+            unit = unit / unit.max()
+        else:
+            k[hist], v[hist] = k[hist].astype(np.float16), v[hist].astype(np.float16)
         rk = composite_rotation(np.asarray(prm[h].u_k, np.float64))
         for i in range(n):
             see = np.concatenate([np.ones(L, bool), mask[i]])
             for e in range(h * gq, (h + 1) * gq):
                 qr = (q[i, e] @ rk).astype(np.float32)
                 scale = 2.0 ** (10 - np.frexp(np.abs(qr).max())[1])
-                qr = (qr * np.float32(scale)).astype(np.float16).astype(np.float64) / scale
+                qr = (qr * (np.float32(scale) * unit)).astype(np.float16).astype(np.float64) / (scale * unit)
                 x = np.where(hist, k @ qr, k @ q[i, e])[see] * sm_scale
                 p = np.exp(x - x.max())
                 p /= p.sum()
