@@ -73,7 +73,7 @@ constexpr int kOffMeta = kOffPid + kPids * 4;
 constexpr int kOffJoin = kOffMeta + kStages * kMetaStage;   // [2 streams][128 rows] (M, l)
 constexpr int kOffF = kOffJoin + 2 * kRows * 8;    // [256 rows] factor of a row's logits
 constexpr int kOffInfo = kOffF + 2 * kRows * 4;    // what the roles read about the slot: kI*
-constexpr int kIPages = 0, kIRest = 4, kIFirst = 8, kILen = 12, kINodes = 16, kILive = 20;
+constexpr int kIPages = 0, kIRest = 4, kIFirst = 8, kILen = 12, kINodes = 16, kILive = 20, kISeen = 24;
 constexpr int kOffBar = kOffInfo + 32;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages, kBKFull = kBMeta + kStages,
               kBVFull = kBKFull + kBufs, kBKFree = kBVFull + kBufs, kBVFree = kBKFree + kBufs, kBSDone = kBVFree + kBufs,
@@ -477,7 +477,7 @@ struct Near {
   const __nv_bfloat16 *k, *v;
   size_t step;
   int rows;
-  bool draft;
+  int draft;                                       // the page of the drafts, -1: a BF16 page
 };
 // one of the bf16 values of a word is a NaN or an infinity
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return __vcmpeq2(x & 0x7F807F80u, 0x7F807F80u); }
@@ -508,7 +508,7 @@ __device__ __forceinline__ bool keys_bf16(const Ctx c, int* status, int e, int n
         bad |= nonfinite2(x[k][j].x) | nonfinite2(x[k][j].y) | nonfinite2(x[k][j].z) | nonfinite2(x[k][j].w);
         sts128(c.base + kOffK + b * kKBytes + (t >> 3) * kSboK + ck * 128 + (t & 7) * 16, x[k][j]);
       }
-    if (bad != 0u && p.draft) flag(status, OSCAR_STATUS_NONFINITE);
+    if (bad != 0u && p.draft >= 0) flag(status, OSCAR_STATUS_NONFINITE);
     fence_async();
     c.arrive(kBKFull + b);
   }
@@ -547,7 +547,7 @@ __device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int
             asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(c.base + kOffPid + 8 * i + 4 * (row >> 5)), "r"(1u << (row & 31)) : "memory");
             x[k][t] = 0u;
           }
-      if (p.draft) flag(status, OSCAR_STATUS_NONFINITE);
+      if (p.draft >= 0) flag(status, OSCAR_STATUS_NONFINITE);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -650,25 +650,33 @@ __device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w,
   return true;
 }
 
+// The sink and the recent pages that hold tokens of a request.
+__device__ __forceinline__ int near_sink(const LayerView& lv, int L) { return (min(L, lv.sink) + kP - 1) / kP; }
+__device__ __forceinline__ int near_recent(const LayerView& lv, int L) { return (min(max(L - lv.sink, 0), lv.recent) + kP - 1) / kP; }
+
 // The BF16 and draft pages of a slot.
 struct NearPages {
   const LayerView& lv;
   const TreeArgs& a;
   int b, h, p0, L, nodes;
+  int seen, n;                                     // the draft pages, the last of the slot's n pages
   __device__ __forceinline__ Near operator()(int i) const {
-    const int u = p0 + i, nbf = (lv.sink + lv.recent) / kP;
-    Near r = {nullptr, nullptr, (size_t)kD, 0, u >= nbf};
-    if (u >= nbf) {
-      const size_t at = (((size_t)b * a.T + (u - nbf) * kP) * lv.hkv + h) * kD;
+    const int held = n - __popc(seen);
+    Near r = {nullptr, nullptr, (size_t)kD, 0, i < held ? -1 : 0};
+    if (i >= held) {
+      int bits = seen;
+      for (int k = i - held; k > 0; --k) bits &= bits - 1;
+      r.draft = __ffs(bits) - 1;
+      const size_t at = (((size_t)b * a.T + r.draft * kP) * lv.hkv + h) * kD;
       r.k = a.kd + at;
       r.v = a.vd + at;
       r.step = (size_t)lv.hkv * kD;
-      r.rows = min(kP, nodes - (u - nbf) * kP);
+      r.rows = min(kP, nodes - r.draft * kP);
       return r;
     }
-    const int rows = u < lv.sink / kP ? min(L, lv.sink) - u * kP : min(max(L - lv.sink, 0), lv.recent) - (u - lv.sink / kP) * kP;
-    if (rows <= 0) return r;
-    const int id = a.bf16_pt[(size_t)b * nbf + u];
+    const int ns = near_sink(lv, L), u = p0 + i, page = u < ns ? u : lv.sink / kP + u - ns, nbf = (lv.sink + lv.recent) / kP;
+    const int rows = u < ns ? min(L, lv.sink) - u * kP : min(L - lv.sink, lv.recent) - (u - ns) * kP;
+    const int id = a.bf16_pt[(size_t)b * nbf + page];
     if (id < 0 || id >= lv.n_bf16) {
       if ((threadIdx.x & 31) == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
       return r;
@@ -744,7 +752,8 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
   const bool hist = (int)blockIdx.x < a.nsplit;
   const int n = (int)lds32(info + kIPages), all = (int)lds32(info + kILive);
   c.rest = (int)lds32(info + kIRest);
-  const NearPages near = {lv, a, (int)blockIdx.z, h, (int)lds32(info + kIFirst), (int)lds32(info + kILen), (int)lds32(info + kINodes)};
+  const NearPages near = {lv, a, (int)blockIdx.z, h, (int)lds32(info + kIFirst), (int)lds32(info + kILen), (int)lds32(info + kINodes),
+                          (int)lds32(info + kISeen), n};
   bool ok = !c.failed();
   if (w < kRowWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
@@ -755,11 +764,11 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
       if (ok && hist) {
         ok = rows_history<WIDE>(c, e, n, F, m, lsum);
       } else if (ok) {
-        const int node = (qt * kRows + row) >> a.gq_log2, nbf = (lv.sink + lv.recent) / kP;
+        const int node = (qt * kRows + row) >> a.gq_log2;
         auto bits = [&](int i) -> unsigned long long {
           const Near p = near(i);
           unsigned long long see = p.rows >= kP ? ~0ull : (1ull << p.rows) - 1ull;
-          if (p.draft) see &= row < live ? a.mask[((size_t)blockIdx.z * a.T + node) * a.W + (near.p0 + i - nbf)] : 0ull;
+          if (p.draft >= 0) see &= row < live ? a.mask[((size_t)blockIdx.z * a.T + node) * a.W + p.draft] : 0ull;
           return see;
         };
         ok = rows_bf16<WIDE>(c, e, n, F, bits, m, lsum);
@@ -869,8 +878,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     if (tid == 0 && slot == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
     Lh = np * kP;
   }
-  const int near_pages = (lv.sink + lv.recent) / kP + (nodes + kP - 1) / kP;
-  int p0, n;                                       // first page and number of pages of the slot
+  int p0, n, seen = 0;                             // first page and number of pages of the slot; draft pages: a bit each
   if (hist) {
     const int slots = tree_hist_slots(a, np);
     if (slot >= slots) return leave();             // a shorter request: the merge knows
@@ -878,8 +886,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     p0 = slot * n + min(slot, np - slots * n);
     n += slot < np - slots * n;
   } else {
-    p0 = (slot - a.nsplit) * near_pages / a.nb;
-    n = (slot - a.nsplit + 1) * near_pages / a.nb - p0;
+    // a share of the BF16 and draft pages that hold tokens; of the draft pages those that some row of this CTA sees
+    const int held = near_sink(lv, L) + near_recent(lv, L), pages = held + (nodes + kP - 1) / kP;
+    p0 = (slot - a.nsplit) * pages / a.nb;
+    const int p1 = (slot - a.nsplit + 1) * pages / a.nb, d0 = max(p0 - held, 0), d1 = max(p1 - held, 0);
+    const int node = (Q0 >> gq_log2) + tid;
+    const bool mine = node <= (Q0 + live - 1) >> gq_log2;
+    unsigned long long words[kMaxDraft / kP];
+#pragma unroll
+    for (int d = 0; d < kMaxDraft / kP; ++d) words[d] = mine && d >= d0 && d < d1 ? a.mask[((size_t)b * a.T + node) * a.W + d] : 0ull;
+    n = max(min(p1, held) - p0, 0);
+#pragma unroll
+    for (int d = 0; d < kMaxDraft / kP; ++d) {
+      if (d < d0 || d >= d1) continue;
+      const int rows = nodes - d * kP;             // bits from n_draft on are ignored
+      if (__syncthreads_or((words[d] & (rows >= kP ? ~0ull : (1ull << rows) - 1ull)) != 0ull)) {
+        seen |= 1 << d;
+        ++n;
+      }
+    }
   }
 
   if (w == kLoadWarp) {
@@ -906,6 +931,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       sts32(info + kILen, (uint32_t)L);
       sts32(info + kINodes, (uint32_t)nodes);
       sts32(info + kILive, (uint32_t)live);
+      sts32(info + kISeen, (uint32_t)seen);
     }
     __syncwarp();
   } else if (w >= kKWarp0 && w < kMmaWarp) {
