@@ -67,13 +67,17 @@ constexpr int kOffPid = kOffRing + kStages * kBlockBytes;
 // BF16 slots keep no page ids; the same bytes hold a bit set per page of the value rows that are not finite
 constexpr int kPoisonTiles = kPids / 2;
 static_assert(kMaxTreeBf16Pages + kMaxDraft / kP <= kPoisonTiles, "a set for every BF16 and draft page");
+// and the ring holds those slots' page descriptors: page id, or -1 - draft page, and rows
+constexpr int kOffNear = kOffRing;
+static_assert(8 * kPoisonTiles <= kStages * kBlockBytes, "a descriptor for every BF16 and draft page");
+constexpr int kWarm = 8;                           // BF16 and draft pages that are asked for at the start
 // [stage][group][scale, zero][32 token pairs in the order of the values' k positions], fp16 pairs
 constexpr int kMetaStage = 2 * 2 * 32 * 4;
 constexpr int kOffMeta = kOffPid + kPids * 4;
 constexpr int kOffJoin = kOffMeta + kStages * kMetaStage;   // [2 streams][128 rows] (M, l)
 constexpr int kOffF = kOffJoin + 2 * kRows * 8;    // [256 rows] factor of a row's logits
 constexpr int kOffInfo = kOffF + 2 * kRows * 4;    // what the roles read about the slot: kI*
-constexpr int kIPages = 0, kIRest = 4, kIFirst = 8, kILen = 12, kINodes = 16, kILive = 20, kISeen = 24;
+constexpr int kIPages = 0, kIRest = 4, kILive = 8;
 constexpr int kOffBar = kOffInfo + 32;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBMeta = kBEmpty + kStages, kBKFull = kBMeta + kStages,
               kBVFull = kBKFull + kBufs, kBKFree = kBVFull + kBufs, kBVFree = kBKFree + kBufs, kBSDone = kBVFree + kBufs,
@@ -479,36 +483,40 @@ struct Near {
   int rows;
   int draft;                                       // the page of the drafts, -1: a BF16 page
 };
-// one of the bf16 values of a word is a NaN or an infinity
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return __vcmpeq2(x & 0x7F807F80u, 0x7F807F80u); }
+// bits 15 and 31: the bf16 value of that half is a NaN or an infinity (its exponent carries)
+__device__ __forceinline__ uint32_t exponents(uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; }
+constexpr uint32_t kNonfinite = 0x80008000u;
 
 // ---- key warps, BF16 pages (natural channel order) -----------------------------------------------------
 template <typename Page>
 __device__ __forceinline__ bool keys_bf16(const Ctx c, int* status, int e, int n, Page page) {
-  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, kw = (threadIdx.x >> 5) & 3, t0 = (lane & 7) + 8 * kw;
+  const uint32_t dst0 = c.base + kOffK + kw * kSboK + (lane & 7) * 16 + (lane >> 3) * 128;
 #pragma unroll 1
   for (int i = e; i < n; i += 2) {
     const int b = i % kBufs;
     const Near p = page(i);
     uint4 x[2][4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.k + (t0 + 32 * k) * p.step) + (lane >> 3);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = (lane & 7) + 8 * (kw + 4 * k), ck = (lane >> 3) + 4 * j;
-        x[k][j] = t < p.rows ? *reinterpret_cast<const uint4*>(p.k + t * p.step + 8 * ck) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int j = 0; j < 4; ++j) x[k][j] = t0 + 32 * k < p.rows ? src[4 * j] : make_uint4(0u, 0u, 0u, 0u);
+    }
     if (i >= kBufs && !c.wait(kBKFree + b, i / kBufs - 1)) return false;
-    uint32_t bad = 0u;
+    if (p.draft >= 0) {
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bad |= exponents(x[k][j].x) | exponents(x[k][j].y) | exponents(x[k][j].z) | exponents(x[k][j].w);
+      if ((bad & kNonfinite) != 0u) flag(status, OSCAR_STATUS_NONFINITE);
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = (lane & 7) + 8 * (kw + 4 * k), ck = (lane >> 3) + 4 * j;
-        bad |= nonfinite2(x[k][j].x) | nonfinite2(x[k][j].y) | nonfinite2(x[k][j].z) | nonfinite2(x[k][j].w);
-        sts128(c.base + kOffK + b * kKBytes + (t >> 3) * kSboK + ck * 128 + (t & 7) * 16, x[k][j]);
-      }
-    if (bad != 0u && p.draft >= 0) flag(status, OSCAR_STATUS_NONFINITE);
+      for (int j = 0; j < 4; ++j)
+        sts128(dst0 + b * kKBytes + 4 * k * kSboK + 4 * j * 128, x[k][j]);
     fence_async();
     c.arrive(kBKFull + b);
   }
@@ -523,44 +531,49 @@ __device__ __forceinline__ bool values_bf16(const Ctx c, int* status, int e, int
   for (int i = e; i < n; i += 2) {
     const int b = i % kBufs;
     const Near p = page(i);
-    uint32_t x[4][8];                              // [token octet, channel half][token]: channels 2 cp, 2 cp + 1
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
+    bool mine = i < kBufs;                         // the buffer is free
+#pragma unroll 1
+    for (int o = vw; o < kP / 8; o += 4) {         // token octets; a small loop: a slot runs it a few times only
+      uint32_t x[2][8];                            // [channel half][token]: channels 2 cp, 2 cp + 1
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.v + 8 * o * p.step) + lane;
+      uint32_t bad = 0u;
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const int row = 8 * (vw + 4 * (k >> 1)) + t, cp = lane + 32 * (k & 1);
-        x[k][t] = row < p.rows ? *reinterpret_cast<const uint32_t*>(p.v + row * p.step + 2 * cp) : 0u;
+        const bool in = 8 * o + t < p.rows;
+        x[0][t] = in ? src[0] : 0u;
+        x[1][t] = in ? src[32] : 0u;
+        src += p.step >> 1;
       }
-    if (i >= kBufs && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
-    uint32_t bad = 0u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int t = 0; t < 8; ++t) bad |= nonfinite2(x[k][t]);
-    if (bad != 0u) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int t = 0; t < 8; ++t) bad |= exponents(x[0][t]) | exponents(x[1][t]);
+      if ((bad & kNonfinite) != 0u) {
+        uint32_t rows = 0u;
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-          if (nonfinite2(x[k][t])) {
-            const int row = 8 * (vw + 4 * (k >> 1)) + t;
-            asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(c.base + kOffPid + 8 * i + 4 * (row >> 5)), "r"(1u << (row & 31)) : "memory");
-            x[k][t] = 0u;
-          }
-      if (p.draft >= 0) flag(status, OSCAR_STATUS_NONFINITE);
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int o = vw + 4 * (k >> 1), ch = 2 * (lane + 32 * (k & 1));
-      const uint32_t d = c.base + kOffV + b * kVBytes + (ch >> 3) * kSboVNear + o * 128 + (ch & 7) * 16;
-      uint32_t lo[4], hi[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        lo[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x5410);
-        hi[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x7632);
+          for (int k = 0; k < 2; ++k)
+            if ((exponents(x[k][t]) & kNonfinite) != 0u) {
+              rows |= 1u << t;
+              x[k][t] = 0u;
+            }
+        asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(c.base + kOffPid + 8 * i + 4 * (o >> 2)), "r"(rows << (8 * (o & 3))) : "memory");
+        if (p.draft >= 0) flag(status, OSCAR_STATUS_NONFINITE);
       }
-      sts128(d, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      sts128(d + 16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      if (!mine && !c.wait(kBVFree + b, i / kBufs - 1)) return false;
+      mine = true;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int ch = 2 * (lane + 32 * k);
+        const uint32_t d = c.base + kOffV + b * kVBytes + (ch >> 3) * kSboVNear + o * 128 + (ch & 7) * 16;
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          lo[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x5410);
+          hi[t] = __byte_perm(x[k][2 * t], x[k][2 * t + 1], 0x7632);
+        }
+        sts128(d, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        sts128(d + 16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      }
     }
     fence_async();
     c.arrive(kBVFull + b);
@@ -654,39 +667,45 @@ __device__ __forceinline__ bool control(const Ctx c, const LayerView& lv, int w,
 __device__ __forceinline__ int near_sink(const LayerView& lv, int L) { return (min(L, lv.sink) + kP - 1) / kP; }
 __device__ __forceinline__ int near_recent(const LayerView& lv, int L) { return (min(max(L - lv.sink, 0), lv.recent) + kP - 1) / kP; }
 
-// The BF16 and draft pages of a slot.
+// The BF16 and draft pages of a slot, by the descriptors that the start has left in shared memory.
 struct NearPages {
   const LayerView& lv;
   const TreeArgs& a;
-  int b, h, p0, L, nodes;
-  int seen, n;                                     // the draft pages, the last of the slot's n pages
+  uint32_t base;
+  int b, h;
   __device__ __forceinline__ Near operator()(int i) const {
-    const int held = n - __popc(seen);
-    Near r = {nullptr, nullptr, (size_t)kD, 0, i < held ? -1 : 0};
-    if (i >= held) {
-      int bits = seen;
-      for (int k = i - held; k > 0; --k) bits &= bits - 1;
-      r.draft = __ffs(bits) - 1;
+    const uint2 d = lds64(base + kOffNear + 8 * i);
+    const int id = (int)d.x;
+    Near r = {nullptr, nullptr, (size_t)kD, (int)d.y, id < 0 ? -1 - id : -1};
+    if (id < 0) {
       const size_t at = (((size_t)b * a.T + r.draft * kP) * lv.hkv + h) * kD;
       r.k = a.kd + at;
       r.v = a.vd + at;
       r.step = (size_t)lv.hkv * kD;
-      r.rows = min(kP, nodes - r.draft * kP);
-      return r;
+    } else {
+      r.k = bf16_row(lv, id, h, 0, 0);
+      r.v = bf16_row(lv, id, h, 1, 0);
     }
-    const int ns = near_sink(lv, L), u = p0 + i, page = u < ns ? u : lv.sink / kP + u - ns, nbf = (lv.sink + lv.recent) / kP;
-    const int rows = u < ns ? min(L, lv.sink) - u * kP : min(L - lv.sink, lv.recent) - (u - ns) * kP;
-    const int id = a.bf16_pt[(size_t)b * nbf + page];
-    if (id < 0 || id >= lv.n_bf16) {
-      if ((threadIdx.x & 31) == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
-      return r;
-    }
-    r.k = bf16_row(lv, id, h, 0, 0);
-    r.v = bf16_row(lv, id, h, 1, 0);
-    r.rows = min(kP, rows);
     return r;
   }
 };
+// Descriptor of page i of n; p0: the slot's first page, seen: its draft pages, the last of the n.
+__device__ __forceinline__ uint2 describe_page(const LayerView& lv, const TreeArgs& a, int b, int i, int n, int p0, int seen, int L,
+                                               int nodes) {
+  const int held = n - __popc(seen);
+  if (i >= held) {
+    int bits = seen;
+    for (int k = i - held; k > 0; --k) bits &= bits - 1;
+    const int d = __ffs(bits) - 1;
+    return make_uint2((uint32_t)(-1 - d), (uint32_t)min(kP, nodes - d * kP));
+  }
+  const int ns = near_sink(lv, L), u = p0 + i, page = u < ns ? u : lv.sink / kP + u - ns, nbf = (lv.sink + lv.recent) / kP;
+  const int rows = u < ns ? min(L, lv.sink) - u * kP : min(L - lv.sink, lv.recent) - (u - ns) * kP;
+  const int id = a.bf16_pt[(size_t)b * nbf + page];
+  if (id >= 0 && id < lv.n_bf16) return make_uint2((uint32_t)id, (uint32_t)min(kP, rows));
+  flag(lv.status, OSCAR_STATUS_BAD_PAGE);
+  return make_uint2(0u, 0u);                       // no rows of it are read
+}
 
 // Partials of a slot, thread = row. One tile: the streams' O joined, a warpgroup per half of the channels; both streams'
 // row warps meet first (each has waited for its stream's last product). Two tiles: a warpgroup each. A CTA that failed
@@ -752,8 +771,7 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
   const bool hist = (int)blockIdx.x < a.nsplit;
   const int n = (int)lds32(info + kIPages), all = (int)lds32(info + kILive);
   c.rest = (int)lds32(info + kIRest);
-  const NearPages near = {lv, a, (int)blockIdx.z, h, (int)lds32(info + kIFirst), (int)lds32(info + kILen), (int)lds32(info + kINodes),
-                          (int)lds32(info + kISeen), n};
+  const NearPages near = {lv, a, c.base, (int)blockIdx.z, h};
   bool ok = !c.failed();
   if (w < kRowWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
@@ -927,11 +945,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       const uint32_t info = c.base + kOffInfo;
       sts32(info + kIPages, (uint32_t)n);
       sts32(info + kIRest, (uint32_t)(Lh - p0 * kP));
-      sts32(info + kIFirst, (uint32_t)p0);
-      sts32(info + kILen, (uint32_t)L);
-      sts32(info + kINodes, (uint32_t)nodes);
       sts32(info + kILive, (uint32_t)live);
-      sts32(info + kISeen, (uint32_t)seen);
     }
     __syncwarp();
   } else if (w >= kKWarp0 && w < kMmaWarp) {
@@ -946,8 +960,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
         }
         sts32(c.base + kOffPid + 4 * k, (uint32_t)id);
       }
-    } else {                                       // the tiles' sets of non-finite rows
-      for (int k = at; k < 2 * n; k += step) sts32(c.base + kOffPid + 4 * k, 0u);
+    } else {                                       // the pages' descriptors and sets of non-finite rows
+      for (int k = at; k < n; k += step) {
+        const uint2 d = describe_page(lv, a, b, k, n, p0, seen, L, nodes);
+        sts32(c.base + kOffNear + 8 * k, d.x);
+        sts32(c.base + kOffNear + 8 * k + 4, d.y);
+        sts32(c.base + kOffPid + 8 * k, 0u);
+        sts32(c.base + kOffPid + 8 * k + 4, 0u);
+      }
     }
   }
   // q staged where the values go, the rotation's A operand (BF16 pages: the second tile where it is used); each row's
@@ -1046,6 +1066,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
         tmem_wait_st();
         if (WIDE) fence_async();
       }
+    }
+  } else if (ok && n > 0 && w >= kKWarp0 && w < kMmaWarp) {
+    // the first pages' rows on their way to L2, and their addresses known to the SM, before the unpacking loads them
+    const NearPages near = {lv, a, c.base, b, h};
+    for (int k = (tid - 32 * kKWarp0) >> 2; k < min(n, kWarm) * 2 * kP; k += 8 * (kMmaWarp - kKWarp0)) {
+      const Near p = near(k / (2 * kP));
+      const int t = k & (kP - 1);
+      const __nv_bfloat16* at = ((k & kP) != 0 ? p.v : p.k) + t * p.step + 32 * (tid & 3);
+      if (t < p.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
     }
   } else if (ok && n > 0 && w < (WIDE ? kRowWarps / 2 : kRowWarps)) {
     const uint32_t trow = c.tmem + ((uint32_t)(32 * (w & 3)) << 16);
