@@ -313,10 +313,8 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
   for (int i = WIDE ? 0 : e; i < n; i += WIDE ? 1 : 2) {
     const int ph = WIDE ? i : i >> 1;
     const unsigned long long see = bits(i);
-    if (!c.wait(kBSDone + e, ph) || !c.wait(kBVFull + i % kBufs, i / kBufs)) return false;
+    if (!c.wait(kBSDone + e, ph)) return false;
     tc_fence_after();
-    const uint2 bad = lds64(c.base + kOffPid + 8 * i);
-    if ((uint32_t)see & bad.x || (uint32_t)(see >> 32) & bad.y) l = NAN;   // a NaN or infinity among the values the row sees
     float mx = -INFINITY;
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {
@@ -337,11 +335,10 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
     }
     l *= al;
     const float mF = m == -INFINITY ? 0.f : m * F;
-    uint32_t lo[32];                               // p = hi + lo, pairs of tokens 2j, 2j + 1
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {                  // p = hi + lo, pairs of tokens 2j, 2j + 1; lo over logits already read
       float s[32];
-      uint32_t hi[16];
+      uint32_t hi[16], lo[16];
       tmem_ld32(ts + 32 * q, s);
       const uint32_t mine = (uint32_t)(see >> (32 * q));
 #pragma unroll
@@ -350,11 +347,14 @@ __device__ __forceinline__ bool rows_bf16(const Ctx c, int e, int n, float F, Bi
         const float y = mine >> (2 * j + 1) & 1u ? fast_exp2(fmaf(s[2 * j + 1], F, -mF)) : 0.f;
         l += x + y;
         hi[j] = pack_bf16x2(x, y);
-        lo[16 * q + j] = pack_bf16x2(x - __uint_as_float(hi[j] << 16), y - __uint_as_float(hi[j] & 0xffff0000u));
+        lo[j] = pack_bf16x2(x - __uint_as_float(hi[j] << 16), y - __uint_as_float(hi[j] & 0xffff0000u));
       }
       tmem_st16(tp + 16 * q, hi);
+      tmem_st16(ts + 16 * q, lo);
     }
-    tmem_st32u(ts, lo);
+    if (!c.wait(kBVFull + i % kBufs, i / kBufs)) return false;   // last: the values take longer than the keys
+    const uint2 bad = lds64(c.base + kOffPid + 8 * i);
+    if ((uint32_t)see & bad.x || (uint32_t)(see >> 32) & bad.y) l = NAN;   // a NaN or infinity among the values the row sees
     tmem_wait_st();
     tc_fence_before();
     c.arrive(kBPReady + e);
