@@ -1150,12 +1150,16 @@ int configure_fmt() {
 
 // Slots of a query row: the history over nsplit of them, the BF16 and draft pages over nb. One CTA runs on an SM at a
 // time; its start (rotation of the rows, first pages) and its end cost about as much as kFixed history pages, a BF16
-// page, which is not pipelined as deeply, about as much as kNear. The counts that need the fewest waves times pages
-// win, and of equal ones those with the fewest slots, which the merge reads. The host knows the page tables' width
-// only: a request shorter than that is spread over as many slots as its own pages fill, *pps each.
+// page, which is not pipelined as deeply, about as much as kNear. If the CTAs fit the SMs at once, the longest of them is
+// the time; else the work of an SM and, since CTAs come whole, one more of the longest. The host knows the page tables'
+// width only (a request shorter than that is spread over as many slots as its own pages fill, *pps each), so the time
+// counts for kFull with all of several requests as long as the tables are wide, and else with kFill of that. The counts
+// of least time win, and of equal ones those with the fewest slots, which the merge reads. (Counting full waves of the
+// longest CTA: 4 requests x 5 nodes over 5K-30K tokens 78 us instead of 66, 5 x 60 over 3K-9K 85 instead of 69, 8 x 133
+// over 98 80 instead of 61; kFull 1: 95, 86, 60; kFull 0: 2 x 17 over 33K 107 instead of 80.)
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
                  int* nb, int* pps) {
-  constexpr double kFixed = 20.0, kNear = 5.0;
+  constexpr double kFixed = 20.0, kNear = 5.0, kFull = 0.35, kFill = 0.75;
   const int tiles = tree_tiles(T, gq);
   const long units = (long)B * hkv * (tree_wide(T, gq) ? (tiles + 1) / 2 : tiles);
   const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
@@ -1163,11 +1167,13 @@ void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int
   *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
   *pps = 1;
   const int least = (pages + kPids - 1) / kPids;   // a slot's page ids fit shared memory
+  // more than four waves of CTAs gain nothing
+  const int most_slots = std::max(least, std::min(pages, (int)std::min<long>(2 * sms, 4 * sms / units + 1)));
   for (int m = 1; m <= near && m < max_slots; ++m)
-    for (int s = least; s <= std::max(least, std::min(pages, 2 * sms)) && s + m <= max_slots; ++s) {
-      const long waves = (units * (s + m) + sms - 1) / sms;
-      const double work = std::max((double)((pages + s - 1) / s), kNear * ((near + m - 1) / m));
-      const double cost = (double)waves * (work + kFixed) + 0.1 * (s + m);
+    for (int s = least; s <= most_slots && s + m <= max_slots; ++s) {
+      const double h = (pages + s - 1) / s + kFixed, g = kNear * ((near + m - 1) / m) + kFixed, longest = std::max(h, g);
+      auto more = [&](double fill) { return units * (fill * s + m) <= sms ? 0.0 : units * (fill * s * h + m * g) / sms; };
+      const double cost = longest + (B > 1 ? kFull * more(1.0) + (1.0 - kFull) * more(kFill) : more(1.0)) + 0.1 * (s + m);
       if (best == 0.0 || cost < best) {
         best = cost;
         *nsplit = s;
