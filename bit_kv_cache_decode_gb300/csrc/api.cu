@@ -803,7 +803,7 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   a.out = out;
   a.out_dtype = out_dtype;
   a.lse = lse;
-  return launch_tree_attention(view(c, layer), a, B, static_cast<cudaStream_t>(stream));
+  return launch_tree_attention(view(c, layer), a, B, c->sms, static_cast<cudaStream_t>(stream));
 }
 
 int oscar_commit_draft(oscar_cache* c, int layer, int B, int T, const void* k_draft, const void* v_draft,

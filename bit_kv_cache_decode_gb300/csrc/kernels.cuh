@@ -123,7 +123,7 @@ struct TreeArgs;
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
                  int* nb, int* pps);
 int configure_tree_kernels();
-int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
+int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, int sms, cudaStream_t st);
 int launch_commit_draft(const LayerView& lv, int B, int T, const void* k, const void* v, const int* seq_lens,
                         const int* n_accept, int max_accept, const int* path, const int* hist_pt, int max_hist_pages,
                         const int* bf16_pt, int sms, cudaStream_t st);

@@ -58,7 +58,7 @@ __device__ __forceinline__ float* tree_part(const LayerView& lv, const TreeArgs&
   return a.partials + ((((size_t)b * tiles + qt) * lv.hkv + h) * (a.nsplit + a.nb) + slot) * a.rows * kPartFloats;
 }
 
-int launch_tree_merge(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st);
+int launch_tree_merge(const LayerView& lv, const TreeArgs& a, int B, int sms, cudaStream_t st);
 int configure_tree_merge();
 
 }  // namespace oscar

@@ -1183,10 +1183,10 @@ void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int
     }
 }
 
-int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
+int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, int sms, cudaStream_t st) {
   const int rc = lv.meta_cb ? launch_fmt<kFmtCB>(lv, a, B, st)
                             : lv.meta_u8 ? launch_fmt<kFmtU8>(lv, a, B, st) : launch_fmt<kFmtF16>(lv, a, B, st);
-  return rc == OSCAR_OK ? launch_tree_merge(lv, a, B, st) : rc;
+  return rc == OSCAR_OK ? launch_tree_merge(lv, a, B, sms, st) : rc;
 }
 
 int configure_tree_kernels() {
