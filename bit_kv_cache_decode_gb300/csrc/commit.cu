@@ -14,9 +14,9 @@
 //
 // Rotation and quantiser are the append's own (rotate_tile16, quantize_pack_row), so the bytes are those of a
 // chain of oscar_append_kv calls. The call moves a few KB per request; its time is latency: the launch, the
-// places, the fragments from L2 and a tile per unit (a tile's rows and fragments from shared memory, its 16 rows'
-// quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 20.5 us (a CTA per 16 tokens of a request: 28.8 us; V fields set row
-// by row: 24.4 us); one request, 3 tokens: 5.7 us.
+// places, the fragments from L2, then a tile for every 16 tokens (its rows and the fragments from shared memory, its 16
+// rows' quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 20.5 us (a CTA per 16 tokens of one request:
+// 28.8 us; V fields set row by row: 24.4 us); one request, 3 tokens: 5.7 us.
 #include <algorithm>
 
 #include "kernels.cuh"

@@ -11,11 +11,12 @@
 // of the new tokens' slots; a slot's page is looked up from the request's table or, for a page popped by this
 // call, from the ring, never from an entry another CTA writes. The last CTA to finish reading writes the new
 // ring positions, which may alias the old ones. The kernel is bound by latency: its launch, the lengths, the scan, a
-// page id. 64 prompts of up to 16K tokens (slots 9 MB): 11.1 us; one prompt of 777: 4.4 us. Up to eight CTAs per SM
+// page id. 64 prompts of up to 16K tokens (slots 9 MB): 10.9 us; one prompt of 777: 4.1 us. Up to eight CTAs per SM
 // hide the slots' lookups (one: 18 us).
 //
 // k_tree_layout. Ancestor sets by pointer doubling: after step k a node's bit set holds its ancestors within
-// 2^k steps, so T nodes take log2 T steps of one OR per word.
+// 2^k steps, so T nodes take log2 T steps of one OR per word. Bound by latency: 26 nodes 2.6 us in a graph, 256 trees of
+// 256 nodes (2.6 MB) 8.6 us.
 #include <algorithm>
 
 #include "kernels.cuh"
