@@ -200,6 +200,28 @@ def test_compact_metadata_rounds_neither_keys_nor_values(T):
     assert (off <= 8.2 * sd + 2.0 ** -18 * np.abs(ref) + 2.0 ** -21).all(), (off / sd).max()
 
 
+def test_many_rows_in_explicit_mode():
+    # enough rows for the merge's 32-row CTAs, of requests with history and without, and a draft that ends inside one
+    lens, hkv, gq, T, B = [700, 90] * 5, 2, 8, 251, 10
+    case = build_decode_case(lens, hkv, gq, 1, seed=68)
+    q, kd, vd = draft(68, B, T, hkv, gq)
+    mask = random_mask(np.random.default_rng(7), B, T, "tree")
+    n = np.array([T, T, 77, 0] + [T] * 6)
+    cache, prm, hp, bp = case
+    out = torch.full((B, T, hkv * gq, 128), -77.0, device=DEV)
+    lse = torch.full((B, T, hkv * gq), -77.0, device=DEV)
+    cache.tree_attention(0, *(to_dev_bf16(x) for x in (q, kd, vd)), torch.from_numpy(mask_words(mask)).to(DEV),
+                         dev(lens), hp, bp, synth.sm_scale(), n_draft=dev(n), out=out, out_dtype=osc.OUT_FP32, lse=lse)
+    assert cache.get_status() == 0
+    for b in range(B):
+        assert (out[b, n[b]:] == -77).all() and (lse[b, n[b]:] == -77).all()
+    few = [1, 2]
+    part = lambda x: np.asarray(x.cpu() if isinstance(x, torch.Tensor) else x)[few]   # noqa: E731
+    compare(out[few], lse[few], (cache, prm, part(hp), part(bp)), [lens[b] for b in few], q[few], kd[few], vd[few], mask[few],
+            n[few], 1, synth.sm_scale())
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[4:]).all()
+
+
 def test_one_node_is_one_decode_step():
     # a single node over the cache and itself, before it is appended: with the recent window not yet full nothing is
     # demoted, so the tokens are those of oscar_decode_step
