@@ -11,8 +11,8 @@
 // of the new tokens' slots; a slot's page is looked up from the request's table or, for a page popped by this
 // call, from the ring, never from an entry another CTA writes. The last CTA to finish reading writes the new
 // ring positions, which may alias the old ones. The kernel is bound by latency: its launch, the lengths, the scan, a
-// page id. 64 prompts of up to 16K tokens (slots 9 MB): 10.9 us; one prompt of 777: 4.1 us. Up to eight CTAs per SM
-// hide the slots' lookups (one: 18 us).
+// page id. 64 prompts of up to 16K tokens (slots 9 MB): 8.0 us; one prompt of 777: 4.2 us. Up to four CTAs per SM
+// hide the slots' lookups (one: 18 us; two: 9.4 us; eight, each with a scan of its own: 11.0 us).
 //
 // k_tree_layout. Ancestor sets by pointer doubling: after step k a node's bit set holds its ancestors within
 // 2^k steps, so T nodes take log2 T steps of one OR per word. Bound by latency: 26 nodes 2.6 us in a graph, 256 trees of
@@ -283,9 +283,9 @@ int launch_build_tables(const oscar_layout& lay, int B, const int* old_lens, con
   a.max_tokens = max_tokens;
   a.status = status;
   a.ticket = ticket;
-  // a CTA per 512 tokens there may be (or per 8 requests), at most eight per SM: each scans all lengths
+  // a CTA per 512 tokens there may be (or per 8 requests), at most four per SM: each scans all lengths
   const int want = std::max(slots != nullptr ? max_tokens / 512 + 1 : 1, (B + 7) / 8);
-  const int grid = std::max(1, std::min(8 * sms, want));
+  const int grid = std::max(1, std::min(4 * sms, want));
   k_build_tables<<<grid, kTabThreads, 3 * (B + 1) * sizeof(int), st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
