@@ -15,8 +15,8 @@
 // Rotation and quantiser are the append's own (rotate_tile16, quantize_pack_row), so the bytes are those of a
 // chain of oscar_append_kv calls. The call moves a few KB per request; its time is latency: the launch, the
 // places, the fragments from L2, then a tile for every 16 tokens (its rows and the fragments from shared memory, its 16
-// rows' quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 20.5 us (a CTA per 16 tokens of one request:
-// 28.8 us; V fields set row by row: 24.4 us); one request, 3 tokens: 5.7 us.
+// rows' quantisers). 64 requests x 1 to 15 tokens x 8 heads, explicit V: 19.7 us (a CTA per 16 tokens of one request:
+// 28.8 us; V fields set row by row: 4 us more); one request, 3 tokens: 5.2 us.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -39,30 +39,29 @@ struct CommitArgs {
 };
 
 constexpr int kWarps = 16;                         // a warp rotates 8 channels of the tile and quantises a row of it
+static_assert(kWarps * 32 == 4 * kD, "a thread for every word of the V fields");
 constexpr int kUnits = 8;                          // units whose places are looked up together
 
-// The 2-bit V fields of a tile's demoted rows, channel-major in their pages. A channel's 64 rows are 16 bytes: thread
-// (channel, half) gathers the fields of the rows in its 8 bytes and sets them with one atomic pair per page (rows of a
-// page follow one another). Atomics, as other rows of the same 8 bytes may be another CTA's. hpage: -1 behind the
-// last demoted row.
+// The 2-bit V fields of a tile's demoted rows, channel-major in their pages: a channel's 64 rows are four words. Thread
+// (channel, word) gathers the fields of the rows in its word and sets them with one atomic pair per page (rows of a page
+// follow one another). Atomics, as other rows of the same word may be another CTA's. hpage: -1 behind the last demoted row.
 __device__ __forceinline__ void set_v_codes(const LayerView& lv, int h, const int* hpage, const int* hrow,
                                             const uint8_t (*codes)[kD / 4]) {
-  const int c = threadIdx.x & (kD - 1), half = threadIdx.x >> 7;
-  unsigned long long mask = 0, value = 0;
-#pragma unroll
+  const int c = threadIdx.x & (kD - 1), word = threadIdx.x >> 7;
+  const uint32_t at_page = v_chan_off(c) + 4 * word;
+  unsigned mask = 0, value = 0;
+#pragma unroll 4
   for (int i = 0; i < kTileRows; ++i) {
     const int page = hpage[i], t = hrow[i];
-    const bool mine = page >= 0 && v_word(t) >> 1 == half;
-    const int sh = 32 * (v_word(t) & 1) + v_bit(t);
-    const unsigned long long code = (codes[i][c >> 2] >> (2 * (c & 3))) & 3u;
-    mask |= mine ? 3ull << sh : 0ull;
-    value |= mine ? code << sh : 0ull;
-    if (i + 1 == kTileRows || hpage[i + 1] != page) {   // alike in all threads
-      if (mask != 0) {
-        auto* at = reinterpret_cast<unsigned long long*>(int2_block_w(lv, page, h) + v_chan_off(c) + 8 * half);
-        atomicAnd(at, ~mask);
-        if (value != 0) atomicOr(at, value);
-      }
+    if (page < 0) break;                           // alike in all threads
+    if (v_word(t) == word) {                       // alike in a warp
+      mask |= 3u << v_bit(t);
+      value |= ((codes[i][c >> 2] >> (2 * (c & 3))) & 3u) << v_bit(t);
+    }
+    if ((i + 1 == kTileRows || hpage[i + 1] != page) && mask != 0) {
+      unsigned* at = reinterpret_cast<unsigned*>(int2_block_w(lv, page, h) + at_page);
+      atomicAnd(at, ~mask);
+      if (value != 0) atomicOr(at, value);
       mask = value = 0;
     }
   }
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_commit_draft(LayerView lv, C
         *reinterpret_cast<uint4*>(bf16_row(lv, s_page[m], h, kind, s_row[m]) + 8 * c8) = x;
       }
       __syncthreads();                             // the tile is free, the codes are complete
-      if (demotes && kind == OSCAR_KIND_V && tid < 2 * kD) set_v_codes(lv, h, s_hpage + t0, s_hrow + t0, codes);
+      if (demotes && kind == OSCAR_KIND_V) set_v_codes(lv, h, s_hpage + t0, s_hrow + t0, codes);
       // the next tile's codes are written after a barrier of its own
     }
     __syncthreads();                               // the places are free
