@@ -183,3 +183,56 @@ def test_verify_steps_from_an_empty_cache():
     assert rings[1] == B * width and rings[3] == 5 * B and (hist == -1).all() and (bf == -1).all()
     assert sorted(fi.tolist()) == list(range(B * width)) and sorted(fb.tolist()) == list(range(5 * B))
     assert c.get_status() == 0
+
+
+def test_verify_step_on_another_stream_and_in_a_graph():
+    # the calls of a step with stream=, and captured and replayed, leave the same bits as in a row on the current stream
+    B, T, hkv, gq = 2, 6, 2, 4
+    cfg = osc.CacheConfig(num_layers=1, num_kv_heads=hkv, num_q_heads=hkv * gq, num_int2_pages=B * 8, num_bf16_pages=5 * B,
+                          max_batch=B, max_splits=16)
+    prm = head_params(81, 0, hkv)
+    rng = np.random.default_rng(9)
+    q = to_dev_bf16(rng.standard_normal((B, T, hkv * gq, 128)) * 0.3)
+    kd, vd = node_rows(90, B, T, hkv)
+    k, v = (to_dev_bf16(x) for x in tokens(85, 0, hkv, 900))
+    parents, path, n = dev([[-1, 0, 0, 1, 3, 2]] * B), dev([[0, 1, 3, 4, 0, 0]] * B), dev([4, 2])
+    plan = osc.RopePlan(128)
+    start, prompt = dev([0, 0]), dev([340, 560])
+
+    def fresh():
+        c = osc.OscarCache(cfg, device=DEV)
+        upload_params(c, 0, prm)
+        s = dict(c=c, hist=torch.full((B, 8), -1, dtype=torch.int32, device=DEV), bf=torch.full((B, 5), -1, dtype=torch.int32, device=DEV),
+                 fi=dev(np.arange(B * 8)), fb=dev(np.arange(5 * B)), rings=dev([0, B * 8, 0, 5 * B]), lens=prompt.clone())
+        _, cu, _ = c.build_tables(start, prompt, s["hist"], s["bf"], s["fi"], s["fb"], s["rings"])
+        c.quantize_prefill(0, k, v, cu, s["hist"], s["bf"])
+        s["new"] = s["lens"] + n
+        return s
+
+    def step(s, stream=None):
+        c = s["c"]
+        c.build_tables(s["lens"], s["new"], s["hist"], s["bf"], s["fi"], s["fb"], s["rings"], stream=stream)
+        mask, pos = c.tree_layout(parents, s["lens"], stream=stream)
+        qr, kr = osc.rope(plan, q.view(B * T, -1, 128), kd.view(B * T, -1, 128), pos.view(-1), stream=stream)
+        s["out"] = c.tree_attention(0, qr.view(q.shape), kr.view(kd.shape), vd, mask, s["lens"], s["hist"], s["bf"], synth.sm_scale(),
+                                    stream=stream)
+        c.commit_draft(0, kr.view(kd.shape), vd, s["lens"], n, s["hist"], s["bf"], path=path, stream=stream)
+
+    plain, other, graphed = fresh(), fresh(), fresh()
+    step(plain)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(other, side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graphed)
+    assert not torch.equal(graphed["c"].pool, plain["c"].pool)   # captured, not run (no page is taken: the rings stay)
+    g.replay()
+    torch.cuda.synchronize()
+    for s in (other, graphed):
+        assert s["c"].get_status() == 0
+        for key in ("hist", "bf", "fi", "fb", "rings", "out"):
+            assert torch.equal(s[key], plain[key]), key
+        assert torch.equal(s["c"].pool, plain["c"].pool)
