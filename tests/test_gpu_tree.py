@@ -377,3 +377,32 @@ def test_streams_and_two_captured_graphs():
     for o, a in zip(outs, alone):
         assert torch.equal(o, a)
     assert cache.get_status() == 0
+
+
+def test_captured_after_a_join_and_after_a_copy():
+    # the call's launch is a programmatic dependent of what is before it on the stream: here two kernels, a copy, a memset
+    lens, hkv, gq, T = [500], 1, 4, 40
+    cache, _, hp, bp = build_decode_case(lens, hkv, gq, 0, seed=69)
+    q, kd, vd = (to_dev_bf16(x) for x in draft(69, 1, T, hkv, gq))
+    words = torch.from_numpy(mask_words(random_mask(np.random.default_rng(8), 1, T, "tree"))).to(DEV)
+    ln, hp, bp = dev(lens), dev(hp), dev(bp)
+    plain = cache.tree_attention(0, q, kd, vd, words, ln, hp, bp, synth.sm_scale())
+    src, zero = q.clone(), torch.zeros_like(q)
+    side, outs = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        q.mul_(0.0)
+        with torch.cuda.stream(side):
+            zero.zero_()
+        main.wait_stream(side)
+        outs.append(cache.tree_attention(0, zero, kd, vd, words, ln, hp, bp, synth.sm_scale()))
+        q.copy_(src)
+        outs.append(cache.tree_attention(0, q, kd, vd, words, ln, hp, bp, synth.sm_scale()))
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert cache.get_status() == 0 and torch.equal(outs[1], plain)
+    assert torch.equal(outs[0], cache.tree_attention(0, zero, kd, vd, words, ln, hp, bp, synth.sm_scale()))
