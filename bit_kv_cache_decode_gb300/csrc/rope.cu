@@ -18,7 +18,8 @@
 // half layout 161 us (whole head). What carried it: streaming loads and stores (206 us with the default policy);
 // short CTAs of 8 tokens (32 tokens: 239 us); two units per thread (one: 166 us; four: 230 us, fewer threads fit);
 // 8 CTAs per SM for the pairs layout (6: 167 us) and 6 for the half layout, whose unit has two parts (8: 171 us);
-// narrower units rather than single elements (head 64, 24 channels rotated in halves: 138 us, elements 364 us).
+// narrower units rather than single elements, and 16 bytes for the channels behind them where those allow it (head 64, 24
+// channels rotated in halves: 99 us, all of it in 8-byte units 138 us, in elements 364 us).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -64,29 +65,37 @@ template <> struct AccessOf<4> { using type = unsigned; };
 template <typename T, int V, bool WIDE> struct alignas(WIDE ? sizeof(T) * V : sizeof(T)) Vec { T v[V]; };
 
 // One head's unit u: half layout: V channels from V u of the first half and their partners; pairs layout: V
-// channels (V / 2 pairs) from V u; units past the rotary part copy V channels. Loading and turning are apart, so that
+// channels (V / 2 pairs) from V u; units past the rotary part copy VP channels. Loading and turning are apart, so that
 // a thread has several units' loads in flight before it stores any (in place, the compiler may not reorder them).
-template <typename T, int V, bool HALF, bool WIDE>
+template <typename T, int V, int VP, bool HALF, bool WIDE>
 struct Unit {
-  using W = Vec<T, V, WIDE>;
-  using Bits = typename AccessOf<WIDE ? sizeof(T) * V : 16>::type;
-  W a, b;
+  Vec<T, VP, WIDE> a;                              // V <= VP: a rotary unit is its first V elements
+  Vec<T, V, WIDE> b;
   // each element is touched once: streaming accesses where they are wide
-  static __device__ __forceinline__ W get(const T* at) {
+  template <int N>
+  static __device__ __forceinline__ void get(T* x, const T* at) {
     if constexpr (WIDE) {
-      const Bits x = __ldcs(reinterpret_cast<const Bits*>(at));
-      return *reinterpret_cast<const W*>(&x);
+      using Bits = typename AccessOf<sizeof(T) * N>::type;
+      *reinterpret_cast<Bits*>(x) = __ldcs(reinterpret_cast<const Bits*>(at));
     } else {
-      return *reinterpret_cast<const W*>(at);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = at[e];
     }
   }
-  static __device__ __forceinline__ void put(T* at, const W& x) {
-    if constexpr (WIDE) __stcs(reinterpret_cast<Bits*>(at), *reinterpret_cast<const Bits*>(&x));
-    else *reinterpret_cast<W*>(at) = x;
+  template <int N>
+  static __device__ __forceinline__ void put(T* at, const T* x) {
+    if constexpr (WIDE) {
+      using Bits = typename AccessOf<sizeof(T) * N>::type;
+      __stcs(reinterpret_cast<Bits*>(at), *reinterpret_cast<const Bits*>(x));
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) at[e] = x[e];
+    }
   }
   __device__ __forceinline__ void load(const T* in, int at, int half, bool rotary) {
-    a = get(in + at);
-    if (HALF && rotary) b = get(in + at + half);
+    if (V == VP || !rotary) get<VP>(a.v, in + at);
+    else get<V>(a.v, in + at);
+    if (HALF && rotary) get<V>(b.v, in + at + half);
   }
   __device__ __forceinline__ void turn(const float2* cs) {
     if (HALF) {
@@ -106,12 +115,13 @@ struct Unit {
     }
   }
   __device__ __forceinline__ void store(T* out, int at, int half, bool rotary) const {
-    put(out + at, a);
-    if (HALF && rotary) put(out + at + half, b);
+    if (V == VP || !rotary) put<VP>(out + at, a.v);
+    else put<V>(out + at, a.v);
+    if (HALF && rotary) put<V>(out + at + half, b.v);
   }
 };
 
-template <typename T, int V, bool HALF, bool WIDE>
+template <typename T, int V, int VP, bool HALF, bool WIDE>
 __global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a) {
   __shared__ float2 table[kRopeTable];             // [token][pair]: (cos, sin) times the scale
   __shared__ int pos_s[kRopeTokens];
@@ -130,13 +140,13 @@ __global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a)
   constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
   constexpr int kBatch = 2;                        // units a thread has in flight
   const int rot_units = HALF ? half / V : a.rot / V;
-  const int units = rot_units + (a.dim - a.rot) / V;
+  const int units = rot_units + (a.dim - a.rot) / VP;
   const int heads = a.q.heads + a.k.heads, items = nt * heads;
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     const bool rotary = u < rot_units;
-    const int at = rotary ? u * V : a.rot + (u - rot_units) * V;
+    const int at = rotary ? u * V : a.rot + (u - rot_units) * VP;
     for (int i0 = threadIdx.y; i0 < items; i0 += kBatch * blockDim.y) {
-      Unit<T, V, HALF, WIDE> x[kBatch];
+      Unit<T, V, VP, HALF, WIDE> x[kBatch];
       T* out[kBatch];
       int tok[kBatch];
 #pragma unroll
@@ -168,37 +178,34 @@ __global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a)
   }
 }
 
-template <typename T, int V, bool HALF, bool WIDE>
+template <typename T, int V, int VP, bool HALF, bool WIDE>
 int launch_as(RopeArgs a, cudaStream_t st) {
   const int half = a.rot / 2;
-  const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / V;
+  const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / VP;
   // two CTAs per SM and more while there are tokens for them
   a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.n / 304));
   const unsigned heads = a.q.heads + a.k.heads;
   a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
-  k_rope<T, V, HALF, WIDE><<<(a.n + a.tokens - 1) / a.tokens, dim3(bx, by), 0, st>>>(a);
+  k_rope<T, V, VP, HALF, WIDE><<<(a.n + a.tokens - 1) / a.tokens, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-// the widest access, of 16 bytes at most, that every row, half and remainder starts on a multiple of; else elements
-template <typename T>
-int launch_typed(const RopeArgs& a, bool half_layout, int bytes, cudaStream_t st) {
-  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), V4 = 4 / sizeof(T);
-  if (half_layout) {
-    if (bytes == 16) return launch_as<T, V16, true, true>(a, st);
-    if (bytes == 8) return launch_as<T, V8, true, true>(a, st);
-    if constexpr (V4 > 1) {
-      if (bytes == 4) return launch_as<T, V4, true, true>(a, st);
-    }
-    return launch_as<T, 1, true, false>(a, st);
-  }
-  if (bytes == 16) return launch_as<T, V16, false, true>(a, st);
-  if (bytes == 8) return launch_as<T, V8, false, true>(a, st);
+// bytes: the widest access, of 16 at most, that every row, half and remainder starts on a multiple of; else elements.
+// Where only the halves are narrower, the channels behind them are copied 16 bytes at a time (copy16).
+template <typename T, bool HALF>
+int launch_layout(const RopeArgs& a, int bytes, bool copy16, cudaStream_t st) {
+  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), V4 = 4 / sizeof(T), kLeast = HALF ? 1 : 2;
+  if (bytes == 16) return launch_as<T, V16, V16, HALF, true>(a, st);
+  if (bytes == 8) return copy16 ? launch_as<T, V8, V16, HALF, true>(a, st) : launch_as<T, V8, V8, HALF, true>(a, st);
   if constexpr (V4 > 1) {
-    if (bytes == 4) return launch_as<T, V4, false, true>(a, st);
+    if (bytes == 4) return copy16 ? launch_as<T, V4, V16, HALF, true>(a, st) : launch_as<T, V4, V4, HALF, true>(a, st);
   }
-  return launch_as<T, 2, false, false>(a, st);
+  return launch_as<T, kLeast, kLeast, HALF, false>(a, st);
+}
+template <typename T>
+int launch_typed(const RopeArgs& a, bool half_layout, int bytes, bool copy16, cudaStream_t st) {
+  return half_layout ? launch_layout<T, true>(a, bytes, copy16, st) : launch_layout<T, false>(a, bytes, copy16, st);
 }
 
 // whether accesses of v elements of `size` bytes fit a tensor's rows
@@ -228,14 +235,16 @@ int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, i
   a.inverse = inverse;
   const bool half_layout = layout == OSCAR_ROPE_HALF;
   const int size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
+  const int v16 = 16 / size;
+  const bool copy16 = fits(q, size, v16) && fits(k, size, v16) && rot % v16 == 0 && (dim - rot) % v16 == 0;
   int bytes = 16;
   for (; bytes > size; bytes /= 2) {
     const int v = bytes / size;
-    if (fits(q, size, v) && fits(k, size, v) && (half_layout ? rot / 2 : rot) % v == 0 && (dim - rot) % v == 0) break;
+    if (fits(q, size, v) && fits(k, size, v) && (half_layout ? rot / 2 : rot) % v == 0 && (copy16 || (dim - rot) % v == 0)) break;
   }
-  if (dtype == OSCAR_DTYPE_FP32) return launch_typed<float>(a, half_layout, bytes, st);
-  if (dtype == OSCAR_DTYPE_FP16) return launch_typed<__half>(a, half_layout, bytes, st);
-  return launch_typed<__nv_bfloat16>(a, half_layout, bytes, st);
+  if (dtype == OSCAR_DTYPE_FP32) return launch_typed<float>(a, half_layout, bytes, copy16, st);
+  if (dtype == OSCAR_DTYPE_FP16) return launch_typed<__half>(a, half_layout, bytes, copy16, st);
+  return launch_typed<__nv_bfloat16>(a, half_layout, bytes, copy16, st);
 }
 
 }  // namespace oscar
