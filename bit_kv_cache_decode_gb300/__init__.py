@@ -465,6 +465,8 @@ class OscarCache:
         dev, st = _here(self.pool)
         sl, hp, bp = _in_i32(seq_lens, dev), _in_i32(hist_pt, dev), _in_i32(bf16_pt, dev)
         nd = None if n_draft is None else _in_i32(n_draft, dev)
+        if q.dim() != 4:
+            raise OscarError(ERR_INVALID_ARG, "oscar_tree_attention")
         B, T = int(q.shape[0]), int(q.shape[1])
         rows = (B, T, self.cfg.num_q_heads, self.cfg.head_dim)
         drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
@@ -505,6 +507,8 @@ class OscarCache:
         sl, na = _in_i32(seq_lens_before, dev), _in_i32(n_accept, dev)
         hp, bp = _in_i32(hist_pt, dev), _in_i32(bf16_pt, dev)
         pa = None if path is None else _in_i32(path, dev)
+        if k_draft.dim() != 4:
+            raise OscarError(ERR_INVALID_ARG, "oscar_commit_draft")
         B, T = int(k_draft.shape[0]), int(k_draft.shape[1])
         drafted = (B, T, self.cfg.num_kv_heads, self.cfg.head_dim)
         _check_like(k_draft, _bf16, drafted, dev, "oscar_commit_draft")

@@ -113,7 +113,7 @@ def test_bad_requests_nodes_and_pages_are_left_out():
     a.commit_draft(0, kd, vd, dev([706, 0, 0, 0, 0]), dev([2, 0, 0, 0, 0]), hp, bp, path=dev(path))
     assert a.get_status() == osc.STATUS_NONFINITE
     for bad in (dict(layer=1), dict(path=dev(path)[:4]), dict(n_accept=dev([1] * 4)), dict(max_accept=9, path=None),
-                dict(k_draft=kd.float()), dict(v_draft=vd[:, :4]), dict(max_accept=0, path=None)):
+                dict(k_draft=kd.float()), dict(k_draft=kd.flatten()), dict(hist_pt=hp.cpu()), dict(v_draft=vd[:, :4]), dict(max_accept=0, path=None)):
         with pytest.raises(osc.OscarError):
             a.commit_draft(**{**dict(layer=0, k_draft=kd, v_draft=vd, seq_lens_before=dev(lens), n_accept=dev([1] * 5),
                                      hist_pt=hp, bf16_pt=bp, path=dev(path)), **bad})

@@ -325,7 +325,8 @@ def test_argument_checks():
     ok = dict(layer=0, q=q, k_draft=kd, v_draft=vd, mask=torch.zeros(1, 3, 1, dtype=torch.int64, device=DEV),
               seq_lens=dev([400]), hist_pt=hp, bf16_pt=bp, sm_scale=0.1)
     cache.tree_attention(**ok)
-    for bad in (dict(layer=1), dict(layer=-1), dict(q=q.float()), dict(q=q[:, :2]), dict(k_draft=kd[:, :2]),
+    for bad in (dict(layer=1), dict(layer=-1), dict(q=q.float()), dict(q=q[:, :2]), dict(q=q.flatten()), dict(q=q.cpu()),
+                dict(seq_lens=dev([400]).cpu()), dict(lse=torch.zeros(1, 3, 4, 1, device=DEV)), dict(k_draft=kd[:, :2]),
                 dict(v_draft=vd.transpose(0, 1)), dict(mask=ok["mask"][:, :2]), dict(mask=ok["mask"].int()),
                 dict(seq_lens=dev([1, 2])), dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(sm_scale=float("inf")),
                 dict(out_dtype=2), dict(n_draft=dev([1, 2])), dict(out=torch.zeros(1, 3, 4, 128, device=DEV)),
