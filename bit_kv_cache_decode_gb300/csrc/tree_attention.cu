@@ -256,8 +256,10 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
     float sum = 0.f;
     bool free_o = ph == 0;                         // O of the stream's last page is complete
     bool redo = __any_sync(0xffffffffu, m == -INFINITY);
+    // Twice at most: the first pass may be for a row of the warp that has no reference yet while the others keep theirs,
+    // so its sums are looked at like any other's; what they raise in the second pass is at the page's maximum.
 #pragma unroll 1
-    for (;;) {
+    for (int pass = 0;; ++pass) {
       if (redo) {                                  // a reference at the rows' maxima: the first page, or weights too large
         float mx = -INFINITY;
 #pragma unroll
@@ -271,9 +273,9 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
         if (!free_o) {
           if (!c.wait(kBODone + e, ph - 1)) return false;
           tc_fence_after();
-          rescale_o(to, al);
           free_o = true;
         }
+        if (ph > 0) rescale_o(to, al);
       }
       // the page's weights against the reference m
       const float mF = m == -INFINITY ? 0.f : fmaf(m, F, -kBias);
@@ -282,7 +284,7 @@ __device__ __forceinline__ bool rows_history(const Ctx c, int e, int n, float F,
       weights32(s0, F2, nm2, r0, t2);
       weights32(s1, F2, nm2, r1, t2);
       sum = t2.x + t2.y;
-      if (redo) break;
+      if (pass > 0) break;
       redo = __any_sync(0xffffffffu, sum > kMostSum);
       if (!redo) break;
     }
@@ -778,7 +780,8 @@ __device__ __forceinline__ void run_roles(const LayerView& lv, const TreeArgs& a
     const int live = WIDE ? min(kRows, all - e * kRows) : all, row = threadIdx.x & (kRows - 1);
     if (32 * (w & 3) < live) {
       const float F = __uint_as_float(lds32(c.base + kOffF + 4 * (WIDE ? e * kRows + row : row)));
-      float m = -INFINITY, lsum = 0.f;
+      // a row whose q is not finite (F is NaN) has NaN weights, whatever the reference: it asks for none
+      float m = hist && F != F ? 0.f : -INFINITY, lsum = 0.f;
       if (ok && hist) {
         ok = rows_history<WIDE>(c, e, n, F, m, lsum);
       } else if (ok) {
@@ -1094,7 +1097,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     }
     tmem_wait_st();
   }
-  if (w < kRowWarps && (WIDE || half == 0)) sts32(c.base + kOffF + 4 * (WIDE ? tid : row), __float_as_uint(F));
+  if (w < kRowWarps && (WIDE || half == 0)) {
+    // a NaN or infinity in q: the whole row is NaN, as its formula's softmax is
+    if (n > 0 && lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >= 0x7F80u) F = NAN;
+    sts32(c.base + kOffF + 4 * (WIDE ? tid : row), __float_as_uint(F));
+  }
   if (!ok) c.fail();
   tc_fence_before();
   __syncthreads();                                 // Q is in; the rotation's operands may be overwritten

@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kTmThreads) k_tree_merge(LayerView lv, TreeArg
   for (int g = 0; g < G; ++g) {
     const int Q = Q0 + kTmRows * g + r, node = Q >> a.gq_log2, hq = h * gq + (Q & (gq - 1));
     if (node >= nodes) continue;                   // rows behind the last node stay as they are
-    const float inv = M[g] == -INFINITY ? 0.f : 1.f / L[g];
+    const bool empty = M[g] == -INFINITY && L[g] == 0.f;   // not: NaN weights, which leave no maximum either
+    const float inv = empty ? 0.f : 1.f / L[g];
     const float4 x = make_float4((hist[g].x + o[g].x) * inv, (hist[g].y + o[g].y) * inv, (hist[g].z + o[g].z) * inv,
                                  (hist[g].w + o[g].w) * inv);
     const size_t orow = ((size_t)b * a.T + node) * lv.hq + hq;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kTmThreads) k_tree_merge(LayerView lv, TreeArg
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * kD + 4 * quad) = u;
     }
     if (a.lse != nullptr && quad == 0)
-      a.lse[orow] = M[g] == -INFINITY ? -INFINITY : (M[g] + log2f(L[g])) * 0.6931471805599453f;
+      a.lse[orow] = empty ? -INFINITY : (M[g] + log2f(L[g])) * 0.6931471805599453f;
   }
 }
 

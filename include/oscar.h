@@ -438,7 +438,8 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  *                     a request and kv head count as a multiple of 8 up to 128 and of 128 above.
  *                     Calls that may overlap need a workspace each.
  * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
- * infinity in a drafted row reaches the rows that attend to it and no others.
+ * infinity in a drafted row reaches the rows that attend to it and no others (NONFINITE); one in a row of q makes that
+ * row's output and lse NaN and touches no other (NONFINITE).
  * The cache is only read; all inputs but the cache's rotations may come from the kernel just before.
  * q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
  * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT, B > 65535, sink + recent above

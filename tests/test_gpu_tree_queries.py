@@ -1,0 +1,85 @@
+"""Tree attention with queries that are not finite, beside rows whose largest logits come late."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import bit_kv_cache_decode_gb300 as osc
+    from gpu_cases import DEV, build_decode_case, to_dev_bf16, tokens
+    from test_gpu_tree import compare, dev, draft
+import synth
+from tree_cases import mask_words, random_mask
+
+PAGES = 24
+
+
+def late_queries(T, hkv, gq, L):
+    """Every row's logits grow along the history: its query follows one token per page, each page's more than the
+    one before, so that a page's largest weight is far more than 2^9 times the first page's."""
+    q, kd, vd = draft(71, 1, T, hkv, gq)
+    k, _ = tokens(71, 0, hkv, L, extra=1)
+    for i in range(T):
+        for h in range(hkv):
+            for e in range(gq):
+                c = 1.5 * (1 + (i + e) % 5)
+                late = k[64 + 64 * (PAGES - 1 - (i % 8)) + 7 * e + 3, h]
+                q[0, i, h * gq + e] = synth.bf16_round(0.02 * c * late)
+    return q, kd, vd
+
+
+@pytest.mark.parametrize("T", [24, 40])                    # rows of one tile and of two
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf, 3.3e38])
+def test_a_bad_query_reaches_no_other_row(T, value):
+    lens, hkv, gq = [64 + 256 + 64 * PAGES + 5], 2, 4
+    case = build_decode_case(lens, hkv, gq, 0, seed=71)
+    cache, _, hp, bp = case
+    q, kd, vd = late_queries(T, hkv, gq, lens[0])
+    mask = random_mask(np.random.default_rng(5), 1, T, "tree")
+    words, sm = torch.from_numpy(mask_words(mask)).to(DEV), synth.sm_scale()
+
+    def run(x):
+        lse = torch.zeros(1, T, hkv * gq, device=DEV)
+        out = cache.tree_attention(0, x, to_dev_bf16(kd), to_dev_bf16(vd), words, dev(lens), hp, bp, sm,
+                                   out_dtype=osc.OUT_FP32, lse=lse)
+        return out, lse
+
+    clean, clean_lse = run(to_dev_bf16(q))
+    assert cache.get_status() == 0
+    compare(clean, clean_lse, case, lens, q, kd, vd, mask, [T], 0, sm)
+    bad = to_dev_bf16(q)
+    hurt = torch.zeros(1, T, hkv * gq, dtype=torch.bool, device=DEV)
+    for i, e in ((1, 0), (7, 2), (T - 1, 5)):              # rows of several warps, of both kv heads
+        hurt[0, i, e] = True
+        if value > 1e38 and np.isfinite(value):            # finite, but its rotation overflows
+            bad[0, i, e] = value
+        else:
+            bad[0, i, e, 40] = value
+    out, lse = run(bad)
+    assert cache.get_status() == (0 if np.isfinite(value) else osc.STATUS_NONFINITE)
+    assert torch.equal(out[~hurt], clean[~hurt]) and torch.equal(lse[~hurt], clean_lse[~hurt])
+    if not np.isfinite(value):
+        assert out[hurt].isnan().all() and lse[hurt].isnan().all()
+
+
+@pytest.mark.parametrize("L", [0, 90])
+def test_a_bad_query_without_history(L):
+    T, hkv, gq = 6, 1, 4
+    case = build_decode_case([max(L, 1)], hkv, gq, 0, seed=72)
+    cache, _, hp, bp = case
+    q, kd, vd = (to_dev_bf16(x) for x in draft(72, 1, T, hkv, gq))
+    mask = np.zeros((1, T, T), bool)
+    mask[0, 1:, 0] = True                                  # node 0 sees no drafted node
+    kd[0, 0, 0, 9] = 2.0
+    q[0, :, 1, 9] = -np.inf                                # every logit of a row that sees node 0 alone is -inf
+    q[0, :, 2, 9] = np.nan
+    lse = torch.zeros(1, T, gq, device=DEV)
+    out = cache.tree_attention(0, q, kd, vd, torch.from_numpy(mask_words(mask)).to(DEV), dev([L]), hp, bp, synth.sm_scale(),
+                               out_dtype=osc.OUT_FP32, lse=lse)
+    assert cache.get_status() == osc.STATUS_NONFINITE
+    sees = torch.arange(T, device=DEV) > 0 if L == 0 else torch.ones(T, dtype=torch.bool, device=DEV)
+    for e in (1, 2):
+        assert out[0, sees, e].isnan().all() and lse[0, sees, e].isnan().all()
+        assert (out[0, ~sees, e] == 0).all() and (lse[0, ~sees, e] == -np.inf).all()
+    assert out[0, :, [0, 3]].isfinite().all() and lse[0, sees][:, [0, 3]].isfinite().all()
