@@ -1168,7 +1168,7 @@ void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int
                  int* nb, int* pps) {
   constexpr double kFixed = 20.0, kNear = 5.0, kFull = 0.35, kFill = 0.75;
   const int tiles = tree_tiles(T, gq);
-  const long units = (long)B * hkv * (tree_wide(T, gq) ? (tiles + 1) / 2 : tiles);
+  const long units = std::max(1L, (long)B * hkv * (tree_wide(T, gq) ? (tiles + 1) / 2 : tiles));   // B may be 0
   const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
   double best = 0.0;
   *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
