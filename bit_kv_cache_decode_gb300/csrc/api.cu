@@ -810,8 +810,9 @@ int oscar_commit_draft(oscar_cache* c, int layer, int B, int T, const void* k_dr
                        const int32_t* seq_lens_before, const int32_t* n_accept, int max_accept, const int32_t* path,
                        const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream) {
   if (!c || layer < 0 || layer >= c->lay.num_layers || B < 0 || T < 1 || max_hist_pages < 0) return OSCAR_ERR_INVALID_ARG;
-  if (max_accept < 1 || max_accept > c->lay.recent || (!path && max_accept > T)) return OSCAR_ERR_INVALID_ARG;
+  if (max_accept < 1 || max_accept > c->lay.recent) return OSCAR_ERR_INVALID_ARG;
   if (B == 0) return OSCAR_OK;
+  if (!path && max_accept > T) return OSCAR_ERR_INVALID_ARG;
   if (!k_draft || !v_draft || !seq_lens_before || !n_accept || !bf16_pt || (max_hist_pages > 0 && !hist_pt))
     return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(k_draft) || !aligned16(v_draft)) return OSCAR_ERR_INVALID_ARG;

@@ -30,3 +30,16 @@ def test_no_requests(T, hq, hkv, pages):
     _, cu, _ = cache.build_tables(i32(0), i32(0), i32(0, pages), i32(0, 5), free, i32(5), rings)
     assert cu.tolist() == [0] and rings.tolist() == [1, 2, 3, 2]
     assert cache.get_status() == 0 and torch.equal(cache.pool, before)
+
+
+@pytest.mark.parametrize("most", [1, 3, 256])
+def test_no_requests_with_paths(most):
+    # more accepted nodes than T are allowed with a path; a path of no requests is a null pointer
+    cache = osc.OscarCache(osc.CacheConfig(num_layers=1, num_kv_heads=1, num_q_heads=1, num_int2_pages=2, num_bf16_pages=5,
+                                           max_batch=1, max_splits=1), device=DEV)
+    i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device=DEV)   # noqa: E731
+    k = torch.zeros(0, 2, 1, 128, dtype=torch.bfloat16, device=DEV)
+    cache.commit_draft(0, k, k, i32(0), i32(0), i32(0, 4), i32(0, 5), path=i32(0, most))
+    with pytest.raises(osc.OscarError):
+        cache.commit_draft(0, k, k, i32(0), i32(0), i32(0, 4), i32(0, 5), path=i32(0, 257))
+    assert cache.get_status() == 0
