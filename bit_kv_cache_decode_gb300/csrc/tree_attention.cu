@@ -1164,20 +1164,29 @@ int configure_fmt() {
 // of least time win, and of equal ones those with the fewest slots, which the merge reads. (Counting full waves of the
 // longest CTA: 4 requests x 5 nodes over 5K-30K tokens 78 us instead of 66, 5 x 60 over 3K-9K 85 instead of 69, 8 x 133
 // over 98 80 instead of 61; kFull 1: 95, 86, 60; kFull 0: 2 x 17 over 33K 107 instead of 80.)
+// The tensor cores' sums truncate, so an accumulator's error grows with the products summed into it. Measured with equal
+// weights over values of one sign, relative to their mean, pages to a slot: 256 0, 512 8e-6, 1,024 2.7e-5, 2,048 1.5e-4,
+// 4,096 5e-4 (two tiles, whose streams take every page: 1.3e-3). A slot therefore takes pages for kProducts MMAs of an
+// accumulator at most (a history page is 4, a BF16 page 8), as far as max_slots allows.
 void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int sms, int max_slots, int* nsplit,
                  int* nb, int* pps) {
   constexpr double kFixed = 20.0, kNear = 5.0, kFull = 0.35, kFill = 0.75;
-  const int tiles = tree_tiles(T, gq);
+  constexpr int kProducts = 1024;
+  const int tiles = tree_tiles(T, gq), streams = tree_wide(T, gq) ? 1 : 2;   // that share a slot's pages
   const long units = std::max(1L, (long)B * hkv * (tree_wide(T, gq) ? (tiles + 1) / 2 : tiles));   // B may be 0
   const int near = nbf + (T + kP - 1) / kP, pages = std::max(1, max_hist_pages);
   double best = 0.0;
   *nsplit = *nb = 0;                               // stays 0 when max_slots is too small
   *pps = 1;
-  const int least = (pages + kPids - 1) / kPids;   // a slot's page ids fit shared memory
+  auto parts = [](int n, int most) { return (n + most - 1) / most; };
+  const int exact_s = parts(pages, streams * kProducts / 4), exact_m = parts(near, streams * kProducts / 8);
+  // at least: a slot's page ids fit shared memory, and what the exact sums take of max_slots
+  const int least_s = std::min(exact_s, std::max(parts(pages, kPids), max_slots - exact_m));
+  const int least_m = std::min(exact_m, std::max(1, max_slots - least_s));
   // more than four waves of CTAs gain nothing
-  const int most_slots = std::max(least, std::min(pages, (int)std::min<long>(2 * sms, 4 * sms / units + 1)));
-  for (int m = 1; m <= near && m < max_slots; ++m)
-    for (int s = least; s <= most_slots && s + m <= max_slots; ++s) {
+  const int most_s = std::max(least_s, std::min(pages, (int)std::min<long>(2 * sms, 4 * sms / units + 1)));
+  for (int m = least_m; m <= near && m < max_slots; ++m)
+    for (int s = least_s; s <= most_s && s + m <= max_slots; ++s) {
       const double h = (pages + s - 1) / s + kFixed, g = kNear * ((near + m - 1) / m) + kFixed, longest = std::max(h, g);
       auto more = [&](double fill) { return units * (fill * s + m) <= sms ? 0.0 : units * (fill * s * h + m * g) / sms; };
       const double cost = longest + (B > 1 ? kFull * more(1.0) + (1.0 - kFull) * more(kFill) : more(1.0)) + 0.1 * (s + m);

@@ -435,8 +435,10 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  *  workspace        : device, 256-byte aligned, of oscar_tree_workspace_bytes(cache, B, T, max_hist_pages) bytes; less
  *                     is accepted and splits the history less, down to two slots of 528 bytes (one more for every
  *                     4,096 history pages beyond the first 4,096) for each query row, where the T Hq / Hkv rows of
- *                     a request and kv head count as a multiple of 8 up to 128 and of 128 above.
- *                     Calls that may overlap need a workspace each.
+ *                     a request and kv head count as a multiple of 8 up to 128 and of 128 above. Slots of more than 512
+ *                     history pages (256 where a kv head has more than 128 rows), which only such a workspace makes,
+ *                     sum so many products into one accumulator that its truncation shows: up to 1.3e-3 of the values'
+ *                     mean at 4,096 pages. Calls that may overlap need a workspace each.
  * Rows of nodes from n_draft[r] on are left as they are. A row that attends to nothing is 0 with lse -inf. A NaN or
  * infinity in a drafted row reaches the rows that attend to it and no others (NONFINITE); one in a row of q makes that
  * row's output and lse NaN and touches no other (NONFINITE).

@@ -33,3 +33,19 @@ def test_an_empty_batch_has_a_plan():
     __graft_entry__.build()
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=__graft_entry__.ROOT)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+@pytest.mark.parametrize("B,T,hkv,gq", [(1, 5, 8, 4), (64, 5, 8, 4), (64, 26, 8, 4), (304, 17, 1, 8), (608, 1, 1, 8), (16, 256, 8, 8)])
+@pytest.mark.parametrize("pages", [1, 511, 513, 2048, 4097, 16384, 200_000])
+@pytest.mark.parametrize("nbf", [5, 129, 2040])
+def test_an_accumulator_takes_1024_products(splits, B, T, hkv, gq, pages, nbf):
+    streams = 1 if T * gq > 128 else 2
+    near = nbf + -(-T // 64)
+    s, m, pps = splits(B, T, hkv, gq, nbf, pages)
+    assert s * pps >= pages and pps <= streams * 256 and -(-near // m) <= streams * 128
+    for slots in (s + m, s + m - 1, 40, 3, 2):               # less workspace: as many as there are, and no refusal
+        least = -(-pages // 4096)
+        s2, m2, p2 = splits(B, T, hkv, gq, nbf, pages, max_slots=slots)
+        assert (s2 == 0) == (least + 1 > slots)
+        if s2:
+            assert s2 + m2 <= slots and s2 * p2 >= pages and p2 <= 4096
