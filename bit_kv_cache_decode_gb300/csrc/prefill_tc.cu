@@ -325,6 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kYBufs * 128) : "memory");
   }
+  // Not before the sink / recent copy, whose CTAs have all started, is complete: a programmatic dependent of this grid
+  // waits for this grid alone.
+  pdl_wait();
 }
 
 // Sink and recent rows of request r, kv head h, one kind: bf16 copies, one warp per row.
@@ -392,8 +395,8 @@ int launch_prefill(const LayerView& lv, int B, const void* k, const void* v, con
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const long long items_max = 2LL * lv.hkv * ((long long)total / kTile + B);
   const int grid = (int)std::max(1LL, std::min((long long)sms, items_max));
-  // launched as a programmatic dependent of the sink / recent copy, which it runs beside (neither waits
-  // for the other; later work on the stream waits for both)
+  // launched as a programmatic dependent of the sink / recent copy, which it runs beside; it ends after it, so that
+  // what waits for this grid has both
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
