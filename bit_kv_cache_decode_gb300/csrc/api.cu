@@ -1,6 +1,8 @@
 // C ABI of the OSCAR INT2 KV-cache library: layout carving, argument checks,
 // launches, status and tracing. The functions and data layouts are described
 // in include/oscar.h.
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -172,6 +174,61 @@ void rotation_image(const std::vector<double>& R, uint8_t* img) {
         r -= bf16_val(b);
       }
     }
+}
+
+// An append reads lengths, page tables and pool rows before it waits for the kernel before it on its stream. Where
+// that kernel may be one of this library's that writes tables or rows, the append is launched without the
+// programmatic overlap: a stream is noted by the writing calls, and its next append takes the note. Streams are
+// told apart by device and capture, since what is captured runs elsewhere; of more of them than kNotes (streams that
+// are never appended on) no account is kept, and every append waits.
+constexpr size_t kNotes = 256;
+struct StreamNote {
+  int dev;
+  cudaStream_t st;
+  unsigned long long capture;                      // 0: none
+  bool operator==(const StreamNote& o) const { return dev == o.dev && st == o.st && capture == o.capture; }
+};
+std::mutex g_notes_mu;
+std::vector<StreamNote> g_notes;
+std::atomic<int> g_noted{0};                       // their number; kNotes: every append waits
+
+StreamNote note_of(cudaStream_t st) {
+  StreamNote n = {0, st, 0};
+  cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+  if (cudaGetDevice(&n.dev) != cudaSuccess || cudaStreamGetCaptureInfo(st, &state, &n.capture) != cudaSuccess) cudaGetLastError();
+  if (state != cudaStreamCaptureStatusActive) n.capture = 0;
+  return n;
+}
+
+// what a call that launched a writer returns
+int wrote(int rc, cudaStream_t st) {
+  if (rc != OSCAR_OK || g_noted.load(std::memory_order_relaxed) >= (int)kNotes) return rc;
+  const StreamNote n = note_of(st);
+  std::lock_guard<std::mutex> lock(g_notes_mu);
+  for (StreamNote& o : g_notes)                    // a stream's earlier captures are over
+    if (o.dev == n.dev && o.st == n.st && (o.capture != 0) == (n.capture != 0)) {
+      o.capture = n.capture;
+      return rc;
+    }
+  g_notes.push_back(n);
+  g_noted.store((int)g_notes.size(), std::memory_order_relaxed);
+  return rc;
+}
+
+// whether an append on this stream has to wait before it reads anything
+bool takes_note(cudaStream_t st) {
+  const int noted = g_noted.load(std::memory_order_relaxed);
+  if (noted == 0) return false;
+  if (noted >= (int)kNotes) return true;
+  const StreamNote n = note_of(st);
+  std::lock_guard<std::mutex> lock(g_notes_mu);
+  const auto at = std::find(g_notes.begin(), g_notes.end(), n);
+  if (at == g_notes.end()) return false;
+  if (st != cudaStreamPerThread) {                 // one handle for the streams of all threads: kept
+    g_notes.erase(at);
+    g_noted.store((int)g_notes.size(), std::memory_order_relaxed);
+  }
+  return true;
 }
 
 // Kernel attributes (dynamic shared memory limits, carveout) belong to one device's context: they are
@@ -482,8 +539,8 @@ int oscar_quantize_prefill(oscar_cache* c, int layer, int B, const void* k, cons
   if (B == 0 || total_tokens == 0) return OSCAR_OK;
   if (!k || !v || !cu_seqlens || !bf16_pt || (max_hist_pages > 0 && !hist_pt)) return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v)) return OSCAR_ERR_INVALID_ARG;
-  return launch_prefill(view(c, layer), B, k, v, cu_seqlens, total_tokens, hist_pt, max_hist_pages, bf16_pt,
-                        static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return wrote(launch_prefill(view(c, layer), B, k, v, cu_seqlens, total_tokens, hist_pt, max_hist_pages, bf16_pt, st), st);
 }
 
 int oscar_project_quantize_prefill(oscar_cache* c, int layer, int B, const void* x, int d_model, const void* w_k,
@@ -495,8 +552,9 @@ int oscar_project_quantize_prefill(oscar_cache* c, int layer, int B, const void*
   if (B == 0 || total_tokens == 0) return OSCAR_OK;
   if (!x || !w_k || !w_v || !cu_seqlens || !bf16_pt || (max_hist_pages > 0 && !hist_pt)) return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_k) || !aligned16(w_v)) return OSCAR_ERR_INVALID_ARG;
-  return launch_project_prefill(view(c, layer), B, x, d_model, w_k, w_v, cu_seqlens, total_tokens, hist_pt,
-                                max_hist_pages, bf16_pt, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return wrote(launch_project_prefill(view(c, layer), B, x, d_model, w_k, w_v, cu_seqlens, total_tokens, hist_pt,
+                                      max_hist_pages, bf16_pt, st), st);
 }
 
 int oscar_append_kv(oscar_cache* c, int layer, int B, const void* k, const void* v, const int32_t* seq_lens_before,
@@ -505,8 +563,9 @@ int oscar_append_kv(oscar_cache* c, int layer, int B, const void* k, const void*
   if (B == 0) return OSCAR_OK;
   if (!k || !v || !seq_lens_before || !bf16_pt || (max_hist_pages > 0 && !hist_pt)) return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v)) return OSCAR_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launch_prologue(view(c, layer), DecodeWorkspace{}, B, nullptr, k, v, seq_lens_before, hist_pt,
-                         max_hist_pages, bf16_pt, 1.f, static_cast<cudaStream_t>(stream));
+                         max_hist_pages, bf16_pt, 1.f, st, takes_note(st));
 }
 
 int oscar_set_decode_algo(oscar_cache* c, int algo) {
@@ -617,7 +676,7 @@ int step_impl(oscar_cache* c, int layer, int B, const void* q, const void* k, co
   // one prologue launch (append with demotion, and the query prologue), then the decode and the
   // merge, each a programmatic dependent of the kernel before it
   const int rc = launch_prologue(lv, c->dws, B, q, k, v, seq_lens_before, hist_pt, max_hist_pages, bf16_pt,
-                                 sm_scale, st);
+                                 sm_scale, st, takes_note(st));
   if (rc != OSCAR_OK) return rc;
   return launch_decode(lv, c->dws, a, st);
 }
@@ -665,9 +724,10 @@ int oscar_build_tables(oscar_cache* c, int B, const int32_t* old_lens, const int
   if (!rings_in || !rings_out || (B > 0 && (!old_lens || !new_lens || !bf16_pt || !free_bf16))) return OSCAR_ERR_INVALID_ARG;
   if (B > 0 && ((max_hist_pages > 0 && !hist_pt) || (c->lay.num_int2_pages > 0 && !free_int2))) return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(slots)) return OSCAR_ERR_INVALID_ARG;
-  return launch_build_tables(c->lay, B, old_lens, new_lens, hist_pt, max_hist_pages, bf16_pt, free_int2, free_bf16,
-                             rings_in, rings_out, cu_tokens, slots, max_tokens, c->status,
-                             reinterpret_cast<unsigned*>(c->ws + 128), c->sms, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return wrote(launch_build_tables(c->lay, B, old_lens, new_lens, hist_pt, max_hist_pages, bf16_pt, free_int2, free_bf16,
+                                   rings_in, rings_out, cu_tokens, slots, max_tokens, c->status,
+                                   reinterpret_cast<unsigned*>(c->ws + 128), c->sms, st), st);
 }
 
 int oscar_tree_layout(oscar_cache* c, int B, int T, const int32_t* parents, const int32_t* n_draft,
@@ -816,8 +876,9 @@ int oscar_commit_draft(oscar_cache* c, int layer, int B, int T, const void* k_dr
   if (!k_draft || !v_draft || !seq_lens_before || !n_accept || !bf16_pt || (max_hist_pages > 0 && !hist_pt))
     return OSCAR_ERR_INVALID_ARG;
   if (!aligned16(k_draft) || !aligned16(v_draft)) return OSCAR_ERR_INVALID_ARG;
-  return launch_commit_draft(view(c, layer), B, T, k_draft, v_draft, seq_lens_before, n_accept, max_accept, path,
-                             hist_pt, max_hist_pages, bf16_pt, c->sms, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return wrote(launch_commit_draft(view(c, layer), B, T, k_draft, v_draft, seq_lens_before, n_accept, max_accept, path,
+                                   hist_pt, max_hist_pages, bf16_pt, c->sms, st), st);
 }
 
 int oscar_get_status(oscar_cache* c, int* code) {

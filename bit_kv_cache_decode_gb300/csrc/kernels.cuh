@@ -56,10 +56,12 @@ int launch_project_prefill(const LayerView& lv, int B, const void* x, int d_mode
                            const int* bf16_pt, cudaStream_t st);
 int configure_project_prefill_kernel();
 // Append (k, v non-null: new tokens, demotion) and / or the decode's query prologue (q non-null) in one
-// launch, a programmatic dependent of the kernel before it (prologue.cu).
+// launch, a programmatic dependent of the kernel before it (prologue.cu) unless `after_all`: that kernel
+// writes page tables or pool rows, which an append reads before it waits.
 int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const void* q, const void* k,
                     const void* v, const int* seq_lens_before, const int* hist_pt, int max_hist_pages,
-                    const int* bf16_pt, float sm_scale, cudaStream_t st);
+                    const int* bf16_pt, float sm_scale, cudaStream_t st,
+                    bool after_all = false);
 int configure_prologue_kernel();
 int configure_write_path_kernels();
 int configure_prefill_kernel();   // prefill_tc.cu

@@ -180,7 +180,7 @@ constexpr int kPrologueSmem = (kRFragWords + kTileFloats + kD) * 4 + 64;
 
 int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const void* q, const void* k,
                     const void* v, const int* seq_lens_before, const int* hist_pt, int max_hist_pages,
-                    const int* bf16_pt, float sm_scale, cudaStream_t st) {
+                    const int* bf16_pt, float sm_scale, cudaStream_t st, bool after_all) {
   if (B == 0) return OSCAR_OK;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -191,7 +191,7 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
   cfg.dynamicSmemBytes = kPrologueSmem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_all ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, k_step_prologue, lv, ws, static_cast<const __nv_bfloat16*>(q),
                             static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                             seq_lens_before, hist_pt, max_hist_pages, bf16_pt, sm_scale * kLog2e) == cudaSuccess

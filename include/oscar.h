@@ -263,7 +263,7 @@ int oscar_project_quantize_prefill(oscar_cache* cache, int layer, int B, const v
  * seq_lens_before[r] - recent - sink before its ring slot is overwritten.
  * As in oscar_decode_step, seq_lens_before, the page tables and the pool's
  * rows are read before the wait for the kernel launched just before; only
- * k and v may come from that kernel. */
+ * k and v may come from a kernel of the caller's launched just before. */
 int oscar_append_kv(oscar_cache* cache, int layer, int B, const void* k, const void* v,
                     const int32_t* seq_lens_before, const int32_t* hist_pt, int max_hist_pages,
                     const int32_t* bf16_pt, void* stream);
@@ -297,8 +297,10 @@ int oscar_decode_attention(oscar_cache* cache, int layer, int B, const void* q, 
  * before this call. The prologue is a programmatic dependent of that kernel:
  * it reads seq_lens_before, the page tables and the pool's BF16 rows before
  * it waits for it. These inputs must be complete when that kernel starts
- * (host copies, or any earlier kernel). No kernel of this library writes
- * them early. */
+ * (host copies, or any earlier kernel). Straight after a call of this library
+ * that writes page tables or pool rows (the prefills, oscar_build_tables,
+ * oscar_commit_draft) on the same stream, also in one capture, the prologue
+ * is launched without that overlap, and all of it is seen. */
 int oscar_decode_step(oscar_cache* cache, int layer, int B, const void* q, const void* k, const void* v,
                       const int32_t* seq_lens_before, const int32_t* hist_pt, int max_hist_pages,
                       const int32_t* bf16_pt, float sm_scale, void* out, int out_dtype, float* lse, void* stream);
@@ -356,10 +358,8 @@ int oscar_decode_step_shared(oscar_cache* cache, int layer, int B, const void* q
  * Nothing is changed, and a status bit says why, if a length is negative, shrinks to other than 0 or needs more
  * than max_hist_pages pages, or the new tokens exceed max_tokens (BAD_SEQLEN), a ring's head or count is out of
  * range (BAD_PAGE) or a ring is too short (NO_PAGES). One word of the cache's workspace orders the call's CTAs:
- * as for decode, calls on one cache must not overlap. oscar_append_kv and oscar_decode_step* read lengths and tables
- * before they wait for the kernel just before them: there has to be another kernel between this call and theirs on
- * the stream (the one that makes k and v is). Errors: INVALID_ARG (B < 0, null pointers, slots not 16-byte aligned,
- * max_tokens < 0), UNSUPPORTED (B > OSCAR_MAX_TABLE_BATCH), CUDA. */
+ * as for decode, calls on one cache must not overlap. Errors: INVALID_ARG (B < 0, null pointers, slots not 16-byte
+ * aligned, max_tokens < 0), UNSUPPORTED (B > OSCAR_MAX_TABLE_BATCH), CUDA. */
 int oscar_build_tables(oscar_cache* cache, int B, const int32_t* old_lens, const int32_t* new_lens,
                        int32_t* hist_pt, int max_hist_pages, int32_t* bf16_pt, int32_t* free_int2,
                        int32_t* free_bf16, const int32_t* rings_in, int32_t* rings_out, int32_t* cu_tokens,
@@ -461,9 +461,8 @@ int oscar_tree_attention(oscar_cache* cache, int layer, int B, int T, const void
  *  max_accept       : 1 .. recent; with a path it may exceed T (a node may be named twice)
  * A request with a length or count out of range is left as it is (BAD_SEQLEN); a token whose node (BAD_TREE), page
  * (BAD_PAGE) or history page (BAD_SEQLEN, BAD_PAGE) is out of range is left out. All inputs may come from the kernel
- * just before. oscar_append_kv and oscar_decode_step* read the pool's rows before they wait: as after
- * oscar_build_tables, there has to be another kernel between this call and theirs. Errors: INVALID_ARG (as
- * oscar_append_kv, T < 1, max_accept outside 1 .. recent, path NULL with max_accept > T), CUDA. */
+ * just before. Errors: INVALID_ARG (as oscar_append_kv, T < 1, max_accept outside 1 .. recent, path NULL with
+ * max_accept > T), CUDA. */
 int oscar_commit_draft(oscar_cache* cache, int layer, int B, int T, const void* k_draft, const void* v_draft,
                        const int32_t* seq_lens_before, const int32_t* n_accept, int max_accept, const int32_t* path,
                        const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream);
