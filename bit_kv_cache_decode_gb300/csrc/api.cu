@@ -2,12 +2,15 @@
 // launches, status and tracing. The functions and data layouts are described
 // in include/oscar.h.
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <system_error>
+#include <thread>
 #include <vector>
 
 #include "kernels.cuh"
@@ -101,79 +104,43 @@ LayerView view(const oscar_cache* c, int layer) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// R = U H P_br (MarkTechPost article "Together AI 开源 OSCAR…", section "OSCAR 有何不同做法"), composed in
-// double from the float32 U as loaded: (U H)[i][c] = sum_m U[i][m] (-1)^popcount(m & c) / sqrt(128), and
-// column j of R is column bitrev7(j) of U H. R[i][j]: i = input channel, j = rotated channel.
-std::vector<double> composite_rotation(const float* U) {
-  std::vector<double> uh((size_t)kD * kD), R((size_t)kD * kD);
-  const double inv = 1.0 / std::sqrt((double)kD);
+// max |U^T U - I| <= 1e-3, summed in double on the host's vector units: kLanes neighbouring columns at a time
+bool orthogonal(const float* U) {
+  constexpr int kLanes = 16;
+  std::array<double, (size_t)kD * kD> u;           // on the stack: the callers' threads neither allocate nor throw
+  std::copy(U, U + u.size(), u.begin());
+  bool ok = true;
   for (int i = 0; i < kD; ++i)
-    for (int c = 0; c < kD; ++c) {
-      double s = 0.0;
-      for (int m = 0; m < kD; ++m) s += (double)U[i * kD + m] * ((__builtin_popcount(m & c) & 1) ? -inv : inv);
-      uh[(size_t)i * kD + c] = s;
+    for (int j0 = i / kLanes * kLanes; j0 < kD; j0 += kLanes) {
+      double s[kLanes] = {};
+      for (int r = 0; r < kD; ++r) {
+        const double x = u[(size_t)r * kD + i];
+        for (int j = 0; j < kLanes; ++j) s[j] += x * u[(size_t)r * kD + j0 + j];
+      }
+      for (int j = 0; j < kLanes; ++j) ok = ok && std::fabs(s[j] - (i == j0 + j ? 1.0 : 0.0)) <= 1e-3;   // false for NaN
     }
-  for (int j = 0; j < kD; ++j) {
-    int rj = 0;
-    for (int bit = 0; bit < 7; ++bit) rj |= ((j >> bit) & 1) << (6 - bit);
-    for (int i = 0; i < kD; ++i) R[(size_t)i * kD + j] = uh[(size_t)i * kD + rj];
+  return ok;
+}
+
+// whether f(0) .. f(n - 1) all hold, over as many threads as there are or can be had
+template <typename F>
+bool all_of(int n, F f) {
+  std::atomic<int> next{0};
+  std::atomic<bool> ok{true};
+  auto work = [&] {
+    for (int i = next.fetch_add(1); i < n && ok; i = next.fetch_add(1))
+      if (!f(i)) ok = false;
+  };
+  std::array<std::thread, 15> others;
+  const int most = std::min({n, (int)std::thread::hardware_concurrency(), (int)others.size() + 1});
+  try {
+    for (int i = 0; i + 1 < most; ++i) others[i] = std::thread(work);
+  } catch (const std::system_error&) {               // no more threads: those there are do it
   }
-  return R;
-}
-
-// R as fp16 hi = fp16(R), lo = fp16(R - hi) (about 22 significant bits) in the B-fragment order of
-// mma.m16n8k16 (k = input channel, n = rotated channel): for k-block kb, n-tile nt and lane (g = lane / 4,
-// t = lane % 4), b0 holds rows 16 kb + 2t, +1 and b1 rows 16 kb + 2t + 8, +9, all of column 8 nt + g.
-void rotation_fragments(const std::vector<double>& R, uint32_t* frag) {
-  auto half_bits = [](double x) -> uint32_t {
-    const __half hv = __double2half(x);
-    return (uint32_t)__half_as_ushort(hv);
-  };
-  auto half_val = [](double x) -> double { return (double)__half2float(__double2half(x)); };
-  for (int kb = 0; kb < 8; ++kb)
-    for (int nt = 0; nt < 16; ++nt)
-      for (int lane = 0; lane < 32; ++lane) {
-        const int g = lane >> 2, t = lane & 3, col = 8 * nt + g;
-        const int rows[4] = {16 * kb + 2 * t, 16 * kb + 2 * t + 1, 16 * kb + 2 * t + 8, 16 * kb + 2 * t + 9};
-        uint32_t hi[4], lo[4];
-        for (int e = 0; e < 4; ++e) {
-          const double r = R[(size_t)rows[e] * kD + col];
-          hi[e] = half_bits(r);
-          lo[e] = half_bits(r - half_val(r));
-        }
-        uint32_t* w = frag + (((size_t)kb * 16 + nt) * 32 + lane) * 4;
-        w[0] = hi[0] | (hi[1] << 16);
-        w[1] = hi[2] | (hi[3] << 16);
-        w[2] = lo[0] | (lo[1] << 16);
-        w[3] = lo[2] | (lo[3] << 16);
-      }
-}
-
-// R as three bf16 parts b1 = bf16(R), b2 = bf16(R - b1), b3 = bf16(R - b1 - b2), each laid out as the
-// bulk prefill's tensor-core B operand (n = rotated channel, k = input channel, K-major, 128-byte swizzle):
-// element (n, k) of part p at byte p * 32768 + (k / 64) * 16384 + n * 128 + (((k % 64) / 8) ^ (n % 8)) * 16
-// + (k % 8) * 2.
-void rotation_image(const std::vector<double>& R, uint8_t* img) {
-  auto bf16_bits = [](double x) -> uint16_t {
-    const __nv_bfloat16 b = __float2bfloat16_rn((float)x);
-    return *reinterpret_cast<const uint16_t*>(&b);
-  };
-  auto bf16_val = [](uint16_t bits) -> double {
-    const uint32_t w = (uint32_t)bits << 16;
-    float f;
-    std::memcpy(&f, &w, 4);
-    return (double)f;
-  };
-  for (int n = 0; n < kD; ++n)
-    for (int k = 0; k < kD; ++k) {
-      double r = R[(size_t)k * kD + n];
-      const size_t off = (size_t)(k >> 6) * 16384 + (size_t)n * 128 + ((((k & 63) >> 3) ^ (n & 7)) << 4) + (k & 7) * 2;
-      for (int p = 0; p < 3; ++p) {
-        const uint16_t b = bf16_bits(r);
-        std::memcpy(img + (size_t)p * 32768 + off, &b, 2);
-        r -= bf16_val(b);
-      }
-    }
+  work();
+  for (std::thread& t : others)
+    if (t.joinable()) t.join();
+  return ok;
 }
 
 // An append reads lengths, page tables and pool rows before it waits for the kernel before it on its stream. Where
@@ -469,44 +436,15 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
   const bool expl = c->lay.v_mode == OSCAR_V_EXPLICIT;
   if (expl && !U_V) return OSCAR_ERR_INVALID_ARG;
   const int hkv = c->lay.num_kv_heads;
+  if (!all_of(hkv, [&](int h) {
+        return orthogonal(U_K + (size_t)h * kD * kD) && (!U_V || orthogonal(U_V + (size_t)h * kD * kD));
+      }))
+    return OSCAR_ERR_NOT_ORTHOGONAL;
+  // per head: the compact-format grid of each (kind, group), T = the group's largest threshold, D = fl32(2T / 255),
+  // E = fl32(D / 3) (single-precision operations, each correctly rounded), then the uniform codebook of both kinds
+  std::vector<float> consts((size_t)hkv * kMetaCFloats, 0.f);
   for (int h = 0; h < hkv; ++h) {
-    for (int which = 0; which < 2; ++which) {
-      const float* U = which == 0 ? U_K : U_V;
-      if (!U) continue;
-      U += (size_t)h * kD * kD;
-      for (int i = 0; i < kD; ++i)
-        for (int j = i; j < kD; ++j) {
-          double s = 0.0;
-          for (int r = 0; r < kD; ++r) s += (double)U[r * kD + i] * (double)U[r * kD + j];
-          const double e = std::fabs(s - (i == j ? 1.0 : 0.0));
-          if (!(e <= 1e-3)) return OSCAR_ERR_NOT_ORTHOGONAL;
-        }
-    }
-  }
-  std::vector<float> host((size_t)hkv * kParamFloats, 0.f);
-  for (int h = 0; h < hkv; ++h) {
-    float* dst = host.data() + (size_t)h * kParamFloats;
-    std::memcpy(dst + kUKOff, U_K + (size_t)h * kD * kD, kD * kD * sizeof(float));
-    {
-      const std::vector<double> R = composite_rotation(U_K + (size_t)h * kD * kD);
-      rotation_fragments(R, reinterpret_cast<uint32_t*>(dst + kRKFragOff));
-      rotation_image(R, reinterpret_cast<uint8_t*>(dst + kRKImgOff));
-    }
-    if (U_V) {
-      const float* u = U_V + (size_t)h * kD * kD;
-      std::memcpy(dst + kUVOff, u, kD * kD * sizeof(float));
-      for (int i = 0; i < kD; ++i)
-        for (int j = 0; j < kD; ++j) dst[kUVtOff + j * kD + i] = u[i * kD + j];
-      if (expl) {
-        const std::vector<double> R = composite_rotation(u);
-        rotation_fragments(R, reinterpret_cast<uint32_t*>(dst + kRVFragOff));
-        rotation_image(R, reinterpret_cast<uint8_t*>(dst + kRVImgOff));
-      }
-    }
-    std::memcpy(dst + kTauKOff, tau_K + (size_t)h * kD, kD * sizeof(float));
-    std::memcpy(dst + kTauVOff, tau_V + (size_t)h * kD, kD * sizeof(float));
-    // compact-format grid per (kind, group): T = the group's largest threshold, D = fl32(2T / 255),
-    // E = fl32(D / 3) (single-precision operations, each correctly rounded)
+    float* dst = consts.data() + (size_t)h * kMetaCFloats;
     for (int kind = 0; kind < 2; ++kind)
       for (int g = 0; g < kNG; ++g) {
         const float* t = (kind == 0 ? tau_K : tau_V) + (size_t)h * kD + g * kG;
@@ -514,21 +452,31 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
         for (int j = 1; j < kG; ++j) T = t[j] > T ? t[j] : T;
         const float D = (T + T) / 255.0f;
         const float E = D / 3.0f;
-        float* mc = dst + kMetaCOff + kind * 8 + g * 4;
+        float* mc = dst + kind * 8 + g * 4;
         mc[0] = T;
         mc[1] = D;
         mc[2] = E;
-        mc[3] = 0.f;
       }
     static const uint8_t kUniform[4] = {0, 85, 170, 255};
-    codebook_consts(kUniform, dst + kCbOff);
-    codebook_consts(kUniform, dst + kCbOff + 8);
+    codebook_consts(kUniform, dst + kCbOff - kMetaCOff);
+    codebook_consts(kUniform, dst + kCbOff - kMetaCOff + 8);
   }
-  LayerView v = view(c, layer);
-  cudaError_t e = cudaMemcpyAsync(const_cast<float*>(v.params), host.data(), host.size() * sizeof(float),
-                                  cudaMemcpyHostToDevice, static_cast<cudaStream_t>(stream));
-  // the source is pageable: the call returns once `host` has been staged, so it may be freed
-  return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+  // U, thresholds and constants as they are; a kernel makes the rest of the parameters from U. The sources are
+  // pageable: a copy returns once its source has been staged, so it may be freed. Copies come last: the kernels that are
+  // launched as programmatic dependents read parameters before they wait for a kernel before them.
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* params = const_cast<float*>(view(c, layer).params);
+  auto put = [&](int off, const float* src, int floats) {
+    const size_t row = floats * sizeof(float);
+    return cudaMemcpy2DAsync(params + off, kParamFloats * sizeof(float), src, row, row, hkv, cudaMemcpyHostToDevice, st) ==
+           cudaSuccess;
+  };
+  if (cudaMemsetAsync(params, 0, (size_t)hkv * kParamFloats * sizeof(float), st) != cudaSuccess ||
+      !put(kUKOff, U_K, kD * kD) || (U_V && !put(kUVOff, U_V, kD * kD)))
+    return OSCAR_ERR_CUDA;
+  if (int rc = launch_rotation_params(params, hkv, U_V != nullptr, expl, st); rc != OSCAR_OK) return rc;
+  const bool put_all = put(kTauKOff, tau_K, kD) && put(kTauVOff, tau_V, kD) && put(kMetaCOff, consts.data(), kMetaCFloats);
+  return put_all ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 int oscar_quantize_prefill(oscar_cache* c, int layer, int B, const void* k, const void* v, const int32_t* cu_seqlens,

@@ -45,6 +45,8 @@ constexpr int kQSigma = 9;               // sigma, the power-of-two scale of the
 // 8 k-blocks x 2 n-tiles x 32 lanes x 2 registers.
 constexpr int kFragWords = 8 * 2 * 32 * 2;
 
+// the parameters of a layer that follow from U (in them already): V's transpose, rotations as operands (rotation_params.cu)
+int launch_rotation_params(float* params, int hkv, bool v, bool v_rotated, cudaStream_t st);
 int launch_pack_rotated(const LayerView& lv, int kind, const float* xrot, const int* page_ids, const int* rows,
                         int N, cudaStream_t st);
 int launch_rotate(const LayerView& lv, int kind, const void* x, float* y, int N, cudaStream_t st);
