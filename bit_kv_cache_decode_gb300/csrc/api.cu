@@ -28,6 +28,7 @@ struct oscar_cache {
   int* status;
   int sms;
   int algo;
+  int tree_rc;                    // what configuring the tree attention's kernels gave
   unsigned long long* timeline;   // kernel timeline buffer (oscar_trace_timeline) or null
   int timeline_cap;
   // tracing
@@ -203,6 +204,7 @@ bool takes_note(cudaStream_t st) {
 constexpr int kMaxConfiguredDevices = 64;
 std::mutex g_configure_mu;
 bool g_configured[kMaxConfiguredDevices];
+int g_tree_rc[kMaxConfiguredDevices];              // the tree attention's own: its callers alone meet a failure
 
 int configure_once() {
   int dev = 0;
@@ -214,8 +216,11 @@ int configure_once() {
   if (rc == OSCAR_OK) rc = configure_decode_kernels();
   if (rc == OSCAR_OK) rc = configure_tables_kernel();
   if (rc == OSCAR_OK) rc = configure_commit_kernel();
-  if (rc == OSCAR_OK) rc = configure_tree_kernels();
-  if (rc == OSCAR_OK) g_configured[dev] = true;
+  if (rc == OSCAR_OK) {
+    g_tree_rc[dev] = configure_tree_kernels();
+    if (g_tree_rc[dev] != OSCAR_OK) cudaGetLastError();
+    g_configured[dev] = true;
+  }
   return rc;
 }
 
@@ -379,6 +384,7 @@ int oscar_cache_create(const oscar_layout* layout, void* pool, void* workspace, 
   p += align_up(B * hq * c->dws.nslots * kPartFloats * sizeof(float));
   c->sms = sms;
   c->algo = kDefaultDecodeAlgo;
+  c->tree_rc = g_tree_rc[dev];
   c->timeline = nullptr;
   c->timeline_cap = 0;
   c->prof_on = false;
@@ -780,6 +786,7 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   if (out_dtype != OSCAR_OUT_BF16 && out_dtype != OSCAR_OUT_FP32) return OSCAR_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return OSCAR_ERR_INVALID_ARG;
   if (T > kMaxDraft || B > 65535 || (c->lay.sink + c->lay.recent) / kP > kMaxTreeBf16Pages) return OSCAR_ERR_UNSUPPORTED;
+  if (c->tree_rc != OSCAR_OK) return c->tree_rc;
   if (B == 0) return OSCAR_OK;
   if (!q || !k_draft || !v_draft || !mask || !seq_lens || !bf16_pt || !out || !workspace ||
       (max_hist_pages > 0 && !hist_pt))

@@ -1141,7 +1141,8 @@ int launch_fmt(const LayerView& lv, const TreeArgs& a, int B, cudaStream_t st) {
 template <int FMT, bool WIDE>
 int configure_as() {
   cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
-  if (cudaFuncGetAttributes(&at, k_tree_attention<FMT, WIDE>) != cudaSuccess || at.numRegs < kRegsLaunch) return OSCAR_ERR_CUDA;
+  if (cudaFuncGetAttributes(&at, k_tree_attention<FMT, WIDE>) != cudaSuccess) return OSCAR_ERR_CUDA;
+  if (at.numRegs < kRegsLaunch) return OSCAR_ERR_UNSUPPORTED;   // a compiler that gives fewer: the shares would wait forever
   if (cudaFuncSetAttribute(k_tree_attention<FMT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem<WIDE>) !=
       cudaSuccess)
     return OSCAR_ERR_CUDA;
@@ -1206,8 +1207,10 @@ int launch_tree_attention(const LayerView& lv, const TreeArgs& a, int B, int sms
 }
 
 int configure_tree_kernels() {
-  if (configure_tree_merge() != OSCAR_OK || configure_fmt<kFmtF16>() != OSCAR_OK || configure_fmt<kFmtU8>() != OSCAR_OK) return OSCAR_ERR_CUDA;
-  return configure_fmt<kFmtCB>();
+  int rc = configure_tree_merge();
+  if (rc == OSCAR_OK) rc = configure_fmt<kFmtF16>();
+  if (rc == OSCAR_OK) rc = configure_fmt<kFmtU8>();
+  return rc == OSCAR_OK ? configure_fmt<kFmtCB>() : rc;
 }
 
 }  // namespace oscar
