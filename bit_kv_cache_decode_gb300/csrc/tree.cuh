@@ -41,7 +41,7 @@ __device__ __forceinline__ int live_nodes(const TreeArgs& a, int b) {
 }
 // history pages of a request (length L), and the slots they are spread over
 __device__ __forceinline__ int tree_pages(const LayerView& lv, const TreeArgs& a, int L) {
-  return min((max(0, L - lv.sink - lv.recent) + kP - 1) / kP, a.max_hist_pages);
+  return min((max(0, max(L, 0) - lv.sink - lv.recent) + kP - 1) / kP, a.max_hist_pages);   // L below 0 counts as 0
 }
 // x / y for 0 <= x < 2^26, y > 0 and a quotient of at most 2^16: a quarter of the integer division's latency, which
 // every CTA's start would wait for twice. The float quotient is off by less than one.

@@ -83,3 +83,20 @@ def test_a_bad_query_without_history(L):
         assert out[0, sees, e].isnan().all() and lse[0, sees, e].isnan().all()
         assert (out[0, ~sees, e] == 0).all() and (lse[0, ~sees, e] == -np.inf).all()
     assert out[0, :, [0, 3]].isfinite().all() and lse[0, sees][:, [0, 3]].isfinite().all()
+
+
+@pytest.mark.parametrize("length", [-1, -321, -2 ** 31])
+@pytest.mark.parametrize("v_mode", [0, 1])
+def test_any_negative_length_is_taken_as_none(length, v_mode):
+    T, hkv, gq = 5, 1, 4
+    case = build_decode_case([64 + 256 + 64 * 3, 700], hkv, gq, v_mode, seed=73)
+    cache, _, hp, bp = case
+    q, kd, vd = (to_dev_bf16(x) for x in draft(73, 2, T, hkv, gq))
+    words = torch.from_numpy(mask_words(random_mask(np.random.default_rng(2), 2, T, "chain"))).to(DEV)
+    ws = torch.empty(cache.tree_workspace_bytes(2, T, hp.shape[1]), dtype=torch.uint8, device=DEV)
+    outs = []
+    for n in (0, length):
+        ws.fill_(0xFF)                                     # what is not written reads as NaN
+        outs.append(cache.tree_attention(0, q, kd, vd, words, dev([n, 700]), hp, bp, synth.sm_scale(), workspace=ws))
+        assert cache.get_status() == (0 if n == 0 else osc.STATUS_BAD_SEQLEN)
+    assert torch.equal(outs[0], outs[1]) and outs[0].isfinite().all()
