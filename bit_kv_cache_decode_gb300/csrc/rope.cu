@@ -192,14 +192,18 @@ int launch_as(RopeArgs a, cudaStream_t st) {
 }
 
 // bytes: the widest access, of 16 at most, that every row, half and remainder starts on a multiple of; else elements.
-// Where only the halves are narrower, the channels behind them are copied 16 bytes at a time (copy16).
+// Where only the halves are narrower, which are then 8 bytes' multiples, the channels behind them are copied 16 bytes at
+// a time (copy16).
 template <typename T, bool HALF>
 int launch_layout(const RopeArgs& a, int bytes, bool copy16, cudaStream_t st) {
   constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), V4 = 4 / sizeof(T), kLeast = HALF ? 1 : 2;
   if (bytes == 16) return launch_as<T, V16, V16, HALF, true>(a, st);
-  if (bytes == 8) return copy16 ? launch_as<T, V8, V16, HALF, true>(a, st) : launch_as<T, V8, V8, HALF, true>(a, st);
+  if constexpr (HALF) {
+    if (bytes == 8 && copy16) return launch_as<T, V8, V16, HALF, true>(a, st);
+  }
+  if (bytes == 8) return launch_as<T, V8, V8, HALF, true>(a, st);
   if constexpr (V4 > 1) {
-    if (bytes == 4) return copy16 ? launch_as<T, V4, V16, HALF, true>(a, st) : launch_as<T, V4, V4, HALF, true>(a, st);
+    if (bytes == 4) return launch_as<T, V4, V4, HALF, true>(a, st);
   }
   return launch_as<T, kLeast, kLeast, HALF, false>(a, st);
 }
@@ -236,7 +240,7 @@ int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, i
   const bool half_layout = layout == OSCAR_ROPE_HALF;
   const int size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
   const int v16 = 16 / size;
-  const bool copy16 = fits(q, size, v16) && fits(k, size, v16) && rot % v16 == 0 && (dim - rot) % v16 == 0;
+  const bool copy16 = half_layout && fits(q, size, v16) && fits(k, size, v16) && rot % v16 == 0 && (dim - rot) % v16 == 0;
   int bytes = 16;
   for (; bytes > size; bytes /= 2) {
     const int v = bytes / size;
