@@ -9,7 +9,9 @@
 // Angles. A float32 product pos * f loses the angle of far positions (at pos 1e5 its half unit is 4e-3
 // radians). The plan therefore holds each frequency as a 64-bit fraction of a turn, F = round(f / (2 pi) 2^64),
 // and the angle is the integer product pos * F modulo 2^64: the full turns fall off by themselves, and the
-// error stays below pos 2^-65 turns. Its upper 32 bits, as a signed number of half turns, go to sincospif.
+// error stays below pos 2^-65 turns. Its upper 32 bits (2^-32 turns), as a signed number of half turns in float32
+// (2^-26 turns, or 1e-7 radians, at most), go to sincospif: what is left of the angle's error is float32's, the same
+// at any position.
 //
 // Each (token, pair) angle is computed once per CTA into shared memory and serves all heads. A thread keeps
 // one unit of the head (16 bytes, or the 8 or 4 that the strides and the halves allow) and walks tokens and heads,

@@ -387,8 +387,8 @@ int oscar_tree_layout(oscar_cache* cache, int B, int T, const int32_t* parents, 
  *               0.1 ln(factor) + 1 (1 for the other kinds)
  *  inv_freq   : host float64 [rotary_dim / 2];  scale : factor of the rotated values
  * oscar_rope_turns turns frequencies (n of them, 0 <= f < 2 pi) into the table oscar_rope reads, 64-bit fractions
- * of a turn per position: integer products keep the angle of any position exact to 2^-33 turns. Copy it to the
- * device once. Errors: INVALID_ARG. */
+ * of a turn per position: integer products keep the angle of any position to 2^-32 turns, and what is rounded to
+ * float32 is less than half a turn (2^-26 turns, or 1e-7 radians). Copy it to the device once. Errors: INVALID_ARG. */
 #define OSCAR_ROPE_NONE   0
 #define OSCAR_ROPE_LINEAR 1
 #define OSCAR_ROPE_NTK    2
