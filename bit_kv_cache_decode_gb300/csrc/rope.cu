@@ -185,7 +185,10 @@ int launch_as(RopeArgs a, cudaStream_t st) {
   const int half = a.rot / 2;
   const int units = (HALF ? half / V : a.rot / V) + (a.dim - a.rot) / VP;
   // four CTAs per SM and more while there are tokens for them (3,000 tokens x 40 heads: 12.2 us; two: 14.9, eight: 14.3)
-  a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.n / 608));
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return OSCAR_ERR_CUDA;
+  a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.n / (4 * sms)));
   const unsigned heads = a.q.heads + a.k.heads;
   a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
