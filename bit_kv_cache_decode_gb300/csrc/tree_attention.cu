@@ -1186,8 +1186,15 @@ void tree_splits(int B, int T, int hkv, int gq, int nbf, int max_hist_pages, int
   const int least_m = std::min(exact_m, std::max(1, max_slots - least_s));
   // more than four waves of CTAs gain nothing
   const int most_s = std::max(least_s, std::min(pages, (int)std::min<long>(2 * sms, 4 * sms / units + 1)));
-  for (int m = least_m; m <= near && m < max_slots; ++m)
-    for (int s = least_s; s <= most_s && s + m <= max_slots; ++s) {
+  // More slots of the same length cost more, so only counts that shorten the longest are looked at: about 2 sqrt(pages) of
+  // each kind. The search runs in every call (one request and kv
+  // head over 1,600 pages: 1.5 us with 5 BF16 pages, 6 with 67, 32 with 2,040; all counts: 7, 84 and 2,519).
+  auto next = [&](int n, int x) {                  // the next count after x with shorter parts of n; beyond n: none
+    const int longest = parts(n, x);
+    return longest == 1 ? n + 1 : parts(n, longest - 1);
+  };
+  for (int m = least_m; m <= near && m < max_slots; m = next(near, m))
+    for (int s = least_s; s <= most_s && s + m <= max_slots; s = next(pages, s)) {
       const double h = (pages + s - 1) / s + kFixed, g = kNear * ((near + m - 1) / m) + kFixed, longest = std::max(h, g);
       auto more = [&](double fill) { return units * (fill * s + m) <= sms ? 0.0 : units * (fill * s * h + m * g) / sms; };
       const double cost = longest + (B > 1 ? kFull * more(1.0) + (1.0 - kFull) * more(kFill) : more(1.0)) + 0.1 * (s + m);

@@ -2,6 +2,7 @@
 import ctypes
 import subprocess
 import sys
+import time
 
 import pytest
 
@@ -49,3 +50,46 @@ def test_an_accumulator_takes_1024_products(splits, B, T, hkv, gq, pages, nbf):
         assert (s2 == 0) == (least + 1 > slots)
         if s2:
             assert s2 + m2 <= slots and s2 * p2 >= pages and p2 <= 4096
+
+
+def searched(B, T, hkv, gq, nbf, pages, sms, max_slots):
+    """The plan of least cost among all counts of slots, and of equal ones the first."""
+    up = lambda n, x: -(-n // x)                             # noqa: E731
+    tiles, wide = up(T * gq, 128), T * gq > 128
+    streams = 1 if wide else 2
+    units = max(1, B * hkv * (up(tiles, 2) if wide else tiles))
+    near, pages = nbf + up(T, 64), max(1, pages)
+    exact_s, exact_m = up(pages, streams * 256), up(near, streams * 128)
+    least_s = min(exact_s, max(up(pages, 4096), max_slots - exact_m))
+    least_m = min(exact_m, max(1, max_slots - least_s))
+    most_s = max(least_s, min(pages, 2 * sms, 4 * sms // units + 1))
+    best = (0.0, 0, 0, 1)
+    for m in range(least_m, near + 1):
+        if m >= max_slots:
+            break
+        for s in range(least_s, min(most_s, max_slots - m) + 1):
+            h, g = up(pages, s) + 20.0, 5.0 * up(near, m) + 20.0
+            more = [0.0 if units * (f * s + m) <= sms else units * (f * s * h + m * g) / sms for f in (1.0, 0.75)]
+            cost = max(h, g) + (0.35 * more[0] + (1.0 - 0.35) * more[1] if B > 1 else more[0]) + 0.1 * (s + m)
+            if best[0] == 0.0 or cost < best[0]:
+                best = (cost, s, m, up(pages, s))
+    return best[1:]
+
+
+@pytest.mark.parametrize("B,T,hkv,gq", [(1, 1, 1, 1), (1, 5, 8, 4), (2, 17, 8, 8), (8, 26, 8, 4), (64, 5, 8, 4), (5, 60, 8, 4)])
+@pytest.mark.parametrize("pages", [0, 1, 2, 63, 190, 500, 1595])
+@pytest.mark.parametrize("nbf", [5, 20, 67])
+@pytest.mark.parametrize("max_slots", [1 << 20, 23, 7, 2])
+def test_the_search_finds_the_least_cost(splits, B, T, hkv, gq, pages, nbf, max_slots):
+    assert splits(B, T, hkv, gq, nbf, pages, 152, max_slots) == searched(B, T, hkv, gq, nbf, pages, 152, max_slots)
+
+
+def test_the_search_is_short_whatever_the_window(splits):
+    for nbf in (5, 67, 2040):
+        took = []
+        for _ in range(5):
+            t = time.perf_counter()
+            for _ in range(20):
+                splits(1, 5, 1, 1, nbf, 1600)
+            took.append((time.perf_counter() - t) / 20)
+        assert min(took) < 2e-4, (nbf, min(took))            # 2.5 ms with every count of slots
