@@ -104,6 +104,7 @@ LayerView view(const oscar_cache* c, int layer) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // max |U^T U - I| <= 1e-3, summed in double on the host's vector units: kLanes neighbouring columns at a time
 bool orthogonal(const float* U) {
@@ -689,7 +690,7 @@ int oscar_tree_layout(oscar_cache* c, int B, int T, const int32_t* parents, cons
   if (!c || B < 0 || T < 1) return OSCAR_ERR_INVALID_ARG;
   if (T > kMaxDraft) return OSCAR_ERR_UNSUPPORTED;
   if (B == 0) return OSCAR_OK;
-  if (!parents || !seq_lens || !mask || !positions) return OSCAR_ERR_INVALID_ARG;
+  if (!parents || !seq_lens || !mask || !positions || !aligned8(mask)) return OSCAR_ERR_INVALID_ARG;
   return launch_tree_layout(B, T, parents, n_draft, seq_lens, mask, positions, c->status,
                             static_cast<cudaStream_t>(stream));
 }
@@ -762,7 +763,7 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
     t[i] = *x;
   }
   if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
-  if (!positions || !turns) return OSCAR_ERR_INVALID_ARG;
+  if (!positions || !turns || !aligned8(turns)) return OSCAR_ERR_INVALID_ARG;
   return launch_rope(t[0], t[1], N, head_dim, rotary_dim, dtype, positions, turns, layout, scale, inverse,
                      static_cast<cudaStream_t>(stream));
 }
@@ -791,7 +792,8 @@ int oscar_tree_attention(oscar_cache* c, int layer, int B, int T, const void* q,
   if (!q || !k_draft || !v_draft || !mask || !seq_lens || !bf16_pt || !out || !workspace ||
       (max_hist_pages > 0 && !hist_pt))
     return OSCAR_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out)) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out) || !aligned8(mask))
+    return OSCAR_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return OSCAR_ERR_INVALID_ARG;
   const int hq = c->lay.num_q_heads, hkv = c->lay.num_kv_heads;
   const size_t slots = workspace_bytes / tree_slot_bytes(c, B, T);

@@ -373,7 +373,8 @@ int oscar_build_tables(oscar_cache* cache, int B, const int32_t* old_lens, const
  *  positions : device int32 [B][T]: seq_lens[r] + the number of drafted nodes above i
  * Nodes from n_draft[r] on, nodes at or below a parent out of range (BAD_TREE), and all nodes of a request whose
  * length is negative or leaves no room for T positions below 2^31 (BAD_SEQLEN) get an empty mask and position -1.
- * Errors: INVALID_ARG (B < 0, T < 1, null pointers), UNSUPPORTED (T > OSCAR_MAX_DRAFT), CUDA. */
+ * Errors: INVALID_ARG (B < 0, T < 1, null pointers, mask not 8-byte aligned), UNSUPPORTED (T > OSCAR_MAX_DRAFT),
+ * CUDA. */
 int oscar_tree_layout(oscar_cache* cache, int B, int T, const int32_t* parents, const int32_t* n_draft,
                       const int32_t* seq_lens, uint64_t* mask, int32_t* positions, void* stream);
 
@@ -417,7 +418,7 @@ typedef struct oscar_rope_tensor {
  * or with -t where inverse is 1: the gradient of the forward rotation. Channels from rotary_dim on are copied.
  * Rows with a negative position are left as they are. q and k have one dtype (OSCAR_DTYPE_*); products in
  * float32, one rounding at the end.
- *  turns : device uint64 [rotary_dim / 2] from oscar_rope_turns
+ *  turns : device uint64 [rotary_dim / 2] from oscar_rope_turns, 8-byte aligned
  * Errors: INVALID_ARG (null pointers, N < 0, negative heads or strides, odd or too large rotary_dim, a bad dtype,
  * layout or scale), UNSUPPORTED (head_dim odd or above 512), CUDA. Works without a cache. */
 int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
@@ -444,7 +445,7 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  * infinity in a drafted row reaches the rows that attend to it and no others (NONFINITE); one in a row of q makes that
  * row's output and lse NaN and touches no other (NONFINITE).
  * The cache is only read; all inputs but the cache's rotations may come from the kernel just before.
- * q, k_draft and v_draft are 16-byte aligned. Errors: INVALID_ARG (as
+ * q, k_draft, v_draft and out are 16-byte aligned, mask 8-byte. Errors: INVALID_ARG (as
  * oscar_decode_attention, workspace too small), UNSUPPORTED (T > OSCAR_MAX_DRAFT, B > 65535, sink + recent above
  * 130,560 tokens), CUDA. */
 int oscar_tree_workspace_bytes(const oscar_cache* cache, int B, int T, int max_hist_pages, size_t* bytes);
