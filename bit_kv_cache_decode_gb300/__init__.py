@@ -635,7 +635,7 @@ def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool
     pos = _in_i32(positions, dev)
     dtype, shape, n = q.dtype, q.shape, pos.numel()
     code = DTYPE_BF16 if dtype is _bf16 else DTYPE_FP32 if dtype is _f32 else DTYPE_FP16
-    if (code == DTYPE_FP16 and dtype is not _f16) or plan.turns.get_device() != dev or len(shape) != 3:
+    if (code == DTYPE_FP16 and dtype is not _f16) or plan.turns.get_device() != dev or len(shape) != 3 or n >> 31:
         raise OscarError(ERR_INVALID_ARG, "oscar_rope")
     dim = shape[2]
     args, outs = [], []

@@ -192,7 +192,7 @@ int launch_as(RopeArgs a, cudaStream_t st) {
   const unsigned heads = a.q.heads + a.k.heads;
   a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
-  k_rope<T, V, VP, HALF, WIDE><<<(a.n + a.tokens - 1) / a.tokens, dim3(bx, by), 0, st>>>(a);
+  k_rope<T, V, VP, HALF, WIDE><<<(a.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
