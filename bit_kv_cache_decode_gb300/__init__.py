@@ -336,6 +336,8 @@ class OscarCache:
                "oscar_project_quantize_prefill")
 
     def append_kv(self, layer: int, k, v, seq_lens_before, hist_pt, bf16_pt, stream=None):
+        """Append one token per request. Lengths and tables on the device are read before the kernel just before this
+        call on the stream is waited for: of a kernel of the caller's launched there only k and v may come."""
         sl = _dev_i32(seq_lens_before, self.device)
         hp = _dev_i32(hist_pt, self.device)
         bp = _dev_i32(bf16_pt, self.device)
@@ -369,7 +371,8 @@ class OscarCache:
     def decode_step(self, layer: int, q, k, v, seq_lens_before, hist_pt, bf16_pt, sm_scale: float, out=None,
                     out_dtype: int = OUT_BF16, lse=None, stream=None, shared_hist_pages: int = 0):
         """append_kv(k, v) then decode_attention(q) over seq_lens_before + 1 tokens, in one call
-        (oscar_decode_step_shared when shared_hist_pages > 0)."""
+        (oscar_decode_step_shared when shared_hist_pages > 0). As for append_kv, only q, k and v may come from a kernel
+        of the caller's launched just before."""
         import torch
         sl = _dev_i32(seq_lens_before, self.device)
         hp = _dev_i32(hist_pt, self.device)
@@ -392,8 +395,9 @@ class OscarCache:
     # ---- verifying drafted tokens -----------------------------------------------------
     def build_tables(self, old_lens, new_lens, hist_pt, bf16_pt, free_int2, free_bf16, rings, max_tokens: int = 0,
                      rings_out=None, cu_tokens=None, slots=None, stream=None):
-        """Page tables and token slots of requests growing (or released) from old_lens to new_lens; the tables and
-        the free rings are int32 device tensors updated in place, the ring positions too unless rings_out is given.
+        """Page tables and token slots of requests growing (or released) from old_lens, the lengths the last call left,
+        to new_lens; the tables and the free rings are int32 device tensors updated in place, the ring positions too
+        unless rings_out is given. A draft needs no pages: grow by what was accepted of it.
         With max_tokens, or a slots tensor [max_tokens, 4], each new token's (position, region, page, row) is
         written. Returns (rings_out, cu_tokens, slots)."""
         if stream is not None:
@@ -456,7 +460,7 @@ class OscarCache:
     def tree_attention(self, layer: int, q, k_draft, v_draft, mask, seq_lens, hist_pt, bf16_pt, sm_scale: float,
                        n_draft=None, out=None, out_dtype: int = OUT_BF16, lse=None, workspace=None, stream=None):
         """Attention of drafted nodes q [B, T, Hq, 128] over the cache's seq_lens tokens and, by mask, the drafted
-        k_draft, v_draft [B, T, Hkv, 128]. workspace: a uint8 tensor of tree_workspace_bytes, allocated per call
+        k_draft, v_draft [B, T, Hkv, 128]. A NaN or infinity in a row of q makes that row NaN. workspace: a uint8 tensor of tree_workspace_bytes, allocated per call
         when not given; calls that may overlap need one each."""
         if stream is not None:
             with _on(stream):

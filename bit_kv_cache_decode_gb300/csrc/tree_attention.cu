@@ -30,10 +30,11 @@
 // stream's next product; it keeps them until its weights stand, in case it has to raise the reference.
 // A history page of one tile is 8 MMAs of M128 N64 K16 (32 cycles each) and 4 of M128 N128 K16 (64): 512 cycles of the
 // tensor pipe. The CUDA cores issue about 725 warp instructions per scheduler beside them (rows 250, keys 190, values
-// 190, control 95) and take 915 cycles a page, 1,770 for two tiles (1,000 instructions): the exponentials (4 cycles a
-// warp), the packed multiplies, adds and half-precision products (2 each) and the bit operations (2) share the issue
-// slots with the hand-overs between the roles. That bounds the kernel. Two threads to a row, half of a page's tokens
-// each, measured 15 % slower: the same instructions and more hand-overs.
+// 190, control 95) and take 915 cycles a page, 1,770 for two tiles (1,000 instructions): the exponentials take 4 cycles a
+// warp, the packed multiplies, adds and half-precision products 2 each, and the bit operations 2. Neither is full (two
+// tiles over 102,400 tokens: tensor pipe 49 % of the cycles, issue slots 56 %; one, 8 requests: 24 and 47 %): what is
+// left is the time the roles wait for one another, page by page. Two threads to a row, half of a page's tokens each,
+// measured 15 % slower: the same instructions and more hand-overs.
 // Every wait is bounded; a CTA whose wait expires flags OSCAR_STATUS_TIMEOUT and writes empty partials.
 #include <algorithm>
 
@@ -133,6 +134,8 @@ __device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 // (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}; blk: shared address of the page block.
+// Codebook format: the levels k / 256 are exact fp16 numbers, 255ths are not; the range takes the factor 256 / 255 and is
+// rounded to fp16 once more, so a key or value has two roundings of 2^-11, of scale times level and of the sum.
 // Compact format: a value is mn8 D - T + code (mx8 - mn8) E with D = 3 E and T = 127.5 D, that is E times
 // 3 mn8 - 382.5 + code (mx8 - mn8), which fp16 holds exactly. The group's E goes into the query rows and, for values,
 // into the partials. (Scale and zero rounded to fp16 tripled the outputs' error.)
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     if (lane == 0 && hist) {                       // the rotation; the parameters come from no kernel
       const uint8_t* img = reinterpret_cast<const uint8_t*>(lv.params + (size_t)h * kParamFloats + kRKImgOff);
       mbar_expect_tx(c.bar(kBImg), 2 * kImgBytes);
-      for (int p = 0; p < 2; ++p)                  // R = b1 + b2 to about 17 bits
+      for (int p = 0; p < 2; ++p)                  // R = b1 + b2 to 2^-16; the rotated row is rounded to 2^-11 next
         bulk_copy_hint(c.base + kOffK + p * kImgBytes, img + p * kImgBytes, kImgBytes, c.bar(kBImg), l2_evict_last());
     }
     __syncwarp();
@@ -1032,7 +1035,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
       }
     } else if (w < kRowWarps) {
       // q R_K has no channel above sqrt(128) max |q|, and one above max |q| / sqrt(128): 2^sigma brings that range to
-      // 2^7.5 .. 2^14.5, away from both ends of fp16
+      // 2^7.5 .. 2^14.5, away from both ends of fp16, the type the dequantised keys need (bf16 would keep 8 bits of them)
       const int ex = (int)(lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >> 7), sigma = min(max(137 - ex, -120), 100);
       const float sc = __int_as_float((127 + sigma) << 23);
       F *= __int_as_float((127 - sigma) << 23);

@@ -335,14 +335,17 @@ int oscar_decode_step_shared(oscar_cache* cache, int layer, int B, const void* q
 /* ---- verifying drafted tokens --------------------------------------------- */
 
 /* The steps of a speculative decoder's verify call, all on the device and capturable into a CUDA graph:
- * oscar_build_tables gives the requests their pages, oscar_tree_layout turns the draft's tree into masks and
- * positions, oscar_rope rotates q and k by them, oscar_tree_attention attends from every drafted node over the
- * cache and the node's drafted ancestors, and oscar_commit_draft moves the accepted path into the cache. */
+ * oscar_tree_layout turns the draft's tree into masks and positions, oscar_rope rotates q and k by them and
+ * oscar_tree_attention attends from every drafted node over the cache and the node's drafted ancestors. Drafted tokens
+ * are not in the cache and need no pages. Once the accepted counts are known, oscar_build_tables gives the requests
+ * the pages of their new lengths and oscar_commit_draft moves the accepted path into the cache. */
 
 #define OSCAR_MAX_DRAFT  256   /* largest T, drafted nodes of a request            */
 #define OSCAR_MAX_TABLE_BATCH 4096   /* largest B of oscar_build_tables            */
 
-/* Page tables and token slots of requests that go from old_lens[r] to new_lens[r] tokens.
+/* Page tables and token slots of requests that go from old_lens[r] to new_lens[r] tokens. old_lens are the lengths that
+ * the last call left: pages once taken go back only when the request is released, and a call that starts from less
+ * takes new ones for entries that are filled, whose old pages are then lost to the rings.
  *  old_lens, new_lens : device int32 [B]. new >= old >= 0 grows the request, new = 0 < old releases it.
  *  hist_pt, bf16_pt   : the page tables, as everywhere. Entries of pages that the new length adds are written,
  *                       those of a released request become -1, all others stay.
@@ -431,7 +434,10 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
  *                     bits from n_draft[r] on are ignored. Any pattern is allowed (oscar_tree_layout's, a chain, a
  *                     block), also an empty row, which then attends to the cache alone.
  *  n_draft          : device int32 [B] (0 .. T), or NULL: T
- *  seq_lens         : device int32 [B]: cached tokens (>= 0), all visible to every node
+ *  seq_lens         : device int32 [B]: cached tokens (>= 0), all visible to every node and read as they are: with a
+ *                     full recent window its oldest token is still BF16 here, while oscar_decode_step, which has the
+ *                     new token in the cache, moves it to the INT2 history before it attends. Below sink + recent
+ *                     tokens a single node is a decode step.
  *  out              : device [B][T][Hq][128], bf16 or fp32 (out_dtype), in the value basis of
  *                     oscar_decode_attention; lse : device float32 [B][T][Hq] or NULL
  *  workspace        : device, 256-byte aligned, of oscar_tree_workspace_bytes(cache, B, T, max_hist_pages) bytes; less
