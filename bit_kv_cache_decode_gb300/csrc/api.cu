@@ -106,25 +106,7 @@ LayerView view(const oscar_cache* c, int layer) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
-// max |U^T U - I| <= 1e-3, summed in double on the host's vector units: kLanes neighbouring columns at a time
-bool orthogonal(const float* U) {
-  constexpr int kLanes = 16;
-  std::array<double, (size_t)kD * kD> u;           // on the stack: the callers' threads neither allocate nor throw
-  std::copy(U, U + u.size(), u.begin());
-  bool ok = true;
-  for (int i = 0; i < kD; ++i)
-    for (int j0 = i / kLanes * kLanes; j0 < kD; j0 += kLanes) {
-      double s[kLanes] = {};
-      for (int r = 0; r < kD; ++r) {
-        const double x = u[(size_t)r * kD + i];
-        for (int j = 0; j < kLanes; ++j) s[j] += x * u[(size_t)r * kD + j0 + j];
-      }
-      for (int j = 0; j < kLanes; ++j) ok = ok && std::fabs(s[j] - (i == j0 + j ? 1.0 : 0.0)) <= 1e-3;   // false for NaN
-    }
-  return ok;
-}
-
-// whether f(0) .. f(n - 1) all hold, over as many threads as there are or can be had
+// whether f(0) .. f(n - 1) all hold, over a thread for every four of them, as far as there are or can be had
 template <typename F>
 bool all_of(int n, F f) {
   std::atomic<int> next{0};
@@ -134,7 +116,7 @@ bool all_of(int n, F f) {
       if (!f(i)) ok = false;
   };
   std::array<std::thread, 15> others;
-  const int most = std::min({n, (int)std::thread::hardware_concurrency(), (int)others.size() + 1});
+  const int most = std::min({(n + 3) / 4, (int)std::thread::hardware_concurrency(), (int)others.size() + 1});
   try {
     for (int i = 0; i + 1 < most; ++i) others[i] = std::thread(work);
   } catch (const std::system_error&) {               // no more threads: those there are do it
@@ -443,9 +425,7 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
   const bool expl = c->lay.v_mode == OSCAR_V_EXPLICIT;
   if (expl && !U_V) return OSCAR_ERR_INVALID_ARG;
   const int hkv = c->lay.num_kv_heads;
-  if (!all_of(hkv, [&](int h) {
-        return orthogonal(U_K + (size_t)h * kD * kD) && (!U_V || orthogonal(U_V + (size_t)h * kD * kD));
-      }))
+  if (!all_of(U_V ? 2 * hkv : hkv, [&](int i) { return orthogonal((i < hkv ? U_K : U_V) + (size_t)(i % hkv) * kD * kD); }))
     return OSCAR_ERR_NOT_ORTHOGONAL;
   // per head: the compact-format grid of each (kind, group), T = the group's largest threshold, D = fl32(2T / 255),
   // E = fl32(D / 3) (single-precision operations, each correctly rounded), then the uniform codebook of both kinds

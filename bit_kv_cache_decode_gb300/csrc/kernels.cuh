@@ -47,6 +47,7 @@ constexpr int kFragWords = 8 * 2 * 32 * 2;
 
 // the parameters of a layer that follow from U (in them already): V's transpose, rotations as operands (rotation_params.cu)
 int launch_rotation_params(float* params, int hkv, bool v, bool v_rotated, cudaStream_t st);
+bool orthogonal(const float* U);                     // host: max |U^T U - I| <= 1e-3 of a rotation (orthogonal.cpp)
 int launch_pack_rotated(const LayerView& lv, int kind, const float* xrot, const int* page_ids, const int* rows,
                         int N, cudaStream_t st);
 int launch_rotate(const LayerView& lv, int kind, const void* x, float* y, int N, cudaStream_t st);

@@ -5,9 +5,9 @@
 // column j of R is column bitrev7(j) of U H. R[i][j]: i = input channel, j = rotated channel.
 //
 // Thread = rotated channel, a CTA 8 input channels: each R element is 128 products in the order of m. 8 heads, K and V:
-// 33.6 million double-precision multiply-adds, 0.03 ms beside the copies. Loading a layer of 8 heads takes 0.9 ms with V
-// absorbed and 1.0 ms with V rotated, most of it the orthogonality check on the host (the same sums and conversions in
-// loops on the host: 25 and 40 ms).
+// 33.6 million double-precision multiply-adds. Loading a layer of 8 heads takes 0.45 ms with V absorbed and 0.53 ms with
+// V rotated, most of it the orthogonality check and the copies (the same sums and conversions in loops on the host: 25
+// and 40 ms).
 #include <cmath>
 
 #include "kernels.cuh"

@@ -119,7 +119,7 @@ def test_attention_straight_after_loading():
 
 @pytest.mark.parametrize("v_mode", [0, 1])
 def test_time_of_a_layer(v_mode):
-    # 0.9 and 1.0 ms for 8 heads; loops on one host thread took 25 and 40
+    # 0.45 and 0.53 ms for 8 heads; loops on one host thread took 25 and 40
     (uk, uv), (tk, tv) = inputs(4, 8)
     c = cache(v_mode, 8, 1)
     took = []
