@@ -9,7 +9,6 @@
 #include <cstring>
 #include <mutex>
 #include <new>
-#include <system_error>
 #include <thread>
 #include <vector>
 
@@ -119,7 +118,7 @@ bool all_of(int n, F f) {
   const int most = std::min({(n + 3) / 4, (int)std::thread::hardware_concurrency(), (int)others.size() + 1});
   try {
     for (int i = 0; i + 1 < most; ++i) others[i] = std::thread(work);
-  } catch (const std::system_error&) {               // no more threads: those there are do it
+  } catch (...) {                                    // no more threads: those there are do it
   }
   work();
   for (std::thread& t : others)
@@ -130,8 +129,8 @@ bool all_of(int n, F f) {
 // An append reads lengths, page tables and pool rows before it waits for the kernel before it on its stream. Where
 // that kernel may be one of this library's that writes tables or rows, the append is launched without the
 // programmatic overlap: a stream is noted by the writing calls, and its next append takes the note. Streams are
-// told apart by device and capture, since what is captured runs elsewhere; of more of them than kNotes (streams that
-// are never appended on) no account is kept, and every append waits.
+// told apart by device and capture, since what is captured runs elsewhere. Once kNotes are noted (streams that are never
+// appended on) no account is kept any more, and every append waits.
 constexpr size_t kNotes = 256;
 struct StreamNote {
   int dev;
@@ -140,8 +139,8 @@ struct StreamNote {
   bool operator==(const StreamNote& o) const { return dev == o.dev && st == o.st && capture == o.capture; }
 };
 std::mutex g_notes_mu;
-std::vector<StreamNote> g_notes;
-std::atomic<int> g_noted{0};                       // their number; kNotes: every append waits
+std::array<StreamNote, kNotes> g_notes;
+std::atomic<size_t> g_noted{0};                    // their number; kNotes: every append waits
 
 StreamNote note_of(cudaStream_t st) {
   StreamNote n = {0, st, 0};
@@ -153,31 +152,35 @@ StreamNote note_of(cudaStream_t st) {
 
 // what a call that launched a writer returns
 int wrote(int rc, cudaStream_t st) {
-  if (rc != OSCAR_OK || g_noted.load(std::memory_order_relaxed) >= (int)kNotes) return rc;
+  if (rc != OSCAR_OK || g_noted.load(std::memory_order_relaxed) == kNotes) return rc;
   const StreamNote n = note_of(st);
   std::lock_guard<std::mutex> lock(g_notes_mu);
-  for (StreamNote& o : g_notes)                    // a stream's earlier captures are over
+  const size_t noted = g_noted.load(std::memory_order_relaxed);
+  for (size_t i = 0; i < noted; ++i) {
+    StreamNote& o = g_notes[i];
     if (o.dev == n.dev && o.st == n.st && (o.capture != 0) == (n.capture != 0)) {
-      o.capture = n.capture;
+      o.capture = n.capture;                       // a stream's earlier captures are over
       return rc;
     }
-  g_notes.push_back(n);
-  g_noted.store((int)g_notes.size(), std::memory_order_relaxed);
+  }
+  if (noted == kNotes) return rc;
+  g_notes[noted] = n;
+  g_noted.store(noted + 1, std::memory_order_relaxed);
   return rc;
 }
 
 // whether an append on this stream has to wait before it reads anything
 bool takes_note(cudaStream_t st) {
-  const int noted = g_noted.load(std::memory_order_relaxed);
-  if (noted == 0) return false;
-  if (noted >= (int)kNotes) return true;
+  if (g_noted.load(std::memory_order_relaxed) == 0) return false;
   const StreamNote n = note_of(st);
   std::lock_guard<std::mutex> lock(g_notes_mu);
-  const auto at = std::find(g_notes.begin(), g_notes.end(), n);
-  if (at == g_notes.end()) return false;
+  const size_t noted = g_noted.load(std::memory_order_relaxed);
+  if (noted == kNotes) return true;
+  const auto end = g_notes.begin() + noted, at = std::find(g_notes.begin(), end, n);
+  if (at == end) return false;
   if (st != cudaStreamPerThread) {                 // one handle for the streams of all threads: kept
-    g_notes.erase(at);
-    g_noted.store((int)g_notes.size(), std::memory_order_relaxed);
+    *at = g_notes[noted - 1];
+    g_noted.store(noted - 1, std::memory_order_relaxed);
   }
   return true;
 }

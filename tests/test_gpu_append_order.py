@@ -3,6 +3,9 @@
 The appends read tables and rows before their programmatic wait, so behind such a call their launch must not be a
 programmatic dependent. Seen in captured graphs: the dependency into the append's kernel is then a full one."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -128,3 +131,37 @@ def test_results_straight_after(how):
         torch.cuda.synchronize()
     assert a.c.get_status() == b.c.get_status() == 0
     assert torch.equal(a.c.pool, b.c.pool)
+
+
+MANY = """
+import ctypes, sys
+sys.path.insert(0, "tests")
+import torch
+from test_gpu_append_order import Loop, PROGRAMMATIC, chain
+cu, s = ctypes.CDLL("libcuda.so.1"), Loop()
+s.write("prefill")
+s.append("append")
+torch.cuda.synchronize()
+def captured():
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        s.append("append")
+        s.append("append")
+    return chain(g)[-1] == PROGRAMMATIC
+assert captured()
+for i in range(300):
+    h = ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(h), 1) == 0
+    with torch.cuda.stream(torch.cuda.ExternalStream(h.value)):
+        s.write("tables")
+    torch.cuda.synchronize()
+    assert captured() == (i < 255), i
+assert s.c.get_status() == 0
+"""
+
+
+def test_more_streams_than_are_told_apart():
+    # in a process of its own: from then on all its appends wait
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", MANY], capture_output=True, text=True, cwd=root, env={**os.environ, "PYTHONPATH": root})
+    assert r.returncode == 0, r.stderr[-800:]
