@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kMaxDraft) k_tree_layout(const int* __restrict
   const int asked = n_draft != nullptr ? n_draft[b] : T, L = seq_lens[b];   // independent loads
   const int parent = i < T ? parents[(size_t)b * T + i] : -1;
   if ((asked < 0 || asked > T) && i == 0) flag(status, OSCAR_STATUS_BAD_TREE);
-  const bool fits = L >= 0 && L <= 0x7fffffff - T; // every node's position is a position
+  const bool fits = asked <= 0 || (L >= 0 && L <= 0x7fffffff - T);   // every node's position is a position
   if (!fits && i == 0) flag(status, OSCAR_STATUS_BAD_SEQLEN);
   const int n = fits ? min(max(asked, 0), T) : 0;
   if (i < T) {

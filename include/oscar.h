@@ -375,7 +375,8 @@ int oscar_build_tables(oscar_cache* cache, int B, const int32_t* old_lens, const
  *  mask      : device uint64 [B][T][(T + 63) / 64]: bit j of node i's words is set when j is i or above it
  *  positions : device int32 [B][T]: seq_lens[r] + the number of drafted nodes above i
  * Nodes from n_draft[r] on, nodes at or below a parent out of range (BAD_TREE), and all nodes of a request whose
- * length is negative or leaves no room for T positions below 2^31 (BAD_SEQLEN) get an empty mask and position -1.
+ * length is negative or leaves no room for T positions below 2^31 (BAD_SEQLEN) get an empty mask and position -1. The
+ * length of a request without nodes is not looked at.
  * Errors: INVALID_ARG (B < 0, T < 1, null pointers, mask not 8-byte aligned), UNSUPPORTED (T > OSCAR_MAX_DRAFT),
  * CUDA. */
 int oscar_tree_layout(oscar_cache* cache, int B, int T, const int32_t* parents, const int32_t* n_draft,
