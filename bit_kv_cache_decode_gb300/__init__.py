@@ -300,6 +300,8 @@ class OscarCache:
 
     # ---- entry points ---------------------------------------------------------------
     def set_rotation(self, layer: int, U_K, U_V, tau_K, tau_V, stream=None):
+        import torch
+        stream = torch.cuda.current_stream(self.pool.device) if stream is None else stream
         f32 = lambda a: None if a is None else np.ascontiguousarray(a, dtype=np.float32)
         uk, uv, tk, tv = f32(U_K), f32(U_V), f32(tau_K), f32(tau_V)
         _check(_lib.oscar_set_rotation(self._h, layer, _ptr(uk), _ptr(uv), _ptr(tk), _ptr(tv), _stream(stream)),

@@ -25,6 +25,7 @@ struct oscar_cache {
   size_t pool_bytes, ws_bytes;
   DecodeWorkspace dws;
   int* status;
+  int dev;                        // the device that was current when the cache was made
   int sms;
   int algo;
   int tree_rc;                    // what configuring the tree attention's kernels gave
@@ -368,6 +369,7 @@ int oscar_cache_create(const oscar_layout* layout, void* pool, void* workspace, 
   c->dws.trace_cap = 0;
   c->dws.nslots = partial_slots(layout->max_splits, (layout->sink + layout->recent) / kP);
   p += align_up(B * hq * c->dws.nslots * kPartFloats * sizeof(float));
+  c->dev = dev;
   c->sms = sms;
   c->algo = kDefaultDecodeAlgo;
   c->tree_rc = g_tree_rc[dev];
@@ -451,6 +453,16 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
     codebook_consts(kUniform, dst + kCbOff - kMetaCOff);
     codebook_consts(kUniform, dst + kCbOff - kMetaCOff + 8);
   }
+  // The kernel runs on the cache's device, whichever is current: loading layers needs no more than copies did.
+  struct OnDevice {
+    int before = -1;
+    explicit OnDevice(int dev) {
+      if (cudaGetDevice(&before) != cudaSuccess || before == dev || cudaSetDevice(dev) != cudaSuccess) before = -1;
+    }
+    ~OnDevice() {
+      if (before >= 0) cudaSetDevice(before);
+    }
+  } on_device(c->dev);
   // U, thresholds and constants as they are; a kernel makes the rest of the parameters from U. The sources are
   // pageable: a copy returns once its source has been staged, so it may be freed. Copies come last: the kernels that are
   // launched as programmatic dependents read parameters before they wait for a kernel before them.
