@@ -1101,6 +1101,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attention(LayerView lv
     tmem_wait_st();
   }
   if (w < kRowWarps && (WIDE || half == 0)) {
+    // Not 0, which times a masked logit's -inf would be NaN: a sum of products is below 2^40, so a factor this small or
+    // smaller gives weights of exactly 1 either way.
+    if (hist) F = fmaxf(F, 1.17549435e-38f);
     // a NaN or infinity in q: the whole row is NaN, as its formula's softmax is
     if (n > 0 && lds32(c.base + kOffJoin + 4 * (WIDE ? tid : row)) >= 0x7F80u) F = NAN;
     sts32(c.base + kOffF + 4 * (WIDE ? tid : row), __float_as_uint(F));

@@ -100,3 +100,22 @@ def test_any_negative_length_is_taken_as_none(length, v_mode):
         outs.append(cache.tree_attention(0, q, kd, vd, words, dev([n, 700]), hp, bp, synth.sm_scale(), workspace=ws))
         assert cache.get_status() == (0 if n == 0 else osc.STATUS_BAD_SEQLEN)
     assert torch.equal(outs[0], outs[1]) and outs[0].isfinite().all()
+
+
+@pytest.mark.parametrize("T", [6, 40])
+@pytest.mark.parametrize("meta", ["f16", "u8"])
+@pytest.mark.parametrize("sm", [1e-12, 1e-20, 1e-38, 1e-44])
+def test_the_smallest_scales_give_the_mean(T, meta, sm):
+    # every logit is 0 to float32, so each row is the mean of what it sees: rows of zeros, tiny, ordinary and large q
+    lens, hkv, gq = [64 + 256 + 64 * 3 + 9], 1, 4
+    case = build_decode_case(lens, hkv, gq, 0, seed=75, meta=meta)
+    cache, _, hp, bp = case
+    q, kd, vd = draft(75, 1, T, hkv, gq)
+    q[0, :, 0] = 0
+    q[0, :, 1] *= 2.0 ** -100
+    mask = random_mask(np.random.default_rng(6), 1, T, "tree")
+    lse = torch.zeros(1, T, gq, device=DEV)
+    out = cache.tree_attention(0, *(to_dev_bf16(x) for x in (q, kd, vd)), torch.from_numpy(mask_words(mask)).to(DEV), dev(lens), hp,
+                               bp, sm, out_dtype=osc.OUT_FP32, lse=lse)
+    assert cache.get_status() == 0
+    compare(out, lse, case, lens, q, kd, vd, mask, [T], 0, sm)
