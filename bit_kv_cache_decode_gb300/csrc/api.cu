@@ -432,10 +432,16 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
   const int hkv = c->lay.num_kv_heads;
   if (!all_of(U_V ? 2 * hkv : hkv, [&](int i) { return orthogonal((i < hkv ? U_K : U_V) + (size_t)(i % hkv) * kD * kD); }))
     return OSCAR_ERR_NOT_ORTHOGONAL;
-  // per head: the compact-format grid of each (kind, group), T = the group's largest threshold, D = fl32(2T / 255),
+  // What is copied, per head, from memory of this call's own (the caller's may change once it returns): U_K and U_V; the
+  // thresholds; the compact-format grid of each (kind, group), T = the group's largest threshold, D = fl32(2T / 255),
   // E = fl32(D / 3) (single-precision operations, each correctly rounded), then the uniform codebook of both kinds
-  std::vector<float> consts((size_t)hkv * kMetaCFloats, 0.f);
+  std::vector<float> rotations(2 * (size_t)hkv * kD * kD, 0.f), taus(2 * (size_t)hkv * kD), consts((size_t)hkv * kMetaCFloats, 0.f);
   for (int h = 0; h < hkv; ++h) {
+    float *u = rotations.data() + 2 * (size_t)h * kD * kD, *tau = taus.data() + 2 * (size_t)h * kD;
+    std::copy_n(U_K + (size_t)h * kD * kD, kD * kD, u);
+    if (U_V) std::copy_n(U_V + (size_t)h * kD * kD, kD * kD, u + kD * kD);
+    std::copy_n(tau_K + (size_t)h * kD, kD, tau);
+    std::copy_n(tau_V + (size_t)h * kD, kD, tau + kD);
     float* dst = consts.data() + (size_t)h * kMetaCFloats;
     for (int kind = 0; kind < 2; ++kind)
       for (int g = 0; g < kNG; ++g) {
@@ -463,22 +469,21 @@ int oscar_set_rotation(oscar_cache* c, int layer, const float* U_K, const float*
       if (before >= 0) cudaSetDevice(before);
     }
   } on_device(c->dev);
-  // U, thresholds and constants as they are; a kernel makes the rest of the parameters from U. The sources are
-  // pageable: a copy returns once its source has been staged, so it may be freed. Copies come last: the kernels that are
-  // launched as programmatic dependents read parameters before they wait for a kernel before them.
+  // A kernel makes the rest of the parameters from U. The sources are pageable: a copy returns once its source has been
+  // staged, so it may be freed. Copies come last: the kernels that are launched as programmatic dependents read
+  // parameters before they wait for a kernel before them.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* params = const_cast<float*>(view(c, layer).params);
-  auto put = [&](int off, const float* src, int floats) {
-    const size_t row = floats * sizeof(float);
-    return cudaMemcpy2DAsync(params + off, kParamFloats * sizeof(float), src, row, row, hkv, cudaMemcpyHostToDevice, st) ==
-           cudaSuccess;
+  static_assert(kUVOff == kUKOff + kD * kD && kTauVOff == kTauKOff + kD, "one copy each");
+  auto put = [&](int off, const std::vector<float>& src) {
+    const size_t row = src.size() / hkv * sizeof(float);
+    return cudaMemcpy2DAsync(params + off, kParamFloats * sizeof(float), src.data(), row, row, hkv, cudaMemcpyHostToDevice,
+                             st) == cudaSuccess;
   };
-  if (cudaMemsetAsync(params, 0, (size_t)hkv * kParamFloats * sizeof(float), st) != cudaSuccess ||
-      !put(kUKOff, U_K, kD * kD) || (U_V && !put(kUVOff, U_V, kD * kD)))
+  if (cudaMemsetAsync(params, 0, (size_t)hkv * kParamFloats * sizeof(float), st) != cudaSuccess || !put(kUKOff, rotations))
     return OSCAR_ERR_CUDA;
   if (int rc = launch_rotation_params(params, hkv, U_V != nullptr, expl, st); rc != OSCAR_OK) return rc;
-  const bool put_all = put(kTauKOff, tau_K, kD) && put(kTauVOff, tau_V, kD) && put(kMetaCOff, consts.data(), kMetaCFloats);
-  return put_all ? OSCAR_OK : OSCAR_ERR_CUDA;
+  return put(kTauKOff, taus) && put(kMetaCOff, consts) ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 int oscar_quantize_prefill(oscar_cache* c, int layer, int B, const void* k, const void* v, const int32_t* cu_seqlens,

@@ -5,7 +5,7 @@
 // column j of R is column bitrev7(j) of U H. R[i][j]: i = input channel, j = rotated channel.
 //
 // Thread = rotated channel, a CTA 8 input channels: each R element is 128 products in the order of m. 8 heads, K and V:
-// 33.6 million double-precision multiply-adds. Loading a layer of 8 heads takes 0.45 ms with V absorbed and 0.53 ms with
+// 33.6 million double-precision multiply-adds. Loading a layer of 8 heads takes 0.5 ms with V absorbed and 0.6 ms with
 // V rotated, most of it the orthogonality check and the copies (the same sums and conversions in loops on the host: 25
 // and 40 ms).
 #include <cmath>

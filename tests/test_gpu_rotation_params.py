@@ -119,7 +119,7 @@ def test_attention_straight_after_loading():
 
 @pytest.mark.parametrize("v_mode", [0, 1])
 def test_time_of_a_layer(v_mode):
-    # 0.45 and 0.53 ms for 8 heads; loops on one host thread took 25 and 40
+    # 0.5 and 0.6 ms for 8 heads; loops on one host thread took 25 and 40
     (uk, uv), (tk, tv) = inputs(4, 8)
     c = cache(v_mode, 8, 1)
     took = []
@@ -129,3 +129,23 @@ def test_time_of_a_layer(v_mode):
         torch.cuda.synchronize()
         took.append(time.perf_counter() - t)
     assert min(took) < 0.01
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+def test_the_sources_may_change_once_the_call_returns(pinned):
+    (uk, uv), (tk, tv) = inputs(5, 8)
+    c, busy = cache(1, 8, 1), torch.zeros(1 << 28, device=DEV)
+    c.set_rotation(0, uk, uv, tk, tv)
+    want = params(c, 0).copy()
+    for _ in range(5):
+        src = [torch.from_numpy(np.array(x)) for x in (uk, uv, tk, tv)]
+        if pinned:
+            src = [x.pin_memory() for x in src]
+        c.pool.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            busy.add_(1.0)                                 # the copies wait on the stream
+        c.set_rotation(0, *(x.numpy() for x in src))
+        for x in src:
+            x.fill_(7.0)
+        assert np.array_equal(params(c, 0).view(np.uint32), want.view(np.uint32))
