@@ -33,6 +33,7 @@ ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 ROPE_HALF, ROPE_PAIRS = 0, 1
 DTYPE_BF16, DTYPE_FP32, DTYPE_FP16 = 0, 1, 2
 MAX_DRAFT = 256
+MAX_ROPE_AXES = 4
 
 # every symbol include/oscar.h declares
 EXPORTS = (
@@ -45,6 +46,7 @@ EXPORTS = (
     "oscar_trace_timeline", "oscar_check_wait_timeout", "oscar_set_codebook", "oscar_calibrate_codebook",
     "oscar_build_tables", "oscar_tree_layout", "oscar_rope_frequencies", "oscar_rope_turns", "oscar_rope",
     "oscar_tree_workspace_bytes", "oscar_tree_attention", "oscar_commit_draft",
+    "oscar_rope_axes", "oscar_norm_rope", "oscar_norm_rope_backward", "oscar_norm_rope_workspace_bytes",
 )
 
 
@@ -63,6 +65,15 @@ class Layout(ctypes.Structure):
 class RopeTensor(ctypes.Structure):
     _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
         (n, ctypes.c_int64) for n in ("in_token", "in_head", "out_token", "out_head")] + [("heads", ctypes.c_int)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("num_axes", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -108,6 +119,14 @@ def _load() -> ctypes.CDLL:
         "oscar_rope_turns": [vp, c_int, vp],
         "oscar_rope": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p, vp, c_int,
                        c_int, c_float, c_int, vp],
+        "oscar_rope_axes": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p,
+                            ctypes.POINTER(Rotary), c_int, vp],
+        "oscar_norm_rope": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p,
+                            ctypes.POINTER(Rotary), ctypes.POINTER(HeadNorm), vp],
+        "oscar_norm_rope_workspace_bytes": [c_int, sz],
+        "oscar_norm_rope_backward": [ctypes.POINTER(RopeTensor)] * 4 + [c_int, c_int, c_int, i32p, ctypes.POINTER(Rotary),
+                                                                        ctypes.POINTER(HeadNorm), vp, vp, vp,
+                                                                        ctypes.c_size_t, vp],
         "oscar_tree_workspace_bytes": [vp, c_int, c_int, c_int, sz],
         "oscar_tree_attention": [vp, c_int, c_int, c_int, vp, vp, vp, vp, i32p, i32p, i32p, c_int, i32p, c_float, vp,
                                  c_int, vp, vp, ctypes.c_size_t, vp],
@@ -160,13 +179,14 @@ def _dev_i32(x, device):
 
 # torch's names that the calls below look up on every call, bound by the first of them: a call costs about 9 us on the
 # host, and looking them up afresh was 2 us of it
-_tensor = _i32 = _words = _bf16 = _f32 = _f16 = _empty = _get_device = _get_stream = None
+_tensor = _i32 = _words = _bf16 = _f32 = _f16 = _u8 = _empty = _get_device = _get_stream = None
 
 
 def _bind_torch():
-    global _tensor, _i32, _words, _bf16, _f32, _f16, _empty, _get_device, _get_stream
+    global _tensor, _i32, _words, _bf16, _f32, _f16, _u8, _empty, _get_device, _get_stream
     import torch
     _i32, _words, _bf16, _f32, _f16 = torch.int32, (torch.int64, torch.uint64), torch.bfloat16, torch.float32, torch.float16
+    _u8 = torch.uint8
     _empty, _get_device, _get_stream = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _tensor = torch.Tensor
 
@@ -606,11 +626,13 @@ def bf16_decode(kv_pages, q, seq_lens, page_table, sm_scale: float, num_kv_heads
 
 class RopePlan:
     """Rotary frequencies of a head's first rotary_dim channels (ROPE_* scaling) in the form rope() reads, on a
-    device; inv_freq (float64, radians per position and pair) may be given instead of the base and its scaling."""
+    device; inv_freq (float64, radians per position and pair) may be given instead of the base and its scaling.
+    axes: for positions with several axes (time, height, width) the axis of every pair, for instance
+    np.repeat([0, 1, 2], [16, 24, 24]); positions are then int32 [num_axes, N]."""
 
     def __init__(self, rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE, factor: float = 1.0,
                  original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None,
-                 scale: float | None = None, device="cuda"):
+                 scale: float | None = None, device="cuda", axes=None):
         import torch
         self.rotary_dim = int(rotary_dim)
         f = np.zeros(max(1, self.rotary_dim // 2), np.float64)
@@ -626,26 +648,37 @@ class RopePlan:
         _check(_lib.oscar_rope_turns(_ptr(f), f.size, _ptr(turns)), "oscar_rope_turns")
         self.inv_freq, self.scale = f, float(s.value) if scale is None else float(scale)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.axes, self.num_axes = None, 1
+        if axes is not None:
+            a = np.asarray(axes)
+            if a.shape != f.shape or a.dtype.kind not in "iu" or a.min() < 0 or a.max() >= MAX_ROPE_AXES:
+                raise OscarError(ERR_INVALID_ARG, "RopePlan: one axis per pair, 0 .. MAX_ROPE_AXES - 1")
+            self.num_axes = int(a.max()) + 1
+            self.axes = torch.from_numpy(a.astype(np.uint8)).to(device)
+
+    def rotary(self, layout: int) -> Rotary:
+        return Rotary(self.turns.data_ptr(), None if self.axes is None else self.axes.data_ptr(), self.num_axes,
+                      self.rotary_dim, layout, self.scale)
+
+    def positions(self, positions, dev: int, what: str):
+        """(positions, tokens): int32 [N], or [num_axes, N] where the plan has axes."""
+        pos = _in_i32(positions, dev)
+        if self.turns.get_device() != dev or (self.axes is not None and (pos.dim() != 2 or pos.shape[0] != self.num_axes)):
+            raise OscarError(ERR_INVALID_ARG, what)
+        return pos, pos.numel() if self.axes is None else pos.shape[1]
 
 
-def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool = False, q_out=None, k_out=None,
-         stream=None):
-    """Rotate q [N, Hq, D] and k [N, Hkv, D] (k may be None) by positions [N]; inverse gives the gradient. Token and
-    head strides are free, a head's channels contiguous. Written to q_out, k_out (new tensors when not given; the
-    inputs themselves for in place). Rows with a negative position are left as they are: new tensors hold them
-    unset. Returns (q_out, k_out)."""
-    if stream is not None:
-        with _on(stream):
-            return rope(plan, q, k, positions, layout, inverse, q_out, k_out)
-    dev, st = _here(q)
-    pos = _in_i32(positions, dev)
-    dtype, shape, n = q.dtype, q.shape, pos.numel()
+def _rows_code(dtype, what: str) -> int:
     code = DTYPE_BF16 if dtype is _bf16 else DTYPE_FP32 if dtype is _f32 else DTYPE_FP16
-    if (code == DTYPE_FP16 and dtype is not _f16) or plan.turns.get_device() != dev or len(shape) != 3 or n >> 31:
-        raise OscarError(ERR_INVALID_ARG, "oscar_rope")
-    dim = shape[2]
+    if code == DTYPE_FP16 and dtype is not _f16:
+        raise OscarError(ERR_INVALID_ARG, what)
+    return code
+
+
+def _rows(pairs, dtype, n: int, dim: int, dev: int, what: str):
+    """RopeTensors of (rows, results) pairs: rows [n, heads, dim] or None, results None for a new tensor."""
     args, outs = [], []
-    for x, out in ((q, q_out), (k, k_out)):
+    for x, out in pairs:
         if x is None:
             args.append(RopeTensor())
             outs.append(None)
@@ -654,15 +687,110 @@ def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool
             out = _empty(x.shape, dtype=dtype, device=dev)
         if x.dtype is not dtype or out.dtype is not dtype or x.get_device() != dev or out.get_device() != dev or \
                 x.dim() != 3 or x.shape != out.shape or x.shape[0] != n or x.shape[2] != dim:
-            raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+            raise OscarError(ERR_INVALID_ARG, what)
         (it, ih, ic), (ot, oh, oc) = x.stride(), out.stride()
         if dim > 1 and (ic != 1 or oc != 1):
-            raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+            raise OscarError(ERR_INVALID_ARG, what)
         args.append(RopeTensor(x.data_ptr(), out.data_ptr(), it, ih, ot, oh, x.shape[1]))
         outs.append(out)
-    _check(_lib.oscar_rope(args[0], args[1], n, dim, code, pos.data_ptr(), plan.turns.data_ptr(), plan.rotary_dim,
-                           layout, plan.scale, inverse, st), "oscar_rope")
+    return args, outs
+
+
+def rope(plan: RopePlan, q, k, positions, layout: int = ROPE_HALF, inverse: bool = False, q_out=None, k_out=None,
+         stream=None):
+    """Rotate q [N, Hq, D] and k [N, Hkv, D] (k may be None) by positions [N], or [num_axes, N] where the plan has axes;
+    inverse gives the gradient. Token and head strides are free, a head's channels contiguous. Written to q_out, k_out
+    (new tensors when not given; the inputs themselves for in place). Rows with a negative position (on any axis) are
+    left as they are: new tensors hold them unset. Returns (q_out, k_out)."""
+    if stream is not None:
+        with _on(stream):
+            return rope(plan, q, k, positions, layout, inverse, q_out, k_out)
+    dev, st = _here(q)
+    pos = _in_i32(positions, dev)
+    dtype, shape, n = q.dtype, q.shape, pos.numel()
+    if plan.axes is not None:
+        pos, n = plan.positions(pos, dev, "oscar_rope_axes")
+    code = DTYPE_BF16 if dtype is _bf16 else DTYPE_FP32 if dtype is _f32 else DTYPE_FP16
+    if (code == DTYPE_FP16 and dtype is not _f16) or plan.turns.get_device() != dev or len(shape) != 3 or n >> 31:
+        raise OscarError(ERR_INVALID_ARG, "oscar_rope")
+    dim = shape[2]
+    args, outs = _rows(((q, q_out), (k, k_out)), dtype, n, dim, dev, "oscar_rope")
+    if plan.axes is None:
+        _check(_lib.oscar_rope(args[0], args[1], n, dim, code, pos.data_ptr(), plan.turns.data_ptr(), plan.rotary_dim,
+                               layout, plan.scale, inverse, st), "oscar_rope")
+    else:
+        _check(_lib.oscar_rope_axes(args[0], args[1], n, dim, code, pos.data_ptr(), plan.rotary(layout), inverse, st),
+               "oscar_rope_axes")
     return outs[0], outs[1]
+
+
+def _head_norm(q_weight, k_weight, eps: float, dtype, dim: int, dev: int, what: str) -> HeadNorm:
+    for w in (q_weight, k_weight):
+        if w is not None:
+            _check_like(w, dtype, (dim,), dev, what)
+    return HeadNorm(_ptr(q_weight), _ptr(k_weight), eps)
+
+
+def norm_rope(plan: RopePlan, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, layout: int = ROPE_HALF,
+              q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of every head's row of q and k, times the weight [D] (of the rows' dtype; None: ones), then
+    rope() of the result, in one pass. Arguments and results as for rope()."""
+    if stream is not None:
+        with _on(stream):
+            return norm_rope(plan, q, k, positions, q_weight, k_weight, eps, layout, q_out, k_out)
+    dev, st = _here(q)
+    pos, n = plan.positions(positions, dev, "oscar_norm_rope")
+    dtype, shape = q.dtype, q.shape
+    code = _rows_code(dtype, "oscar_norm_rope")
+    if len(shape) != 3 or n >> 31:
+        raise OscarError(ERR_INVALID_ARG, "oscar_norm_rope")
+    norm = _head_norm(q_weight, k_weight, eps, dtype, shape[2], dev, "oscar_norm_rope")
+    args, outs = _rows(((q, q_out), (k, k_out)), dtype, n, shape[2], dev, "oscar_norm_rope")
+    _check(_lib.oscar_norm_rope(args[0], args[1], n, shape[2], code, pos.data_ptr(), plan.rotary(layout), norm, st),
+           "oscar_norm_rope")
+    return outs[0], outs[1]
+
+
+def norm_rope_backward(plan: RopePlan, q, k, positions, grad_q, grad_k, q_weight=None, k_weight=None, eps: float = 1e-6,
+                       layout: int = ROPE_HALF, dq=None, dk=None, weight_grads: bool = True, workspace=None, stream=None):
+    """Gradient of norm_rope() for the same q, k (k and grad_k may be None), positions and weights, from the gradients
+    grad_q, grad_k by its results. Returns (dq, dk, dq_weight, dk_weight): dq, dk of the rows' dtype (they may be grad_q
+    and grad_k, or q and k; rows with a negative position stay as they are), the weights' gradients float32 [D] (None
+    without weight_grads; the weight of a k that is None gets zeros). workspace: a uint8 tensor of
+    norm_rope_workspace_bytes(D), allocated per call when not given; calls that may overlap need one each."""
+    if stream is not None:
+        with _on(stream):
+            return norm_rope_backward(plan, q, k, positions, grad_q, grad_k, q_weight, k_weight, eps, layout, dq, dk,
+                                      weight_grads, workspace)
+    what = "oscar_norm_rope_backward"
+    dev, st = _here(q)
+    pos, n = plan.positions(positions, dev, what)
+    dtype, shape = q.dtype, q.shape
+    code = _rows_code(dtype, what)
+    if len(shape) != 3 or n >> 31 or grad_q is None or grad_q.shape != shape or (k is None) != (grad_k is None) or \
+            (k is not None and k.shape != grad_k.shape):
+        raise OscarError(ERR_INVALID_ARG, what)
+    dim = shape[2]
+    norm = _head_norm(q_weight, k_weight, eps, dtype, dim, dev, what)
+    grads, _ = _rows(((grad_q, grad_q), (grad_k, grad_k)), dtype, n, dim, dev, what)
+    args, outs = _rows(((q, dq), (k, dk)), dtype, n, dim, dev, what)
+    dw = ws = None
+    if weight_grads:
+        dw = _empty((2, dim), dtype=_f32, device=dev)
+        ws = q.new_empty(norm_rope_workspace_bytes(dim), dtype=_u8) if workspace is None else workspace
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise OscarError(ERR_INVALID_ARG, what)
+    _check(_lib.oscar_norm_rope_backward(args[0], args[1], grads[0], grads[1], n, dim, code, pos.data_ptr(),
+                                         plan.rotary(layout), norm, None if dw is None else dw.data_ptr(),
+                                         None if dw is None else dw.data_ptr() + 4 * dim, _ptr(ws),
+                                         0 if ws is None else ws.nbytes, st), what)
+    return outs[0], outs[1], None if dw is None else dw[0], None if dw is None else dw[1]
+
+
+def norm_rope_workspace_bytes(head_dim: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.oscar_norm_rope_workspace_bytes(head_dim, ctypes.byref(n)), "oscar_norm_rope_workspace_bytes")
+    return n.value
 
 
 def calibrate_codebook(x_rot, tau) -> np.ndarray:

@@ -106,6 +106,34 @@ LayerView view(const oscar_cache* c, int layer) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+// Checks of the calls that rotate rows; the tensors there are go to t. writes: whether they are written too.
+int check_rows(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype, const oscar_rotary* r,
+               bool writes, oscar_rope_tensor (&t)[2]) {
+  if (!r || N < 0 || head_dim < 2 || r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > head_dim) return OSCAR_ERR_INVALID_ARG;
+  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_FP32 && dtype != OSCAR_DTYPE_FP16) return OSCAR_ERR_INVALID_ARG;
+  if (r->layout != OSCAR_ROPE_HALF && r->layout != OSCAR_ROPE_PAIRS) return OSCAR_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale) || r->num_axes < 1 || r->num_axes > OSCAR_MAX_ROPE_AXES) return OSCAR_ERR_INVALID_ARG;
+  if (head_dim % 2 || head_dim > 512) return OSCAR_ERR_UNSUPPORTED;
+  const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
+  for (int i = 0; i < 2; ++i) {
+    const oscar_rope_tensor* x = i ? k : q;
+    if (!x || x->heads == 0) continue;
+    oscar_rope_tensor y = *x;
+    if (!writes) y.out = nullptr, y.out_token = y.out_head = 0;
+    if (y.heads < 0 || y.in_token < 0 || y.in_head < 0 || y.out_token < 0 || y.out_head < 0) return OSCAR_ERR_INVALID_ARG;
+    if (N > 0 && (!y.in || (writes && !y.out))) return OSCAR_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(y.in) | reinterpret_cast<uintptr_t>(y.out)) % size) return OSCAR_ERR_INVALID_ARG;
+    if (writes && y.in == y.out && (y.in_token != y.out_token || y.in_head != y.out_head)) return OSCAR_ERR_INVALID_ARG;
+    t[i] = y;
+  }
+  return OSCAR_OK;
+}
+int check_norm(const oscar_head_norm* n, int dtype) {
+  if (!n || !(n->eps > 0.f) || !std::isfinite(n->eps)) return OSCAR_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
+  return (reinterpret_cast<uintptr_t>(n->q_weight) | reinterpret_cast<uintptr_t>(n->k_weight)) % size ? OSCAR_ERR_INVALID_ARG : OSCAR_OK;
+}
+
 // whether f(0) .. f(n - 1) all hold, over a thread for every four of them, as far as there are or can be had
 template <typename F>
 bool all_of(int n, F f) {
@@ -746,26 +774,64 @@ int oscar_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
 int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
                const int32_t* positions, const uint64_t* turns, int rotary_dim, int layout, float scale, int inverse,
                void* stream) {
-  if (N < 0 || head_dim < 2 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return OSCAR_ERR_INVALID_ARG;
-  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_FP32 && dtype != OSCAR_DTYPE_FP16) return OSCAR_ERR_INVALID_ARG;
-  if (layout != OSCAR_ROPE_HALF && layout != OSCAR_ROPE_PAIRS) return OSCAR_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || (inverse != 0 && inverse != 1)) return OSCAR_ERR_INVALID_ARG;
-  if (head_dim % 2 || head_dim > 512) return OSCAR_ERR_UNSUPPORTED;
+  const oscar_rotary r = {turns, nullptr, 1, rotary_dim, layout, scale};
+  return oscar_rope_axes(q, k, N, head_dim, dtype, positions, &r, inverse, stream);
+}
+
+int oscar_rope_axes(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+                    const int32_t* positions, const oscar_rotary* rotary, int inverse, void* stream) {
   oscar_rope_tensor t[2] = {};
-  const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
-  for (int i = 0; i < 2; ++i) {
-    const oscar_rope_tensor* x = i ? k : q;
-    if (!x || x->heads == 0) continue;
-    if (x->heads < 0 || x->in_token < 0 || x->in_head < 0 || x->out_token < 0 || x->out_head < 0) return OSCAR_ERR_INVALID_ARG;
-    if (N > 0 && (!x->in || !x->out)) return OSCAR_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(x->in) | reinterpret_cast<uintptr_t>(x->out)) % size) return OSCAR_ERR_INVALID_ARG;
-    if (x->in == x->out && (x->in_token != x->out_token || x->in_head != x->out_head)) return OSCAR_ERR_INVALID_ARG;
-    t[i] = *x;
+  if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
+  if (inverse != 0 && inverse != 1) return OSCAR_ERR_INVALID_ARG;
+  if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
+  if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
+  return launch_rope(t[0], t[1], N, head_dim, dtype, positions, *rotary, inverse, static_cast<cudaStream_t>(stream));
+}
+
+int oscar_norm_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+                    const int32_t* positions, const oscar_rotary* rotary, const oscar_head_norm* norm, void* stream) {
+  oscar_rope_tensor t[2] = {};
+  if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
+  if (int rc = check_norm(norm, dtype); rc != OSCAR_OK) return rc;
+  if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
+  if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
+  return launch_norm_rope(t[0], t[1], nullptr, N, head_dim, dtype, positions, *rotary, *norm, nullptr, nullptr, nullptr,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int oscar_norm_rope_workspace_bytes(int head_dim, size_t* bytes) {
+  if (!bytes || head_dim < 2) return OSCAR_ERR_INVALID_ARG;
+  if (head_dim % 2 || head_dim > 512) return OSCAR_ERR_UNSUPPORTED;
+  *bytes = norm_rope_workspace_bytes(head_dim);
+  return OSCAR_OK;
+}
+
+int oscar_norm_rope_backward(const oscar_rope_tensor* q, const oscar_rope_tensor* k, const oscar_rope_tensor* grad_q,
+                             const oscar_rope_tensor* grad_k, int N, int head_dim, int dtype, const int32_t* positions,
+                             const oscar_rotary* rotary, const oscar_head_norm* norm, float* dq_weight, float* dk_weight,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  oscar_rope_tensor t[2] = {}, g[2] = {};
+  if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
+  if (int rc = check_rows(grad_q, grad_k, N, head_dim, dtype, rotary, false, g); rc != OSCAR_OK) return rc;
+  if (int rc = check_norm(norm, dtype); rc != OSCAR_OK) return rc;
+  if (g[0].heads != t[0].heads || g[1].heads != t[1].heads) return OSCAR_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)                        // in the place of the gradient: rows must fall on each other
+    if (g[i].heads != 0 && t[i].out == g[i].in && (t[i].out_token != g[i].in_token || t[i].out_head != g[i].in_head))
+      return OSCAR_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) % sizeof(float)) return OSCAR_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (int i = 0; i < 2; ++i) {                      // no rows: their weight's gradient is 0
+    float* dw = i ? dk_weight : dq_weight;
+    if (dw != nullptr && (N == 0 || t[i].heads == 0) && cudaMemsetAsync(dw, 0, head_dim * sizeof(float), st) != cudaSuccess)
+      return OSCAR_ERR_CUDA;
   }
   if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
-  if (!positions || !turns || !aligned8(turns)) return OSCAR_ERR_INVALID_ARG;
-  return launch_rope(t[0], t[1], N, head_dim, rotary_dim, dtype, positions, turns, layout, scale, inverse,
-                     static_cast<cudaStream_t>(stream));
+  if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
+  float* dqw = t[0].heads ? dq_weight : nullptr;
+  float* dkw = t[1].heads ? dk_weight : nullptr;
+  if ((dqw || dkw) && (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_workspace_bytes(head_dim)))
+    return OSCAR_ERR_INVALID_ARG;
+  return launch_norm_rope(t[0], t[1], g, N, head_dim, dtype, positions, *rotary, *norm, dqw, dkw, static_cast<float*>(workspace), st);
 }
 
 int oscar_tree_workspace_bytes(const oscar_cache* c, int B, int T, int max_hist_pages, size_t* bytes) {

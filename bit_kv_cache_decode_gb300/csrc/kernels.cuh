@@ -115,8 +115,13 @@ int configure_merge_kernel();
 
 // verifying drafted tokens: rope.cu, tables.cu, tree_attention.cu, tree_merge.cu, commit.cu
 constexpr int kMaxDraft = OSCAR_MAX_DRAFT, kMaxTableBatch = OSCAR_MAX_TABLE_BATCH;
-int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, int dim, int rot, int dtype,
-                const int* positions, const uint64_t* turns, int layout, float scale, int inverse, cudaStream_t st);
+int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, int dim, int dtype, const int* positions,
+                const oscar_rotary& r, int inverse, cudaStream_t st);
+// norm_rope.cu: grad (the gradients of q's and k's results) null: forward
+int launch_norm_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, const oscar_rope_tensor* grad, int n, int dim,
+                     int dtype, const int* positions, const oscar_rotary& r, const oscar_head_norm& norm, float* dqw, float* dkw,
+                     float* partials, cudaStream_t st);
+size_t norm_rope_workspace_bytes(int dim);
 int launch_build_tables(const oscar_layout& lay, int B, const int* old_lens, const int* new_lens, int* hist_pt,
                         int max_hist_pages, int* bf16_pt, int* free_int2, int* free_bf16, const int* rings_in,
                         int* rings_out, int* cu_tokens, int* slots, int max_tokens, int* status, unsigned* ticket,

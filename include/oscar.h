@@ -429,6 +429,54 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
                const int32_t* positions, const uint64_t* turns, int rotary_dim, int layout, float scale, int inverse,
                void* stream);
 
+/* A rotation as the calls below take it. Positions may have several axes (time, height and width of images and video):
+ * pair i then turns by its frequency and the token's position on axis axes[i]. */
+#define OSCAR_MAX_ROPE_AXES 4
+typedef struct oscar_rotary {
+  const uint64_t* turns;           /* device [rotary_dim / 2] from oscar_rope_turns, 8-byte aligned                */
+  const uint8_t* axes;             /* device [rotary_dim / 2], or NULL: axis 0. Values from num_axes on count as
+                                      num_axes - 1                                                                */
+  int num_axes;                    /* 1 .. OSCAR_MAX_ROPE_AXES                                                    */
+  int rotary_dim, layout;          /* as for oscar_rope                                                           */
+  float scale;
+} oscar_rotary;
+
+/* oscar_rope with positions on several axes: positions is device int32 [num_axes][N]. A row with a negative position on
+ * any axis is left as it is. With one axis the results are oscar_rope's, bit by bit. Errors: as oscar_rope, INVALID_ARG
+ * (num_axes out of range). Works without a cache. */
+int oscar_rope_axes(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+                    const int32_t* positions, const oscar_rotary* rotary, int inverse, void* stream);
+
+/* Root-mean-square norm of every head's row and the rotation of the result, in one pass:
+ *   y = Rot(x r w),  r = (mean of x^2 over the head's channels + eps)^-1/2.
+ * All channels are normalised, the first rotary_dim of them rotated. Everything is float32 up to one rounding at the
+ * end (squares beyond float32's range are the caller's to avoid). q and k, positions and padded rows as for
+ * oscar_rope_axes; out = in with equal strides works in place.
+ *  q_weight, k_weight : device [head_dim], of the rows' dtype, or NULL: ones;  eps > 0
+ * Errors: as oscar_rope_axes, INVALID_ARG (eps, a weight not aligned to its type). Works without a cache. */
+typedef struct oscar_head_norm {
+  const void *q_weight, *k_weight;
+  float eps;
+} oscar_head_norm;
+int oscar_norm_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
+                    const int32_t* positions, const oscar_rotary* rotary, const oscar_head_norm* norm, void* stream);
+
+/* Gradient of oscar_norm_rope. q, k: in = the rows that were normalised, out = the gradient by them; grad_q, grad_k: in =
+ * the gradient by the results (heads as in q and k; out is not used). With g that gradient: h = Rot^T g, u = h w,
+ *   dx = r (u - x r^2 mean(u x)),   dw = sum over tokens and heads of h x r.
+ * out may be in, or the gradient that was given, with equal strides. Rows with a negative position are left as they are
+ * and add nothing to dw.
+ *  dq_weight, dk_weight : device float32 [head_dim], written (not added to), each may be NULL. Sums are taken in an order
+ *                         that depends on the sizes alone: the same inputs give the same bits. No rows give zeros.
+ *  workspace : device, 16-byte aligned, of oscar_norm_rope_workspace_bytes(head_dim) bytes, not needed (NULL) without
+ *              weight gradients; calls that may overlap need one each
+ * Errors: as oscar_norm_rope, INVALID_ARG (workspace too small). Works without a cache. */
+int oscar_norm_rope_workspace_bytes(int head_dim, size_t* bytes);
+int oscar_norm_rope_backward(const oscar_rope_tensor* q, const oscar_rope_tensor* k, const oscar_rope_tensor* grad_q,
+                             const oscar_rope_tensor* grad_k, int N, int head_dim, int dtype, const int32_t* positions,
+                             const oscar_rotary* rotary, const oscar_head_norm* norm, float* dq_weight, float* dk_weight,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Attention of drafted nodes over the cache and their drafted ancestors.
  *  q                : device bf16 [B][T][Hq][128]; k_draft, v_draft : device bf16 [B][T][Hkv][128] (not in the cache)
  *  mask             : device uint64 [B][T][(T + 63) / 64]: bit j of row i lets node i attend to drafted node j;
