@@ -47,6 +47,7 @@ EXPORTS = (
     "oscar_build_tables", "oscar_tree_layout", "oscar_rope_frequencies", "oscar_rope_turns", "oscar_rope",
     "oscar_tree_workspace_bytes", "oscar_tree_attention", "oscar_commit_draft",
     "oscar_rope_axes", "oscar_norm_rope", "oscar_norm_rope_backward", "oscar_norm_rope_workspace_bytes",
+    "oscar_append_kv_rope", "oscar_decode_step_rope",
 )
 
 
@@ -70,6 +71,11 @@ class RopeTensor(ctypes.Structure):
 class Rotary(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("num_axes", ctypes.c_int),
                 ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class RawStep(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in "qkv"] + [(n, ctypes.c_int64) for n in ("q_row", "k_row", "v_row")] + [
+        (n, ctypes.c_void_p) for n in ("q_out", "positions", "rotary", "norm")]
 
 
 class HeadNorm(ctypes.Structure):
@@ -123,6 +129,9 @@ def _load() -> ctypes.CDLL:
                             ctypes.POINTER(Rotary), c_int, vp],
         "oscar_norm_rope": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p,
                             ctypes.POINTER(Rotary), ctypes.POINTER(HeadNorm), vp],
+        "oscar_append_kv_rope": [vp, c_int, c_int, ctypes.POINTER(RawStep), i32p, i32p, c_int, i32p, vp],
+        "oscar_decode_step_rope": [vp, c_int, c_int, ctypes.POINTER(RawStep), i32p, i32p, c_int, c_int, i32p, c_float, vp,
+                                   c_int, vp, vp],
         "oscar_norm_rope_workspace_bytes": [c_int, sz],
         "oscar_norm_rope_backward": [ctypes.POINTER(RopeTensor)] * 4 + [c_int, c_int, c_int, i32p, ctypes.POINTER(Rotary),
                                                                         ctypes.POINTER(HeadNorm), vp, vp, vp,
@@ -412,6 +421,93 @@ class OscarCache:
             _check(_lib.oscar_decode_step(self._h, layer, sl.numel(), _ptr(q), _ptr(k), _ptr(v), _ptr(sl), _ptr(hp),
                                           mhp, _ptr(bp), float(sm_scale), _ptr(out), out_dtype, _ptr(lse),
                                           _stream(stream)), "oscar_decode_step")
+        return out
+
+    # ---- a token's raw projections ---------------------------------------------------
+    def _raw_step(self, plan, q, k, v, q_weight, k_weight, eps, positions, layout, q_out, B: int, dev: int, what: str):
+        """(RawStep, q_out, what has to live until the call) of raw rows q [B, Hq, 128] (or None), k and v [B, Hkv, 128]."""
+        heads, d = (self.cfg.num_q_heads, self.cfg.num_kv_heads, self.cfg.num_kv_heads), self.cfg.head_dim
+        rows = []
+        for x, h in zip((q, k, v), heads):
+            if x is None and not rows:   # no queries: k and v are appended
+                rows.append(0)
+                continue
+            if x is None or x.dtype is not _bf16 or x.get_device() != dev or x.shape != (B, h, d) or x.stride(2) != 1 or \
+                    (h > 1 and x.stride(1) != d):
+                raise OscarError(ERR_INVALID_ARG, what)
+            rows.append(x.stride(0) if B > 1 else h * d)
+        if q is not None:
+            if q_out is None:
+                q_out = _empty((B, heads[0], d), dtype=_bf16, device=dev)
+            else:
+                _check_like(q_out, _bf16, (B, heads[0], d), dev, what)
+        pos = None
+        if positions is None:
+            if plan.turns.get_device() != dev:
+                raise OscarError(ERR_INVALID_ARG, what)
+        else:
+            pos, n = plan.positions(positions, dev, what)
+            if n != B:
+                raise OscarError(ERR_INVALID_ARG, what)
+        rotary = plan.rotary(layout)
+        norm = None if eps is None else _head_norm(q_weight, k_weight, eps, _bf16, d, dev, what)
+        step = RawStep(_ptr(q), k.data_ptr(), v.data_ptr(), *rows, _ptr(q_out), _ptr(pos), ctypes.addressof(rotary),
+                       None if norm is None else ctypes.addressof(norm))
+        return step, q_out, (rotary, norm, pos)
+
+    def _step_tables(self, seq_lens, hist_pt, bf16_pt, dev: int, what: str):
+        sl, hp, bp = _in_i32(seq_lens, dev), _in_i32(hist_pt, dev), _in_i32(bf16_pt, dev)
+        B, mhp = sl.numel(), hp.shape[1] if hp.dim() == 2 else 0
+        if hp.numel() != B * mhp or bp.numel() != B * ((self.cfg.sink + self.cfg.recent) // self.cfg.page_size):
+            raise OscarError(ERR_INVALID_ARG, what)
+        return sl, hp, bp, B, mhp
+
+    def append_kv_rope(self, layer: int, plan: RopePlan, q, k, v, seq_lens_before, hist_pt, bf16_pt, q_weight=None,
+                       k_weight=None, eps: float | None = 1e-6, positions=None, layout: int = ROPE_HALF, q_out=None,
+                       stream=None):
+        """append_kv of one token per request from its raw projections: norm_rope() of q [B, Hq, 128] (or None) and k
+        [B, Hkv, 128] on the way (eps None: the rotation alone), at positions [B] ([num_axes, B] where the plan has axes),
+        seq_lens_before by default. Rows of q, k and v may be views of one projection. Returns q_out, the queries for
+        decode_attention. As for append_kv, lengths and tables may not come from a kernel launched just before."""
+        if stream is not None:
+            with _on(stream):
+                return self.append_kv_rope(layer, plan, q, k, v, seq_lens_before, hist_pt, bf16_pt, q_weight, k_weight, eps,
+                                           positions, layout, q_out)
+        dev, st = _here(self.pool)
+        sl, hp, bp, B, mhp = self._step_tables(seq_lens_before, hist_pt, bf16_pt, dev, "oscar_append_kv_rope")
+        step, q_out, _keep = self._raw_step(plan, q, k, v, q_weight, k_weight, eps, positions, layout, q_out, B, dev,
+                                            "oscar_append_kv_rope")
+        _check(_lib.oscar_append_kv_rope(self._h, layer, B, step, sl.data_ptr(), hp.data_ptr(), mhp, bp.data_ptr(), st),
+               "oscar_append_kv_rope")
+        return q_out
+
+    def decode_step_rope(self, layer: int, plan: RopePlan, q, k, v, seq_lens_before, hist_pt, bf16_pt, sm_scale: float,
+                         q_weight=None, k_weight=None, eps: float | None = 1e-6, positions=None, layout: int = ROPE_HALF,
+                         q_out=None, out=None, out_dtype: int = OUT_BF16, lse=None, stream=None,
+                         shared_hist_pages: int = 0):
+        """decode_step from raw projections, arguments as for append_kv_rope: the same three launches, with the norm and
+        the rotation in the first. q_out [B, Hq, 128] receives the queries (allocated per call when not given)."""
+        if stream is not None:
+            with _on(stream):
+                return self.decode_step_rope(layer, plan, q, k, v, seq_lens_before, hist_pt, bf16_pt, sm_scale, q_weight,
+                                             k_weight, eps, positions, layout, q_out, out, out_dtype, lse,
+                                             shared_hist_pages=shared_hist_pages)
+        dev, st = _here(self.pool)
+        sl, hp, bp, B, mhp = self._step_tables(seq_lens_before, hist_pt, bf16_pt, dev, "oscar_decode_step_rope")
+        if q is None:
+            raise OscarError(ERR_INVALID_ARG, "oscar_decode_step_rope")
+        step, q_out, _keep = self._raw_step(plan, q, k, v, q_weight, k_weight, eps, positions, layout, q_out, B, dev,
+                                            "oscar_decode_step_rope")
+        rows, out_type = (B, self.cfg.num_q_heads, self.cfg.head_dim), _f32 if out_dtype == OUT_FP32 else _bf16
+        if out is None:
+            out = _empty(rows, dtype=out_type, device=dev)
+        else:
+            _check_like(out, out_type, rows, dev, "oscar_decode_step_rope")
+        if lse is not None:
+            _check_like(lse, _f32, rows[:2], dev, "oscar_decode_step_rope")
+        _check(_lib.oscar_decode_step_rope(self._h, layer, B, step, sl.data_ptr(), hp.data_ptr(), mhp, int(shared_hist_pages),
+                                           bp.data_ptr(), float(sm_scale), out.data_ptr(), out_dtype, _ptr(lse), st),
+               "oscar_decode_step_rope")
         return out
 
     # ---- verifying drafted tokens -----------------------------------------------------

@@ -133,6 +133,29 @@ int check_norm(const oscar_head_norm* n, int dtype) {
   const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
   return (reinterpret_cast<uintptr_t>(n->q_weight) | reinterpret_cast<uintptr_t>(n->k_weight)) % size ? OSCAR_ERR_INVALID_ARG : OSCAR_OK;
 }
+// a raw step's rows and rotation, as the prologue takes them
+int check_raw(const oscar_cache* c, int B, const oscar_raw_step* x, bool prepare, RawStep* raw) {
+  if (!c || !x || !x->rotary || B < 0) return OSCAR_ERR_INVALID_ARG;
+  const oscar_rotary& r = *x->rotary;
+  if (r.rotary_dim < 2 || r.rotary_dim % 2 || r.rotary_dim > kD || !std::isfinite(r.scale)) return OSCAR_ERR_INVALID_ARG;
+  if ((r.layout != OSCAR_ROPE_HALF && r.layout != OSCAR_ROPE_PAIRS) || r.num_axes < 1 || r.num_axes > OSCAR_MAX_ROPE_AXES)
+    return OSCAR_ERR_INVALID_ARG;
+  if (x->norm)
+    if (int rc = check_norm(x->norm, OSCAR_DTYPE_BF16); rc != OSCAR_OK) return rc;
+  if (B == 0) return OSCAR_OK;
+  if (!r.turns || !aligned8(r.turns) || !x->k || !x->v || (prepare && !x->q) || (x->q && !x->q_out)) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16(x->q) || !aligned16(x->k) || !aligned16(x->v) || (x->q && !aligned16(x->q_out))) return OSCAR_ERR_INVALID_ARG;
+  if ((x->q && (x->q_row < 0 || x->q_row % 8)) || x->k_row < 0 || x->k_row % 8 || x->v_row < 0 || x->v_row % 8)
+    return OSCAR_ERR_INVALID_ARG;
+  if (x->q && x->q == x->q_out && x->q_row != (int64_t)c->lay.num_q_heads * kD) return OSCAR_ERR_INVALID_ARG;
+  *raw = {x->q_row, x->k_row, x->v_row, static_cast<__nv_bfloat16*>(x->q_out), nullptr, nullptr, rotary_of(r, x->positions, B),
+          x->norm ? x->norm->eps : 0.f, x->norm != nullptr, r.layout == OSCAR_ROPE_PAIRS, prepare};
+  if (x->norm) {
+    raw->qw = static_cast<const __nv_bfloat16*>(x->norm->q_weight);
+    raw->kw = static_cast<const __nv_bfloat16*>(x->norm->k_weight);
+  }
+  return OSCAR_OK;
+}
 
 // whether f(0) .. f(n - 1) all hold, over a thread for every four of them, as far as there are or can be had
 template <typename F>
@@ -622,7 +645,8 @@ int decode_impl(oscar_cache* c, int layer, int B, const void* q, const int32_t* 
 
 int step_impl(oscar_cache* c, int layer, int B, const void* q, const void* k, const void* v,
               const int32_t* seq_lens_before, const int32_t* hist_pt, int max_hist_pages, int shared_pages,
-              const int32_t* bf16_pt, float sm_scale, void* out, int out_dtype, float* lse, void* stream) {
+              const int32_t* bf16_pt, float sm_scale, void* out, int out_dtype, float* lse, void* stream,
+              const RawStep* raw = nullptr) {
   if (!c || layer < 0 || layer >= c->lay.num_layers || B < 0 || B > c->lay.max_batch || max_hist_pages < 0)
     return OSCAR_ERR_INVALID_ARG;
   if (shared_pages < 0 || shared_pages > max_hist_pages) return OSCAR_ERR_INVALID_ARG;
@@ -636,7 +660,7 @@ int step_impl(oscar_cache* c, int layer, int B, const void* q, const void* k, co
   LayerView lv = view(c, layer);
   DecodeArgs a;
   a.B = B;
-  a.q = q;
+  a.q = raw ? raw->q_out : q;            // the prologue's queries, for the BF16 rows
   a.seq_lens = seq_lens_before;
   a.len_add = 1;                         // attend over the appended token too
   a.skip_qprep = 1;                      // the step prologue below rotates the queries
@@ -659,7 +683,7 @@ int step_impl(oscar_cache* c, int layer, int B, const void* q, const void* k, co
   // one prologue launch (append with demotion, and the query prologue), then the decode and the
   // merge, each a programmatic dependent of the kernel before it
   const int rc = launch_prologue(lv, c->dws, B, q, k, v, seq_lens_before, hist_pt, max_hist_pages, bf16_pt,
-                                 sm_scale, st, takes_note(st));
+                                 sm_scale, st, takes_note(st), raw);
   if (rc != OSCAR_OK) return rc;
   return launch_decode(lv, c->dws, a, st);
 }
@@ -832,6 +856,27 @@ int oscar_norm_rope_backward(const oscar_rope_tensor* q, const oscar_rope_tensor
   if ((dqw || dkw) && (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_workspace_bytes(head_dim)))
     return OSCAR_ERR_INVALID_ARG;
   return launch_norm_rope(t[0], t[1], g, N, head_dim, dtype, positions, *rotary, *norm, dqw, dkw, static_cast<float*>(workspace), st);
+}
+
+int oscar_append_kv_rope(oscar_cache* c, int layer, int B, const oscar_raw_step* x, const int32_t* seq_lens_before,
+                         const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream) {
+  RawStep raw = {};
+  if (int rc = check_raw(c, B, x, false, &raw); rc != OSCAR_OK) return rc;
+  if (layer < 0 || layer >= c->lay.num_layers || max_hist_pages < 0) return OSCAR_ERR_INVALID_ARG;
+  if (B == 0) return OSCAR_OK;
+  if (!seq_lens_before || !bf16_pt || (max_hist_pages > 0 && !hist_pt)) return OSCAR_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_prologue(view(c, layer), DecodeWorkspace{}, B, x->q, x->k, x->v, seq_lens_before, hist_pt, max_hist_pages,
+                         bf16_pt, 1.f, st, takes_note(st), &raw);
+}
+
+int oscar_decode_step_rope(oscar_cache* c, int layer, int B, const oscar_raw_step* x, const int32_t* seq_lens_before,
+                           const int32_t* hist_pt, int max_hist_pages, int shared_hist_pages, const int32_t* bf16_pt,
+                           float sm_scale, void* out, int out_dtype, float* lse, void* stream) {
+  RawStep raw = {};
+  if (int rc = check_raw(c, B, x, true, &raw); rc != OSCAR_OK) return rc;
+  return step_impl(c, layer, B, x->q, x->k, x->v, seq_lens_before, hist_pt, max_hist_pages, shared_hist_pages, bf16_pt, sm_scale,
+                   out, out_dtype, lse, stream, &raw);
 }
 
 int oscar_tree_workspace_bytes(const oscar_cache* c, int B, int T, int max_hist_pages, size_t* bytes) {

@@ -45,6 +45,29 @@ constexpr int kQSigma = 9;               // sigma, the power-of-two scale of the
 // 8 k-blocks x 2 n-tiles x 32 lanes x 2 registers.
 constexpr int kFragWords = 8 * 2 * 32 * 2;
 
+// A plan on the device, and where the tokens are on its axes.
+struct Rotary {
+  const int* positions;                            // [axes][n]
+  const unsigned long long* turns;                 // [rot / 2]
+  const uint8_t* axes;                             // [rot / 2], or null: axis 0
+  int n, rot, n_axes;
+  float scale;
+};
+inline Rotary rotary_of(const oscar_rotary& r, const int* positions, int n) {
+  return {positions, reinterpret_cast<const unsigned long long*>(r.turns), r.axes, n, r.rotary_dim, r.num_axes, r.scale};
+}
+
+constexpr int kRopeAxes = OSCAR_MAX_ROPE_AXES;
+// Raw q, k and v of one token per request, normalised and rotated by the prologue.
+struct RawStep {
+  long long q_row, k_row, v_row;                   // elements between two requests
+  __nv_bfloat16* q_out;                            // [B][hq][kD]
+  const __nv_bfloat16 *qw, *kw;                    // [kD], or null: ones
+  Rotary r;                                        // positions null: the request's length
+  float eps;
+  int normed, pairs, prepare;                      // prepare: the queries' fragments too (a decode follows)
+};
+
 // the parameters of a layer that follow from U (in them already): V's transpose, rotations as operands (rotation_params.cu)
 int launch_rotation_params(float* params, int hkv, bool v, bool v_rotated, cudaStream_t st);
 bool orthogonal(const float* U);                     // host: max |U^T U - I| <= 1e-3 of a rotation (orthogonal.cpp)
@@ -64,7 +87,7 @@ int configure_project_prefill_kernel();
 int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const void* q, const void* k,
                     const void* v, const int* seq_lens_before, const int* hist_pt, int max_hist_pages,
                     const int* bf16_pt, float sm_scale, cudaStream_t st,
-                    bool after_all = false);
+                    bool after_all = false, const RawStep* raw = nullptr);
 int configure_prologue_kernel();
 int configure_write_path_kernels();
 int configure_prefill_kernel();   // prefill_tc.cu

@@ -1,5 +1,5 @@
 // Step prologue (sm_103a): the append with demotion and the decode's query
-// prologue in one launch.
+// prologue in one launch; optionally with the norm and the rotation of raw q and k on the way.
 //
 // * Append (news article "超越 TurboQuant…OSCAR…", section "OSCAR 的设计思路":
 //   the new token enters the recent window, and the oldest recent token is
@@ -25,7 +25,14 @@
 // dependent launch) before it reads q, k and v, then lets the decode be
 // scheduled. Sequence lengths, page tables and the pool's rows (inputs the
 // kernel before does not produce) are read before that wait.
+//
+// From raw rows (RAW: oscar_append_kv_rope, oscar_decode_step_rope): after the wait eight lanes a row normalise and
+// rotate the gq query rows of the head and its new key row (norm_rope.cu's formulas: float32, one rounding to BF16), 16
+// channels a lane; the sum of squares is three shuffles, a pair's partner comes through shared memory. The results are
+// what the rest of the kernel takes for q and k, and the queries are written out for the kernels behind. The angles
+// (64 of them, all heads share the request's position) are made before the wait where the position is the request's length.
 #include "kernels.cuh"
+#include "rope.cuh"
 #include "rotate.cuh"
 #include "tma.cuh"
 #include "timeline.cuh"
@@ -39,11 +46,43 @@ __device__ __forceinline__ bool valid_page(int p, int n) { return p >= 0 && p < 
 // smem: rotation fragments | 16-row tile | tau | 8 mbarriers
 constexpr int kTileFloats = 16 * kTileStride;
 
+// Eight lanes' rows (a group of lanes per row, l the lane in it): norm and rotation of the 128 channels x[16] (channels
+// 8 l .. and 64 + 8 l ..), through the float row buf of this group; y gets the same channels' results.
+__device__ __forceinline__ void norm_rope_row(const float (&x)[16], const float (&w)[16], const RawStep& raw, const float2* cs,
+                                              float* buf, int l, float (&y)[16]) {
+  float r = 1.f;
+  if (raw.normed) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    r = rsqrtf(ss * (1.f / kD) + raw.eps);
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    y[e] = raw.normed ? x[e] * (r * w[e]) : x[e];
+    buf[(e < 8 ? 8 * l : 56 + 8 * l) + e] = y[e];
+  }
+  __syncwarp();
+  const int rot = raw.r.rot, half = rot / 2;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int c = (e < 8 ? 8 * l : 56 + 8 * l) + e;
+    if (c >= rot) continue;
+    const bool second = raw.pairs ? (c & 1) != 0 : c >= half;
+    const int j = raw.pairs ? c >> 1 : second ? c - half : c, partner = raw.pairs ? c ^ 1 : second ? c - half : c + half;
+    const float2 t = cs[j];
+    y[e] = second ? y[e] * t.x + buf[partner] * t.y : y[e] * t.x - buf[partner] * t.y;
+  }
+}
+
+template <bool RAW>
 __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
     k_step_prologue(LayerView lv, DecodeWorkspace ws, const __nv_bfloat16* __restrict__ q,
                     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                     const int* __restrict__ seq_lens_before, const int* __restrict__ hist_pt, int max_hist_pages,
-                    const int* __restrict__ bf16_pt, float scale_log2) {
+                    const int* __restrict__ bf16_pt, float scale_log2, RawStep raw) {
   TimelineSpan timeline_span(lv, k != nullptr ? kTlAppend : kTlQprep);
   extern __shared__ __align__(128) float smem[];
   uint32_t* frag_s = reinterpret_cast<uint32_t*>(smem);
@@ -55,7 +94,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int gq = lv.hq / lv.hkv;
   const float* prm = lv.params + (size_t)h * kParamFloats;
-  const bool do_q = q != nullptr && kind == OSCAR_KIND_K;
+  const bool do_q = q != nullptr && kind == OSCAR_KIND_K && (!RAW || raw.prepare);
   const bool rotate = (kind == OSCAR_KIND_K) || lv.v_explicit;
   // The rotation fragments do not depend on the kernel before: they are requested before the wait below,
   // while that kernel still runs (this grid is scheduled early). Every CTA that may rotate requests them.
@@ -108,16 +147,91 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   const int r = tid >> 4, c8 = tid & 15;
   uint4 u = make_uint4(0u, 0u, 0u, 0u);
   if (r == 0 && demote) u = __ldcg(reinterpret_cast<const uint4*>(bf16_row(lv, spage, h, kind, slot % kP) + 8 * c8));
+  __shared__ float2 cs[RAW ? kD / 2 : 1];                  // the request's angles
+  __shared__ float raw_rows[RAW ? 12 * kTileStride : 1];    // raw rows (of three warps, four each) between norm and rotation
+  __shared__ uint4 new_key[RAW ? kD / 8 : 1];              // the new key row, BF16
+  const bool raw_k = RAW && kind == OSCAR_KIND_K;
+  auto angles = [&](bool given) {
+    for (int j = tid; j < raw.r.rot / 2; j += kPrologueWarps * 32) {
+      int pos[kRopeAxes];
+      for (int a = 0; a < raw.r.n_axes; ++a) {
+        const int p = given ? raw.r.positions[(size_t)a * raw.r.n + b] : L_old;
+        if (p < 0 && j == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
+        pos[a] = max(p, 0);
+      }
+      cs[j] = rope_turn(raw.r, pos, j, 1.f);
+    }
+  };
+  if (raw_k && raw.r.positions == nullptr) angles(false);
   // Wait for the grid before (in a model, the kernel that made q, k and v), then let the decode be
   // scheduled; it waits for this grid before it reads anything this kernel writes.
   pdl_wait();
   pdl_launch_dependents();
-  if (r >= 1 && r <= gq && do_q) {
+  if constexpr (RAW) {
+    if (raw_k) {
+      // rows 0 .. gq - 1: queries, row gq: the new key; a warp's rows are four, and all its lanes take part
+      const int row = tid >> 3, l = tid & 7, rows_here = gq + 1, first = tid >> 5 << 2;
+      const bool isq = row < gq, live = row == gq || (isq && q != nullptr);
+      float x[16] = {}, w[16], y[16];
+      if (first < rows_here && live) {
+        const __nv_bfloat16* src = isq ? q + b * raw.q_row + (h * gq + row) * kD : k + b * raw.k_row + h * kD;
+        const __nv_bfloat16* wt = isq ? raw.qw : raw.kw;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint4 u4 = *reinterpret_cast<const uint4*>(src + 64 * part + 8 * l);
+          const uint32_t wds[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[8 * part + 2 * e] = __uint_as_float(wds[e] << 16);
+            x[8 * part + 2 * e + 1] = __uint_as_float(wds[e] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[8 * part + e] = wt != nullptr ? __bfloat162float(wt[64 * part + 8 * l + e]) : 1.f;
+        }
+      }
+      if (raw.r.positions != nullptr) angles(true);
+      __syncthreads();
+      if (first < rows_here) {
+        norm_rope_row(x, w, raw, cs, raw_rows + row * kTileStride, l, y);
+        uint4 z[2];
+        bool bad = false;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          __nv_bfloat162 p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            bad |= nonfinite(y[8 * part + 2 * e]) || nonfinite(y[8 * part + 2 * e + 1]);
+            p[e] = __floats2bfloat162_rn(y[8 * part + 2 * e], y[8 * part + 2 * e + 1]);
+          }
+          z[part] = *reinterpret_cast<const uint4*>(p);
+        }
+        if (live && bad) flag(lv.status, OSCAR_STATUS_NONFINITE);
+        if (live && isq) {
+          uint4* dst = reinterpret_cast<uint4*>(raw.q_out + ((size_t)b * lv.hq + h * gq + row) * kD);
+          dst[l] = z[0];
+          dst[8 + l] = z[1];
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t wds[4] = {z[part].x, z[part].y, z[part].z, z[part].w};
+            float* t = rows + (row + 1) * kTileStride + 64 * part + 8 * l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              t[2 * e] = __uint_as_float(wds[e] << 16);
+              t[2 * e + 1] = __uint_as_float(wds[e] & 0xffff0000u);
+            }
+          }
+        } else if (live) {
+          new_key[l] = z[0];
+          new_key[8 + l] = z[1];
+        }
+      }
+    }
+  } else if (r >= 1 && r <= gq && do_q) {
     u = *reinterpret_cast<const uint4*>(q + ((size_t)b * lv.hq + h * gq + r - 1) * kD + 8 * c8);
     if (bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w))
       flag(lv.status, OSCAR_STATUS_NONFINITE);
   }
-  {
+  if (!raw_k || q == nullptr || r == 0 || r > gq) {  // rows 1 .. gq of raw queries are there
     const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
     float4* dst = reinterpret_cast<float4*>(rows + r * kTileStride + 8 * c8);
     dst[0] = make_float4(__uint_as_float(wds[0] << 16), __uint_as_float(wds[0] & 0xffff0000u),
@@ -167,8 +281,13 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
     if (lane == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
     return;
   }
-  const __nv_bfloat16* src = (kind == OSCAR_KIND_K ? k : v) + ((size_t)b * lv.hkv + h) * kD;
-  const uint2 x = reinterpret_cast<const uint2*>(src)[lane];
+  uint2 x;
+  if (raw_k) {
+    x = reinterpret_cast<const uint2*>(new_key)[lane];
+  } else {
+    const __nv_bfloat16* src = RAW ? v + b * raw.v_row + h * kD : (kind == OSCAR_KIND_K ? k : v) + ((size_t)b * lv.hkv + h) * kD;
+    x = reinterpret_cast<const uint2*>(src)[lane];
+  }
   if (__any_sync(0xffffffffu, bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y)) && lane == 0)
     flag(lv.status, OSCAR_STATUS_NONFINITE);
   reinterpret_cast<uint2*>(bf16_row(lv, page, h, kind, row))[lane] = x;
@@ -180,7 +299,7 @@ constexpr int kPrologueSmem = (kRFragWords + kTileFloats + kD) * 4 + 64;
 
 int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const void* q, const void* k,
                     const void* v, const int* seq_lens_before, const int* hist_pt, int max_hist_pages,
-                    const int* bf16_pt, float sm_scale, cudaStream_t st, bool after_all) {
+                    const int* bf16_pt, float sm_scale, cudaStream_t st, bool after_all, const RawStep* raw) {
   if (B == 0) return OSCAR_OK;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -192,18 +311,21 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = after_all ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, k_step_prologue, lv, ws, static_cast<const __nv_bfloat16*>(q),
-                            static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
-                            seq_lens_before, hist_pt, max_hist_pages, bf16_pt, sm_scale * kLog2e) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, raw ? k_step_prologue<true> : k_step_prologue<false>, lv, ws,
+                            static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                            static_cast<const __nv_bfloat16*>(v), seq_lens_before, hist_pt, max_hist_pages, bf16_pt,
+                            sm_scale * kLog2e, raw ? *raw : RawStep{}) == cudaSuccess
              ? OSCAR_OK
              : OSCAR_ERR_CUDA;
 }
 
 int configure_prologue_kernel() {
-  if (cudaFuncSetAttribute(k_step_prologue, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrologueSmem) !=
-      cudaSuccess)
-    return OSCAR_ERR_CUDA;
-  return set_max_shared_carveout(reinterpret_cast<const void*>(k_step_prologue));
+  for (auto fn : {k_step_prologue<false>, k_step_prologue<true>}) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrologueSmem) != cudaSuccess)
+      return OSCAR_ERR_CUDA;
+    if (int rc = set_max_shared_carveout(reinterpret_cast<const void*>(fn)); rc != OSCAR_OK) return rc;
+  }
+  return OSCAR_OK;
 }
 
 }  // namespace oscar

@@ -8,7 +8,6 @@ namespace oscar {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 1024;                   // (cos, sin) entries of a CTA's tokens
 constexpr int kRopeTokens = 8;                     // tokens of a CTA, at most
-constexpr int kRopeAxes = OSCAR_MAX_ROPE_AXES;
 
 struct RopeSide {                                  // q or k
   const void* in;
@@ -16,18 +15,6 @@ struct RopeSide {                                  // q or k
   long long in_tok, in_head, out_tok, out_head;    // strides in elements
   int heads;
 };
-// A plan on the device, and where the tokens are on its axes.
-struct Rotary {
-  const int* positions;                            // [axes][n]
-  const unsigned long long* turns;                 // [rot / 2]
-  const uint8_t* axes;                             // [rot / 2], or null: axis 0
-  int n, rot, n_axes;
-  float scale;
-};
-inline Rotary rotary_of(const oscar_rotary& r, const int* positions, int n) {
-  return {positions, reinterpret_cast<const unsigned long long*>(r.turns), r.axes, n, r.rotary_dim, r.num_axes, r.scale};
-}
-
 // Positions of tokens t0 .. t0 + nt - 1 into shared memory [token][axis]; axis 0 is negative where any is (a padded row).
 __device__ __forceinline__ void load_positions(const Rotary& r, int t0, int nt, int* pos_s, int tid, int nthr) {
   for (int i = tid; i < nt; i += nthr) {

@@ -477,6 +477,39 @@ int oscar_norm_rope_backward(const oscar_rope_tensor* q, const oscar_rope_tensor
                              const oscar_rotary* rotary, const oscar_head_norm* norm, float* dq_weight, float* dk_weight,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* One token per request from the raw projections: q and k are normalised and rotated on the way into the append and the
+ * decode, with oscar_norm_rope's formulas and one rounding to bf16.
+ *  q, k, v   : device bf16 [B][Hq][128], [B][Hkv][128], [B][Hkv][128], 16-byte aligned; q_row, k_row, v_row: elements
+ *              between two requests' rows, multiples of 8 (views of one fused projection)
+ *  q_out     : device bf16 [B][Hq][128], 16-byte aligned: the normed and rotated queries; may be q where q_row is Hq * 128
+ *  positions : device int32 [num_axes][B], or NULL: seq_lens_before[r] on every axis. A negative one counts as 0
+ *              (BAD_SEQLEN).
+ *  norm      : NULL: no norm, the rotation alone */
+typedef struct oscar_raw_step {
+  const void *q, *k, *v;
+  int64_t q_row, k_row, v_row;
+  void* q_out;
+  const int32_t* positions;
+  const oscar_rotary* rotary;
+  const oscar_head_norm* norm;
+} oscar_raw_step;
+
+/* oscar_append_kv of the normed and rotated k and of v; q_out gets the queries for an oscar_decode_attention behind it.
+ * q may be NULL (then q_out is not used). As in oscar_append_kv, seq_lens_before, the page tables and the pool's rows are
+ * read before the wait for the kernel launched just before; q, k, v, positions and the weights may come from it.
+ * A key, or a query, that is not finite raises NONFINITE. Errors: as oscar_append_kv and oscar_norm_rope, INVALID_ARG (a
+ * missing structure, rows not 16-byte aligned or not a multiple of 8 elements apart, q_out = q with another row, a
+ * rotary_dim above 128). */
+int oscar_append_kv_rope(oscar_cache* cache, int layer, int B, const oscar_raw_step* raw, const int32_t* seq_lens_before,
+                         const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream);
+
+/* oscar_decode_step (oscar_decode_step_shared where shared_hist_pages > 0) from raw q, k and v: the same three launches,
+ * with the norm and the rotation in the first. The results are those of oscar_append_kv_rope followed by
+ * oscar_decode_attention of q_out over seq_lens_before[r] + 1 tokens. */
+int oscar_decode_step_rope(oscar_cache* cache, int layer, int B, const oscar_raw_step* raw, const int32_t* seq_lens_before,
+                           const int32_t* hist_pt, int max_hist_pages, int shared_hist_pages, const int32_t* bf16_pt,
+                           float sm_scale, void* out, int out_dtype, float* lse, void* stream);
+
 /* Attention of drafted nodes over the cache and their drafted ancestors.
  *  q                : device bf16 [B][T][Hq][128]; k_draft, v_draft : device bf16 [B][T][Hkv][128] (not in the cache)
  *  mask             : device uint64 [B][T][(T + 63) / 64]: bit j of row i lets node i attend to drafted node j;

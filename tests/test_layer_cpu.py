@@ -116,3 +116,9 @@ def test_plan_with_axes(osc):
     p = osc.RopePlan(64, axes=np.repeat([0, 2], [10, 22]), device="cpu")
     assert p.num_axes == 3 and p.rotary(0).num_axes == 3 and p.axes.tolist() == [0] * 10 + [2] * 22
     assert osc.RopePlan(64, device="cpu").axes is None
+
+
+def test_raw_steps_without_a_cache_are_refused(osc):
+    lib, bad = osc.lib(), osc.ERR_INVALID_ARG
+    assert lib.oscar_append_kv_rope(None, 0, 1, osc.RawStep(), None, None, 0, None, None) == bad
+    assert lib.oscar_decode_step_rope(None, 0, 1, osc.RawStep(), None, None, 0, 0, None, 0.1, None, 0, None, None) == bad
