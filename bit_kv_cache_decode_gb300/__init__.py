@@ -47,7 +47,7 @@ EXPORTS = (
     "oscar_build_tables", "oscar_tree_layout", "oscar_rope_frequencies", "oscar_rope_turns", "oscar_rope",
     "oscar_tree_workspace_bytes", "oscar_tree_attention", "oscar_commit_draft",
     "oscar_rope_axes", "oscar_norm_rope", "oscar_norm_rope_backward", "oscar_norm_rope_workspace_bytes",
-    "oscar_append_kv_rope", "oscar_decode_step_rope",
+    "oscar_append_kv_rope", "oscar_decode_step_rope", "oscar_prompt_attention",
 )
 
 
@@ -71,6 +71,10 @@ class RopeTensor(ctypes.Structure):
 class Rotary(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("num_axes", ctypes.c_int),
                 ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class RawStep(ctypes.Structure):
@@ -129,6 +133,7 @@ def _load() -> ctypes.CDLL:
                             ctypes.POINTER(Rotary), c_int, vp],
         "oscar_norm_rope": [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), c_int, c_int, c_int, i32p,
                             ctypes.POINTER(Rotary), ctypes.POINTER(HeadNorm), vp],
+        "oscar_prompt_attention": [vp, c_int] + [ctypes.POINTER(Heads)] * 3 + [i32p, c_int, c_float, vp, c_int, vp, vp],
         "oscar_append_kv_rope": [vp, c_int, c_int, ctypes.POINTER(RawStep), i32p, i32p, c_int, i32p, vp],
         "oscar_decode_step_rope": [vp, c_int, c_int, ctypes.POINTER(RawStep), i32p, i32p, c_int, c_int, i32p, c_float, vp,
                                    c_int, vp, vp],
@@ -421,6 +426,37 @@ class OscarCache:
             _check(_lib.oscar_decode_step(self._h, layer, sl.numel(), _ptr(q), _ptr(k), _ptr(v), _ptr(sl), _ptr(hp),
                                           mhp, _ptr(bp), float(sm_scale), _ptr(out), out_dtype, _ptr(lse),
                                           _stream(stream)), "oscar_decode_step")
+        return out
+
+    # ---- a prompt over itself ----------------------------------------------------------
+    def prompt_attention(self, q, k, v, cu_seqlens, sm_scale: float, out=None, out_dtype: int = OUT_BF16, lse=None,
+                         stream=None):
+        """Causal attention of whole prompts, packed one behind the other as for quantize_prefill: q [N, Hq, 128],
+        k, v [N, Hkv, 128] with free token and head strides (views of one projection), cu_seqlens [B + 1]. Rows of tokens
+        that belong to no prompt stay as they are: a new out holds them unset. Returns out [N, Hq, 128]."""
+        if stream is not None:
+            with _on(stream):
+                return self.prompt_attention(q, k, v, cu_seqlens, sm_scale, out, out_dtype, lse)
+        what = "oscar_prompt_attention"
+        dev, st = _here(self.pool)
+        cu = _in_i32(cu_seqlens, dev)
+        N, d = int(q.shape[0]), self.cfg.head_dim
+        heads = []
+        for x, h in ((q, self.cfg.num_q_heads), (k, self.cfg.num_kv_heads), (v, self.cfg.num_kv_heads)):
+            if x.dtype is not _bf16 or x.get_device() != dev or x.shape != (N, h, d) or x.stride(2) != 1:
+                raise OscarError(ERR_INVALID_ARG, what)
+            heads.append(Heads(x.data_ptr(), x.stride(0), x.stride(1)))
+        rows, out_type = (N, self.cfg.num_q_heads, d), _f32 if out_dtype == OUT_FP32 else _bf16
+        if cu.dim() != 1 or cu.numel() < 1 or N >> 31:
+            raise OscarError(ERR_INVALID_ARG, what)
+        if out is None:
+            out = _empty(rows, dtype=out_type, device=dev)
+        else:
+            _check_like(out, out_type, rows, dev, what)
+        if lse is not None:
+            _check_like(lse, _f32, rows[:2], dev, what)
+        _check(_lib.oscar_prompt_attention(self._h, cu.numel() - 1, heads[0], heads[1], heads[2], cu.data_ptr(), N,
+                                           float(sm_scale), out.data_ptr(), out_dtype, _ptr(lse), st), what)
         return out
 
     # ---- a token's raw projections ---------------------------------------------------

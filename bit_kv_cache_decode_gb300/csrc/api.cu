@@ -28,7 +28,7 @@ struct oscar_cache {
   int dev;                        // the device that was current when the cache was made
   int sms;
   int algo;
-  int tree_rc;                    // what configuring the tree attention's kernels gave
+  int tree_rc, prompt_rc;         // what configuring the tree attention's and the prompt attention's kernels gave
   unsigned long long* timeline;   // kernel timeline buffer (oscar_trace_timeline) or null
   int timeline_cap;
   // tracing
@@ -242,7 +242,7 @@ bool takes_note(cudaStream_t st) {
 constexpr int kMaxConfiguredDevices = 64;
 std::mutex g_configure_mu;
 bool g_configured[kMaxConfiguredDevices];
-int g_tree_rc[kMaxConfiguredDevices];              // the tree attention's own: its callers alone meet a failure
+int g_tree_rc[kMaxConfiguredDevices], g_prompt_rc[kMaxConfiguredDevices];   // these kernels' own: their callers alone meet a failure
 
 int configure_once() {
   int dev = 0;
@@ -256,7 +256,8 @@ int configure_once() {
   if (rc == OSCAR_OK) rc = configure_commit_kernel();
   if (rc == OSCAR_OK) {
     g_tree_rc[dev] = configure_tree_kernels();
-    if (g_tree_rc[dev] != OSCAR_OK) cudaGetLastError();
+    g_prompt_rc[dev] = configure_prompt_kernel();
+    if (g_tree_rc[dev] != OSCAR_OK || g_prompt_rc[dev] != OSCAR_OK) cudaGetLastError();
     g_configured[dev] = true;
   }
   return rc;
@@ -424,6 +425,7 @@ int oscar_cache_create(const oscar_layout* layout, void* pool, void* workspace, 
   c->sms = sms;
   c->algo = kDefaultDecodeAlgo;
   c->tree_rc = g_tree_rc[dev];
+  c->prompt_rc = g_prompt_rc[dev];
   c->timeline = nullptr;
   c->timeline_cap = 0;
   c->prof_on = false;
@@ -547,6 +549,27 @@ int oscar_quantize_prefill(oscar_cache* c, int layer, int B, const void* k, cons
   if (!aligned16(k) || !aligned16(v)) return OSCAR_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return wrote(launch_prefill(view(c, layer), B, k, v, cu_seqlens, total_tokens, hist_pt, max_hist_pages, bf16_pt, st), st);
+}
+
+int oscar_prompt_attention(oscar_cache* c, int B, const oscar_heads* q, const oscar_heads* k, const oscar_heads* v,
+                           const int32_t* cu_seqlens, int total_tokens, float sm_scale, void* out, int out_dtype,
+                           float* lse, void* stream) {
+  if (!c || B < 0 || total_tokens < 0 || (out_dtype != OSCAR_OUT_BF16 && out_dtype != OSCAR_OUT_FP32)) return OSCAR_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return OSCAR_ERR_INVALID_ARG;
+  if (c->prompt_rc != OSCAR_OK) return c->prompt_rc;
+  if (B == 0 || total_tokens == 0) return OSCAR_OK;
+  if (!q || !k || !v || !cu_seqlens || !out || !aligned16(out) || reinterpret_cast<uintptr_t>(lse) % sizeof(float))
+    return OSCAR_ERR_INVALID_ARG;
+  oscar_heads x[3] = {*q, *k, *v};
+  for (int i = 0; i < 3; ++i) {
+    if (!x[i].ptr || !aligned16(x[i].ptr)) return OSCAR_ERR_INVALID_ARG;
+    // the step over a single head or token is never taken
+    if ((i == 0 ? c->lay.num_q_heads : c->lay.num_kv_heads) == 1) x[i].head = kD;
+    if (total_tokens == 1) x[i].token = kD;
+    if (x[i].token < 8 || x[i].token % 8 || x[i].head < 8 || x[i].head % 8) return OSCAR_ERR_INVALID_ARG;
+  }
+  return launch_prompt_attention(c->lay.num_q_heads, c->lay.num_kv_heads, B, x[0], x[1], x[2], cu_seqlens, total_tokens,
+                                 sm_scale, out, out_dtype, lse, c->status, static_cast<cudaStream_t>(stream));
 }
 
 int oscar_project_quantize_prefill(oscar_cache* c, int layer, int B, const void* x, int d_model, const void* w_k,

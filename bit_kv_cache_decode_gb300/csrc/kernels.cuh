@@ -136,6 +136,12 @@ int launch_merge(const LayerView& lv, const DecodeWorkspace& ws, int B, int nspl
 constexpr int kMergeChunk = 96;            // partial slots staged in shared memory at a time by the merge
 int configure_merge_kernel();
 
+// causal attention of packed prompts (prompt_attention.cu)
+int launch_prompt_attention(int hq, int hkv, int B, const oscar_heads& q, const oscar_heads& k, const oscar_heads& v,
+                            const int* cu_seqlens, int total, float sm_scale, void* out, int out_dtype, float* lse, int* status,
+                            cudaStream_t st);
+int configure_prompt_kernel();
+
 // verifying drafted tokens: rope.cu, tables.cu, tree_attention.cu, tree_merge.cu, commit.cu
 constexpr int kMaxDraft = OSCAR_MAX_DRAFT, kMaxTableBatch = OSCAR_MAX_TABLE_BATCH;
 int launch_rope(const oscar_rope_tensor& q, const oscar_rope_tensor& k, int n, int dim, int dtype, const int* positions,

@@ -38,6 +38,7 @@
 // Every wait is bounded; a CTA whose wait expires flags OSCAR_STATUS_TIMEOUT and writes empty partials.
 #include <algorithm>
 
+#include "smem.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
 #include "tree.cuh"
@@ -111,28 +112,6 @@ template <int FMT>
 __device__ __forceinline__ uint32_t value_at(uint32_t x, int p, uint32_t lut, uint32_t s2, uint32_t z2) {
   return hfma2_u(FMT == kFmtCB ? levels_at(x, p, lut) : codes_at(x, p), s2, z2);
 }
-// shared memory by 32-bit address: the roles' pointers stay one register each
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t x;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 x;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-  return x;
-}
-__device__ __forceinline__ void sts32(uint32_t at, uint32_t x) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
-}
 // (scale, zero) of the two groups of a row as fp16 pairs {s0, z0}, {s1, z1}; blk: shared address of the page block.
 // Codebook format: the levels k / 256 are exact fp16 numbers, 255ths are not; the range takes the factor 256 / 255 and is
 // rounded to fp16 once more, so a key or value has two roundings of 2^-11, of scale times level and of the sum.
@@ -163,12 +142,6 @@ __device__ __forceinline__ uint32_t lut_of(const LayerView& lv, int h, int kind)
   for (int i = 0; i < 4; ++i) lut |= (uint32_t)c[i] << (8 * i);
   return lut;
 }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // What the roles share.
 struct Ctx {
   uint32_t base;                                   // shared memory, 1,024-byte aligned

@@ -233,6 +233,31 @@ int oscar_quantize_prefill(oscar_cache* cache, int layer, int B, const void* k, 
                            const int32_t* cu_seqlens, int total_tokens, const int32_t* hist_pt,
                            int max_hist_pages, const int32_t* bf16_pt, void* stream);
 
+/* Rows [tokens][heads][128] with free strides (elements, multiples of 8), the channels of a head contiguous; 16-byte
+ * aligned. */
+typedef struct oscar_heads {
+  const void* ptr;
+  int64_t token, head;
+} oscar_heads;
+
+/* Causal attention of B whole prompts over themselves: token i of a prompt attends to its tokens 0 .. i, in the caller's
+ * q, k and v (nothing of the pool is read or written: store the prompt with oscar_quantize_prefill).
+ *  q          : bf16 [total_tokens] rows of Hq heads; k, v: of Hkv heads; query head i reads kv head i / (Hq / Hkv)
+ *  cu_seqlens : device int32 [B+1], as for oscar_quantize_prefill; tokens before cu_seqlens[0] and from cu_seqlens[B] on
+ *               belong to no prompt, and their rows of out and lse stay as they are
+ *  out        : device [total_tokens][Hq][128], bf16 or fp32 (out_dtype), 16-byte aligned
+ *  lse        : device float32 [total_tokens][Hq] natural-log sum of exp(sm_scale q.k), or NULL
+ * Logits, softmax statistics and sums are float32; weights are rounded once to bf16 (2^-8 at most) for the product with
+ * v, and the tensor cores' sums truncate (a few 1e-5 of the values' mean at 32K tokens, about 1e-3 at 256K): an fp32 out
+ * carries that error too. Bounds out of order or outside [0, total_tokens] are taken within them (BAD_SEQLEN), and rows of
+ * such prompts may be left unwritten. A NaN or infinity in k or v reaches no rows but those that attend to it, one in q no
+ * row but its own; a row of out that is not finite raises NONFINITE. All inputs may come from the kernel just before; calls
+ * may overlap. Errors: INVALID_ARG (B or total_tokens < 0, null pointers, strides that are not positive multiples of 8,
+ * alignment, out_dtype, sm_scale), UNSUPPORTED (more than 2^31 - 1 tiles), CUDA. */
+int oscar_prompt_attention(oscar_cache* cache, int B, const oscar_heads* q, const oscar_heads* k, const oscar_heads* v,
+                           const int32_t* cu_seqlens, int total_tokens, float sm_scale, void* out, int out_dtype,
+                           float* lse, void* stream);
+
 /* The same bulk write from the prompt's hidden states, fused with the K and V
  * projections (MarkTechPost article, "服务系统：混合精度缓存布局": the write path
  * runs fused, so K and V are never written out and read back):

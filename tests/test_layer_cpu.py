@@ -122,3 +122,8 @@ def test_raw_steps_without_a_cache_are_refused(osc):
     lib, bad = osc.lib(), osc.ERR_INVALID_ARG
     assert lib.oscar_append_kv_rope(None, 0, 1, osc.RawStep(), None, None, 0, None, None) == bad
     assert lib.oscar_decode_step_rope(None, 0, 1, osc.RawStep(), None, None, 0, 0, None, 0.1, None, 0, None, None) == bad
+
+
+def test_prompt_attention_without_a_cache_is_refused(osc):
+    x = osc.Heads(4096, 128, 128)
+    assert osc.lib().oscar_prompt_attention(None, 1, x, x, x, 4096, 1, 0.1, 4096, 0, None, None) == osc.ERR_INVALID_ARG
