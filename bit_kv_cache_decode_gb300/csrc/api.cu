@@ -128,6 +128,7 @@ int check_rows(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
   }
   return OSCAR_OK;
 }
+constexpr int kMostNormHeads = 8192;               // norm_rope.cu divides row numbers by the heads in 32 bits
 int check_norm(const oscar_head_norm* n, int dtype) {
   if (!n || !(n->eps > 0.f) || !std::isfinite(n->eps)) return OSCAR_ERR_INVALID_ARG;
   const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
@@ -840,6 +841,7 @@ int oscar_norm_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int 
   oscar_rope_tensor t[2] = {};
   if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
   if (int rc = check_norm(norm, dtype); rc != OSCAR_OK) return rc;
+  if (t[0].heads > kMostNormHeads || t[1].heads > kMostNormHeads) return OSCAR_ERR_UNSUPPORTED;
   if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
   if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
   return launch_norm_rope(t[0], t[1], nullptr, N, head_dim, dtype, positions, *rotary, *norm, nullptr, nullptr, nullptr,
@@ -861,6 +863,7 @@ int oscar_norm_rope_backward(const oscar_rope_tensor* q, const oscar_rope_tensor
   if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
   if (int rc = check_rows(grad_q, grad_k, N, head_dim, dtype, rotary, false, g); rc != OSCAR_OK) return rc;
   if (int rc = check_norm(norm, dtype); rc != OSCAR_OK) return rc;
+  if (t[0].heads > kMostNormHeads || t[1].heads > kMostNormHeads) return OSCAR_ERR_UNSUPPORTED;
   if (g[0].heads != t[0].heads || g[1].heads != t[1].heads) return OSCAR_ERR_INVALID_ARG;
   for (int i = 0; i < 2; ++i)                        // in the place of the gradient: rows must fall on each other
     if (g[i].heads != 0 && t[i].out == g[i].in && (t[i].out_token != g[i].in_token || t[i].out_head != g[i].in_head))

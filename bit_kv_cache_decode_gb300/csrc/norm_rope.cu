@@ -12,13 +12,17 @@
 // Gradient: the weights' sums are held in registers over all rows of a CTA, which walks tokens of q or of k; CTAs'
 // partial sums go to the workspace and are added in a fixed order by a second kernel, so results do not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "rope.cuh"
+#include "smem.cuh"
+#include "tma.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kGradCtas = 608;                     // partial sums of the weights' gradients, at most: four CTAs per SM of 152
+constexpr int kGradCtas = 304;                     // partial sums of the weights' gradients, at most: two CTAs per SM of 152
+constexpr int kGradTable = 2048, kGradTokens = 32; // as kRopeTable and kRopeTokens, for the gradient's CTAs
 constexpr int kSumRows = 8;                        // threads that share a channel's partial sums
 
 struct NormArgs {
@@ -26,22 +30,30 @@ struct NormArgs {
   RopeSide gq, gk;                                 // gradient: dL/dy (in); q, k: x (in) and dL/dx (out)
   const void *qw, *kw;                             // weights of the rows' type, or null: ones
   Rotary r;
-  int dim, tokens, lanes;                          // tokens per CTA (forward), lanes per row
+  int dim, tokens, lanes;                          // tokens per CTA (gradient: at a time), lanes per row
   int q_ctas;                                      // gradient: the first CTAs walk q, the others k
   float eps;
   float* partials;                                 // gradient: [CTA][dim], or null
 };
 
+// whether a lane holds no more than 32 bytes of a row
+template <typename T, int V, bool HALF, int K>
+constexpr bool few() {
+  return sizeof(T) * V * K * (HALF ? 2 : 1) <= 32;
+}
+
 // What a lane holds of a row: K units.
 template <typename T, int V, bool HALF, int K>
 struct Place {
-  int at[K];                                       // first channel of unit k
+  int at[K], unit[K], rot_units;                   // first channel of unit k
   bool there[K], rotary[K];
   __device__ __forceinline__ Place(int lane, int lanes, int dim, int rot) {
-    const int rot_units = HALF ? rot / 2 / V : rot / V, units = rot_units + (dim - rot) / V;
+    rot_units = HALF ? rot / 2 / V : rot / V;
+    const int units = rot_units + (dim - rot) / V;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int u = lane + k * lanes;
+      unit[k] = u;
       there[k] = u < units;
       rotary[k] = u < rot_units;
       at[k] = rotary[k] ? u * V : rot + (u - rot_units) * V;
@@ -49,54 +61,180 @@ struct Place {
   }
 };
 
+// Two values an instruction where there are two.
+template <int N>
+__device__ __forceinline__ void mul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    const float2 r = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    d[i] = r.x;
+    d[i + 1] = r.y;
+  }
+  if constexpr (N % 2) d[N - 1] = a[N - 1] * b[N - 1];
+}
+template <int N>
+__device__ __forceinline__ void mul(float (&d)[N], const float (&a)[N], float b) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    const float2 r = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b, b));
+    d[i] = r.x;
+    d[i + 1] = r.y;
+  }
+  if constexpr (N % 2) d[N - 1] = a[N - 1] * b;
+}
+template <int N>
+__device__ __forceinline__ void fma(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    const float2 r = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+    d[i] = r.x;
+    d[i + 1] = r.y;
+  }
+  if constexpr (N % 2) d[N - 1] = fmaf(a[N - 1], b[N - 1], c[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ void fma(float (&d)[N], const float (&a)[N], float b, const float (&c)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    const float2 r = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b, b), make_float2(c[i], c[i + 1]));
+    d[i] = r.x;
+    d[i + 1] = r.y;
+  }
+  if constexpr (N % 2) d[N - 1] = fmaf(a[N - 1], b, c[N - 1]);
+}
+// sum of a b, added to two partial sums
+template <int N>
+__device__ __forceinline__ void dot(float2& s, const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) s = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), s);
+  if constexpr (N % 2) s.x = fmaf(a[N - 1], b[N - 1], s.x);
+}
+
 // A unit's values in float32: V channels and, for a rotary unit of the half layout, their V partners (else zeros).
 template <int V, bool HALF> struct Values {
   float a[V], b[HALF ? V : 1];
 };
-template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ Values<V, HALF> values_of(const Unit<T, V, V, HALF, WIDE>& x, bool rotary) {
-  Values<V, HALF> f;
+// N values to and from float32, two of a 16-bit type at a time where they come as words
+template <typename T, int N, bool WIDE>
+__device__ __forceinline__ void widen(float (&f)[N], const T* x) {
+  if constexpr (WIDE && sizeof(T) == 2) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    f.a[e] = to_f(x.a.v[e]);
-    if (HALF) f.b[e] = rotary ? to_f(x.b.v[e]) : 0.f;
-  }
-  return f;
-}
-// turned by the unit's angles (cs[0] belongs to its first pair)
-template <int V, bool HALF>
-__device__ __forceinline__ void turn(Values<V, HALF>& f, const float2* cs) {
-  if constexpr (HALF) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = f.a[e], y = f.b[e];
-      const float2 t = cs[e];
-      f.a[e] = x * t.x - y * t.y;
-      f.b[e] = y * t.x + x * t.y;
+    for (int i = 0; i < N / 2; ++i) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(x)[i];
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      } else {
+        f[2 * i] = __uint_as_float(w << 16);
+        f[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+      }
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      const float x = f.a[2 * e], y = f.a[2 * e + 1];
-      const float2 t = cs[e];
-      f.a[2 * e] = x * t.x - y * t.y;
-      f.a[2 * e + 1] = y * t.x + x * t.y;
+    for (int i = 0; i < N; ++i) f[i] = to_f(x[i]);
+  }
+}
+template <typename T, int N, bool WIDE>
+__device__ __forceinline__ void narrow(T* x, const float (&f)[N]) {
+  if constexpr (WIDE && sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        reinterpret_cast<uint32_t*>(x)[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        reinterpret_cast<uint32_t*>(x)[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = from_f<T>(f[i]);
+  }
+}
+template <typename T, int V, bool HALF, bool WIDE>
+__device__ __forceinline__ Values<V, HALF> values_of(const Unit<T, V, V, HALF, WIDE>& x) {
+  Values<V, HALF> f;
+  widen<T, V, WIDE>(f.a, x.a.v);
+  if constexpr (HALF) widen<T, V, WIDE>(f.b, x.b.v);
+  else f.b[0] = 0.f;
+  return f;
+}
+
+// The rotations of a token, as its rotary units read them: 4 floats a pair, weights included (wa, wb: of the pair's
+// channels). Half layout: V floats each of wa cos, -wb sin, wb cos, wa sin; pairs layout: V floats of (wa cos, wb cos) and V
+// of (-wb sin, wa sin). The 16-byte chunks of a unit are rot_units apart, so that the lanes of a row read without bank
+// conflicts.
+template <int V, bool HALF>
+__device__ __forceinline__ void put_turn(float* token, int rot_units, int j, float2 cs, float wa, float wb) {
+  constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
+  const int u = j / kPer, e = j - u * kPer;
+  const float f[4] = {wa * cs.x, HALF ? -wb * cs.y : wb * cs.x, HALF ? wb * cs.x : -wb * cs.y, wa * cs.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = HALF ? i * V + e : (i >> 1) * V + 2 * e + (i & 1);
+    token[((at >> 2) * rot_units + u) * 4 + (at & 3)] = f[i];
+  }
+}
+// a unit's values turned: Rot(w x) for the table's weights w
+template <int V, bool HALF>
+__device__ __forceinline__ void turn(Values<V, HALF>& f, const float* token, int rot_units, int u) {
+  constexpr int kFloats = HALF ? 4 * V : 2 * V;
+  float t[kFloats];
+#pragma unroll
+  for (int i = 0; i < kFloats / 4; ++i) {
+    const float4 c = *reinterpret_cast<const float4*>(token + (i * rot_units + u) * 4);
+    t[4 * i] = c.x;
+    t[4 * i + 1] = c.y;
+    t[4 * i + 2] = c.z;
+    t[4 * i + 3] = c.w;
+  }
+  float swapped[V];
+  if constexpr (HALF) {
+    float ac[V], bs[V], bc[V], as[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      ac[e] = t[e];
+      bs[e] = t[V + e];
+      bc[e] = t[2 * V + e];
+      as[e] = t[3 * V + e];
+      swapped[e] = f.a[e];
+    }
+    mul<V>(f.a, f.a, ac);
+    fma<V>(f.a, f.b, bs, f.a);
+    mul<V>(f.b, f.b, bc);
+    fma<V>(f.b, swapped, as, f.b);
+  } else {
+    float c2[V], s2[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      c2[e] = t[e];
+      s2[e] = t[V + e];
+      swapped[e] = f.a[e ^ 1];
+    }
+    mul<V>(f.a, f.a, c2);
+    fma<V>(f.a, swapped, s2, f.a);
   }
 }
 template <typename T, int V, bool HALF, bool WIDE>
 __device__ __forceinline__ void store(T* out, const Values<V, HALF>& f, int at, int half, bool rotary) {
   Unit<T, V, V, HALF, WIDE> x;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    x.a.v[e] = from_f<T>(f.a[e]);
-    if (HALF) x.b.v[e] = from_f<T>(f.b[e]);
-  }
+  narrow<T, V, WIDE>(x.a.v, f.a);
+  if constexpr (HALF) narrow<T, V, WIDE>(x.b.v, f.b);
   x.store(out, at, half, rotary);
+}
+// What a lane has nothing of is zeros, so that the arithmetic needs no conditions: only loads and stores do.
+template <typename T, int V, bool HALF, bool WIDE>
+__device__ __forceinline__ Unit<T, V, V, HALF, WIDE> zeros() {
+  Unit<T, V, V, HALF, WIDE> x;
+#pragma unroll
+  for (int e = 0; e < V; ++e) x.a.v[e] = x.b.v[e] = from_f<T>(0.f);
+  return x;
 }
 template <typename T, int V, bool HALF, bool WIDE>
 __device__ __forceinline__ Unit<T, V, V, HALF, WIDE> weights(const void* w, int at, int half, bool rotary) {
-  Unit<T, V, V, HALF, WIDE> x;
+  Unit<T, V, V, HALF, WIDE> x = zeros<T, V, HALF, WIDE>();
   if (w != nullptr) {
     x.load(static_cast<const T*>(w), at, half, rotary);
   } else {
@@ -106,163 +244,334 @@ __device__ __forceinline__ Unit<T, V, V, HALF, WIDE> weights(const void* w, int 
   return x;
 }
 __device__ __forceinline__ float group_sum(float s, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    if (m >= lanes) break;
+    s += __shfl_xor_sync(0xffffffffu, s, m);
+  }
+  return s;
+}
+__device__ __forceinline__ float2 group_sum(float2 s, int lanes) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    if (m >= lanes) break;
+    const float x = __shfl_xor_sync(0xffffffffu, s.x, m), y = __shfl_xor_sync(0xffffffffu, s.y, m);
+    s = make_float2(s.x + x, s.y + y);
+  }
   return s;
 }
 
+// A group's rows (token, head) of a CTA's tokens, head after head: rows group, group + groups, ... Steps are additions.
+template <typename T>
+struct Walk {
+  const T* in;
+  T* out;
+  int t, h, dt, dh, heads;
+  long long in_step, in_wrap, out_step, out_wrap;  // a step, and what a step past the last head adds
+  __device__ __forceinline__ Walk(const RopeSide& s, long long t0, int group, int groups) {
+    heads = s.heads;
+    t = group / heads;
+    h = group - t * heads;
+    dt = groups / heads;
+    dh = groups - dt * heads;
+    in = static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + h * s.in_head;
+    out = static_cast<T*>(s.out) + (t0 + t) * s.out_tok + h * s.out_head;
+    in_step = dt * s.in_tok + dh * s.in_head;
+    in_wrap = s.in_tok - heads * s.in_head;
+    out_step = dt * s.out_tok + dh * s.out_head;
+    out_wrap = s.out_tok - heads * s.out_head;
+  }
+  __device__ __forceinline__ void next() {
+    t += dt;
+    h += dh;
+    in += in_step;
+    out += out_step;
+    if (h >= heads) {
+      h -= heads;
+      ++t;
+      in += in_wrap;
+      out += out_wrap;
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const void* w, int c) {
+  return w != nullptr ? to_f(static_cast<const T*>(w)[c]) : 1.f;
+}
+
 template <typename T, int V, bool HALF, bool WIDE, int K>
-__global__ void __launch_bounds__(kRopeThreads, K == 1 ? 4 : 2) k_norm_rope(NormArgs a) {
-  __shared__ float2 table[kRopeTable];
+__global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 4 : 2) k_norm_rope(NormArgs a) {
+  __shared__ __align__(16) float table[2][4 * kRopeTable];   // of q, of k: [token][4 rot / 2]
+  __shared__ __align__(16) float rest[2][512];     // the weights of the channels behind the rotated ones
   __shared__ int pos_s[kRopeTokens * kRopeAxes];
-  constexpr int kBatch = K == 1 ? 2 : 1;           // rows a group has in flight
+  constexpr bool kFew = few<T, V, HALF, K>();      // of wide rows, units that a lane does not have are skipped
+  constexpr int kBatch = kFew ? 2 : 1;           // rows a group has in flight
   const int rot = a.r.rot, half = rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.r.n - t0), tid = threadIdx.x;
   const int lane = tid & (a.lanes - 1), group = tid / a.lanes, groups = kRopeThreads / a.lanes;
   const Place<T, V, HALF, K> p(lane, a.lanes, a.dim, rot);
-  Unit<T, V, V, HALF, WIDE> wq[K], wk[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (p.there[k]) {
-      wq[k] = weights<T, V, HALF, WIDE>(a.qw, p.at[k], half, p.rotary[k]);
-      wk[k] = weights<T, V, HALF, WIDE>(a.kw, p.at[k], half, p.rotary[k]);
-    }
   load_positions(a.r, t0, nt, pos_s, tid, kRopeThreads);
   __syncthreads();
-  load_turns(a.r, nt, pos_s, 1.f, table, tid, kRopeThreads);
+  for (int i = tid; i < nt * half; i += kRopeThreads) {
+    const int t = i / half, j = i - t * half, ca = HALF ? j : 2 * j, cb = HALF ? j + half : 2 * j + 1;
+    const float2 cs = rope_turn(a.r, pos_s + t * kRopeAxes, j, 1.f);
+    put_turn<V, HALF>(table[0] + t * 2 * rot, p.rot_units, j, cs, weight_at<T>(a.qw, ca), weight_at<T>(a.qw, cb));
+    put_turn<V, HALF>(table[1] + t * 2 * rot, p.rot_units, j, cs, weight_at<T>(a.kw, ca), weight_at<T>(a.kw, cb));
+  }
+  for (int c = rot + tid; c < a.dim; c += kRopeThreads) {
+    rest[0][c - rot] = weight_at<T>(a.qw, c);
+    rest[1][c - rot] = weight_at<T>(a.kw, c);
+  }
   __syncthreads();
-  const int heads = a.q.heads + a.k.heads, items = nt * heads;
   const float inv_dim = 1.f / (float)a.dim;
-  // the same trips for every lane of a warp: the row's sum is a shuffle
-  for (int i0 = 0; i0 < items; i0 += kBatch * groups) {
-    Unit<T, V, V, HALF, WIDE> x[kBatch][K];
-    T* out[kBatch];
-    int tok[kBatch];
-    bool isq[kBatch];
+#pragma unroll 1
+  for (int isk = 0; isk < 2; ++isk) {              // the heads of q, then of k
+    const RopeSide s = isk ? a.k : a.q;
+    if (s.heads == 0) continue;
+    Walk<T> row(s, t0, group, groups);
+    // the same trips for every lane of a warp: the row's sum is a shuffle
+#pragma unroll 1
+    for (int i0 = 0; i0 < nt * s.heads; i0 += kBatch * groups) {
+      Unit<T, V, V, HALF, WIDE> x[kBatch][K];
+      T* out[kBatch];
+      const float* turns[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * groups + group;       // (token, head)
-      const int t = min(i, items - 1) / heads, h = min(i, items - 1) - t * heads;
-      isq[b] = h < a.q.heads;
-      const RopeSide& s = isq[b] ? a.q : a.k;
-      const int hh = isq[b] ? h : h - a.q.heads;
-      const T* in = static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + hh * s.in_head;
-      out[b] = static_cast<T*>(s.out) + (t0 + t) * s.out_tok + hh * s.out_head;
-      tok[b] = t;
-      if (i >= items || pos_s[t * kRopeAxes] < 0) out[b] = nullptr;       // a padded row is left as it is
-      if (out[b] != nullptr)
+      for (int b = 0; b < kBatch; ++b) {
+        const bool live = row.t < nt && pos_s[row.t * kRopeAxes] >= 0;   // a padded row is left as it is
+        out[b] = live ? row.out : nullptr;
+        turns[b] = table[isk] + (live ? row.t : 0) * 2 * rot;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (p.there[k]) x[b][k].load(in, p.at[k], half, p.rotary[k]);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      float ss = 0.f;
-      Values<V, HALF> f[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (p.there[k] && out[b] != nullptr) {
-          f[k] = values_of<T, V, HALF, WIDE>(x[b][k], p.rotary[k]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            ss = fmaf(f[k].a[e], f[k].a[e], ss);
-            if (HALF) ss = fmaf(f[k].b[e], f[k].b[e], ss);
-          }
+        for (int k = 0; k < K; ++k) {
+          x[b][k] = zeros<T, V, HALF, WIDE>();
+          if (live && p.there[k]) x[b][k].load(row.in, p.at[k], half, p.rotary[k]);
         }
-      const float r = rsqrtf(group_sum(ss, a.lanes) * inv_dim + a.eps);
+        row.next();
+      }
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (p.there[k] && out[b] != nullptr) {
-          const Values<V, HALF> w = values_of<T, V, HALF, WIDE>(isq[b] ? wq[k] : wk[k], p.rotary[k]);
+      for (int b = 0; b < kBatch; ++b) {
+        float2 ss = make_float2(0.f, 0.f);
+        Values<V, HALF> f[K];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f[k].a[e] *= r * w.a[e];
-            if (HALF) f[k].b[e] *= r * w.b[e];
-          }
-          if (p.rotary[k]) turn<V, HALF>(f[k], table + tok[b] * half + (HALF ? p.at[k] : p.at[k] / 2));
-          store<T, V, HALF, WIDE>(out[b], f[k], p.at[k], half, p.rotary[k]);
+        for (int k = 0; k < K; ++k) {
+          if (!kFew && !p.there[k]) continue;
+          f[k] = values_of<T, V, HALF, WIDE>(x[b][k]);
+          dot(ss, f[k].a, f[k].a);
+          if (HALF && (kFew || p.rotary[k])) dot(ss, f[k].b, f[k].b);
         }
+        const float r = rsqrtf(group_sum(ss.x + ss.y, a.lanes) * inv_dim + a.eps);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (!kFew && !p.there[k]) continue;
+          mul(f[k].a, f[k].a, r);
+          if (HALF && (kFew || p.rotary[k])) mul(f[k].b, f[k].b, r);
+          if (p.rotary[k]) {
+            turn<V, HALF>(f[k], turns[b], p.rot_units, p.unit[k]);
+          } else if (p.there[k]) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[k].a[e] *= rest[isk][p.at[k] - rot + e];
+          }
+          if (out[b] != nullptr && p.there[k]) store<T, V, HALF, WIDE>(out[b], f[k], p.at[k], half, p.rotary[k]);
+        }
+      }
     }
   }
 }
 
+// What a lane has loaded of a row for the gradient.
 template <typename T, int V, bool HALF, bool WIDE, int K>
-__global__ void __launch_bounds__(kRopeThreads, K == 1 ? 3 : 1) k_norm_rope_grad(NormArgs a) {
-  __shared__ float2 table[kRopeTable];
-  __shared__ int pos_s[kRopeTokens * kRopeAxes];
-  __shared__ float sums[kRopeThreads / 32][512];   // a warp's share of the weights' gradient
+struct GradRow {
+  Unit<T, V, V, HALF, WIDE> x[K], g[K];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = g[k] = zeros<T, V, HALF, WIDE>();
+  }
+  template <typename P>
+  __device__ __forceinline__ void load(const P& p, const T* in, const T* gin, int half) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (p.there[k]) {
+        x[k].load(in, p.at[k], half, p.rotary[k]);
+        g[k].load(gin, p.at[k], half, p.rotary[k]);
+      }
+  }
+  // The same through shared memory: asynchronous 16-byte copies into slots of the thread's own, chunk j of all threads side by
+  // side at slot + j * 16 * kRopeThreads.
+  static constexpr int kParts = HALF ? 2 : 1, kChunks = 2 * K * kParts;
+  template <typename P>
+  static __device__ __forceinline__ void copy(uint32_t slot, const P& p, const T* in, const T* gin, int half) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+        if (p.there[k] && (part == 0 || p.rotary[k])) {
+          const int at = p.at[k] + part * half, j = 2 * (k * kParts + part);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + j * 16 * kRopeThreads), "l"(in + at) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (j + 1) * 16 * kRopeThreads), "l"(gin + at)
+                       : "memory");
+        }
+  }
+  template <typename P>
+  __device__ __forceinline__ void take(uint32_t slot, const P& p) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+        if (p.there[k] && (part == 0 || p.rotary[k])) {
+          const int j = 2 * (k * kParts + part);
+          const uint4 cx = lds128(slot + j * 16 * kRopeThreads), cg = lds128(slot + (j + 1) * 16 * kRopeThreads);
+          *reinterpret_cast<uint4*>(part ? x[k].b.v : x[k].a.v) = cx;
+          *reinterpret_cast<uint4*>(part ? g[k].b.v : g[k].a.v) = cg;
+        }
+  }
+};
+
+// The rows of a group, some trips ahead of those it works on: trip by trip, tokens by tokens as the CTA walks them.
+template <typename T>
+struct Ahead {
+  RopeSide s;
+  Walk<T> row;                                     // out: the gradient's row
+  long long t0, step, n;
+  int tokens, group, groups, i0, nt;
+  __device__ __forceinline__ Ahead(const RopeSide& s_, long long t0_, long long step_, long long n_, int tokens_, int group_, int groups_)
+      : s(s_), row(s_, t0_, group_, groups_), t0(t0_), step(step_), n(n_), tokens(tokens_), group(group_), groups(groups_), i0(0),
+        nt((int)min((long long)tokens_, n_ - t0_)) {}
+  __device__ __forceinline__ bool there() const { return row.t < nt; }     // nt < 1 behind the last tokens
+  __device__ __forceinline__ void next() {
+    i0 += groups;
+    if (i0 < nt * s.heads) {
+      row.next();
+    } else {
+      t0 += step;
+      i0 = 0;
+      nt = (int)max(min((long long)tokens, n - t0), 0ll);
+      row = Walk<T>(s, t0, group, groups);
+    }
+  }
+};
+
+template <typename T, int V, bool HALF, bool WIDE, int K>
+constexpr bool grad_async() {
+  return WIDE && sizeof(T) * V == 16 && few<T, V, HALF, K>();
+}
+constexpr int kSlots = 3;                          // rows of a thread in shared memory: one worked on, two on their way
+template <typename T, int V, bool HALF, bool WIDE, int K>
+constexpr int grad_smem() {
+  return 16 * kGradTable + (grad_async<T, V, HALF, WIDE, K>() ? kSlots * GradRow<T, V, HALF, WIDE, K>::kChunks * 16 * kRopeThreads : 0);
+}
+
+template <typename T, int V, bool HALF, bool WIDE, int K>
+__global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 2 : 1) k_norm_rope_grad(NormArgs a) {
+  extern __shared__ __align__(16) float smem[];
+  float* const table = smem;                       // [token][4 rot / 2]; at the end a warp's share of dw: [8][512]
+  __shared__ int pos_s[kGradTokens * kRopeAxes];
+  static_assert(4 * kGradTable >= kRopeThreads / 32 * 512, "the warps' shares fit");
+  using Row = GradRow<T, V, HALF, WIDE, K>;
+  constexpr bool kAsync = grad_async<T, V, HALF, WIDE, K>(), kFew = few<T, V, HALF, K>();
   const int rot = a.r.rot, half = rot / 2, tid = threadIdx.x;
   const int lane = tid & (a.lanes - 1), group = tid / a.lanes, groups = kRopeThreads / a.lanes;
   const bool isq = (int)blockIdx.x < a.q_ctas;
   const RopeSide s = isq ? a.q : a.k, sg = isq ? a.gq : a.gk;
-  const int first = isq ? blockIdx.x : blockIdx.x - a.q_ctas, step = isq ? a.q_ctas : gridDim.x - a.q_ctas;
+  const int first = isq ? blockIdx.x : blockIdx.x - a.q_ctas, ctas = isq ? a.q_ctas : gridDim.x - a.q_ctas;
+  const long long step = (long long)ctas * a.tokens;
   const Place<T, V, HALF, K> p(lane, a.lanes, a.dim, rot);
   Unit<T, V, V, HALF, WIDE> w[K];
   Values<V, HALF> dw[K] = {};
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (p.there[k]) w[k] = weights<T, V, HALF, WIDE>(isq ? a.qw : a.kw, p.at[k], half, p.rotary[k]);
+    w[k] = p.there[k] ? weights<T, V, HALF, WIDE>(isq ? a.qw : a.kw, p.at[k], half, p.rotary[k]) : zeros<T, V, HALF, WIDE>();
   const float inv_dim = 1.f / (float)a.dim;
-  for (long long t0 = (long long)first * a.tokens; t0 < a.r.n; t0 += (long long)step * a.tokens) {
+  // A group's next rows are on their way while it works on one, also across the CTA's tokens.
+  const RopeSide both = {s.in, const_cast<void*>(sg.in), s.in_tok, s.in_head, sg.in_tok, sg.in_head, s.heads};
+  Ahead<T> ahead(both, (long long)first * a.tokens, step, a.r.n, a.tokens, group, groups);
+  const uint32_t slots = smem_addr(smem) + 16 * kGradTable + 16 * tid;
+  int slot = 0;                                    // of the row that is worked on
+  Row next;
+  auto fetch = [&](int to) {
+    if constexpr (kAsync) {
+      if (ahead.there()) Row::copy(slots + to * (Row::kChunks * 16 * kRopeThreads), p, ahead.row.in, ahead.row.out, half);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      next.clear();
+      if (ahead.there()) next.load(p, ahead.row.in, ahead.row.out, half);
+    }
+    ahead.next();
+  };
+#pragma unroll 1
+  for (int i = 0; i < (kAsync ? kSlots - 1 : 1); ++i) fetch(i);
+#pragma unroll 1
+  for (long long t0 = (long long)first * a.tokens; t0 < a.r.n; t0 += step) {
     const int nt = (int)min((long long)a.tokens, a.r.n - t0), items = nt * s.heads;
+    Walk<T> row(s, t0, group, groups);
     __syncthreads();                               // the last tokens' angles have been read
     load_positions(a.r, (int)t0, nt, pos_s, tid, kRopeThreads);
     __syncthreads();
-    load_turns(a.r, nt, pos_s, -1.f, table, tid, kRopeThreads);
+    for (int i = tid; i < nt * half; i += kRopeThreads) {
+      const int t = i / half, j = i - t * half;
+      put_turn<V, HALF>(table + t * 2 * rot, p.rot_units, j, rope_turn(a.r, pos_s + t * kRopeAxes, j, -1.f), 1.f, 1.f);
+    }
     __syncthreads();
+#pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += groups) {
-      const int i = i0 + group, t = min(i, items - 1) / s.heads, h = min(i, items - 1) - t * s.heads;
-      const bool live = i < items && pos_s[t * kRopeAxes] >= 0;
-      const T* in = static_cast<const T*>(s.in) + (t0 + t) * s.in_tok + h * s.in_head;
-      const T* gin = static_cast<const T*>(sg.in) + (t0 + t) * sg.in_tok + h * sg.in_head;
-      T* out = static_cast<T*>(s.out) + (t0 + t) * s.out_tok + h * s.out_head;
-      Unit<T, V, V, HALF, WIDE> x[K], g[K];
+      const bool live = row.t < nt && pos_s[row.t * kRopeAxes] >= 0;
+      Row now;
+      now.clear();
+      if constexpr (kAsync) {
+        // the row worked on before is read: its slot is the next to fill
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+        if (live) now.take(slots + slot * (Row::kChunks * 16 * kRopeThreads), p);
+        fetch(slot == 0 ? kSlots - 1 : slot - 1);
+        slot = slot == kSlots - 1 ? 0 : slot + 1;
+      } else {
+        if (live) now = next;
+        fetch(0);
+      }
+      T* const out = row.out;
+      const float* const turns = table + (live ? row.t : 0) * 2 * rot;
+      row.next();
+      float2 ss = make_float2(0.f, 0.f), ux = ss;
+      Values<V, HALF> fh[K], fu[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (p.there[k] && live) {
-          x[k].load(in, p.at[k], half, p.rotary[k]);
-          g[k].load(gin, p.at[k], half, p.rotary[k]);
+      for (int k = 0; k < K; ++k) {
+        if (!kFew && !p.there[k]) continue;
+        const Values<V, HALF> fx = values_of<T, V, HALF, WIDE>(now.x[k]), fw = values_of<T, V, HALF, WIDE>(w[k]);
+        fh[k] = values_of<T, V, HALF, WIDE>(now.g[k]);
+        if (p.rotary[k]) turn<V, HALF>(fh[k], turns, p.rot_units, p.unit[k]);
+        mul(fu[k].a, fh[k].a, fw.a);
+        dot(ss, fx.a, fx.a);
+        dot(ux, fu[k].a, fx.a);
+        if (HALF && (kFew || p.rotary[k])) {
+          mul(fu[k].b, fh[k].b, fw.b);
+          dot(ss, fx.b, fx.b);
+          dot(ux, fu[k].b, fx.b);
         }
-      float ss = 0.f, ux = 0.f;
-      Values<V, HALF> fx[K], fh[K];
+      }
+      const float2 both_sums = group_sum(make_float2(ss.x + ss.y, ux.x + ux.y), a.lanes);
+      const float r = rsqrtf(both_sums.x * inv_dim + a.eps), along = -both_sums.y * inv_dim * r * r;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (p.there[k] && live) {
-          fx[k] = values_of<T, V, HALF, WIDE>(x[k], p.rotary[k]);
-          fh[k] = values_of<T, V, HALF, WIDE>(g[k], p.rotary[k]);
-          if (p.rotary[k]) turn<V, HALF>(fh[k], table + t * half + (HALF ? p.at[k] : p.at[k] / 2));
-          const Values<V, HALF> fw = values_of<T, V, HALF, WIDE>(w[k], p.rotary[k]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            ss = fmaf(fx[k].a[e], fx[k].a[e], ss);
-            ux = fmaf(fh[k].a[e] * fw.a[e], fx[k].a[e], ux);
-            if (HALF) {
-              ss = fmaf(fx[k].b[e], fx[k].b[e], ss);
-              ux = fmaf(fh[k].b[e] * fw.b[e], fx[k].b[e], ux);
-            }
-          }
+      for (int k = 0; k < K; ++k) {
+        if (!kFew && !p.there[k]) continue;
+        const Values<V, HALF> fx = values_of<T, V, HALF, WIDE>(now.x[k]);
+        Values<V, HALF> xr, dx;
+        mul(xr.a, fx.a, r);
+        fma(dw[k].a, fh[k].a, xr.a, dw[k].a);
+        fma(dx.a, fx.a, along, fu[k].a);
+        mul(dx.a, dx.a, r);
+        if (HALF && (kFew || p.rotary[k])) {
+          mul(xr.b, fx.b, r);
+          fma(dw[k].b, fh[k].b, xr.b, dw[k].b);
+          fma(dx.b, fx.b, along, fu[k].b);
+          mul(dx.b, dx.b, r);
         }
-      const float r = rsqrtf(group_sum(ss, a.lanes) * inv_dim + a.eps);
-      const float along = group_sum(ux, a.lanes) * inv_dim * r * r;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (p.there[k] && live) {
-          const Values<V, HALF> fw = values_of<T, V, HALF, WIDE>(w[k], p.rotary[k]);
-          Values<V, HALF> dx;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            dw[k].a[e] = fmaf(fh[k].a[e], fx[k].a[e] * r, dw[k].a[e]);
-            dx.a[e] = r * (fh[k].a[e] * fw.a[e] - fx[k].a[e] * along);
-            if (HALF) {
-              dw[k].b[e] = fmaf(fh[k].b[e], fx[k].b[e] * r, dw[k].b[e]);
-              dx.b[e] = r * (fh[k].b[e] * fw.b[e] - fx[k].b[e] * along);
-            }
-          }
-          store<T, V, HALF, WIDE>(out, dx, p.at[k], half, p.rotary[k]);
-        }
+        if (live && p.there[k]) store<T, V, HALF, WIDE>(out, dx, p.at[k], half, p.rotary[k]);
+      }
     }
   }
+  if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
   if (a.partials == nullptr) return;
   // the groups of a warp, then the warps, in a fixed order
   const int warp = tid >> 5;
+  float* sums = table + warp * 512;
+  __syncthreads();                                 // the last angles have been read
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -273,8 +582,8 @@ __global__ void __launch_bounds__(kRopeThreads, K == 1 ? 3 : 1) k_norm_rope_grad
         if (HALF) db += __shfl_xor_sync(0xffffffffu, db, m);
       }
       if (p.there[k] && (tid & 31) < a.lanes) {
-        sums[warp][p.at[k] + e] = da;
-        if (HALF && p.rotary[k]) sums[warp][p.at[k] + half + e] = db;
+        sums[p.at[k] + e] = da;
+        if (HALF && p.rotary[k]) sums[p.at[k] + half + e] = db;
       }
     }
   }
@@ -282,7 +591,7 @@ __global__ void __launch_bounds__(kRopeThreads, K == 1 ? 3 : 1) k_norm_rope_grad
   for (int c = tid; c < a.dim; c += kRopeThreads) {
     float s8 = 0.f;
 #pragma unroll
-    for (int i = 0; i < kRopeThreads / 32; ++i) s8 += sums[i][c];
+    for (int i = 0; i < kRopeThreads / 32; ++i) s8 += table[i * 512 + c];
     a.partials[(size_t)blockIdx.x * a.dim + c] = s8;
   }
 }
@@ -321,21 +630,26 @@ template <typename T, int V, bool HALF, bool WIDE, int K>
 int launch_as(NormArgs a, bool grad, float* dqw, float* dkw, cudaStream_t st) {
   const int rot = a.r.rot, half = rot / 2, units = (HALF ? half / V : rot / V) + (a.dim - rot) / V;
   a.lanes = 1;
-  while (a.lanes < 32 && a.lanes < units) a.lanes *= 2;
+  while (a.lanes < 32 && a.lanes * K < units) a.lanes *= 2;
   int sms = 0;
   if (int rc = sm_count(&sms); rc != OSCAR_OK) return rc;
-  a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.r.n / (4 * sms)));
   if (!grad) {
+    a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.r.n / (4 * sms)));
     k_norm_rope<T, V, HALF, WIDE, K><<<(a.r.n - 1) / a.tokens + 1, kRopeThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
   }
+  a.tokens = std::max(1, std::min(std::min(kGradTable / half, kGradTokens), a.r.n / (2 * sms)));
   // CTAs are shared between q and k by their heads
   const int tiles = (a.r.n - 1) / a.tokens + 1, heads = a.q.heads + a.k.heads;
   const int most_q = std::max(1, std::min(kGradCtas - 1, (int)((long long)kGradCtas * a.q.heads / heads)));
   a.q_ctas = a.q.heads == 0 ? 0 : std::min(tiles, a.k.heads == 0 ? kGradCtas : most_q);
   const int k_ctas = a.k.heads == 0 ? 0 : std::min(tiles, a.q.heads == 0 ? kGradCtas : kGradCtas - most_q);
   const int ctas = a.q_ctas + k_ctas;
-  k_norm_rope_grad<T, V, HALF, WIDE, K><<<ctas, kRopeThreads, 0, st>>>(a);
+  constexpr int smem = grad_smem<T, V, HALF, WIDE, K>();
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(k_norm_rope_grad<T, V, HALF, WIDE, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return OSCAR_ERR_CUDA;
+  k_norm_rope_grad<T, V, HALF, WIDE, K><<<ctas, kRopeThreads, smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return OSCAR_ERR_CUDA;
   if (a.partials == nullptr) return OSCAR_OK;
   k_norm_rope_sum<<<dim3((a.dim + 31) / 32, 2), dim3(32, kSumRows), 0, st>>>(a.partials, a.dim, a.q_ctas, ctas, dqw, dkw);
@@ -349,7 +663,9 @@ int launch_layout(const NormArgs& a, int bytes, bool grad, float* dqw, float* dk
   const int rot = a.r.rot;
   if (bytes == 16) {
     const int units = (HALF ? rot / 2 : rot) / V16 + (a.dim - rot) / V16;
-    if (units <= 32) return launch_as<T, V16, HALF, true, 1>(a, grad, dqw, dkw, st);
+    // 32 bytes a lane: a unit of the half layout with its partners, two of the pairs layout (one: PAIRS_MEASURED)
+    constexpr int kFew = HALF ? 1 : 2;
+    if (units <= 32 * kFew) return launch_as<T, V16, HALF, true, kFew>(a, grad, dqw, dkw, st);
     return launch_as<T, V16, HALF, true, 128 / (32 * V16 / 4)>(a, grad, dqw, dkw, st);
   }
   if (bytes == 8) return launch_as<T, V8, HALF, true, 16 / V8>(a, grad, dqw, dkw, st);

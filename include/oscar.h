@@ -478,7 +478,8 @@ int oscar_rope_axes(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int 
  * end (squares beyond float32's range are the caller's to avoid). q and k, positions and padded rows as for
  * oscar_rope_axes; out = in with equal strides works in place.
  *  q_weight, k_weight : device [head_dim], of the rows' dtype, or NULL: ones;  eps > 0
- * Errors: as oscar_rope_axes, INVALID_ARG (eps, a weight not aligned to its type). Works without a cache. */
+ * Errors: as oscar_rope_axes, INVALID_ARG (eps, a weight not aligned to its type), UNSUPPORTED (more than 8,192 heads of q
+ * or k). Works without a cache. */
 typedef struct oscar_head_norm {
   const void *q_weight, *k_weight;
   float eps;

@@ -90,6 +90,11 @@ def test_unsupported_heads(osc, call, dim):
     assert call(osc, dict(dim=dim)) == osc.ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("call", [_norm, _grad])
+def test_too_many_heads(osc, call):
+    assert call(osc, dict(heads=8193, gheads=8193)) == osc.ERR_UNSUPPORTED
+
+
 def test_missing_structures_and_no_work(osc):
     lib, none = osc.lib(), osc.RopeTensor()
     assert lib.oscar_rope_axes(_row(osc), none, 1, 128, 0, 4096, None, 0, None) == osc.ERR_INVALID_ARG
