@@ -899,30 +899,41 @@ def norm_rope_backward(plan: RopePlan, q, k, positions, grad_q, grad_k, q_weight
     pos, n = plan.positions(positions, dev, what)
     dtype, shape = q.dtype, q.shape
     code = _rows_code(dtype, what)
-    if len(shape) != 3 or n >> 31 or grad_q is None or grad_q.shape != shape or (k is None) != (grad_k is None) or \
-            (k is not None and k.shape != grad_k.shape):
+    if len(shape) != 3 or n >> 31 or grad_q is None or (k is None) != (grad_k is None):
         raise OscarError(ERR_INVALID_ARG, what)
     dim = shape[2]
     norm = _head_norm(q_weight, k_weight, eps, dtype, dim, dev, what)
-    grads, _ = _rows(((grad_q, grad_q), (grad_k, grad_k)), dtype, n, dim, dev, what)
     args, outs = _rows(((q, dq), (k, dk)), dtype, n, dim, dev, what)
-    dw = ws = None
+    grads = []
+    for x, g in ((q, grad_q), (k, grad_k)):
+        if g is None:
+            grads.append(RopeTensor())
+            continue
+        token, head, channel = g.stride() if g.dim() == 3 else (0, 0, 0)
+        if g.dtype is not dtype or g.get_device() != dev or g.shape != x.shape or channel != 1:
+            raise OscarError(ERR_INVALID_ARG, what)
+        grads.append(RopeTensor(g.data_ptr(), None, token, head, 0, 0, x.shape[1]))
+    dqw = dkw = ws = None
     if weight_grads:
-        dw = _empty((2, dim), dtype=_f32, device=dev)
-        ws = q.new_empty(norm_rope_workspace_bytes(dim), dtype=_u8) if workspace is None else workspace
+        dqw, dkw = _empty(dim, dtype=_f32, device=dev), _empty(dim, dtype=_f32, device=dev)
+        ws = _empty(norm_rope_workspace_bytes(dim), dtype=_u8, device=dev) if workspace is None else workspace
         if ws.get_device() != dev or not ws.is_contiguous():
             raise OscarError(ERR_INVALID_ARG, what)
     _check(_lib.oscar_norm_rope_backward(args[0], args[1], grads[0], grads[1], n, dim, code, pos.data_ptr(),
-                                         plan.rotary(layout), norm, None if dw is None else dw.data_ptr(),
-                                         None if dw is None else dw.data_ptr() + 4 * dim, _ptr(ws),
+                                         plan.rotary(layout), norm, _ptr(dqw), _ptr(dkw), _ptr(ws),
                                          0 if ws is None else ws.nbytes, st), what)
-    return outs[0], outs[1], None if dw is None else dw[0], None if dw is None else dw[1]
+    return outs[0], outs[1], dqw, dkw
+
+
+_norm_rope_workspace = {}                          # head_dim: bytes, which depend on nothing else
 
 
 def norm_rope_workspace_bytes(head_dim: int) -> int:
-    n = ctypes.c_size_t()
-    _check(_lib.oscar_norm_rope_workspace_bytes(head_dim, ctypes.byref(n)), "oscar_norm_rope_workspace_bytes")
-    return n.value
+    if head_dim not in _norm_rope_workspace:
+        n = ctypes.c_size_t()
+        _check(_lib.oscar_norm_rope_workspace_bytes(head_dim, ctypes.byref(n)), "oscar_norm_rope_workspace_bytes")
+        _norm_rope_workspace[head_dim] = n.value
+    return _norm_rope_workspace[head_dim]
 
 
 def calibrate_codebook(x_rot, tau) -> np.ndarray:

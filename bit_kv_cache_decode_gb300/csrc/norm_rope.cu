@@ -12,6 +12,8 @@
 // Gradient: the weights' sums are held in registers over all rows of a CTA, which walks tokens of q or of k; CTAs'
 // partial sums go to the workspace and are added in a fixed order by a second kernel, so results do not depend on timing.
 #include <algorithm>
+#include <mutex>
+#include <set>
 #include <type_traits>
 
 #include "rope.cuh"
@@ -36,27 +38,34 @@ struct NormArgs {
   float* partials;                                 // gradient: [CTA][dim], or null
 };
 
-// whether a lane holds no more than 32 bytes of a row
+// Units of a row. Half layout: two chunks of V channels, those of the first half that turn and their partners; pairs layout:
+// one chunk. Behind the rotated channels a unit of either layout is as many channels in a row. A lane holds K units.
+template <bool HALF> constexpr int kParts = HALF ? 2 : 1;
+// whether a lane holds no more than 32 bytes of a row: all but odd alignments and the longest float32 rows
 template <typename T, int V, bool HALF, int K>
 constexpr bool few() {
-  return sizeof(T) * V * K * (HALF ? 2 : 1) <= 32;
+  return sizeof(T) * V * K * kParts<HALF> <= 32;
+}
+template <int V, bool HALF>
+__host__ __device__ inline int units_of(int dim, int rot) {
+  constexpr int n = V * kParts<HALF>;
+  return (HALF ? rot / 2 / V : rot / V) + (dim - rot + n - 1) / n;
 }
 
-// What a lane holds of a row: K units.
-template <typename T, int V, bool HALF, int K>
+template <int V, bool HALF, int K>
 struct Place {
-  int at[K], unit[K], rot_units;                   // first channel of unit k
-  bool there[K], rotary[K];
+  int rot_units, unit[K], at[K], second[K];        // first channel of a unit, and from it to its second chunk
+  bool there[K][kParts<HALF>], rotary[K];
   __device__ __forceinline__ Place(int lane, int lanes, int dim, int rot) {
     rot_units = HALF ? rot / 2 / V : rot / V;
-    const int units = rot_units + (dim - rot) / V;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = lane + k * lanes;
-      unit[k] = u;
-      there[k] = u < units;
-      rotary[k] = u < rot_units;
-      at[k] = rotary[k] ? u * V : rot + (u - rot_units) * V;
+      unit[k] = lane + k * lanes;
+      rotary[k] = unit[k] < rot_units;
+      at[k] = rotary[k] ? unit[k] * V : rot + (unit[k] - rot_units) * V * kParts<HALF>;
+      second[k] = rotary[k] ? rot / 2 : V;
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p) there[k][p] = at[k] + p * second[k] + V <= dim;
     }
   }
 };
@@ -110,10 +119,6 @@ __device__ __forceinline__ void dot(float2& s, const float (&a)[N], const float 
   if constexpr (N % 2) s.x = fmaf(a[N - 1], b[N - 1], s.x);
 }
 
-// A unit's values in float32: V channels and, for a rotary unit of the half layout, their V partners (else zeros).
-template <int V, bool HALF> struct Values {
-  float a[V], b[HALF ? V : 1];
-};
 // N values to and from float32, two of a 16-bit type at a time where they come as words
 template <typename T, int N, bool WIDE>
 __device__ __forceinline__ void widen(float (&f)[N], const T* x) {
@@ -153,14 +158,77 @@ __device__ __forceinline__ void narrow(T* x, const float (&f)[N]) {
     for (int i = 0; i < N; ++i) x[i] = from_f<T>(f[i]);
   }
 }
-template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ Values<V, HALF> values_of(const Unit<T, V, V, HALF, WIDE>& x) {
-  Values<V, HALF> f;
-  widen<T, V, WIDE>(f.a, x.a.v);
-  if constexpr (HALF) widen<T, V, WIDE>(f.b, x.b.v);
-  else f.b[0] = 0.f;
-  return f;
+// each element is touched once: streaming accesses where they are wide
+template <typename T, int V, bool WIDE>
+__device__ __forceinline__ void get(Vec<T, V, WIDE>& x, const T* at) {
+  if constexpr (WIDE) {
+    using Bits = typename AccessOf<sizeof(T) * V>::type;
+    *reinterpret_cast<Bits*>(x.v) = __ldcs(reinterpret_cast<const Bits*>(at));
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) x.v[e] = at[e];
+  }
 }
+template <typename T, int V, bool WIDE>
+__device__ __forceinline__ void put(T* at, const Vec<T, V, WIDE>& x) {
+  if constexpr (WIDE) {
+    using Bits = typename AccessOf<sizeof(T) * V>::type;
+    __stcs(reinterpret_cast<Bits*>(at), *reinterpret_cast<const Bits*>(x.v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) at[e] = x.v[e];
+  }
+}
+// What a lane has of a row, as it is loaded and in float32.
+template <typename T, int V, bool HALF, bool WIDE, int K>
+struct Raw {
+  Vec<T, V, WIDE> x[K][kParts<HALF>];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p)
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[k][p].v[e] = from_f<T>(0.f);
+  }
+  __device__ __forceinline__ void load(const Place<V, HALF, K>& pl, const T* in) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p)
+        if (pl.there[k][p]) get<T, V, WIDE>(x[k][p], in + pl.at[k] + p * pl.second[k]);
+  }
+};
+template <int V, bool HALF, int K>
+struct Values {
+  float f[K][kParts<HALF>][V];
+  template <typename T, bool WIDE>
+  __device__ __forceinline__ explicit Values(const Raw<T, V, HALF, WIDE, K>& r) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p) widen<T, V, WIDE>(f[k][p], r.x[k][p].v);
+  }
+  __device__ __forceinline__ explicit Values(float x) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p)
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[k][p][e] = x;
+  }
+  template <typename T, bool WIDE>
+  __device__ __forceinline__ void store(const Place<V, HALF, K>& pl, T* out) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int p = 0; p < kParts<HALF>; ++p) {
+        Vec<T, V, WIDE> x;
+        narrow<T, V, WIDE>(x.v, f[k][p]);
+        if (pl.there[k][p]) put<T, V, WIDE>(out + pl.at[k] + p * pl.second[k], x);
+      }
+  }
+};
 
 // The rotations of a token, as its rotary units read them: 4 floats a pair, weights included (wa, wb: of the pair's
 // channels). Half layout: V floats each of wa cos, -wb sin, wb cos, wa sin; pairs layout: V floats of (wa cos, wb cos) and V
@@ -179,69 +247,27 @@ __device__ __forceinline__ void put_turn(float* token, int rot_units, int j, flo
 }
 // a unit's values turned: Rot(w x) for the table's weights w
 template <int V, bool HALF>
-__device__ __forceinline__ void turn(Values<V, HALF>& f, const float* token, int rot_units, int u) {
+__device__ __forceinline__ void turn(float (&f)[kParts<HALF>][V], const float* token, int rot_units, int u) {
   constexpr int kFloats = HALF ? 4 * V : 2 * V;
-  float t[kFloats];
+  float t[kFloats / V][V], swapped[V];
 #pragma unroll
   for (int i = 0; i < kFloats / 4; ++i) {
     const float4 c = *reinterpret_cast<const float4*>(token + (i * rot_units + u) * 4);
-    t[4 * i] = c.x;
-    t[4 * i + 1] = c.y;
-    t[4 * i + 2] = c.z;
-    t[4 * i + 3] = c.w;
+    t[4 * i / V][4 * i % V] = c.x;
+    t[(4 * i + 1) / V][(4 * i + 1) % V] = c.y;
+    t[(4 * i + 2) / V][(4 * i + 2) % V] = c.z;
+    t[(4 * i + 3) / V][(4 * i + 3) % V] = c.w;
   }
-  float swapped[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) swapped[e] = f[0][HALF ? e : e ^ 1];
+  mul<V>(f[0], f[0], t[0]);
   if constexpr (HALF) {
-    float ac[V], bs[V], bc[V], as[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      ac[e] = t[e];
-      bs[e] = t[V + e];
-      bc[e] = t[2 * V + e];
-      as[e] = t[3 * V + e];
-      swapped[e] = f.a[e];
-    }
-    mul<V>(f.a, f.a, ac);
-    fma<V>(f.a, f.b, bs, f.a);
-    mul<V>(f.b, f.b, bc);
-    fma<V>(f.b, swapped, as, f.b);
+    fma<V>(f[0], f[1], t[1], f[0]);
+    mul<V>(f[1], f[1], t[2]);
+    fma<V>(f[1], swapped, t[3], f[1]);
   } else {
-    float c2[V], s2[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      c2[e] = t[e];
-      s2[e] = t[V + e];
-      swapped[e] = f.a[e ^ 1];
-    }
-    mul<V>(f.a, f.a, c2);
-    fma<V>(f.a, swapped, s2, f.a);
+    fma<V>(f[0], swapped, t[1], f[0]);
   }
-}
-template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ void store(T* out, const Values<V, HALF>& f, int at, int half, bool rotary) {
-  Unit<T, V, V, HALF, WIDE> x;
-  narrow<T, V, WIDE>(x.a.v, f.a);
-  if constexpr (HALF) narrow<T, V, WIDE>(x.b.v, f.b);
-  x.store(out, at, half, rotary);
-}
-// What a lane has nothing of is zeros, so that the arithmetic needs no conditions: only loads and stores do.
-template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ Unit<T, V, V, HALF, WIDE> zeros() {
-  Unit<T, V, V, HALF, WIDE> x;
-#pragma unroll
-  for (int e = 0; e < V; ++e) x.a.v[e] = x.b.v[e] = from_f<T>(0.f);
-  return x;
-}
-template <typename T, int V, bool HALF, bool WIDE>
-__device__ __forceinline__ Unit<T, V, V, HALF, WIDE> weights(const void* w, int at, int half, bool rotary) {
-  Unit<T, V, V, HALF, WIDE> x = zeros<T, V, HALF, WIDE>();
-  if (w != nullptr) {
-    x.load(static_cast<const T*>(w), at, half, rotary);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) x.a.v[e] = x.b.v[e] = from_f<T>(1.f);
-  }
-  return x;
 }
 __device__ __forceinline__ float group_sum(float s, int lanes) {
 #pragma unroll
@@ -300,23 +326,25 @@ __device__ __forceinline__ float weight_at(const void* w, int c) {
   return w != nullptr ? to_f(static_cast<const T*>(w)[c]) : 1.f;
 }
 
+// Rows are zeros where a lane has nothing of them, so that the arithmetic of the usual rows needs no conditions.
 template <typename T, int V, bool HALF, bool WIDE, int K>
 __global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 4 : 2) k_norm_rope(NormArgs a) {
   __shared__ __align__(16) float table[2][4 * kRopeTable];   // of q, of k: [token][4 rot / 2]
   __shared__ __align__(16) float rest[2][512];     // the weights of the channels behind the rotated ones
   __shared__ int pos_s[kRopeTokens * kRopeAxes];
-  constexpr bool kFew = few<T, V, HALF, K>();      // of wide rows, units that a lane does not have are skipped
-  constexpr int kBatch = kFew ? 2 : 1;           // rows a group has in flight
+  constexpr bool kFew = few<T, V, HALF, K>();
+  constexpr int kBatch = kFew ? 2 : 1;             // rows a group has in flight
+  using Data = Raw<T, V, HALF, WIDE, K>;
   const int rot = a.r.rot, half = rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.r.n - t0), tid = threadIdx.x;
   const int lane = tid & (a.lanes - 1), group = tid / a.lanes, groups = kRopeThreads / a.lanes;
-  const Place<T, V, HALF, K> p(lane, a.lanes, a.dim, rot);
+  const Place<V, HALF, K> pl(lane, a.lanes, a.dim, rot);
   load_positions(a.r, t0, nt, pos_s, tid, kRopeThreads);
   __syncthreads();
   for (int i = tid; i < nt * half; i += kRopeThreads) {
     const int t = i / half, j = i - t * half, ca = HALF ? j : 2 * j, cb = HALF ? j + half : 2 * j + 1;
     const float2 cs = rope_turn(a.r, pos_s + t * kRopeAxes, j, 1.f);
-    put_turn<V, HALF>(table[0] + t * 2 * rot, p.rot_units, j, cs, weight_at<T>(a.qw, ca), weight_at<T>(a.qw, cb));
-    put_turn<V, HALF>(table[1] + t * 2 * rot, p.rot_units, j, cs, weight_at<T>(a.kw, ca), weight_at<T>(a.kw, cb));
+    put_turn<V, HALF>(table[0] + t * 2 * rot, pl.rot_units, j, cs, weight_at<T>(a.qw, ca), weight_at<T>(a.qw, cb));
+    put_turn<V, HALF>(table[1] + t * 2 * rot, pl.rot_units, j, cs, weight_at<T>(a.kw, ca), weight_at<T>(a.kw, cb));
   }
   for (int c = rot + tid; c < a.dim; c += kRopeThreads) {
     rest[0][c - rot] = weight_at<T>(a.qw, c);
@@ -332,7 +360,7 @@ __global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 4 : 2) k_
     // the same trips for every lane of a warp: the row's sum is a shuffle
 #pragma unroll 1
     for (int i0 = 0; i0 < nt * s.heads; i0 += kBatch * groups) {
-      Unit<T, V, V, HALF, WIDE> x[kBatch][K];
+      Data x[kBatch];
       T* out[kBatch];
       const float* turns[kBatch];
 #pragma unroll
@@ -340,124 +368,116 @@ __global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 4 : 2) k_
         const bool live = row.t < nt && pos_s[row.t * kRopeAxes] >= 0;   // a padded row is left as it is
         out[b] = live ? row.out : nullptr;
         turns[b] = table[isk] + (live ? row.t : 0) * 2 * rot;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          x[b][k] = zeros<T, V, HALF, WIDE>();
-          if (live && p.there[k]) x[b][k].load(row.in, p.at[k], half, p.rotary[k]);
-        }
+        x[b].clear();
+        if (live) x[b].load(pl, row.in);
         row.next();
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
+        Values<V, HALF, K> f(x[b]);
         float2 ss = make_float2(0.f, 0.f);
-        Values<V, HALF> f[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (!kFew && !p.there[k]) continue;
-          f[k] = values_of<T, V, HALF, WIDE>(x[b][k]);
-          dot(ss, f[k].a, f[k].a);
-          if (HALF && (kFew || p.rotary[k])) dot(ss, f[k].b, f[k].b);
-        }
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int p = 0; p < kParts<HALF>; ++p)
+            if (kFew || pl.there[k][p]) dot(ss, f.f[k][p], f.f[k][p]);
         const float r = rsqrtf(group_sum(ss.x + ss.y, a.lanes) * inv_dim + a.eps);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!kFew && !p.there[k]) continue;
-          mul(f[k].a, f[k].a, r);
-          if (HALF && (kFew || p.rotary[k])) mul(f[k].b, f[k].b, r);
-          if (p.rotary[k]) {
-            turn<V, HALF>(f[k], turns[b], p.rot_units, p.unit[k]);
-          } else if (p.there[k]) {
+          if (!kFew && !pl.there[k][0]) continue;
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[k].a[e] *= rest[isk][p.at[k] - rot + e];
+          for (int p = 0; p < kParts<HALF>; ++p) mul(f.f[k][p], f.f[k][p], r);
+          if (pl.rotary[k]) {
+            turn<V, HALF>(f.f[k], turns[b], pl.rot_units, pl.unit[k]);
+          } else {
+#pragma unroll
+            for (int p = 0; p < kParts<HALF>; ++p)
+              if (pl.there[k][p])
+#pragma unroll
+                for (int e = 0; e < V; ++e) f.f[k][p][e] *= rest[isk][pl.at[k] + p * V - rot + e];
           }
-          if (out[b] != nullptr && p.there[k]) store<T, V, HALF, WIDE>(out[b], f[k], p.at[k], half, p.rotary[k]);
         }
+        if (out[b] != nullptr) f.template store<T, WIDE>(pl, out[b]);
       }
     }
   }
 }
 
-// What a lane has loaded of a row for the gradient.
-template <typename T, int V, bool HALF, bool WIDE, int K>
-struct GradRow {
-  Unit<T, V, V, HALF, WIDE> x[K], g[K];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < K; ++k) x[k] = g[k] = zeros<T, V, HALF, WIDE>();
-  }
-  template <typename P>
-  __device__ __forceinline__ void load(const P& p, const T* in, const T* gin, int half) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (p.there[k]) {
-        x[k].load(in, p.at[k], half, p.rotary[k]);
-        g[k].load(gin, p.at[k], half, p.rotary[k]);
-      }
-  }
-  // The same through shared memory: asynchronous 16-byte copies into slots of the thread's own, chunk j of all threads side by
-  // side at slot + j * 16 * kRopeThreads.
-  static constexpr int kParts = HALF ? 2 : 1, kChunks = 2 * K * kParts;
-  template <typename P>
-  static __device__ __forceinline__ void copy(uint32_t slot, const P& p, const T* in, const T* gin, int half) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int part = 0; part < kParts; ++part)
-        if (p.there[k] && (part == 0 || p.rotary[k])) {
-          const int at = p.at[k] + part * half, j = 2 * (k * kParts + part);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + j * 16 * kRopeThreads), "l"(in + at) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (j + 1) * 16 * kRopeThreads), "l"(gin + at)
-                       : "memory");
-        }
-  }
-  template <typename P>
-  __device__ __forceinline__ void take(uint32_t slot, const P& p) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int part = 0; part < kParts; ++part)
-        if (p.there[k] && (part == 0 || p.rotary[k])) {
-          const int j = 2 * (k * kParts + part);
-          const uint4 cx = lds128(slot + j * 16 * kRopeThreads), cg = lds128(slot + (j + 1) * 16 * kRopeThreads);
-          *reinterpret_cast<uint4*>(part ? x[k].b.v : x[k].a.v) = cx;
-          *reinterpret_cast<uint4*>(part ? g[k].b.v : g[k].a.v) = cg;
-        }
-  }
-};
-
-// The rows of a group, some trips ahead of those it works on: trip by trip, tokens by tokens as the CTA walks them.
+// A group's rows, some trips ahead of those it works on: trip by trip, tokens by tokens as the CTA walks them.
 template <typename T>
 struct Ahead {
   RopeSide s;
-  Walk<T> row;                                     // out: the gradient's row
-  long long t0, step, n;
+  Walk<T> row;                                     // out: the row of the gradient that is given
+  long long t0, end;
   int tokens, group, groups, i0, nt;
-  __device__ __forceinline__ Ahead(const RopeSide& s_, long long t0_, long long step_, long long n_, int tokens_, int group_, int groups_)
-      : s(s_), row(s_, t0_, group_, groups_), t0(t0_), step(step_), n(n_), tokens(tokens_), group(group_), groups(groups_), i0(0),
-        nt((int)min((long long)tokens_, n_ - t0_)) {}
-  __device__ __forceinline__ bool there() const { return row.t < nt; }     // nt < 1 behind the last tokens
+  __device__ __forceinline__ Ahead(const RopeSide& s_, long long begin, long long end_, int tokens_, int group_, int groups_)
+      : s(s_), row(s_, begin, group_, groups_), t0(begin), end(end_), tokens(tokens_), group(group_), groups(groups_), i0(0),
+        nt((int)min((long long)tokens_, end_ - begin)) {}
+  __device__ __forceinline__ bool there() const { return row.t < nt; }     // behind the last tokens nt is 0
   __device__ __forceinline__ void next() {
     i0 += groups;
     if (i0 < nt * s.heads) {
       row.next();
     } else {
-      t0 += step;
+      t0 = min(t0 + tokens, end);
       i0 = 0;
-      nt = (int)max(min((long long)tokens, n - t0), 0ll);
+      nt = (int)min((long long)tokens, end - t0);
       row = Walk<T>(s, t0, group, groups);
     }
   }
 };
 
+// Rows on their way: x and g of a row by asynchronous copies into slots of the thread's own in shared memory, chunk j of all
+// threads side by side (no bank conflicts, no registers). Single elements, and rows of more than 32 bytes a lane, wait in registers.
+constexpr int kSlots = 3;                          // one row worked on, two on their way
 template <typename T, int V, bool HALF, bool WIDE, int K>
-constexpr bool grad_async() {
-  return WIDE && sizeof(T) * V == 16 && few<T, V, HALF, K>();
-}
-constexpr int kSlots = 3;                          // rows of a thread in shared memory: one worked on, two on their way
-template <typename T, int V, bool HALF, bool WIDE, int K>
-constexpr int grad_smem() {
-  return 16 * kGradTable + (grad_async<T, V, HALF, WIDE, K>() ? kSlots * GradRow<T, V, HALF, WIDE, K>::kChunks * 16 * kRopeThreads : 0);
-}
+struct Slots {
+  static constexpr bool kAsync = WIDE && few<T, V, HALF, K>();
+  static constexpr int kBytes = sizeof(T) * V, kChunk = kBytes * kRopeThreads, kSlot = 2 * K * kParts<HALF> * kChunk;
+  static constexpr int kSmem = kAsync ? kSlots * kSlot : 0;
+  static __device__ __forceinline__ void copy(uint32_t slot, const Place<V, HALF, K>& pl, const T* in, const T* gin) {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int p = 0; p < kParts<HALF>; ++p)
+          if (pl.there[k][p]) {
+            const int c = pl.at[k] + p * pl.second[k];
+            const uint32_t to = slot + 2 * (k * kParts<HALF> + p) * kChunk;
+            if constexpr (kBytes == 16) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(in + c) : "memory");
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kChunk), "l"(gin + c) : "memory");
+            } else {
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(in + c) : "memory");
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + kChunk), "l"(gin + c) : "memory");
+            }
+          }
+    }
+  }
+  // chunks that a lane does not have stay the zeros of the start
+  static __device__ __forceinline__ void clear(uint32_t slots) {
+    if constexpr (kAsync)
+      for (int i = 0; i < kSlots * kSlot / kChunk; ++i)
+        for (int b = 0; b < kBytes; b += 4) sts32(slots + i * kChunk + b, 0u);
+  }
+  static __device__ __forceinline__ void take(uint32_t slot, Raw<T, V, HALF, WIDE, K>& x, Raw<T, V, HALF, WIDE, K>& g) {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int p = 0; p < kParts<HALF>; ++p) {
+          const uint32_t at = slot + 2 * (k * kParts<HALF> + p) * kChunk;
+          if constexpr (kBytes == 16) {
+            *reinterpret_cast<uint4*>(x.x[k][p].v) = lds128(at);
+            *reinterpret_cast<uint4*>(g.x[k][p].v) = lds128(at + kChunk);
+          } else {
+            *reinterpret_cast<uint2*>(x.x[k][p].v) = lds64(at);
+            *reinterpret_cast<uint2*>(g.x[k][p].v) = lds64(at + kChunk);
+          }
+        }
+    }
+  }
+};
 
 template <typename T, int V, bool HALF, bool WIDE, int K>
 __global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 2 : 1) k_norm_rope_grad(NormArgs a) {
@@ -465,134 +485,135 @@ __global__ void __launch_bounds__(kRopeThreads, few<T, V, HALF, K>() ? 2 : 1) k_
   float* const table = smem;                       // [token][4 rot / 2]; at the end a warp's share of dw: [8][512]
   __shared__ int pos_s[kGradTokens * kRopeAxes];
   static_assert(4 * kGradTable >= kRopeThreads / 32 * 512, "the warps' shares fit");
-  using Row = GradRow<T, V, HALF, WIDE, K>;
-  constexpr bool kAsync = grad_async<T, V, HALF, WIDE, K>(), kFew = few<T, V, HALF, K>();
+  using Data = Raw<T, V, HALF, WIDE, K>;
+  using Ring = Slots<T, V, HALF, WIDE, K>;
+  using Floats = Values<V, HALF, K>;
+  constexpr bool kFew = few<T, V, HALF, K>();
   const int rot = a.r.rot, half = rot / 2, tid = threadIdx.x;
   const int lane = tid & (a.lanes - 1), group = tid / a.lanes, groups = kRopeThreads / a.lanes;
   const bool isq = (int)blockIdx.x < a.q_ctas;
   const RopeSide s = isq ? a.q : a.k, sg = isq ? a.gq : a.gk;
   const int first = isq ? blockIdx.x : blockIdx.x - a.q_ctas, ctas = isq ? a.q_ctas : gridDim.x - a.q_ctas;
-  const long long step = (long long)ctas * a.tokens;
-  const Place<T, V, HALF, K> p(lane, a.lanes, a.dim, rot);
-  Unit<T, V, V, HALF, WIDE> w[K];
-  Values<V, HALF> dw[K] = {};
+  // a range of the tokens, a few at a time (every ctas-th few: a fifth of the time in CTAs that had one more to do)
+  const long long begin = (long long)a.r.n * first / ctas, end = (long long)a.r.n * (first + 1) / ctas;
+  const Place<V, HALF, K> pl(lane, a.lanes, a.dim, rot);
+  Floats fw(0.f), dw(0.f);
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    w[k] = p.there[k] ? weights<T, V, HALF, WIDE>(isq ? a.qw : a.kw, p.at[k], half, p.rotary[k]) : zeros<T, V, HALF, WIDE>();
+#pragma unroll
+    for (int p = 0; p < kParts<HALF>; ++p)
+      if (pl.there[k][p])
+#pragma unroll
+        for (int e = 0; e < V; ++e) fw.f[k][p][e] = weight_at<T>(isq ? a.qw : a.kw, pl.at[k] + p * pl.second[k] + e);
   const float inv_dim = 1.f / (float)a.dim;
   // A group's next rows are on their way while it works on one, also across the CTA's tokens.
   const RopeSide both = {s.in, const_cast<void*>(sg.in), s.in_tok, s.in_head, sg.in_tok, sg.in_head, s.heads};
-  Ahead<T> ahead(both, (long long)first * a.tokens, step, a.r.n, a.tokens, group, groups);
-  const uint32_t slots = smem_addr(smem) + 16 * kGradTable + 16 * tid;
+  Ahead<T> ahead(both, begin, end, a.tokens, group, groups);
+  const uint32_t slots = smem_addr(smem) + 16 * kGradTable + Ring::kBytes * tid;
   int slot = 0;                                    // of the row that is worked on
-  Row next;
+  Ring::clear(slots);
+  Data next_x, next_g;
   auto fetch = [&](int to) {
-    if constexpr (kAsync) {
-      if (ahead.there()) Row::copy(slots + to * (Row::kChunks * 16 * kRopeThreads), p, ahead.row.in, ahead.row.out, half);
+    if constexpr (Ring::kAsync) {
+      if (ahead.there()) Ring::copy(slots + to * Ring::kSlot, pl, ahead.row.in, ahead.row.out);
       asm volatile("cp.async.commit_group;" ::: "memory");
     } else {
-      next.clear();
-      if (ahead.there()) next.load(p, ahead.row.in, ahead.row.out, half);
+      next_x.clear();
+      next_g.clear();
+      if (ahead.there()) {
+        next_x.load(pl, ahead.row.in);
+        next_g.load(pl, ahead.row.out);
+      }
     }
     ahead.next();
   };
 #pragma unroll 1
-  for (int i = 0; i < (kAsync ? kSlots - 1 : 1); ++i) fetch(i);
+  for (int i = 0; i < (Ring::kAsync ? kSlots - 1 : 1); ++i) fetch(i);
 #pragma unroll 1
-  for (long long t0 = (long long)first * a.tokens; t0 < a.r.n; t0 += step) {
-    const int nt = (int)min((long long)a.tokens, a.r.n - t0), items = nt * s.heads;
+  for (long long t0 = begin; t0 < end; t0 += a.tokens) {
+    const int nt = (int)min((long long)a.tokens, end - t0), items = nt * s.heads;
     Walk<T> row(s, t0, group, groups);
     __syncthreads();                               // the last tokens' angles have been read
     load_positions(a.r, (int)t0, nt, pos_s, tid, kRopeThreads);
     __syncthreads();
     for (int i = tid; i < nt * half; i += kRopeThreads) {
       const int t = i / half, j = i - t * half;
-      put_turn<V, HALF>(table + t * 2 * rot, p.rot_units, j, rope_turn(a.r, pos_s + t * kRopeAxes, j, -1.f), 1.f, 1.f);
+      put_turn<V, HALF>(table + t * 2 * rot, pl.rot_units, j, rope_turn(a.r, pos_s + t * kRopeAxes, j, -1.f), 1.f, 1.f);
     }
     __syncthreads();
 #pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += groups) {
       const bool live = row.t < nt && pos_s[row.t * kRopeAxes] >= 0;
-      Row now;
-      now.clear();
-      if constexpr (kAsync) {
-        // the row worked on before is read: its slot is the next to fill
+      Data x, g;
+      if constexpr (Ring::kAsync) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
-        if (live) now.take(slots + slot * (Row::kChunks * 16 * kRopeThreads), p);
-        fetch(slot == 0 ? kSlots - 1 : slot - 1);
+        Ring::take(slots + slot * Ring::kSlot, x, g);
+        fetch(slot == 0 ? kSlots - 1 : slot - 1);  // the row before this one is done with
         slot = slot == kSlots - 1 ? 0 : slot + 1;
       } else {
-        if (live) now = next;
+        x = next_x;
+        g = next_g;
         fetch(0);
+      }
+      if (!__all_sync(0xffffffffu, live) && !live) {   // no row, or a padded one: it adds nothing, whatever it holds
+        x.clear();
+        g.clear();
       }
       T* const out = row.out;
       const float* const turns = table + (live ? row.t : 0) * 2 * rot;
       row.next();
+      const Floats fx(x);
+      Floats h(g), u(0.f);
       float2 ss = make_float2(0.f, 0.f), ux = ss;
-      Values<V, HALF> fh[K], fu[K];
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!kFew && !p.there[k]) continue;
-        const Values<V, HALF> fx = values_of<T, V, HALF, WIDE>(now.x[k]), fw = values_of<T, V, HALF, WIDE>(w[k]);
-        fh[k] = values_of<T, V, HALF, WIDE>(now.g[k]);
-        if (p.rotary[k]) turn<V, HALF>(fh[k], turns, p.rot_units, p.unit[k]);
-        mul(fu[k].a, fh[k].a, fw.a);
-        dot(ss, fx.a, fx.a);
-        dot(ux, fu[k].a, fx.a);
-        if (HALF && (kFew || p.rotary[k])) {
-          mul(fu[k].b, fh[k].b, fw.b);
-          dot(ss, fx.b, fx.b);
-          dot(ux, fu[k].b, fx.b);
+        if (!kFew && !pl.there[k][0]) continue;
+        if (pl.rotary[k]) turn<V, HALF>(h.f[k], turns, pl.rot_units, pl.unit[k]);
+#pragma unroll
+        for (int p = 0; p < kParts<HALF>; ++p) {
+          mul(u.f[k][p], h.f[k][p], fw.f[k][p]);
+          dot(ss, fx.f[k][p], fx.f[k][p]);
+          dot(ux, u.f[k][p], fx.f[k][p]);
         }
       }
-      const float2 both_sums = group_sum(make_float2(ss.x + ss.y, ux.x + ux.y), a.lanes);
-      const float r = rsqrtf(both_sums.x * inv_dim + a.eps), along = -both_sums.y * inv_dim * r * r;
+      const float2 sums = group_sum(make_float2(ss.x + ss.y, ux.x + ux.y), a.lanes);
+      const float r = rsqrtf(sums.x * inv_dim + a.eps), along = -sums.y * inv_dim * r * r;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!kFew && !p.there[k]) continue;
-        const Values<V, HALF> fx = values_of<T, V, HALF, WIDE>(now.x[k]);
-        Values<V, HALF> xr, dx;
-        mul(xr.a, fx.a, r);
-        fma(dw[k].a, fh[k].a, xr.a, dw[k].a);
-        fma(dx.a, fx.a, along, fu[k].a);
-        mul(dx.a, dx.a, r);
-        if (HALF && (kFew || p.rotary[k])) {
-          mul(xr.b, fx.b, r);
-          fma(dw[k].b, fh[k].b, xr.b, dw[k].b);
-          fma(dx.b, fx.b, along, fu[k].b);
-          mul(dx.b, dx.b, r);
+        if (!kFew && !pl.there[k][0]) continue;
+#pragma unroll
+        for (int p = 0; p < kParts<HALF>; ++p) {
+          float xr[V];
+          mul(xr, fx.f[k][p], r);
+          fma(dw.f[k][p], h.f[k][p], xr, dw.f[k][p]);
+          fma(u.f[k][p], fx.f[k][p], along, u.f[k][p]);
+          mul(u.f[k][p], u.f[k][p], r);
         }
-        if (live && p.there[k]) store<T, V, HALF, WIDE>(out, dx, p.at[k], half, p.rotary[k]);
       }
+      if (live) u.template store<T, WIDE>(pl, out);
     }
   }
-  if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (Ring::kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
   if (a.partials == nullptr) return;
   // the groups of a warp, then the warps, in a fixed order
-  const int warp = tid >> 5;
-  float* sums = table + warp * 512;
+  float* share = table + (tid >> 5) * 512;
   __syncthreads();                                 // the last angles have been read
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float da = dw[k].a[e], db = HALF ? dw[k].b[e] : 0.f;
-      for (int m = a.lanes; m < 32; m <<= 1) {
-        da += __shfl_xor_sync(0xffffffffu, da, m);
-        if (HALF) db += __shfl_xor_sync(0xffffffffu, db, m);
+    for (int p = 0; p < kParts<HALF>; ++p)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float d = dw.f[k][p][e];
+        for (int m = a.lanes; m < 32; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+        if (pl.there[k][p] && (tid & 31) < a.lanes) share[pl.at[k] + p * pl.second[k] + e] = d;
       }
-      if (p.there[k] && (tid & 31) < a.lanes) {
-        sums[p.at[k] + e] = da;
-        if (HALF && p.rotary[k]) sums[p.at[k] + half + e] = db;
-      }
-    }
-  }
   __syncthreads();
   for (int c = tid; c < a.dim; c += kRopeThreads) {
-    float s8 = 0.f;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kRopeThreads / 32; ++i) s8 += table[i * 512 + c];
-    a.partials[(size_t)blockIdx.x * a.dim + c] = s8;
+    for (int i = 0; i < kRopeThreads / 32; ++i) sum += table[i * 512 + c];
+    a.partials[(size_t)blockIdx.x * a.dim + c] = sum;
   }
 }
 
@@ -619,6 +640,21 @@ __global__ void __launch_bounds__(32 * kSumRows) k_norm_rope_sum(const float* pa
   out[c] = s;
 }
 
+// a kernel's dynamic shared memory, allowed once on each device
+int allow_smem(void (*kernel)(NormArgs), int bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, void (*)(NormArgs)>> allowed;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return OSCAR_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (allowed.count({dev, kernel})) return OSCAR_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return OSCAR_ERR_CUDA;
+  try {
+    allowed.insert({dev, kernel});
+  } catch (...) {                                  // no memory to note it in: it is done again
+  }
+  return OSCAR_OK;
+}
 int sm_count(int* sms) {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
@@ -628,7 +664,7 @@ int sm_count(int* sms) {
 
 template <typename T, int V, bool HALF, bool WIDE, int K>
 int launch_as(NormArgs a, bool grad, float* dqw, float* dkw, cudaStream_t st) {
-  const int rot = a.r.rot, half = rot / 2, units = (HALF ? half / V : rot / V) + (a.dim - rot) / V;
+  const int half = a.r.rot / 2, units = units_of<V, HALF>(a.dim, a.r.rot);
   a.lanes = 1;
   while (a.lanes < 32 && a.lanes * K < units) a.lanes *= 2;
   int sms = 0;
@@ -638,17 +674,16 @@ int launch_as(NormArgs a, bool grad, float* dqw, float* dkw, cudaStream_t st) {
     k_norm_rope<T, V, HALF, WIDE, K><<<(a.r.n - 1) / a.tokens + 1, kRopeThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
   }
-  a.tokens = std::max(1, std::min(std::min(kGradTable / half, kGradTokens), a.r.n / (2 * sms)));
-  // CTAs are shared between q and k by their heads
-  const int tiles = (a.r.n - 1) / a.tokens + 1, heads = a.q.heads + a.k.heads;
-  const int most_q = std::max(1, std::min(kGradCtas - 1, (int)((long long)kGradCtas * a.q.heads / heads)));
-  a.q_ctas = a.q.heads == 0 ? 0 : std::min(tiles, a.k.heads == 0 ? kGradCtas : most_q);
-  const int k_ctas = a.k.heads == 0 ? 0 : std::min(tiles, a.q.heads == 0 ? kGradCtas : kGradCtas - most_q);
+  a.tokens = std::min(kGradTable / half, kGradTokens);
+  // CTAs are shared between q and k by their heads; each of a token's angles counts as half of a lane's row (32,769 tokens
+  // x 32 and 8 heads: 173 us; a quarter: 180, not at all: 202)
+  const long long cost_q = 2ll * a.lanes * a.q.heads + half, cost_k = 2ll * a.lanes * a.k.heads + half;
+  const int most_q = std::max(1, std::min(kGradCtas - 1, (int)(kGradCtas * cost_q / (cost_q + cost_k))));
+  a.q_ctas = a.q.heads == 0 ? 0 : std::min(a.r.n, a.k.heads == 0 ? kGradCtas : most_q);
+  const int k_ctas = a.k.heads == 0 ? 0 : std::min(a.r.n, a.q.heads == 0 ? kGradCtas : kGradCtas - most_q);
   const int ctas = a.q_ctas + k_ctas;
-  constexpr int smem = grad_smem<T, V, HALF, WIDE, K>();
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k_norm_rope_grad<T, V, HALF, WIDE, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return OSCAR_ERR_CUDA;
+  constexpr int smem = 16 * kGradTable + Slots<T, V, HALF, WIDE, K>::kSmem;
+  if (int rc = allow_smem(k_norm_rope_grad<T, V, HALF, WIDE, K>, smem); rc != OSCAR_OK) return rc;
   k_norm_rope_grad<T, V, HALF, WIDE, K><<<ctas, kRopeThreads, smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return OSCAR_ERR_CUDA;
   if (a.partials == nullptr) return OSCAR_OK;
@@ -659,17 +694,21 @@ int launch_as(NormArgs a, bool grad, float* dqw, float* dkw, cudaStream_t st) {
 // bytes: the widest access (16, 8 or single elements) that every row, half and remainder starts on a multiple of
 template <typename T, bool HALF>
 int launch_layout(const NormArgs& a, int bytes, bool grad, float* dqw, float* dkw, cudaStream_t st) {
-  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), kLeast = HALF ? 1 : 2;
-  const int rot = a.r.rot;
+  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T), V1 = HALF ? 1 : 2;
+  // 32 bytes a lane where 32 lanes hold a row so; K16, K8: units of a lane then (16 bytes a lane, pairs layout: 32,769 tokens
+  // x 40 heads 152 us instead of 120)
+  constexpr int K16 = 2 / kParts<HALF>, K8 = 4 / kParts<HALF>;
   if (bytes == 16) {
-    const int units = (HALF ? rot / 2 : rot) / V16 + (a.dim - rot) / V16;
-    // 32 bytes a lane: a unit of the half layout with its partners, two of the pairs layout (one: PAIRS_MEASURED)
-    constexpr int kFew = HALF ? 1 : 2;
-    if (units <= 32 * kFew) return launch_as<T, V16, HALF, true, kFew>(a, grad, dqw, dkw, st);
-    return launch_as<T, V16, HALF, true, 128 / (32 * V16 / 4)>(a, grad, dqw, dkw, st);
+    if constexpr (sizeof(T) == 4)
+      if (units_of<V16, HALF>(a.dim, a.r.rot) > 32 * K16) return launch_as<T, V16, HALF, true, 2 * K16>(a, grad, dqw, dkw, st);
+    return launch_as<T, V16, HALF, true, K16>(a, grad, dqw, dkw, st);
   }
-  if (bytes == 8) return launch_as<T, V8, HALF, true, 16 / V8>(a, grad, dqw, dkw, st);
-  return launch_as<T, kLeast, HALF, false, 16 / kLeast>(a, grad, dqw, dkw, st);
+  if (bytes == 8) {
+    if constexpr (sizeof(T) == 4)
+      if (units_of<V8, HALF>(a.dim, a.r.rot) > 32 * K8) return launch_as<T, V8, HALF, true, 2 * K8>(a, grad, dqw, dkw, st);
+    return launch_as<T, V8, HALF, true, K8>(a, grad, dqw, dkw, st);
+  }
+  return launch_as<T, V1, HALF, false, 8>(a, grad, dqw, dkw, st);
 }
 template <typename T>
 int launch_typed(const NormArgs& a, bool half_layout, int bytes, bool grad, float* dqw, float* dkw, cudaStream_t st) {
