@@ -504,7 +504,7 @@ class OscarCache:
         """append_kv of one token per request from its raw projections: norm_rope() of q [B, Hq, 128] (or None) and k
         [B, Hkv, 128] on the way (eps None: the rotation alone), at positions [B] ([num_axes, B] where the plan has axes),
         seq_lens_before by default. Rows of q, k and v may be views of one projection. Returns q_out, the queries for
-        decode_attention. As for append_kv, lengths and tables may not come from a kernel launched just before."""
+        decode_attention."""
         if stream is not None:
             with _on(stream):
                 return self.append_kv_rope(layer, plan, q, k, v, seq_lens_before, hist_pt, bf16_pt, q_weight, k_weight, eps,

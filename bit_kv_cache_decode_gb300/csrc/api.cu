@@ -150,7 +150,7 @@ int check_raw(const oscar_cache* c, int B, const oscar_raw_step* x, bool prepare
     return OSCAR_ERR_INVALID_ARG;
   if (x->q && x->q == x->q_out && x->q_row != (int64_t)c->lay.num_q_heads * kD) return OSCAR_ERR_INVALID_ARG;
   *raw = {x->q_row, x->k_row, x->v_row, static_cast<__nv_bfloat16*>(x->q_out), nullptr, nullptr, rotary_of(r, x->positions, B),
-          x->norm ? x->norm->eps : 0.f, x->norm != nullptr, r.layout == OSCAR_ROPE_PAIRS, prepare};
+          x->norm ? x->norm->eps : 0.f, x->norm && aligned16(x->norm->q_weight) && aligned16(x->norm->k_weight), x->norm != nullptr, r.layout == OSCAR_ROPE_PAIRS, prepare};
   if (x->norm) {
     raw->qw = static_cast<const __nv_bfloat16*>(x->norm->q_weight);
     raw->kw = static_cast<const __nv_bfloat16*>(x->norm->k_weight);

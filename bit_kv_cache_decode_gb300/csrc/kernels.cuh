@@ -65,6 +65,7 @@ struct RawStep {
   const __nv_bfloat16 *qw, *kw;                    // [kD], or null: ones
   Rotary r;                                        // positions null: the request's length
   float eps;
+  int wide_weights;                                // both weights on 16 bytes
   int normed, pairs, prepare;                      // prepare: the queries' fragments too (a decode follows)
 };
 

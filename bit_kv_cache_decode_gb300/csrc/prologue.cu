@@ -26,11 +26,12 @@
 // scheduled. Sequence lengths, page tables and the pool's rows (inputs the
 // kernel before does not produce) are read before that wait.
 //
-// From raw rows (RAW: oscar_append_kv_rope, oscar_decode_step_rope): after the wait eight lanes a row normalise and
+// From raw rows (RAW: oscar_append_kv_rope, oscar_decode_step_rope) the grid waits first: the raw rows, the length and the
+// new token's page are then read side by side, one latency instead of three. Eight lanes a row normalise and
 // rotate the gq query rows of the head and its new key row (norm_rope.cu's formulas: float32, one rounding to BF16), 16
 // channels a lane; the sum of squares is three shuffles, a pair's partner comes through shared memory. The results are
 // what the rest of the kernel takes for q and k, and the queries are written out for the kernels behind. The angles
-// (64 of them, all heads share the request's position) are made before the wait where the position is the request's length.
+// (64 of them) are the same for all heads of a request.
 #include "kernels.cuh"
 #include "rope.cuh"
 #include "rotate.cuh"
@@ -46,47 +47,77 @@ __device__ __forceinline__ bool valid_page(int p, int n) { return p >= 0 && p < 
 // smem: rotation fragments | 16-row tile | tau | 8 mbarriers
 constexpr int kTileFloats = 16 * kTileStride;
 
-// Eight lanes' rows (a group of lanes per row, l the lane in it): norm and rotation of the 128 channels x[16] (channels
-// 8 l .. and 64 + 8 l ..), through the float row buf of this group; y gets the same channels' results.
-__device__ __forceinline__ void norm_rope_row(const float (&x)[16], const float (&w)[16], const RawStep& raw, const float2* cs,
-                                              float* buf, int l, float (&y)[16]) {
-  float r = 1.f;
+// What a launch does: rows as they come; raw rows; raw rows, with the rotation's fragments read from L2 (and L1, which CTAs
+// of one head share) when they are needed. The last takes 64 KB less of shared memory, so that more CTAs fit an SM.
+enum { kPlain, kRaw, kRawLate };
+
+// Norm and rotation of a row by eight lanes: lane l has channels 8 l .. and 64 + 8 l .. in x, their weights in w. buf: a float
+// row of the group's own.
+__device__ __forceinline__ void norm_rope_row(float (&x)[16], const float (&w)[16], const RawStep& raw, const float2* cs,
+                                              float* buf, int l) {
   if (raw.normed) {
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
     for (int m = 1; m < 8; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    r = rsqrtf(ss * (1.f / kD) + raw.eps);
-  }
+    const float r = rsqrtf(ss * (1.f / kD) + raw.eps);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    y[e] = raw.normed ? x[e] * (r * w[e]) : x[e];
-    buf[(e < 8 ? 8 * l : 56 + 8 * l) + e] = y[e];
+    for (int e = 0; e < 16; ++e) x[e] *= r * w[e];
   }
-  __syncwarp();
   const int rot = raw.r.rot, half = rot / 2;
+  if (raw.pairs) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int c = (e < 8 ? 8 * l : 56 + 8 * l) + e;
-    if (c >= rot) continue;
-    const bool second = raw.pairs ? (c & 1) != 0 : c >= half;
-    const int j = raw.pairs ? c >> 1 : second ? c - half : c, partner = raw.pairs ? c ^ 1 : second ? c - half : c + half;
-    const float2 t = cs[j];
-    y[e] = second ? y[e] * t.x + buf[partner] * t.y : y[e] * t.x - buf[partner] * t.y;
+    for (int e = 0; e < 16; e += 2) {
+      const int c = (e < 8 ? 8 * l : 56 + 8 * l) + e;
+      if (c >= rot) continue;
+      const float2 t = cs[c >> 1];
+      const float u = x[e], v = x[e + 1];
+      x[e] = u * t.x - v * t.y;
+      x[e + 1] = v * t.x + u * t.y;
+    }
+  } else if (rot == kD) {                            // a pair is in one lane
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 t = cs[8 * l + e];
+      const float u = x[e], v = x[e + 8];
+      x[e] = u * t.x - v * t.y;
+      x[e + 8] = v * t.x + u * t.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) buf[(e < 8 ? 8 * l : 56 + 8 * l) + e] = x[e];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int c = (e < 8 ? 8 * l : 56 + 8 * l) + e;
+      if (c >= rot) continue;
+      const bool second = c >= half;
+      const float2 t = cs[second ? c - half : c];
+      x[e] = second ? x[e] * t.x + buf[c - half] * t.y : x[e] * t.x - buf[c + half] * t.y;
+    }
+  }
+}
+__device__ __forceinline__ void widen8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = __uint_as_float(w[e] << 16);
+    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
   }
 }
 
-template <bool RAW>
-__global__ void __launch_bounds__(kPrologueWarps * 32, 1)
+template <int MODE>
+__global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
     k_step_prologue(LayerView lv, DecodeWorkspace ws, const __nv_bfloat16* __restrict__ q,
                     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                     const int* __restrict__ seq_lens_before, const int* __restrict__ hist_pt, int max_hist_pages,
                     const int* __restrict__ bf16_pt, float scale_log2, RawStep raw) {
   TimelineSpan timeline_span(lv, k != nullptr ? kTlAppend : kTlQprep);
+  constexpr bool RAW = MODE != kPlain, kLate = MODE == kRawLate;
   extern __shared__ __align__(128) float smem[];
   uint32_t* frag_s = reinterpret_cast<uint32_t*>(smem);
-  float* rows = smem + kRFragWords;                  // [16][kTileStride]
+  float* rows = smem + (kLate ? 0 : kRFragWords);    // [16][kTileStride]
   float* tau_s = rows + kTileFloats;                 // [128]
   const uint32_t bars = smem_addr(tau_s + kD);
   __shared__ int sig[8];
@@ -98,7 +129,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   const bool rotate = (kind == OSCAR_KIND_K) || lv.v_explicit;
   // The rotation fragments do not depend on the kernel before: they are requested before the wait below,
   // while that kernel still runs (this grid is scheduled early). Every CTA that may rotate requests them.
-  const bool fetch_frags = rotate && (do_q || k != nullptr);
+  const bool fetch_frags = rotate && (do_q || k != nullptr) && !kLate;
   if (fetch_frags && tid == 0) {
     const float* f = prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff);
     const uint64_t keep = l2_evict_last();
@@ -115,8 +146,48 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   int L_old = 0;
   bool demote = false;
   int slot = 0, spage = -1, hh = 0, hpage = -1;
+  if (k != nullptr) L_old = __ldcg(seq_lens_before + b);   // L2 reads: nothing older may sit in this SM's L1
+  // Raw rows are waited for first, so that their loads and those that follow from the length are in flight together.
+  // Rows 0 .. gq - 1: queries, row gq: the new key; four rows a warp.
+  const bool raw_k = RAW && kind == OSCAR_KIND_K;
+  const int rrow = tid >> 3, rl = tid & 7;
+  const bool rq = rrow < gq, rlive = raw_k && (rrow == gq || (rq && q != nullptr));
+  uint4 rx[2] = {}, rw[2] = {};
+  int rpos[kRopeAxes] = {}, new_page = -1;
+  if constexpr (RAW) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (rlive) {
+      const __nv_bfloat16* src = rq ? q + b * raw.q_row + (h * gq + rrow) * kD : k + b * raw.k_row + h * kD;
+      const __nv_bfloat16* wt = rq ? raw.qw : raw.kw;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        rx[part] = *reinterpret_cast<const uint4*>(src + 64 * part + 8 * rl);
+        if (wt == nullptr) {
+          rw[part] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // BF16 ones
+        } else if (raw.wide_weights) {
+          rw[part] = *reinterpret_cast<const uint4*>(wt + 64 * part + 8 * rl);
+        } else {
+          __nv_bfloat162 p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = __halves2bfloat162(wt[64 * part + 8 * rl + 2 * e], wt[64 * part + 8 * rl + 2 * e + 1]);
+          rw[part] = *reinterpret_cast<const uint4*>(p);
+        }
+      }
+    }
+    if (RAW && !raw_k && w == kPrologueWarps - 2) {
+      const uint2 x = reinterpret_cast<const uint2*>(v + b * raw.v_row + h * kD)[lane];
+      rx[0].x = x.x;
+      rx[0].y = x.y;
+    }
+    if (raw_k && raw.r.positions != nullptr && tid < raw.r.rot / 2)
+      for (int a = 0; a < raw.r.n_axes; ++a) rpos[a] = raw.r.positions[(size_t)a * raw.r.n + b];
+    if (L_old >= 0) {                                // the new token's page
+      const int pos = L_old, s2 = pos < lv.sink ? pos : lv.sink + (pos - lv.sink) % lv.recent;
+      new_page = __ldcg(bf16_pt + b * bf16_per_req + s2 / kP);
+    }
+  }
   if (k != nullptr) {
-    L_old = __ldcg(seq_lens_before + b);          // L2 reads: nothing older may sit in this SM's L1
     if (L_old < 0 && tid == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
     demote = L_old >= lv.sink + lv.recent;
     if (demote) {
@@ -135,7 +206,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   // The next layer's prologue needs its rotation fragments from L2 about one layer's decode from now:
   // ask for them now, with the same evict-last priority, so the page stream of this layer does not
   // leave them to be fetched from HBM on the next critical path.
-  if (lv.next_params != nullptr && b == 0 && tid == 0 && rotate) {
+  if (lv.next_params != nullptr && b == 0 && tid == 0 && rotate && !kLate) {
     const float* nf = lv.next_params + (size_t)h * kParamFloats + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff);
     l2_prefetch(nf, kRFragWords * 4, l2_evict_last());
   }
@@ -150,80 +221,55 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   __shared__ float2 cs[RAW ? kD / 2 : 1];                  // the request's angles
   __shared__ float raw_rows[RAW ? 12 * kTileStride : 1];    // raw rows (of three warps, four each) between norm and rotation
   __shared__ uint4 new_key[RAW ? kD / 8 : 1];              // the new key row, BF16
-  const bool raw_k = RAW && kind == OSCAR_KIND_K;
-  auto angles = [&](bool given) {
-    for (int j = tid; j < raw.r.rot / 2; j += kPrologueWarps * 32) {
-      int pos[kRopeAxes];
-      for (int a = 0; a < raw.r.n_axes; ++a) {
-        const int p = given ? raw.r.positions[(size_t)a * raw.r.n + b] : L_old;
-        if (p < 0 && j == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
-        pos[a] = max(p, 0);
-      }
-      cs[j] = rope_turn(raw.r, pos, j, 1.f);
-    }
-  };
-  if (raw_k && raw.r.positions == nullptr) angles(false);
   // Wait for the grid before (in a model, the kernel that made q, k and v), then let the decode be
   // scheduled; it waits for this grid before it reads anything this kernel writes.
-  pdl_wait();
-  pdl_launch_dependents();
+  if constexpr (!RAW) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   if constexpr (RAW) {
     if (raw_k) {
-      // rows 0 .. gq - 1: queries, row gq: the new key; a warp's rows are four, and all its lanes take part
-      const int row = tid >> 3, l = tid & 7, rows_here = gq + 1, first = tid >> 5 << 2;
-      const bool isq = row < gq, live = row == gq || (isq && q != nullptr);
-      float x[16] = {}, w[16], y[16];
-      if (first < rows_here && live) {
-        const __nv_bfloat16* src = isq ? q + b * raw.q_row + (h * gq + row) * kD : k + b * raw.k_row + h * kD;
-        const __nv_bfloat16* wt = isq ? raw.qw : raw.kw;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint4 u4 = *reinterpret_cast<const uint4*>(src + 64 * part + 8 * l);
-          const uint32_t wds[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[8 * part + 2 * e] = __uint_as_float(wds[e] << 16);
-            x[8 * part + 2 * e + 1] = __uint_as_float(wds[e] & 0xffff0000u);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[8 * part + e] = wt != nullptr ? __bfloat162float(wt[64 * part + 8 * l + e]) : 1.f;
+      if (tid < raw.r.rot / 2) {
+        bool low = false;
+        for (int a = 0; a < raw.r.n_axes; ++a) {
+          if (raw.r.positions == nullptr) rpos[a] = L_old;
+          low |= rpos[a] < 0;
+          rpos[a] = max(rpos[a], 0);
         }
+        if (low && tid == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
+        cs[tid] = rope_turn(raw.r, rpos, tid, 1.f);
       }
-      if (raw.r.positions != nullptr) angles(true);
       __syncthreads();
-      if (first < rows_here) {
-        norm_rope_row(x, w, raw, cs, raw_rows + row * kTileStride, l, y);
-        uint4 z[2];
+      if (4 * w < gq + 1) {                          // all lanes of a warp take part
+        float x[16], wt[16];
+        widen8(rx[0], x);
+        widen8(rx[1], x + 8);
+        widen8(rw[0], wt);
+        widen8(rw[1], wt + 8);
+        norm_rope_row(x, wt, raw, cs, raw_rows + rrow * kTileStride, rl);
         bool bad = false;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           __nv_bfloat162 p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            bad |= nonfinite(y[8 * part + 2 * e]) || nonfinite(y[8 * part + 2 * e + 1]);
-            p[e] = __floats2bfloat162_rn(y[8 * part + 2 * e], y[8 * part + 2 * e + 1]);
+            bad |= nonfinite(x[8 * part + 2 * e]) || nonfinite(x[8 * part + 2 * e + 1]);
+            p[e] = __floats2bfloat162_rn(x[8 * part + 2 * e], x[8 * part + 2 * e + 1]);
           }
-          z[part] = *reinterpret_cast<const uint4*>(p);
-        }
-        if (live && bad) flag(lv.status, OSCAR_STATUS_NONFINITE);
-        if (live && isq) {
-          uint4* dst = reinterpret_cast<uint4*>(raw.q_out + ((size_t)b * lv.hq + h * gq + row) * kD);
-          dst[l] = z[0];
-          dst[8 + l] = z[1];
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint32_t wds[4] = {z[part].x, z[part].y, z[part].z, z[part].w};
-            float* t = rows + (row + 1) * kTileStride + 64 * part + 8 * l;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[2 * e] = __uint_as_float(wds[e] << 16);
-              t[2 * e + 1] = __uint_as_float(wds[e] & 0xffff0000u);
+          const uint4 z = *reinterpret_cast<const uint4*>(p);
+          if (rlive && rq) {
+            reinterpret_cast<uint4*>(raw.q_out + ((size_t)b * lv.hq + h * gq + rrow) * kD)[8 * part + rl] = z;
+            if (do_q) {
+              widen8(z, x + 8 * part);
+              float4* t = reinterpret_cast<float4*>(rows + (rrow + 1) * kTileStride + 64 * part + 8 * rl);
+              t[0] = make_float4(x[8 * part], x[8 * part + 1], x[8 * part + 2], x[8 * part + 3]);
+              t[1] = make_float4(x[8 * part + 4], x[8 * part + 5], x[8 * part + 6], x[8 * part + 7]);
             }
+          } else if (rlive) {
+            new_key[8 * part + rl] = z;
           }
-        } else if (live) {
-          new_key[l] = z[0];
-          new_key[8 + l] = z[1];
         }
+        if (rlive && bad) flag(lv.status, OSCAR_STATUS_NONFINITE);
       }
     }
   } else if (r >= 1 && r <= gq && do_q) {
@@ -231,7 +277,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
     if (bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w))
       flag(lv.status, OSCAR_STATUS_NONFINITE);
   }
-  if (!raw_k || q == nullptr || r == 0 || r > gq) {  // rows 1 .. gq of raw queries are there
+  if (!RAW || !do_q || r == 0 || r > gq) {       // rows 1 .. gq of raw queries are there
     const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
     float4* dst = reinterpret_cast<float4*>(rows + r * kTileStride + 8 * c8);
     dst[0] = make_float4(__uint_as_float(wds[0] << 16), __uint_as_float(wds[0] & 0xffff0000u),
@@ -241,7 +287,9 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   }
   if (tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
   __syncthreads();                                   // barriers initialised, tile staged, old slot read
-  if (need_frags && !rotate_tile16(frag_s, rows, bars)) {
+  if (kLate) {
+    if (need_frags) rotate_tile16_l2(reinterpret_cast<const uint32_t*>(prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff)), rows);
+  } else if (need_frags && !rotate_tile16(frag_s, rows, bars)) {
     if (tid == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
     mbar_wait(bars + 8 * w, 0);                      // one more bounded wait for the copies in flight
     return;                                          // the pool is left untouched
@@ -267,16 +315,8 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   }
   // --- the new token into its slot (the old row was staged before the first barrier) ---
   if (k == nullptr || L_old < 0 || w != kPrologueWarps - 2) return;
-  const int pos = L_old;
-  int page, row;
-  if (pos < lv.sink) {
-    page = bf16_pt[b * bf16_per_req + pos / kP];
-    row = pos % kP;
-  } else {
-    const int s2 = (pos - lv.sink) % lv.recent;
-    page = bf16_pt[b * bf16_per_req + lv.sink / kP + s2 / kP];
-    row = s2 % kP;
-  }
+  const int pos = L_old, at = pos < lv.sink ? pos : lv.sink + (pos - lv.sink) % lv.recent, row = at % kP;
+  const int page = RAW ? new_page : bf16_pt[b * bf16_per_req + at / kP];
   if (!valid_page(page, lv.n_bf16)) {
     if (lane == 0) flag(lv.status, OSCAR_STATUS_BAD_PAGE);
     return;
@@ -284,16 +324,17 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, 1)
   uint2 x;
   if (raw_k) {
     x = reinterpret_cast<const uint2*>(new_key)[lane];
+  } else if (RAW) {
+    x = make_uint2(rx[0].x, rx[0].y);
   } else {
-    const __nv_bfloat16* src = RAW ? v + b * raw.v_row + h * kD : (kind == OSCAR_KIND_K ? k : v) + ((size_t)b * lv.hkv + h) * kD;
-    x = reinterpret_cast<const uint2*>(src)[lane];
+    x = reinterpret_cast<const uint2*>((kind == OSCAR_KIND_K ? k : v) + ((size_t)b * lv.hkv + h) * kD)[lane];
   }
   if (__any_sync(0xffffffffu, bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y)) && lane == 0)
     flag(lv.status, OSCAR_STATUS_NONFINITE);
   reinterpret_cast<uint2*>(bf16_row(lv, page, h, kind, row))[lane] = x;
 }
 
-constexpr int kPrologueSmem = (kRFragWords + kTileFloats + kD) * 4 + 64;
+constexpr int kLateSmem = (kTileFloats + kD) * 4 + 64, kPrologueSmem = kRFragWords * 4 + kLateSmem;
 
 }  // namespace
 
@@ -307,11 +348,15 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(B, lv.hkv, k != nullptr ? 2 : 1);   // query-only: the K CTAs
   cfg.blockDim = dim3(kPrologueWarps * 32);
-  cfg.dynamicSmemBytes = kPrologueSmem;
+  // An append of raw rows rotates demoted rows only (256 requests x 8 heads, none demoted: 16 us; with every CTA asking for
+  // the fragments 40). A step's queries take them from L2 where there are more than four CTAs for each of 152 SMs: decode
+  // steps of 256 requests x 8 heads 140 us (bulk copies: 158), of 64 38.1 (41.5), of 32 24.1 (23.8), of 8 13.5 (13.0).
+  const bool late = raw != nullptr && (!raw->prepare || 2ll * B * lv.hkv > 4 * 152);
+  cfg.dynamicSmemBytes = late ? kLateSmem : kPrologueSmem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = after_all ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, raw ? k_step_prologue<true> : k_step_prologue<false>, lv, ws,
+  return cudaLaunchKernelEx(&cfg, late ? k_step_prologue<kRawLate> : raw ? k_step_prologue<kRaw> : k_step_prologue<kPlain>, lv, ws,
                             static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
                             static_cast<const __nv_bfloat16*>(v), seq_lens_before, hist_pt, max_hist_pages, bf16_pt,
                             sm_scale * kLog2e, raw ? *raw : RawStep{}) == cudaSuccess
@@ -320,7 +365,7 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
 }
 
 int configure_prologue_kernel() {
-  for (auto fn : {k_step_prologue<false>, k_step_prologue<true>}) {
+  for (auto fn : {k_step_prologue<kPlain>, k_step_prologue<kRaw>, k_step_prologue<kRawLate>}) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrologueSmem) != cudaSuccess)
       return OSCAR_ERR_CUDA;
     if (int rc = set_max_shared_carveout(reinterpret_cast<const void*>(fn)); rc != OSCAR_OK) return rc;

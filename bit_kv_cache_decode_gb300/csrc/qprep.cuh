@@ -118,6 +118,39 @@ __device__ __forceinline__ bool rotate_tile16(const uint32_t* frag_s, float* row
   return true;
 }
 
+// The same with the fragments read from global memory (8 warps): all of them in flight, then the products.
+__device__ __forceinline__ void rotate_tile16_l2(const uint32_t* frag, float* rows) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint4 f[8][2];
+#pragma unroll
+  for (int kb = 0; kb < 8; ++kb)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f[kb][j] = __ldg(reinterpret_cast<const uint4*>(frag + ((kb * 16 + 2 * w + j) * 32 + lane) * 4));
+  float acc[2][4] = {};
+#pragma unroll
+  for (int kb = 0; kb < 8; ++kb) {
+    const float* r0 = rows + g * kTileStride + 16 * kb + 2 * t;
+    const float* r8 = rows + (g + 8) * kTileStride + 16 * kb + 2 * t;
+    const uint32_t a0 = f16x2_of(r0), a1 = f16x2_of(r8), a2 = f16x2_of(r0 + 8), a3 = f16x2_of(r8 + 8);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float d[4];
+      qp_mma(d, a0, a1, a2, a3, f[kb][j].x, f[kb][j].y, true);    // x R_hi
+      qp_mma(d, a0, a1, a2, a3, f[kb][j].z, f[kb][j].w, false);   // + x R_lo
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+    }
+  }
+  __syncthreads();                                   // every warp has read its A rows
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int col = 8 * (2 * w + j) + 2 * t;
+    *reinterpret_cast<float2*>(rows + g * kTileStride + col) = make_float2(acc[j][0], acc[j][1]);
+    *reinterpret_cast<float2*>(rows + (g + 8) * kTileStride + col) = make_float2(acc[j][2], acc[j][3]);
+  }
+  __syncthreads();
+}
+
 // Per query head qi of group (b, h) (warp w takes heads w, w + nwarps, ...):
 // q~ (xs[qi * stride + 0..127], rotated channel order) goes to the workspace with its
 // group sums, and sig[qi] = sigma, the power of two that brings max|q~| near 2^12.

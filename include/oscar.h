@@ -521,11 +521,10 @@ typedef struct oscar_raw_step {
 } oscar_raw_step;
 
 /* oscar_append_kv of the normed and rotated k and of v; q_out gets the queries for an oscar_decode_attention behind it.
- * q may be NULL (then q_out is not used). As in oscar_append_kv, seq_lens_before, the page tables and the pool's rows are
- * read before the wait for the kernel launched just before; q, k, v, positions and the weights may come from it.
- * A key, or a query, that is not finite raises NONFINITE. Errors: as oscar_append_kv and oscar_norm_rope, INVALID_ARG (a
- * missing structure, rows not 16-byte aligned or not a multiple of 8 elements apart, q_out = q with another row, a
- * rotary_dim above 128). */
+ * q may be NULL (then q_out is not used). All inputs but the cache's rotations may come from the kernel just before, unlike
+ * those of oscar_append_kv. A key, value or query that is not finite raises NONFINITE. Errors: as oscar_append_kv and
+ * oscar_norm_rope, INVALID_ARG (a missing structure, rows not 16-byte aligned or not a multiple of 8 elements apart,
+ * q_out = q with another row, a rotary_dim above 128). */
 int oscar_append_kv_rope(oscar_cache* cache, int layer, int B, const oscar_raw_step* raw, const int32_t* seq_lens_before,
                          const int32_t* hist_pt, int max_hist_pages, const int32_t* bf16_pt, void* stream);
 

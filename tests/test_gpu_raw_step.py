@@ -49,6 +49,7 @@ CASES = [  # lens, hkv, gq, v_mode, meta, algo, rot, layout, axes
     ([383, 384], 1, 8, 0, "u8", 1, 24, 0, 3),
     ([640, 10, 2000], 4, 1, 1, "cb", 1, 20, 0, 1),
     ([900, 333], 2, 2, 0, "f16", 0, 2, 1, 1),
+    ([20 * i for i in range(42)], 8, 1, 1, "f16", 1, 64, 0, 1),      # many CTAs: the fragments come from L2
     ([900, 333], 2, 2, 0, "f16", 2, 128, 1, 3),
 ]
 
@@ -96,6 +97,17 @@ def test_against_ready_made_rows(lens, hkv, gq, v_mode, meta, algo, rot, layout,
     assert torch.equal(mine, q_out) and torch.equal(out, want) and torch.equal(lse, lse_b) and torch.equal(a.pool, b.pool)
 
 
+def test_weights_off_16_bytes():
+    a, b, hist, bf = pair([500], 2, 4, 0, 85, algo=1)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q, k, v = raw(g, 1, 8, 2)
+    w = (1 + 0.3 * torch.randn(2, 129, generator=g, device=DEV)).bfloat16()
+    plan, sl = osc.RopePlan(128), np.array([500], np.int32)
+    x = a.decode_step_rope(0, plan, q, k, v, sl, hist, bf, SM, w[0, 1:], w[1, 1:])
+    y = b.decode_step_rope(0, plan, q, k, v, sl, hist, bf, SM, w[0, 1:].clone(), w[1, 1:].clone())
+    assert torch.equal(x, y) and torch.equal(a.pool, b.pool)
+
+
 def test_shared_prefix():
     lens, hkv, gq = [1100, 1200], 2, 4
     a, b, hist, bf = pair(lens, hkv, gq, 0, 81, shared_prefix=576, algo=1)
@@ -134,10 +146,9 @@ def test_in_place_streams_and_graphs():
     graph = torch.cuda.CUDAGraph()
     pos = sl.clone()
     with torch.cuda.graph(graph):
-        # positions and projections from the kernels straight before
-        q2, k2 = q * 1, k * 1
-        osc.rope(plan, v, None, sl, q_out=torch.empty_like(v))
-        a.decode_step_rope(0, plan, q2, k2, v, sl, hist, bf, SM, positions=pos + 0, q_out=q_out, out=out)
+        # projections, positions, tables and last the lengths from the kernels straight before
+        q2, k2, pos2, hist2, bf2 = q * 1, k * 1, pos + 0, hist + 0, bf + 0
+        a.decode_step_rope(0, plan, q2, k2, v, sl + 0, hist2, bf2, SM, positions=pos2, q_out=q_out, out=out)
     for _ in range(3):
         a.pool.copy_(before)
         out.zero_()
