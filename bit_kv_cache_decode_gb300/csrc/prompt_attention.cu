@@ -13,8 +13,12 @@
 //  * O += P V, M128 N128 K16 x 4 for 64 tokens, A = P in TMEM, B = V as it lies in shared memory (channels contiguous).
 // The tensor pipe takes 1,024 cycles for a block of one tile (512 for S, 512 for O); while it works for one tile, the row
 // threads of the other have its logits. Products run in issue order, so an S may be issued over weights whose O is issued.
-// Warps: 0-3 and 4-7 rows of the two tiles, 8 loads, 9 issues the products.
+// Warps: 0-3 and 4-7 rows of the two tiles, 8 finds the work and loads, 9 issues the products.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
+//
+// Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
+// takes over CTAs that have not started yet (clusterlaunchcontrol), so that the loads and the first S of an item overlap
+// the end of the one before it; nothing is counted in memory that calls could share.
 //
 // Masked places hold whatever the packed buffer holds: logits are replaced by -inf before anything looks at them. Values
 // that some row of the CTA does not see would reach it as 0 times a NaN; before the products of those last blocks the row
@@ -32,16 +36,23 @@ using qtile::tma_load_3d;
 constexpr int kTile = 128;                         // rows of a tile
 constexpr int kBlock = 128, kSub = 64;             // tokens of a block, and of what the row threads take at a time
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kWarps = 12;
-constexpr int kStages = 5;                         // ring of blocks: keys and values in turn
+constexpr int kStages = 4;                         // ring of blocks: keys and values in turn
 constexpr int kHalfBytes = 128 * 128;              // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;         // 32 KB: Q of a tile, K or V of a block
-constexpr int kMasks = 8;                          // 64-token groups at the end that not all rows see: 5 at most
-constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffMask = kOffRing + kStages * kTileBytes, kOffItem = kOffMask + 8 * kMasks;
-constexpr int kOffBar = kOffItem + 32;
-constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQ = kBEmpty + kStages, kBS = kBQ + 1, kBP = kBS + 2, kBC = kBP + 4, kBO = kBC + 2,
-              kBFinal = kBO + 4, kNumBars = kBFinal + 1;
+constexpr int kOutBytes = 32 * 128;                // a warp's rows on their way out, 128 bytes of each
+constexpr int kItems = 3;                          // items found ahead
+constexpr int kMasks = 8;                          // 64-token groups at an item's end that not all rows see: 5 at most
+constexpr int kItemBytes = 16 + 8 * kMasks;        // start, len, h, q0; a bit set of each such group
+constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffOut = kOffRing + kStages * kTileBytes, kOffItem = kOffOut + 8 * kOutBytes;
+constexpr int kOffNext = kOffItem + kItems * kItemBytes;   // the CTA that was taken over, 16 bytes
+constexpr int kOffBar = kOffNext + 16;
+// two barriers for a tile's weights and products: both halves of a block may be there before the first is used
+constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQ = kBEmpty + kStages, kBQFree = kBQ + 1, kBS = kBQFree + 1, kBP = kBS + 2,
+              kBC = kBP + 4, kBOFree = kBC + 2, kBO = kBOFree + 2, kBItem = kBO + 4, kBItemFree = kBItem + kItems,
+              kBNext = kBItemFree + kItems, kBFinal = kBNext + 1, kNumBars = kBFinal + 1;
 constexpr int kOffTmem = kOffBar + 8 * kNumBars, kOffFailed = kOffTmem + 4;
 constexpr int kSmem = kOffFailed + 4 + 1024;       // with alignment slack
+static_assert(kOffItem % 16 == 0 && kItemBytes % 16 == 0 && kOffBar % 16 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;   // tile t: + 128 t
 constexpr uint32_t kBf16Bits = (1u << 7) | (1u << 10);        // A and B bf16
@@ -92,11 +103,11 @@ __device__ __forceinline__ Item find_item(const PromptArgs& a, long long i) {
       it.h = at / n;
       it.q0 = (n - 1 - (at - it.h * n)) * tokens;
       found = true;
-      if (blockIdx.x != 0) break;                  // the first CTA looks at all bounds
+      if (i != 0) break;                           // the first item's finder looks at all bounds
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, OSCAR_STATUS_BAD_SEQLEN);
+  if (i == 0 && __any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, OSCAR_STATUS_BAD_SEQLEN);
   return it;
 }
 
@@ -179,8 +190,84 @@ __device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
   }
 }
 
+// An item as the roles read it; false: there is none any more. The shuffles tell the compiler that a warp's lanes have the same
+// numbers: operands of products that follow from them stay in uniform registers (without: 32,769 tokens 8.1 ms instead of ITEM_MS).
+__device__ __forceinline__ bool read_item(const Ctx c, int slot, Item& it) {
+  const uint4 x = lds128(c.base + kOffItem + slot * kItemBytes);
+  it.start = __shfl_sync(0xffffffffu, (int)x.x, 0);
+  it.len = __shfl_sync(0xffffffffu, (int)x.y, 0);
+  it.h = __shfl_sync(0xffffffffu, (int)x.z, 0);
+  it.q0 = __shfl_sync(0xffffffffu, (int)x.w, 0);
+  return it.len >= 0;
+}
+
 // ---- row threads of tile t ------------------------------------------------------------------------------
-__device__ __forceinline__ bool rows_role(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens) {
+// What has gone before in this CTA, by which the barriers' phases go.
+struct RowCount {
+  int s = 0, half0 = 0, half1 = 0, cleaned = 0, ring = 0;
+  __device__ __forceinline__ int half(int h) const { return h ? half1 : half0; }
+};
+
+// the rows' results: 128 bytes of each row at a time through shared memory, so that eight lanes write a row's 128 bytes
+__device__ __forceinline__ void write_rows(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens, uint32_t to, float inv,
+                                           float& bad) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = 32 * (warp & 3);
+  const uint32_t buf = c.base + kOffOut + warp * kOutBytes;
+  const int gq = 1 << a.gq_log2, chunks = a.out_fp32 ? 4 : 2;
+#pragma unroll 1
+  for (int q = 0; q < chunks; ++q) {
+    if (a.out_fp32) {
+      float o[32];
+      tmem_ld32(to + 32 * q, o);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        o[x] *= inv;
+        bad = fmaf(o[x], 0.f, bad);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
+                                                                      __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
+    } else {
+      float o[32], p[32];
+      tmem_ld32x2(to + 64 * q, to + 64 * q + 32, o, p);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        o[x] *= inv;
+        p[x] *= inv;
+        bad = fmaf(o[x], 0.f, fmaf(p[x], 0.f, bad));
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4),
+               make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                          pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7])));
+        sts128(buf + lane * 128 + (((x + 4) ^ (lane & 7)) << 4),
+               make_uint4(pack_bf16x2(p[8 * x], p[8 * x + 1]), pack_bf16x2(p[8 * x + 2], p[8 * x + 3]),
+                          pack_bf16x2(p[8 * x + 4], p[8 * x + 5]), pack_bf16x2(p[8 * x + 6], p[8 * x + 7])));
+      }
+    }
+    if (q == chunks - 1) {                         // O is read: the next item's may be written
+      tc_fence_before();
+      c.arrive(kBOFree + t);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), row = first + r, token = it.q0 + t * tokens + (row >> a.gq_log2);
+      const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      if (token < it.len) {
+        const long long at = (long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & (gq - 1));
+        char* dst = static_cast<char*>(a.out) + at * (a.out_fp32 ? 4 * kD : 2 * kD) + 128 * q + 16 * (lane & 7);
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+__device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int t, int tokens,
+                                          RowCount& k) {
   const int row = threadIdx.x & (kTile - 1), w = (threadIdx.x >> 5) & 3;
   const uint32_t lane0 = (uint32_t)(32 * w) << 16, to = c.tmem + lane0 + kColO + 128 * t, ts = c.tmem + lane0 + kColS + 128 * t;
   const int token = it.q0 + t * tokens + (row >> a.gq_log2);
@@ -189,7 +276,7 @@ __device__ __forceinline__ bool rows_role(const Ctx c, const PromptArgs& a, cons
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     if (!(i & 1)) {
-      if (!c.wait(kBS + t, i >> 1)) return false;
+      if (!c.wait(kBS + t, k.s + (i >> 1))) return false;
       tc_fence_after();
     }
     float s0[32], s1[32];
@@ -221,7 +308,8 @@ __device__ __forceinline__ bool rows_role(const Ctx c, const PromptArgs& a, cons
         }
         l *= al;
         if (i > 0) {
-          if (!c.wait(kBO + 2 * t + ((i - 1) & 1), (i - 1) >> 1)) return false;
+          const int h = (i - 1) & 1;
+          if (!c.wait(kBO + 2 * t + h, k.half(h) + ((i - 1) >> 1))) return false;
           tc_fence_after();
           rescale_o(to, al);
         }
@@ -241,12 +329,12 @@ __device__ __forceinline__ bool rows_role(const Ctx c, const PromptArgs& a, cons
     tmem_st16(at, r0);
     tmem_st16(at + 16, r1);
     if (i >= masked) {
-      const int stage = (i >> 1) * 2 + 1;          // the block's values in the ring
-      if (!c.wait(kBFull + stage % kStages, stage / kStages)) return false;
-      const uint32_t mask = c.base + kOffMask + 8 * (i - masked);
-      clean_values(c.base + kOffRing + (stage % kStages) * kTileBytes + (i & 1) * kSub * 128, mask);
+      const int v = k.ring + (i >> 1) * 2 + 1;     // the block's values in the ring
+      if (!c.wait(kBFull + v % kStages, v / kStages)) return false;
+      const uint32_t mask = c.base + kOffItem + slot * kItemBytes + 16 + 8 * (i - masked);
+      clean_values(c.base + kOffRing + (v % kStages) * kTileBytes + (i & 1) * kSub * 128, mask);
       c.arrive(kBC + t);                           // all four warps have looked
-      if (!c.wait(kBC + t, i - masked)) return false;
+      if (!c.wait(kBC + t, k.cleaned + i - masked)) return false;
       const uint2 bad = lds64(mask);
       const uint32_t lo = live >= 32 ? ~0u : live <= 0 ? 0u : (1u << live) - 1u;
       const uint32_t hi = live >= 64 ? ~0u : live <= 32 ? 0u : (1u << (live - 32)) - 1u;
@@ -254,106 +342,157 @@ __device__ __forceinline__ bool rows_role(const Ctx c, const PromptArgs& a, cons
     }
     tmem_wait_st();
     tc_fence_before();
-    c.arrive(kBP + 2 * t + (i & 1));            // a barrier for each half: both may be there before the first is used
+    c.arrive(kBP + 2 * t + (i & 1));
   }
-  if (n == 0) return true;
-  if (!c.wait(kBO + 2 * t + ((n - 1) & 1), (n - 1) >> 1)) return false;
-  tc_fence_after();
-  // ---- the rows' results ----
-  const bool live_row = token < it.len;
-  const long long at = (long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & ((1 << a.gq_log2) - 1));
-  const float inv = 1.f / l;
-  float bad = 0.f;
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    float o[32];
-    tmem_ld32(to + 32 * q, o);
-#pragma unroll
-    for (int x = 0; x < 32; ++x) {
-      o[x] *= inv;
-      bad = fmaf(o[x], 0.f, bad);
-    }
-    if (!live_row) continue;
-    if (a.out_fp32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * kD + 32 * q);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * kD + 32 * q);
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        dst[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                            pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+  if (n > 0) {
+    const int h = (n - 1) & 1;
+    if (!c.wait(kBO + 2 * t + h, k.half(h) + ((n - 1) >> 1))) return false;
+    tc_fence_after();
+    float bad = 0.f;
+    write_rows(c, a, it, t, tokens, to, 1.f / l, bad);
+    if (token < it.len) {
+      if (bad != 0.f) flag(a.status, OSCAR_STATUS_NONFINITE);
+      if (a.lse != nullptr)
+        a.lse[(long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & ((1 << a.gq_log2) - 1))] =
+            (m * a.F + log2f(l)) * 0.69314718055994531f;
     }
   }
-  if (live_row && bad != 0.f) flag(a.status, OSCAR_STATUS_NONFINITE);
-  if (live_row && a.lse != nullptr) a.lse[at] = (m * a.F + log2f(l)) * 0.69314718055994531f;
+  const int most = max(c.seen(it, 0, tokens), c.seen(it, 1, tokens));
+  k.s += (n + 1) / 2;
+  k.half0 += (n + 1) / 2;
+  k.half1 += n / 2;
+  k.cleaned += max(n - masked, 0);
+  k.ring += 2 * ((most + kBlock - 1) / kBlock);
   return true;
 }
 
-// ---- loads: Q of the tiles, then keys and values of each block ----------------------------------------------
-__device__ __forceinline__ bool load_role(const Ctx c, const Item& it, const CUtensorMap* mq, const CUtensorMap* mk,
-                                          const CUtensorMap* mv, int gq_log2, int tokens, int blocks, int* issued) {
-  const uint64_t keep = qtile::l2_evict_normal();
+// ---- finding and loading: an item's first keys, Q of its tiles, then values and keys of each block ------------
+struct LoadCount {
+  int ring = 0, items = 0, asked = 0;
+};
+__device__ __forceinline__ bool load_block(const Ctx c, const Item& it, const CUtensorMap* map, int j, LoadCount& k, uint64_t keep) {
+  const int s = k.ring % kStages;
+  if (k.ring >= kStages && !c.wait(kBEmpty + s, k.ring / kStages - 1)) return false;
   if ((threadIdx.x & 31) == 0) {
-    mbar_expect_tx(c.bar(kBQ), 2 * kTileBytes);
-    for (int t = 0; t < 2; ++t)
-      for (int p = 0; p < 2; ++p)
-        tma_load_3d(c.base + kOffQ + t * kTileBytes + p * kHalfBytes, mq, 64 * p, it.h << gq_log2, it.start + it.q0 + t * tokens,
-                    c.bar(kBQ), keep);
+    const uint32_t dst = c.base + kOffRing + s * kTileBytes;
+    mbar_expect_tx(c.bar(kBFull + s), kTileBytes);
+    for (int p = 0; p < 2; ++p)
+      tma_load_3d(dst + p * kHalfBytes, map, 64 * p, it.h, it.start + j * kBlock, c.bar(kBFull + s), keep);
   }
-  for (int i = 0; i < 2 * blocks; ++i) {
-    const int s = i % kStages;
-    if (i >= kStages && !c.wait(kBEmpty + s, i / kStages - 1)) return false;
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t dst = c.base + kOffRing + s * kTileBytes;
-      mbar_expect_tx(c.bar(kBFull + s), kTileBytes);
-      for (int p = 0; p < 2; ++p)
-        tma_load_3d(dst + p * kHalfBytes, i & 1 ? mv : mk, 64 * p, it.h, it.start + (i >> 1) * kBlock, c.bar(kBFull + s), keep);
+  ++k.ring;
+  __syncwarp();
+  return true;
+}
+__device__ __forceinline__ bool load_role(const Ctx c, const PromptArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv, int tokens, LoadCount& k) {
+  const uint64_t keep = qtile::l2_evict_normal();
+  const int lane = threadIdx.x & 31;
+  unsigned index = blockIdx.x;
+  for (bool more = true; more;) {
+    __syncwarp();                                  // the last answer is read
+    if (lane == 0) {                               // ask for the CTA after this one
+      fence_async();
+      mbar_expect_tx(c.bar(kBNext), 16);
+      asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                       c.base + kOffNext),
+                   "r"(c.bar(kBNext))
+                   : "memory");
     }
-    *issued = i + 1;
-    __syncwarp();
+    ++k.asked;
+    const Item it = find_item(a, index);
+    if (it.q0 < it.len) {                          // the grid holds room for the prompts' last tiles
+      const int slot = k.items % kItems;
+      if (k.items >= kItems && !c.wait(kBItemFree + slot, k.items / kItems - 1)) return false;
+      const uint32_t at = c.base + kOffItem + slot * kItemBytes;
+      if (lane < 2 * kMasks) sts32(at + 16 + 4 * lane, 0u);
+      if (lane == 0) sts128(at, make_uint4((uint32_t)it.start, (uint32_t)it.len, (uint32_t)it.h, (uint32_t)it.q0));
+      c.arrive(kBItem + slot);
+      const int blocks = (max(c.seen(it, 0, tokens), c.seen(it, 1, tokens)) + kBlock - 1) / kBlock;
+      if (!load_block(c, it, mk, 0, k, keep)) return false;
+      if (k.items > 0 && !c.wait(kBQFree, k.items - 1)) return false;
+      if (lane == 0) {
+        mbar_expect_tx(c.bar(kBQ), 2 * kTileBytes);
+        for (int t = 0; t < 2; ++t)
+          for (int p = 0; p < 2; ++p)
+            tma_load_3d(c.base + kOffQ + t * kTileBytes + p * kHalfBytes, mq, 64 * p, it.h << a.gq_log2,
+                        it.start + it.q0 + t * tokens, c.bar(kBQ), keep);
+      }
+      __syncwarp();
+      ++k.items;
+#pragma unroll 1
+      for (int j = 0; j < blocks; ++j) {
+        if (!load_block(c, it, mv, j, k, keep)) return false;
+        if (j + 1 < blocks && !load_block(c, it, mk, j + 1, k, keep)) return false;
+      }
+    }
+    if (!c.wait(kBNext, k.asked - 1)) return false;
+    const uint4 x = lds128(c.base + kOffNext);
+    uint32_t taken;
+    asm volatile(
+        "{\n.reg .b128 r;\n.reg .b64 lo, hi;\n.reg .pred p;\nmov.b64 lo, {%2, %3};\nmov.b64 hi, {%4, %5};\nmov.b128 r, {lo, hi};\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+        : "=r"(taken), "=r"(index)
+        : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
+    more = taken != 0u;
   }
+  const int slot = k.items % kItems;               // no more items
+  if (k.items >= kItems && !c.wait(kBItemFree + slot, k.items / kItems - 1)) return false;
+  if (lane == 0) sts32(c.base + kOffItem + slot * kItemBytes + 4, 0xffffffffu);
+  c.arrive(kBItem + slot);
   return true;
 }
 
 // ---- products ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ bool mma_role(const Ctx c, const Item& it, int tokens, int blocks) {
+struct MmaCount {
+  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, ring = 0;
+};
+__device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens, int items, MmaCount& k) {
   const int n0 = (c.seen(it, 0, tokens) + kSub - 1) / kSub, n1 = (c.seen(it, 1, tokens) + kSub - 1) / kSub;
-  if (!c.wait(kBQ, 0)) return false;
+  const int blocks = (max(n0, n1) + 1) / 2;
+  if (!c.wait(kBQ, items)) return false;
 #pragma unroll 1
   for (int j = 0; j <= blocks; ++j)
-#pragma unroll 1
+#pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int n = t ? n1 : n0;
       const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
+      const int kk0 = k.ring + 2 * j, vv0 = kk0 - 1;   // this block's keys and the last one's values in the ring
 #pragma unroll 1
       for (int i = 2 * (j - 1); i >= 0 && i < min(n, 2 * j); ++i) {   // O of the block before
-        const int stage = 2 * j - 1;
-        if (!c.wait(kBFull + stage % kStages, stage / kStages) || !c.wait(kBP + 2 * t + (i & 1), i >> 1)) return false;
+        if (i == 0 && k.tiles[t] > 0 && !c.wait(kBOFree + t, k.tiles[t] - 1)) return false;
+        if (!c.wait(kBFull + vv0 % kStages, vv0 / kStages) || !c.wait(kBP + 2 * t + (i & 1), (i & 1 ? k.half[t][1] : k.half[t][0]) + (i >> 1))) return false;
         tc_fence_after();
-        const uint32_t v = desc_lo(c.base + kOffRing + (stage % kStages) * kTileBytes + (i & 1) * kSub * 128, kHalfBytes);
+        const uint32_t v = desc_lo(c.base + kOffRing + (vv0 % kStages) * kTileBytes + (i & 1) * kSub * 128, kHalfBytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_ta_warp(to, ts + 64 * (i & 1) + 8 * kk, v + kk * (16 * 128 / 16), desc_hi(1024, true), kIdescO, i > 0 || kk > 0);
         umma_commit_warp(c.bar(kBO + 2 * t + (i & 1)));
       }
-      if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + (2 * j - 1) % kStages));   // both tiles are done with the values
+      if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + vv0 % kStages));   // both tiles are done with the values
       if (2 * j < n) {                             // S of this one
-        const int stage = 2 * j;
-        if (!c.wait(kBFull + stage % kStages, stage / kStages)) return false;
+        if (!c.wait(kBFull + kk0 % kStages, kk0 / kStages)) return false;
         tc_fence_after();
         const uint32_t q = desc_lo(c.base + kOffQ + t * kTileBytes, 16);
-        const uint32_t k = desc_lo(c.base + kOffRing + (stage % kStages) * kTileBytes, 16);
+        const uint32_t key = desc_lo(c.base + kOffRing + (kk0 % kStages) * kTileBytes, 16);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t step = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
-          umma_warp(ts, q + step, desc_hi(1024, true), k + step, desc_hi(1024, true), kIdescS, kk > 0);
+          umma_warp(ts, q + step, desc_hi(1024, true), key + step, desc_hi(1024, true), kIdescS, kk > 0);
         }
         umma_commit_warp(c.bar(kBS + t));
       }
-      if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + 2 * j % kStages));
+      if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + kk0 % kStages));
+      if (j == blocks - 1 && t == 1) umma_commit_warp(c.bar(kBQFree));
     }
+  k.ring += 2 * blocks;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = t ? n1 : n0;
+    k.half[t][0] += (n + 1) / 2;
+    k.half[t][1] += n / 2;
+    k.tiles[t] += n > 0;
+  }
   return true;
 }
 
@@ -365,28 +504,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   c.base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int tokens = kTile >> a.gq_log2;           // of a tile
-  if (w == 0) {
-    const Item x = find_item(a, blockIdx.x);
-    if (lane == 0) {
-      sts32(c.base + kOffItem, (uint32_t)x.start);
-      sts32(c.base + kOffItem + 4, (uint32_t)x.len);
-      sts32(c.base + kOffItem + 8, (uint32_t)x.h);
-      sts32(c.base + kOffItem + 12, (uint32_t)x.q0);
-    }
-  } else if (w == kLoadWarp) {
-    for (int k = lane; k < kNumBars; k += 32) mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : 1);
+  if (w == kLoadWarp) {
+    for (int k = lane; k < kNumBars; k += 32)
+      mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : k >= kBItemFree && k < kBNext ? 9 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (lane < 2 * kMasks) sts32(c.base + kOffMask + 4 * lane, 0u);
     if (lane == 0) sts32(c.base + kOffFailed, 0u);
-  }
-  __syncthreads();
-  Item it;
-  it.start = (int)lds32(c.base + kOffItem);
-  it.len = (int)lds32(c.base + kOffItem + 4);
-  it.h = (int)lds32(c.base + kOffItem + 8);
-  it.q0 = (int)lds32(c.base + kOffItem + 12);
-  if (it.q0 >= it.len) return;                     // the grid holds room for the prompts' last tiles
-  if (w == kMmaWarp) {
+  } else if (w == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.base + kOffTmem),
                  "r"(kTmemCols)
                  : "memory");
@@ -396,12 +519,33 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   __syncthreads();
   tc_fence_after();
   bool ok = lds32(c.base + kOffTmem) == c.tmem;
-  const int blocks = (max(c.seen(it, 0, tokens), c.seen(it, 1, tokens)) + kBlock - 1) / kBlock;
-  int issued = 0;
-  if (ok) {
-    if (w < 8) ok = rows_role(c, a, it, w >> 2, tokens);
-    else if (w == kLoadWarp) ok = load_role(c, it, &mq, &mk, &mv, a.gq_log2, tokens, blocks, &issued);
-    else if (w == kMmaWarp) ok = mma_role(c, it, tokens, blocks);
+  LoadCount loads;
+  if (ok && w == kLoadWarp) {
+    ok = load_role(c, a, &mq, &mk, &mv, tokens, loads);
+  } else if (ok && w == kMmaWarp) {
+    MmaCount products;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int slot = i % kItems;
+      Item it;
+      ok = c.wait(kBItem + slot, i / kItems);
+      if (!ok || !read_item(c, slot, it)) break;
+      ok = mma_item(c, it, tokens, i, products);
+      if (!ok) break;
+      c.arrive(kBItemFree + slot);
+    }
+  } else if (ok && w < kLoadWarp) {
+    RowCount rows;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int slot = i % kItems;
+      Item it;
+      ok = c.wait(kBItem + slot, i / kItems);
+      if (!ok || !read_item(c, slot, it)) break;
+      ok = rows_item(c, a, it, slot, w >> 2, tokens, rows);
+      if (!ok) break;
+      c.arrive(kBItemFree + slot);
+    }
   }
   if (!ok) {
     if (lane == 0) flag(a.status, OSCAR_STATUS_TIMEOUT);
@@ -411,9 +555,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     umma_commit_warp(c.bar(kBFinal));
     mbar_wait(c.bar(kBFinal), 0);
   }
-  if (w == kLoadWarp && issued > 0) {              // and every copy lands before the CTA leaves
-    mbar_wait(c.bar(kBQ), 0);
-    for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(c.bar(kBFull + i % kStages), (i / kStages) & 1);
+  if (w == kLoadWarp) {                            // and every copy and answer lands before the CTA leaves
+    if (loads.asked > 0) mbar_wait(c.bar(kBNext), (loads.asked - 1) & 1);
+    if (loads.items > 0) mbar_wait(c.bar(kBQ), (loads.items - 1) & 1);
+    for (int i = max(0, loads.ring - kStages); i < loads.ring; ++i) mbar_wait(c.bar(kBFull + i % kStages), (i / kStages) & 1);
   }
   tc_fence_before();
   __syncthreads();
