@@ -13,7 +13,8 @@
 //  * O += P V, M128 N128 K16 x 4 for 64 tokens, A = P in TMEM, B = V as it lies in shared memory (channels contiguous).
 // The tensor pipe takes 1,024 cycles for a block of one tile (512 for S, 512 for O); while it works for one tile, the row
 // threads of the other have its logits. Products run in issue order, so an S may be issued over weights whose O is issued.
-// Warps: 0-3 and 4-7 rows of the two tiles, 8 finds the work and loads, 9 issues the products.
+// Warps: 0-3 and 4-7 rows of the two tiles, 8 finds the work and loads, 9 issues the products, 12-15 write the results: the
+// row threads are at the next item's weights by then.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
 //
 // Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
@@ -35,7 +36,10 @@ using qtile::tma_load_3d;
 
 constexpr int kTile = 128;                         // rows of a tile
 constexpr int kBlock = 128, kSub = 64;             // tokens of a block, and of what the row threads take at a time
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kWarps = 12;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kOutWarp = 12, kWarps = 16;
+// registers per thread: at launch, then of the rows' and the other warpgroups; the shares are what the CTA was launched with
+constexpr int kRegsLaunch = 128, kRegsRows = 144, kRegsOther = 112;
+static_assert(2 * kRegsRows + 2 * kRegsOther <= 4 * kRegsLaunch, "register shares");
 constexpr int kStages = 4;                         // ring of blocks: keys and values in turn
 constexpr int kHalfBytes = 128 * 128;              // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;         // 32 KB: Q of a tile, K or V of a block
@@ -43,12 +47,13 @@ constexpr int kOutBytes = 32 * 128;                // a warp's rows on their way
 constexpr int kItems = 3;                          // items found ahead
 constexpr int kMasks = 8;                          // 64-token groups at an item's end that not all rows see: 5 at most
 constexpr int kItemBytes = 16 + 8 * kMasks;        // start, len, h, q0; a bit set of each such group
-constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffOut = kOffRing + kStages * kTileBytes, kOffItem = kOffOut + 8 * kOutBytes;
+constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffOut = kOffRing + kStages * kTileBytes, kOffStat = kOffOut + 4 * kOutBytes,
+              kOffItem = kOffStat + 2 * kTile * 8;   // [tile][row] (reference, sum)
 constexpr int kOffNext = kOffItem + kItems * kItemBytes;   // the CTA that was taken over, 16 bytes
 constexpr int kOffBar = kOffNext + 16;
 // two barriers for a tile's weights and products: both halves of a block may be there before the first is used
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQ = kBEmpty + kStages, kBQFree = kBQ + 1, kBS = kBQFree + 1, kBP = kBS + 2,
-              kBC = kBP + 4, kBOFree = kBC + 2, kBO = kBOFree + 2, kBItem = kBO + 4, kBItemFree = kBItem + kItems,
+              kBC = kBP + 4, kBOFree = kBC + 2, kBStat = kBOFree + 2, kBO = kBStat + 2, kBItem = kBO + 4, kBItemFree = kBItem + kItems,
               kBNext = kBItemFree + kItems, kBFinal = kBNext + 1, kNumBars = kBFinal + 1;
 constexpr int kOffTmem = kOffBar + 8 * kNumBars, kOffFailed = kOffTmem + 4;
 constexpr int kSmem = kOffFailed + 4 + 1024;       // with alignment slack
@@ -204,67 +209,9 @@ __device__ __forceinline__ bool read_item(const Ctx c, int slot, Item& it) {
 // ---- row threads of tile t ------------------------------------------------------------------------------
 // What has gone before in this CTA, by which the barriers' phases go.
 struct RowCount {
-  int s = 0, half0 = 0, half1 = 0, cleaned = 0, ring = 0;
+  int s = 0, half0 = 0, half1 = 0, cleaned = 0, ring = 0, tiles = 0;
   __device__ __forceinline__ int half(int h) const { return h ? half1 : half0; }
 };
-
-// the rows' results: 128 bytes of each row at a time through shared memory, so that eight lanes write a row's 128 bytes
-__device__ __forceinline__ void write_rows(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens, uint32_t to, float inv,
-                                           float& bad) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = 32 * (warp & 3);
-  const uint32_t buf = c.base + kOffOut + warp * kOutBytes;
-  const int gq = 1 << a.gq_log2, chunks = a.out_fp32 ? 4 : 2;
-#pragma unroll 1
-  for (int q = 0; q < chunks; ++q) {
-    if (a.out_fp32) {
-      float o[32];
-      tmem_ld32(to + 32 * q, o);
-#pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        o[x] *= inv;
-        bad = fmaf(o[x], 0.f, bad);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
-                                                                      __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
-    } else {
-      float o[32], p[32];
-      tmem_ld32x2(to + 64 * q, to + 64 * q + 32, o, p);
-#pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        o[x] *= inv;
-        p[x] *= inv;
-        bad = fmaf(o[x], 0.f, fmaf(p[x], 0.f, bad));
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4),
-               make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                          pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7])));
-        sts128(buf + lane * 128 + (((x + 4) ^ (lane & 7)) << 4),
-               make_uint4(pack_bf16x2(p[8 * x], p[8 * x + 1]), pack_bf16x2(p[8 * x + 2], p[8 * x + 3]),
-                          pack_bf16x2(p[8 * x + 4], p[8 * x + 5]), pack_bf16x2(p[8 * x + 6], p[8 * x + 7])));
-      }
-    }
-    if (q == chunks - 1) {                         // O is read: the next item's may be written
-      tc_fence_before();
-      c.arrive(kBOFree + t);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3), row = first + r, token = it.q0 + t * tokens + (row >> a.gq_log2);
-      const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-      if (token < it.len) {
-        const long long at = (long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & (gq - 1));
-        char* dst = static_cast<char*>(a.out) + at * (a.out_fp32 ? 4 * kD : 2 * kD) + 128 * q + 16 * (lane & 7);
-        *reinterpret_cast<uint4*>(dst) = x;
-      }
-    }
-    __syncwarp();
-  }
-}
 
 __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int t, int tokens,
                                           RowCount& k) {
@@ -298,9 +245,10 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
       if (redo) {
-        float mx = -INFINITY;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 32; ++x) mx = fmaxf(mx, fmaxf(s0[x], s1[x]));
+        for (int x = 0; x < 32; ++x) mx4[x & 3] = qtile::max3f(mx4[x & 3], s0[x], s1[x]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float al = 1.f;
         if ((m == -INFINITY || sum > kMostSum) && mx > m) {
           al = m == -INFINITY ? 0.f : exp2f((m - mx) * a.F);
@@ -345,17 +293,12 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
     c.arrive(kBP + 2 * t + (i & 1));
   }
   if (n > 0) {
-    const int h = (n - 1) & 1;
-    if (!c.wait(kBO + 2 * t + h, k.half(h) + ((n - 1) >> 1))) return false;
-    tc_fence_after();
-    float bad = 0.f;
-    write_rows(c, a, it, t, tokens, to, 1.f / l, bad);
-    if (token < it.len) {
-      if (bad != 0.f) flag(a.status, OSCAR_STATUS_NONFINITE);
-      if (a.lse != nullptr)
-        a.lse[(long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & ((1 << a.gq_log2) - 1))] =
-            (m * a.F + log2f(l)) * 0.69314718055994531f;
-    }
+    if (k.tiles > 0 && !c.wait(kBOFree + t, k.tiles - 1)) return false;   // the last item's sums are read
+    const uint32_t stat = c.base + kOffStat + 8 * (t * kTile + row);
+    sts32(stat, __float_as_uint(m));
+    sts32(stat + 4, __float_as_uint(l));
+    c.arrive(kBStat + t);
+    ++k.tiles;
   }
   const int most = max(c.seen(it, 0, tokens), c.seen(it, 1, tokens));
   k.s += (n + 1) / 2;
@@ -363,6 +306,90 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
   k.half1 += n / 2;
   k.cleaned += max(n - masked, 0);
   k.ring += 2 * ((most + kBlock - 1) / kBlock);
+  return true;
+}
+
+// ---- the results: warps 12-15, a quarter of a tile's rows each -----------------------------------------------
+struct OutCount {
+  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0};
+};
+// 128 bytes of each row at a time go through shared memory, so that eight lanes write a row's 128 bytes
+__device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens, int n, OutCount& k) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, first = 32 * warp, row = first + lane;
+  const uint32_t buf = c.base + kOffOut + warp * kOutBytes, to = c.tmem + ((uint32_t)first << 16) + kColO + 128 * t;
+  const int gq = 1 << a.gq_log2, chunks = a.out_fp32 ? 4 : 2, h = (n - 1) & 1;
+  if (!c.wait(kBStat + t, k.tiles[t]) || !c.wait(kBO + 2 * t + h, (h ? k.half[t][1] : k.half[t][0]) + ((n - 1) >> 1))) return false;
+  tc_fence_after();
+  const uint2 stat = lds64(c.base + kOffStat + 8 * (t * kTile + row));
+  const float l = __uint_as_float(stat.y), inv = 1.f / l;
+  float bad = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < chunks; ++q) {
+    if (a.out_fp32) {
+      float o[32];
+      tmem_ld32(to + 32 * q, o);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        o[x] *= inv;
+        bad = fmaf(o[x], 0.f, bad);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
+                                                                      __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
+    } else {
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p) {
+        float o[32];
+        tmem_ld32(to + 64 * q + 32 * p, o);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          o[x] *= inv;
+          bad = fmaf(o[x], 0.f, bad);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          sts128(buf + lane * 128 + (((x + 4 * p) ^ (lane & 7)) << 4),
+                 make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                            pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7])));
+      }
+    }
+    if (q == chunks - 1) {                         // O and the sums are read: the next item's may be written
+      tc_fence_before();
+      c.arrive(kBOFree + t);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), tr = first + r, token = it.q0 + t * tokens + (tr >> a.gq_log2);
+      const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      if (token < it.len) {
+        const long long at = (long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (tr & (gq - 1));
+        char* dst = static_cast<char*>(a.out) + at * (a.out_fp32 ? 4 * kD : 2 * kD) + 128 * q + 16 * (lane & 7);
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+    __syncwarp();
+  }
+  const int token = it.q0 + t * tokens + (row >> a.gq_log2);
+  if (token < it.len) {
+    if (bad != 0.f) flag(a.status, OSCAR_STATUS_NONFINITE);
+    if (a.lse != nullptr)
+      a.lse[(long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & (gq - 1))] =
+          (__uint_as_float(stat.x) * a.F + log2f(l)) * 0.69314718055994531f;
+  }
+  return true;
+}
+__device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const Item& it, int tokens, OutCount& k) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = (c.seen(it, t, tokens) + kSub - 1) / kSub;
+    if (n == 0) continue;
+    if (!out_tile(c, a, it, t, tokens, n, k)) return false;
+    k.half[t][0] += (n + 1) / 2;
+    k.half[t][1] += n / 2;
+    ++k.tiles[t];
+  }
   return true;
 }
 
@@ -453,15 +480,16 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
   if (!c.wait(kBQ, items)) return false;
 #pragma unroll 1
   for (int j = 0; j <= blocks; ++j)
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       const int n = t ? n1 : n0;
       const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
+      const int tiles = t ? k.tiles[1] : k.tiles[0], h0 = t ? k.half[1][0] : k.half[0][0], h1 = t ? k.half[1][1] : k.half[0][1];
       const int kk0 = k.ring + 2 * j, vv0 = kk0 - 1;   // this block's keys and the last one's values in the ring
 #pragma unroll 1
       for (int i = 2 * (j - 1); i >= 0 && i < min(n, 2 * j); ++i) {   // O of the block before
-        if (i == 0 && k.tiles[t] > 0 && !c.wait(kBOFree + t, k.tiles[t] - 1)) return false;
-        if (!c.wait(kBFull + vv0 % kStages, vv0 / kStages) || !c.wait(kBP + 2 * t + (i & 1), (i & 1 ? k.half[t][1] : k.half[t][0]) + (i >> 1))) return false;
+        if (i == 0 && tiles > 0 && !c.wait(kBOFree + t, tiles - 1)) return false;
+        if (!c.wait(kBFull + vv0 % kStages, vv0 / kStages) || !c.wait(kBP + 2 * t + (i & 1), (i & 1 ? h1 : h0) + (i >> 1))) return false;
         tc_fence_after();
         const uint32_t v = desc_lo(c.base + kOffRing + (vv0 % kStages) * kTileBytes + (i & 1) * kSub * 128, kHalfBytes);
 #pragma unroll
@@ -506,7 +534,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   const int tokens = kTile >> a.gq_log2;           // of a tile
   if (w == kLoadWarp) {
     for (int k = lane; k < kNumBars; k += 32)
-      mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : k >= kBItemFree && k < kBNext ? 9 : 1);
+      mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : k >= kBItemFree && k < kBNext ? 13 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane == 0) sts32(c.base + kOffFailed, 0u);
   } else if (w == kMmaWarp) {
@@ -519,6 +547,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   __syncthreads();
   tc_fence_after();
   bool ok = lds32(c.base + kOffTmem) == c.tmem;
+  if (w < kLoadWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   LoadCount loads;
   if (ok && w == kLoadWarp) {
     ok = load_role(c, a, &mq, &mk, &mv, tokens, loads);
@@ -531,6 +561,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       ok = c.wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
       ok = mma_item(c, it, tokens, i, products);
+      if (!ok) break;
+      c.arrive(kBItemFree + slot);
+    }
+  } else if (ok && w >= kOutWarp) {
+    OutCount results;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int slot = i % kItems;
+      Item it;
+      ok = c.wait(kBItem + slot, i / kItems);
+      if (!ok || !read_item(c, slot, it)) break;
+      ok = out_item(c, a, it, tokens, results);
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
@@ -604,6 +646,9 @@ int launch_prompt_attention(int hq, int hkv, int B, const oscar_heads& q, const 
 }
 
 int configure_prompt_kernel() {
+  cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
+  if (cudaFuncGetAttributes(&at, k_prompt_attention) != cudaSuccess) return OSCAR_ERR_CUDA;
+  if (at.numRegs < kRegsLaunch) return OSCAR_ERR_UNSUPPORTED;   // a compiler that gives fewer: the shares would wait forever
   if (cudaFuncSetAttribute(k_prompt_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return OSCAR_ERR_CUDA;
   return set_max_shared_carveout(reinterpret_cast<const void*>(k_prompt_attention));
