@@ -13,8 +13,8 @@
 //  * O += P V, M128 N128 K16 x 4 for 64 tokens, A = P in TMEM, B = V as it lies in shared memory (channels contiguous).
 // The tensor pipe takes 1,024 cycles for a block of one tile (512 for S, 512 for O); while it works for one tile, the row
 // threads of the other have its logits. Products run in issue order, so an S may be issued over weights whose O is issued.
-// Warps: 0-3 and 4-7 rows of the two tiles, 8 finds the work and loads, 9 issues the products, 12-15 write the results: the
-// row threads are at the next item's weights by then.
+// Warps: 0-3 and 4-7 rows of the two tiles, 8 loads, 9 issues the products, 10 looks at values that are not finite,
+// 11 finds the work, 12-15 write the results: the row threads are at the next item's weights by then.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
 //
 // Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
@@ -22,8 +22,9 @@
 // the end of the one before it; nothing is counted in memory that calls could share.
 //
 // Masked places hold whatever the packed buffer holds: logits are replaced by -inf before anything looks at them. Values
-// that some row of the CTA does not see would reach it as 0 times a NaN; before the products of those last blocks the row
-// threads look at their values, note rows that are not finite, replace them by zeros, and make the rows that do see them NaN.
+// that a row does not see could reach it as 0 times a NaN. So an item with a result that is not finite is done once more, and then
+// warp 10 looks at the values that not all rows see before they are used, notes tokens that are not finite and replaces them
+// by zeros; rows that do see one of them become NaN. (Looking at all items' last blocks took a tenth of the time of short prompts.)
 #include <algorithm>
 
 #include "quant_tile.cuh"
@@ -36,25 +37,26 @@ using qtile::tma_load_3d;
 
 constexpr int kTile = 128;                         // rows of a tile
 constexpr int kBlock = 128, kSub = 64;             // tokens of a block, and of what the row threads take at a time
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kOutWarp = 12, kWarps = 16;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 10, kFindWarp = 11, kOutWarp = 12, kWarps = 16;
 // registers per thread: at launch, then of the rows' and the other warpgroups; the shares are what the CTA was launched with
-constexpr int kRegsLaunch = 128, kRegsRows = 144, kRegsOther = 112;
+constexpr int kRegsLaunch = 128, kRegsRows = 136, kRegsOther = 120;
 static_assert(2 * kRegsRows + 2 * kRegsOther <= 4 * kRegsLaunch, "register shares");
 constexpr int kStages = 4;                         // ring of blocks: keys and values in turn
 constexpr int kHalfBytes = 128 * 128;              // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;         // 32 KB: Q of a tile, K or V of a block
 constexpr int kOutBytes = 32 * 128;                // a warp's rows on their way out, 128 bytes of each
-constexpr int kItems = 3;                          // items found ahead
-constexpr int kMasks = 8;                          // 64-token groups at an item's end that not all rows see: 5 at most
-constexpr int kItemBytes = 16 + 8 * kMasks;        // start, len, h, q0; a bit set of each such group
+constexpr int kItems = 3;                          // worked on, loaded, found
+constexpr int kNear = 4;                           // blocks before the end of an item's loads at which the next one is looked for
+constexpr int kMasks = 8;                          // 64-token groups at an item's end that not all rows see: 6 at most
+constexpr int kItemMasks = 32, kItemBytes = kItemMasks + 8 * kMasks;   // start, len, h, q0; clean, bad; a bit set of each such group
 constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffOut = kOffRing + kStages * kTileBytes, kOffStat = kOffOut + 4 * kOutBytes,
               kOffItem = kOffStat + 2 * kTile * 8;   // [tile][row] (reference, sum)
 constexpr int kOffNext = kOffItem + kItems * kItemBytes;   // the CTA that was taken over, 16 bytes
 constexpr int kOffBar = kOffNext + 16;
 // two barriers for a tile's weights and products: both halves of a block may be there before the first is used
-constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQ = kBEmpty + kStages, kBQFree = kBQ + 1, kBS = kBQFree + 1, kBP = kBS + 2,
-              kBC = kBP + 4, kBOFree = kBC + 2, kBStat = kBOFree + 2, kBO = kBStat + 2, kBItem = kBO + 4, kBItemFree = kBItem + kItems,
-              kBNext = kBItemFree + kItems, kBFinal = kBNext + 1, kNumBars = kBFinal + 1;
+constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQ = kBEmpty + kStages, kBQFree = kBQ + 2, kBS = kBQFree + 2, kBP = kBS + 2,
+              kBOFree = kBP + 4, kBStat = kBOFree + 2, kBO = kBStat + 2, kBItem = kBO + 4, kBItemFree = kBItem + kItems,
+              kBGo = kBItemFree + kItems, kBCheck = kBGo + 1, kBNear = kBCheck + 1, kBNext = kBNear + 1, kBFinal = kBNext + 1, kNumBars = kBFinal + 1;
 constexpr int kOffTmem = kOffBar + 8 * kNumBars, kOffFailed = kOffTmem + 4;
 constexpr int kSmem = kOffFailed + 4 + 1024;       // with alignment slack
 static_assert(kOffItem % 16 == 0 && kItemBytes % 16 == 0 && kOffBar % 16 == 0, "alignment");
@@ -77,37 +79,48 @@ struct PromptArgs {
 struct Item {
   int start, len;                                  // the prompt's tokens
   int h, q0;                                       // key head, first token of the CTA's tiles (len <= q0: nothing to do)
+  bool clean;                                      // values that not all rows see are looked at
 };
 
 // Item i of prompt-major, then key head, then tiles from the last (which sees most) to the first; one warp. A prompt's
-// bounds are taken within [0, total] and in order, whatever cu holds.
-__device__ __forceinline__ Item find_item(const PromptArgs& a, long long i) {
+// bounds are taken within [0, total] and in order, whatever cu holds. from, before: the 32 prompts that held the last item
+// and the items before them, where the search starts unless i is further in front.
+struct Finder {
+  int from = 0;
+  unsigned before = 0;
+};
+__device__ __forceinline__ Item find_item(const PromptArgs& a, unsigned i, Finder& f) {
   const int lane = threadIdx.x & 31, tokens = 2 * kTile >> a.gq_log2;
-  long long before = 0;
-  bool bad = false;
-  Item it = {0, 0, 0, 0};
-  bool found = false;
-  for (int c = 0; c < a.B; c += 32) {
+  if (i < f.before) f = Finder();
+  Item it = {0, 0, 0, 0, false};
+  bool bad = false, found = false;
+  unsigned before = f.before;
+  for (int c = f.from; c < a.B; c += 32) {
     const int r = min(c + lane, a.B - 1), lo = a.cu[r], hi = a.cu[r + 1];
     const int start = min(max(lo, 0), a.total), end = min(max(hi, start), a.total);
     bad |= start != lo || end != hi;
     const int tiles = c + lane < a.B ? (end - start + tokens - 1) / tokens : 0;
-    long long sum = (long long)tiles * a.hkv;
+    unsigned sum = (unsigned)tiles * a.hkv;        // below 2^31 in all where the bounds are in order
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, sum, m);
+      const unsigned x = __shfl_up_sync(0xffffffffu, sum, m);
       if (lane >= m) sum += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, i < before + sum);
+    const unsigned hit = __ballot_sync(0xffffffffu, i - before < sum);
     if (hit != 0u && !found) {
       const int src = __ffs(hit) - 1, n = __shfl_sync(0xffffffffu, tiles, src);
-      const long long first = before + __shfl_sync(0xffffffffu, sum, src) - (long long)n * a.hkv;
+      const unsigned at = i - before - (__shfl_sync(0xffffffffu, sum, src) - (unsigned)n * a.hkv);
       it.start = __shfl_sync(0xffffffffu, start, src);
       it.len = __shfl_sync(0xffffffffu, end, src) - it.start;
-      const int at = (int)(i - first);
-      it.h = at / n;
-      it.q0 = (n - 1 - (at - it.h * n)) * tokens;
+      if (n > 0 && at < (unsigned)n * a.hkv) {
+        it.h = at / n;
+        it.q0 = (n - 1 - ((int)at - it.h * n)) * tokens;
+      } else {
+        it.len = 0;
+      }
       found = true;
+      f.from = c;
+      f.before = before;
       if (i != 0) break;                           // the first item's finder looks at all bounds
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
@@ -166,55 +179,26 @@ __device__ __forceinline__ void weights32(const float (&s)[32], float2 F2, float
   }
 }
 
-// The values of 64 tokens, two threads a token: rows that are not finite are noted in the mask at `mask` and replaced by
-// zeros. Both tiles may look at the same rows: the note stands before the zeros do, and a noted row is zeroed again.
-__device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
-  const int x = threadIdx.x & (kTile - 1), row = x >> 1;
-  const uint32_t at = rows + (x & 1) * kHalfBytes + row * 128;
-  __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
-  const __nv_bfloat162 zero = acc;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint4 v = lds128(at + 16 * (j ^ (row & 7)));   // chunks in an order without bank conflicts
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, acc);
-  }
-  const float2 f = __bfloat1622float2(acc);
-  const uint32_t word = mask + 4 * (row >> 5), bit = 1u << (row & 31);
-  const bool bad = f.x != 0.f || f.y != 0.f;         // 0 times a NaN or an infinity is NaN
-  if (__any_sync(0xffffffffu, bad || (lds32(mask) | lds32(mask + 4)) != 0u)) {
-    if (bad) asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(word), "r"(bit) : "memory");
-    __threadfence_block();
-    __syncwarp();                                    // a token's two threads are in one warp
-    if (lds32(word) & bit) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sts128(at + 16 * j, make_uint4(0u, 0u, 0u, 0u));
-    }
-    fence_async();
-  }
-}
-
 // An item as the roles read it; false: there is none any more. The shuffles tell the compiler that a warp's lanes have the same
-// numbers: operands of products that follow from them stay in uniform registers (without: 32,769 tokens 8.1 ms instead of ITEM_MS).
+// numbers.
 __device__ __forceinline__ bool read_item(const Ctx c, int slot, Item& it) {
   const uint4 x = lds128(c.base + kOffItem + slot * kItemBytes);
   it.start = __shfl_sync(0xffffffffu, (int)x.x, 0);
   it.len = __shfl_sync(0xffffffffu, (int)x.y, 0);
   it.h = __shfl_sync(0xffffffffu, (int)x.z, 0);
   it.q0 = __shfl_sync(0xffffffffu, (int)x.w, 0);
+  it.clean = __shfl_sync(0xffffffffu, (int)lds32(c.base + kOffItem + slot * kItemBytes + 16), 0) != 0;
   return it.len >= 0;
 }
 
 // ---- row threads of tile t ------------------------------------------------------------------------------
 // What has gone before in this CTA, by which the barriers' phases go.
 struct RowCount {
-  int s = 0, half0 = 0, half1 = 0, cleaned = 0, ring = 0, tiles = 0;
+  int s = 0, half0 = 0, half1 = 0, tiles = 0;
   __device__ __forceinline__ int half(int h) const { return h ? half1 : half0; }
 };
 
-__device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int t, int tokens,
-                                          RowCount& k) {
+__device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens, RowCount& k) {
   const int row = threadIdx.x & (kTile - 1), w = (threadIdx.x >> 5) & 3;
   const uint32_t lane0 = (uint32_t)(32 * w) << 16, to = c.tmem + lane0 + kColO + 128 * t, ts = c.tmem + lane0 + kColS + 128 * t;
   const int token = it.q0 + t * tokens + (row >> a.gq_log2);
@@ -229,13 +213,14 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
     float s0[32], s1[32];
     const uint32_t at = ts + 64 * (i & 1);
     tmem_ld32x2(at, at + 32, s0, s1);
-    const int live = token + 1 - i * kSub;         // of the 64 tokens
     if (i >= masked) {
+      const int live = token + 1 - i * kSub;       // of the 64 tokens
+      if (__any_sync(0xffffffffu, live < 32)) {
 #pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        s0[x] = x < live ? s0[x] : -INFINITY;
-        s1[x] = 32 + x < live ? s1[x] : -INFINITY;
+        for (int x = 0; x < 32; ++x) s0[x] = x < live ? s0[x] : -INFINITY;
       }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) s1[x] = 32 + x < live ? s1[x] : -INFINITY;
     }
     uint32_t r0[16], r1[16];
     float sum = 0.f;
@@ -247,7 +232,9 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
       if (redo) {
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 32; ++x) mx4[x & 3] = qtile::max3f(mx4[x & 3], s0[x], s1[x]);
+        for (int x = 0; x < 32; x += 2) mx4[x >> 1 & 3] = qtile::max3f(mx4[x >> 1 & 3], s0[x], s0[x + 1]);
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) mx4[x >> 1 & 3] = qtile::max3f(mx4[x >> 1 & 3], s1[x], s1[x + 1]);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float al = 1.f;
         if ((m == -INFINITY || sum > kMostSum) && mx > m) {
@@ -276,18 +263,6 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
     l += sum;
     tmem_st16(at, r0);
     tmem_st16(at + 16, r1);
-    if (i >= masked) {
-      const int v = k.ring + (i >> 1) * 2 + 1;     // the block's values in the ring
-      if (!c.wait(kBFull + v % kStages, v / kStages)) return false;
-      const uint32_t mask = c.base + kOffItem + slot * kItemBytes + 16 + 8 * (i - masked);
-      clean_values(c.base + kOffRing + (v % kStages) * kTileBytes + (i & 1) * kSub * 128, mask);
-      c.arrive(kBC + t);                           // all four warps have looked
-      if (!c.wait(kBC + t, k.cleaned + i - masked)) return false;
-      const uint2 bad = lds64(mask);
-      const uint32_t lo = live >= 32 ? ~0u : live <= 0 ? 0u : (1u << live) - 1u;
-      const uint32_t hi = live >= 64 ? ~0u : live <= 32 ? 0u : (1u << (live - 32)) - 1u;
-      if ((bad.x & lo) | (bad.y & hi)) l = NAN;
-    }
     tmem_wait_st();
     tc_fence_before();
     c.arrive(kBP + 2 * t + (i & 1));
@@ -300,12 +275,59 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
     c.arrive(kBStat + t);
     ++k.tiles;
   }
-  const int most = max(c.seen(it, 0, tokens), c.seen(it, 1, tokens));
   k.s += (n + 1) / 2;
   k.half0 += (n + 1) / 2;
   k.half1 += n / 2;
-  k.cleaned += max(n - masked, 0);
-  k.ring += 2 * ((most + kBlock - 1) / kBlock);
+  return true;
+}
+
+// ---- values that not all rows see: warp 10 ---------------------------------------------------------------------
+// 64 tokens, two a lane: tokens that are not finite are noted in the bit set at `mask` and replaced by zeros.
+__device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 acc[2][4];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[k][e] = zero;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 v = lds128(rows + (j >> 3) * kHalfBytes + (32 * k + lane) * 128 + 16 * ((j ^ lane) & 7));   // no bank conflicts
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[k][e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, acc[k][e]);
+    }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float2 f = __bfloat1622float2(__hadd2(__hadd2(acc[k][0], acc[k][1]), __hadd2(acc[k][2], acc[k][3])));
+    const bool bad = f.x != 0.f || f.y != 0.f;     // 0 times a NaN or an infinity is NaN
+    const unsigned set = __ballot_sync(0xffffffffu, bad);
+    if (set != 0u) {
+      if (lane == 0) sts32(mask + 4 * k, set);
+      if (bad)
+        for (int j = 0; j < 16; ++j) sts128(rows + (j >> 3) * kHalfBytes + (32 * k + lane) * 128 + 16 * (j & 7), make_uint4(0u, 0u, 0u, 0u));
+      fence_async();
+    }
+  }
+}
+__device__ __forceinline__ bool check_item(const Ctx c, const Item& it, int slot, int tokens, int& ring, int& checked) {
+  const int masked = it.q0 / kSub, most = max(c.seen(it, 0, tokens), c.seen(it, 1, tokens));
+  const int blocks = (most + kBlock - 1) / kBlock;
+#pragma unroll 1
+  for (int j = masked / 2; it.clean && j < blocks; ++j) {
+    const int v = ring + 2 * j + 1;
+    if (!c.wait(kBGo, checked)) return false;      // the values are there, and no product uses them yet
+#pragma unroll 1
+    for (int i = max(2 * j, masked); i < 2 * j + 2 && i * kSub < most; ++i)
+      clean_values(c.base + kOffRing + (v % kStages) * kTileBytes + (i & 1) * kSub * 128,
+                   c.base + kOffItem + slot * kItemBytes + kItemMasks + 8 * (i - masked));
+    c.arrive(kBCheck);
+    ++checked;
+  }
+  ring += 2 * blocks;
   return true;
 }
 
@@ -314,78 +336,102 @@ struct OutCount {
   int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0};
 };
 // 128 bytes of each row at a time go through shared memory, so that eight lanes write a row's 128 bytes
-__device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const Item& it, int t, int tokens, int n, OutCount& k) {
+__device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const Item& it, int slot, int t, int tokens, int n,
+                                         OutCount& k) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, first = 32 * warp, row = first + lane;
   const uint32_t buf = c.base + kOffOut + warp * kOutBytes, to = c.tmem + ((uint32_t)first << 16) + kColO + 128 * t;
-  const int gq = 1 << a.gq_log2, chunks = a.out_fp32 ? 4 : 2, h = (n - 1) & 1;
+  const int gq = 1 << a.gq_log2, h = (n - 1) & 1;
   if (!c.wait(kBStat + t, k.tiles[t]) || !c.wait(kBO + 2 * t + h, (h ? k.half[t][1] : k.half[t][0]) + ((n - 1) >> 1))) return false;
   tc_fence_after();
   const uint2 stat = lds64(c.base + kOffStat + 8 * (t * kTile + row));
-  const float l = __uint_as_float(stat.y), inv = 1.f / l;
-  float bad = 0.f;
+  const int token = it.q0 + t * tokens + (row >> a.gq_log2), masked = it.q0 / kSub;
+  float l = __uint_as_float(stat.y);
+  for (int i = masked; it.clean && i < n; ++i) {   // values that are not finite
+    const uint2 b = lds64(c.base + kOffItem + slot * kItemBytes + kItemMasks + 8 * (i - masked));
+    const int live = token + 1 - i * kSub;         // of the 64 tokens
+    const uint32_t lo = live >= 32 ? ~0u : live <= 0 ? 0u : (1u << live) - 1u;
+    const uint32_t hi = live >= 64 ? ~0u : live <= 32 ? 0u : (1u << (live - 32)) - 1u;
+    if ((b.x & lo) | (b.y & hi)) l = NAN;
+  }
+  const float inv = 1.f / l;
+  const int left = it.len - it.q0 - t * tokens;    // tokens of the tile
+  const long long base = ((long long)(it.start + it.q0 + t * tokens) * a.hq + (it.h << a.gq_log2)) * kD;
+  float bad4[4] = {0.f, 0.f, 0.f, 0.f};            // stays 0 while all is finite
+  auto write = [&](int q) {                        // 128 bytes of each row
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), tr = first + r, tok = tr >> a.gq_log2;
+      const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      if (tok < left) {
+        const int at = (tok * a.hq + (tr & (gq - 1))) * kD;   // in the tile
+        char* dst = static_cast<char*>(a.out) + (base + at) * (a.out_fp32 ? 4 : 2) + 128 * q + 16 * (lane & 7);
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+    __syncwarp();
+  };
+  auto free_o = [&] {                              // O and the sums are read: the next item's may be written
+    tc_fence_before();
+    c.arrive(kBOFree + t);
+  };
+  if (a.out_fp32) {
 #pragma unroll 1
-  for (int q = 0; q < chunks; ++q) {
-    if (a.out_fp32) {
+    for (int q = 0; q < 4; ++q) {
       float o[32];
       tmem_ld32(to + 32 * q, o);
 #pragma unroll
       for (int x = 0; x < 32; ++x) {
         o[x] *= inv;
-        bad = fmaf(o[x], 0.f, bad);
+        bad4[x & 3] = fmaf(o[x], 0.f, bad4[x & 3]);
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x)
         sts128(buf + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
                                                                       __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
-    } else {
+      if (q == 3) free_o();
+      write(q);
+    }
+  } else {
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll 1
       for (int p = 0; p < 2; ++p) {
         float o[32];
         tmem_ld32(to + 64 * q + 32 * p, o);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          o[x] *= inv;
-          bad = fmaf(o[x], 0.f, bad);
+        for (int x = 0; x < 4; ++x) {
+          uint32_t r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = __fmul2_rn(make_float2(o[8 * x + 2 * e], o[8 * x + 2 * e + 1]), make_float2(inv, inv));
+            bad4[e] = fmaf(v.x, 0.f, fmaf(v.y, 0.f, bad4[e]));
+            r[e] = pack_bf16x2(v.x, v.y);
+          }
+          sts128(buf + lane * 128 + (((x + 4 * p) ^ (lane & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          sts128(buf + lane * 128 + (((x + 4 * p) ^ (lane & 7)) << 4),
-                 make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                            pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7])));
       }
+      if (q == 1) free_o();
+      write(q);
     }
-    if (q == chunks - 1) {                         // O and the sums are read: the next item's may be written
-      tc_fence_before();
-      c.arrive(kBOFree + t);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3), tr = first + r, token = it.q0 + t * tokens + (tr >> a.gq_log2);
-      const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-      if (token < it.len) {
-        const long long at = (long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (tr & (gq - 1));
-        char* dst = static_cast<char*>(a.out) + at * (a.out_fp32 ? 4 * kD : 2 * kD) + 128 * q + 16 * (lane & 7);
-        *reinterpret_cast<uint4*>(dst) = x;
-      }
-    }
-    __syncwarp();
   }
-  const int token = it.q0 + t * tokens + (row >> a.gq_log2);
   if (token < it.len) {
-    if (bad != 0.f) flag(a.status, OSCAR_STATUS_NONFINITE);
+    if (bad4[0] + bad4[1] + bad4[2] + bad4[3] != 0.f) {
+      if (it.clean) flag(a.status, OSCAR_STATUS_NONFINITE);
+      else sts32(c.base + kOffItem + slot * kItemBytes + 20, 1u);   // once more
+    }
     if (a.lse != nullptr)
       a.lse[(long long)(it.start + token) * a.hq + (it.h << a.gq_log2) + (row & (gq - 1))] =
           (__uint_as_float(stat.x) * a.F + log2f(l)) * 0.69314718055994531f;
   }
   return true;
 }
-__device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const Item& it, int tokens, OutCount& k) {
+__device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int tokens, OutCount& k) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = (c.seen(it, t, tokens) + kSub - 1) / kSub;
     if (n == 0) continue;
-    if (!out_tile(c, a, it, t, tokens, n, k)) return false;
+    if (!out_tile(c, a, it, slot, t, tokens, n, k)) return false;
     k.half[t][0] += (n + 1) / 2;
     k.half[t][1] += n / 2;
     ++k.tiles[t];
@@ -393,9 +439,77 @@ __device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const
   return true;
 }
 
-// ---- finding and loading: an item's first keys, Q of its tiles, then values and keys of each block ------------
+// ---- finding ------------------------------------------------------------------------------------------------------
+// Each item once, and once more if its results ask for it; the next one is looked for when the loads of the one before near their
+// end. (Two found ahead whatever their lengths: CTAs that are done wait for items others hold, 2 x 8K tokens 1.44 ms instead of 1.32.)
+__device__ __forceinline__ bool find_role(const Ctx c, const PromptArgs& a, int& asked) {
+  const int lane = threadIdx.x & 31;
+  Finder f;
+  int items = 0, done = 0, near = 0;               // given out; of which the results are known; of which the loads near their end
+  unsigned index = blockIdx.x;
+  bool more = true, first = true;
+  auto wait_near = [&] {                           // a barrier's phases can be told apart only one by one
+    for (; near < items; ++near)
+      if (!c.wait(kBNear, near)) return false;
+    return true;
+  };
+  for (;;) {
+    Item it = {0, -1, 0, 0, false};                // the end
+    if (items - done == kItems || (!more && done < items)) {
+      const int slot = done % kItems;
+      if (!c.wait(kBItemFree + slot, done / kItems)) return false;
+      ++done;
+      Item old;
+      read_item(c, slot, old);
+      const bool bad = __shfl_sync(0xffffffffu, (int)lds32(c.base + kOffItem + slot * kItemBytes + 20), 0) != 0;
+      if (!bad) continue;
+      it = old;
+      it.clean = true;
+      if (!wait_near()) return false;
+    } else if (more) {
+      if (!first) {                                // the next CTA that has not started
+        if (!wait_near()) return false;
+        __syncwarp();                              // the last answer is read
+        if (lane == 0) {
+          fence_async();
+          mbar_expect_tx(c.bar(kBNext), 16);
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                           c.base + kOffNext),
+                       "r"(c.bar(kBNext))
+                       : "memory");
+        }
+        if (!c.wait(kBNext, asked++)) return false;
+        const uint4 x = lds128(c.base + kOffNext);
+        uint32_t taken;
+        asm volatile(
+            "{\n.reg .b128 r;\n.reg .b64 lo, hi;\n.reg .pred p;\nmov.b64 lo, {%2, %3};\nmov.b64 hi, {%4, %5};\nmov.b128 r, {lo, hi};\n"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+            : "=r"(taken), "=r"(index)
+            : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
+        more = __shfl_sync(0xffffffffu, taken, 0) != 0u;
+        if (!more) continue;
+      }
+      first = false;
+      it = find_item(a, index, f);
+      if (it.q0 >= it.len) continue;               // the grid holds room for the prompts' last tiles
+    }
+    const int slot = items % kItems;
+    const uint32_t at = c.base + kOffItem + slot * kItemBytes;
+    if (lane < 2 * kMasks) sts32(at + kItemMasks + 4 * lane, 0u);
+    if (lane == 0) {
+      sts128(at, make_uint4((uint32_t)it.start, (uint32_t)it.len, (uint32_t)it.h, (uint32_t)it.q0));
+      sts128(at + 16, make_uint4((uint32_t)it.clean, 0u, 0u, 0u));
+    }
+    c.arrive(kBItem + slot);
+    if (it.len < 0) return true;
+    ++items;
+  }
+}
+
+// ---- loading: an item's first keys, Q of its tiles, then values and keys of each block -------------------------
 struct LoadCount {
-  int ring = 0, items = 0, asked = 0;
+  int ring = 0, items = 0;
 };
 __device__ __forceinline__ bool load_block(const Ctx c, const Item& it, const CUtensorMap* map, int j, LoadCount& k, uint64_t keep) {
   const int s = k.ring % kStages;
@@ -410,74 +524,41 @@ __device__ __forceinline__ bool load_block(const Ctx c, const Item& it, const CU
   __syncwarp();
   return true;
 }
-__device__ __forceinline__ bool load_role(const Ctx c, const PromptArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
-                                          const CUtensorMap* mv, int tokens, LoadCount& k) {
+__device__ __forceinline__ bool load_item(const Ctx c, const Item& it, const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv, int gq_log2, int tokens, LoadCount& k) {
   const uint64_t keep = qtile::l2_evict_normal();
-  const int lane = threadIdx.x & 31;
-  unsigned index = blockIdx.x;
-  for (bool more = true; more;) {
-    __syncwarp();                                  // the last answer is read
-    if (lane == 0) {                               // ask for the CTA after this one
-      fence_async();
-      mbar_expect_tx(c.bar(kBNext), 16);
-      asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                       c.base + kOffNext),
-                   "r"(c.bar(kBNext))
-                   : "memory");
-    }
-    ++k.asked;
-    const Item it = find_item(a, index);
-    if (it.q0 < it.len) {                          // the grid holds room for the prompts' last tiles
-      const int slot = k.items % kItems;
-      if (k.items >= kItems && !c.wait(kBItemFree + slot, k.items / kItems - 1)) return false;
-      const uint32_t at = c.base + kOffItem + slot * kItemBytes;
-      if (lane < 2 * kMasks) sts32(at + 16 + 4 * lane, 0u);
-      if (lane == 0) sts128(at, make_uint4((uint32_t)it.start, (uint32_t)it.len, (uint32_t)it.h, (uint32_t)it.q0));
-      c.arrive(kBItem + slot);
-      const int blocks = (max(c.seen(it, 0, tokens), c.seen(it, 1, tokens)) + kBlock - 1) / kBlock;
-      if (!load_block(c, it, mk, 0, k, keep)) return false;
-      if (k.items > 0 && !c.wait(kBQFree, k.items - 1)) return false;
-      if (lane == 0) {
-        mbar_expect_tx(c.bar(kBQ), 2 * kTileBytes);
-        for (int t = 0; t < 2; ++t)
-          for (int p = 0; p < 2; ++p)
-            tma_load_3d(c.base + kOffQ + t * kTileBytes + p * kHalfBytes, mq, 64 * p, it.h << a.gq_log2,
-                        it.start + it.q0 + t * tokens, c.bar(kBQ), keep);
-      }
-      __syncwarp();
-      ++k.items;
+  const int blocks = (max(c.seen(it, 0, tokens), c.seen(it, 1, tokens)) + kBlock - 1) / kBlock;
+  if (blocks <= kNear) c.arrive(kBNear);
+  if (!load_block(c, it, mk, 0, k, keep)) return false;
 #pragma unroll 1
-      for (int j = 0; j < blocks; ++j) {
-        if (!load_block(c, it, mv, j, k, keep)) return false;
-        if (j + 1 < blocks && !load_block(c, it, mk, j + 1, k, keep)) return false;
-      }
+  for (int t = 0; t < 2; ++t) {
+    if (k.items > 0 && !c.wait(kBQFree + t, k.items - 1)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      mbar_expect_tx(c.bar(kBQ + t), kTileBytes);
+      for (int p = 0; p < 2; ++p)
+        tma_load_3d(c.base + kOffQ + t * kTileBytes + p * kHalfBytes, mq, 64 * p, it.h << gq_log2, it.start + it.q0 + t * tokens,
+                    c.bar(kBQ + t), keep);
     }
-    if (!c.wait(kBNext, k.asked - 1)) return false;
-    const uint4 x = lds128(c.base + kOffNext);
-    uint32_t taken;
-    asm volatile(
-        "{\n.reg .b128 r;\n.reg .b64 lo, hi;\n.reg .pred p;\nmov.b64 lo, {%2, %3};\nmov.b64 hi, {%4, %5};\nmov.b128 r, {lo, hi};\n"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
-        : "=r"(taken), "=r"(index)
-        : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
-    more = taken != 0u;
+    __syncwarp();
   }
-  const int slot = k.items % kItems;               // no more items
-  if (k.items >= kItems && !c.wait(kBItemFree + slot, k.items / kItems - 1)) return false;
-  if (lane == 0) sts32(c.base + kOffItem + slot * kItemBytes + 4, 0xffffffffu);
-  c.arrive(kBItem + slot);
+  ++k.items;
+#pragma unroll 1
+  for (int j = 0; j < blocks; ++j) {
+    if (j > 0 && blocks - j == kNear) c.arrive(kBNear);
+    if (!load_block(c, it, mv, j, k, keep)) return false;
+    if (j + 1 < blocks && !load_block(c, it, mk, j + 1, k, keep)) return false;
+  }
   return true;
 }
 
 // ---- products ---------------------------------------------------------------------------------------------
 struct MmaCount {
   int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, ring = 0;
+  int checked = 0;                                 // blocks whose values were looked at
 };
 __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens, int items, MmaCount& k) {
   const int n0 = (c.seen(it, 0, tokens) + kSub - 1) / kSub, n1 = (c.seen(it, 1, tokens) + kSub - 1) / kSub;
-  const int blocks = (max(n0, n1) + 1) / 2;
-  if (!c.wait(kBQ, items)) return false;
+  const int blocks = (max(n0, n1) + 1) / 2, checked = it.q0 / kBlock;   // from here on values may have to be looked at
 #pragma unroll 1
   for (int j = 0; j <= blocks; ++j)
 #pragma unroll 1
@@ -490,6 +571,10 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
       for (int i = 2 * (j - 1); i >= 0 && i < min(n, 2 * j); ++i) {   // O of the block before
         if (i == 0 && tiles > 0 && !c.wait(kBOFree + t, tiles - 1)) return false;
         if (!c.wait(kBFull + vv0 % kStages, vv0 / kStages) || !c.wait(kBP + 2 * t + (i & 1), (i & 1 ? h1 : h0) + (i >> 1))) return false;
+        if (it.clean && j - 1 >= checked && i == 2 * (j - 1) && (t == 0 || n0 <= i)) {   // the block's first product
+          c.arrive(kBGo);
+          if (!c.wait(kBCheck, k.checked++)) return false;
+        }
         tc_fence_after();
         const uint32_t v = desc_lo(c.base + kOffRing + (vv0 % kStages) * kTileBytes + (i & 1) * kSub * 128, kHalfBytes);
 #pragma unroll
@@ -498,6 +583,7 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
         umma_commit_warp(c.bar(kBO + 2 * t + (i & 1)));
       }
       if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + vv0 % kStages));   // both tiles are done with the values
+      if (j == 0 && !c.wait(kBQ + t, items)) return false;   // also of a tile without rows: its place is filled again
       if (2 * j < n) {                             // S of this one
         if (!c.wait(kBFull + kk0 % kStages, kk0 / kStages)) return false;
         tc_fence_after();
@@ -511,7 +597,7 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
         umma_commit_warp(c.bar(kBS + t));
       }
       if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + kk0 % kStages));
-      if (j == blocks - 1 && t == 1) umma_commit_warp(c.bar(kBQFree));
+      if (j == blocks - 1) umma_commit_warp(c.bar(kBQFree + t));   // the tile's last S
     }
   k.ring += 2 * blocks;
 #pragma unroll
@@ -534,7 +620,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   const int tokens = kTile >> a.gq_log2;           // of a tile
   if (w == kLoadWarp) {
     for (int k = lane; k < kNumBars; k += 32)
-      mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : k >= kBItemFree && k < kBNext ? 13 : 1);
+      mbar_init_n(c.bar(k), k >= kBP && k < kBO ? 4 : k >= kBItemFree && k < kBGo ? 15 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane == 0) sts32(c.base + kOffFailed, 0u);
   } else if (w == kMmaWarp) {
@@ -549,9 +635,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   bool ok = lds32(c.base + kOffTmem) == c.tmem;
   if (w < kLoadWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  // Each role walks the items by itself. (One loop around all of them made the products wait for their operands: 32,769
+  // tokens 8.1 ms.)
   LoadCount loads;
-  if (ok && w == kLoadWarp) {
-    ok = load_role(c, a, &mq, &mk, &mv, tokens, loads);
+  int asked = 0;
+  if (ok && w == kFindWarp) {
+    ok = find_role(c, a, asked);
+  } else if (ok && w == kLoadWarp) {
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int slot = i % kItems;
+      Item it;
+      ok = c.wait(kBItem + slot, i / kItems);
+      if (!ok || !read_item(c, slot, it)) break;
+      ok = load_item(c, it, &mq, &mk, &mv, a.gq_log2, tokens, loads);
+      if (!ok) break;
+      c.arrive(kBItemFree + slot);
+    }
   } else if (ok && w == kMmaWarp) {
     MmaCount products;
 #pragma unroll 1
@@ -564,6 +664,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
+  } else if (ok && w == kCheckWarp) {
+    int ring = 0, checked = 0;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int slot = i % kItems;
+      Item it;
+      ok = c.wait(kBItem + slot, i / kItems);
+      if (!ok || !read_item(c, slot, it)) break;
+      ok = check_item(c, it, slot, tokens, ring, checked);
+      if (!ok) break;
+      c.arrive(kBItemFree + slot);
+    }
   } else if (ok && w >= kOutWarp) {
     OutCount results;
 #pragma unroll 1
@@ -572,11 +684,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       Item it;
       ok = c.wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
-      ok = out_item(c, a, it, tokens, results);
+      ok = out_item(c, a, it, slot, tokens, results);
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
-  } else if (ok && w < kLoadWarp) {
+  } else if (ok) {
     RowCount rows;
 #pragma unroll 1
     for (int i = 0;; ++i) {
@@ -584,7 +696,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       Item it;
       ok = c.wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
-      ok = rows_item(c, a, it, slot, w >> 2, tokens, rows);
+      ok = rows_item(c, a, it, w >> 2, tokens, rows);
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
@@ -597,9 +709,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     umma_commit_warp(c.bar(kBFinal));
     mbar_wait(c.bar(kBFinal), 0);
   }
-  if (w == kLoadWarp) {                            // and every copy and answer lands before the CTA leaves
-    if (loads.asked > 0) mbar_wait(c.bar(kBNext), (loads.asked - 1) & 1);
-    if (loads.items > 0) mbar_wait(c.bar(kBQ), (loads.items - 1) & 1);
+  if (w == kFindWarp && asked > 0) mbar_wait(c.bar(kBNext), (asked - 1) & 1);   // and every answer and copy lands before the CTA leaves
+  if (w == kLoadWarp) {
+    if (loads.items > 0)
+      for (int t = 0; t < 2; ++t) mbar_wait(c.bar(kBQ + t), (loads.items - 1) & 1);
     for (int i = max(0, loads.ring - kStages); i < loads.ring; ++i) mbar_wait(c.bar(kBFull + i % kStages), (i / kStages) & 1);
   }
   tc_fence_before();
