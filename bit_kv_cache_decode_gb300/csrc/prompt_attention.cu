@@ -16,6 +16,9 @@
 // Warps: 0-3 and 4-7 rows of the two tiles, 8 loads, 9 issues the products, 10 looks at values that are not finite,
 // 11 finds the work, 12-15 write the results: the row threads are at the next item's weights by then.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
+// Measured: 32,769 tokens, 32 query and 8 key heads, 5.3 ms, 2 prompts of 8,192 with 64 and 8, 1.27 ms (1.66 and 1.69 PFLOP/s of
+// products that count; bound by the tensor pipe); 64 prompts of 1-901 tokens 156 us (0.91 PFLOP/s: blocks on the diagonal, half of
+// them masked, and the chain S, weights, O at an item's ends); one of 777 tokens 18 us (a CTA's chain of seven blocks, and the launch).
 //
 // Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
 // takes over CTAs that have not started yet (clusterlaunchcontrol), so that the loads and the first S of an item overlap
@@ -41,7 +44,8 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 10, kFindWarp = 11, kOut
 // registers per thread: at launch, then of the rows' and the other warpgroups; the shares are what the CTA was launched with
 constexpr int kRegsLaunch = 128, kRegsRows = 136, kRegsOther = 120;
 static_assert(2 * kRegsRows + 2 * kRegsOther <= 4 * kRegsLaunch, "register shares");
-constexpr int kStages = 4;                         // ring of blocks: keys and values in turn
+// Two pairs of places for a block's keys (0, 2) and values (1, 3), taken in turn.
+constexpr int kStages = 4;
 constexpr int kHalfBytes = 128 * 128;              // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;         // 32 KB: Q of a tile, K or V of a block
 constexpr int kOutBytes = 32 * 128;                // a warp's rows on their way out, 128 bytes of each
@@ -71,7 +75,6 @@ struct PromptArgs {
   int B, total, hq, hkv, gq_log2;
   float F;
   void* out;                                       // [total][hq][kD]
-  int out_fp32;
   float* lse;                                      // [total][hq], or null
   int* status;
 };
@@ -136,15 +139,20 @@ struct Ctx {
   __device__ __forceinline__ uint32_t bar(int k) const { return base + kOffBar + 8u * (uint32_t)k; }
   __device__ __forceinline__ bool failed() const { return lds32(base + kOffFailed) != 0u; }
   __device__ __forceinline__ void fail() const { sts32(base + kOffFailed, 1u); }
-  // one wait of a whole warp; false (the CTA has failed, or the wait expired) ends its work
+  // One wait of a whole warp; false (the CTA has failed, or the wait expired) ends its work. The loads' and the finder's waits are
+  // bounded in time; the other roles', whose code is to be small, end once one of those has failed (and by their tries).
   __device__ __forceinline__ bool wait(int k, int phase) const {
-    const uint32_t parity = (uint32_t)phase & 1u;
-    bool ok = mbar_try(bar(k), parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
+#pragma unroll 1
+    for (unsigned i = 0; !__all_sync(0xffffffffu, mbar_try(bar(k), (uint32_t)phase & 1u)); ++i)
+      if (failed() || i == kWaitLimit) return false;
+    return true;
+  }
+  __device__ __forceinline__ bool timed_wait(int k, int phase) const {
     const unsigned long long t0 = global_ns();
 #pragma unroll 1
-    while (!ok && !failed() && global_ns() - t0 <= kWaitNs) ok = mbar_try(bar(k), parity);
-    return __all_sync(0xffffffffu, ok);
+    while (!__all_sync(0xffffffffu, mbar_try(bar(k), (uint32_t)phase & 1u)))
+      if (failed() || __any_sync(0xffffffffu, global_ns() - t0 > kWaitNs)) return false;
+    return true;
   }
   __device__ __forceinline__ void arrive(int k) const {
     __syncwarp();
@@ -313,35 +321,35 @@ __device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
     }
   }
 }
-__device__ __forceinline__ bool check_item(const Ctx c, const Item& it, int slot, int tokens, int& ring, int& checked) {
+__device__ __forceinline__ bool check_item(const Ctx c, const Item& it, int slot, int tokens, int& seen_blocks, int& checked) {
   const int masked = it.q0 / kSub, most = max(c.seen(it, 0, tokens), c.seen(it, 1, tokens));
   const int blocks = (most + kBlock - 1) / kBlock;
 #pragma unroll 1
   for (int j = masked / 2; it.clean && j < blocks; ++j) {
-    const int v = ring + 2 * j + 1;
     if (!c.wait(kBGo, checked)) return false;      // the values are there, and no product uses them yet
 #pragma unroll 1
     for (int i = max(2 * j, masked); i < 2 * j + 2 && i * kSub < most; ++i)
-      clean_values(c.base + kOffRing + (v % kStages) * kTileBytes + (i & 1) * kSub * 128,
+      clean_values(c.base + kOffRing + (2 * ((seen_blocks + j) & 1) + 1) * kTileBytes + (i & 1) * kSub * 128,
                    c.base + kOffItem + slot * kItemBytes + kItemMasks + 8 * (i - masked));
     c.arrive(kBCheck);
     ++checked;
   }
-  ring += 2 * blocks;
+  seen_blocks += blocks;
   return true;
 }
 
 // ---- the results: warps 12-15, a quarter of a tile's rows each -----------------------------------------------
-struct OutCount {
-  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0};
+struct OutCount {                                  // of a tile
+  int half0 = 0, half1 = 0, tiles = 0;
 };
 // 128 bytes of each row at a time go through shared memory, so that eight lanes write a row's 128 bytes
+template <bool FP32>
 __device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const Item& it, int slot, int t, int tokens, int n,
-                                         OutCount& k) {
+                                         const OutCount& k) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, first = 32 * warp, row = first + lane;
   const uint32_t buf = c.base + kOffOut + warp * kOutBytes, to = c.tmem + ((uint32_t)first << 16) + kColO + 128 * t;
   const int gq = 1 << a.gq_log2, h = (n - 1) & 1;
-  if (!c.wait(kBStat + t, k.tiles[t]) || !c.wait(kBO + 2 * t + h, (h ? k.half[t][1] : k.half[t][0]) + ((n - 1) >> 1))) return false;
+  if (!c.wait(kBStat + t, k.tiles) || !c.wait(kBO + 2 * t + h, (h ? k.half1 : k.half0) + ((n - 1) >> 1))) return false;
   tc_fence_after();
   const uint2 stat = lds64(c.base + kOffStat + 8 * (t * kTile + row));
   const int token = it.q0 + t * tokens + (row >> a.gq_log2), masked = it.q0 / kSub;
@@ -365,7 +373,7 @@ __device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const
       const uint4 x = lds128(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
       if (tok < left) {
         const int at = (tok * a.hq + (tr & (gq - 1))) * kD;   // in the tile
-        char* dst = static_cast<char*>(a.out) + (base + at) * (a.out_fp32 ? 4 : 2) + 128 * q + 16 * (lane & 7);
+        char* dst = static_cast<char*>(a.out) + (base + at) * (FP32 ? 4 : 2) + 128 * q + 16 * (lane & 7);
         *reinterpret_cast<uint4*>(dst) = x;
       }
     }
@@ -375,7 +383,7 @@ __device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const
     tc_fence_before();
     c.arrive(kBOFree + t);
   };
-  if (a.out_fp32) {
+  if constexpr (FP32) {
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       float o[32];
@@ -426,15 +434,19 @@ __device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const
   }
   return true;
 }
-__device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int tokens, OutCount& k) {
-#pragma unroll
+template <bool FP32>
+__device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const Item& it, int slot, int tokens, OutCount& k0,
+                                         OutCount& k1) {
+#pragma unroll 1
   for (int t = 0; t < 2; ++t) {
     const int n = (c.seen(it, t, tokens) + kSub - 1) / kSub;
     if (n == 0) continue;
-    if (!out_tile(c, a, it, slot, t, tokens, n, k)) return false;
-    k.half[t][0] += (n + 1) / 2;
-    k.half[t][1] += n / 2;
-    ++k.tiles[t];
+    OutCount k = t ? k1 : k0;
+    if (!out_tile<FP32>(c, a, it, slot, t, tokens, n, k)) return false;
+    k.half0 += (n + 1) / 2;
+    k.half1 += n / 2;
+    ++k.tiles;
+    (t ? k1 : k0) = k;
   }
   return true;
 }
@@ -450,14 +462,14 @@ __device__ __forceinline__ bool find_role(const Ctx c, const PromptArgs& a, int&
   bool more = true, first = true;
   auto wait_near = [&] {                           // a barrier's phases can be told apart only one by one
     for (; near < items; ++near)
-      if (!c.wait(kBNear, near)) return false;
+      if (!c.timed_wait(kBNear, near)) return false;
     return true;
   };
   for (;;) {
     Item it = {0, -1, 0, 0, false};                // the end
     if (items - done == kItems || (!more && done < items)) {
       const int slot = done % kItems;
-      if (!c.wait(kBItemFree + slot, done / kItems)) return false;
+      if (!c.timed_wait(kBItemFree + slot, done / kItems)) return false;
       ++done;
       Item old;
       read_item(c, slot, old);
@@ -478,7 +490,7 @@ __device__ __forceinline__ bool find_role(const Ctx c, const PromptArgs& a, int&
                        "r"(c.bar(kBNext))
                        : "memory");
         }
-        if (!c.wait(kBNext, asked++)) return false;
+        if (!c.timed_wait(kBNext, asked++)) return false;
         const uint4 x = lds128(c.base + kOffNext);
         uint32_t taken;
         asm volatile(
@@ -509,53 +521,88 @@ __device__ __forceinline__ bool find_role(const Ctx c, const PromptArgs& a, int&
 
 // ---- loading: an item's first keys, Q of its tiles, then values and keys of each block -------------------------
 struct LoadCount {
-  int ring = 0, items = 0;
+  int items = 0, queries = 0, ring = 0;            // items; loads of Q, of keys and values
 };
-__device__ __forceinline__ bool load_block(const Ctx c, const Item& it, const CUtensorMap* map, int j, LoadCount& k, uint64_t keep) {
-  const int s = k.ring % kStages;
-  if (k.ring >= kStages && !c.wait(kBEmpty + s, k.ring / kStages - 1)) return false;
-  if ((threadIdx.x & 31) == 0) {
-    const uint32_t dst = c.base + kOffRing + s * kTileBytes;
-    mbar_expect_tx(c.bar(kBFull + s), kTileBytes);
-    for (int p = 0; p < 2; ++p)
-      tma_load_3d(dst + p * kHalfBytes, map, 64 * p, it.h, it.start + j * kBlock, c.bar(kBFull + s), keep);
-  }
-  ++k.ring;
-  __syncwarp();
-  return true;
-}
 __device__ __forceinline__ bool load_item(const Ctx c, const Item& it, const CUtensorMap* mq, const CUtensorMap* mk,
                                           const CUtensorMap* mv, int gq_log2, int tokens, LoadCount& k) {
   const uint64_t keep = qtile::l2_evict_normal();
   const int blocks = (max(c.seen(it, 0, tokens), c.seen(it, 1, tokens)) + kBlock - 1) / kBlock;
-  if (blocks <= kNear) c.arrive(kBNear);
-  if (!load_block(c, it, mk, 0, k, keep)) return false;
+  // the first keys, Q, then the values and the next keys of each block
 #pragma unroll 1
-  for (int t = 0; t < 2; ++t) {
-    if (k.items > 0 && !c.wait(kBQFree + t, k.items - 1)) return false;
-    if ((threadIdx.x & 31) == 0) {
-      mbar_expect_tx(c.bar(kBQ + t), kTileBytes);
-      for (int p = 0; p < 2; ++p)
-        tma_load_3d(c.base + kOffQ + t * kTileBytes + p * kHalfBytes, mq, 64 * p, it.h << gq_log2, it.start + it.q0 + t * tokens,
-                    c.bar(kBQ + t), keep);
+  for (int i = 0; i < 2 * blocks + 2; ++i) {
+    const bool query = i == 1 || i == 2;
+    const int t = i - 1, x = i == 0 ? 0 : i - 2, s = k.ring % kStages;   // tile; keys or values of block x / 2
+    if (query) {
+      if (k.items > 0 && !c.timed_wait(kBQFree + t, k.items - 1)) return false;
+    } else {
+      if (k.ring >= kStages && !c.timed_wait(kBEmpty + s, k.ring / kStages - 1)) return false;
+      if (i == 0 ? blocks <= kNear : (x & 1) == 1 && blocks - (x >> 1) - 1 == kNear) c.arrive(kBNear);
     }
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t dst = c.base + (query ? kOffQ + t * kTileBytes : kOffRing + s * kTileBytes);
+      const uint32_t bar = c.bar(query ? kBQ + t : kBFull + s);
+      const CUtensorMap* map = query ? mq : x & 1 ? mv : mk;
+      const int head = query ? it.h << gq_log2 : it.h, token = it.start + (query ? it.q0 + t * tokens : (x >> 1) * kBlock);
+      mbar_expect_tx(bar, kTileBytes);
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p) tma_load_3d(dst + p * kHalfBytes, map, 64 * p, head, token, bar, keep);
+    }
+    k.queries += query;
+    k.ring += !query;
     __syncwarp();
   }
   ++k.items;
-#pragma unroll 1
-  for (int j = 0; j < blocks; ++j) {
-    if (j > 0 && blocks - j == kNear) c.arrive(kBNear);
-    if (!load_block(c, it, mv, j, k, keep)) return false;
-    if (j + 1 < blocks && !load_block(c, it, mk, j + 1, k, keep)) return false;
-  }
   return true;
 }
 
 // ---- products ---------------------------------------------------------------------------------------------
+// One elected lane issues the eight (four) products of a batch from one set of operands: issued one by one in a loop, each
+// takes about 90 cycles instead of 64 (2 prompts of 8K: 1.35 ms, now 1.27). Four copies of the loop below, with tile and places
+// as constants, are 2 % faster on long prompts and 20 % slower on short ones (187 us instead of 156 for 64 of 1-901 tokens).
 struct MmaCount {
-  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, ring = 0;
+  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, blocks = 0;
   int checked = 0;                                 // blocks whose values were looked at
 };
+// Eight products over 128 channels, A and B in shared memory: one elected lane issues them all (see umma_warp).
+__device__ __forceinline__ void umma_channels(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n.reg .pred p, q, t;\n.reg .b64 a, b;\n.reg .b32 x, y;\nelect.sync _|q, 0xffffffff;\nsetp.ne.u32 p, 0, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      "add.u32 x, %1, 2;\nadd.u32 y, %2, 2;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 4;\nadd.u32 y, %2, 4;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 6;\nadd.u32 y, %2, 6;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 1024;\nadd.u32 y, %2, 1024;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 1026;\nadd.u32 y, %2, 1026;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 1028;\nadd.u32 y, %2, 1028;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "add.u32 x, %1, 1030;\nadd.u32 y, %2, 1030;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+      : "memory");
+}
+// Four products over 64 tokens, A in tensor memory.
+__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, q, t;\n.reg .b64 b;\n.reg .b32 x, y;\nelect.sync _|q, 0xffffffff;\nsetp.ne.u32 p, %5, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, p;\n"
+      "add.u32 x, %1, 8;\nadd.u32 y, %2, 128;\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      "add.u32 x, %1, 16;\nadd.u32 y, %2, 256;\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      "add.u32 x, %1, 24;\nadd.u32 y, %2, 384;\nmov.b64 b, {y, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
 __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens, int items, MmaCount& k) {
   const int n0 = (c.seen(it, 0, tokens) + kSub - 1) / kSub, n1 = (c.seen(it, 1, tokens) + kSub - 1) / kSub;
   const int blocks = (max(n0, n1) + 1) / 2, checked = it.q0 / kBlock;   // from here on values may have to be looked at
@@ -563,43 +610,36 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
   for (int j = 0; j <= blocks; ++j)
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-      const int n = t ? n1 : n0;
-      const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
+      const int n = t ? n1 : n0, b = k.blocks + j, pk = 2 * (b & 1), pv = 3 - pk;   // places of this block's keys, the last one's values
       const int tiles = t ? k.tiles[1] : k.tiles[0], h0 = t ? k.half[1][0] : k.half[0][0], h1 = t ? k.half[1][1] : k.half[0][1];
-      const int kk0 = k.ring + 2 * j, vv0 = kk0 - 1;   // this block's keys and the last one's values in the ring
+      const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
 #pragma unroll 1
       for (int i = 2 * (j - 1); i >= 0 && i < min(n, 2 * j); ++i) {   // O of the block before
+        const int h = i & 1;
         if (i == 0 && tiles > 0 && !c.wait(kBOFree + t, tiles - 1)) return false;
-        if (!c.wait(kBFull + vv0 % kStages, vv0 / kStages) || !c.wait(kBP + 2 * t + (i & 1), (i & 1 ? h1 : h0) + (i >> 1))) return false;
-        if (it.clean && j - 1 >= checked && i == 2 * (j - 1) && (t == 0 || n0 <= i)) {   // the block's first product
+        if (!c.wait(kBFull + pv, (b - 1) >> 1) || !c.wait(kBP + 2 * t + h, (h ? h1 : h0) + (i >> 1))) return false;
+        if (it.clean && j - 1 >= checked && h == 0 && (t == 0 || n0 <= i)) {   // the block's first product
           c.arrive(kBGo);
           if (!c.wait(kBCheck, k.checked++)) return false;
         }
         tc_fence_after();
-        const uint32_t v = desc_lo(c.base + kOffRing + (vv0 % kStages) * kTileBytes + (i & 1) * kSub * 128, kHalfBytes);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ta_warp(to, ts + 64 * (i & 1) + 8 * kk, v + kk * (16 * 128 / 16), desc_hi(1024, true), kIdescO, i > 0 || kk > 0);
-        umma_commit_warp(c.bar(kBO + 2 * t + (i & 1)));
+        umma_tokens(to, ts + 64 * h, desc_lo(c.base + kOffRing + pv * kTileBytes + h * kSub * 128, kHalfBytes), desc_hi(1024, true),
+                    kIdescO, i > 0);
+        umma_commit_warp(c.bar(kBO + 2 * t + h));
       }
-      if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + vv0 % kStages));   // both tiles are done with the values
+      if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + pv));   // both tiles are done with the values
       if (j == 0 && !c.wait(kBQ + t, items)) return false;   // also of a tile without rows: its place is filled again
       if (2 * j < n) {                             // S of this one
-        if (!c.wait(kBFull + kk0 % kStages, kk0 / kStages)) return false;
+        if (!c.wait(kBFull + pk, b >> 1)) return false;
         tc_fence_after();
-        const uint32_t q = desc_lo(c.base + kOffQ + t * kTileBytes, 16);
-        const uint32_t key = desc_lo(c.base + kOffRing + (kk0 % kStages) * kTileBytes, 16);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t step = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
-          umma_warp(ts, q + step, desc_hi(1024, true), key + step, desc_hi(1024, true), kIdescS, kk > 0);
-        }
+        umma_channels(ts, desc_lo(c.base + kOffQ + t * kTileBytes, 16), desc_lo(c.base + kOffRing + pk * kTileBytes, 16),
+                      desc_hi(1024, true), kIdescS);
         umma_commit_warp(c.bar(kBS + t));
       }
-      if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + kk0 % kStages));
+      if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + pk));
       if (j == blocks - 1) umma_commit_warp(c.bar(kBQFree + t));   // the tile's last S
     }
-  k.ring += 2 * blocks;
+  k.blocks += blocks;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = t ? n1 : n0;
@@ -610,6 +650,7 @@ __device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens
   return true;
 }
 
+template <bool FP32>
 __global__ void __launch_bounds__(32 * kWarps, 1)
     k_prompt_attention(PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv) {
@@ -646,7 +687,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     for (int i = 0;; ++i) {
       const int slot = i % kItems;
       Item it;
-      ok = c.wait(kBItem + slot, i / kItems);
+      ok = c.timed_wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
       ok = load_item(c, it, &mq, &mk, &mv, a.gq_log2, tokens, loads);
       if (!ok) break;
@@ -665,26 +706,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       c.arrive(kBItemFree + slot);
     }
   } else if (ok && w == kCheckWarp) {
-    int ring = 0, checked = 0;
+    int checked = 0, seen_blocks = 0;
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int slot = i % kItems;
       Item it;
       ok = c.wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
-      ok = check_item(c, it, slot, tokens, ring, checked);
+      ok = check_item(c, it, slot, tokens, seen_blocks, checked);
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
   } else if (ok && w >= kOutWarp) {
-    OutCount results;
+    OutCount results0, results1;
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int slot = i % kItems;
       Item it;
       ok = c.wait(kBItem + slot, i / kItems);
       if (!ok || !read_item(c, slot, it)) break;
-      ok = out_item(c, a, it, slot, tokens, results);
+      ok = out_item<FP32>(c, a, it, slot, tokens, results0, results1);
       if (!ok) break;
       c.arrive(kBItemFree + slot);
     }
@@ -711,8 +752,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   }
   if (w == kFindWarp && asked > 0) mbar_wait(c.bar(kBNext), (asked - 1) & 1);   // and every answer and copy lands before the CTA leaves
   if (w == kLoadWarp) {
-    if (loads.items > 0)
-      for (int t = 0; t < 2; ++t) mbar_wait(c.bar(kBQ + t), (loads.items - 1) & 1);
+    for (int t = 0; t < 2; ++t) {
+      const int n = (loads.queries + 1 - t) / 2;
+      if (n > 0) mbar_wait(c.bar(kBQ + t), (n - 1) & 1);
+    }
     for (int i = max(0, loads.ring - kStages); i < loads.ring; ++i) mbar_wait(c.bar(kBFull + i % kStages), (i / kStages) & 1);
   }
   tc_fence_before();
@@ -745,7 +788,7 @@ int launch_prompt_attention(int hq, int hkv, int B, const oscar_heads& q, const 
                             const int* cu_seqlens, int total, float sm_scale, void* out, int out_dtype, float* lse, int* status,
                             cudaStream_t st) {
   const int gq = hq / hkv, tokens = 2 * kTile / gq;
-  PromptArgs a = {cu_seqlens, B, total, hq, hkv, 0, sm_scale * kLog2e, out, out_dtype == OSCAR_OUT_FP32, lse, status};
+  PromptArgs a = {cu_seqlens, B, total, hq, hkv, 0, sm_scale * kLog2e, out, lse, status};
   while (1 << a.gq_log2 < gq) ++a.gq_log2;
   CUtensorMap mq, mk, mv;
   if (!rows_map(&mq, q, hq, total, gq, kTile / gq) || !rows_map(&mk, k, hkv, total, 1, kBlock) ||
@@ -754,17 +797,20 @@ int launch_prompt_attention(int hq, int hkv, int B, const oscar_heads& q, const 
   // a prompt of n tokens has ceil(n / tokens) items a head
   const long long items = hkv * (((long long)total + (long long)B * (tokens - 1)) / tokens);
   if (items >= 1ll << 31) return OSCAR_ERR_UNSUPPORTED;
-  k_prompt_attention<<<(int)items, 32 * kWarps, kSmem, st>>>(a, mq, mk, mv);
+  const auto kernel = out_dtype == OSCAR_OUT_FP32 ? k_prompt_attention<true> : k_prompt_attention<false>;
+  kernel<<<(int)items, 32 * kWarps, kSmem, st>>>(a, mq, mk, mv);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 int configure_prompt_kernel() {
-  cudaFuncAttributes at;                           // the register shares assume what the CTA is launched with
-  if (cudaFuncGetAttributes(&at, k_prompt_attention) != cudaSuccess) return OSCAR_ERR_CUDA;
-  if (at.numRegs < kRegsLaunch) return OSCAR_ERR_UNSUPPORTED;   // a compiler that gives fewer: the shares would wait forever
-  if (cudaFuncSetAttribute(k_prompt_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return OSCAR_ERR_CUDA;
-  return set_max_shared_carveout(reinterpret_cast<const void*>(k_prompt_attention));
+  for (auto fn : {k_prompt_attention<false>, k_prompt_attention<true>}) {
+    cudaFuncAttributes at;                         // the register shares assume what the CTA is launched with
+    if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return OSCAR_ERR_CUDA;
+    if (at.numRegs < kRegsLaunch) return OSCAR_ERR_UNSUPPORTED;   // a compiler that gives fewer: the shares would wait forever
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return OSCAR_ERR_CUDA;
+    if (int rc = set_max_shared_carveout(reinterpret_cast<const void*>(fn)); rc != OSCAR_OK) return rc;
+  }
+  return OSCAR_OK;
 }
 
 }  // namespace oscar
