@@ -205,3 +205,42 @@ def test_refusals_and_nothing_to_do():
     cache.prompt_attention(q, k, v, np.zeros(1, np.int32), SM, out=out)  # no prompts
     cache.prompt_attention(q, k, v, np.zeros(9, np.int32), SM, out=out)  # empty ones
     assert (out == 5).all() and cache.get_status() == 0
+
+
+@pytest.mark.parametrize("gq", [1, 4])
+def test_many_items_for_a_cta(gq):
+    # dozens of items a CTA, of all lengths; then values that are not finite in some prompts, between others that are
+    hkv, B = 8, 400
+    g = torch.Generator().manual_seed(gq)
+    lens = torch.randint(0, 420, (B,), generator=g).tolist()
+    n, cu = sum(lens), bounds(lens)
+    q, k, v = (x.clone() for x in rows(12, n, hkv * gq, hkv))
+    cache = cache_of(hkv * gq, hkv)
+    lse = torch.zeros(n, hkv * gq, device=DEV)
+    out = cache.prompt_attention(q, k, v, cu, SM, lse=lse)
+    some = set(torch.randint(0, n, (80,), generator=g).tolist())
+    C.check(out, lse, q, k, v, lens, cu[:-1], SM, rows=some)
+    for _ in range(3):                                                   # whoever takes what: the same bits
+        assert torch.equal(cache.prompt_attention(q, k, v, cu, SM), out)
+    hit = torch.zeros(n, hkv * gq, dtype=torch.bool, device=DEV)
+    for r in range(0, B, 3):
+        if lens[r] == 0:
+            continue
+        at, h = int(cu[r]) + (7 * r) % lens[r], r % hkv
+        v[at, h, r % 128] = (float("nan"), float("inf"), -float("inf"))[r // 3 % 3]
+        hit[at:int(cu[r + 1]), h * gq:(h + 1) * gq] = True
+    got = cache.prompt_attention(q, k, v, cu, SM)
+    assert cache.get_status() == osc.STATUS_NONFINITE
+    assert torch.equal(got[~hit], out[~hit]) and (~got[hit].isfinite()).any(-1).all()
+
+
+def test_more_prompts_than_a_search_holds():
+    # thousands of prompts, most of them empty, the others where searches of 32 begin and end
+    lens = [0] * 5000
+    for i, at in enumerate((0, 31, 32, 33, 1023, 1024, 2047, 3000, 4095, 4990, 4999)):
+        lens[at] = 1 + 37 * i
+    q, k, v = rows(13, sum(lens), 8, 2)
+    cu, cache = bounds(lens), cache_of(8, 2)
+    out = cache.prompt_attention(q, k, v, cu, SM)
+    C.check(out, None, q, k, v, lens, cu[:-1], SM)
+    assert cache.get_status() == 0
