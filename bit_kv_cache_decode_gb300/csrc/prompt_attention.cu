@@ -16,9 +16,10 @@
 // Warps: 0-3 and 4-7 rows of the two tiles, 8 loads, 9 issues the products, 10 looks at values that are not finite,
 // 11 finds the work, 12-15 write the results: the row threads are at the next item's weights by then.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
-// Measured: 32,769 tokens, 32 query and 8 key heads, 5.3 ms, 2 prompts of 8,192 with 64 and 8, 1.27 ms (1.66 and 1.69 PFLOP/s of
-// products that count; bound by the tensor pipe); 64 prompts of 1-901 tokens 156 us (0.91 PFLOP/s: blocks on the diagonal, half of
-// them masked, and the chain S, weights, O at an item's ends); one of 777 tokens 18 us (a CTA's chain of seven blocks, and the launch).
+// Measured: 32,769 tokens, 32 query and 8 key heads, 5.1 to 5.3 ms, 2 prompts of 8,192 with 64 and 8, 1.22 ms (1.71 and 1.76
+// PFLOP/s of products that count; bound by the tensor pipe); 64 prompts of 1-901 tokens 150 us (0.95 PFLOP/s: blocks on the diagonal,
+// half of them masked, and the chain S, weights, O at an item's ends); one of 777 tokens 18 us (a CTA's chain of seven blocks, and
+// the launch).
 //
 // Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
 // takes over CTAs that have not started yet (clusterlaunchcontrol), so that the loads and the first S of an item overlap
@@ -557,12 +558,8 @@ __device__ __forceinline__ bool load_item(const Ctx c, const Item& it, const CUt
 
 // ---- products ---------------------------------------------------------------------------------------------
 // One elected lane issues the eight (four) products of a batch from one set of operands: issued one by one in a loop, each
-// takes about 90 cycles instead of 64 (2 prompts of 8K: 1.35 ms, now 1.27). Four copies of the loop below, with tile and places
-// as constants, are 2 % faster on long prompts and 20 % slower on short ones (187 us instead of 156 for 64 of 1-901 tokens).
-struct MmaCount {
-  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, blocks = 0;
-  int checked = 0;                                 // blocks whose values were looked at
-};
+// takes about 90 cycles instead of 64 (2 prompts of 8K: 1.35 ms instead of 1.27). Both tiles in one loop body, places as numbers:
+// one copy of the code for each place is 20 % slower on short prompts, one for both tiles 10 % (8 and 4 % on long ones).
 // Eight products over 128 channels, A and B in shared memory: one elected lane issues them all (see umma_warp).
 __device__ __forceinline__ void umma_channels(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
   asm volatile(
@@ -603,51 +600,105 @@ __device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint32_t b_l
       "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-__device__ __forceinline__ bool mma_item(const Ctx c, const Item& it, int tokens, int items, MmaCount& k) {
-  const int n0 = (c.seen(it, 0, tokens) + kSub - 1) / kSub, n1 = (c.seen(it, 1, tokens) + kSub - 1) / kSub;
-  const int blocks = (max(n0, n1) + 1) / 2, checked = it.q0 / kBlock;   // from here on values may have to be looked at
+// Whether a barrier's phase is over, without waiting as a try does.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// What the products need of an item.
+struct Work {
+  int n0, n1, blocks, checked;                     // 64-token groups of the tiles, blocks, the first block to look at
+  bool clean;
+  __device__ __forceinline__ Work(const Ctx& c, const Item& it, int tokens)
+      : n0((c.seen(it, 0, tokens) + kSub - 1) / kSub), n1((c.seen(it, 1, tokens) + kSub - 1) / kSub),
+        blocks((max(n0, n1) + 1) / 2), checked(it.q0 / kBlock), clean(it.clean) {}
+};
+// In each step and for each tile, O of a block and S of the next one, which may be the next item's first: its logits are
+// then there when the rows' threads come to them. (Item by item: 64 prompts of 1-901 tokens 155 us instead of 150.)
+__device__ __forceinline__ bool mma_role(const Ctx c, int tokens) {
+  int half[2][2] = {{0, 0}, {0, 0}}, tiles[2] = {0, 0}, blocks = 0, looked = 0;   // what has gone before
+  Item it;
+  if (!c.wait(kBItem, 0)) return false;
+  if (!read_item(c, 0, it)) return true;
+  Work x(c, it, tokens), y = x;
+  bool ahead = false;                              // the item's first S have been issued
 #pragma unroll 1
-  for (int j = 0; j <= blocks; ++j)
+  for (int item = 0;; ++item) {
+    bool next = false;
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      const int n = t ? n1 : n0, b = k.blocks + j, pk = 2 * (b & 1), pv = 3 - pk;   // places of this block's keys, the last one's values
-      const int tiles = t ? k.tiles[1] : k.tiles[0], h0 = t ? k.half[1][0] : k.half[0][0], h1 = t ? k.half[1][1] : k.half[0][1];
-      const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
-#pragma unroll 1
-      for (int i = 2 * (j - 1); i >= 0 && i < min(n, 2 * j); ++i) {   // O of the block before
-        const int h = i & 1;
-        if (i == 0 && tiles > 0 && !c.wait(kBOFree + t, tiles - 1)) return false;
-        if (!c.wait(kBFull + pv, (b - 1) >> 1) || !c.wait(kBP + 2 * t + h, (h ? h1 : h0) + (i >> 1))) return false;
-        if (it.clean && j - 1 >= checked && h == 0 && (t == 0 || n0 <= i)) {   // the block's first product
-          c.arrive(kBGo);
-          if (!c.wait(kBCheck, k.checked++)) return false;
-        }
-        tc_fence_after();
-        umma_tokens(to, ts + 64 * h, desc_lo(c.base + kOffRing + pv * kTileBytes + h * kSub * 128, kHalfBytes), desc_hi(1024, true),
-                    kIdescO, i > 0);
-        umma_commit_warp(c.bar(kBO + 2 * t + h));
-      }
-      if (j > 0 && t == 1) umma_commit_warp(c.bar(kBEmpty + pv));   // both tiles are done with the values
-      if (j == 0 && !c.wait(kBQ + t, items)) return false;   // also of a tile without rows: its place is filled again
-      if (2 * j < n) {                             // S of this one
-        if (!c.wait(kBFull + pk, b >> 1)) return false;
-        tc_fence_after();
-        umma_channels(ts, desc_lo(c.base + kOffQ + t * kTileBytes, 16), desc_lo(c.base + kOffRing + pk * kTileBytes, 16),
-                      desc_hi(1024, true), kIdescS);
-        umma_commit_warp(c.bar(kBS + t));
-      }
-      if (j < blocks && t == 1) umma_commit_warp(c.bar(kBEmpty + pk));
-      if (j == blocks - 1) umma_commit_warp(c.bar(kBQFree + t));   // the tile's last S
-    }
-  k.blocks += blocks;
+    for (int j = ahead; j <= x.blocks; ++j)
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int n = t ? n1 : n0;
-    k.half[t][0] += (n + 1) / 2;
-    k.half[t][1] += n / 2;
-    k.tiles[t] += n > 0;
+      for (int t = 0; t < 2; ++t) {
+        const int b = blocks + j, pk = 2 * (b & 1), pv = 3 - pk;   // places of this block's keys, the last one's values
+        const uint32_t ts = c.tmem + kColS + 128 * t, to = c.tmem + kColO + 128 * t;
+        if (j > 0) {                               // O of the block before
+          // both tiles' wait at once: a wait that is over costs 64 cycles, which the few products in the queue do not cover
+          if (t == 0 && !c.wait(kBFull + pv, (b - 1) >> 1)) return false;
+#pragma unroll 1
+          for (int i = 2 * (j - 1); i < min(t ? x.n1 : x.n0, 2 * j); ++i) {
+            const int h = i & 1;
+            if (i == 0 && tiles[t] > 0 && !c.wait(kBOFree + t, tiles[t] - 1)) return false;
+            if (!c.wait(kBP + 2 * t + h, (h ? half[t][1] : half[t][0]) + (i >> 1))) return false;
+            if (x.clean && j - 1 >= x.checked && h == 0 && (t == 0 || x.n0 <= i)) {   // the block's first product
+              c.arrive(kBGo);
+              if (!c.wait(kBCheck, looked++)) return false;
+            }
+            tc_fence_after();
+            umma_tokens(to, ts + 64 * h, desc_lo(c.base + kOffRing + pv * kTileBytes + h * kSub * 128, kHalfBytes),
+                        desc_hi(1024, true), kIdescO, i > 0);
+            umma_commit_warp(c.bar(kBO + 2 * t + h));
+          }
+          if (t == 1) umma_commit_warp(c.bar(kBEmpty + pv));   // both tiles are done with the values
+        }
+        int n = t ? x.n1 : x.n0, at = j, last = x.blocks - 1;   // S of block `at`
+        if (j == x.blocks) {
+          if (t == 0) {                            // not waited for: there may be no item until this one's results are known
+            const int slot = (item + 1) % kItems;
+            next = __all_sync(0xffffffffu, mbar_done(c.bar(kBItem + slot), (uint32_t)((item + 1) / kItems) & 1u)) &&
+                   read_item(c, slot, it);
+            if (next) y = Work(c, it, tokens);
+          }
+          if (!next) continue;
+          n = t ? y.n1 : y.n0;
+          at = 0;
+          last = y.blocks - 1;
+        }
+        // Q is waited for also by a tile without rows: its place is filled again
+        if (at == 0 && !c.wait(kBQ + t, item + (j > 0))) return false;
+        if (t == 0 && !c.wait(kBFull + pk, b >> 1)) return false;
+        if (2 * at < n) {
+          tc_fence_after();
+          umma_channels(ts, desc_lo(c.base + kOffQ + t * kTileBytes, 16), desc_lo(c.base + kOffRing + pk * kTileBytes, 16),
+                        desc_hi(1024, true), kIdescS);
+          umma_commit_warp(c.bar(kBS + t));
+        }
+        if (t == 1) umma_commit_warp(c.bar(kBEmpty + pk));
+        if (at == last) umma_commit_warp(c.bar(kBQFree + t));   // the tile's last S
+      }
+    blocks += x.blocks;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int n = t ? x.n1 : x.n0;
+      half[t][0] += (n + 1) / 2;
+      half[t][1] += n / 2;
+      tiles[t] += n > 0;
+    }
+    c.arrive(kBItemFree + item % kItems);
+    ahead = next;
+    if (next) {
+      x = y;
+      continue;
+    }
+    const int slot = (item + 1) % kItems;
+    if (!c.wait(kBItem + slot, (item + 1) / kItems)) return false;
+    if (!read_item(c, slot, it)) return true;
+    x = Work(c, it, tokens);
   }
-  return true;
 }
 
 template <bool FP32>
@@ -694,17 +745,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       c.arrive(kBItemFree + slot);
     }
   } else if (ok && w == kMmaWarp) {
-    MmaCount products;
-#pragma unroll 1
-    for (int i = 0;; ++i) {
-      const int slot = i % kItems;
-      Item it;
-      ok = c.wait(kBItem + slot, i / kItems);
-      if (!ok || !read_item(c, slot, it)) break;
-      ok = mma_item(c, it, tokens, i, products);
-      if (!ok) break;
-      c.arrive(kBItemFree + slot);
-    }
+    ok = mma_role(c, tokens);
   } else if (ok && w == kCheckWarp) {
     int checked = 0, seen_blocks = 0;
 #pragma unroll 1
