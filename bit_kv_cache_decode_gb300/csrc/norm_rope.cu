@@ -9,8 +9,13 @@
 // are computed once per CTA and token into shared memory and serve all heads. Everything between the load and the one
 // rounding at the store is float32. A row is read once and written once: bound by memory.
 //
+// Measured, 128 channels, all turned in halves, bf16: 32,769 tokens x (64 + 8) heads, 1.208 GB, 197 us (6.1 TB/s, 92 % of the
+// copy rate); one token 4.2 us in a graph.
+//
 // Gradient: the weights' sums are held in registers over all rows of a CTA, which walks tokens of q or of k; CTAs'
 // partial sums go to the workspace and are added in a fixed order by a second kernel, so results do not depend on timing.
+// Registers allow two CTAs an SM, too few loads to fill the memory's latency: rows come by asynchronous copies, two rows ahead.
+// 32,769 tokens x (32 + 8) heads, 1.007 GB: 169 to 173 us (5.9 TB/s, 88 %; 62 % of the issue slots); 301 tokens 7.6 us in a graph.
 #include <algorithm>
 #include <mutex>
 #include <set>
