@@ -134,6 +134,7 @@ int check_norm(const oscar_head_norm* n, int dtype) {
   const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;
   return (reinterpret_cast<uintptr_t>(n->q_weight) | reinterpret_cast<uintptr_t>(n->k_weight)) % size ? OSCAR_ERR_INVALID_ARG : OSCAR_OK;
 }
+constexpr int64_t kMostPromptHeads = 1 << 24;      // prompts times key heads of a call
 // a raw step's rows and rotation, as the prologue takes them
 int check_raw(const oscar_cache* c, int B, const oscar_raw_step* x, bool prepare, RawStep* raw) {
   if (!c || !x || !x->rotary || B < 0) return OSCAR_ERR_INVALID_ARG;
@@ -559,6 +560,8 @@ int oscar_prompt_attention(oscar_cache* c, int B, const oscar_heads* q, const os
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return OSCAR_ERR_INVALID_ARG;
   if (c->prompt_rc != OSCAR_OK) return c->prompt_rc;
   if (B == 0 || total_tokens == 0) return OSCAR_OK;
+  // a CTA passes over empty prompts one by one while its loads wait, and waits are bounded in time
+  if ((int64_t)B * c->lay.num_kv_heads > kMostPromptHeads) return OSCAR_ERR_UNSUPPORTED;
   if (!q || !k || !v || !cu_seqlens || !out || !aligned16(out) || reinterpret_cast<uintptr_t>(lse) % sizeof(float))
     return OSCAR_ERR_INVALID_ARG;
   oscar_heads x[3] = {*q, *k, *v};

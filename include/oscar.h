@@ -253,7 +253,8 @@ typedef struct oscar_heads {
  * such prompts may be left unwritten. A NaN or infinity in k or v reaches no rows but those that attend to it, one in q no
  * row but its own; a row of out that is not finite raises NONFINITE. All inputs may come from the kernel just before; calls
  * may overlap. Errors: INVALID_ARG (B or total_tokens < 0, null pointers, strides that are not positive multiples of 8,
- * alignment, out_dtype, sm_scale), UNSUPPORTED (more than 2^31 - 1 tiles), CUDA. */
+ * alignment, out_dtype, sm_scale), UNSUPPORTED (more than 2^31 - 1 tiles, or than 2^24 prompts
+ * times kv heads), CUDA. */
 int oscar_prompt_attention(oscar_cache* cache, int B, const oscar_heads* q, const oscar_heads* k, const oscar_heads* v,
                            const int32_t* cu_seqlens, int total_tokens, float sm_scale, void* out, int out_dtype,
                            float* lse, void* stream);

@@ -244,3 +244,17 @@ def test_more_prompts_than_a_search_holds():
     out = cache.prompt_attention(q, k, v, cu, SM)
     C.check(out, None, q, k, v, lens, cu[:-1], SM)
     assert cache.get_status() == 0
+
+
+def test_more_prompts_than_a_call_takes():
+    # the most prompts (times key heads) that a call takes, all but four of them empty, and one more
+    q, k, v = rows(14, 300, 64, 64)
+    cache, most = cache_of(64, 64), 2 ** 24 // 64
+    cu = torch.zeros(most + 2, dtype=torch.int32, device=DEV)
+    cu[7:], cu[40_000:], cu[200_000:], cu[most:] = 1, 130, 131, 300
+    out = cache.prompt_attention(q, k, v, cu[:-1], SM)
+    lens = [1, 129, 1, 169]
+    C.check(out, None, q, k, v, lens, [0, 1, 130, 131], SM)
+    assert cache.get_status() == 0
+    with pytest.raises(osc.OscarError):
+        cache.prompt_attention(q, k, v, cu, SM)
