@@ -32,7 +32,7 @@
 // channels a lane; the sum of squares is three shuffles, a pair's partner comes through shared memory. The results are
 // what the rest of the kernel takes for q and k, and the queries are written out for the kernels behind. The angles
 // (64 of them) are the same for all heads of a request. Bound by latency (loads, two barriers, sums, stores): one request
-// 3.0 us in a graph, 256 requests x 8 heads 16 us.
+// 3.1 us in a graph, 256 requests x 8 heads 16 us.
 #include "kernels.cuh"
 #include "rope.cuh"
 #include "rotate.cuh"
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
   int L_old = 0;
   bool demote = false;
   int slot = 0, spage = -1, hh = 0, hpage = -1;
-  if (k != nullptr) L_old = __ldcg(seq_lens_before + b);   // L2 reads: nothing older may sit in this SM's L1
-  // Raw rows are waited for first, so that their loads and those that follow from the length are in flight together.
+  if (!RAW && k != nullptr) L_old = __ldcg(seq_lens_before + b);   // L2 reads: nothing older may sit in this SM's L1
+  // With raw rows everything waits, and all loads but those that follow from the length are in flight together: the kernel
+  // before may be the one that counts the requests' lengths up.
   // Rows 0 .. gq - 1: queries, row gq: the new key; four rows a warp.
   const bool raw_k = RAW && kind == OSCAR_KIND_K;
   const int rrow = tid >> 3, rl = tid & 7;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
   if constexpr (RAW) {
     pdl_wait();
     pdl_launch_dependents();
+    L_old = __ldcg(seq_lens_before + b);
     if (rlive) {
       const __nv_bfloat16* src = rq ? q + b * raw.q_row + (h * gq + rrow) * kD : k + b * raw.k_row + h * kD;
       const __nv_bfloat16* wt = rq ? raw.qw : raw.kw;

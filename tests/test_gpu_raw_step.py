@@ -209,3 +209,39 @@ def test_refusals():
     empty = dict(q=q[:0], k=k[:0], v=v[:0], seq_lens_before=np.zeros(0, np.int32), hist_pt=hist[:0], bf16_pt=bf[:0])
     assert a.append_kv_rope(**{**good, **empty}).shape == (0, 8, 128)
     assert a.decode_step_rope(**{**good, **empty}, sm_scale=SM).shape == (0, 8, 128)
+
+
+def test_lengths_from_the_kernel_just_before():
+    # each step's lengths and tables come from kernels right in front of it, in a graph that is replayed
+    lens, hkv, gq, steps = [300, 63, 318, 1000], 2, 4, 6
+    a, b, hist, bf = pair([n + steps for n in lens], hkv, gq, 0, 87, algo=1)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = [raw(g, 4, 8, hkv) for _ in range(steps)]
+    plan, start = osc.RopePlan(128), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    hist, bf = (torch.as_tensor(t, dtype=torch.int32, device=DEV) for t in (hist, bf))
+    now, tables = start.clone(), torch.zeros_like(bf)
+    before = a.pool.clone()
+
+    def run():
+        outs = []
+        for q, k, v in x:
+            torch.add(bf, 0, out=tables)
+            outs.append(a.decode_step_rope(0, plan, q, k, v, now, hist, tables, SM, out_dtype=osc.OUT_FP32))
+            torch.add(now, 1, out=now)
+            tables.fill_(-1)
+        return outs
+
+    want = []
+    for i, (q, k, v) in enumerate(x):
+        torch.cuda.synchronize()
+        want.append(b.decode_step_rope(0, plan, q, k, v, start + i, hist, bf, SM, out_dtype=osc.OUT_FP32))
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for _ in range(20):
+        a.pool.copy_(before)
+        now.copy_(start)
+        graph.replay()
+        assert all(torch.equal(p, r) for p, r in zip(outs, want)) and torch.equal(a.pool, b.pool)
+    assert a.get_status() == 0 and b.get_status() == 0
