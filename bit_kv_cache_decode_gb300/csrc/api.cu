@@ -832,8 +832,8 @@ int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
 int oscar_rope_axes(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
                     const int32_t* positions, const oscar_rotary* rotary, int inverse, void* stream) {
   oscar_rope_tensor t[2] = {};
-  if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
   if (inverse != 0 && inverse != 1) return OSCAR_ERR_INVALID_ARG;
+  if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
   if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
   if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
   return launch_rope(t[0], t[1], N, head_dim, dtype, positions, *rotary, inverse, static_cast<cudaStream_t>(stream));
