@@ -468,10 +468,12 @@ class OscarCache:
             if x is None and not rows:   # no queries: k and v are appended
                 rows.append(0)
                 continue
-            if x is None or x.dtype is not _bf16 or x.get_device() != dev or x.shape != (B, h, d) or x.stride(2) != 1 or \
-                    (h > 1 and x.stride(1) != d):
+            if x is None or x.dtype is not _bf16 or x.get_device() != dev or x.shape != (B, h, d):
                 raise OscarError(ERR_INVALID_ARG, what)
-            rows.append(x.stride(0) if B > 1 else h * d)
+            row, head, channel = x.stride()
+            if channel != 1 or (h > 1 and head != d):
+                raise OscarError(ERR_INVALID_ARG, what)
+            rows.append(row if B > 1 else h * d)
         if q is not None:
             if q_out is None:
                 q_out = _empty((B, heads[0], d), dtype=_bf16, device=dev)
@@ -815,15 +817,18 @@ def _rows(pairs, dtype, n: int, dim: int, dev: int, what: str):
             args.append(RopeTensor())
             outs.append(None)
             continue
+        shape = x.shape                            # asked for once: a tensor's attribute costs 0.1 us
+        if x.dtype is not dtype or x.get_device() != dev or len(shape) != 3:
+            raise OscarError(ERR_INVALID_ARG, what)
+        tokens, heads, channels = shape
         if out is None:
-            out = _empty(x.shape, dtype=dtype, device=dev)
-        if x.dtype is not dtype or out.dtype is not dtype or x.get_device() != dev or out.get_device() != dev or \
-                x.dim() != 3 or x.shape != out.shape or x.shape[0] != n or x.shape[2] != dim:
+            out = _empty(shape, dtype=dtype, device=dev)
+        elif out.dtype is not dtype or out.get_device() != dev or out.shape != shape:
             raise OscarError(ERR_INVALID_ARG, what)
         (it, ih, ic), (ot, oh, oc) = x.stride(), out.stride()
-        if dim > 1 and (ic != 1 or oc != 1):
+        if tokens != n or channels != dim or (dim > 1 and (ic != 1 or oc != 1)):
             raise OscarError(ERR_INVALID_ARG, what)
-        args.append(RopeTensor(x.data_ptr(), out.data_ptr(), it, ih, ot, oh, x.shape[1]))
+        args.append(RopeTensor(x.data_ptr(), out.data_ptr(), it, ih, ot, oh, heads))
         outs.append(out)
     return args, outs
 
@@ -909,19 +914,28 @@ def norm_rope_backward(plan: RopePlan, q, k, positions, grad_q, grad_k, q_weight
         if g is None:
             grads.append(RopeTensor())
             continue
-        token, head, channel = g.stride() if g.dim() == 3 else (0, 0, 0)
-        if g.dtype is not dtype or g.get_device() != dev or g.shape != x.shape or channel != 1:
+        rows = x.shape                             # three numbers: _rows
+        if g.dtype is not dtype or g.get_device() != dev or g.shape != rows:
             raise OscarError(ERR_INVALID_ARG, what)
-        grads.append(RopeTensor(g.data_ptr(), None, token, head, 0, 0, x.shape[1]))
+        token, head, channel = g.stride()
+        if channel != 1:
+            raise OscarError(ERR_INVALID_ARG, what)
+        grads.append(RopeTensor(g.data_ptr(), None, token, head, 0, 0, rows[1]))
     dqw = dkw = ws = None
+    ws_bytes = 0
     if weight_grads:
         dqw, dkw = _empty(dim, dtype=_f32, device=dev), _empty(dim, dtype=_f32, device=dev)
-        ws = _empty(norm_rope_workspace_bytes(dim), dtype=_u8, device=dev) if workspace is None else workspace
-        if ws.get_device() != dev or not ws.is_contiguous():
-            raise OscarError(ERR_INVALID_ARG, what)
+        if workspace is None:
+            ws_bytes = norm_rope_workspace_bytes(dim)
+            ws = _empty(ws_bytes, dtype=_u8, device=dev)
+        else:
+            ws, ws_bytes = workspace, workspace.nbytes
+            if ws.get_device() != dev or not ws.is_contiguous():
+                raise OscarError(ERR_INVALID_ARG, what)
     _check(_lib.oscar_norm_rope_backward(args[0], args[1], grads[0], grads[1], n, dim, code, pos.data_ptr(),
-                                         plan.rotary(layout), norm, _ptr(dqw), _ptr(dkw), _ptr(ws),
-                                         0 if ws is None else ws.nbytes, st), what)
+                                         plan.rotary(layout), norm, None if dqw is None else dqw.data_ptr(),
+                                         None if dkw is None else dkw.data_ptr(), None if ws is None else ws.data_ptr(),
+                                         ws_bytes, st), what)
     return outs[0], outs[1], dqw, dkw
 
 
