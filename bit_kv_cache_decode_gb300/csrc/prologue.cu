@@ -32,7 +32,7 @@
 // channels a lane; the sum of squares is three shuffles, a pair's partner comes through shared memory. The results are
 // what the rest of the kernel takes for q and k, and the queries are written out for the kernels behind. The angles
 // (64 of them) are the same for all heads of a request. Bound by latency (loads, two barriers, sums, stores): one request
-// 3.1 us in a graph, 256 requests x 8 heads 16 us.
+// 2.7 us in a graph, 256 requests x 8 heads 11.9 us.
 #include "kernels.cuh"
 #include "rope.cuh"
 #include "rotate.cuh"
@@ -49,8 +49,9 @@ __device__ __forceinline__ bool valid_page(int p, int n) { return p >= 0 && p < 
 constexpr int kTileFloats = 16 * kTileStride;
 
 // What a launch does: rows as they come; raw rows; raw rows, with the rotation's fragments read from L2 (and L1, which CTAs
-// of one head share) when they are needed. The last takes 64 KB less of shared memory, so that more CTAs fit an SM.
-enum { kPlain, kRaw, kRawLate };
+// of one head share) when they are needed; the same without a decode behind it. The last two take 64 KB less of shared
+// memory, so that more CTAs fit an SM.
+enum { kPlain, kRaw, kRawLate, kRawAppend };
 
 // Norm and rotation of a row by eight lanes: lane l has channels 8 l .. and 64 + 8 l .. in x, their weights in w. buf: a float
 // row of the group's own.
@@ -108,14 +109,18 @@ __device__ __forceinline__ void widen8(const uint4& u, float* f) {
   }
 }
 
+// CTAs an SM, and k-blocks of fragments in flight, of appends without a decode: 256 requests x 8 heads 11.9 us, 36.2 where all
+// demote (4 and 8: 14.0, 39.5; 6 and 2: 12.8, 36.5); one request 2.7 and 3.1 (2.7, 2.9; 3.1, 3.3).
+constexpr int kAppendCtas = 5, kAppendAhead = 2;
 template <int MODE>
-__global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
+__global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawAppend ? kAppendCtas : MODE == kRawLate ? 4 : 1)
     k_step_prologue(LayerView lv, DecodeWorkspace ws, const __nv_bfloat16* __restrict__ q,
                     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                     const int* __restrict__ seq_lens_before, const int* __restrict__ hist_pt, int max_hist_pages,
                     const int* __restrict__ bf16_pt, float scale_log2, RawStep raw) {
   TimelineSpan timeline_span(lv, k != nullptr ? kTlAppend : kTlQprep);
-  constexpr bool RAW = MODE != kPlain, kLate = MODE == kRawLate;
+  constexpr int kTokenWarp = kPrologueWarps - 2, kRowWarps = 3;   // the raw rows' warps: 4 rows each, 9 at most
+  constexpr bool RAW = MODE != kPlain, kLate = MODE == kRawLate || MODE == kRawAppend;
   extern __shared__ __align__(128) float smem[];
   uint32_t* frag_s = reinterpret_cast<uint32_t*>(smem);
   float* rows = smem + (kLate ? 0 : kRFragWords);    // [16][kTileStride]
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int gq = lv.hq / lv.hkv;
   const float* prm = lv.params + (size_t)h * kParamFloats;
-  const bool do_q = q != nullptr && kind == OSCAR_KIND_K && (!RAW || raw.prepare);
+  const bool do_q = MODE != kRawAppend && q != nullptr && kind == OSCAR_KIND_K && (!RAW || raw.prepare);
   const bool rotate = (kind == OSCAR_KIND_K) || lv.v_explicit;
   // The rotation fragments do not depend on the kernel before: they are requested before the wait below,
   // while that kernel still runs (this grid is scheduled early). Every CTA that may rotate requests them.
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
         }
       }
     }
-    if (RAW && !raw_k && w == kPrologueWarps - 2) {
+    if (RAW && !raw_k && w == kTokenWarp) {
       const uint2 x = reinterpret_cast<const uint2*>(v + b * raw.v_row + h * kD)[lane];
       rx[0].x = x.x;
       rx[0].y = x.y;
@@ -206,6 +211,13 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
       }
     }
   }
+  // An append that demotes nothing: the warps with raw rows, and the one that writes the new token.
+  const bool light = MODE == kRawAppend && !demote;
+  if (light && w != kTokenWarp && (kind != OSCAR_KIND_K || w >= kRowWarps)) return;
+  auto sync = [&] {
+    if (!light) __syncthreads();
+    else if (kind == OSCAR_KIND_K) asm volatile("bar.sync 2, %0;" ::"n"(32 * (kRowWarps + 1)) : "memory");
+  };
   // The next layer's prologue needs its rotation fragments from L2 about one layer's decode from now:
   // ask for them now, with the same evict-last priority, so the page stream of this layer does not
   // leave them to be fetched from HBM on the next critical path.
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
         if (low && tid == 0) flag(lv.status, OSCAR_STATUS_BAD_SEQLEN);
         cs[tid] = rope_turn(raw.r, rpos, tid, 1.f);
       }
-      __syncthreads();
+      sync();
       if (4 * w < gq + 1) {                          // all lanes of a warp take part
         float x[16], wt[16];
         widen8(rx[0], x);
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
     if (bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w))
       flag(lv.status, OSCAR_STATUS_NONFINITE);
   }
-  if (!RAW || !do_q || r == 0 || r > gq) {       // rows 1 .. gq of raw queries are there
+  if (!light && (!RAW || !do_q || r == 0 || r > gq)) {   // rows 1 .. gq of raw queries are there
     const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
     float4* dst = reinterpret_cast<float4*>(rows + r * kTileStride + 8 * c8);
     dst[0] = make_float4(__uint_as_float(wds[0] << 16), __uint_as_float(wds[0] & 0xffff0000u),
@@ -288,10 +300,10 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
     dst[1] = make_float4(__uint_as_float(wds[2] << 16), __uint_as_float(wds[2] & 0xffff0000u),
                          __uint_as_float(wds[3] << 16), __uint_as_float(wds[3] & 0xffff0000u));
   }
-  if (tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
-  __syncthreads();                                   // barriers initialised, tile staged, old slot read
+  if (!light && tid < kD) tau_s[tid] = prm[(kind == OSCAR_KIND_K ? kTauKOff : kTauVOff) + tid];
+  sync();                                            // barriers initialised, tile staged, old slot read
   if (kLate) {
-    if (need_frags) rotate_tile16_l2(reinterpret_cast<const uint32_t*>(prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff)), rows);
+    if (need_frags) rotate_tile16_l2<MODE == kRawAppend ? kAppendAhead : 8>(reinterpret_cast<const uint32_t*>(prm + (kind == OSCAR_KIND_K ? kRKFragOff : kRVFragOff)), rows);
   } else if (need_frags && !rotate_tile16(frag_s, rows, bars)) {
     if (tid == 0) flag(lv.status, OSCAR_STATUS_TIMEOUT);
     mbar_wait(bars + 8 * w, 0);                      // one more bounded wait for the copies in flight
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawLate ? 4 : 1)
     qprep_finish(lv, ws, rows + kTileStride, kTileStride, sig, b, h, scale_log2, kQWarps);
   }
   // --- the new token into its slot (the old row was staged before the first barrier) ---
-  if (k == nullptr || L_old < 0 || w != kPrologueWarps - 2) return;
+  if (k == nullptr || L_old < 0 || w != kTokenWarp) return;
   const int pos = L_old, at = pos < lv.sink ? pos : lv.sink + (pos - lv.sink) % lv.recent, row = at % kP;
   const int page = RAW ? new_page : bf16_pt[b * bf16_per_req + at / kP];
   if (!valid_page(page, lv.n_bf16)) {
@@ -351,7 +363,7 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(B, lv.hkv, k != nullptr ? 2 : 1);   // query-only: the K CTAs
   cfg.blockDim = dim3(kPrologueWarps * 32);
-  // An append of raw rows rotates demoted rows only (256 requests x 8 heads, none demoted: 16 us; with every CTA asking for
+  // An append of raw rows rotates demoted rows only (256 requests x 8 heads, none demoted: 12 us; with every CTA asking for
   // the fragments 40). A step's queries take them from L2 where there are more than four CTAs for each of 152 SMs: decode
   // steps of 256 requests x 8 heads 140 us (bulk copies: 158), of 64 38.1 (41.5), of 32 24.1 (23.8), of 8 13.5 (13.0).
   const bool late = raw != nullptr && (!raw->prepare || 2ll * B * lv.hkv > 4 * 152);
@@ -359,7 +371,9 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = after_all ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, late ? k_step_prologue<kRawLate> : raw ? k_step_prologue<kRaw> : k_step_prologue<kPlain>, lv, ws,
+  const auto kernel = raw == nullptr ? k_step_prologue<kPlain> : !raw->prepare ? k_step_prologue<kRawAppend>
+                      : late ? k_step_prologue<kRawLate> : k_step_prologue<kRaw>;
+  return cudaLaunchKernelEx(&cfg, kernel, lv, ws,
                             static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
                             static_cast<const __nv_bfloat16*>(v), seq_lens_before, hist_pt, max_hist_pages, bf16_pt,
                             sm_scale * kLog2e, raw ? *raw : RawStep{}) == cudaSuccess
@@ -368,7 +382,7 @@ int launch_prologue(const LayerView& lv, const DecodeWorkspace& ws, int B, const
 }
 
 int configure_prologue_kernel() {
-  for (auto fn : {k_step_prologue<kPlain>, k_step_prologue<kRaw>, k_step_prologue<kRawLate>}) {
+  for (auto fn : {k_step_prologue<kPlain>, k_step_prologue<kRaw>, k_step_prologue<kRawLate>, k_step_prologue<kRawAppend>}) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrologueSmem) != cudaSuccess)
       return OSCAR_ERR_CUDA;
     if (int rc = set_max_shared_carveout(reinterpret_cast<const void*>(fn)); rc != OSCAR_OK) return rc;

@@ -118,27 +118,31 @@ __device__ __forceinline__ bool rotate_tile16(const uint32_t* frag_s, float* row
   return true;
 }
 
-// The same with the fragments read from global memory (8 warps): all of them in flight, then the products.
+// The same with the fragments read from global memory (8 warps): AHEAD k-blocks of them in flight, then their products.
+template <int AHEAD>
 __device__ __forceinline__ void rotate_tile16_l2(const uint32_t* frag, float* rows) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint4 f[8][2];
-#pragma unroll
-  for (int kb = 0; kb < 8; ++kb)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) f[kb][j] = __ldg(reinterpret_cast<const uint4*>(frag + ((kb * 16 + 2 * w + j) * 32 + lane) * 4));
   float acc[2][4] = {};
 #pragma unroll
-  for (int kb = 0; kb < 8; ++kb) {
-    const float* r0 = rows + g * kTileStride + 16 * kb + 2 * t;
-    const float* r8 = rows + (g + 8) * kTileStride + 16 * kb + 2 * t;
-    const uint32_t a0 = f16x2_of(r0), a1 = f16x2_of(r8), a2 = f16x2_of(r0 + 8), a3 = f16x2_of(r8 + 8);
+  for (int k0 = 0; k0 < 8; k0 += AHEAD) {
+    uint4 f[AHEAD][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float d[4];
-      qp_mma(d, a0, a1, a2, a3, f[kb][j].x, f[kb][j].y, true);    // x R_hi
-      qp_mma(d, a0, a1, a2, a3, f[kb][j].z, f[kb][j].w, false);   // + x R_lo
+    for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+      for (int j = 0; j < 2; ++j) f[k][j] = __ldg(reinterpret_cast<const uint4*>(frag + (((k0 + k) * 16 + 2 * w + j) * 32 + lane) * 4));
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float* r0 = rows + g * kTileStride + 16 * (k0 + k) + 2 * t;
+      const float* r8 = rows + (g + 8) * kTileStride + 16 * (k0 + k) + 2 * t;
+      const uint32_t a0 = f16x2_of(r0), a1 = f16x2_of(r8), a2 = f16x2_of(r0 + 8), a3 = f16x2_of(r8 + 8);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float d[4];
+        qp_mma(d, a0, a1, a2, a3, f[k][j].x, f[k][j].y, true);    // x R_hi
+        qp_mma(d, a0, a1, a2, a3, f[k][j].z, f[k][j].w, false);   // + x R_lo
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+      }
     }
   }
   __syncthreads();                                   // every warp has read its A rows
