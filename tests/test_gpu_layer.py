@@ -156,3 +156,50 @@ def test_gradient_of_the_rows_that_are_attended():
         size = (rx.abs() * tx.abs()).sum() + (rw.abs() * tw.abs()).sum()
         off = (bx * tx.abs()).sum() + (bw * tw.abs()).sum() + 1e-6 * size
         assert abs((dx.double().cpu() * tx).sum() + (dw.double().cpu() * tw).sum() - want) <= off
+
+
+def far(n, heads, g):
+    """Rows [n, heads, 128] of normal values, the last ones more than 2^32 bytes (and 2^31 elements) behind the first."""
+    step = (2 ** 31 // (n - 1) + 16) // 8 * 8
+    x = torch.empty((n - 1) * step + heads * 128, dtype=torch.bfloat16, device=DEV).as_strided((n, heads, 128), (step, 128, 1))
+    return x.copy_(torch.randn(n, heads, 128, generator=g, device=DEV))
+
+
+def test_rows_far_apart():
+    g = torch.Generator(device=DEV).manual_seed(8)
+    q, k, v, gq, gk = far(65, 4, g), far(65, 2, g), far(65, 2, g), far(65, 4, g), far(65, 2, g)
+    plan, pos = osc.RopePlan(128), torch.arange(65, dtype=torch.int32, device=DEV)
+    w = (1 + 0.3 * torch.randn(2, 128, generator=g, device=DEV)).bfloat16()
+    near = [x.contiguous() for x in (q, k, v, gq, gk)]
+    # the same bits as from rows side by side, which have their own tests
+    for a, b in zip(osc.norm_rope(plan, q, k, pos, w[0], w[1]), osc.norm_rope(plan, *near[:2], pos, w[0], w[1])):
+        assert torch.equal(a, b)
+    for a, b in zip(osc.norm_rope_backward(plan, q, k, pos, gq, gk, w[0], w[1]),
+                    osc.norm_rope_backward(plan, *near[:2], pos, *near[3:], w[0], w[1])):
+        assert torch.equal(a, b)
+    cache = osc.OscarCache(osc.CacheConfig(num_layers=1, num_kv_heads=2, num_q_heads=4, num_int2_pages=1, num_bf16_pages=325,
+                                           max_batch=65), device=DEV)
+    cu = torch.tensor([0, 65], dtype=torch.int32, device=DEV)
+    assert torch.equal(cache.prompt_attention(q, k, v, cu, SM), cache.prompt_attention(*near[:3], cu, SM))
+    bf = torch.arange(325, dtype=torch.int32, device=DEV)
+    hist = torch.full((65, 1), -1, dtype=torch.int32, device=DEV)
+    outs = []
+    for rows in ((q, k, v), near[:3]):
+        cache.pool.zero_()
+        out = cache.append_kv_rope(0, plan, *rows, pos, hist, bf, w[0], w[1])
+        outs.append((out, cache.pool.clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert cache.get_status() == 0
+
+
+def test_results_past_32_bits():
+    # 270,000 prompts of one token with 64 heads: results past 2^31 elements; a token that sees itself alone has its own value
+    n = 270_000
+    g = torch.Generator(device=DEV).manual_seed(9)
+    q = torch.empty(n, 64, 128, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    k, v = (torch.empty(n, 8, 128, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(2))
+    cache = osc.OscarCache(osc.CacheConfig(num_layers=1, num_kv_heads=8, num_q_heads=64, num_int2_pages=1, num_bf16_pages=5), device=DEV)
+    out = cache.prompt_attention(q, k, v, torch.arange(n + 1, dtype=torch.int32, device=DEV), SM)
+    assert cache.get_status() == 0
+    for h in range(8):
+        assert torch.equal(out[:, 8 * h:8 * h + 8], v[:, h:h + 1].expand(n, 8, 128))
