@@ -15,15 +15,16 @@
 //
 // Positions with several axes (time, height and width of images and video): each pair has its axis, and turns by the
 // token's position on it. The axes' positions and the pairs' axes are read by the CTA's angles alone, so the time is the
-// rows': 40,961 tokens x 40 heads x 128 bf16, 3 axes, all turned in halves (0.84 GB), 138 us (6.1 TB/s, 91 % of the copy rate).
+// rows': 40,961 tokens x 40 heads x 128 bf16, 3 axes, all turned in halves (0.84 GB), 129 us (6.5 TB/s, 98 % of the copy rate).
 //
 // Each (token, pair) angle is computed once per CTA into shared memory and serves all heads. A thread keeps
 // one unit of the head (16 bytes, or the 8 or 4 that the strides and the halves allow) and walks tokens and heads,
 // two units in flight; every element is read and written once, so the kernel is bound by memory. For 49,153 tokens
-// x 40 heads x 128 bf16 (1.007 GB): pairs layout 157 us (half of the head rotated; 6.42 TB/s, 95 % of the copy rate),
-// half layout 161 us (whole head). What carried it: streaming loads and stores (206 us with the default policy);
+// x 40 heads x 128 bf16 (1.007 GB): pairs layout 157 us (half of the head rotated; 6.40 TB/s, 96 % of the copy rate),
+// half layout 152 us (whole head; 6.61 TB/s). What carried it: streaming loads and stores (206 us with the default policy);
 // short CTAs of 8 tokens (32 tokens: 239 us); two units per thread (one: 166 us; four: 230 us, fewer threads fit);
-// 8 CTAs per SM for the pairs layout (6: 167 us) and 6 for the half layout, whose unit has two parts (8: 171 us);
+// 8 CTAs per SM for the pairs layout (6: 167 us) and 5 for the half layout, whose unit has two parts (6: 154.6 us); one unit
+// and 8 CTAs where half a head is turned in halves (26,214 tokens x 40 heads: 117 us, as whole heads 124);
 // narrower units rather than single elements, and 16 bytes for the channels behind them where those allow it (head 64, 24
 // channels rotated in halves: 99 us, all of it in 8-byte units 138 us, in elements 364 us).
 #include <algorithm>
@@ -42,31 +43,32 @@ struct RopeArgs {
   int inverse;
 };
 
-template <typename T, int V, int VP, bool HALF, bool WIDE>
-__global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a) {
-  __shared__ float2 table[kRopeTable];             // [token][pair]: (cos, sin) times the scale
+// Where a token's pair j lies among its (cos, sin), for units of PER pairs: two pairs (16 bytes) of all units side by side, then
+// the next two, so that threads of neighbouring units read without bank conflicts (pair by pair, 16,384 tokens x 40 heads x 256
+// in halves took 186 us instead of 109).
+template <int PER>
+__device__ __forceinline__ int slot(int j, int units) {
+  const int u = j / PER, e = j % PER;
+  return PER == 1 ? j : ((e >> 1) * units + u) * 2 + (e & 1);
+}
+
+// PART: half layout with channels behind the rotated ones
+template <typename T, int V, int VP, bool HALF, bool WIDE, bool PART>
+__global__ void __launch_bounds__(kRopeThreads, HALF && !PART ? 5 : 8) k_rope(RopeArgs a) {
+  __shared__ __align__(16) float2 table[kRopeTable];   // [token][slot of a pair]: (cos, sin) times the scale
   __shared__ int pos_s[kRopeTokens * kRopeAxes];
   const int rot = a.r.rot, half = rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.r.n - t0);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
-  if (HALF && a.r.n_axes == 1) {                   // written out: 49,153 tokens x 40 heads 160.6 us, as below 162.4 (pairs: 160.3, 158.8)
-    for (int i = tid; i < nt; i += nthr) pos_s[i * kRopeAxes] = a.r.positions[t0 + i];
-    __syncthreads();
-    for (int i = tid; i < nt * half; i += nthr) {
-      const int t = i / half, j = i - t * half;
-      const unsigned long long turn = (unsigned long long)(unsigned)pos_s[t * kRopeAxes] * a.r.turns[j];
-      float s, c;
-      sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-      table[i] = make_float2(c * a.r.scale, (a.inverse ? -s : s) * a.r.scale);
-    }
-  } else {
-    load_positions(a.r, t0, nt, pos_s, tid, nthr);
-    __syncthreads();
-    load_turns(a.r, nt, pos_s, a.inverse ? -1.f : 1.f, table, tid, nthr);
+  constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
+  const int rot_units = HALF ? half / V : rot / V;
+  load_positions(a.r, t0, nt, pos_s, tid, nthr);
+  __syncthreads();
+  for (int i = tid; i < nt * half; i += nthr) {
+    const int t = i / half, j = i - t * half;
+    table[t * half + slot<kPer>(j, rot_units)] = rope_turn(a.r, pos_s + t * kRopeAxes, j, a.inverse ? -1.f : 1.f);
   }
   __syncthreads();
-  constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
-  constexpr int kBatch = 2;                        // units a thread has in flight
-  const int rot_units = HALF ? half / V : rot / V;
+  constexpr int kBatch = PART ? 1 : 2;             // units a thread has in flight
   const int units = rot_units + (a.dim - rot) / VP;
   const int heads = a.q.heads + a.k.heads, items = nt * heads;
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
@@ -96,7 +98,16 @@ __global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a)
         if (rotary) {
           float2 cs[kPer];
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) cs[e] = table[tok[k] * half + u * kPer + e];
+          for (int e = 0; e < kPer; e += 2) {
+            const float2* at = table + tok[k] * half + slot<kPer>(u * kPer + e, rot_units);
+            if constexpr (kPer == 1) {
+              cs[e] = *at;
+            } else {
+              const float4 two = *reinterpret_cast<const float4*>(at);
+              cs[e] = make_float2(two.x, two.y);
+              cs[e + 1] = make_float2(two.z, two.w);
+            }
+          }
           x[k].turn(cs);
         }
         x[k].store(out[k], at, half, rotary);
@@ -105,8 +116,8 @@ __global__ void __launch_bounds__(kRopeThreads, HALF ? 6 : 8) k_rope(RopeArgs a)
   }
 }
 
-template <typename T, int V, int VP, bool HALF, bool WIDE>
-int launch_as(RopeArgs a, cudaStream_t st) {
+template <typename T, int V, int VP, bool HALF, bool WIDE, bool PART>
+int launch_with(RopeArgs a, cudaStream_t st) {
   const int rot = a.r.rot, half = rot / 2;
   const int units = (HALF ? half / V : rot / V) + (a.dim - rot) / VP;
   // four CTAs per SM and more while there are tokens for them (3,000 tokens x 40 heads: 12.2 us; two: 14.9, eight: 14.3)
@@ -117,8 +128,15 @@ int launch_as(RopeArgs a, cudaStream_t st) {
   const unsigned heads = a.q.heads + a.k.heads;
   a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
-  k_rope<T, V, VP, HALF, WIDE><<<(a.r.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
+  k_rope<T, V, VP, HALF, WIDE, PART><<<(a.r.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+template <typename T, int V, int VP, bool HALF, bool WIDE>
+int launch_as(const RopeArgs& a, cudaStream_t st) {
+  if constexpr (HALF)
+    if (a.r.rot < a.dim) return launch_with<T, V, VP, HALF, WIDE, true>(a, st);
+  return launch_with<T, V, VP, HALF, WIDE, false>(a, st);
 }
 
 // bytes: the widest access, of 16 at most, that every row, half and remainder starts on a multiple of; else elements.

@@ -35,16 +35,6 @@ __device__ __forceinline__ float2 rope_turn(const Rotary& r, const int* pos, int
   sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
   return make_float2(c * r.scale, s * sign * r.scale);
 }
-// the table of those, [token][pair]
-__device__ __forceinline__ void load_turns(const Rotary& r, int nt, const int* pos_s, float sign, float2* table, int tid,
-                                           int nthr) {
-  const int half = r.rot / 2;
-  for (int i = tid; i < nt * half; i += nthr) {
-    const int t = i / half, j = i - t * half;
-    table[i] = rope_turn(r, pos_s + t * kRopeAxes, j, sign);
-  }
-}
-
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f(float x) { return x; }
 template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
