@@ -128,6 +128,7 @@ int check_rows(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
   }
   return OSCAR_OK;
 }
+constexpr int64_t kMostRopeHeads = 1 << 30;        // of q and k together: rope.cu counts a CTA's rows in 32 bits
 constexpr int kMostNormHeads = 8192;               // norm_rope.cu divides row numbers by the heads in 32 bits
 int check_norm(const oscar_head_norm* n, int dtype) {
   if (!n || !(n->eps > 0.f) || !std::isfinite(n->eps)) return OSCAR_ERR_INVALID_ARG;
@@ -834,6 +835,7 @@ int oscar_rope_axes(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int 
   oscar_rope_tensor t[2] = {};
   if (inverse != 0 && inverse != 1) return OSCAR_ERR_INVALID_ARG;
   if (int rc = check_rows(q, k, N, head_dim, dtype, rotary, true, t); rc != OSCAR_OK) return rc;
+  if ((int64_t)t[0].heads + t[1].heads > kMostRopeHeads) return OSCAR_ERR_UNSUPPORTED;
   if (N == 0 || t[0].heads + t[1].heads == 0) return OSCAR_OK;
   if (!positions || !rotary->turns || !aligned8(rotary->turns)) return OSCAR_ERR_INVALID_ARG;
   return launch_rope(t[0], t[1], N, head_dim, dtype, positions, *rotary, inverse, static_cast<cudaStream_t>(stream));

@@ -39,7 +39,7 @@ struct RopeArgs {
   Rotary r;
   int dim;
   int tokens;                                      // tokens per CTA
-  unsigned per_head;                               // ceil(2^32 / heads), i / heads for i heads < 2^32; 0 for one head
+  unsigned per_head;                               // i / heads as the upper half of i times this; 0 for one head: i itself
   int inverse;
 };
 
@@ -125,8 +125,11 @@ int launch_with(RopeArgs a, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return OSCAR_ERR_CUDA;
   a.tokens = std::max(1, std::min(std::min(kRopeTable / half, kRopeTokens), a.r.n / (4 * sms)));
-  const unsigned heads = a.q.heads + a.k.heads;
-  a.per_head = heads == 1 ? 0u : (unsigned)((0x100000000ull + heads - 1) / heads);
+  // i / heads is the upper half of i ceil(2^32 / heads) while i heads <= 2^32: for all rows of a CTA's tokens, so many heads
+  // leave it fewer of them. A single token's rows are all its own: 1 gives 0 for each.
+  const unsigned long long heads = a.q.heads + a.k.heads;
+  a.tokens = (int)std::max(1ull, std::min((unsigned long long)a.tokens, 0x100000000ull / (heads * heads)));
+  a.per_head = heads == 1 ? 0u : a.tokens == 1 ? 1u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
   k_rope<T, V, VP, HALF, WIDE, PART><<<(a.r.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;

@@ -450,7 +450,8 @@ typedef struct oscar_rope_tensor {
  * float32, one rounding at the end.
  *  turns : device uint64 [rotary_dim / 2] from oscar_rope_turns, 8-byte aligned
  * Errors: INVALID_ARG (null pointers, N < 0, negative heads or strides, odd or too large rotary_dim, a bad dtype,
- * layout or scale), UNSUPPORTED (head_dim odd or above 512), CUDA. Works without a cache. */
+ * layout or scale), UNSUPPORTED (head_dim odd or above 512, more than 2^30 heads of q and k together), CUDA. Works without
+ * a cache. */
 int oscar_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, int head_dim, int dtype,
                const int32_t* positions, const uint64_t* turns, int rotary_dim, int layout, float scale, int inverse,
                void* stream);
