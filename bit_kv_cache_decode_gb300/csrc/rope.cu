@@ -23,8 +23,8 @@
 // x 40 heads x 128 bf16 (1.007 GB): pairs layout 157 us (half of the head rotated; 6.40 TB/s, 96 % of the copy rate),
 // half layout 152 us (whole head; 6.61 TB/s). What carried it: streaming loads and stores (206 us with the default policy);
 // short CTAs of 8 tokens (32 tokens: 239 us); two units per thread (one: 166 us; four: 230 us, fewer threads fit);
-// 8 CTAs per SM for the pairs layout (6: 167 us) and 5 for the half layout, whose unit has two parts (6: 154.6 us); one unit
-// and 8 CTAs where half a head is turned in halves (26,214 tokens x 40 heads: 117 us, as whole heads 124);
+// 8 CTAs per SM for the pairs layout (6: 167 us) and 5 for the half layout, whose unit has two parts (6: 154.6 us; where only
+// a part of a head is turned see launch_as);
 // narrower units rather than single elements, and 16 bytes for the channels behind them where those allow it (head 64, 24
 // channels rotated in halves: 99 us, all of it in 8-byte units 138 us, in elements 364 us).
 #include <algorithm>
@@ -52,34 +52,33 @@ __device__ __forceinline__ int slot(int j, int units) {
   return PER == 1 ? j : ((e >> 1) * units + u) * 2 + (e & 1);
 }
 
-// PART: half layout with channels behind the rotated ones
-template <typename T, int V, int VP, bool HALF, bool WIDE, bool PART>
-__global__ void __launch_bounds__(kRopeThreads, HALF && !PART ? 5 : 8) k_rope(RopeArgs a) {
+// BATCH: units a thread has in flight; CTAS: CTAs an SM
+template <typename T, int V, int VP, bool HALF, bool WIDE, int BATCH, int CTAS>
+__global__ void __launch_bounds__(kRopeThreads, CTAS) k_rope(RopeArgs a) {
   __shared__ __align__(16) float2 table[kRopeTable];   // [token][slot of a pair]: (cos, sin) times the scale
   __shared__ int pos_s[kRopeTokens * kRopeAxes];
   const int rot = a.r.rot, half = rot / 2, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.r.n - t0);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
   constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
   const int rot_units = HALF ? half / V : rot / V;
-  load_positions(a.r, t0, nt, pos_s, tid, nthr);
+  load_positions<HALF || sizeof(T) == 4>(a.r, t0, nt, pos_s, tid, nthr);
   __syncthreads();
   for (int i = tid; i < nt * half; i += nthr) {
     const int t = i / half, j = i - t * half;
     table[t * half + slot<kPer>(j, rot_units)] = rope_turn(a.r, pos_s + t * kRopeAxes, j, a.inverse ? -1.f : 1.f);
   }
   __syncthreads();
-  constexpr int kBatch = PART ? 1 : 2;             // units a thread has in flight
   const int units = rot_units + (a.dim - rot) / VP;
   const int heads = a.q.heads + a.k.heads, items = nt * heads;
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     const bool rotary = u < rot_units;
     const int at = rotary ? u * V : rot + (u - rot_units) * VP;
-    for (int i0 = threadIdx.y; i0 < items; i0 += kBatch * blockDim.y) {
-      Unit<T, V, VP, HALF, WIDE> x[kBatch];
-      T* out[kBatch];
-      int tok[kBatch];
+    for (int i0 = threadIdx.y; i0 < items; i0 += BATCH * blockDim.y) {
+      Unit<T, V, VP, HALF, WIDE> x[BATCH];
+      T* out[BATCH];
+      int tok[BATCH];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         const unsigned i = i0 + k * blockDim.y;    // (token, head): i = t heads + h
         const int t = a.per_head != 0u ? __umulhi(i, a.per_head) : i, h = (int)i - t * heads;
         const bool isq = h < a.q.heads;
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(kRopeThreads, HALF && !PART ? 5 : 8) k_rope(Ro
         if (out[k] != nullptr) x[k].load(in, at, half, rotary);
       }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         if (out[k] == nullptr) continue;
         if (rotary) {
           float2 cs[kPer];
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads, HALF && !PART ? 5 : 8) k_rope(Ro
   }
 }
 
-template <typename T, int V, int VP, bool HALF, bool WIDE, bool PART>
+template <typename T, int V, int VP, bool HALF, bool WIDE, int BATCH, int CTAS>
 int launch_with(RopeArgs a, cudaStream_t st) {
   const int rot = a.r.rot, half = rot / 2;
   const int units = (HALF ? half / V : rot / V) + (a.dim - rot) / VP;
@@ -131,15 +130,32 @@ int launch_with(RopeArgs a, cudaStream_t st) {
   a.tokens = (int)std::max(1ull, std::min((unsigned long long)a.tokens, 0x100000000ull / (heads * heads)));
   a.per_head = heads == 1 ? 0u : a.tokens == 1 ? 1u : (unsigned)((0x100000000ull + heads - 1) / heads);
   const int bx = std::min(units, kRopeThreads), by = std::max(1, std::min(kRopeThreads / bx, a.q.heads + a.k.heads));
-  k_rope<T, V, VP, HALF, WIDE, PART><<<(a.r.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
+  k_rope<T, V, VP, HALF, WIDE, BATCH, CTAS><<<(a.r.n - 1) / a.tokens + 1, dim3(bx, by), 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
+// Units in flight and CTAs an SM of the half layout where a part of a head is turned, whose threads do unequal work: one and 8
+// for rows of a power of two of bytes up to 512 (8,192 tokens x 40 heads x 128 float32, 64 turned: 60 us; two and 5: 74), for
+// 16 bits unless a quarter or less is turned (6,553 x 40 x 160, 80 turned: 35 us, 40; 10,922 x 40 x 96, 24 turned: 41, 37),
+// for other float32 rows while L2 holds them (2,400 x 24 x 160: 12.2 us; two and 6: 13.9). Beyond it two and 6 (6,553 x 40 x
+// 160, 80 turned: 60 us; one and 8: 65; two and 5: 74), and two and 5 for single elements (4,096 x 40 x 128 float32, 64
+// turned: 72 us; one and 8: 85).
 template <typename T, int V, int VP, bool HALF, bool WIDE>
 int launch_as(const RopeArgs& a, cudaStream_t st) {
-  if constexpr (HALF)
-    if (a.r.rot < a.dim) return launch_with<T, V, VP, HALF, WIDE, true>(a, st);
-  return launch_with<T, V, VP, HALF, WIDE, false>(a, st);
+  if constexpr (!HALF) {
+    return launch_with<T, V, VP, HALF, WIDE, 2, 8>(a, st);
+  } else {
+    if constexpr (WIDE) {
+      const int row = a.dim * (int)sizeof(T);
+      const bool even = row <= 512 && (row & (row - 1)) == 0;
+      const bool in_l2 = 2.0 * a.r.n * (a.q.heads + a.k.heads) * row <= 1 << 27;   // input and output
+      if (a.r.rot < a.dim && (even || (sizeof(T) == 2 ? 4 * a.r.rot > a.dim : in_l2)))
+        return launch_with<T, V, VP, HALF, WIDE, 1, 8>(a, st);
+      if constexpr (sizeof(T) == 4)
+        if (a.r.rot < a.dim) return launch_with<T, V, VP, HALF, WIDE, 2, 6>(a, st);
+    }
+    return launch_with<T, V, VP, HALF, WIDE, 2, 5>(a, st);
+  }
 }
 
 // bytes: the widest access, of 16 at most, that every row, half and remainder starts on a multiple of; else elements.
