@@ -92,7 +92,8 @@ struct Item {
 
 // Item i of prompt-major, then key head, then tiles from the last (which sees most) to the first; one warp. A prompt's
 // bounds are taken within [0, total] and in order, whatever cu holds. from, before: the 32 prompts that held the last item
-// and the items before them, where the search starts unless i is further in front.
+// and the items before them, where the search starts unless i is further in front; once a number was behind the last item,
+// the end and all items.
 struct Finder {
   int from = 0;
   unsigned before = 0;
@@ -132,6 +133,10 @@ __device__ __forceinline__ Item find_item(const PromptArgs& a, unsigned i, Finde
       if (i != 0) break;                           // the first item's finder looks at all bounds
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (!found) {                                    // behind the last item: so are all numbers from `before` on, without a look
+    f.from = a.B;
+    f.before = before;
   }
   if (i == 0 && __any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, OSCAR_STATUS_BAD_SEQLEN);
   return it;
