@@ -56,7 +56,9 @@ constexpr int kTileBytes = 2 * kHalfBytes;         // 32 KB: Q of a tile, K or V
 constexpr int kOutBytes = 32 * 128;                // a warp's rows on their way out, 128 bytes of each
 constexpr int kItems = 3;                          // worked on, loaded, found
 constexpr int kNear = 4;                           // blocks before the end of an item's loads at which the next one is looked for
-constexpr int kMasks = 8;                          // 64-token groups at an item's end that not all rows see: 6 at most
+// 64-token groups at an item's end that not all rows see: an item is 2 kTile / gq tokens from a multiple of as many on
+constexpr int kMasks = 2 * kTile / kSub;
+static_assert(2 * kTile % kSub == 0, "an item of one head begins at a group");
 constexpr int kItemMasks = 32, kItemBytes = kItemMasks + 8 * kMasks;   // start, len, h, q0; clean, bad; a bit set of each such group
 constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffOut = kOffRing + kStages * kTileBytes, kOffStat = kOffOut + 4 * kOutBytes,
               kOffItem = kOffStat + 2 * kTile * 8;   // [tile][row] (reference, sum)
