@@ -31,8 +31,10 @@
 //
 // Masked places hold whatever the packed buffer holds: logits are replaced by -inf before anything looks at them. Values
 // that a row does not see could reach it as 0 times a NaN. So an item with a result that is not finite is done once more, and then
-// warp 10 looks at the values that not all rows see before they are used, notes tokens that are not finite and replaces them
-// by zeros; rows that do see one of them become NaN. (Looking at all items' last blocks took a tenth of the time of short prompts.)
+// warp 10 looks at the values that not all rows see before they are used, notes tokens with values that are not finite and
+// replaces those values by zeros; rows that do see such a token get its values added to their results, channel by channel, so
+// that a value does the same wherever it lies in the item, and nothing to the sum of the weights. (Looking at all items' last
+// blocks took a tenth of the time of short prompts.)
 #include <algorithm>
 
 #include "quant_tile.cuh"
@@ -84,6 +86,8 @@ struct PromptArgs {
   void* out;                                       // [total][hq][kD]
   float* lse;                                      // [total][hq], or null
   int* status;
+  const __nv_bfloat16* v;                          // what the map of v covers
+  long long v_token, v_head;
 };
 
 struct Item {
@@ -302,7 +306,12 @@ __device__ __forceinline__ bool rows_item(const Ctx c, const PromptArgs& a, cons
 }
 
 // ---- values that not all rows see: warp 10 ---------------------------------------------------------------------
-// 64 tokens, two a lane: tokens that are not finite are noted in the bit set at `mask` and replaced by zeros.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {   // two BF16 values
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xffff0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xffffu;
+  return w;
+}
+// 64 tokens, two a lane: tokens with values that are not finite are noted in the bit set at `mask`, those values replaced by zeros.
 __device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
   const int lane = threadIdx.x & 31;
   const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
@@ -328,7 +337,11 @@ __device__ __forceinline__ void clean_values(uint32_t rows, uint32_t mask) {
     if (set != 0u) {
       if (lane == 0) sts32(mask + 4 * k, set);
       if (bad)
-        for (int j = 0; j < 16; ++j) sts128(rows + (j >> 3) * kHalfBytes + (32 * k + lane) * 128 + 16 * (j & 7), make_uint4(0u, 0u, 0u, 0u));
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t at = rows + (j >> 3) * kHalfBytes + (32 * k + lane) * 128 + 16 * (j & 7);
+          const uint4 v = lds128(at);
+          sts128(at, make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w)));
+        }
       fence_async();
     }
   }
@@ -364,15 +377,8 @@ __device__ __forceinline__ bool out_tile(const Ctx c, const PromptArgs& a, const
   if (!c.wait(kBStat + t, k.tiles) || !c.wait(kBO + 2 * t + h, (h ? k.half1 : k.half0) + ((n - 1) >> 1))) return false;
   tc_fence_after();
   const uint2 stat = lds64(c.base + kOffStat + 8 * (t * kTile + row));
-  const int token = it.q0 + t * tokens + (row >> a.gq_log2), masked = it.q0 / kSub;
-  float l = __uint_as_float(stat.y);
-  for (int i = masked; it.clean && i < n; ++i) {   // values that are not finite
-    const uint2 b = lds64(c.base + kOffItem + slot * kItemBytes + kItemMasks + 8 * (i - masked));
-    const int live = token + 1 - i * kSub;         // of the 64 tokens
-    const uint32_t lo = live >= 32 ? ~0u : live <= 0 ? 0u : (1u << live) - 1u;
-    const uint32_t hi = live >= 64 ? ~0u : live <= 32 ? 0u : (1u << (live - 32)) - 1u;
-    if ((b.x & lo) | (b.y & hi)) l = NAN;
-  }
+  const int token = it.q0 + t * tokens + (row >> a.gq_log2);
+  const float l = __uint_as_float(stat.y);
   const float inv = 1.f / l;
   const int left = it.len - it.q0 - t * tokens;    // tokens of the tile
   const long long base = ((long long)(it.start + it.q0 + t * tokens) * a.hq + (it.h << a.gq_log2)) * kD;
@@ -461,6 +467,45 @@ __device__ __forceinline__ bool out_item(const Ctx c, const PromptArgs& a, const
     (t ? k1 : k0) = k;
   }
   return true;
+}
+
+// Values that were left out of an item's products, into the results of a warp's rows that see them: infinities and NaN, which no
+// weight changes. A lane has a channel, and needs the first token of each kind.
+template <bool FP32>
+__device__ __forceinline__ void add_left_out(const Ctx c, const PromptArgs& a, const Item& it, int slot, int tokens) {
+  const int first = threadIdx.x & 96, groups = (min(it.len, it.q0 + 2 * tokens) - it.q0 / kSub * kSub + kSub - 1) / kSub;
+  bool any = false;
+  __syncwarp();                                    // the rows are written
+#pragma unroll 1
+  for (int channel = threadIdx.x & 31; channel < kD; channel += 32) {
+    int up = it.len, down = it.len, nan = it.len;
+#pragma unroll 1
+    for (int i = 0; i < 2 * groups; ++i)
+#pragma unroll 1
+      for (uint32_t set = lds32(c.base + kOffItem + slot * kItemBytes + kItemMasks + 4 * i); set != 0u; set &= set - 1u) {
+        const int j = it.q0 / kSub * kSub + 32 * i + __ffs(set) - 1;
+        const float v = __bfloat162float(a.v[(it.start + j) * a.v_token + it.h * a.v_head + channel]);
+        if (v != v) nan = min(nan, j);
+        if (v == INFINITY) up = min(up, j);
+        if (v == -INFINITY) down = min(down, j);
+      }
+    nan = min(nan, max(up, down));
+#pragma unroll 1
+    for (int r = first; r < 2 * kTile; r += (r & 31) == 31 ? kTile - 31 : 1) {   // rows first .. first + 31 of both tiles
+      const int tok = r >> a.gq_log2, token = it.q0 + tok;
+      const float v = nan <= token ? NAN : up <= token ? INFINITY : down <= token ? -INFINITY : 0.f;
+      if (token >= it.len || v == 0.f) continue;
+      any = true;
+      const long long at = (((long long)(it.start + token)) * a.hq + (it.h << a.gq_log2) + (r & ((1 << a.gq_log2) - 1))) * kD + channel;
+      if constexpr (FP32) {
+        static_cast<float*>(a.out)[at] += v;
+      } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + v);
+      }
+    }
+  }
+  if (any) flag(a.status, OSCAR_STATUS_NONFINITE);
 }
 
 // ---- finding ------------------------------------------------------------------------------------------------------
@@ -779,6 +824,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       if (!ok || !read_item(c, slot, it)) break;
       ok = out_item<FP32>(c, a, it, slot, tokens, results0, results1);
       if (!ok) break;
+      if (it.clean) add_left_out<FP32>(c, a, it, slot, tokens);
       c.arrive(kBItemFree + slot);
     }
   } else if (ok) {
@@ -840,7 +886,8 @@ int launch_prompt_attention(int hq, int hkv, int B, const oscar_heads& q, const 
                             const int* cu_seqlens, int total, float sm_scale, void* out, int out_dtype, float* lse, int* status,
                             cudaStream_t st) {
   const int gq = hq / hkv, tokens = 2 * kTile / gq;
-  PromptArgs a = {cu_seqlens, B, total, hq, hkv, 0, sm_scale * kLog2e, out, lse, status};
+  PromptArgs a = {cu_seqlens, B, total, hq, hkv, 0, sm_scale * kLog2e, out, lse, status,
+                  static_cast<const __nv_bfloat16*>(v.ptr), v.token, v.head};
   while (1 << a.gq_log2 < gq) ++a.gq_log2;
   CUtensorMap mq, mk, mv;
   if (!rows_map(&mq, q, hq, total, gq, kTile / gq) || !rows_map(&mk, k, hkv, total, 1, kBlock) ||

@@ -246,15 +246,16 @@ typedef struct oscar_heads {
  *  cu_seqlens : device int32 [B+1], as for oscar_quantize_prefill; tokens before cu_seqlens[0] and from cu_seqlens[B] on
  *               belong to no prompt, and their rows of out and lse stay as they are
  *  out        : device [total_tokens][Hq][128], bf16 or fp32 (out_dtype), 16-byte aligned
- *  lse        : device float32 [total_tokens][Hq] natural-log sum of exp(sm_scale q.k), or NULL
+ *  lse        : device float32 [total_tokens][Hq] natural-log sum of exp(sm_scale q.k), or NULL; NaN where a logit is NaN or
+ *               +infinity
  * Logits, softmax statistics and sums are float32; weights are rounded once to bf16 (2^-8 at most) for the product with
  * v, and the tensor cores' sums truncate (a few 1e-5 of the values' mean at 32K tokens, about 1e-3 at 256K): an fp32 out
  * carries that error too. Bounds out of order or outside [0, total_tokens] are taken within them (BAD_SEQLEN), and rows of
- * such prompts may be left unwritten. A NaN or infinity in k or v reaches no rows but those that attend to it, one in q no
- * row but its own; a row of out that is not finite raises NONFINITE. All inputs may come from the kernel just before; calls
- * may overlap. Errors: INVALID_ARG (B or total_tokens < 0, null pointers, strides that are not positive multiples of 8,
- * alignment, out_dtype, sm_scale), UNSUPPORTED (more than 2^31 - 1 tiles, or than 2^24 prompts
- * times kv heads), CUDA. */
+ * such prompts may be left unwritten. A NaN or infinity in k or v reaches no rows but those that attend to it, one in v
+ * their results in its own channel alone and no lse, one in q no row but its own; a row of out that is not finite raises
+ * NONFINITE. All inputs may come from the kernel just before; calls may overlap. Errors: INVALID_ARG (B or total_tokens < 0,
+ * null pointers, strides that are not positive multiples of 8, alignment, out_dtype, sm_scale), UNSUPPORTED (more than
+ * 2^31 - 1 tiles, or than 2^24 prompts times kv heads), CUDA. */
 int oscar_prompt_attention(oscar_cache* cache, int B, const oscar_heads* q, const oscar_heads* k, const oscar_heads* v,
                            const int32_t* cu_seqlens, int total_tokens, float sm_scale, void* out, int out_dtype,
                            float* lse, void* stream);
