@@ -267,11 +267,9 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawAppend ? kApp
         for (int part = 0; part < 2; ++part) {
           __nv_bfloat162 p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            bad |= nonfinite(x[8 * part + 2 * e]) || nonfinite(x[8 * part + 2 * e + 1]);
-            p[e] = __floats2bfloat162_rn(x[8 * part + 2 * e], x[8 * part + 2 * e + 1]);
-          }
+          for (int e = 0; e < 4; ++e) p[e] = __floats2bfloat162_rn(x[8 * part + 2 * e], x[8 * part + 2 * e + 1]);
           const uint4 z = *reinterpret_cast<const uint4*>(p);
+          bad |= bf16x2_nonfinite(z.x) || bf16x2_nonfinite(z.y) || bf16x2_nonfinite(z.z) || bf16x2_nonfinite(z.w);
           if (rlive && rq) {
             reinterpret_cast<uint4*>(raw.q_out + ((size_t)b * lv.hq + h * gq + rrow) * kD)[8 * part + rl] = z;
             if (do_q) {
