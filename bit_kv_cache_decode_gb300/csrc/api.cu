@@ -129,7 +129,7 @@ int check_rows(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int N, in
   return OSCAR_OK;
 }
 constexpr int64_t kMostRopeHeads = 1 << 30;        // of q and k together: rope.cu counts a CTA's rows in 32 bits
-constexpr int kMostNormHeads = 8192;               // norm_rope.cu divides row numbers by the heads in 32 bits
+constexpr int kMostNormHeads = 8192;               // of q, of k: norm_rope.cu counts the rows of up to 32 tokens in 32 bits, with room
 int check_norm(const oscar_head_norm* n, int dtype) {
   if (!n || !(n->eps > 0.f) || !std::isfinite(n->eps)) return OSCAR_ERR_INVALID_ARG;
   const uintptr_t size = dtype == OSCAR_DTYPE_FP32 ? 4 : 2;

@@ -496,7 +496,8 @@ int oscar_norm_rope(const oscar_rope_tensor* q, const oscar_rope_tensor* k, int 
  * out may be in, or the gradient that was given, with equal strides. Rows with a negative position are left as they are
  * and add nothing to dw.
  *  dq_weight, dk_weight : device float32 [head_dim], written (not added to), each may be NULL. Sums are taken in an order
- *                         that depends on the sizes alone: the same inputs give the same bits. No rows give zeros.
+ *                         that depends on the sizes, the dtype, the layout and the rows' alignment alone: the same call gives
+ *                         the same bits. No rows give zeros.
  *  workspace : device, 16-byte aligned, of oscar_norm_rope_workspace_bytes(head_dim) bytes, not needed (NULL) without
  *              weight gradients; calls that may overlap need one each
  * Errors: as oscar_norm_rope, INVALID_ARG (workspace too small). Works without a cache. */
