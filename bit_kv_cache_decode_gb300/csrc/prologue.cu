@@ -100,6 +100,7 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[16], const float (&w)[1
     }
   }
 }
+constexpr float kBf16End = 0x1.FFp127f;              // from here on a float32 rounds to an infinite BF16
 __device__ __forceinline__ void widen8(const uint4& u, float* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -267,9 +268,11 @@ __global__ void __launch_bounds__(kPrologueWarps * 32, MODE == kRawAppend ? kApp
         for (int part = 0; part < 2; ++part) {
           __nv_bfloat162 p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = __floats2bfloat162_rn(x[8 * part + 2 * e], x[8 * part + 2 * e + 1]);
+          for (int e = 0; e < 4; ++e) {
+            bad |= !(fabsf(x[8 * part + 2 * e]) < kBf16End) || !(fabsf(x[8 * part + 2 * e + 1]) < kBf16End);
+            p[e] = __floats2bfloat162_rn(x[8 * part + 2 * e], x[8 * part + 2 * e + 1]);
+          }
           const uint4 z = *reinterpret_cast<const uint4*>(p);
-          bad |= bf16x2_nonfinite(z.x) || bf16x2_nonfinite(z.y) || bf16x2_nonfinite(z.z) || bf16x2_nonfinite(z.w);
           if (rlive && rq) {
             reinterpret_cast<uint4*>(raw.q_out + ((size_t)b * lv.hq + h * gq + rrow) * kD)[8 * part + rl] = z;
             if (do_q) {
