@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kRopeThreads, CTAS) k_rope(RopeArgs a) {
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
   constexpr int kPer = HALF ? V : V / 2;           // pairs of a unit
   const int rot_units = HALF ? half / V : rot / V;
-  load_positions<HALF || sizeof(T) == 4>(a.r, t0, nt, pos_s, tid, nthr);
+  load_positions<!HALF && sizeof(T) == 4>(a.r, t0, nt, pos_s, tid, nthr);
   __syncthreads();
   for (int i = tid; i < nt * half; i += nthr) {
     const int t = i / half, j = i - t * half;
@@ -134,12 +134,12 @@ int launch_with(RopeArgs a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-// Units in flight and CTAs an SM of the half layout where a part of a head is turned, whose threads do unequal work: one and 8
-// for rows of a power of two of bytes up to 512 (8,192 tokens x 40 heads x 128 float32, 64 turned: 60 us; two and 5: 74), for
-// 16 bits unless a quarter or less is turned (6,553 x 40 x 160, 80 turned: 35 us, 40; 10,922 x 40 x 96, 24 turned: 41, 37),
-// for other float32 rows while L2 holds them (2,400 x 24 x 160: 12.2 us; two and 6: 13.9). Beyond it two and 6 (6,553 x 40 x
-// 160, 80 turned: 60 us; one and 8: 65; two and 5: 74), and two and 5 for single elements (4,096 x 40 x 128 float32, 64
-// turned: 72 us; one and 8: 85).
+// Units in flight and CTAs an SM of the half layout where a part of a head is turned, whose threads do unequal work. One and 8
+// while L2 holds the call (2,400 tokens x 24 heads x 160 float32, 80 turned: 12.2 us; two and 6: 13.9; 1,024 x 9 x 512 bf16, 128
+// turned: 5.8; two and 5: 7.4), for rows of a power of two of bytes up to 512 (8,192 x 40 x 128 float32, 64 turned: 60 us; two
+// and 5: 74), and of 16 bits unless a quarter or less is turned (6,553 x 40 x 160, 80 turned: 35 us, 40; 10,922 x 40 x 96, 24
+// turned: 41, 37). Other float32 rows two and 6 (6,553 x 40 x 160, 80 turned: 60 us; one and 8: 65; two and 5: 74), all else
+// two and 5 (single elements, 4,096 x 40 x 128 float32, 64 turned: 72 us; one and 8: 85).
 template <typename T, int V, int VP, bool HALF, bool WIDE>
 int launch_as(const RopeArgs& a, cudaStream_t st) {
   if constexpr (!HALF) {
@@ -149,7 +149,7 @@ int launch_as(const RopeArgs& a, cudaStream_t st) {
       const int row = a.dim * (int)sizeof(T);
       const bool even = row <= 512 && (row & (row - 1)) == 0;
       const bool in_l2 = 2.0 * a.r.n * (a.q.heads + a.k.heads) * row <= 1 << 27;   // input and output
-      if (a.r.rot < a.dim && (even || (sizeof(T) == 2 ? 4 * a.r.rot > a.dim : in_l2)))
+      if (a.r.rot < a.dim && (even || in_l2 || (sizeof(T) == 2 && 4 * a.r.rot > a.dim)))
         return launch_with<T, V, VP, HALF, WIDE, 1, 8>(a, st);
       if constexpr (sizeof(T) == 4)
         if (a.r.rot < a.dim) return launch_with<T, V, VP, HALF, WIDE, 2, 6>(a, st);
