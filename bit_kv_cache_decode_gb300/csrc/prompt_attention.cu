@@ -16,14 +16,14 @@
 // Warps: 0-3 and 4-7 rows of the two tiles, 8 loads, 9 issues the products, 10 looks at values that are not finite,
 // 11 finds the work, 12-15 write the results: the row threads are at the next item's weights by then.
 // TMEM is full: O (2 x 128 columns), S and P (2 x 128).
-// Measured: 32,769 tokens, 32 query and 8 key heads, 5.1 to 5.3 ms, 2 prompts of 8,192 with 64 and 8, 1.22 ms (1.71 and 1.76
-// PFLOP/s of products that count): the tensor pipe works in 77 % of the cycles, the rest is the chain of a tile (two times 64
+// Measured: 32,769 tokens, 32 query and 8 key heads, 5.05 to 5.3 ms, 2 prompts of 8,192 with 64 and 8, 1.22 ms (1.74 to 1.66 and
+// 1.76 PFLOP/s of products that count): the tensor pipe works in 77 % of the cycles, the rest is the chain of a tile (two times 64
 // weights, 1,870 cycles, O of the last 64 and the next S, 768, and three hand-overs), which the other tile covers but for that.
 // Halves of S that are asked for by themselves would take the chain apart, but N = 64 takes as long as N = 128 (6.2 ms); a warp
 // of its own for each tile's products mixes the tiles' products in the pipe (5.6 ms); logits loaded under the stores of the
 // weights before them change nothing. 64 prompts of 1-901 tokens 150 us (0.95 PFLOP/s; 49 %): half of a diagonal block is
 // masked, and a tile's first and masked weights and its end cost as much as two more groups of 64. One prompt of 777 tokens
-// 18 us: a CTA's chain of up to seven blocks, and the launch.
+// 15.5 us in a graph: a CTA's chain of up to seven blocks, and the launch.
 //
 // Work. The grid has a CTA for every item (prompt, key head, two tiles), the long ones of a head first. A CTA that runs
 // takes over CTAs that have not started yet (clusterlaunchcontrol), so that the loads and the first S of an item overlap
